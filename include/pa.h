@@ -91,6 +91,9 @@ typedef struct pa_dims {
 #define PA_DEVERR_BAD_PAIR 8u    /* pa_copy_blocks id outside [0, N): pair skipped    */
 #define PA_DEVERR_TIMEOUT 16u    /* a bounded in-kernel wait gave up; outputs of the  */
                                  /* affected work item were not written              */
+#define PA_DEVERR_BAD_ROW 32u    /* a row of key sums outside [0, num_rows): the      */
+                                 /* sequence's sums are not updated, and pa_evict     */
+                                 /* leaves the sequence as it is                      */
 
 /* ------------------------------------------------------------------ GPU calls */
 
@@ -331,6 +334,212 @@ PA_API int32_t pa_swap_blocks(const pa_dims *dims, void *k_cache, void *v_cache,
                               int32_t direction, void *stream);
 
 /*
+ * pa_rope_write_kv -- rotary positions and the KV write in one pass: rotate
+ * the new tokens' queries and keys by their positions, write the queries to
+ * q_out and store the rotated keys and the values in the tokens' slots (as
+ * pa_write_kv does).  The pages have no counterpart; it is the step between a
+ * model's projections and pa_decode / pa_chunk_attention.
+ *
+ * Pair i of the first rotary_dim elements of a head (0 <= i < rotary_dim / 2),
+ * (a, b) = (x[i], x[i + rotary_dim / 2]), or (x[2 i], x[2 i + 1]) when
+ * interleaved, becomes, with t = positions[token] * freqs[i],
+ *
+ *     a' = mscale * (a cos t - b sin t)      b' = mscale * (b cos t + a sin t)
+ *
+ * and the elements from rotary_dim on are copied.  Angles are reduced in 64
+ * bits (so far positions lose nothing), the rotation is in fp32, the result
+ * is rounded once to kv_dtype.
+ *
+ *   rope          rotary_dim even, 2 .. D; freqs: double [rotary_dim / 2],
+ *                 device, radians per position (pa_rope_freqs computes them on
+ *                 the host); mscale finite
+ *   q, k, v       [num_tokens, Hq | Hkv | Hkv, D] kv_dtype, device: each
+ *                 token's heads are contiguous, consecutive tokens are
+ *                 *_stride elements apart (a stride of at least heads * D, its
+ *                 bytes a multiple of 16), so column ranges of one projection
+ *                 output need no copy
+ *   q_out         [num_tokens, Hq, D], tokens q_out_stride elements apart; may
+ *                 be q itself (same pointer and stride), and must not overlap
+ *                 q otherwise
+ *   positions     int32 [num_tokens], device (any value)
+ *   slot_mapping  int64 [num_tokens], device, as for pa_write_kv; a token with
+ *                 a negative slot is padding: nothing is written for it, in
+ *                 q_out either; one with a slot >= N * B is skipped the same
+ *                 way and flagged (PA_DEVERR_BAD_SLOT)
+ * Distinct tokens must have distinct slots.  Any head_dim whose row is a
+ * multiple of 16 bytes; num_q_heads a multiple of num_kv_heads; only the heads,
+ * head_dim, block_size, num_blocks and kv_dtype of dims are used.  Returns
+ * PA_OK, PA_ERR_INVALID, PA_ERR_UNSUPPORTED (head_dim) or PA_ERR_CUDA.
+ */
+typedef struct pa_rope {
+    int32_t rotary_dim;
+    int32_t interleaved;   /* 0: pairs (i, i + rotary_dim / 2); 1: pairs (2 i, 2 i + 1) */
+    const double *freqs;
+    float mscale;
+} pa_rope;
+PA_API int32_t pa_rope_write_kv(const pa_dims *dims, const pa_rope *rope, const void *q, int64_t q_stride,
+                                const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                const int32_t *positions, const int64_t *slot_mapping, int32_t num_tokens,
+                                void *q_out, int64_t q_out_stride, void *k_cache, void *v_cache, void *stream);
+
+/*
+ * pa_rope_freqs -- the rotary frequencies of a model on the host:
+ * f_i = theta^(-2 i / rotary_dim), scaled for contexts longer than the
+ * original_len positions that a model was trained on (factor >= 1):
+ *   PA_ROPE_PLAIN    f_i
+ *   PA_ROPE_LINEAR   f_i / factor
+ *   PA_ROPE_BASE     theta replaced by theta * factor^(R / (R - 2)), R =
+ *                    rotary_dim > 2: the fastest pair stays, the slowest is
+ *                    divided by factor
+ *   PA_ROPE_RAMP     pairs turning more than `fast` times over original_len
+ *                    keep f_i, pairs turning less than `slow` times get
+ *                    f_i / factor, and between, from pair low = max(0, floor
+ *                    d(fast)) to high = min(R - 1, ceil d(slow)), a linear
+ *                    ramp; d(turns) = R ln(original_len / (2 pi turns)) /
+ *                    (2 ln theta); *mscale = 0.1 ln(factor) + 1
+ *   PA_ROPE_BANDS    wavelengths w = 2 pi / f_i below original_len / fast keep
+ *                    f_i, above original_len / slow get f_i / factor, and
+ *                    between, with u = (original_len / w - slow) / (fast -
+ *                    slow), (1 - u) f_i / factor + u f_i
+ * *mscale is 1 except for PA_ROPE_RAMP.  theta > 1; 0 < slow < fast (RAMP and
+ * BANDS).  freqs_out: host double [rotary_dim / 2].  Returns PA_OK or
+ * PA_ERR_INVALID.
+ */
+#define PA_ROPE_PLAIN 0
+#define PA_ROPE_LINEAR 1
+#define PA_ROPE_BASE 2
+#define PA_ROPE_RAMP 3
+#define PA_ROPE_BANDS 4
+PA_API int32_t pa_rope_freqs(int32_t rotary_dim, double theta, int32_t scaling, double factor, double original_len,
+                             double fast, double slow, double *freqs_out, float *mscale);
+
+/*
+ * Scores other than scale * q . k, for pa_decode_scored and pa_chunk_scored.
+ * For the query row at position pos of its sequence (pa_decode: the last
+ * token, pos = context length - 1) and the key at position j,
+ *
+ *     z = scale * q . k_j
+ *     z = softcap * tanh(z / softcap)          if softcap > 0
+ *     z = z - slopes[h] * |pos - j|            if slopes
+ *
+ * and the softmax runs over the keys begin <= j < end only, where
+ *     begin = max(0, key_begin[row], pos - window + 1)   (a NULL key_begin and
+ *                                               a window of 0 count as absent)
+ *     end   = min(context length, key_end[row]),  or pos + 1 if key_end is NULL
+ * A row with no key left gets zeros.  So key_begin holds the first position of
+ * the row's document when several are packed into one sequence (a document
+ * mask), key_end = max(pos + 1, prefix length) lets the tokens of a prefix see
+ * each other (a prefix mask; the keys after pos are in the cache already),
+ * and window is a sliding window.  Positions are places in the block table:
+ * after pa_evict, distances count the kept tokens.  A NULL pa_score is
+ * pa_decode's plain score.
+ *
+ * What slots outside every row's range hold does not matter (NaN included).
+ * The rows of one chunk are worked on together: a key or value that some row of
+ * a sequence's chunk sees must be finite, or it may reach the chunk's others.
+ */
+typedef struct pa_score {
+    float softcap;             /* 0: none; else finite and > 0                  */
+    int32_t window;            /* 0: none; else > 0                             */
+    const float *slopes;       /* float32 [Hq], device, or NULL                 */
+    const int32_t *key_begin;  /* int32 [rows], device, or NULL (rows: S for    */
+    const int32_t *key_end;    /* pa_decode_scored, T for pa_chunk_scored)      */
+} pa_score;
+
+/*
+ * Running sums of attention weights, for choosing what to evict: after a
+ * pa_decode_scored call, for every key j that the sequence's query saw,
+ *
+ *     sums[row, kvh, j] += sum over the query heads h of KV head kvh of p[h, j]
+ *
+ * with p the softmax weights.  sums is float32 [num_rows, Hkv, cols], device;
+ * sequence s uses row rows[s] (int32 [S], device), or row s if rows is NULL; the
+ * rows of one call must be distinct.  Sums belong to a sequence, not to its
+ * blocks, so forks and cached prefixes keep their own.  cols is a multiple of
+ * 4 and at least max_blocks_per_seq * B; set a row to 0 when a sequence starts
+ * (the caller's step), pa_evict keeps it in step with the table from then on.
+ */
+typedef struct pa_key_sums {
+    float *sums;
+    const int32_t *rows;
+    int32_t num_rows;
+    int32_t cols;
+} pa_key_sums;
+
+/*
+ * pa_decode_scored -- pa_decode with a pa_score, a choice of the output's type
+ * and, optionally, the running sums of attention weights.
+ *
+ *   score         NULL: plain
+ *   key_sums      NULL: none
+ *   out           [S, Hq, D] float32, or kv_dtype when out_dtype == kv_dtype
+ *                 (out_dtype is PA_F32 or kv_dtype)
+ *   workspace     >= pa_decode_scored_workspace_bytes(dims, with_sums) bytes,
+ *                 256-byte aligned; concurrent calls need separate workspaces:
+ *                 pa_decode's parts and, with sums, the logits, S * Hq *
+ *                 max_blocks_per_seq * B floats
+ *   other arguments, shapes and errors as for pa_decode
+ */
+PA_API size_t pa_decode_scored_workspace_bytes(const pa_dims *dims, int32_t with_sums);
+PA_API int32_t pa_decode_scored(const pa_dims *dims, const pa_score *score, const void *q, const void *k_cache,
+                                const void *v_cache, const int32_t *block_tables, const int32_t *context_lens,
+                                float scale, const pa_key_sums *key_sums, void *out, int32_t out_dtype,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * pa_chunk_scored -- pa_chunk_attention with a pa_score and a choice of the
+ * output's type (as for pa_decode_scored), for f32 caches too.  Rows, ranges
+ * and errors as for pa_chunk_attention: rows outside every range, and those of
+ * a sequence that is skipped and flagged, are not written.
+ */
+PA_API size_t pa_chunk_scored_workspace_bytes(const pa_dims *dims, int32_t num_tokens, int32_t max_query_len);
+PA_API int32_t pa_chunk_scored(const pa_dims *dims, const pa_score *score, const void *q, const void *k_cache,
+                               const void *v_cache, const int32_t *block_tables, const int32_t *context_lens,
+                               const int32_t *query_start, int32_t num_tokens, int32_t max_query_len, float scale,
+                               void *out, int32_t out_dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * pa_evict -- shrink sequences that outgrew a budget, keeping the tokens that
+ * attention looked at most.  For each sequence s with context_lens[s] >
+ * keep_lens[s], and each KV head on its own, keep
+ *   - the last min(recent, keep_lens[s]) tokens, and
+ *   - of the tokens before them the keep_lens[s] - min(recent, keep_lens[s])
+ *     with the largest sums (equal sums: the lower position; NaN is below
+ *     everything),
+ * and copy their keys and values, in their order, to positions 0 ..
+ * keep_lens[s] - 1 of new_tables[s].  Sharing stays valid: no source block is
+ * written, so other sequences and the prefix cache keep theirs.  (The token
+ * at one position then differs between KV heads, which attention does not
+ * notice: it reads each head's keys and values together.)  Sequences within
+ * their budget keep their table, and nothing of new_tables[s] is read.
+ *
+ *   block_tables, context_lens   the tables and lengths before the eviction
+ *   new_tables    int32 [S, max_blocks_per_seq], device: pa_seq_evict's blocks
+ *                 for the sequences that shrink; none of them may occur in
+ *                 block_tables, nor twice
+ *   keep_lens     int32 [S], device; a negative one leaves the sequence as it
+ *                 is and sets PA_DEVERR_BAD_LEN
+ *   recent        >= 0
+ *   key_sums      the sums to go by (as for pa_decode_scored)
+ *   sums_out      float32 [num_rows, Hkv, cols]: the sums of the kept tokens at
+ *                 their new positions, 0 from the new length on; may be
+ *                 key_sums->sums itself, and must not overlap it otherwise;
+ *                 only the rows of the call's sequences are written
+ *   new_lens      int32 [S], device: min(context_lens[s], keep_lens[s]); must
+ *                 not overlap context_lens or keep_lens
+ *   workspace     >= pa_evict_workspace_bytes(dims) bytes, 256-byte aligned
+ * num_q_heads of dims is not used; num_seqs * num_kv_heads is at most 65535
+ * (PA_ERR_INVALID above).  Any block_size and any head_dim whose row
+ * is a multiple of 16 bytes.  A row whose source or destination block is
+ * outside [0, N) is skipped and flagged (PA_DEVERR_BAD_BLOCK).
+ */
+PA_API size_t pa_evict_workspace_bytes(const pa_dims *dims);
+PA_API int32_t pa_evict(const pa_dims *dims, void *k_cache, void *v_cache, const int32_t *block_tables,
+                        const int32_t *context_lens, const int32_t *new_tables, const int32_t *keep_lens,
+                        int32_t recent, const pa_key_sums *key_sums, float *sums_out, int32_t *new_lens,
+                        void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * pa_copy_to_device / pa_copy_to_host -- one asynchronous copy of `bytes`
  * bytes between host memory and device memory of the current device, on
  * `stream` (cudaMemcpyAsync).  The pages have no counterpart: this is the hop
@@ -500,6 +709,19 @@ PA_API int32_t pa_seq_swap_out(pa_pool *dev, pa_pool *host, int32_t seq, int32_t
  */
 PA_API int32_t pa_seq_swap_in(pa_pool *dev, pa_pool *host, int32_t host_seq, int32_t *dev_seq, int64_t *pairs_out,
                               int32_t *n_pairs);
+
+/*
+ * Give a sequence of more than keep_tokens tokens a table of ceil(keep_tokens /
+ * B) fresh private blocks and that length; its old blocks lose one reference
+ * each (in table order, as pa_seq_free).  Export the table before the call
+ * (pa_pool_export) for pa_evict's block_tables and after it for new_tables, and
+ * run pa_evict before any kernel writes to a freed block.  A sequence of at
+ * most keep_tokens tokens is left as it is.  *evicted (nullable) is 1 if the
+ * table changed, else 0.  All-or-nothing: PA_ERR_OOM if fewer blocks are free
+ * than the new table needs (evict a few sequences at a time), nothing changed;
+ * PA_ERR_INVALID for keep_tokens < 0, PA_ERR_BAD_INDEX for an unknown id.
+ */
+PA_API int32_t pa_seq_evict(pa_pool *pool, int32_t seq, int32_t keep_tokens, int32_t *evicted);
 
 /* ------------------------------------------------------- prefix cache
  *

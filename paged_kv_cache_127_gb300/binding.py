@@ -26,6 +26,10 @@ STATUS_NAMES = {0: "PA_OK", 1: "PA_ERR_INVALID", 2: "PA_ERR_UNSUPPORTED", 3: "PA
 PA_SWAP_OUT, PA_SWAP_IN = 0, 1
 PA_DEVERR_BAD_BLOCK, PA_DEVERR_BAD_LEN, PA_DEVERR_BAD_SLOT, PA_DEVERR_BAD_PAIR, PA_DEVERR_TIMEOUT = (
     1, 2, 4, 8, 16)
+PA_DEVERR_BAD_ROW = 32
+PA_ROPE_PLAIN, PA_ROPE_LINEAR, PA_ROPE_BASE, PA_ROPE_RAMP, PA_ROPE_BANDS = range(5)
+ROPE_SCALINGS = {"plain": PA_ROPE_PLAIN, "linear": PA_ROPE_LINEAR, "base": PA_ROPE_BASE, "ramp": PA_ROPE_RAMP,
+                 "bands": PA_ROPE_BANDS}
 
 
 class PaError(RuntimeError):
@@ -48,6 +52,21 @@ class pa_pool_stats(ctypes.Structure):
                 ("shared_blocks", ctypes.c_int32), ("live_seqs", ctypes.c_int32),
                 ("cow_copies", ctypes.c_int64), ("tokens", ctypes.c_int64),
                 ("table_slots", ctypes.c_int64), ("padded_slots", ctypes.c_int64)]
+
+
+class pa_rope(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("freqs", ctypes.c_void_p),
+                ("mscale", ctypes.c_float)]
+
+
+class pa_score(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32), ("slopes", ctypes.c_void_p),
+                ("key_begin", ctypes.c_void_p), ("key_end", ctypes.c_void_p)]
+
+
+class pa_key_sums(ctypes.Structure):
+    _fields_ = [("sums", ctypes.c_void_p), ("rows", ctypes.c_void_p), ("num_rows", ctypes.c_int32),
+                ("cols", ctypes.c_int32)]
 
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
@@ -95,6 +114,18 @@ _SIGNATURES = {
     "pa_prefix_evict": (_i32, [_vp, _i32]),
     "pa_prefix_cached_blocks": (_i32, [_vp]),
     "pa_seq_create_from_prefix": (_i32, [_vp, _vp, _i32]),
+    "pa_rope_write_kv": (_i32, [_vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _vp, _i64, _vp, _vp,
+                                _vp]),
+    "pa_rope_freqs": (_i32, [_i32, ctypes.c_double, _i32, ctypes.c_double, ctypes.c_double, ctypes.c_double,
+                             ctypes.c_double, _vp, _vp]),
+    "pa_decode_scored_workspace_bytes": (_sz, [_vp, _i32]),
+    "pa_decode_scored": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp, _i32, _vp, _sz, _vp]),
+    "pa_chunk_scored_workspace_bytes": (_sz, [_vp, _i32, _i32]),
+    "pa_chunk_scored": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, ctypes.c_float, _vp, _i32, _vp,
+                               _sz, _vp]),
+    "pa_evict_workspace_bytes": (_sz, [_vp]),
+    "pa_evict": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "pa_seq_evict": (_i32, [_vp, _i32, _i32, _vp]),
 }
 
 
@@ -310,6 +341,244 @@ def pa_write_kv(dims: pa_dims, k, v, slot_mapping, k_cache, v_cache, stream=None
     args = (ctypes.byref(dims), k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(), T, k_cache.data_ptr(),
             v_cache.data_ptr(), _stream_ptr(stream, dev))
     return _issue(lib.pa_write_kv, args, "pa_write_kv", dev, prepare, (dims, k, v, slot_mapping, k_cache, v_cache))
+
+
+class Rope:
+    """What pa_rope_write_kv rotates: see make_rope."""
+
+    __slots__ = ("rotary_dim", "freqs", "interleaved", "mscale")
+
+    def __init__(self, rotary_dim, freqs, interleaved, mscale):
+        self.rotary_dim, self.freqs, self.interleaved, self.mscale = int(rotary_dim), freqs, bool(interleaved), float(mscale)
+
+
+def make_rope(rotary_dim: int, freqs, interleaved: bool = False, mscale: float = 1.0) -> Rope:
+    """Rotation of the first rotary_dim elements of a head: freqs is a float64 CUDA
+    tensor [rotary_dim // 2] of radians per position (pa_rope_freqs computes them);
+    interleaved pairs are (2i, 2i+1), else (i, i + rotary_dim // 2)."""
+    return Rope(rotary_dim, freqs, interleaved, mscale)
+
+
+def pa_rope_freqs(rotary_dim: int, theta: float = 10000.0, scaling="plain", factor: float = 1.0,
+                  original_len: float = 0.0, fast: float = 0.0, slow: float = 0.0):
+    """Returns (freqs float64[rotary_dim // 2], mscale) of a model; scaling is "plain", "linear",
+    "base", "ramp" or "bands" (include/pa.h has the formulas)."""
+    code = ROPE_SCALINGS[scaling] if isinstance(scaling, str) else int(scaling)
+    out = np.empty(max(int(rotary_dim) // 2, 1), dtype=np.float64)
+    ms = ctypes.c_float(0.0)
+    _check(lib.pa_rope_freqs(int(rotary_dim), float(theta), code, float(factor), float(original_len), float(fast),
+                             float(slow), _np_ptr(out), ctypes.byref(ms)), "pa_rope_freqs")
+    return out, float(ms.value)
+
+
+def _expect_tokens(t, name, shape, dtype, device):
+    """A [tokens, heads, D] tensor whose tokens' rows are contiguous; returns its token stride."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    row = shape[1] * shape[2]
+    if (shape[2] > 1 and t.stride(2) != 1) or (shape[1] > 1 and t.stride(1) != shape[2]):
+        raise ValueError(f"{name}: each token's heads must be contiguous")
+    return t.stride(0) if shape[0] > 1 else row
+
+
+def pa_rope_write_kv(dims: pa_dims, rope: Rope, q, k, v, positions, slot_mapping, q_out, k_cache, v_cache,
+                     stream=None, prepare: bool = False):
+    """Rotate q into q_out and k into its cache slots, and write v: pa_write_kv with
+    rotary positions.  q, k, v and q_out are [T, heads, D] with contiguous heads and
+    any token stride (column ranges of one projection); q_out may be q.
+    With prepare=True nothing runs: the checked call is returned as a Prepared."""
+    t = _torch()
+    d, kv = dims, _torch_dtype(dims.kv_dtype)
+    dev = q.device
+    T = int(slot_mapping.shape[0])
+    qs = _expect_tokens(q, "q", (T, d.num_q_heads, d.head_dim), kv, dev)
+    ks = _expect_tokens(k, "k", (T, d.num_kv_heads, d.head_dim), kv, dev)
+    vs = _expect_tokens(v, "v", (T, d.num_kv_heads, d.head_dim), kv, dev)
+    os_ = _expect_tokens(q_out, "q_out", (T, d.num_q_heads, d.head_dim), kv, dev)
+    _expect(positions, "positions", (T,), t.int32, dev)
+    _expect(slot_mapping, "slot_mapping", (T,), t.int64, dev)
+    _expect(rope.freqs, "rope.freqs", (rope.rotary_dim // 2,), t.float64, dev)
+    cache_shape = (d.num_blocks, d.num_kv_heads, d.block_size, d.head_dim)
+    _expect(k_cache, "k_cache", cache_shape, kv, dev)
+    _expect(v_cache, "v_cache", cache_shape, kv, dev)
+    rp = pa_rope(rope.rotary_dim, int(rope.interleaved), rope.freqs.data_ptr(), rope.mscale)
+    args = (ctypes.byref(dims), ctypes.byref(rp), q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+            positions.data_ptr(), slot_mapping.data_ptr(), T, q_out.data_ptr(), os_, k_cache.data_ptr(),
+            v_cache.data_ptr(), _stream_ptr(stream, dev))
+    return _issue(lib.pa_rope_write_kv, args, "pa_rope_write_kv", dev, prepare,
+                  (dims, rp, rope.freqs, q, k, v, positions, slot_mapping, q_out, k_cache, v_cache))
+
+
+class Score:
+    """Scores other than scale * q . k: see make_score."""
+
+    __slots__ = ("softcap", "window", "slopes", "key_begin", "key_end")
+
+    def __init__(self, softcap, window, slopes, key_begin, key_end):
+        self.softcap, self.window = float(softcap), int(window)
+        self.slopes, self.key_begin, self.key_end = slopes, key_begin, key_end
+
+
+def make_score(softcap: float = 0.0, window: int = 0, slopes=None, key_begin=None, key_end=None) -> Score:
+    """softcap: z -> softcap * tanh(z / softcap); slopes (float32 [Hq]): z - slopes[h] * |pos - j|;
+    window, key_begin and key_end (int32, one per query row): the keys a row sees, begin <= j < end."""
+    return Score(softcap, window, slopes, key_begin, key_end)
+
+
+def _marshal_score(score, num_q_heads, rows, dev):
+    """(pointer argument, objects to keep) of a Score, checked against the call."""
+    t = _torch()
+    if score is None:
+        return None, ()
+    ptr = lambda x: None if x is None else x.data_ptr()  # noqa: E731
+    if score.slopes is not None:
+        _expect(score.slopes, "score.slopes", (num_q_heads,), t.float32, dev)
+    for name in ("key_begin", "key_end"):
+        if getattr(score, name) is not None:
+            _expect(getattr(score, name), "score." + name, (rows,), t.int32, dev)
+    sc = pa_score(score.softcap, score.window, ptr(score.slopes), ptr(score.key_begin), ptr(score.key_end))
+    return ctypes.byref(sc), (sc, score.slopes, score.key_begin, score.key_end)
+
+
+def _marshal_sums(key_sums, sum_rows, dims, dev):
+    """(pointer argument, objects to keep) of the running sums [rows, Hkv, cols]."""
+    t = _torch()
+    if key_sums is None:
+        if sum_rows is not None:
+            raise ValueError("sum_rows without key_sums")
+        return None, ()
+    if key_sums.dim() != 3:
+        raise ValueError(f"key_sums has shape {tuple(key_sums.shape)}, expected (rows, {dims.num_kv_heads}, cols)")
+    R, C = int(key_sums.shape[0]), int(key_sums.shape[2])
+    _expect(key_sums, "key_sums", (R, dims.num_kv_heads, C), t.float32, dev)
+    if sum_rows is not None:
+        _expect(sum_rows, "sum_rows", (dims.num_seqs,), t.int32, dev)
+    ks = pa_key_sums(key_sums.data_ptr(), None if sum_rows is None else sum_rows.data_ptr(), R, C)
+    return ctypes.byref(ks), (ks, key_sums, sum_rows)
+
+
+def _out_code(out, dims):
+    """The pa_dtype of a scored call's output: float32 or the cache's type."""
+    t = _torch()
+    if out.dtype == t.float32:
+        return PA_F32
+    if out.dtype != _torch_dtype(dims.kv_dtype):
+        raise ValueError(f"out has dtype {out.dtype}, expected float32 or {_torch_dtype(dims.kv_dtype)}")
+    return dims.kv_dtype
+
+
+def _workspace(workspace, need, what, dev):
+    """(pointer, bytes) of a caller's workspace."""
+    if not need:
+        return None, 0
+    if workspace is None:
+        raise ValueError(f"{what} needs a workspace of {need} bytes")
+    if not workspace.is_cuda or not workspace.is_contiguous() or workspace.device != dev:
+        raise ValueError("workspace must be a contiguous CUDA tensor on the same device")
+    return ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size()
+
+
+def pa_decode_scored_workspace_bytes(dims: pa_dims, with_sums: bool = False) -> int:
+    return int(lib.pa_decode_scored_workspace_bytes(ctypes.byref(dims), 1 if with_sums else 0))
+
+
+def pa_decode_scored(dims: pa_dims, score, q, k_cache, v_cache, block_tables, context_lens, scale: float, out,
+                     workspace=None, key_sums=None, sum_rows=None, stream=None, prepare: bool = False):
+    """pa_decode with a Score (or None), an out of float32 or the cache's dtype, and
+    optionally key_sums [rows, Hkv, cols] (row sum_rows[s], or s), to which every
+    key's attention weights are added.
+    With prepare=True nothing runs: the checked call is returned as a Prepared."""
+    t = _torch()
+    d, kv = dims, _torch_dtype(dims.kv_dtype)
+    dev = q.device
+    _expect(q, "q", (d.num_seqs, d.num_q_heads, d.head_dim), kv, dev)
+    cache_shape = (d.num_blocks, d.num_kv_heads, d.block_size, d.head_dim)
+    _expect(k_cache, "k_cache", cache_shape, kv, dev)
+    _expect(v_cache, "v_cache", cache_shape, kv, dev)
+    _expect(block_tables, "block_tables", (d.num_seqs, d.max_blocks_per_seq), t.int32, dev)
+    _expect(context_lens, "context_lens", (d.num_seqs,), t.int32, dev)
+    code = _out_code(out, dims)
+    _expect(out, "out", (d.num_seqs, d.num_q_heads, d.head_dim), out.dtype, dev)
+    sc, keep_score = _marshal_score(score, d.num_q_heads, d.num_seqs, dev)
+    ks, keep_sums = _marshal_sums(key_sums, sum_rows, dims, dev)
+    need = pa_decode_scored_workspace_bytes(dims, key_sums is not None)
+    ws_ptr, ws_bytes = _workspace(workspace, need, "pa_decode_scored", dev)
+    args = (ctypes.byref(dims), sc, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+            context_lens.data_ptr(), float(scale), ks, out.data_ptr(), code, ws_ptr, ws_bytes,
+            _stream_ptr(stream, dev))
+    return _issue(lib.pa_decode_scored, args, "pa_decode_scored", dev, prepare,
+                  (dims, q, k_cache, v_cache, block_tables, context_lens, out, workspace, keep_score, keep_sums))
+
+
+def pa_chunk_scored_workspace_bytes(dims: pa_dims, num_tokens: int, max_query_len: int) -> int:
+    return int(lib.pa_chunk_scored_workspace_bytes(ctypes.byref(dims), int(num_tokens), int(max_query_len)))
+
+
+def pa_chunk_scored(dims: pa_dims, score, q, k_cache, v_cache, block_tables, context_lens, query_start, scale: float,
+                    out, max_query_len: int, workspace=None, stream=None, prepare: bool = False):
+    """pa_chunk_attention with a Score (or None) and an out of float32 or the cache's dtype.
+    With prepare=True nothing runs: the checked call is returned as a Prepared."""
+    t = _torch()
+    d, kv = dims, _torch_dtype(dims.kv_dtype)
+    dev = q.device
+    T = int(q.shape[0])
+    _expect(q, "q", (T, d.num_q_heads, d.head_dim), kv, dev)
+    cache_shape = (d.num_blocks, d.num_kv_heads, d.block_size, d.head_dim)
+    _expect(k_cache, "k_cache", cache_shape, kv, dev)
+    _expect(v_cache, "v_cache", cache_shape, kv, dev)
+    _expect(block_tables, "block_tables", (d.num_seqs, d.max_blocks_per_seq), t.int32, dev)
+    _expect(context_lens, "context_lens", (d.num_seqs,), t.int32, dev)
+    _expect(query_start, "query_start", (d.num_seqs + 1,), t.int32, dev)
+    code = _out_code(out, dims)
+    _expect(out, "out", (T, d.num_q_heads, d.head_dim), out.dtype, dev)
+    sc, keep_score = _marshal_score(score, d.num_q_heads, T, dev)
+    need = pa_chunk_scored_workspace_bytes(dims, T, max_query_len)
+    ws_ptr, ws_bytes = _workspace(workspace, need, "pa_chunk_scored", dev)
+    args = (ctypes.byref(dims), sc, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+            context_lens.data_ptr(), query_start.data_ptr(), T, int(max_query_len), float(scale), out.data_ptr(), code,
+            ws_ptr, ws_bytes, _stream_ptr(stream, dev))
+    return _issue(lib.pa_chunk_scored, args, "pa_chunk_scored", dev, prepare,
+                  (dims, q, k_cache, v_cache, block_tables, context_lens, query_start, out, workspace, keep_score))
+
+
+def pa_evict_workspace_bytes(dims: pa_dims) -> int:
+    return int(lib.pa_evict_workspace_bytes(ctypes.byref(dims)))
+
+
+def pa_evict(dims: pa_dims, k_cache, v_cache, block_tables, context_lens, new_tables, keep_lens, recent: int, key_sums,
+             sums_out, new_lens, workspace=None, sum_rows=None, stream=None, prepare: bool = False):
+    """Copy, for every sequence longer than keep_lens[s] and each KV head, the last
+    `recent` tokens and those with the largest key_sums to the blocks of
+    new_tables[s], and write the kept tokens' sums to sums_out (which may be
+    key_sums) and the new lengths.
+    With prepare=True nothing runs: the checked call is returned as a Prepared."""
+    t = _torch()
+    d, kv = dims, _torch_dtype(dims.kv_dtype)
+    dev = k_cache.device
+    cache_shape = (d.num_blocks, d.num_kv_heads, d.block_size, d.head_dim)
+    _expect(k_cache, "k_cache", cache_shape, kv, dev)
+    _expect(v_cache, "v_cache", cache_shape, kv, dev)
+    for name, x in (("block_tables", block_tables), ("new_tables", new_tables)):
+        _expect(x, name, (d.num_seqs, d.max_blocks_per_seq), t.int32, dev)
+    for name, x in (("context_lens", context_lens), ("keep_lens", keep_lens), ("new_lens", new_lens)):
+        _expect(x, name, (d.num_seqs,), t.int32, dev)
+    if key_sums is None:
+        raise ValueError("pa_evict needs key_sums")
+    ks, keep_sums = _marshal_sums(key_sums, sum_rows, dims, dev)
+    _expect(sums_out, "sums_out", tuple(key_sums.shape), t.float32, dev)
+    ws_ptr, ws_bytes = _workspace(workspace, pa_evict_workspace_bytes(dims), "pa_evict", dev)
+    args = (ctypes.byref(dims), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+            context_lens.data_ptr(), new_tables.data_ptr(), keep_lens.data_ptr(), int(recent), ks, sums_out.data_ptr(),
+            new_lens.data_ptr(), ws_ptr, ws_bytes, _stream_ptr(stream, dev))
+    return _issue(lib.pa_evict, args, "pa_evict", dev, prepare,
+                  (dims, k_cache, v_cache, block_tables, context_lens, new_tables, keep_lens, keep_sums, sums_out,
+                   new_lens, workspace))
 
 
 def pa_copy_blocks(dims: pa_dims, k_cache, v_cache, src_dst_pairs, stream=None, prepare: bool = False):
@@ -590,6 +859,14 @@ def pa_seq_len(pool, seq: int) -> int:
     if r < 0:
         raise PaError(-r, "pa_seq_len")
     return r
+
+
+def pa_seq_evict(pool, seq: int, keep_tokens: int) -> bool:
+    """Give a sequence of more than keep_tokens tokens a fresh table of that length;
+    returns whether the table changed."""
+    out = ctypes.c_int32(0)
+    _check(lib.pa_seq_evict(pool, int(seq), int(keep_tokens), ctypes.byref(out)), "pa_seq_evict")
+    return bool(out.value)
 
 
 def pa_pool_export(pool, seqs, max_blocks: int, pad: int = -1):

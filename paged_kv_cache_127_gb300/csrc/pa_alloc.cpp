@@ -319,6 +319,29 @@ int32_t pa_seq_swap_in(pa_pool *dev, pa_pool *host, int32_t host_seq, int32_t *d
     return PA_OK;
 }
 
+int32_t pa_seq_evict(pa_pool *pool, int32_t seq, int32_t keep_tokens, int32_t *evicted) {
+    if (!pool || keep_tokens < 0) return PA_ERR_INVALID;
+    if (!valid_seq(pool, seq)) return PA_ERR_BAD_INDEX;
+    if (evicted) *evicted = 0;
+    pa_seq_rec &s = pool->seqs[seq];
+    if (s.len <= keep_tokens) return PA_OK;
+    const int64_t nb = blocks_for(keep_tokens, pool->B);
+    if (nb > available(pool)) return PA_ERR_OOM;
+    // the fresh blocks are taken before the old ones are released, so that none is both
+    std::vector<int32_t> fresh;
+    try {
+        fresh.reserve((size_t)nb);
+    } catch (const std::bad_alloc &) {
+        return PA_ERR_OOM;
+    }
+    for (int64_t j = 0; j < nb; ++j) fresh.push_back(take_block(pool));
+    for (int32_t b : s.table) release_block(pool, b);
+    s.table.swap(fresh);
+    s.len = keep_tokens;
+    if (evicted) *evicted = 1;
+    return PA_OK;
+}
+
 int32_t pa_copy_pairs_check(const int64_t *pairs, int32_t num_pairs, int32_t num_blocks) {
     if (num_pairs < 0 || num_blocks <= 0 || (num_pairs > 0 && !pairs)) return PA_ERR_INVALID;
     std::vector<int64_t> dst;

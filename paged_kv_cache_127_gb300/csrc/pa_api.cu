@@ -284,6 +284,27 @@ int32_t to_status(cudaError_t e) {
 
 }  // namespace
 
+// The parts of this file that the scored-attention, rotary and eviction calls
+// (pa_scored_api.cu) share.
+namespace pa {
+unsigned int *device_error_word() { return error_word(); }
+int32_t check_cache(const pa_dims *d) { return check_cache_dims(d); }
+int32_t check_attention(const pa_dims *d, int32_t partition, int32_t *max_parts) {
+    return check_decode_dims_pt(d, partition, max_parts);
+}
+int32_t decode_partition_size(const pa_dims *d) { return effective_partition(d); }
+int32_t chunk_partition_size(const pa_dims *d) { return chunk_partition(d); }
+cudaError_t cached_cache_map(const void *ptr, bool bf16, int D, int B, long long block_heads, int hg, CUtensorMap *out) {
+    return cache_tensor_map(ptr, bf16, D, B, block_heads, hg, out);
+}
+cudaError_t cached_query_map(const void *q, bool bf16, int D, int Hq, long long T, int G, CUtensorMap *out) {
+    return query_tensor_map(q, bf16, D, Hq, T, G, out);
+}
+cudaError_t cached_output_map(float *o, int D, int Hq, long long T, int G, CUtensorMap *out) {
+    return output_tensor_map(o, D, Hq, T, G, out);
+}
+}  // namespace pa
+
 extern "C" {
 
 size_t pa_decode_workspace_bytes(const pa_dims *dims) {

@@ -1,0 +1,109 @@
+"""GPU tests of pa_rope_write_kv against a plain reference in extended precision.
+
+Tolerance: the turn's fraction as fp32 and sincospif give (cos, sin) to 2^-21
+absolute; two products and a sum in fp32 add 2^-23 of |a| + |b|; the result is
+rounded once (half a step of its type)."""
+import numpy as np
+import pytest
+
+from gpu_helpers import require_gpu, to_dev, to_host
+from paged_helpers import widen
+from paged_kv_cache_127_gb300 import synth
+from scored_helpers import HALF_STEP, rotate
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def gpu():
+    return require_gpu()
+
+
+def check(got, x, pos, freqs, R, interleaved, mscale, dtype):
+    ref, mag = rotate(widen(x, dtype), pos, freqs, R, interleaved, mscale)
+    tol = mag * (2.0 ** -21 + 2.0 ** -22) + HALF_STEP[dtype] * np.abs(ref) * (mag > 0) + 2.0 ** -24 * (dtype == "f16") * (mag > 0)
+    bad = np.abs(widen(got, dtype) - ref) > tol
+    assert not bad.any(), f"{int(bad.sum())} of {bad.size} outside"
+
+
+def run(torch, pa, dtype, T, Hq, Hkv, D, B, R, interleaved, pos, slots, N, rng, fused=True, mscale=1.0, in_place=False):
+    freqs, _ = pa.pa_rope_freqs(R, 10000.0)
+    heads = Hq + 2 * Hkv
+    x = synth.normal(rng, (T, heads, D), 1.0, dtype)
+    kc, vc = (synth.normal(rng, (N, Hkv, B, D), 1.0, dtype) for _ in range(2))
+    all_ = to_dev(torch, x, dtype)
+    q, k, v = all_[:, :Hq], all_[:, Hq:Hq + Hkv], all_[:, Hq + Hkv:]
+    if not fused:
+        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+    out = q if in_place else torch.full_like(all_[:, :Hq].contiguous(), 7.0)
+    dk, dv = to_dev(torch, kc, dtype), to_dev(torch, vc, dtype)
+    dims = pa.make_dims(0, Hq, Hkv, D, B, N, 1, 0, dtype)
+    pa.pa_rope_write_kv(dims, pa.make_rope(R, torch.from_numpy(freqs).cuda(), interleaved, mscale), q, k, v,
+                        torch.from_numpy(np.asarray(pos, np.int32)).cuda(), torch.from_numpy(np.asarray(slots, np.int64)).cuda(),
+                        out, dk, dv)
+    torch.cuda.synchronize()
+    ok = (np.asarray(slots) >= 0) & (np.asarray(slots) < N * B)
+    got_q = to_host(out.contiguous(), dtype)
+    check(got_q[ok], x[ok, :Hq], np.asarray(pos)[ok], freqs, R, interleaved, mscale, dtype)
+    # padding and skipped tokens: nothing written
+    want = x[:, :Hq] if in_place else np.broadcast_to(to_host(torch.full((1,), 7.0).to(all_.dtype), dtype), got_q.shape)
+    np.testing.assert_array_equal(got_q[~ok], want[~ok])
+    k2, v2 = to_host(dk, dtype), to_host(dv, dtype)
+    for t in np.nonzero(ok)[0]:
+        b, o = divmod(int(slots[t]), B)
+        check(k2[b, :, o][None], x[t:t + 1, Hq:Hq + Hkv], [pos[t]], freqs, R, interleaved, mscale, dtype)
+        np.testing.assert_array_equal(v2[b, :, o], x[t, Hq + Hkv:])
+        kc[b, :, o], vc[b, :, o] = k2[b, :, o], v2[b, :, o]
+    np.testing.assert_array_equal(k2, kc)     # every other slot holds what it held
+    np.testing.assert_array_equal(v2, vc)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("D,R", [(128, 128), (128, 64), (64, 64), (64, 20), (128, 2), (96, 90), (80, 48), (8, 8)])
+def test_rope_layouts_and_sizes(gpu, dtype, D, R, interleaved):
+    torch, pa = gpu
+    rng = synth.make_rng(8000 + D + R + interleaved)
+    for T, Hq, Hkv, B in ((1, 4, 1, 16), (37, 6, 3, 32), (5, 8, 8, 16)):
+        N = 9
+        slots = rng.permutation(N * B)[:T]
+        pos = rng.integers(0, 5000, T)
+        run(torch, pa, dtype, T, Hq, Hkv, D, B, R, interleaved, pos, slots, N, rng, fused=T != 5)
+    assert pa.pa_device_errors(clear=True) == 0
+
+
+def test_rope_far_and_negative_positions_padding_and_bad_slots(gpu):
+    torch, pa = gpu
+    rng = synth.make_rng(8100)
+    pos = np.array([0, 1, 2 ** 20 + 3, 2 ** 31 - 1, -7, -2 ** 31, 131071, 12])
+    slots = np.array([5, 40, 0, 159, 12, 13, -1, 160])
+    for dtype in ("f32", "bf16"):
+        run(torch, pa, dtype, 8, 4, 2, 128, 16, 128, False, pos, slots, 10, rng)
+        assert pa.pa_device_errors(clear=True) == pa.PA_DEVERR_BAD_SLOT
+
+
+def test_rope_in_place_and_mscale(gpu):
+    torch, pa = gpu
+    rng = synth.make_rng(8200)
+    for dtype, fused in (("bf16", True), ("f32", False), ("f16", True)):
+        slots = np.where(np.arange(50) % 7 == 3, -1, rng.permutation(64)[:50])
+        run(torch, pa, dtype, 50, 8, 2, 64, 16, 32, True, rng.integers(0, 99999, 50), slots, 4, rng, fused, 1.2079, True)
+    assert pa.pa_device_errors(clear=True) == 0
+
+
+def test_rope_matches_the_separate_write(gpu):
+    # at position 0 with mscale 1 the call is pa_write_kv, bit for bit
+    torch, pa = gpu
+    rng = synth.make_rng(8300)
+    T, Hq, Hkv, D, B, N = 40, 4, 2, 64, 16, 6
+    k, v = (to_dev(torch, synth.normal(rng, (T, Hkv, D), 1.0, "bf16"), "bf16") for _ in range(2))
+    q = to_dev(torch, synth.normal(rng, (T, Hq, D), 1.0, "bf16"), "bf16")
+    slots = torch.from_numpy(rng.permutation(N * B)[:T]).cuda()
+    dims = pa.make_dims(0, Hq, Hkv, D, B, N, 1, 0, "bf16")
+    a = [torch.zeros(N, Hkv, B, D, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    pa.pa_write_kv(dims, k, v, slots, a[0], a[1])
+    freqs = torch.from_numpy(pa.pa_rope_freqs(D)[0]).cuda()
+    out = torch.empty_like(q)
+    pa.pa_rope_write_kv(dims, pa.make_rope(D, freqs), q, k, v, torch.zeros(T, dtype=torch.int32, device="cuda"), slots, out,
+                        a[2], a[3])
+    assert torch.equal(a[0], a[2]) and torch.equal(a[1], a[3]) and torch.equal(out, q)
