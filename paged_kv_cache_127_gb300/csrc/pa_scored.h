@@ -57,6 +57,17 @@ struct ScoredArgs {
     float scale, softcap;         // softcap 0: none
 };
 
+// Mark of a work item that holds its sequence's whole range (in the partition's int).
+constexpr int kWholeRange = 1 << 30;
+
+// Tensor-core decode (f16 / bf16): the work list, the persistent kernel, and the
+// CTAs it launches on the current device (SMs x resident CTAs per SM).
+cudaError_t launch_scored_decode_plan(const ScoredArgs &a, cudaStream_t st);
+cudaError_t launch_scored_decode_f16(const ScoredArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
+cudaError_t launch_scored_decode_bf16(const ScoredArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
+cudaError_t scored_decode_ctas_f16(const ScoredArgs &a, int *ctas);
+cudaError_t scored_decode_ctas_bf16(const ScoredArgs &a, int *ctas);
+
 // Merge of the split-K partials, and the sums of attention weights.
 cudaError_t launch_scored_finish(const ScoredArgs &a, bool bf16, cudaStream_t st);
 // CUDA-core kernel, one CTA per (row, KV head, partition): f32 caches.

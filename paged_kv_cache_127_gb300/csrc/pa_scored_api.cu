@@ -159,9 +159,26 @@ int32_t pa_decode_scored(const pa_dims *dims, const pa_score *score, const void 
     a.err = pa::device_error_word();
     if (!a.err) return PA_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = pa::launch_scored_rows(a, dims->kv_dtype, st);
+    cudaError_t e;
+    const bool bf16 = dims->kv_dtype == PA_BF16;
+    if (dims->kv_dtype == PA_F32) {
+        e = pa::launch_scored_rows(a, PA_F32, st);
+    } else {
+        // work list, the persistent tensor-core kernel, then merge and sums
+        // (each launch a programmatic dependent of the one before)
+        const long long block_heads = (long long)dims->num_blocks * dims->num_kv_heads;
+        CUtensorMap tmk, tmv;
+        e = pa::cached_cache_map(k_cache, bf16, dims->head_dim, dims->block_size, block_heads, a.head_group, &tmk);
+        if (e == cudaSuccess)
+            e = pa::cached_cache_map(v_cache, bf16, dims->head_dim, dims->block_size, block_heads, a.head_group, &tmv);
+        if (e != cudaSuccess) return PA_ERR_CUDA;
+        e = bf16 ? pa::scored_decode_ctas_bf16(a, &a.ctas) : pa::scored_decode_ctas_f16(a, &a.ctas);
+        if (e == cudaSuccess) e = pa::launch_scored_decode_plan(a, st);
+        if (e == cudaSuccess)
+            e = bf16 ? pa::launch_scored_decode_bf16(a, tmk, tmv, st) : pa::launch_scored_decode_f16(a, tmk, tmv, st);
+    }
     if (e != cudaSuccess) return to_status(e);
-    return to_status(pa::launch_scored_finish(a, dims->kv_dtype == PA_BF16, st));
+    return to_status(pa::launch_scored_finish(a, bf16, st));
 }
 
 size_t pa_chunk_scored_workspace_bytes(const pa_dims *dims, int32_t num_tokens, int32_t max_query_len) {
