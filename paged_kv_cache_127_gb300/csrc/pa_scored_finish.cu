@@ -9,6 +9,7 @@
 //   sums[row, kvh, j] += sum_g 2^(z_gj - M_g) / L_g
 // from the logits z that the partition kernel left (4 bytes per query head and
 // key, against 2 D elements of K and V that a second pass would read again).
+#include "pa_mma.cuh"
 #include "pa_score.cuh"
 
 namespace pa {
@@ -16,7 +17,6 @@ namespace pa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTile = 4 * kThreads;  // keys of one block of the sums
 
 // Maximum and sum over partitions p0 .. p1 of the (m, l) pairs at ml.  Whole warp.
 __device__ __forceinline__ float2 merged_ml(const float *ml, int p0, int p1, int lane) {
@@ -31,96 +31,123 @@ __device__ __forceinline__ float2 merged_ml(const float *ml, int p0, int p1, int
     return make_float2(M, L);
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) scored_finish_kernel(const ScoredArgs a, int merge_blocks, int tiles) {
-    constexpr int kPer = D / 32;
+// The running sums of four keys and the logits of the G heads for them.
+template <int G>
+struct KeySpan {
+    float4 v, x[G];
+    __device__ __forceinline__ void load(const float *sums, const float *z, size_t heads, int j) {
+        v = *reinterpret_cast<const float4 *>(sums + j);
+#pragma unroll
+        for (int g = 0; g < G; ++g) x[g] = *reinterpret_cast<const float4 *>(z + g * heads + j);
+    }
+    // += sum over the heads of 2^(z - M) / L for the keys of [begin, end); keys
+    // outside have no logit (whatever the workspace holds there is not used)
+    __device__ __forceinline__ void add(float *sums, const float2 *tot, int j, int begin, int end) {
+        float w[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const float2 t = tot[g];
+            w[0] += ex2(x[g].x - t.x) * t.y;
+            w[1] += ex2(x[g].y - t.x) * t.y;
+            w[2] += ex2(x[g].z - t.x) * t.y;
+            w[3] += ex2(x[g].w - t.x) * t.y;
+        }
+        if (j >= begin) v.x += w[0];
+        if (j + 1 >= begin && j + 1 < end) v.y += w[1];
+        if (j + 2 >= begin && j + 2 < end) v.z += w[2];
+        if (j + 3 >= begin && j + 3 < end) v.w += w[3];
+        *reinterpret_cast<float4 *>(sums + j) = v;
+    }
+};
+
+// One block per (query row, KV head) and, with sums, part of the row's keys: the
+// G heads' (M, L) once for the merge and the sums.  The first four keys of a
+// thread are loaded before the totals are known, and each next four while the
+// last are added, so that a block pays one chain of loads, not one per step.
+template <typename T, int D, int G>
+__global__ void __launch_bounds__(kThreads) scored_finish_kernel(const ScoredArgs a, int splits) {
+    __shared__ float2 tot[G];  // (M, 1 / L) of each head of the group
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int cap = a.max_blocks * a.B;
+    const int split = blockIdx.x % splits, kvh = blockIdx.x / splits % a.Hkv, i = blockIdx.x / splits / a.Hkv;
+    const int cap = a.max_blocks * a.B, P = a.max_parts;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (a.query_start && a.plan_hdr[0] < 0) return;
-    if ((int)blockIdx.x < merge_blocks) {
-        const long long w = (long long)blockIdx.x * (kThreads / 32) + warp;
-        if (w >= (long long)a.T * a.Hq) return;
-        const int i = (int)(w / a.Hq);
-        const RowOf r = row_of(a, i, cap);
-        if (r.s < 0) return;
-        const int2 range = row_range(a, i, r.pos, r.len);
-        if (range.x >= range.y) return;
-        const int p0 = range.x / a.partition_size, p1 = (range.y - 1) / a.partition_size;
-        if (p0 == p1) return;  // written in place
-        const float *ml = a.ws_ml + 2 * w * a.max_parts;
-        const float *acc = a.ws_acc + (size_t)w * a.max_parts * D + lane * kPer;
-        const float2 t = merged_ml(ml, p0, p1, lane);
-        float o[kPer];
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) o[e] = 0.f;
-        for (int p = p0; p <= p1; ++p) {
-            const float wt = ex2(ml[2 * p] - t.x);
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) o[e] = fmaf(wt, acc[(size_t)p * D + e], o[e]);
-        }
-        const float inv = t.y != 0.f ? 1.f / t.y : 0.f;
-        const size_t at = (size_t)w * D + lane * kPer;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-            if (a.out16) store_out(static_cast<T *>(a.out) + at + e, o[e] * inv);
-            else static_cast<float *>(a.out)[at + e] = o[e] * inv;
-        }
-        return;
-    }
-    // ---- sums of one (sequence, KV head), kTile keys
-    const int b = (int)blockIdx.x - merge_blocks;
-    const int s = b / tiles / a.Hkv, kvh = b / tiles % a.Hkv;
-    const int G = a.Hq / a.Hkv;
-    const RowOf r = row_of(a, s, cap);
-    const int2 range = row_range(a, s, r.pos, r.len);
-    const int k0 = (range.x & ~3) + (b % tiles) * kTile;
-    if (range.x >= range.y || k0 >= range.y) return;
-    const int row = a.sum_rows ? a.sum_rows[s] : s;
-    if (row < 0 || row >= a.sum_num_rows) {
-        if (threadIdx.x == 0) set_error(a.err, PA_DEVERR_BAD_ROW);
-        return;
-    }
-    __shared__ float2 tot[8];
+    const RowOf r = row_of(a, i, cap);
+    if (r.s < 0) return;
+    const int2 range = row_range(a, i, r.pos, r.len);
+    if (range.x >= range.y) return;
+    const int p0 = range.x / a.partition_size, p1 = (range.y - 1) / a.partition_size;
+    const bool merge = p0 != p1 && split == 0;  // else written in place, or by another block
+    if (!merge && !a.sums) return;
+    const size_t head0 = (size_t)i * a.Hq + kvh * G;
+    const int row = a.sums ? (a.sum_rows ? a.sum_rows[i] : i) : -1;
+    const bool add = row >= 0 && row < a.sum_num_rows;
+    if (a.sums && !add && threadIdx.x == 0) set_error(a.err, PA_DEVERR_BAD_ROW);
+    float *sums = a.sums + ((size_t)(add ? row : 0) * a.Hkv + kvh) * a.sum_cols;
+    const float *z = a.ws_logits + head0 * cap;
+    int j = (range.x & ~3) + 4 * (split * kThreads + (int)threadIdx.x);
+    KeySpan<G> cur;
+    if (add && j < range.y) cur.load(sums, z, cap, j);
     if (warp < G) {
-        const int p0 = range.x / a.partition_size, p1 = (range.y - 1) / a.partition_size;
-        const float2 t = merged_ml(a.ws_ml + 2 * ((size_t)s * a.Hq + kvh * G + warp) * a.max_parts, p0, p1, lane);
+        const float2 t = merged_ml(a.ws_ml + 2 * (head0 + warp) * P, p0, p1, lane);
         if (lane == 0) tot[warp] = make_float2(t.x, t.y != 0.f ? 1.f / t.y : 0.f);
     }
     __syncthreads();
-    const int j = k0 + 4 * threadIdx.x;
-    if (j >= range.y) return;
-    float *dst = a.sums + ((size_t)row * a.Hkv + kvh) * a.sum_cols + j;
-    float add[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int g = 0; g < G; ++g) {
-        const float4 z = *reinterpret_cast<const float4 *>(a.ws_logits + ((size_t)s * a.Hq + kvh * G + g) * cap + j);
-        const float2 t = tot[g];
-        add[0] += ex2(z.x - t.x) * t.y;
-        add[1] += ex2(z.y - t.x) * t.y;
-        add[2] += ex2(z.z - t.x) * t.y;
-        add[3] += ex2(z.w - t.x) * t.y;
+    if (merge) {
+        for (int c = threadIdx.x; c < G * D / 4; c += kThreads) {
+            const int g = c / (D / 4), d = c % (D / 4) * 4;
+            const float *ml = a.ws_ml + 2 * (head0 + g) * P;
+            const float *acc = a.ws_acc + (head0 + g) * P * D + d;
+            const float2 t = tot[g];
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int p = p0; p <= p1; ++p) {
+                const float w = ex2(ml[2 * p] - t.x);
+                const float4 x = *reinterpret_cast<const float4 *>(acc + (size_t)p * D);
+                o.x = fmaf(w, x.x, o.x);
+                o.y = fmaf(w, x.y, o.y);
+                o.z = fmaf(w, x.z, o.z);
+                o.w = fmaf(w, x.w, o.w);
+            }
+            const size_t at = (head0 + g) * D + d;
+            if (a.out16) {
+                const uint2 y = make_uint2(Mma16<T>::pack(o.x * t.y, o.y * t.y), Mma16<T>::pack(o.z * t.y, o.w * t.y));
+                *reinterpret_cast<uint2 *>(static_cast<T *>(a.out) + at) = y;
+            } else {
+                *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) =
+                    make_float4(o.x * t.y, o.y * t.y, o.z * t.y, o.w * t.y);
+            }
+        }
     }
-    // keys outside the range have no logit: what the workspace holds there is not used
-    float4 v = *reinterpret_cast<float4 *>(dst);
-    if (j >= range.x && j < range.y) v.x += add[0];
-    if (j + 1 >= range.x && j + 1 < range.y) v.y += add[1];
-    if (j + 2 >= range.x && j + 2 < range.y) v.z += add[2];
-    if (j + 3 >= range.x && j + 3 < range.y) v.w += add[3];
-    *reinterpret_cast<float4 *>(dst) = v;
+    if (!add) return;
+    const int step = 4 * kThreads * splits;
+    while (j < range.y) {
+        KeySpan<G> next;
+        if (j + step < range.y) next.load(sums, z, cap, j + step);
+        cur.add(sums, tot, j, range.x, range.y);
+        cur = next;
+        j += step;
+    }
 }
 
-template <typename T>
+template <typename T, int D>
 cudaError_t launch_finish_t(const ScoredArgs &a, cudaStream_t st) {
-    const long long warps = (long long)a.T * a.Hq;
-    const int merge = a.max_parts > 1 ? (int)((warps + kThreads / 32 - 1) / (kThreads / 32)) : 0;
-    const int cap = a.max_blocks * a.B;
-    const int tiles = a.sums ? (cap + 3 + kTile - 1) / kTile : 0;
-    const long long blocks = merge + (long long)a.S * a.Hkv * tiles * (a.sums ? 1 : 0);
-    if (blocks == 0) return cudaSuccess;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    if (a.max_parts == 1 && !a.sums) return cudaSuccess;
+    const long long pairs = (long long)a.T * a.Hkv;
+    // Blocks for the sums: one resident wave (8 per SM), so that a few long sequences fill the GPU,
+    // at most one per 1024 positions of the tables.  One block per 1024 positions whatever
+    // the batch took 35 us on 256 sequences of up to 4096 tokens (8,192 blocks, most
+    // with no keys, each paying the chain of loads up to the heads' totals).
+    long long splits = 1;
+    if (a.sums) {
+        const long long most = ((long long)a.max_blocks * a.B + 4 * kThreads - 1) / (4 * kThreads);
+        splits = 8 * 152 / pairs;
+        splits = splits < 1 ? 1 : (splits > most ? most : splits);
+    }
+    if (pairs * splits > 0x7fffffffLL) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.gridDim = dim3((unsigned)(pairs * splits));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -128,15 +155,21 @@ cudaError_t launch_finish_t(const ScoredArgs &a, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (a.D == 64) return cudaLaunchKernelEx(&cfg, scored_finish_kernel<T, 64>, a, merge, tiles);
-    if (a.D == 128) return cudaLaunchKernelEx(&cfg, scored_finish_kernel<T, 128>, a, merge, tiles);
-    return cudaErrorNotSupported;
+    switch (a.Hq / a.Hkv) {
+        case 1: return cudaLaunchKernelEx(&cfg, scored_finish_kernel<T, D, 1>, a, (int)splits);
+        case 2: return cudaLaunchKernelEx(&cfg, scored_finish_kernel<T, D, 2>, a, (int)splits);
+        case 4: return cudaLaunchKernelEx(&cfg, scored_finish_kernel<T, D, 4>, a, (int)splits);
+        case 8: return cudaLaunchKernelEx(&cfg, scored_finish_kernel<T, D, 8>, a, (int)splits);
+        default: return cudaErrorNotSupported;
+    }
 }
 
 }  // namespace
 
 cudaError_t launch_scored_finish(const ScoredArgs &a, bool bf16, cudaStream_t st) {
-    return bf16 ? launch_finish_t<__nv_bfloat16>(a, st) : launch_finish_t<__half>(a, st);
+    if (a.D == 64) return bf16 ? launch_finish_t<__nv_bfloat16, 64>(a, st) : launch_finish_t<__half, 64>(a, st);
+    if (a.D == 128) return bf16 ? launch_finish_t<__nv_bfloat16, 128>(a, st) : launch_finish_t<__half, 128>(a, st);
+    return cudaErrorNotSupported;
 }
 
 }  // namespace pa
