@@ -68,6 +68,16 @@ cudaError_t launch_scored_decode_bf16(const ScoredArgs &a, const CUtensorMap &tm
 cudaError_t scored_decode_ctas_f16(const ScoredArgs &a, int *ctas);
 cudaError_t scored_decode_ctas_bf16(const ScoredArgs &a, int *ctas);
 
+// Tensor-core chunk attention: the work list, the mma.sync kernel for short chunks
+// and the tcgen05 kernel for long ones (tmo: the output's map, 16-bit or f32).
+cudaError_t launch_scored_chunk_plan(const ScoredArgs &a, cudaStream_t st);
+cudaError_t launch_scored_chunk_f16(const ScoredArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
+cudaError_t launch_scored_chunk_bf16(const ScoredArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
+cudaError_t launch_scored_umma_f16(const ScoredArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv,
+                                   const CUtensorMap &tmq, const CUtensorMap &tmo, cudaStream_t st);
+cudaError_t launch_scored_umma_bf16(const ScoredArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv,
+                                    const CUtensorMap &tmq, const CUtensorMap &tmo, cudaStream_t st);
+
 // Merge of the split-K partials, and the sums of attention weights.
 cudaError_t launch_scored_finish(const ScoredArgs &a, bool bf16, cudaStream_t st);
 // CUDA-core kernel, one CTA per (row, KV head, partition): f32 caches.

@@ -77,8 +77,13 @@ ScoredLayout decode_layout(const pa_dims *d, int32_t parts, bool sums) {
     return scored_layout(d, (size_t)d->num_seqs * parts, (size_t)d->num_seqs, parts, parts > 1, sums);
 }
 
-ScoredLayout chunk_layout(const pa_dims *d, int32_t T, int32_t, int32_t parts) {
-    return scored_layout(d, 0, (size_t)T, parts, parts > 1, false);
+// f32 chunks have no list; the tcgen05 path has no partials (it walks a tile's whole span).
+ScoredLayout chunk_layout(const pa_dims *d, int32_t T, int32_t max_q, int32_t parts) {
+    const int G = d->num_q_heads / d->num_kv_heads;
+    const bool f32 = d->kv_dtype == PA_F32, umma = !f32 && pa::chunk_uses_umma(max_q, G);
+    const int64_t rows = umma ? pa::chunk_umma_rows(max_q, G) : 16 * pa::chunk_row_warps(max_q, G);
+    const size_t blocks = (size_t)(((int64_t)max_q * G + rows - 1) / rows) * d->num_seqs;
+    return scored_layout(d, f32 ? 0 : blocks * (umma ? 1 : parts), (size_t)T, parts, parts > 1 && !umma, false);
 }
 
 void fill_args(pa::ScoredArgs &a, const pa_dims *d, const pa_score *sc, const ScoredLayout &L, void *workspace) {
@@ -222,9 +227,45 @@ int32_t pa_chunk_scored(const pa_dims *dims, const pa_score *score, const void *
     a.err = pa::device_error_word();
     if (!a.err) return PA_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = pa::launch_scored_rows(a, dims->kv_dtype, st);
+    cudaError_t e;
+    const bool bf16 = dims->kv_dtype == PA_BF16;
+    if (dims->kv_dtype == PA_F32) {
+        e = pa::launch_scored_rows(a, PA_F32, st);
+        if (e != cudaSuccess) return to_status(e);
+        return to_status(pa::launch_scored_finish(a, false, st));
+    }
+    const int G = dims->num_q_heads / dims->num_kv_heads;
+    const bool umma = pa::chunk_uses_umma(max_query_len, G);
+    a.row_warps = pa::chunk_row_warps(max_query_len, G);
+    a.umma_rows = umma ? pa::chunk_umma_rows(max_query_len, G) : 0;
+    const long long block_heads = (long long)dims->num_blocks * dims->num_kv_heads;
+    const int box_heads = umma ? 1 : a.head_group;
+    CUtensorMap tmk, tmv;
+    e = pa::cached_cache_map(k_cache, bf16, dims->head_dim, dims->block_size, block_heads, box_heads, &tmk);
+    if (e == cudaSuccess)
+        e = pa::cached_cache_map(v_cache, bf16, dims->head_dim, dims->block_size, block_heads, box_heads, &tmv);
+    if (e != cudaSuccess) return PA_ERR_CUDA;
+    if (umma) {
+        // long chunks: plan, then the tcgen05 kernel, which loads queries and stores full tiles by TMA
+        CUtensorMap tmq, tmo;
+        e = pa::cached_query_map(q, bf16, dims->head_dim, dims->num_q_heads, num_tokens, G, &tmq);
+        if (e == cudaSuccess)
+            e = a.out16 ? pa::cached_query_map(out, bf16, dims->head_dim, dims->num_q_heads, num_tokens, G, &tmo)
+                        : pa::cached_output_map(static_cast<float *>(out), dims->head_dim, dims->num_q_heads, num_tokens, G,
+                                                &tmo);
+        if (e != cudaSuccess) return PA_ERR_CUDA;
+        e = pa::launch_scored_chunk_plan(a, st);
+        if (e == cudaSuccess)
+            e = bf16 ? pa::launch_scored_umma_bf16(a, tmk, tmv, tmq, tmo, st)
+                     : pa::launch_scored_umma_f16(a, tmk, tmv, tmq, tmo, st);
+        return to_status(e);
+    }
+    // short chunks: plan, the mma.sync kernel, merge
+    e = pa::launch_scored_chunk_plan(a, st);
+    if (e == cudaSuccess)
+        e = bf16 ? pa::launch_scored_chunk_bf16(a, tmk, tmv, st) : pa::launch_scored_chunk_f16(a, tmk, tmv, st);
     if (e != cudaSuccess) return to_status(e);
-    return to_status(pa::launch_scored_finish(a, dims->kv_dtype == PA_BF16, st));
+    return to_status(pa::launch_scored_finish(a, bf16, st));
 }
 
 int32_t pa_rope_write_kv(const pa_dims *dims, const pa_rope *rope, const void *q, int64_t q_stride, const void *k,

@@ -1,6 +1,6 @@
-// pa_scored_plan.cu -- work list of the scored tensor-core decode.
+// pa_scored_plan.cu -- work lists of the scored tensor-core kernels.
 //
-// One CTA lists every (sequence, partition) that holds keys of the sequence's
+// Decode: one CTA lists every (sequence, partition) that holds keys of the sequence's
 // range, as (sequence, partition, first key, one past the last key), most 16-key
 // chunks first (a counting sort), so that the persistent decode hands out big
 // items before small ones.  Bit 30 of the partition marks an item that holds
@@ -9,6 +9,8 @@
 // (sequence b / groups), before this list is complete.  The plan also
 // resets the claim counters, writes the zero rows of empty ranges and flags bad
 // lengths.
+#include <climits>
+
 #include "pa_score.cuh"
 
 namespace pa {
@@ -69,7 +71,114 @@ __global__ void __launch_bounds__(1024) scored_decode_plan_kernel(const ScoredAr
     }
 }
 
+// Keys that some of the query rows i0 .. i1 - 1 (positions pos0 ..) of a sequence of
+// len tokens see, with key_begin / key_end arrays: the lanes of a warp share the
+// rows.  (0, 0) when no row sees any.
+__device__ __forceinline__ int2 span_of_rows(const ScoredArgs &a, int i0, int i1, int pos0, int len, int lane) {
+    int lo = INT_MAX, hi = 0;
+    for (int i = i0 + lane; i < i1; i += 32) {
+        const int2 k = row_range(a, i, pos0 + (i - i0), len);
+        if (k.x < k.y) {
+            lo = min(lo, k.x);
+            hi = max(hi, k.y);
+        }
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    return lo < hi ? make_int2(lo, hi) : make_int2(0, 0);
+}
+
+// Chunk calls.  An entry is a row block of a sequence -- the tcgen05 path's group
+// of one or two 128-row tiles, or the mma.sync path's 16 or 32 rows -- and, on
+// the mma.sync path, a partition: (sequence, block, lo, hi) or (sequence,
+// partition | block << 16, lo, hi), with the keys [lo, hi) that some row of the
+// block sees; most keys first.  Two passes over the blocks, a warp each (with
+// key_begin or key_end it reads its rows' ranges together): count, then place.
+// Rows with an empty range are zeroed here.  plan_hdr[0] = -1 when
+// query_start is not non-decreasing within [0, T].
+__global__ void __launch_bounds__(1024) scored_chunk_plan_kernel(const ScoredArgs a) {
+    __shared__ int hist[kBins];
+    __shared__ int start[kBins];
+    __shared__ int warp_sums[32];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int G = a.Hq / a.Hkv, cap = a.max_blocks * a.B;
+    const int rows = a.umma_rows > 0 ? a.umma_rows : 16 * a.row_warps;  // query rows of a block
+    const int Pt = a.umma_rows > 0 ? INT_MAX : a.partition_size;
+    const int unit = a.umma_rows > 0 ? PA_CHUNK_UMMA_KEYS : 16;         // keys of a step
+    for (int i = tid; i < kBins; i += blockDim.x) hist[i] = 0;
+    if (tid == 0) a.plan_hdr[1] = 0;
+    int bad = tid == 0 && (a.query_start[0] < 0 || a.query_start[a.S] > a.T);
+    for (int s = tid; s < a.S; s += blockDim.x) bad |= a.query_start[s] > a.query_start[s + 1];
+    if (__syncthreads_or(bad)) {
+        if (tid == 0) {
+            set_error(a.err, PA_DEVERR_BAD_LEN);
+            a.plan_hdr[0] = -1;
+        }
+        return;
+    }
+    const bool arrays = a.key_begin || a.key_end;  // else the ranges follow from the positions, and none is empty
+    const int blocks = (int)(((long long)a.max_query_len * G + rows - 1) / rows);  // of a sequence, at most
+    for (int pass = 0; pass < 2; ++pass) {
+        for (long long b = warp; b < (long long)a.S * blocks; b += 32) {
+            const int s = (int)(b / blocks), rb = (int)(b % blocks);
+            const int q0 = a.query_start[s], n = a.query_start[s + 1] - q0, len = a.context_lens[s];
+            if (len < 0 || len > cap || n > len || n > a.max_query_len) {
+                if (pass == 0 && rb == 0 && lane == 0) set_error(a.err, PA_DEVERR_BAD_LEN);
+                continue;
+            }
+            if (rb * rows >= n * G) continue;
+            const int t0 = rb * rows / G, t1 = min(n, (rb * rows + rows + G - 1) / G);  // tokens of the block
+            int2 k;
+            if (arrays) {
+                k = span_of_rows(a, q0 + t0, q0 + t1, len - n + t0, len, lane);
+            } else {
+                k.x = row_range(a, 0, len - n + t0, len).x;
+                k.y = len - n + t1;
+            }
+            if (k.x >= k.y) continue;
+            const int p0 = k.x / Pt, p1 = (k.y - 1) / Pt;
+            for (int p = p0 + lane; p <= p1; p += 32) {
+                const int lo = p == p0 ? k.x : p * Pt, hi = p == p1 ? k.y : (p + 1) * Pt;
+                const int bin = min((hi - 1) / unit - lo / unit + 1, kBins - 1);
+                if (pass == 0) {
+                    atomicAdd(&hist[bin], 1);
+                } else {
+                    const int at = atomicAdd(&start[bin], 1);
+                    a.plan_list[at] = make_int4(s, a.umma_rows > 0 ? rb : p | rb << 16, lo, hi);
+                }
+            }
+        }
+        __syncthreads();
+        if (pass == 0) {
+            const int total = scan_bins_desc(hist, start, kBins - 1, kBins, warp_sums);
+            if (tid == 0) a.plan_hdr[0] = total;
+        }
+    }
+    if (arrays)
+        for (int i = tid; i < a.T; i += blockDim.x) {
+            const RowOf r = row_of(a, i, cap);
+            if (r.s < 0) continue;
+            const int2 k = row_range(a, i, r.pos, r.len);
+            if (k.x >= k.y) zero_row(a, i);
+        }
+}
+
 }  // namespace
+
+cudaError_t launch_scored_chunk_plan(const ScoredArgs &a, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, scored_chunk_plan_kernel, a);
+}
 
 cudaError_t launch_scored_decode_plan(const ScoredArgs &a, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
