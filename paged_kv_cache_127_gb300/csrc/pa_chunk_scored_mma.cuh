@@ -81,6 +81,24 @@ __global__ void __launch_bounds__(ChunkCfg<D, HG, RW>::kThreads, ChunkCfg<D, HG,
     const uint32_t kx = (uint32_t)(lm ^ lr);          // swizzled chunk bits for K reads
     const uint32_t vx = (uint32_t)((lm >> 1) ^ lr);   // and for V reads
     const ScoreCap score(a);
+    const float sl = a.scale * kLog2e;
+    // dot products to logits in log2 units
+    auto to_log2 = [&](auto &f) {
+        constexpr int N = sizeof(f) / sizeof(f[0]);
+        if (score.cap && sl > 0.f) {
+            float most = fabsf(f[0]);
+#pragma unroll
+            for (int i = 1; i < N; ++i) most = fmaxf(most, fabsf(f[i]));
+            cap_in_place(f, score.in, most);
+        }
+        if (score.cap && !(sl > 0.f)) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) f[i] = score(f[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) f[i] *= sl;
+        }
+    };
     const int head = warp % HG;      // KV head of the item's group
     const int tile_of = warp / HG;   // row tile within the item's row block
 
@@ -296,15 +314,20 @@ __global__ void __launch_bounds__(ChunkCfg<D, HG, RW>::kThreads, ChunkCfg<D, HG,
                     }
                 }
                 // logits of the 32 keys: chunk c, keys c2, c2+1, 8+c2, 9+c2 at [4c .. 4c+3]
-                float x0[8], x1[8];
+                float f[16];  // rows g, then g + 8
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int c = i >> 2, nt = i >> 1 & 1, e = i & 1;
-                    const int key = kb + 16 * c + 8 * nt + c2 + e;
-                    const float z0 = score(sc[c][nt][0][e] + sc[c][nt][1][e]) - s0 * fabsf((float)(pos0 - key));
-                    const float z1 = score(sc[c][nt][0][2 + e] + sc[c][nt][1][2 + e]) - s1 * fabsf((float)(pos1 - key));
-                    x0[i] = key >= k0.x && key < k0.y ? z0 : -INFINITY;
-                    x1[i] = key >= k1.x && key < k1.y ? z1 : -INFINITY;
+                    f[i] = sc[c][nt][0][e] + sc[c][nt][1][e];
+                    f[8 + i] = sc[c][nt][0][2 + e] + sc[c][nt][1][2 + e];
+                }
+                to_log2(f);
+                float x0[8], x1[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int key = kb + 16 * (i >> 2) + 8 * (i >> 1 & 1) + c2 + (i & 1);
+                    x0[i] = key >= k0.x && key < k0.y ? f[i] - s0 * fabsf((float)(pos0 - key)) : -INFINITY;
+                    x1[i] = key >= k1.x && key < k1.y ? f[8 + i] - s1 * fabsf((float)(pos1 - key)) : -INFINITY;
                 }
                 float mx0 = x0[0], mx1 = x1[0];
 #pragma unroll
@@ -422,15 +445,21 @@ __global__ void __launch_bounds__(ChunkCfg<D, HG, RW>::kThreads, ChunkCfg<D, HG,
                     }
                 }
                 // ---- logits, masks and online softmax; keys c2, c2+1, 8+c2, 9+c2 of rows g, g+8
-                float x0[4], x1[4];
+                float f[8];  // rows g, then g + 8
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int nt = i >> 1, e = i & 1;
-                    const int key = kb + 8 * nt + c2 + e;
-                    const float z0 = score(sc[nt][0][e] + sc[nt][1][e]) - s0 * fabsf((float)(pos0 - key));
-                    const float z1 = score(sc[nt][0][2 + e] + sc[nt][1][2 + e]) - s1 * fabsf((float)(pos1 - key));
-                    x0[i] = key >= k0.x && key < k0.y && key < kb + n1 ? z0 : -INFINITY;
-                    x1[i] = key >= k1.x && key < k1.y && key < kb + n1 ? z1 : -INFINITY;
+                    f[i] = sc[nt][0][e] + sc[nt][1][e];
+                    f[4 + i] = sc[nt][0][2 + e] + sc[nt][1][2 + e];
+                }
+                to_log2(f);
+                float x0[4], x1[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int key = kb + 8 * (i >> 1) + c2 + (i & 1);
+                    const bool in = key < kb + n1;
+                    x0[i] = in && key >= k0.x && key < k0.y ? f[i] - s0 * fabsf((float)(pos0 - key)) : -INFINITY;
+                    x1[i] = in && key >= k1.x && key < k1.y ? f[4 + i] - s1 * fabsf((float)(pos1 - key)) : -INFINITY;
                 }
                 float mx0 = fmaxf(fmaxf(x0[0], x0[1]), fmaxf(x0[2], x0[3]));
                 float mx1 = fmaxf(fmaxf(x1[0], x1[1]), fmaxf(x1[2], x1[3]));

@@ -80,9 +80,6 @@ __global__ void __launch_bounds__(UmmaCfg<D, MT>::kThreads, 1)
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
 
-    griddep_wait();  // the plan kernel's list of (sequence, tile group), longest first
-    const int nwork = a.plan_hdr[0] > 0 ? a.plan_hdr[0] * a.Hkv : 0;
-    if ((int)blockIdx.x >= nwork) return;
     const int G = a.Hq / a.Hkv;
 
     const uint32_t qb = base + (uint32_t)C::kQOff;
@@ -154,6 +151,8 @@ __global__ void __launch_bounds__(UmmaCfg<D, MT>::kThreads, 1)
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tbase = *tslot;
+    griddep_wait();  // the plan kernel's list of (sequence, tile group), longest first
+    const int nwork = a.plan_hdr[0] > 0 ? a.plan_hdr[0] * a.Hkv : 0;
 
     if (warp == 0 || warp == 2) {
         // ------------------------------------------------------------ producers: K (warp 0), V (warp 2)
@@ -398,8 +397,12 @@ __global__ void __launch_bounds__(UmmaCfg<D, MT>::kThreads, 1)
         const int wq = warp & 3;                 // TMEM lanes 32 * wq .. 32 * wq + 31
         const int r = 32 * wq + lane;            // row within the tile
         const ScoreCap score(a);
-        const bool shaped = score.cap || a.slopes != nullptr;
         const float sl = a.scale * kLog2e;
+        const float slope_units = sl > 0.f ? 1.f / sl : 1.f;  // a bias in the units of the logits below
+        // Capped logits lie within cap log2(e) of 0, so with bf16 weights (the exponents of fp32)
+        // and a cap of at most 59, 2^z, its sum over 2^20 keys and its low part stay
+        // normal numbers without a maximum: no maximum, no rescaling.  A bias has no bound.
+        const bool fixed = kBf16 && score.cap && sl > 0.f && !a.slopes && score.out <= 86.f;
         const uint32_t tl = tbase + ((uint32_t)(wq * 32) << 16);
         int g = 0, c = 0, ku = 0;
         bool ok = true;
@@ -443,22 +446,25 @@ __global__ void __launch_bounds__(UmmaCfg<D, MT>::kThreads, 1)
                 float f[C::kN];
 #pragma unroll
                 for (int cc = 0; cc < C::kN; ++cc) f[cc] = __uint_as_float(sv[cc >> 5][cc & 31]);
-                // plain positive scales are folded into the exponent's FFMA; else to log2 units here
+                // raw units (the positive scale is folded into the exponent's FFMA), or log2 units here
                 float mul = sl;
-                if (shaped || !(sl > 0.f)) {
-                    if (score.cap) {
+                if (!(sl > 0.f)) {
 #pragma unroll
-                        for (int cc = 0; cc < C::kN; ++cc) f[cc] = score.out * rational_tanh(score.in * f[cc]);
-                    } else {
-#pragma unroll
-                        for (int cc = 0; cc < C::kN; ++cc) f[cc] *= sl;
-                    }
-                    if (a.slopes) {
-                        const float d0 = (float)(pos - k0);
-#pragma unroll
-                        for (int cc = 0; cc < C::kN; ++cc) f[cc] = fmaf(-slope, fabsf(d0 - (float)cc), f[cc]);
-                    }
+                    for (int cc = 0; cc < C::kN; ++cc) f[cc] = score(f[cc]);
                     mul = 1.f;
+                } else if (score.cap) {
+                    float am[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) am[i] = fabsf(f[i]);
+#pragma unroll
+                    for (int cc = 8; cc < C::kN; ++cc) am[cc & 7] = fmaxf(am[cc & 7], fabsf(f[cc]));
+                    cap_in_place(f, score.in, fmaxf(fmaxf(fmaxf(am[0], am[1]), fmaxf(am[2], am[3])),
+                                                    fmaxf(fmaxf(am[4], am[5]), fmaxf(am[6], am[7]))));
+                }
+                if (a.slopes) {
+                    const float d0 = (float)(pos - k0), sr = slope * slope_units;
+#pragma unroll
+                    for (int cc = 0; cc < C::kN; ++cc) f[cc] = fmaf(-sr, fabsf(d0 - (float)cc), f[cc]);
                 }
                 if (!(__all_sync(0xffffffffu, vb <= 0 && ve >= C::kN) && mask == (1 << C::kBoxes) - 1)) {
                     // a step that some row sees in part, or over boxes not loaded
@@ -468,17 +474,21 @@ __global__ void __launch_bounds__(UmmaCfg<D, MT>::kThreads, 1)
                 }
                 // row maximum as 8 independent chains (a single 64-long chain of
                 // dependent max operations would sit on the critical path)
-                float mx[8];
+                bool need = false;
+                float alpha = 1.f;
+                if (!fixed) {
+                    float mx[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) mx[i] = f[i];
+                    for (int i = 0; i < 8; ++i) mx[i] = f[i];
 #pragma unroll
-                for (int cc = 8; cc < C::kN; ++cc) mx[cc & 7] = fmaxf(mx[cc & 7], f[cc]);
-                const float mr = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                       fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
-                const float mc = mr * mul;  // -inf when nothing is visible
-                const bool need = mc > m_used + 8.f;
-                const float alpha = (need && j > 0) ? ex2(m_used - mc) : 1.f;
-                if (need) m_used = mc;
+                    for (int cc = 8; cc < C::kN; ++cc) mx[cc & 7] = fmaxf(mx[cc & 7], f[cc]);
+                    const float mr = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                           fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+                    const float mc = mr * mul;  // -inf when nothing is visible
+                    need = mc > m_used + 8.f;
+                    alpha = (need && j > 0) ? ex2(m_used - mc) : 1.f;
+                    if (need) m_used = mc;
+                }
                 const float mu = m_used == -INFINITY ? 0.f : m_used;
                 // P = exp2(x - m) split into P_hi + P_lo, in registers before waiting,
                 // two keys per packed f32x2 operation; the row sum in 4 pair accumulators

@@ -71,35 +71,25 @@ __global__ void __launch_bounds__(1024) scored_decode_plan_kernel(const ScoredAr
     }
 }
 
-// Keys that some of the query rows i0 .. i1 - 1 (positions pos0 ..) of a sequence of
-// len tokens see, with key_begin / key_end arrays: the lanes of a warp share the
-// rows.  (0, 0) when no row sees any.
-__device__ __forceinline__ int2 span_of_rows(const ScoredArgs &a, int i0, int i1, int pos0, int len, int lane) {
-    int lo = INT_MAX, hi = 0;
-    for (int i = i0 + lane; i < i1; i += 32) {
-        const int2 k = row_range(a, i, pos0 + (i - i0), len);
-        if (k.x < k.y) {
-            lo = min(lo, k.x);
-            hi = max(hi, k.y);
-        }
-    }
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
-    return lo < hi ? make_int2(lo, hi) : make_int2(0, 0);
-}
-
 // Chunk calls.  An entry is a row block of a sequence -- the tcgen05 path's group
 // of one or two 128-row tiles, or the mma.sync path's 16 or 32 rows -- and, on
 // the mma.sync path, a partition: (sequence, block, lo, hi) or (sequence,
 // partition | block << 16, lo, hi), with the keys [lo, hi) that some row of the
-// block sees; most keys first.  Two passes over the blocks, a warp each (with
-// key_begin or key_end it reads its rows' ranges together): count, then place.
-// Rows with an empty range are zeroed here.  plan_hdr[0] = -1 when
-// query_start is not non-decreasing within [0, T].
+// block sees; most keys first.  Two passes over the blocks, a warp each: with
+// key_begin or key_end its lanes read the rows' ranges together and write the
+// zeros of empty ones, and the first pass keeps the spans for the second in
+// shared memory.  plan_hdr[0] = -1 when query_start is not non-decreasing
+// within [0, T].
+constexpr int kSeqCache = 2048;
+constexpr int kSpanCache = 2048;
+
 __global__ void __launch_bounds__(1024) scored_chunk_plan_kernel(const ScoredArgs a) {
     __shared__ int hist[kBins];
     __shared__ int start[kBins];
     __shared__ int warp_sums[32];
+    __shared__ int qs_cache[kSeqCache + 1];
+    __shared__ int len_cache[kSeqCache];
+    __shared__ int2 spans[kSpanCache];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -107,10 +97,18 @@ __global__ void __launch_bounds__(1024) scored_chunk_plan_kernel(const ScoredArg
     const int rows = a.umma_rows > 0 ? a.umma_rows : 16 * a.row_warps;  // query rows of a block
     const int Pt = a.umma_rows > 0 ? INT_MAX : a.partition_size;
     const int unit = a.umma_rows > 0 ? PA_CHUNK_UMMA_KEYS : 16;         // keys of a step
+    const bool cached = a.S <= kSeqCache;
+    if (cached) {
+        for (int s = tid; s <= a.S; s += blockDim.x) qs_cache[s] = a.query_start[s];
+        for (int s = tid; s < a.S; s += blockDim.x) len_cache[s] = a.context_lens[s];
+    }
     for (int i = tid; i < kBins; i += blockDim.x) hist[i] = 0;
     if (tid == 0) a.plan_hdr[1] = 0;
-    int bad = tid == 0 && (a.query_start[0] < 0 || a.query_start[a.S] > a.T);
-    for (int s = tid; s < a.S; s += blockDim.x) bad |= a.query_start[s] > a.query_start[s + 1];
+    __syncthreads();
+    const int *qs = cached ? qs_cache : a.query_start;
+    const int *lens = cached ? len_cache : a.context_lens;
+    int bad = tid == 0 && (qs[0] < 0 || qs[a.S] > a.T);
+    for (int s = tid; s < a.S; s += blockDim.x) bad |= qs[s] > qs[s + 1];
     if (__syncthreads_or(bad)) {
         if (tid == 0) {
             set_error(a.err, PA_DEVERR_BAD_LEN);
@@ -120,22 +118,37 @@ __global__ void __launch_bounds__(1024) scored_chunk_plan_kernel(const ScoredArg
     }
     const bool arrays = a.key_begin || a.key_end;  // else the ranges follow from the positions, and none is empty
     const int blocks = (int)(((long long)a.max_query_len * G + rows - 1) / rows);  // of a sequence, at most
+    const long long all = (long long)a.S * blocks;
     for (int pass = 0; pass < 2; ++pass) {
-        for (long long b = warp; b < (long long)a.S * blocks; b += 32) {
+        for (long long b = warp; b < all; b += 32) {
             const int s = (int)(b / blocks), rb = (int)(b % blocks);
-            const int q0 = a.query_start[s], n = a.query_start[s + 1] - q0, len = a.context_lens[s];
+            const int q0 = qs[s], n = qs[s + 1] - q0, len = lens[s];
             if (len < 0 || len > cap || n > len || n > a.max_query_len) {
                 if (pass == 0 && rb == 0 && lane == 0) set_error(a.err, PA_DEVERR_BAD_LEN);
                 continue;
             }
             if (rb * rows >= n * G) continue;
-            const int t0 = rb * rows / G, t1 = min(n, (rb * rows + rows + G - 1) / G);  // tokens of the block
+            const int t0 = rb * rows / G, t1 = min(n, (rb * rows + rows) / G);  // tokens of the block (G divides rows)
             int2 k;
-            if (arrays) {
-                k = span_of_rows(a, q0 + t0, q0 + t1, len - n + t0, len, lane);
-            } else {
-                k.x = row_range(a, 0, len - n + t0, len).x;
+            if (!arrays) {
+                k.x = a.window > 0 ? max(0, len - n + t0 - a.window + 1) : 0;
                 k.y = len - n + t1;
+            } else if (pass == 1 && b < kSpanCache) {
+                k = spans[b];
+            } else {
+                int lo = INT_MAX, hi = 0;
+                for (int t = t0 + lane; t < t1; t += 32) {
+                    const int2 r = row_range(a, q0 + t, len - n + t, len);
+                    if (r.x < r.y) {
+                        lo = min(lo, r.x);
+                        hi = max(hi, r.y);
+                    } else if (pass == 0) {
+                        zero_row(a, q0 + t);
+                    }
+                }
+                k.x = __reduce_min_sync(0xffffffffu, lo);
+                k.y = __reduce_max_sync(0xffffffffu, hi);
+                if (pass == 0 && b < kSpanCache && lane == 0) spans[b] = k;
             }
             if (k.x >= k.y) continue;
             const int p0 = k.x / Pt, p1 = (k.y - 1) / Pt;
@@ -156,13 +169,6 @@ __global__ void __launch_bounds__(1024) scored_chunk_plan_kernel(const ScoredArg
             if (tid == 0) a.plan_hdr[0] = total;
         }
     }
-    if (arrays)
-        for (int i = tid; i < a.T; i += blockDim.x) {
-            const RowOf r = row_of(a, i, cap);
-            if (r.s < 0) continue;
-            const int2 k = row_range(a, i, r.pos, r.len);
-            if (k.x >= k.y) zero_row(a, i);
-        }
 }
 
 }  // namespace
