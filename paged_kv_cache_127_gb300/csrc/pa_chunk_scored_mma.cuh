@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, HG, RW>::kThreads, ChunkCfg<D, HG,
     const int G = a.Hq / a.Hkv;
     const int Pt = a.partition_size;
     const int ngroups = a.Hkv / HG;
-    const int B = a.B;
+    const int lb = __ffs(a.B) - 1;  // block_size is a power of two
 
     const uint32_t full0 = base + (uint32_t)C::kFullOff;
     const uint32_t empty0 = base + (uint32_t)C::kEmptyOff;
@@ -144,8 +144,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, HG, RW>::kThreads, ChunkCfg<D, HG,
                 const int k16 = e.z & ~15;
                 e1 = make_int4((idx % ngroups) * HG, (e.w - k16 + 15) >> 4, 1, qs);
                 e2 = make_int4(n, a.context_lens[e.x], rb, 0);
-                const int blk0 = k16 / B;
-                const int nblk = (e.w - 1) / B - blk0 + 1;
+                const int blk0 = k16 >> lb;
+                const int nblk = ((e.w - 1) >> lb) - blk0 + 1;
                 const int32_t *row = a.block_tables + (size_t)e.x * a.max_blocks + blk0;
                 for (int i = lane; i < nblk; i += 32) {
                     int pb = row[i];
@@ -176,12 +176,12 @@ __global__ void __launch_bounds__(ChunkCfg<D, HG, RW>::kThreads, ChunkCfg<D, HG,
                 if (lane == 0) {
                     const uint32_t bar = full0 + 8 * st;
                     const int key = (e0.z & ~15) + 16 * c;
-                    const int pb = tb[key / B - (e0.z & ~15) / B];
+                    const int pb = tb[(key >> lb) - (e0.z >> lb)];
                     if (pb < 0) {
                         mbar_arrive(bar);  // bad table entry: complete the phase without data
                     } else {
                         const uint32_t dst = base + (uint32_t)(st * C::kStageBytes);
-                        const int y = key % B;
+                        const int y = key & (a.B - 1);
                         const int z = pb * a.Hkv + e1.x;
                         mbar_arrive_expect_tx(bar, C::kStageBytes);
 #pragma unroll
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, HG, RW>::kThreads, ChunkCfg<D, HG,
         const int4 e1 = info[3 * slot + 1];
         const int4 e2 = info[3 * slot + 2];
         if (!e1.z) break;  // no more work
-        const int p = e0.y, lo = e0.z, hi = e0.w, k16 = lo & ~15, blk0 = k16 / B;
+        const int p = e0.y, lo = e0.z, hi = e0.w, k16 = lo & ~15, blk0 = k16 >> lb;
         const int kvh = e1.x + head;
         const int nchunk = e1.y;
         const int qs = e1.w;
@@ -237,6 +237,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, HG, RW>::kThreads, ChunkCfg<D, HG,
         // keys that some row of this warp sees
         const int wend = __reduce_max_sync(0xffffffffu, max(k0.y, k1.y));
         const int wbegin = __reduce_min_sync(0xffffffffu, min(k0.x < k0.y ? k0.x : INT_MAX, k1.x < k1.y ? k1.x : INT_MAX));
+        // keys that every row of this warp sees, among the rows that see any
+        const int win0 = __reduce_max_sync(0xffffffffu, max(k0.x < k0.y ? k0.x : 0, k1.x < k1.y ? k1.x : 0));
+        const int win1 = __reduce_min_sync(0xffffffffu, min(k0.x < k0.y ? k0.y : INT_MAX, k1.x < k1.y ? k1.y : INT_MAX));
         const float s0 = a.slopes ? a.slopes[h0] * kLog2e : 0.f, s1 = a.slopes ? a.slopes[h1] * kLog2e : 0.f;
         {
             const uint16_t *qb = static_cast<const uint16_t *>(a.q);
@@ -266,9 +269,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, HG, RW>::kThreads, ChunkCfg<D, HG,
             }
             const int kb = k16 + 16 * j;
             const int n0 = max(lo - kb, 0);  // keys n0 .. n1 - 1 of the chunk are in the item's span
-            const int n1 = ctb[kb / B - blk0] < 0 ? 0 : min(16, hi - kb);
+            const int n1 = ctb[(kb >> lb) - blk0] < 0 ? 0 : min(16, hi - kb);
             // two full chunks that some row of this warp sees: one softmax step over 32 keys
-            const bool pair = C::kRegSplit && j + 1 < nchunk && n0 == 0 && n1 == 16 && ctb[(kb + 16) / B - blk0] >= 0 &&
+            const bool pair = C::kRegSplit && j + 1 < nchunk && n0 == 0 && n1 == 16 && ctb[((kb + 16) >> lb) - blk0] >= 0 &&
                               hi - kb >= 32 && kb + 16 < wend && kb + 16 > wbegin;
             if (pair) {
                 const int st2 = (cons + 1) % C::kStages;
@@ -325,9 +328,24 @@ __global__ void __launch_bounds__(ChunkCfg<D, HG, RW>::kThreads, ChunkCfg<D, HG,
                 float x0[8], x1[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int key = kb + 16 * (i >> 2) + 8 * (i >> 1 & 1) + c2 + (i & 1);
-                    x0[i] = key >= k0.x && key < k0.y ? f[i] - s0 * fabsf((float)(pos0 - key)) : -INFINITY;
-                    x1[i] = key >= k1.x && key < k1.y ? f[8 + i] - s1 * fabsf((float)(pos1 - key)) : -INFINITY;
+                    x0[i] = f[i];
+                    x1[i] = f[8 + i];
+                }
+                if (a.slopes) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int key = kb + 16 * (i >> 2) + 8 * (i >> 1 & 1) + c2 + (i & 1);
+                        x0[i] -= s0 * fabsf((float)(pos0 - key));
+                        x1[i] -= s1 * fabsf((float)(pos1 - key));
+                    }
+                }
+                if (kb < win0 || kb + 32 > win1) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int key = kb + 16 * (i >> 2) + 8 * (i >> 1 & 1) + c2 + (i & 1);
+                        if (key < k0.x || key >= k0.y) x0[i] = -INFINITY;
+                        if (key < k1.x || key >= k1.y) x1[i] = -INFINITY;
+                    }
                 }
                 float mx0 = x0[0], mx1 = x1[0];
 #pragma unroll

@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(UmmaCfg<D, MT>::kThreads, 1)
                 it = sl.it;
             }
             const int32_t *row = a.block_tables + (size_t)it.s * a.max_blocks;
-            const int j0 = it.lo / C::kN, B = a.B;
+            const int j0 = it.lo / C::kN, lb = __ffs(a.B) - 1;  // B is a power of two
             for (int j = j0; j < j0 + it.nch; ++j, ++g) {
                 const int st = g % C::kStages;
                 if (g >= C::kStages &&
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(UmmaCfg<D, MT>::kThreads, 1)
                         const int tok = j * C::kN + 16 * i;
                         blk[i] = -1;
                         if (tok + 15 >= it.lo && tok < it.hi) {
-                            const int pbk = row[tok / B];
+                            const int pbk = row[tok >> lb];
                             if (pbk >= 0 && pbk < a.N) {
                                 blk[i] = pbk;
                                 mask |= 1 << i;
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(UmmaCfg<D, MT>::kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < C::kBoxes; ++i) {
                             if (!(mask >> i & 1)) continue;
-                            const int y = (j * C::kN + 16 * i) % B;
+                            const int y = (j * C::kN + 16 * i) & (a.B - 1);
                             const int z = blk[i] * a.Hkv + it.kvh;
 #pragma unroll
                             for (int sb = 0; sb < C::kSub; ++sb)

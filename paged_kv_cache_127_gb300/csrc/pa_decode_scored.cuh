@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(ScoredDecodeCfg<D, HG>::kThreads, 2)
         // ------------------------------------------------------------ producer
         const uint64_t pol = policy_evict_first();
         const int nstatic = min(a.S, (int)gridDim.x / ngroups) * ngroups;  // items taken without the list
-        const int B = a.B;
+        const int lb = __ffs(a.B) - 1;  // block_size is a power of two
         bool listed = false;
         int n_items = 0;
         int iss = 0;  // chunks issued
@@ -148,9 +148,9 @@ __global__ void __launch_bounds__(ScoredDecodeCfg<D, HG>::kThreads, 2)
             const int k16 = e.z & ~15;  // first key of the first chunk
             const int nchunk = have ? (e.w - k16 + 15) >> 4 : 0;
             int32_t *tb = tbl + slot * kMaxPartitionBlocks;
-            const int blk0 = k16 / B;
+            const int blk0 = k16 >> lb;
             if (have) {
-                const int nblk = (e.w - 1) / B - blk0 + 1;
+                const int nblk = ((e.w - 1) >> lb) - blk0 + 1;
                 const int32_t *row = a.block_tables + (size_t)e.x * a.max_blocks + blk0;
                 for (int i = lane; i < nblk; i += 32) {
                     int pb = row[i];
@@ -184,12 +184,12 @@ __global__ void __launch_bounds__(ScoredDecodeCfg<D, HG>::kThreads, 2)
                 if (lane == 0) {
                     const uint32_t bar = full0 + 8 * st;
                     const int key = k16 + 16 * c;
-                    const int pb = tb[key / B - blk0];
+                    const int pb = tb[(key >> lb) - blk0];
                     if (pb < 0) {
                         mbar_arrive(bar);  // bad table entry: complete the phase without data
                     } else {
                         const uint32_t dst = base + (uint32_t)(st * C::kStageBytes);
-                        const int y = key % B;
+                        const int y = key & (a.B - 1);
                         const int z = pb * a.Hkv + g0;
                         mbar_arrive_expect_tx(bar, C::kStageBytes);
 #pragma unroll
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(ScoredDecodeCfg<D, HG>::kThreads, 2)
         const int nchunk = e1.y, pos = e1.w;
         const int h = kvh * G + g;
         const int32_t *ctb = tbl + slot * kMaxPartitionBlocks;
-        const int blk0 = k16 / a.B;
+        const int lb = __ffs(a.B) - 1, blk0 = k16 >> lb;
         const uint16_t *qrow = static_cast<const uint16_t *>(a.q) + ((size_t)s * a.Hq + h) * D;
 #pragma unroll
         for (int ks = 0; ks < C::kKS; ++ks) {
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(ScoredDecodeCfg<D, HG>::kThreads, 2)
             }
             const int kb = k16 + 16 * j;
             const int n0 = max(lo - kb, 0);                                         // keys n0 .. n1 - 1 of the chunk count
-            const int n1 = ctb[kb / a.B - blk0] < 0 ? 0 : min(16, hi - kb);
+            const int n1 = ctb[(kb >> lb) - blk0] < 0 ? 0 : min(16, hi - kb);
             const uint32_t kst = base + (uint32_t)(st * C::kStageBytes) + (uint32_t)(warp * C::kHeadSub);
             const uint32_t vst = kst + C::kTileBytes;
             float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
