@@ -38,8 +38,9 @@ struct ScoredArgs {
     float *ws_ml;                 // [T, Hq, P, 2]  (m in log2 units, l)
     float *ws_acc;                // [T, Hq, P, D]
     float *ws_logits;             // [S, Hq, cap] logits in log2 units; null without sums
-    int *plan_hdr;                // [0] work items, [1] claim counter, [2] CTAs done claiming
+    int *plan_hdr;                // [0] work items, [1] claim counter, [2] rows to merge
     int4 *plan_list;              // work items
+    int4 *merge_list;             // (row, first partition, last partition, -) of the rows to merge
     unsigned int *err;
     float *sums;                  // [sum_num_rows, Hkv, sum_cols], or null
     const int32_t *sum_rows;      // [S], or null: row s
@@ -78,7 +79,9 @@ cudaError_t launch_scored_umma_f16(const ScoredArgs &a, const CUtensorMap &tmk, 
 cudaError_t launch_scored_umma_bf16(const ScoredArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv,
                                     const CUtensorMap &tmq, const CUtensorMap &tmo, cudaStream_t st);
 
-// Merge of the split-K partials, and the sums of attention weights.
+// Merge of the split-K partials of the rows that the plan listed.
+cudaError_t launch_scored_merge(const ScoredArgs &a, bool bf16, cudaStream_t st);
+// The same without a list (f32 caches), and with the sums of attention weights.
 cudaError_t launch_scored_finish(const ScoredArgs &a, bool bf16, cudaStream_t st);
 // CUDA-core kernel, one CTA per (row, KV head, partition): f32 caches.
 cudaError_t launch_scored_rows(const ScoredArgs &a, int dtype, cudaStream_t st);

@@ -38,16 +38,19 @@ int32_t check_sums(const pa_key_sums *ks, int64_t cap) {
 // Scored-attention workspace, each part 256-byte aligned:
 //   header    3 ints: work items, claim counter, CTAs done claiming
 //   list      int4 [list_entries]
+//   merge     int4 [T]: rows whose range lies in several partitions (only with partials)
 //   acc, ml   float [T, Hq, P, D] and [T, Hq, P, 2]   (acc only if P > 1)
 //   logits    float [S, Hq, cap]                      (only with sums)
 struct ScoredLayout {
-    size_t list, acc, ml, logits, total;
+    size_t list, merge, acc, ml, logits, total;
 };
 ScoredLayout scored_layout(const pa_dims *d, size_t list_entries, size_t T, int32_t parts, bool partials, bool sums) {
     ScoredLayout L{};
     size_t off = 256;
     L.list = off;
     off += up256(list_entries * sizeof(int4));
+    L.merge = off;
+    off += partials ? up256(T * sizeof(int4)) : 0;
     L.acc = off;
     off += partials ? up256(T * d->num_q_heads * parts * d->head_dim * sizeof(float)) : 0;
     L.ml = off;
@@ -70,6 +73,9 @@ int32_t check_scored_chunk(const pa_dims *d, int32_t T, int32_t max_q, int32_t *
     const int32_t rc = pa::check_attention(d, pa::chunk_partition_size(d), parts);
     if (rc != PA_OK) return rc;
     if (T < 0 || max_q < 1 || max_q > (1 << 20) || d->num_seqs > 65535) return PA_ERR_INVALID;
+    // work items of the plan, at most: row blocks of every sequence (16 rows or more each) x partitions
+    const int64_t G = d->num_q_heads / d->num_kv_heads;
+    if ((max_q * G / 16 + 1) * d->num_seqs > INT32_MAX / *parts) return PA_ERR_INVALID;
     return (int64_t)T * d->num_q_heads > INT32_MAX ? PA_ERR_INVALID : PA_OK;
 }
 
@@ -90,6 +96,7 @@ void fill_args(pa::ScoredArgs &a, const pa_dims *d, const pa_score *sc, const Sc
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     a.plan_hdr = reinterpret_cast<int *>(ws);
     a.plan_list = reinterpret_cast<int4 *>(ws + L.list);
+    a.merge_list = reinterpret_cast<int4 *>(ws + L.merge);
     a.ws_acc = reinterpret_cast<float *>(ws + L.acc);
     a.ws_ml = reinterpret_cast<float *>(ws + L.ml);
     a.S = d->num_seqs;
@@ -183,7 +190,8 @@ int32_t pa_decode_scored(const pa_dims *dims, const pa_score *score, const void 
             e = bf16 ? pa::launch_scored_decode_bf16(a, tmk, tmv, st) : pa::launch_scored_decode_f16(a, tmk, tmv, st);
     }
     if (e != cudaSuccess) return to_status(e);
-    return to_status(pa::launch_scored_finish(a, bf16, st));
+    const bool listed = dims->kv_dtype != PA_F32 && !a.sums;
+    return to_status(listed ? pa::launch_scored_merge(a, bf16, st) : pa::launch_scored_finish(a, bf16, st));
 }
 
 size_t pa_chunk_scored_workspace_bytes(const pa_dims *dims, int32_t num_tokens, int32_t max_query_len) {
@@ -265,7 +273,7 @@ int32_t pa_chunk_scored(const pa_dims *dims, const pa_score *score, const void *
     if (e == cudaSuccess)
         e = bf16 ? pa::launch_scored_chunk_bf16(a, tmk, tmv, st) : pa::launch_scored_chunk_f16(a, tmk, tmv, st);
     if (e != cudaSuccess) return to_status(e);
-    return to_status(pa::launch_scored_finish(a, bf16, st));
+    return to_status(pa::launch_scored_merge(a, bf16, st));
 }
 
 int32_t pa_rope_write_kv(const pa_dims *dims, const pa_rope *rope, const void *q, int64_t q_stride, const void *k,

@@ -164,7 +164,104 @@ cudaError_t launch_finish_t(const ScoredArgs &a, cudaStream_t st) {
     }
 }
 
+// Partials p0 .. p0 + N - 1 (those below np) of one (row, head): every load first,
+// then the sums in partition order.
+template <int D, int N>
+__device__ __forceinline__ void merge_short(const float *ml, const float *acc, int np, float (&o)[D / 32], float &L) {
+    constexpr int kPer = D / 32;
+    float2 w[N];
+    float x[N][kPer];
+#pragma unroll
+    for (int p = 0; p < N; ++p)
+        if (p < np) {
+            w[p] = *reinterpret_cast<const float2 *>(ml + 2 * p);
+#pragma unroll
+            for (int e = 0; e < kPer; e += 2) {
+                const float2 v = *reinterpret_cast<const float2 *>(acc + (size_t)p * D + e);
+                x[p][e] = v.x;
+                x[p][e + 1] = v.y;
+            }
+        }
+    float M = -INFINITY;
+#pragma unroll
+    for (int p = 0; p < N; ++p)
+        if (p < np) M = fmaxf(M, w[p].x);
+    if (M == -INFINITY) M = 0.f;
+#pragma unroll
+    for (int p = 0; p < N; ++p)
+        if (p < np) {
+            const float t = ex2(w[p].x - M);
+            L = fmaf(t, w[p].y, L);
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) o[e] = fmaf(t, x[p][e], o[e]);
+        }
+}
+
+// One warp per listed (row, head), lane i owning D / 32 columns; the blocks stride over the list.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) scored_merge_kernel(const ScoredArgs a) {
+    constexpr int kPer = D / 32;
+    const int lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const long long n = (long long)a.plan_hdr[2] * a.Hq;
+    for (long long w = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); w < n;
+         w += (long long)gridDim.x * (kThreads / 32)) {
+        const int4 e = a.merge_list[w / a.Hq];
+        const size_t head = (size_t)e.x * a.Hq + (int)(w % a.Hq);
+        const int np = e.z - e.y + 1;
+        const float *ml = a.ws_ml + 2 * (head * a.max_parts + e.y);
+        const float *acc = a.ws_acc + (head * a.max_parts + e.y) * D + lane * kPer;
+        float o[kPer], L = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) o[i] = 0.f;
+        if (np <= 2) {
+            merge_short<D, 2>(ml, acc, np, o, L);
+        } else if (np <= 8) {
+            merge_short<D, 8>(ml, acc, np, o, L);
+        } else {
+            const float2 t = merged_ml(ml, 0, np - 1, lane);
+            L = t.y;
+#pragma unroll 8
+            for (int p = 0; p < np; ++p) {
+                const float x = ex2(ml[2 * p] - t.x);
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) o[i] = fmaf(x, acc[(size_t)p * D + i], o[i]);
+            }
+        }
+        const float inv = L != 0.f ? 1.f / L : 0.f;
+        const size_t at = head * D + lane * kPer;
+#pragma unroll
+        for (int i = 0; i < kPer; i += 2) {
+            if (a.out16) *reinterpret_cast<uint32_t *>(static_cast<T *>(a.out) + at + i) = Mma16<T>::pack(o[i] * inv, o[i + 1] * inv);
+            else *reinterpret_cast<float2 *>(static_cast<float *>(a.out) + at + i) = make_float2(o[i] * inv, o[i + 1] * inv);
+        }
+    }
+}
+
+template <typename T, int D>
+cudaError_t launch_merge_t(const ScoredArgs &a, cudaStream_t st) {
+    if (a.max_parts == 1) return cudaSuccess;
+    const long long blocks = ((long long)a.T * a.Hq + kThreads / 32 - 1) / (kThreads / 32);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(blocks < 8 * 152 ? blocks : 8 * 152));  // one resident wave at most
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, scored_merge_kernel<T, D>, a);
+}
+
 }  // namespace
+
+cudaError_t launch_scored_merge(const ScoredArgs &a, bool bf16, cudaStream_t st) {
+    if (a.D == 64) return bf16 ? launch_merge_t<__nv_bfloat16, 64>(a, st) : launch_merge_t<__half, 64>(a, st);
+    if (a.D == 128) return bf16 ? launch_merge_t<__nv_bfloat16, 128>(a, st) : launch_merge_t<__half, 128>(a, st);
+    return cudaErrorNotSupported;
+}
 
 cudaError_t launch_scored_finish(const ScoredArgs &a, bool bf16, cudaStream_t st) {
     if (a.D == 64) return bf16 ? launch_finish_t<__nv_bfloat16, 64>(a, st) : launch_finish_t<__half, 64>(a, st);

@@ -35,9 +35,10 @@ __global__ void __launch_bounds__(1024) scored_decode_plan_kernel(const ScoredAr
     const int groups = a.Hkv / a.head_group;
     const int nstatic = min(a.S, a.ctas / groups);
     for (int i = tid; i < kBins; i += blockDim.x) hist[i] = 0;
+    __shared__ int merges;  // sequences whose range lies in several partitions
     if (tid == 0) {
         a.plan_hdr[1] = 0;
-        a.plan_hdr[2] = 0;
+        merges = 0;
     }
     __syncthreads();
     for (int s = tid; s < a.S; s += blockDim.x) {
@@ -50,6 +51,7 @@ __global__ void __launch_bounds__(1024) scored_decode_plan_kernel(const ScoredAr
             continue;
         }
         const int p0 = k.x / Pt, p1 = (k.y - 1) / Pt;
+        if (p0 != p1) a.merge_list[atomicAdd(&merges, 1)] = make_int4(s, p0, p1, 0);
         for (int p = s < nstatic ? p0 + 1 : p0; p <= p1; ++p) {
             const int lo = max(k.x, p * Pt), hi = min(k.y, (p + 1) * Pt);
             atomicAdd(&hist[min((hi - (lo & ~15) + 15) >> 4, kBins - 1)], 1);
@@ -57,7 +59,10 @@ __global__ void __launch_bounds__(1024) scored_decode_plan_kernel(const ScoredAr
     }
     __syncthreads();
     const int total = scan_bins_desc(hist, start, kBins - 1, kBins, warp_sums);
-    if (tid == 0) a.plan_hdr[0] = total * groups;
+    if (tid == 0) {
+        a.plan_hdr[0] = total * groups;
+        a.plan_hdr[2] = merges;
+    }
     for (int s = tid; s < a.S; s += blockDim.x) {
         const RowOf r = row_of(a, s, cap);
         const int2 k = row_range(a, s, r.pos, r.len);
@@ -75,11 +80,12 @@ __global__ void __launch_bounds__(1024) scored_decode_plan_kernel(const ScoredAr
 // of one or two 128-row tiles, or the mma.sync path's 16 or 32 rows -- and, on
 // the mma.sync path, a partition: (sequence, block, lo, hi) or (sequence,
 // partition | block << 16, lo, hi), with the keys [lo, hi) that some row of the
-// block sees; most keys first.  Two passes over the blocks, a warp each: with
-// key_begin or key_end its lanes read the rows' ranges together and write the
-// zeros of empty ones, and the first pass keeps the spans for the second in
-// shared memory.  plan_hdr[0] = -1 when query_start is not non-decreasing
-// within [0, T].
+// block sees; most keys first.  Two passes over the blocks, counting and
+// placing: a thread each while the ranges follow from the positions, a warp each with
+// key_begin or key_end (its lanes read the rows' ranges together, write the zeros of
+// empty ones, and the first pass keeps the spans for the second).  On the mma.sync path
+// the rows whose range lies in several partitions are listed for the merge.
+// plan_hdr[0] = -1 when query_start is not non-decreasing within [0, T].
 constexpr int kSeqCache = 2048;
 constexpr int kSpanCache = 2048;
 
@@ -90,11 +96,13 @@ __global__ void __launch_bounds__(1024) scored_chunk_plan_kernel(const ScoredArg
     __shared__ int qs_cache[kSeqCache + 1];
     __shared__ int len_cache[kSeqCache];
     __shared__ int2 spans[kSpanCache];
+    __shared__ int merges;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
     const int G = a.Hq / a.Hkv, cap = a.max_blocks * a.B;
     const int rows = a.umma_rows > 0 ? a.umma_rows : 16 * a.row_warps;  // query rows of a block
+    const int tokens = rows / G;                                        // its tokens (G divides rows)
     const int Pt = a.umma_rows > 0 ? INT_MAX : a.partition_size;
     const int unit = a.umma_rows > 0 ? PA_CHUNK_UMMA_KEYS : 16;         // keys of a step
     const bool cached = a.S <= kSeqCache;
@@ -103,7 +111,10 @@ __global__ void __launch_bounds__(1024) scored_chunk_plan_kernel(const ScoredArg
         for (int s = tid; s < a.S; s += blockDim.x) len_cache[s] = a.context_lens[s];
     }
     for (int i = tid; i < kBins; i += blockDim.x) hist[i] = 0;
-    if (tid == 0) a.plan_hdr[1] = 0;
+    if (tid == 0) {
+        a.plan_hdr[1] = 0;
+        merges = 0;
+    }
     __syncthreads();
     const int *qs = cached ? qs_cache : a.query_start;
     const int *lens = cached ? len_cache : a.context_lens;
@@ -113,22 +124,25 @@ __global__ void __launch_bounds__(1024) scored_chunk_plan_kernel(const ScoredArg
         if (tid == 0) {
             set_error(a.err, PA_DEVERR_BAD_LEN);
             a.plan_hdr[0] = -1;
+            a.plan_hdr[2] = 0;
         }
         return;
     }
+    for (int s = tid; s < a.S; s += blockDim.x) {
+        const int len = lens[s], n = qs[s + 1] - qs[s];
+        if (len < 0 || len > cap || n > len || n > a.max_query_len) set_error(a.err, PA_DEVERR_BAD_LEN);
+    }
     const bool arrays = a.key_begin || a.key_end;  // else the ranges follow from the positions, and none is empty
-    const int blocks = (int)(((long long)a.max_query_len * G + rows - 1) / rows);  // of a sequence, at most
-    const long long all = (long long)a.S * blocks;
+    const int blocks = (a.max_query_len + tokens - 1) / tokens;  // of a sequence, at most
+    const unsigned all = (unsigned)a.S * (unsigned)blocks;       // bounded by the entry point
+    const unsigned first = arrays ? tid >> 5 : tid, stride = arrays ? 32 : 1024;
+    const int l0 = arrays ? lane : 0, lstep = arrays ? 32 : 1;   // the lanes of a warp share a block's partitions
     for (int pass = 0; pass < 2; ++pass) {
-        for (long long b = warp; b < all; b += 32) {
-            const int s = (int)(b / blocks), rb = (int)(b % blocks);
+        for (unsigned b = first; b < all; b += stride) {
+            const int s = (int)(b / (unsigned)blocks), rb = (int)(b - (unsigned)s * (unsigned)blocks);
             const int q0 = qs[s], n = qs[s + 1] - q0, len = lens[s];
-            if (len < 0 || len > cap || n > len || n > a.max_query_len) {
-                if (pass == 0 && rb == 0 && lane == 0) set_error(a.err, PA_DEVERR_BAD_LEN);
-                continue;
-            }
-            if (rb * rows >= n * G) continue;
-            const int t0 = rb * rows / G, t1 = min(n, (rb * rows + rows) / G);  // tokens of the block (G divides rows)
+            if (len < 0 || len > cap || n > len || n > a.max_query_len || rb * tokens >= n) continue;
+            const int t0 = rb * tokens, t1 = min(n, t0 + tokens);
             int2 k;
             if (!arrays) {
                 k.x = a.window > 0 ? max(0, len - n + t0 - a.window + 1) : 0;
@@ -152,7 +166,7 @@ __global__ void __launch_bounds__(1024) scored_chunk_plan_kernel(const ScoredArg
             }
             if (k.x >= k.y) continue;
             const int p0 = k.x / Pt, p1 = (k.y - 1) / Pt;
-            for (int p = p0 + lane; p <= p1; p += 32) {
+            for (int p = p0 + l0; p <= p1; p += lstep) {
                 const int lo = p == p0 ? k.x : p * Pt, hi = p == p1 ? k.y : (p + 1) * Pt;
                 const int bin = min((hi - 1) / unit - lo / unit + 1, kBins - 1);
                 if (pass == 0) {
@@ -163,10 +177,28 @@ __global__ void __launch_bounds__(1024) scored_chunk_plan_kernel(const ScoredArg
                 }
             }
         }
+        if (pass == 0 && a.umma_rows == 0 && a.max_parts > 1) {
+            for (int i = tid; i < a.T; i += blockDim.x) {
+                int s0 = 0, s1 = a.S;  // qs[s0] <= i (or s0 == 0), the row's sequence in [s0, s1)
+                while (s1 - s0 > 1) {
+                    const int mid = (s0 + s1) >> 1;
+                    if (qs[mid] <= i) s0 = mid; else s1 = mid;
+                }
+                const int n = qs[s0 + 1] - qs[s0], len = lens[s0], t = i - qs[s0];
+                if (t < 0 || t >= n || len < 0 || len > cap || n > len || n > a.max_query_len) continue;
+                const int2 k = row_range(a, i, len - n + t, len);
+                if (k.x >= k.y) continue;
+                const int p0 = k.x / Pt, p1 = (k.y - 1) / Pt;
+                if (p0 != p1) a.merge_list[atomicAdd(&merges, 1)] = make_int4(i, p0, p1, 0);
+            }
+        }
         __syncthreads();
         if (pass == 0) {
             const int total = scan_bins_desc(hist, start, kBins - 1, kBins, warp_sums);
-            if (tid == 0) a.plan_hdr[0] = total;
+            if (tid == 0) {
+                a.plan_hdr[0] = total;
+                a.plan_hdr[2] = merges;
+            }
         }
     }
 }
