@@ -29,6 +29,29 @@
 
 namespace pa {
 
+// What a kernel's softmax does to the logits, fixed at compile time so that the
+// others' state takes no registers in the loop (at most 128 a thread).  All but
+// kGeneral need a positive scale.
+enum ScoredMode {
+    kMaskOnly,   // ranges only
+    kCapFixed,   // bf16, cap of at most 59: no running maximum (see below)
+    kCapMax,     // cap, running maximum
+    kBias,       // distance bias
+    kGeneral,    // cap and bias, or a scale that is not positive
+};
+inline ScoredMode scored_mode(const ScoredArgs &a, bool bf16) {
+    if (!(a.scale > 0.f) || (a.softcap > 0.f && a.slopes)) return kGeneral;
+    if (a.slopes) return kBias;
+    if (a.softcap > 0.f) return bf16 && a.softcap * kLog2e <= 86.f ? kCapFixed : kCapMax;
+    return kMaskOnly;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // One work item: KV head kvh of the plan's entry (sequence s, tile group), i.e.
 // rows r0 .. r0 + 128 MT - 1 of that head's (query token, query head) rows, and
 // the keys [lo, hi) that some of those rows see, in nch steps from j0 on.
@@ -65,7 +88,7 @@ __device__ __forceinline__ bool scored_item(const ScoredArgs &a, int w, int nwor
 // The ring's stage and phase follow the count g of steps so far, the S/P buffers
 // and their phases the count c of the tile's own steps, the slots and query-tile
 // sets the count of items published.
-template <typename T, int D, int MT>
+template <typename T, int D, int MT, int kMode>
 __global__ void __launch_bounds__(UmmaCfg<D, MT>::kThreads, 1)
     scored_umma_kernel(const ScoredArgs a, const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmq,
@@ -396,13 +419,15 @@ __global__ void __launch_bounds__(UmmaCfg<D, MT>::kThreads, 1)
         const int u = (warp - C::kSoftWarp0) / 4;  // tile of this warpgroup
         const int wq = warp & 3;                 // TMEM lanes 32 * wq .. 32 * wq + 31
         const int r = 32 * wq + lane;            // row within the tile
-        const ScoreCap score(a);
         const float sl = a.scale * kLog2e;
-        const float slope_units = sl > 0.f ? 1.f / sl : 1.f;  // a bias in the units of the logits below
-        // Capped logits lie within cap log2(e) of 0, so with bf16 weights (the exponents of fp32)
-        // and a cap of at most 59, 2^z, its sum over 2^20 keys and its low part stay
-        // normal numbers without a maximum: no maximum, no rescaling.  A bias has no bound.
-        const bool fixed = kBf16 && score.cap && sl > 0.f && !a.slopes && score.out <= 86.f;
+        // a bias in the units of the logits below (raw, or log2 with a scale that is not positive)
+        const float slope_units = kMode == kGeneral && !(sl > 0.f) ? 1.f : 1.f / sl;
+        // kCapFixed: capped logits lie within cap log2(e) <= 86 of 0, so with bf16 weights (the
+        // exponents of fp32) 2^z, its sum over 2^20 keys and its low part stay normal numbers
+        // without a maximum: no maximum, no rescaling.  A bias has no such bound.
+        constexpr bool kCap = kMode == kCapFixed || kMode == kCapMax;
+        constexpr bool kSlopes = kMode == kBias || kMode == kGeneral;
+        static_assert(kMode != kCapFixed || kBf16, "f16 weights need the maximum");
         const uint32_t tl = tbase + ((uint32_t)(wq * 32) << 16);
         int g = 0, c = 0, ku = 0;
         bool ok = true;
@@ -425,7 +450,7 @@ __global__ void __launch_bounds__(UmmaCfg<D, MT>::kThreads, 1)
             const int t = R / G;
             const int pos = it.len - n + t;
             const int2 range = t < n ? row_range(a, it.qs + t, pos, it.len) : make_int2(0, 0);
-            const float slope = a.slopes ? a.slopes[it.kvh * G + R % G] * kLog2e : 0.f;
+            const float slope = kSlopes && a.slopes ? a.slopes[it.kvh * G + R % G] * kLog2e * slope_units : 0.f;
             const int k_first = it.lo / C::kN * C::kN;
             float m_used = -INFINITY, l = 0.f;
             for (int j = 0; j < nch; ++j, ++g, ++c) {
@@ -448,23 +473,21 @@ __global__ void __launch_bounds__(UmmaCfg<D, MT>::kThreads, 1)
                 for (int cc = 0; cc < C::kN; ++cc) f[cc] = __uint_as_float(sv[cc >> 5][cc & 31]);
                 // raw units (the positive scale is folded into the exponent's FFMA), or log2 units here
                 float mul = sl;
-                if (!(sl > 0.f)) {
+                if (kMode == kGeneral && !(sl > 0.f)) {
+                    const ScoreCap score(a);
 #pragma unroll
                     for (int cc = 0; cc < C::kN; ++cc) f[cc] = score(f[cc]);
                     mul = 1.f;
-                } else if (score.cap) {
-                    float am[8];
+                } else if (kCap || (kMode == kGeneral && a.softcap > 0.f)) {
+                    float am[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) am[i] = fabsf(f[i]);
-#pragma unroll
-                    for (int cc = 8; cc < C::kN; ++cc) am[cc & 7] = fmaxf(am[cc & 7], fabsf(f[cc]));
-                    cap_in_place(f, score.in, fmaxf(fmaxf(fmaxf(am[0], am[1]), fmaxf(am[2], am[3])),
-                                                    fmaxf(fmaxf(am[4], am[5]), fmaxf(am[6], am[7]))));
+                    for (int cc = 0; cc < C::kN; cc += 2) am[cc >> 1 & 3] = max3(am[cc >> 1 & 3], fabsf(f[cc]), fabsf(f[cc + 1]));
+                    cap_in_place(f, a.scale / a.softcap, fmaxf(fmaxf(am[0], am[1]), fmaxf(am[2], am[3])));
                 }
-                if (a.slopes) {
-                    const float d0 = (float)(pos - k0), sr = slope * slope_units;
+                if (kSlopes) {
+                    const float d0 = (float)(pos - k0);
 #pragma unroll
-                    for (int cc = 0; cc < C::kN; ++cc) f[cc] = fmaf(-sr, fabsf(d0 - (float)cc), f[cc]);
+                    for (int cc = 0; cc < C::kN; ++cc) f[cc] = fmaf(-slope, fabsf(d0 - (float)cc), f[cc]);
                 }
                 if (!(__all_sync(0xffffffffu, vb <= 0 && ve >= C::kN) && mask == (1 << C::kBoxes) - 1)) {
                     // a step that some row sees in part, or over boxes not loaded
@@ -476,7 +499,7 @@ __global__ void __launch_bounds__(UmmaCfg<D, MT>::kThreads, 1)
                 // dependent max operations would sit on the critical path)
                 bool need = false;
                 float alpha = 1.f;
-                if (!fixed) {
+                if (kMode != kCapFixed) {
                     float mx[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) mx[i] = f[i];
@@ -723,14 +746,14 @@ __global__ void __launch_bounds__(UmmaCfg<D, MT>::kThreads, 1)
     }
 }
 
-template <typename T, int D, int MT>
+template <typename T, int D, int MT, int kMode>
 cudaError_t launch_scored_umma_t(const ScoredArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv,
                                  const CUtensorMap &tmq, const CUtensorMap &tmo, cudaStream_t st) {
     using C = UmmaCfg<D, MT>;
     static std::atomic<int> sms_of[kMaxLaunchDevices];
     int sms = 0;
     cudaError_t e = per_device_value(sms_of, &sms, [](int dev, int *v) {
-        cudaError_t r = cudaFuncSetAttribute(scored_umma_kernel<T, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t r = cudaFuncSetAttribute(scored_umma_kernel<T, D, MT, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)C::kSmem);
         if (r != cudaSuccess) return r;
         return cudaDeviceGetAttribute(v, cudaDevAttrMultiProcessorCount, dev);
@@ -752,19 +775,19 @@ cudaError_t launch_scored_umma_t(const ScoredArgs &a, const CUtensorMap &tmk, co
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, scored_umma_kernel<T, D, MT>, a, tmk, tmv, tmq, tmo);
+    return cudaLaunchKernelEx(&cfg, scored_umma_kernel<T, D, MT, kMode>, a, tmk, tmv, tmq, tmo);
 }
 
 // Two tiles per CTA once a sequence can fill them (chunk_umma_rows).
-template <typename T>
-cudaError_t dispatch_scored_umma(const ScoredArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv,
-                                 const CUtensorMap &tmq, const CUtensorMap &tmo, cudaStream_t st) {
+template <typename T, int kMode>
+cudaError_t launch_scored_umma(const ScoredArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv,
+                               const CUtensorMap &tmq, const CUtensorMap &tmo, cudaStream_t st) {
     if (a.D == 64)
-        return a.umma_rows == 256 ? launch_scored_umma_t<T, 64, 2>(a, tmk, tmv, tmq, tmo, st)
-                                  : launch_scored_umma_t<T, 64, 1>(a, tmk, tmv, tmq, tmo, st);
+        return a.umma_rows == 256 ? launch_scored_umma_t<T, 64, 2, kMode>(a, tmk, tmv, tmq, tmo, st)
+                                  : launch_scored_umma_t<T, 64, 1, kMode>(a, tmk, tmv, tmq, tmo, st);
     if (a.D == 128)
-        return a.umma_rows == 256 ? launch_scored_umma_t<T, 128, 2>(a, tmk, tmv, tmq, tmo, st)
-                                  : launch_scored_umma_t<T, 128, 1>(a, tmk, tmv, tmq, tmo, st);
+        return a.umma_rows == 256 ? launch_scored_umma_t<T, 128, 2, kMode>(a, tmk, tmv, tmq, tmo, st)
+                                  : launch_scored_umma_t<T, 128, 1, kMode>(a, tmk, tmv, tmq, tmo, st);
     return cudaErrorNotSupported;
 }
 

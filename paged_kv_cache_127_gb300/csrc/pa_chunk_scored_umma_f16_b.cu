@@ -1,0 +1,15 @@
+// pa_chunk_scored_umma_f16_b.cu -- scored chunk attention for f16 KV caches, the
+// tcgen05 kernel: bias, general (translation units of their own,
+// to compile in parallel).
+#include "pa_chunk_scored_umma.cuh"
+
+namespace pa {
+cudaError_t launch_scored_umma_f16_bias(const ScoredArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv,
+    const CUtensorMap &tmq, const CUtensorMap &tmo, cudaStream_t st) {
+    return launch_scored_umma<__half, kBias>(a, tmk, tmv, tmq, tmo, st);
+}
+cudaError_t launch_scored_umma_f16_general(const ScoredArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv,
+    const CUtensorMap &tmq, const CUtensorMap &tmo, cudaStream_t st) {
+    return launch_scored_umma<__half, kGeneral>(a, tmk, tmv, tmq, tmo, st);
+}
+}  // namespace pa

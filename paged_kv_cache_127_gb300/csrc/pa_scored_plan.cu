@@ -81,9 +81,9 @@ __global__ void __launch_bounds__(1024) scored_decode_plan_kernel(const ScoredAr
 // the mma.sync path, a partition: (sequence, block, lo, hi) or (sequence,
 // partition | block << 16, lo, hi), with the keys [lo, hi) that some row of the
 // block sees; most keys first.  Two passes over the blocks, counting and
-// placing: a thread each while the ranges follow from the positions, a warp each with
-// key_begin or key_end (its lanes read the rows' ranges together, write the zeros of
-// empty ones, and the first pass keeps the spans for the second).  On the mma.sync path
+// placing, a thread each.  With key_begin or key_end the blocks' spans come
+// first, a thread per row into shared memory (zeroing empty rows on the way); calls of
+// more than kSpanCache blocks take a warp per block in both passes instead.  On the mma.sync path
 // the rows whose range lies in several partitions are listed for the merge.
 // plan_hdr[0] = -1 when query_start is not non-decreasing within [0, T].
 constexpr int kSeqCache = 2048;
@@ -132,9 +132,60 @@ __global__ void __launch_bounds__(1024) scored_chunk_plan_kernel(const ScoredArg
         const int len = lens[s], n = qs[s + 1] - qs[s];
         if (len < 0 || len > cap || n > len || n > a.max_query_len) set_error(a.err, PA_DEVERR_BAD_LEN);
     }
-    const bool arrays = a.key_begin || a.key_end;  // else the ranges follow from the positions, and none is empty
     const int blocks = (a.max_query_len + tokens - 1) / tokens;  // of a sequence, at most
     const unsigned all = (unsigned)a.S * (unsigned)blocks;       // bounded by the entry point
+    // The row's sequence, or -1 (qs[s0] <= i, or s0 == 0; the row's sequence in [s0, s1)).
+    auto seq_of = [&](int i) {
+        int s0 = 0, s1 = a.S;
+        while (s1 - s0 > 1) {
+            const int mid = (s0 + s1) >> 1;
+            if (qs[mid] <= i) s0 = mid; else s1 = mid;
+        }
+        const int n = qs[s0 + 1] - qs[s0], len = lens[s0], t = i - qs[s0];
+        return t < 0 || t >= n || len < 0 || len > cap || n > len || n > a.max_query_len ? -1 : s0;
+    };
+    const bool masks = a.key_begin || a.key_end;  // else the ranges follow from the positions, and none is empty
+    const bool in_smem = masks && all <= kSpanCache;
+    if (in_smem) {
+        for (unsigned b = tid; b < all; b += 1024) spans[b] = make_int2(INT_MAX, 0);
+        __syncthreads();
+        for (int i0 = 0; i0 < a.T; i0 += 4096) {
+            int begin[4], end[4];  // four rows a thread in flight
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = i0 + 1024 * e + tid;
+                begin[e] = a.key_begin && i < a.T ? a.key_begin[i] : 0;
+                end[e] = a.key_end && i < a.T ? a.key_end[i] : INT_MAX;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = i0 + 1024 * e + tid;
+                int lo = INT_MAX, hi = 0, b = -1;
+                const int s = i < a.T ? seq_of(i) : -1;
+                if (s >= 0) {
+                    const int t = i - qs[s], pos = lens[s] - (qs[s + 1] - qs[s]) + t;
+                    const int x = max(max(0, begin[e]), a.window > 0 ? pos - a.window + 1 : 0);
+                    const int y = min(lens[s], a.key_end ? end[e] : pos + 1);
+                    b = s * blocks + t / tokens;
+                    if (x < y) lo = x, hi = y;
+                    else zero_row(a, i);
+                }
+                // neighbouring rows mostly share their block: one update a warp then
+                int same;
+                __match_all_sync(0xffffffffu, b, &same);
+                if (same) {
+                    lo = __reduce_min_sync(0xffffffffu, lo);
+                    hi = __reduce_max_sync(0xffffffffu, hi);
+                }
+                if (b >= 0 && lo < hi && (!same || lane == 0)) {
+                    atomicMin(&spans[b].x, lo);
+                    atomicMax(&spans[b].y, hi);
+                }
+            }
+        }
+        __syncthreads();
+    }
+    const bool arrays = masks && !in_smem;
     const unsigned first = arrays ? tid >> 5 : tid, stride = arrays ? 32 : 1024;
     const int l0 = arrays ? lane : 0, lstep = arrays ? 32 : 1;   // the lanes of a warp share a block's partitions
     for (int pass = 0; pass < 2; ++pass) {
@@ -144,11 +195,11 @@ __global__ void __launch_bounds__(1024) scored_chunk_plan_kernel(const ScoredArg
             if (len < 0 || len > cap || n > len || n > a.max_query_len || rb * tokens >= n) continue;
             const int t0 = rb * tokens, t1 = min(n, t0 + tokens);
             int2 k;
-            if (!arrays) {
+            if (in_smem) {
+                k = spans[b];
+            } else if (!masks) {
                 k.x = a.window > 0 ? max(0, len - n + t0 - a.window + 1) : 0;
                 k.y = len - n + t1;
-            } else if (pass == 1 && b < kSpanCache) {
-                k = spans[b];
             } else {
                 int lo = INT_MAX, hi = 0;
                 for (int t = t0 + lane; t < t1; t += 32) {
@@ -162,7 +213,6 @@ __global__ void __launch_bounds__(1024) scored_chunk_plan_kernel(const ScoredArg
                 }
                 k.x = __reduce_min_sync(0xffffffffu, lo);
                 k.y = __reduce_max_sync(0xffffffffu, hi);
-                if (pass == 0 && b < kSpanCache && lane == 0) spans[b] = k;
             }
             if (k.x >= k.y) continue;
             const int p0 = k.x / Pt, p1 = (k.y - 1) / Pt;
@@ -179,13 +229,9 @@ __global__ void __launch_bounds__(1024) scored_chunk_plan_kernel(const ScoredArg
         }
         if (pass == 0 && a.umma_rows == 0 && a.max_parts > 1) {
             for (int i = tid; i < a.T; i += blockDim.x) {
-                int s0 = 0, s1 = a.S;  // qs[s0] <= i (or s0 == 0), the row's sequence in [s0, s1)
-                while (s1 - s0 > 1) {
-                    const int mid = (s0 + s1) >> 1;
-                    if (qs[mid] <= i) s0 = mid; else s1 = mid;
-                }
-                const int n = qs[s0 + 1] - qs[s0], len = lens[s0], t = i - qs[s0];
-                if (t < 0 || t >= n || len < 0 || len > cap || n > len || n > a.max_query_len) continue;
+                const int s = seq_of(i);
+                if (s < 0) continue;
+                const int n = qs[s + 1] - qs[s], len = lens[s], t = i - qs[s];
                 const int2 k = row_range(a, i, len - n + t, len);
                 if (k.x >= k.y) continue;
                 const int p0 = k.x / Pt, p1 = (k.y - 1) / Pt;
