@@ -82,6 +82,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, HG, RW>::kThreads, ChunkCfg<D, HG,
     const uint32_t vx = (uint32_t)((lm >> 1) ^ lr);   // and for V reads
     const ScoreCap score(a);
     const float sl = a.scale * kLog2e;
+    const CapFit fit(score.in);
     // dot products to logits in log2 units
     auto to_log2 = [&](auto &f) {
         constexpr int N = sizeof(f) / sizeof(f[0]);
@@ -89,7 +90,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, HG, RW>::kThreads, ChunkCfg<D, HG,
             float most = fabsf(f[0]);
 #pragma unroll
             for (int i = 1; i < N; ++i) most = fmaxf(most, fabsf(f[i]));
-            cap_in_place(f, score.in, most);
+            cap_in_place(f, fit, most);
         }
         if (score.cap && !(sl > 0.f)) {
 #pragma unroll

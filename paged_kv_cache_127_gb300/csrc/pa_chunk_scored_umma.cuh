@@ -427,6 +427,7 @@ __global__ void __launch_bounds__(UmmaCfg<D, MT>::kThreads, 1)
         // without a maximum: no maximum, no rescaling.  A bias has no such bound.
         constexpr bool kCap = kMode == kCapFixed || kMode == kCapMax;
         constexpr bool kSlopes = kMode == kBias || kMode == kGeneral;
+        const CapFit fit(a.softcap > 0.f ? a.scale / a.softcap : 0.f);
         static_assert(kMode != kCapFixed || kBf16, "f16 weights need the maximum");
         const uint32_t tl = tbase + ((uint32_t)(wq * 32) << 16);
         int g = 0, c = 0, ku = 0;
@@ -482,12 +483,27 @@ __global__ void __launch_bounds__(UmmaCfg<D, MT>::kThreads, 1)
                     float am[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int cc = 0; cc < C::kN; cc += 2) am[cc >> 1 & 3] = max3(am[cc >> 1 & 3], fabsf(f[cc]), fabsf(f[cc + 1]));
-                    cap_in_place(f, a.scale / a.softcap, fmaxf(fmaxf(am[0], am[1]), fmaxf(am[2], am[3])));
+                    cap_in_place(f, fit, fmaxf(fmaxf(am[0], am[1]), fmaxf(am[2], am[3])));
                 }
+                // bias: -slope |pos - key| = -slope (pos - k0) + slope cc where no key of the step lies
+                // past pos (any step but the last of a prefix): the first part goes into the exponent's FFMA
+                float shift = 0.f;
                 if (kSlopes) {
                     const float d0 = (float)(pos - k0);
+                    if (__all_sync(0xffffffffu, d0 >= (float)(C::kN - 1) || range.y <= pos + 1)) {
+                        const uint64_t s2 = tc::f2(slope, slope);
+                        shift = -slope * d0;
 #pragma unroll
-                    for (int cc = 0; cc < C::kN; ++cc) f[cc] = fmaf(-slope, fabsf(d0 - (float)cc), f[cc]);
+                        for (int v = 0; v < C::kN / 2; ++v) {
+                            const float2 y = tc::f2split(tc::fma2(s2, tc::f2((float)(2 * v), (float)(2 * v + 1)),
+                                                                  tc::f2(f[2 * v], f[2 * v + 1])));
+                            f[2 * v] = y.x;
+                            f[2 * v + 1] = y.y;
+                        }
+                    } else {
+#pragma unroll
+                        for (int cc = 0; cc < C::kN; ++cc) f[cc] = fmaf(-slope, fabsf(d0 - (float)cc), f[cc]);
+                    }
                 }
                 if (!(__all_sync(0xffffffffu, vb <= 0 && ve >= C::kN) && mask == (1 << C::kBoxes) - 1)) {
                     // a step that some row sees in part, or over boxes not loaded
@@ -507,7 +523,7 @@ __global__ void __launch_bounds__(UmmaCfg<D, MT>::kThreads, 1)
                     for (int cc = 8; cc < C::kN; ++cc) mx[cc & 7] = fmaxf(mx[cc & 7], f[cc]);
                     const float mr = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
                                            fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
-                    const float mc = mr * mul;  // -inf when nothing is visible
+                    const float mc = (mr + shift) * mul;  // -inf when nothing is visible
                     need = mc > m_used + 8.f;
                     alpha = (need && j > 0) ? ex2(m_used - mc) : 1.f;
                     if (need) m_used = mc;
@@ -517,7 +533,7 @@ __global__ void __launch_bounds__(UmmaCfg<D, MT>::kThreads, 1)
                 // two keys per packed f32x2 operation; the row sum in 4 pair accumulators
                 uint32_t hw[C::kN / 2], lw[C::kN / 2];
                 uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
-                const uint64_t mul2 = tc::f2(mul, mul), nmu2 = tc::f2(-mu, -mu);
+                const uint64_t mul2 = tc::f2(mul, mul), nmu2 = tc::f2(shift * mul - mu, shift * mul - mu);
 #pragma unroll
                 for (int v = 0; v < C::kN / 2; ++v) {
                     const float2 xa = tc::f2split(tc::fma2(tc::f2(f[2 * v], f[2 * v + 1]), mul2, nmu2));

@@ -82,23 +82,50 @@ struct ScoreCap {
     }
 };
 
-// The cap on N raw dot products in place, in raw units: f -> tanh(in f) / in, so
-// that the logit is f times the plain scale with a cap or without.  Needs in > 0;
-// `most` is at least every |f| of the calling thread.  Where |in f| <= 0.9 in the whole warp
-// -- logits rarely come near their cap -- tanh(y) / y is a polynomial of degree 6 in y^2
-// (fitted as above, 1.1e-8), two values per packed operation and no special function: 4.5
-// issue slots a value against 15 and a reciprocal for the rational form.
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-constexpr float kCapPolyLimit = 0.9f;
+
+// The cap on N raw dot products in place, in raw units: f -> tanh(in f) / in, so
+// that the logit is f times the plain scale with a cap or without.  Needs in > 0;
+// `most` is at least every |f| of the calling thread.  Logits rarely come near their cap, so a
+// whole warp mostly takes the first form:
+//   |in f| <= 0.5   f + f^3 (c1 + c2 f^2 + c3 f^4 + c4 f^6): tanh(y) = y (1 + y^2 Q(y^2)), Q of
+//                   degree 3 (fitted as above, 1.5e-8), the powers of `in` taken into its coefficients;
+//   |in f| <= 0.9   y P(y^2), P of degree 6 (1.4e-8);
+//   else            the rational form.
+// The polynomials cost 3 and 4.5 issue slots a value in packed arithmetic and no
+// special function, the rational form 15 and a reciprocal.
+struct CapFit {
+    float in, c1, c2, c3, c4, near;
+    __device__ __forceinline__ explicit CapFit(float in_) : in(in_) {
+        const float z = in * in;
+        c1 = -0.333331435918808f * z;
+        c2 = 0.13325878977775574f * z * z;
+        c3 = -0.05304549261927605f * z * z * z;
+        c4 = 0.01724148355424404f * z * z * (z * z);
+        // the scaled coefficients and the powers of f stay normal numbers in this range of `in`
+        near = in >= 0x1p-14f && in <= 0x1p10f ? 0.5f / in : -1.f;
+    }
+};
 template <int N>
-__device__ __forceinline__ void cap_in_place(float (&f)[N], float in, float most) {
-    if (__all_sync(0xffffffffu, most * in <= kCapPolyLimit)) {
-        const uint64_t in2 = tc::f2(in, in);
-        auto both = [](float c) { return tc::f2(c, c); };
+__device__ __forceinline__ void cap_in_place(float (&f)[N], const CapFit &c, float most) {
+    auto both = [](float x) { return tc::f2(x, x); };
+    if (__all_sync(0xffffffffu, most <= c.near)) {
+        const uint64_t c1 = both(c.c1), c2 = both(c.c2), c3 = both(c.c3), c4 = both(c.c4);
+#pragma unroll
+        for (int v = 0; v < N / 2; ++v) {
+            const uint64_t x = tc::f2(f[2 * v], f[2 * v + 1]);
+            const uint64_t z = mul2(x, x);
+            const uint64_t q = tc::fma2(tc::fma2(tc::fma2(z, c4, c3), z, c2), z, c1);
+            const float2 r = tc::f2split(tc::fma2(mul2(x, z), q, x));
+            f[2 * v] = r.x;
+            f[2 * v + 1] = r.y;
+        }
+    } else if (__all_sync(0xffffffffu, most * c.in <= 0.9f)) {
+        const uint64_t in2 = both(c.in);
 #pragma unroll
         for (int v = 0; v < N / 2; ++v) {
             const uint64_t x = tc::f2(f[2 * v], f[2 * v + 1]);
@@ -114,9 +141,9 @@ __device__ __forceinline__ void cap_in_place(float (&f)[N], float in, float most
             f[2 * v + 1] = r.y;
         }
     } else {
-        const float back = 1.f / in;
+        const float back = 1.f / c.in;
 #pragma unroll
-        for (int i = 0; i < N; ++i) f[i] = back * rational_tanh(in * f[i]);
+        for (int i = 0; i < N; ++i) f[i] = back * rational_tanh(c.in * f[i]);
     }
 }
 
