@@ -52,6 +52,19 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
+// The plain kernel's tiles and shared memory.  With two tiles and logits that are capped or
+// biased, the softmax warpgroups come behind two whole warpgroups of producers and issuers (two
+// warps of which idle), so that the latter's registers can be handed to them: 512 threads
+// are launched at 128 registers, 8 warps keep 72 and 8 take 184 (8 x 72 + 8 x 184 = 16 x 128).
+// Measured on 16 x 512-token chunks: capped 356 -> 348 us, biased 382 -> 373, both 563 -> 534; with
+// ranges only, 280 -> 286, so that kernel keeps the 14 warps.
+template <int D, int MT, int kMode>
+struct ScoredUmmaCfg : UmmaCfg<D, MT> {
+    static constexpr bool kRegSplit = MT == 2 && kMode != kMaskOnly;
+    static constexpr int kSoftWarp0 = kRegSplit ? 8 : UmmaCfg<D, MT>::kSoftWarp0;
+    static constexpr int kThreads = 32 * (kSoftWarp0 + 4 * MT);
+};
+
 // One work item: KV head kvh of the plan's entry (sequence s, tile group), i.e.
 // rows r0 .. r0 + 128 MT - 1 of that head's (query token, query head) rows, and
 // the keys [lo, hi) that some of those rows see, in nch steps from j0 on.
@@ -89,11 +102,11 @@ __device__ __forceinline__ bool scored_item(const ScoredArgs &a, int w, int nwor
 // and their phases the count c of the tile's own steps, the slots and query-tile
 // sets the count of items published.
 template <typename T, int D, int MT, int kMode>
-__global__ void __launch_bounds__(UmmaCfg<D, MT>::kThreads, 1)
+__global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
     scored_umma_kernel(const ScoredArgs a, const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmq,
                       const __grid_constant__ CUtensorMap tmo) {
-    using C = UmmaCfg<D, MT>;
+    using C = ScoredUmmaCfg<D, MT, kMode>;
     using M = Mma16<T>;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     extern __shared__ unsigned char smem_raw[];
@@ -177,6 +190,8 @@ __global__ void __launch_bounds__(UmmaCfg<D, MT>::kThreads, 1)
     griddep_wait();  // the plan kernel's list of (sequence, tile group), longest first
     const int nwork = a.plan_hdr[0] > 0 ? a.plan_hdr[0] * a.Hkv : 0;
 
+    if (warp < C::kSoftWarp0) {
+    if constexpr (C::kRegSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n" ::: "memory");
     if (warp == 0 || warp == 2) {
         // ------------------------------------------------------------ producers: K (warp 0), V (warp 2)
         const bool is_v = warp == 2;
@@ -414,7 +429,9 @@ __global__ void __launch_bounds__(UmmaCfg<D, MT>::kThreads, 1)
         if (lane == 0) tc::mma_commit(drain_p(u));
         __syncwarp();
         mbar_wait_bounded(drain_p(u), 0u, kWaitLimit);
-    } else if (warp >= C::kSoftWarp0) {
+    }
+    } else {
+        if constexpr (C::kRegSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;\n" ::: "memory");
         // ------------------------------------------------------------ softmax (one row per thread)
         const int u = (warp - C::kSoftWarp0) / 4;  // tile of this warpgroup
         const int wq = warp & 3;                 // TMEM lanes 32 * wq .. 32 * wq + 31
@@ -491,15 +508,9 @@ __global__ void __launch_bounds__(UmmaCfg<D, MT>::kThreads, 1)
                 if (kSlopes) {
                     const float d0 = (float)(pos - k0);
                     if (__all_sync(0xffffffffu, d0 >= (float)(C::kN - 1) || range.y <= pos + 1)) {
-                        const uint64_t s2 = tc::f2(slope, slope);
                         shift = -slope * d0;
 #pragma unroll
-                        for (int v = 0; v < C::kN / 2; ++v) {
-                            const float2 y = tc::f2split(tc::fma2(s2, tc::f2((float)(2 * v), (float)(2 * v + 1)),
-                                                                  tc::f2(f[2 * v], f[2 * v + 1])));
-                            f[2 * v] = y.x;
-                            f[2 * v + 1] = y.y;
-                        }
+                        for (int cc = 0; cc < C::kN; ++cc) f[cc] = fmaf(slope, (float)cc, f[cc]);  // an immediate each
                     } else {
 #pragma unroll
                         for (int cc = 0; cc < C::kN; ++cc) f[cc] = fmaf(-slope, fabsf(d0 - (float)cc), f[cc]);
@@ -765,13 +776,20 @@ __global__ void __launch_bounds__(UmmaCfg<D, MT>::kThreads, 1)
 template <typename T, int D, int MT, int kMode>
 cudaError_t launch_scored_umma_t(const ScoredArgs &a, const CUtensorMap &tmk, const CUtensorMap &tmv,
                                  const CUtensorMap &tmq, const CUtensorMap &tmo, cudaStream_t st) {
-    using C = UmmaCfg<D, MT>;
+    using C = ScoredUmmaCfg<D, MT, kMode>;
     static std::atomic<int> sms_of[kMaxLaunchDevices];
     int sms = 0;
     cudaError_t e = per_device_value(sms_of, &sms, [](int dev, int *v) {
         cudaError_t r = cudaFuncSetAttribute(scored_umma_kernel<T, D, MT, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)C::kSmem);
         if (r != cudaSuccess) return r;
+        if (C::kRegSplit) {
+            // the split draws on the registers of the launch: it must have been built for exactly these
+            cudaFuncAttributes at;
+            r = cudaFuncGetAttributes(&at, scored_umma_kernel<T, D, MT, kMode>);
+            if (r != cudaSuccess) return r;
+            if (at.numRegs != 128) return cudaErrorInvalidConfiguration;
+        }
         return cudaDeviceGetAttribute(v, cudaDevAttrMultiProcessorCount, dev);
     });
     if (e != cudaSuccess) return e;

@@ -1,22 +1,33 @@
 // pa_evict.cu -- eviction by summed attention weights: which tokens each KV head
 // keeps, and their copy to fresh blocks.
 //
-// Selection, one CTA per (sequence, KV head): of the n = len - recent older
-// tokens the m = keep - recent with the largest sums.  Sums become 32-bit keys
-// whose unsigned order is theirs (NaN lowest, -0 as +0), and the m-th largest
-// key is found by radix selection, a histogram of 8 bits per pass.  A token is
-// kept if its key is larger, or equal and among the first `ties` equal ones, or
-// if it is recent; a block-wide scan in index order gives each kept token its
-// new position, written to the move list, and its sum to the new place.
-// Copy: one thread per 16 bytes of a kept key or value row.
+// Selection, one cluster of CTAs per (sequence, KV head): of the n = len - recent
+// older tokens the m = keep - recent with the largest sums.  Sums become 32-bit keys
+// whose unsigned order is theirs (NaN lowest, -0 as +0).  Each CTA holds a slice of
+// the keys in shared memory; the m-th largest key is found by radix selection, a
+// digit of 11 or 10 bits a pass, over the cluster's histograms (read through distributed shared
+// memory).  A token is kept if its key is larger, or equal and among the first
+// `want` equal ones in index order, or if it is recent.  With G(j) larger and E(j)
+// equal keys before token j, its new position is G(j) + min(E(j), want), a recent
+// one's m + j - n: counts of larger and equal keys by segment give them all.  Each new
+// place gets the token's cache slot (the move list) and its sum.
+//
+// Copy: 16 bytes of a K and a V row per thread and row, several rows in flight.
+//
+// Bound: HBM for a batch (the kept rows, read and written); latency for one sequence.
+#include <cooperative_groups.h>
+
 #include "pa_device.cuh"
 #include "pa_scored.h"
+
+namespace cg = cooperative_groups;
 
 namespace pa {
 
 namespace {
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
+constexpr int kMaxSlice = 48 * 1024;  // keys of a slice kept in shared memory
 
 // Unsigned order of the keys = order of the sums; NaN below everything.
 __device__ __forceinline__ uint32_t sum_key(float x) {
@@ -25,8 +36,8 @@ __device__ __forceinline__ uint32_t sum_key(float x) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Exclusive prefix sum of v over the block (1024 threads); *total gets the sum.
-__device__ __forceinline__ int block_scan(int v, int *warp_sums, int *total) {
+// Exclusive prefix sum of v over the block (all threads call).
+__device__ __forceinline__ int block_scan(int v, int *warp_sums) {
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     int incl = v;
 #pragma unroll
@@ -36,166 +47,293 @@ __device__ __forceinline__ int block_scan(int v, int *warp_sums, int *total) {
     }
     if (lane == 31) warp_sums[wid] = incl;
     __syncthreads();
-    if (wid == 0) {
-        int w = warp_sums[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, w, o);
-            if (lane >= o) w += u;
-        }
-        warp_sums[lane] = w;
-    }
-    __syncthreads();
-    const int base = wid > 0 ? warp_sums[wid - 1] : 0;
-    *total = warp_sums[31];
-    __syncthreads();
+    int base = 0;
+    for (int w = 0; w < wid; ++w) base += warp_sums[w];
     return base + incl - v;
 }
 
+// Radix digits, from the top.  11 bits first: sums are positive numbers of a few
+// octaves, whose top 8 bits (sign and 7 of the exponent) would fall into a handful of bins
+// that every thread of the block then adds to.
+constexpr int kBins = 2048;
+
+// kFit: the cluster's slices hold every key in shared memory; else the keys are
+// read from the sums again in each pass.
+template <bool kFit>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
-    __shared__ int hist[256];
-    __shared__ int warp_sums[32];
+    constexpr int kWarps = kSelThreads / 32;
+    extern __shared__ uint32_t keys[];          // kFit: this CTA's slice
+    __shared__ alignas(16) int hist[2][kBins];  // counts, alternating between passes
+    __shared__ int warp_sums[kWarps];
+    __shared__ unsigned long long found[kWarps];  // (larger << 32) + equal keys of each warp's segment
+    __shared__ unsigned long long slice_total;
     __shared__ uint32_t s_key;
     __shared__ int s_want;
+    cg::cluster_group cluster = cg::this_cluster();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int s = blockIdx.x / a.Hkv, h = blockIdx.x % a.Hkv, tid = threadIdx.x;
+    const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int pair = blockIdx.x / C, s = pair / a.Hkv, h = pair % a.Hkv;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int cap = a.max_blocks * a.B;
     int len = a.lens[s], keep = a.keep_lens[s];
+    const int row = a.sum_rows ? a.sum_rows[s] : s;
+    const bool first = tid == 0 && rank == 0;
     if (len < 0 || len > cap || keep < 0) {
-        if (tid == 0 && h == 0) set_error(a.err, PA_DEVERR_BAD_LEN);
+        if (first && h == 0) set_error(a.err, PA_DEVERR_BAD_LEN);
         len = len < 0 ? 0 : (len > cap ? cap : len);
         if (keep < 0) keep = len;
     }
-    const int row = a.sum_rows ? a.sum_rows[s] : s;
     const bool bad_row = row < 0 || row >= a.sum_num_rows;
     if (bad_row) {
-        if (tid == 0 && h == 0) set_error(a.err, PA_DEVERR_BAD_ROW);
+        if (first && h == 0) set_error(a.err, PA_DEVERR_BAD_ROW);
         keep = len;
     }
     const int now = min(len, keep);
-    if (tid == 0) {
-        a.counts[blockIdx.x] = len > keep ? keep : 0;
+    if (first) {
+        a.counts[pair] = len > keep ? keep : 0;
         if (h == 0) a.new_lens[s] = now;
     }
-    if (bad_row) return;
+    if (bad_row) return;  // the whole cluster
     const float *in = a.sums + ((size_t)row * a.Hkv + h) * a.sum_cols;
     float *out = a.sums_out + ((size_t)row * a.Hkv + h) * a.sum_cols;
     if (len <= keep) {
-        for (int j = tid; j < a.sum_cols; j += blockDim.x) out[j] = j < now ? in[j] : 0.f;
-        return;
+        for (int j = rank * kSelThreads + tid; j < a.sum_cols; j += C * kSelThreads) out[j] = j < now ? in[j] : 0.f;
+        return;  // the whole cluster
     }
     const int recent = min(a.recent, keep);
     const int n = len - recent, m = keep - recent;  // m < n
-    // the m-th largest key, 8 bits at a time; `want` of the keys that share the prefix so far
+    const int slice = ((n + C - 1) / C + 3) & ~3;
+    const int j0 = min(n, rank * slice), count = min(n, j0 + slice) - j0;  // this CTA's older tokens
+    const float *mine = in + j0;
+    if (kFit) {
+        const int whole = count & ~3;  // j0 is a multiple of 4 unless count is 0
+        for (int j = 4 * tid; j < whole; j += 4 * kSelThreads) {
+            const float4 x = *reinterpret_cast<const float4 *>(mine + j);
+            *reinterpret_cast<uint4 *>(keys + j) = make_uint4(sum_key(x.x), sum_key(x.y), sum_key(x.z), sum_key(x.w));
+        }
+        if (tid < count - whole) keys[whole + tid] = sum_key(mine[whole + tid]);
+    }
+    auto key_at = [&](int j) { return kFit ? keys[j] : sum_key(mine[j]); };
+    for (int b = tid; b < kBins; b += kSelThreads) hist[0][b] = 0;
+    __syncthreads();
+    // the m-th largest key, a digit at a time; `want` of the keys that share the prefix so far
     uint32_t prefix = 0;
     int want = m;
-    if (m > 0) {
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            if (tid < 256) hist[tid] = 0;
-            __syncthreads();
-            const uint32_t high = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-            for (int j = tid; j < n; j += blockDim.x) {
-                const uint32_t k = sum_key(in[j]);
-                if ((k & high) == prefix) atomicAdd(&hist[k >> shift & 255u], 1);
-            }
-            __syncthreads();
-            // bins from the largest down: the one that holds the want-th key
-            int total;
-            const int v = tid < 256 ? hist[255 - tid] : 0;
-            const int before = block_scan(v, warp_sums, &total);
-            if (tid < 256 && before < want && want <= before + v) {
-                s_key = prefix | (uint32_t)(255 - tid) << shift;
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+        if (m == 0) break;
+        constexpr int kPer = kBins / kSelThreads;
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, digits = pass < 2 ? 11 : 10;
+        const uint32_t mask = (1u << digits) - 1u;
+        const uint32_t high = pass == 0 ? 0u : 0xffffffffu << (shift + digits);
+        int *mh = hist[pass & 1];
+        for (int j = tid; j < count; j += kSelThreads) {
+            const uint32_t k = key_at(j);
+            if ((k & high) == prefix) atomicAdd(&mh[k >> shift & mask], 1);
+        }
+        cluster.sync();
+        // bins from the largest down, kPer a thread: the one that holds the want-th key
+        int v[kPer], sum = 0;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) v[e] = 0;
+        for (int c = 0; c < C; ++c) {
+            const int4 x = *reinterpret_cast<const int4 *>(cluster.map_shared_rank(mh, c) + kBins - kPer * (tid + 1));
+            v[0] += x.w;
+            v[1] += x.z;
+            v[2] += x.y;
+            v[3] += x.x;
+        }
+        static_assert(kPer == 4, "one int4 of bins a thread");
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) sum += v[e];
+        for (int b = tid; b < kBins; b += kSelThreads) hist[~pass & 1][b] = 0;  // read by the cluster before the sync above
+        int before = block_scan(sum, warp_sums);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            if (before < want && want <= before + v[e]) {
+                s_key = prefix | (uint32_t)(kBins - 1 - kPer * tid - e) << shift;
                 s_want = want - before;
             }
-            __syncthreads();
-            prefix = s_key;
-            want = s_want;
-            __syncthreads();
+            before += v[e];
         }
+        __syncthreads();
+        prefix = s_key;
+        want = s_want;
+        __syncthreads();
     }
-    // kept tokens in index order; `want` of those equal to the m-th largest key
-    int *list = a.list + ((size_t)s * a.Hkv + h) * cap;
-    int kept = 0, equal = 0;
-    for (int j0 = 0; j0 < len; j0 += kSelThreads) {
-        const int j = j0 + tid;
-        const float x = j < len ? in[j] : 0.f;
-        const uint32_t k = sum_key(x);
-        const bool old = j < n, eq = old && m > 0 && k == prefix;
-        int total;
-        const int eq_before = equal + block_scan(eq ? 1 : 0, warp_sums, &total);
-        equal += total;
-        const bool keep_it = (old && m > 0 && (k > prefix || (eq && eq_before < want))) || (j >= n && j < len);
-        const int at = kept + block_scan(keep_it ? 1 : 0, warp_sums, &total);
-        kept += total;
-        // `at` <= j, and every sum of this tile has been read: in place is safe
-        if (keep_it) {
-            list[at] = j;
-            out[at] = x;
-        }
+    // larger and equal keys: each warp counts a segment of the slice, 32 keys at a time
+    const int seg = (((count + kWarps - 1) / kWarps) + 31) & ~31;
+    const int w0 = min(count, warp * seg), w1 = min(count, w0 + seg);
+    int larger = 0, equal = 0;
+    for (int j = w0 + lane; j - lane < w1 && m > 0; j += 32) {
+        const uint32_t k = j < w1 ? key_at(j) : 0u;
+        larger += __popc(__ballot_sync(0xffffffffu, j < w1 && k > prefix));
+        equal += __popc(__ballot_sync(0xffffffffu, j < w1 && k == prefix));
     }
+    if (lane == 0) found[warp] = (unsigned long long)larger << 32 | (unsigned)equal;
     __syncthreads();
-    for (int j = now + tid; j < a.sum_cols; j += blockDim.x) out[j] = 0.f;
+    unsigned long long before = 0;
+    for (int w = 0; w < warp; ++w) before += found[w];
+    if (tid == kSelThreads - 1) slice_total = before + found[kWarps - 1];
+    cluster.sync();
+    for (int c = 0; c < rank; ++c) before += *cluster.map_shared_rank(&slice_total, c);
+    larger = (int)(before >> 32);
+    equal = (int)(uint32_t)before;
+    // the kept tokens' old positions, at their new ones
+    int *list = a.list + (size_t)pair * cap;
+    for (int j = w0 + lane; j - lane < w1 && m > 0; j += 32) {
+        const uint32_t k = j < w1 ? key_at(j) : 0u;
+        const bool gt = j < w1 && k > prefix, eq = j < w1 && k == prefix;
+        const unsigned gts = __ballot_sync(0xffffffffu, gt), eqs = __ballot_sync(0xffffffffu, eq);
+        const unsigned below = (1u << lane) - 1u;
+        const int g = larger + __popc(gts & below), e = equal + __popc(eqs & below);
+        if (gt || (eq && e < want)) list[g + min(e, want)] = j0 + j;
+        larger += __popc(gts);
+        equal += __popc(eqs);
+    }
+    for (int i = rank * kSelThreads + tid; i < recent; i += C * kSelThreads) list[m + i] = n + i;
+    cluster.sync();  // the list is complete, and the keys have been read
+    // sums to their new places, and cache slots in place of positions.  A token never moves up, so
+    // with sums_out == sums a tile of places is read before any of it is written.
+    constexpr int kU = 4;
+    const int32_t *table = a.tables + (size_t)s * a.max_blocks;
+    const int tile = C * kSelThreads * kU;
+    const bool in_place = in == out;
+    for (int t0 = 0; t0 < keep; t0 += tile) {
+        float x[kU];
+        int slot[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int i = t0 + (u * C + rank) * kSelThreads + tid;
+            slot[u] = -1;
+            if (i < keep) {
+                const int p = list[i];
+                x[u] = in[p];
+                const int b = table[p / a.B];
+                if (b >= 0 && b < a.N) slot[u] = b * a.B + p % a.B;
+                else set_error(a.err, PA_DEVERR_BAD_BLOCK);
+            }
+        }
+        if (in_place) cluster.sync();
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int i = t0 + (u * C + rank) * kSelThreads + tid;
+            if (i < keep) {
+                out[i] = x[u];
+                list[i] = slot[u];
+            }
+        }
+    }
+    for (int j = keep + rank * kSelThreads + tid; j < a.sum_cols; j += C * kSelThreads) out[j] = 0.f;
 }
 
-// grid: (tiles of kMoveRows rows, sequence * Hkv, {K, V})
-constexpr int kMoveRows = 64;
-__global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a, int chunks) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+// Copy of the listed rows.  A block takes kRowsInFlight rows per thread column: thread
+// (row, c) moves 16-byte chunk c of them, K and V, all loads before the stores.
+// lb: log2 of the block size, or -1.
+constexpr int kMoveThreads = 256;
+constexpr int kRowsInFlight = 4;
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a, int chunks, int lb) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int sh = blockIdx.y, s = sh / a.Hkv, h = sh % a.Hkv;
-    const int count = a.counts[sh];
-    const int r0 = blockIdx.x * kMoveRows;
-    if (r0 >= count) return;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int pair = blockIdx.y, s = pair / a.Hkv, h = pair % a.Hkv;
+    const int width = min(chunks, kMoveThreads), per = kMoveThreads / width;  // threads of a row, rows side by side
+    const int r0 = blockIdx.x * per * kRowsInFlight + (int)threadIdx.x / width;
+    const int count = a.counts[pair];
+    if (r0 >= count || (int)threadIdx.x >= width * per) return;
     const int cap = a.max_blocks * a.B;
-    uint4 *cache = static_cast<uint4 *>(blockIdx.z ? a.v_cache : a.k_cache);
-    const int32_t *from = a.tables + (size_t)s * a.max_blocks;
     const int32_t *to = a.new_tables + (size_t)s * a.max_blocks;
-    const int *list = a.list + (size_t)sh * cap;
-    const int rows = min(kMoveRows, count - r0);
-    for (int u = threadIdx.x; u < rows * chunks; u += blockDim.x) {
-        const int r = r0 + u / chunks, c = u % chunks;
-        const int j = list[r];
-        const int fb = from[j / a.B], tb = to[r / a.B];
-        if (fb < 0 || fb >= a.N || tb < 0 || tb >= a.N) {
-            set_error(a.err, PA_DEVERR_BAD_BLOCK);
-            continue;
+    const int *list = a.list + (size_t)pair * cap;
+    auto block_of = [&](int x) { return lb >= 0 ? x >> lb : x / a.B; };
+    size_t src[kRowsInFlight], dst[kRowsInFlight];
+    bool ok[kRowsInFlight];
+#pragma unroll
+    for (int u = 0; u < kRowsInFlight; ++u) {
+        const int r = r0 + u * per;
+        ok[u] = r < count;
+        if (ok[u]) {
+            const int slot = list[r], tb = to[block_of(r)];
+            ok[u] = slot >= 0;
+            if (tb < 0 || tb >= a.N) {
+                set_error(a.err, PA_DEVERR_BAD_BLOCK);
+                ok[u] = false;
+            }
+            const int fb = block_of(slot);
+            src[u] = (((size_t)fb * a.Hkv + h) * a.B + (slot - fb * a.B)) * chunks;
+            dst[u] = (((size_t)tb * a.Hkv + h) * a.B + (r - block_of(r) * a.B)) * chunks;
         }
-        cache[(((size_t)tb * a.Hkv + h) * a.B + r % a.B) * chunks + c] =
-            cache[(((size_t)fb * a.Hkv + h) * a.B + j % a.B) * chunks + c];
+    }
+    uint4 *kc = static_cast<uint4 *>(a.k_cache), *vc = static_cast<uint4 *>(a.v_cache);
+    for (int c = (int)threadIdx.x % width; c < chunks; c += kMoveThreads) {
+        uint4 k[kRowsInFlight], v[kRowsInFlight];
+#pragma unroll
+        for (int u = 0; u < kRowsInFlight; ++u)
+            if (ok[u]) {
+                k[u] = __ldcs(kc + src[u] + c);
+                v[u] = __ldcs(vc + src[u] + c);
+            }
+#pragma unroll
+        for (int u = 0; u < kRowsInFlight; ++u)
+            if (ok[u]) {
+                kc[dst[u] + c] = k[u];
+                vc[dst[u] + c] = v[u];
+            }
     }
 }
 
-cudaError_t launch_pdl(void (*kernel)(EvictArgs), dim3 grid, int threads, const EvictArgs &a, cudaStream_t st) {
+template <bool kFit>
+cudaError_t launch_select(const EvictArgs &a, int C, size_t smem, cudaStream_t st) {
+    static std::atomic<int> configured[kMaxLaunchDevices];
+    int one = 0;
+    const cudaError_t e = per_device_value(configured, &one, [](int, int *v) {
+        *v = 1;
+        return cudaFuncSetAttribute(evict_select_kernel<kFit>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kFit ? kMaxSlice * 4 : 0);
+    });
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
+    cfg.gridDim = dim3((unsigned)(a.S * a.Hkv * C));
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)C;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, evict_select_kernel<kFit>, a);
 }
 
 }  // namespace
 
 cudaError_t launch_evict(const EvictArgs &a, cudaStream_t st) {
     if (a.S == 0) return cudaSuccess;
-    cudaError_t e = launch_pdl(evict_select_kernel, dim3((unsigned)(a.S * a.Hkv)), kSelThreads, a, st);
+    const int cap = a.max_blocks * a.B, pairs = a.S * a.Hkv;
+    // CTAs per (sequence, KV head): while two CTAs an SM are not filled and a slice stays above 1024
+    // keys, and as many as the keys need to fit in shared memory, at most 8 (a portable cluster)
+    int C = 1;
+    while (C < 8 && ((pairs * C < 2 * 152 && cap / C >= 2048) || cap / C > kMaxSlice - 8)) C *= 2;
+    const int slice = (((cap + C - 1) / C) + 7) & ~3;
+    const bool fit = slice <= kMaxSlice;
+    cudaError_t e = fit ? launch_select<true>(a, C, (size_t)slice * 4, st) : launch_select<false>(a, C, 0, st);
     if (e != cudaSuccess) return e;
-    const int cap = a.max_blocks * a.B;
+    const int chunks = a.row_bytes / 16;
+    const int rows = kRowsInFlight * (chunks < kMoveThreads ? kMoveThreads / chunks : 1);
+    const int lb = (a.B & (a.B - 1)) == 0 ? __builtin_ctz((unsigned)a.B) : -1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((cap + kMoveRows - 1) / kMoveRows), (unsigned)(a.S * a.Hkv), 2u);
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3((unsigned)((cap + rows - 1) / rows), (unsigned)pairs);
+    cfg.blockDim = dim3(kMoveThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, evict_move_kernel, a, a.row_bytes / 16);
+    return cudaLaunchKernelEx(&cfg, evict_move_kernel, a, chunks, lb);
 }
 
 }  // namespace pa
