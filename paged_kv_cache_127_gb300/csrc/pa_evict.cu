@@ -26,7 +26,7 @@ namespace pa {
 
 namespace {
 
-constexpr int kSelThreads = 512;
+constexpr int kSelThreads = 256;
 constexpr int kMaxSlice = 48 * 1024;  // keys of a slice kept in shared memory
 
 // Unsigned order of the keys = order of the sums; NaN below everything.
@@ -48,7 +48,8 @@ __device__ __forceinline__ int block_scan(int v, int *warp_sums) {
     if (lane == 31) warp_sums[wid] = incl;
     __syncthreads();
     int base = 0;
-    for (int w = 0; w < wid; ++w) base += warp_sums[w];
+#pragma unroll
+    for (int w = 0; w < kSelThreads / 32; ++w) base += w < wid ? warp_sums[w] : 0;
     return base + incl - v;
 }
 
@@ -60,7 +61,7 @@ constexpr int kBins = 2048;
 // kFit: the cluster's slices hold every key in shared memory; else the keys are
 // read from the sums again in each pass.
 template <bool kFit>
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a, int lb) {
     constexpr int kWarps = kSelThreads / 32;
     extern __shared__ uint32_t keys[];          // kFit: this CTA's slice
     __shared__ alignas(16) int hist[2][kBins];  // counts, alternating between passes
@@ -68,7 +69,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     __shared__ unsigned long long found[kWarps];  // (larger << 32) + equal keys of each warp's segment
     __shared__ unsigned long long slice_total;
     __shared__ uint32_t s_key;
-    __shared__ int s_want;
+    __shared__ int s_want, s_done;
     cg::cluster_group cluster = cg::this_cluster();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     for (int b = tid; b < kBins; b += kSelThreads) hist[0][b] = 0;
     __syncthreads();
     // the m-th largest key, a digit at a time; `want` of the keys that share the prefix so far
-    uint32_t prefix = 0;
+    uint32_t prefix = 0, known = 0xffffffffu;  // a key counts as equal if its `known` bits are
     int want = m;
 #pragma unroll
     for (int pass = 0; pass < 3; ++pass) {
@@ -128,46 +129,66 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
         const uint32_t mask = (1u << digits) - 1u;
         const uint32_t high = pass == 0 ? 0u : 0xffffffffu << (shift + digits);
         int *mh = hist[pass & 1];
-        for (int j = tid; j < count; j += kSelThreads) {
-            const uint32_t k = key_at(j);
+        auto add = [&](uint32_t k) {
             if ((k & high) == prefix) atomicAdd(&mh[k >> shift & mask], 1);
-        }
+        };
+        int j = 0;
+        if (kFit)
+            for (; j + 4 * kSelThreads <= count; j += 4 * kSelThreads) {
+                const uint4 k = *reinterpret_cast<const uint4 *>(keys + j + 4 * tid);
+                add(k.x);
+                add(k.y);
+                add(k.z);
+                add(k.w);
+            }
+        for (j += tid; j < count; j += kSelThreads) add(key_at(j));
         cluster.sync();
         // bins from the largest down, kPer a thread: the one that holds the want-th key
         int v[kPer], sum = 0;
 #pragma unroll
         for (int e = 0; e < kPer; ++e) v[e] = 0;
         for (int c = 0; c < C; ++c) {
-            const int4 x = *reinterpret_cast<const int4 *>(cluster.map_shared_rank(mh, c) + kBins - kPer * (tid + 1));
-            v[0] += x.w;
-            v[1] += x.z;
-            v[2] += x.y;
-            v[3] += x.x;
+            const int4 *x = reinterpret_cast<const int4 *>(cluster.map_shared_rank(mh, c) + kBins - kPer * (tid + 1));
+            const int4 lo = x[0], hi = x[1];
+            v[0] += hi.w;
+            v[1] += hi.z;
+            v[2] += hi.y;
+            v[3] += hi.x;
+            v[4] += lo.w;
+            v[5] += lo.z;
+            v[6] += lo.y;
+            v[7] += lo.x;
         }
-        static_assert(kPer == 4, "one int4 of bins a thread");
+        static_assert(kPer == 8, "two int4 of bins a thread");
 #pragma unroll
         for (int e = 0; e < kPer; ++e) sum += v[e];
-        for (int b = tid; b < kBins; b += kSelThreads) hist[~pass & 1][b] = 0;  // read by the cluster before the sync above
+        // the other counts, which the cluster read before the sync above, for the next pass
+#pragma unroll
+        for (int e = 0; e < 2; ++e) reinterpret_cast<int4 *>(hist[~pass & 1])[tid + e * kSelThreads] = make_int4(0, 0, 0, 0);
         int before = block_scan(sum, warp_sums);
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
             if (before < want && want <= before + v[e]) {
                 s_key = prefix | (uint32_t)(kBins - 1 - kPer * tid - e) << shift;
                 s_want = want - before;
+                s_done = want - before == v[e];  // every key of the bin is kept: its lower bits do not matter
             }
             before += v[e];
         }
         __syncthreads();
         prefix = s_key;
         want = s_want;
+        known = mask << shift | high;
+        const int done = s_done;
         __syncthreads();
+        if (done) break;  // the whole cluster alike
     }
     // larger and equal keys: each warp counts a segment of the slice, 32 keys at a time
     const int seg = (((count + kWarps - 1) / kWarps) + 31) & ~31;
     const int w0 = min(count, warp * seg), w1 = min(count, w0 + seg);
     int larger = 0, equal = 0;
     for (int j = w0 + lane; j - lane < w1 && m > 0; j += 32) {
-        const uint32_t k = j < w1 ? key_at(j) : 0u;
+        const uint32_t k = j < w1 ? key_at(j) & known : 0u;
         larger += __popc(__ballot_sync(0xffffffffu, j < w1 && k > prefix));
         equal += __popc(__ballot_sync(0xffffffffu, j < w1 && k == prefix));
     }
@@ -183,7 +204,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     // the kept tokens' old positions, at their new ones
     int *list = a.list + (size_t)pair * cap;
     for (int j = w0 + lane; j - lane < w1 && m > 0; j += 32) {
-        const uint32_t k = j < w1 ? key_at(j) : 0u;
+        const uint32_t k = j < w1 ? key_at(j) & known : 0u;
         const bool gt = j < w1 && k > prefix, eq = j < w1 && k == prefix;
         const unsigned gts = __ballot_sync(0xffffffffu, gt), eqs = __ballot_sync(0xffffffffu, eq);
         const unsigned below = (1u << lane) - 1u;
@@ -210,8 +231,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
             if (i < keep) {
                 const int p = list[i];
                 x[u] = in[p];
-                const int b = table[p / a.B];
-                if (b >= 0 && b < a.N) slot[u] = b * a.B + p % a.B;
+                const int tb = lb >= 0 ? p >> lb : p / a.B, b = table[tb];
+                if (b >= 0 && b < a.N) slot[u] = b * a.B + (p - tb * a.B);
                 else set_error(a.err, PA_DEVERR_BAD_BLOCK);
             }
         }
@@ -228,61 +249,74 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     for (int j = keep + rank * kSelThreads + tid; j < a.sum_cols; j += C * kSelThreads) out[j] = 0.f;
 }
 
-// Copy of the listed rows.  A block takes kRowsInFlight rows per thread column: thread
-// (row, c) moves 16-byte chunk c of them, K and V, all loads before the stores.
-// lb: log2 of the block size, or -1.
+// Copy of the listed rows.  A block takes kMoveTiles tiles of rows; in a tile a thread moves
+// 16-byte chunk c of kRowsInFlight rows, K and V, all loads before the stores, and has read
+// the next tile's slots by then.  lb: log2 of the block size, or -1.
 constexpr int kMoveThreads = 256;
 constexpr int kRowsInFlight = 4;
+constexpr int kMoveTiles = 4;
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a, int chunks, int lb) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int pair = blockIdx.y, s = pair / a.Hkv, h = pair % a.Hkv;
     const int width = min(chunks, kMoveThreads), per = kMoveThreads / width;  // threads of a row, rows side by side
-    const int r0 = blockIdx.x * per * kRowsInFlight + (int)threadIdx.x / width;
+    const int rows = per * kRowsInFlight;                                     // of a tile
+    int r = blockIdx.x * rows * kMoveTiles + (int)threadIdx.x / width;
     const int count = a.counts[pair];
-    if (r0 >= count || (int)threadIdx.x >= width * per) return;
+    const int end = min(count, (int)(blockIdx.x + 1) * rows * kMoveTiles);
+    if (r >= end || (int)threadIdx.x >= width * per) return;
     const int cap = a.max_blocks * a.B;
     const int32_t *to = a.new_tables + (size_t)s * a.max_blocks;
     const int *list = a.list + (size_t)pair * cap;
-    auto block_of = [&](int x) { return lb >= 0 ? x >> lb : x / a.B; };
-    size_t src[kRowsInFlight], dst[kRowsInFlight];
-    bool ok[kRowsInFlight];
-#pragma unroll
-    for (int u = 0; u < kRowsInFlight; ++u) {
-        const int r = r0 + u * per;
-        ok[u] = r < count;
-        if (ok[u]) {
-            const int slot = list[r], tb = to[block_of(r)];
-            ok[u] = slot >= 0;
-            if (tb < 0 || tb >= a.N) {
-                set_error(a.err, PA_DEVERR_BAD_BLOCK);
-                ok[u] = false;
-            }
-            const int fb = block_of(slot);
-            src[u] = (((size_t)fb * a.Hkv + h) * a.B + (slot - fb * a.B)) * chunks;
-            dst[u] = (((size_t)tb * a.Hkv + h) * a.B + (r - block_of(r) * a.B)) * chunks;
-        }
-    }
     uint4 *kc = static_cast<uint4 *>(a.k_cache), *vc = static_cast<uint4 *>(a.v_cache);
-    for (int c = (int)threadIdx.x % width; c < chunks; c += kMoveThreads) {
-        uint4 k[kRowsInFlight], v[kRowsInFlight];
+    auto block_of = [&](int x) { return lb >= 0 ? x >> lb : x / a.B; };
+    int slot[kRowsInFlight], tb[kRowsInFlight];
+    auto fetch = [&](int r) {
 #pragma unroll
-        for (int u = 0; u < kRowsInFlight; ++u)
-            if (ok[u]) {
-                k[u] = __ldcs(kc + src[u] + c);
-                v[u] = __ldcs(vc + src[u] + c);
+        for (int u = 0; u < kRowsInFlight; ++u) {
+            slot[u] = -1;
+            if (r + u * per < end) {
+                slot[u] = list[r + u * per];
+                tb[u] = to[block_of(r + u * per)];
             }
+        }
+    };
+    fetch(r);
+    for (; r < end; r += rows) {
+        int src[kRowsInFlight], dst[kRowsInFlight];  // rows of the cache
 #pragma unroll
-        for (int u = 0; u < kRowsInFlight; ++u)
-            if (ok[u]) {
-                kc[dst[u] + c] = k[u];
-                vc[dst[u] + c] = v[u];
+        for (int u = 0; u < kRowsInFlight; ++u) {
+            src[u] = -1;
+            if (slot[u] < 0) continue;
+            if (tb[u] < 0 || tb[u] >= a.N) {
+                set_error(a.err, PA_DEVERR_BAD_BLOCK);
+                continue;
             }
+            const int fb = block_of(slot[u]), at = r + u * per;
+            src[u] = (fb * a.Hkv + h) * a.B + (slot[u] - fb * a.B);
+            dst[u] = (tb[u] * a.Hkv + h) * a.B + (at - block_of(at) * a.B);
+        }
+        fetch(r + rows);
+        for (int c = (int)threadIdx.x % width; c < chunks; c += kMoveThreads) {
+            uint4 k[kRowsInFlight], v[kRowsInFlight];
+#pragma unroll
+            for (int u = 0; u < kRowsInFlight; ++u)
+                if (src[u] >= 0) {
+                    k[u] = __ldcs(kc + (size_t)src[u] * chunks + c);
+                    v[u] = __ldcs(vc + (size_t)src[u] * chunks + c);
+                }
+#pragma unroll
+            for (int u = 0; u < kRowsInFlight; ++u)
+                if (src[u] >= 0) {
+                    kc[(size_t)dst[u] * chunks + c] = k[u];
+                    vc[(size_t)dst[u] * chunks + c] = v[u];
+                }
+        }
     }
 }
 
 template <bool kFit>
-cudaError_t launch_select(const EvictArgs &a, int C, size_t smem, cudaStream_t st) {
+cudaError_t launch_select(const EvictArgs &a, int C, int lb, size_t smem, cudaStream_t st) {
     static std::atomic<int> configured[kMaxLaunchDevices];
     int one = 0;
     const cudaError_t e = per_device_value(configured, &one, [](int, int *v) {
@@ -305,7 +339,7 @@ cudaError_t launch_select(const EvictArgs &a, int C, size_t smem, cudaStream_t s
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, evict_select_kernel<kFit>, a);
+    return cudaLaunchKernelEx(&cfg, evict_select_kernel<kFit>, a, lb);
 }
 
 }  // namespace
@@ -319,13 +353,13 @@ cudaError_t launch_evict(const EvictArgs &a, cudaStream_t st) {
     while (C < 8 && ((pairs * C < 2 * 152 && cap / C >= 2048) || cap / C > kMaxSlice - 8)) C *= 2;
     const int slice = (((cap + C - 1) / C) + 7) & ~3;
     const bool fit = slice <= kMaxSlice;
-    cudaError_t e = fit ? launch_select<true>(a, C, (size_t)slice * 4, st) : launch_select<false>(a, C, 0, st);
+    const int lb = (a.B & (a.B - 1)) == 0 ? __builtin_ctz((unsigned)a.B) : -1;  // log2 of the block size, or -1
+    cudaError_t e = fit ? launch_select<true>(a, C, lb, (size_t)slice * 4, st) : launch_select<false>(a, C, lb, 0, st);
     if (e != cudaSuccess) return e;
     const int chunks = a.row_bytes / 16;
     const int rows = kRowsInFlight * (chunks < kMoveThreads ? kMoveThreads / chunks : 1);
-    const int lb = (a.B & (a.B - 1)) == 0 ? __builtin_ctz((unsigned)a.B) : -1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((cap + rows - 1) / rows), (unsigned)pairs);
+    cfg.gridDim = dim3((unsigned)((cap + rows * kMoveTiles - 1) / (rows * kMoveTiles)), (unsigned)pairs);
     cfg.blockDim = dim3(kMoveThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];

@@ -20,6 +20,7 @@
 #include <cmath>
 
 #include "pa_device.cuh"
+#include "pa_mma.cuh"
 #include "pa_scored.h"
 
 namespace pa {
@@ -101,25 +102,31 @@ __global__ void __launch_bounds__(kRopeThreads) rope_elements_kernel(const RopeA
     }
 }
 
+// A 16-byte unit of elements, as fp32 and back (each element rounded once).
 template <typename T>
-struct alignas(16) Unit {  // 16 bytes of elements
+struct Unit {
     static constexpr int kN = 16 / sizeof(T);
-    T e[kN];
+    static __device__ __forceinline__ uint4 pack(const float *f) {
+        if constexpr (sizeof(T) == 4)
+            return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+        else
+            return make_uint4(Mma16<T>::pack(f[0], f[1]), Mma16<T>::pack(f[2], f[3]), Mma16<T>::pack(f[4], f[5]),
+                              Mma16<T>::pack(f[6], f[7]));
+    }
 };
 
 // Vector kernel.  grid: (groups of up to kTokens tokens, parts of their heads).  A head is `upq`
 // columns: column i holds one unit (interleaved) or two (half layout): the units R / 2 apart
 // that rotate together, then pairs of the units behind R.  The heads of q, k and v are numbered
-// through and token by token; part y of gridDim.y takes every gridDim.y-th group of them, kU a
-// thread in flight.  A thread stays with one column, so its offsets are fixed.
+// through; part y of gridDim.y takes every gridDim.y-th group of them, kU a thread in flight.
+// A thread stays with one column, so its offsets within a head are fixed.
 constexpr int kTokens = 4;
 
 template <typename T, bool kInterleaved>
 __global__ void __launch_bounds__(kRopeThreads) rope_units_kernel(const RopeArgs a, int tokens, int upq) {
-    using U = Unit<T>;
-    constexpr int V = U::kN;
+    constexpr int V = Unit<T>::kN;
     constexpr int kAngles = kInterleaved ? V / 2 : V;  // (cos, sin) pairs of a column
-    constexpr int kU = 4;
+    constexpr int kU = kInterleaved ? 6 : 4;
     extern __shared__ float2 cs[];  // [tokens][R / 2]
     __shared__ int64_t slots[kTokens];
     const int half = a.R / 2, tid = threadIdx.x;
@@ -141,55 +148,56 @@ __global__ void __launch_bounds__(kRopeThreads) rope_units_kernel(const RopeArgs
     const int behind = (a.D - a.R) / V;                     // units behind R, the first half of them paired with the rest
     const int delta = kInterleaved ? 0 : turns ? half : (behind + 1) / 2 * V;
     const bool two = !kInterleaved && (turns || first + delta < a.D);
-    const int heads = a.Hq + 2 * a.Hkv, total = nt * heads;
-    const int step = per * (int)gridDim.y;
-    for (int x0 = blockIdx.y * per + h0; x0 < total; x0 += kU * step) {
-        U x[kU], y[kU];
-        T *to[kU];
-        int tok[kU];  // the token whose angles apply, or -1: a value head
+    const int k_head = a.Hq, v_head = a.Hq + a.Hkv, heads = a.Hq + 2 * a.Hkv;
+    const int step = per * (int)gridDim.y, row = a.B * a.D;
+    for (int t = 0; t < nt; ++t) {
+        const int64_t slot = slots[t];
+        if (slot < 0) continue;
+        const int64_t blk = slot / a.B;
+        const size_t place = ((size_t)blk * a.Hkv * a.B + (size_t)(slot - blk * a.B)) * a.D + first;  // head 0's row
+        // each kind's head 0 stands at its own number, so that head h is `h * D` (or rows of the cache) on
+        const T *q = static_cast<const T *>(a.q) + (size_t)(t0 + t) * a.q_stride + first;
+        const T *k = static_cast<const T *>(a.k) + (size_t)(t0 + t) * a.k_stride + first - (ptrdiff_t)k_head * a.D;
+        const T *v = static_cast<const T *>(a.v) + (size_t)(t0 + t) * a.v_stride + first - (ptrdiff_t)v_head * a.D;
+        T *qo = static_cast<T *>(a.q_out) + (size_t)(t0 + t) * a.q_out_stride + first;
+        T *kc = static_cast<T *>(a.k_cache) + place - (ptrdiff_t)k_head * row;
+        T *vc = static_cast<T *>(a.v_cache) + place - (ptrdiff_t)v_head * row;
+        const float2 *w = cs + t * half + i * kAngles;
+        for (int h = blockIdx.y * per + h0; h < heads; h += kU * step) {
+            uint4 x[kU], y[kU];
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int n = x0 + u * step;
-            const int t = (n >= heads) + (n >= 2 * heads) + (n >= 3 * heads);
-            const int h = n - t * heads;
-            to[u] = nullptr;
-            if (n >= total) continue;
-            const int64_t slot = slots[t];
-            if (slot < 0) continue;
-            const size_t row = t0 + t;
-            const int64_t blk = slot / a.B, off = slot - blk * a.B;
-            const T *from;
-            if (h < a.Hq) {
-                from = static_cast<const T *>(a.q) + row * a.q_stride + (size_t)h * a.D;
-                to[u] = static_cast<T *>(a.q_out) + row * a.q_out_stride + (size_t)h * a.D;
-            } else {
-                const bool is_v = h >= a.Hq + a.Hkv;
-                const int kh = h - a.Hq - (is_v ? a.Hkv : 0);
-                from = static_cast<const T *>(is_v ? a.v : a.k) + row * (is_v ? a.v_stride : a.k_stride) + (size_t)kh * a.D;
-                to[u] = static_cast<T *>(is_v ? a.v_cache : a.k_cache) + (((size_t)blk * a.Hkv + kh) * a.B + off) * a.D;
-            }
-            tok[u] = turns && h < a.Hq + a.Hkv ? t : -1;
-            to[u] += first;
-            x[u] = *reinterpret_cast<const U *>(from + first);
-            if (two) y[u] = *reinterpret_cast<const U *>(from + first + delta);
-        }
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            if (!to[u]) continue;
-            if (tok[u] >= 0) {
-                const float2 *w = cs + tok[u] * half + i * kAngles;
-#pragma unroll
-                for (int e = 0; e < kAngles; ++e) {
-                    T &p = kInterleaved ? x[u].e[2 * e] : x[u].e[e];
-                    T &r = kInterleaved ? x[u].e[2 * e + 1] : y[u].e[e];
-                    const float pf = static_cast<float>(p), rf = static_cast<float>(r);
-                    const float2 c = w[e];
-                    p = narrow<T>(pf * c.x - rf * c.y);
-                    r = narrow<T>(rf * c.x + pf * c.y);
+            for (int u = 0; u < kU; ++u) {
+                const int n = h + u * step;
+                if (n < heads) {
+                    const T *from = (n < k_head ? q : n < v_head ? k : v) + (ptrdiff_t)n * a.D;
+                    x[u] = *reinterpret_cast<const uint4 *>(from);
+                    if (two) y[u] = *reinterpret_cast<const uint4 *>(from + delta);
                 }
             }
-            *reinterpret_cast<U *>(to[u]) = x[u];
-            if (two) *reinterpret_cast<U *>(to[u] + delta) = y[u];
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                const int n = h + u * step;
+                if (n < heads) {
+                    if (turns && n < v_head) {
+                        float f[V], g[V];
+                        Elem<T>::unpack(x[u], f);
+                        if (!kInterleaved) Elem<T>::unpack(y[u], g);
+#pragma unroll
+                        for (int e = 0; e < kAngles; ++e) {
+                            float &p = kInterleaved ? f[2 * e] : f[e], &r = kInterleaved ? f[2 * e + 1] : g[e];
+                            const float2 c = w[e];
+                            const float pn = p * c.x - r * c.y;
+                            r = r * c.x + p * c.y;
+                            p = pn;
+                        }
+                        x[u] = Unit<T>::pack(f);
+                        if (!kInterleaved) y[u] = Unit<T>::pack(g);
+                    }
+                    T *to = n < k_head ? qo + (ptrdiff_t)n * a.D : (n < v_head ? kc : vc) + (ptrdiff_t)n * row;
+                    *reinterpret_cast<uint4 *>(to) = x[u];
+                    if (two) *reinterpret_cast<uint4 *>(to + delta) = y[u];
+                }
+            }
         }
     }
 }
@@ -220,7 +228,7 @@ cudaError_t launch_rope_t(const RopeArgs &a, cudaStream_t st) {
     // one chain of loads and one barrier.
     const int tokens = a.T >= 16 * 152 && a.R <= 1024 ? kTokens : 1;
     const int groups = (a.T + tokens - 1) / tokens, per = kRopeThreads / upq;
-    const int passes = (tokens * (a.Hq + 2 * a.Hkv) + per - 1) / per;
+    const int passes = (a.Hq + 2 * a.Hkv + per - 1) / per;
     int parts = (4 * 152 + groups - 1) / groups;
     parts = parts < passes ? parts : passes;
     const dim3 grid((unsigned)groups, (unsigned)(parts > 0 ? parts : 1));

@@ -376,7 +376,8 @@ static int32_t check_evict_dims(const pa_dims *d) {
     if (d->num_seqs < 0 || d->max_blocks_per_seq <= 0) return PA_ERR_INVALID;
     if ((int64_t)d->max_blocks_per_seq * d->block_size > INT32_MAX) return PA_ERR_INVALID;
     if ((int64_t)d->num_seqs * d->num_kv_heads > 65535) return PA_ERR_INVALID;  // the copy grid's y extent
-    if ((int64_t)d->num_blocks * d->block_size > INT32_MAX) return PA_ERR_INVALID;  // 32-bit slots
+    // cache rows (N * Hkv * B) are numbered in 32 bits
+    if ((int64_t)d->num_blocks * d->num_kv_heads > INT32_MAX / d->block_size) return PA_ERR_INVALID;
     return PA_OK;
 }
 
