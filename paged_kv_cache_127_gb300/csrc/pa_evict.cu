@@ -26,7 +26,6 @@ namespace pa {
 
 namespace {
 
-constexpr int kSelThreads = 256;
 constexpr int kMaxSlice = 48 * 1024;  // keys of a slice kept in shared memory
 
 // Unsigned order of the keys = order of the sums; NaN below everything.
@@ -37,6 +36,7 @@ __device__ __forceinline__ uint32_t sum_key(float x) {
 }
 
 // Exclusive prefix sum of v over the block (all threads call).
+template <int kThreads>
 __device__ __forceinline__ int block_scan(int v, int *warp_sums) {
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     int incl = v;
@@ -47,9 +47,8 @@ __device__ __forceinline__ int block_scan(int v, int *warp_sums) {
     }
     if (lane == 31) warp_sums[wid] = incl;
     __syncthreads();
-    int base = 0;
-#pragma unroll
-    for (int w = 0; w < kSelThreads / 32; ++w) base += w < wid ? warp_sums[w] : 0;
+    static_assert(kThreads / 32 <= 32, "one lane a warp");
+    const int base = __reduce_add_sync(0xffffffffu, lane < wid && lane < kThreads / 32 ? warp_sums[lane] : 0);
     return base + incl - v;
 }
 
@@ -59,21 +58,24 @@ __device__ __forceinline__ int block_scan(int v, int *warp_sums) {
 constexpr int kBins = 2048;
 
 // kFit: the cluster's slices hold every key in shared memory; else the keys are
-// read from the sums again in each pass.
-template <bool kFit>
+// read from the sums again in each pass.  kCluster: more than one CTA a (sequence, head).
+template <bool kFit, bool kCluster, int kSelThreads>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a, int lb) {
     constexpr int kWarps = kSelThreads / 32;
     extern __shared__ uint32_t keys[];          // kFit: this CTA's slice
     __shared__ alignas(16) int hist[2][kBins];  // counts, alternating between passes
     __shared__ int warp_sums[kWarps];
-    __shared__ unsigned long long found[kWarps];  // (larger << 32) + equal keys of each warp's segment
-    __shared__ unsigned long long slice_total;
+    __shared__ int2 found[kWarps];  // larger and equal keys of each warp's segment
+    __shared__ int2 slice_total;
     __shared__ uint32_t s_key;
     __shared__ int s_want, s_done;
     cg::cluster_group cluster = cg::this_cluster();
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int C = kCluster ? (int)cluster.num_blocks() : 1, rank = kCluster ? (int)cluster.block_rank() : 0;
+    auto sync_all = [&] {
+        if constexpr (kCluster) cluster.sync();
+        else __syncthreads();
+    };
     const int pair = blockIdx.x / C, s = pair / a.Hkv, h = pair % a.Hkv;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int cap = a.max_blocks * a.B;
@@ -142,30 +144,33 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
                 add(k.w);
             }
         for (j += tid; j < count; j += kSelThreads) add(key_at(j));
-        cluster.sync();
+        sync_all();
         // bins from the largest down, kPer a thread: the one that holds the want-th key
         int v[kPer], sum = 0;
 #pragma unroll
         for (int e = 0; e < kPer; ++e) v[e] = 0;
-        for (int c = 0; c < C; ++c) {
-            const int4 *x = reinterpret_cast<const int4 *>(cluster.map_shared_rank(mh, c) + kBins - kPer * (tid + 1));
-            const int4 lo = x[0], hi = x[1];
-            v[0] += hi.w;
-            v[1] += hi.z;
-            v[2] += hi.y;
-            v[3] += hi.x;
-            v[4] += lo.w;
-            v[5] += lo.z;
-            v[6] += lo.y;
-            v[7] += lo.x;
+        auto add_bins = [&](const int *counts) {
+            const int2 *x = reinterpret_cast<const int2 *>(counts + kBins - kPer * (tid + 1));
+#pragma unroll
+            for (int e = 0; e < kPer / 2; ++e) {
+                const int2 b = x[kPer / 2 - 1 - e];
+                v[2 * e] += b.y;
+                v[2 * e + 1] += b.x;
+            }
+        };
+        if constexpr (kCluster) {
+#pragma unroll 4
+            for (int c = 0; c < C; ++c) add_bins(cluster.map_shared_rank(mh, c));
+        } else {
+            add_bins(mh);
         }
-        static_assert(kPer == 8, "two int4 of bins a thread");
+        static_assert(kPer % 2 == 0, "pairs of bins");
 #pragma unroll
         for (int e = 0; e < kPer; ++e) sum += v[e];
         // the other counts, which the cluster read before the sync above, for the next pass
 #pragma unroll
-        for (int e = 0; e < 2; ++e) reinterpret_cast<int4 *>(hist[~pass & 1])[tid + e * kSelThreads] = make_int4(0, 0, 0, 0);
-        int before = block_scan(sum, warp_sums);
+        for (int e = 0; e < kPer / 2; ++e) reinterpret_cast<int2 *>(hist[~pass & 1])[tid + e * kSelThreads] = make_int2(0, 0);
+        int before = block_scan<kSelThreads>(sum, warp_sums);
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
             if (before < want && want <= before + v[e]) {
@@ -192,15 +197,19 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
         larger += __popc(__ballot_sync(0xffffffffu, j < w1 && k > prefix));
         equal += __popc(__ballot_sync(0xffffffffu, j < w1 && k == prefix));
     }
-    if (lane == 0) found[warp] = (unsigned long long)larger << 32 | (unsigned)equal;
+    if (lane == 0) found[warp] = make_int2(larger, equal);
     __syncthreads();
-    unsigned long long before = 0;
-    for (int w = 0; w < warp; ++w) before += found[w];
-    if (tid == kSelThreads - 1) slice_total = before + found[kWarps - 1];
-    cluster.sync();
-    for (int c = 0; c < rank; ++c) before += *cluster.map_shared_rank(&slice_total, c);
-    larger = (int)(before >> 32);
-    equal = (int)(uint32_t)before;
+    const int2 mine_of = lane < kWarps ? found[lane] : make_int2(0, 0);
+    larger = __reduce_add_sync(0xffffffffu, lane < warp ? mine_of.x : 0);
+    equal = __reduce_add_sync(0xffffffffu, lane < warp ? mine_of.y : 0);
+    if (tid == kSelThreads - 1) slice_total = make_int2(larger + found[kWarps - 1].x, equal + found[kWarps - 1].y);
+    sync_all();
+    if constexpr (kCluster)
+        for (int c = 0; c < rank; ++c) {
+            const int2 t = *cluster.map_shared_rank(&slice_total, c);
+            larger += t.x;
+            equal += t.y;
+        }
     // the kept tokens' old positions, at their new ones
     int *list = a.list + (size_t)pair * cap;
     for (int j = w0 + lane; j - lane < w1 && m > 0; j += 32) {
@@ -214,7 +223,9 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
         equal += __popc(eqs);
     }
     for (int i = rank * kSelThreads + tid; i < recent; i += C * kSelThreads) list[m + i] = n + i;
-    cluster.sync();  // the list is complete, and the keys have been read
+    // The copy's blocks may come now: earlier they would hold registers that this grid's CTAs need.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    sync_all();  // the list is complete, and the keys have been read
     // sums to their new places, and cache slots in place of positions.  A token never moves up, so
     // with sums_out == sums a tile of places is read before any of it is written.
     constexpr int kU = 4;
@@ -236,7 +247,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
                 else set_error(a.err, PA_DEVERR_BAD_BLOCK);
             }
         }
-        if (in_place) cluster.sync();
+        if (in_place) sync_all();
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
             const int i = t0 + (u * C + rank) * kSelThreads + tid;
@@ -256,7 +267,6 @@ constexpr int kMoveThreads = 256;
 constexpr int kRowsInFlight = 4;
 constexpr int kMoveTiles = 4;
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a, int chunks, int lb) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int pair = blockIdx.y, s = pair / a.Hkv, h = pair % a.Hkv;
     const int width = min(chunks, kMoveThreads), per = kMoveThreads / width;  // threads of a row, rows side by side
@@ -296,6 +306,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
             src[u] = (fb * a.Hkv + h) * a.B + (slot[u] - fb * a.B);
             dst[u] = (tb[u] * a.Hkv + h) * a.B + (at - block_of(at) * a.B);
         }
+        if (r + rows >= end) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         fetch(r + rows);
         for (int c = (int)threadIdx.x % width; c < chunks; c += kMoveThreads) {
             uint4 k[kRowsInFlight], v[kRowsInFlight];
@@ -315,14 +326,14 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
     }
 }
 
-template <bool kFit>
+template <bool kFit, bool kCluster, int kSelThreads>
 cudaError_t launch_select(const EvictArgs &a, int C, int lb, size_t smem, cudaStream_t st) {
     static std::atomic<int> configured[kMaxLaunchDevices];
     int one = 0;
     const cudaError_t e = per_device_value(configured, &one, [](int, int *v) {
         *v = 1;
-        return cudaFuncSetAttribute(evict_select_kernel<kFit>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    kFit ? kMaxSlice * 4 : 0);
+        return cudaFuncSetAttribute(evict_select_kernel<kFit, kCluster, kSelThreads>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kFit ? kMaxSlice * 4 : 0);
     });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -338,8 +349,8 @@ cudaError_t launch_select(const EvictArgs &a, int C, int lb, size_t smem, cudaSt
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, evict_select_kernel<kFit>, a, lb);
+    cfg.numAttrs = kCluster ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, evict_select_kernel<kFit, kCluster, kSelThreads>, a, lb);
 }
 
 }  // namespace
@@ -354,7 +365,22 @@ cudaError_t launch_evict(const EvictArgs &a, cudaStream_t st) {
     const int slice = (((cap + C - 1) / C) + 7) & ~3;
     const bool fit = slice <= kMaxSlice;
     const int lb = (a.B & (a.B - 1)) == 0 ? __builtin_ctz((unsigned)a.B) : -1;  // log2 of the block size, or -1
-    cudaError_t e = fit ? launch_select<true>(a, C, lb, (size_t)slice * 4, st) : launch_select<false>(a, C, lb, 0, st);
+    // Small CTAs when every SM holds several (less of the fixed work a warp does), large ones when a
+    // pair's chain of steps is what takes the time.
+    cudaError_t e = !fit      ? launch_select<false, true, 1024>(a, C, lb, 0, st)
+                    : C > 1   ? launch_select<true, true, 1024>(a, C, lb, (size_t)slice * 4, st)
+                    : pairs >= 152 ? launch_select<true, false, 256>(a, C, lb, (size_t)slice * 4, st)
+                                   : launch_select<true, false, 1024>(a, C, lb, (size_t)slice * 4, st);
+    if (e != cudaSuccess) return e;
+    // The copy wants the whole L1 for its loads in flight: left with the split that the selection's
+    // shared memory asked for, it takes 208 us for 64 sequences instead of 168.
+    static std::atomic<int> configured[kMaxLaunchDevices];
+    int one = 0;
+    e = per_device_value(configured, &one, [](int, int *v) {
+        *v = 1;
+        return cudaFuncSetAttribute(evict_move_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                    cudaSharedmemCarveoutMaxL1);
+    });
     if (e != cudaSuccess) return e;
     const int chunks = a.row_bytes / 16;
     const int rows = kRowsInFlight * (chunks < kMoveThreads ? kMoveThreads / chunks : 1);

@@ -217,6 +217,21 @@ cudaError_t launch_rope(void (*kernel)(Args...), dim3 grid, size_t smem, cudaStr
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// The unit kernels want the whole L1 for their loads in flight, also right after a kernel
+// that asked for a large part of it as shared memory.
+template <typename T, bool kInterleaved>
+cudaError_t launch_units(const RopeArgs &a, int tokens, int upq, dim3 grid, size_t smem, cudaStream_t st) {
+    static std::atomic<int> configured[kMaxLaunchDevices];
+    int one = 0;
+    const cudaError_t e = per_device_value(configured, &one, [](int, int *v) {
+        *v = 1;
+        return cudaFuncSetAttribute(rope_units_kernel<T, kInterleaved>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                    cudaSharedmemCarveoutMaxL1);
+    });
+    if (e != cudaSuccess) return e;
+    return launch_rope(rope_units_kernel<T, kInterleaved>, grid, smem, st, a, tokens, upq);
+}
+
 template <typename T>
 cudaError_t launch_rope_t(const RopeArgs &a, cudaStream_t st) {
     constexpr int V = Unit<T>::kN;
@@ -233,8 +248,8 @@ cudaError_t launch_rope_t(const RopeArgs &a, cudaStream_t st) {
     parts = parts < passes ? parts : passes;
     const dim3 grid((unsigned)groups, (unsigned)(parts > 0 ? parts : 1));
     const size_t smem = (size_t)tokens * (a.R / 2) * sizeof(float2);
-    return a.interleaved ? launch_rope(rope_units_kernel<T, true>, grid, smem, st, a, tokens, upq)
-                         : launch_rope(rope_units_kernel<T, false>, grid, smem, st, a, tokens, upq);
+    return a.interleaved ? launch_units<T, true>(a, tokens, upq, grid, smem, st)
+                         : launch_units<T, false>(a, tokens, upq, grid, smem, st);
 }
 
 }  // namespace
