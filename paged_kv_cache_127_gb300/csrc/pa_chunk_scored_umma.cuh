@@ -204,20 +204,19 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
 #pragma unroll
         for (int u = 0; u < MT; ++u) ku[u] = 0;
         int k0 = 0;                 // V producer: tile 0's items taken so far
+        int items = 0;              // K producer: entries taken so far
         bool ok = true;
         for (;;) {
             ScoredItem it;
             if (!is_v) {
-                // claim the next entry of the longest-first list (skipping entries
-                // without rows); past its end, publish the end mark to every tile
-                bool have = false;
-                while (!have) {
-                    int w = 0;
-                    if (lane == 0) w = atomicAdd(&a.plan_hdr[1], 1);
+                // claim the next entry of the longest-first list; past its end, publish the
+                // end mark to every tile
+                int w = blockIdx.x;  // a CTA's first entry needs no claim
+                if (items++ > 0) {
+                    if (lane == 0) w = (int)gridDim.x + atomicAdd(&a.plan_hdr[1], 1);
                     w = __shfl_sync(0xffffffffu, w, 0);
-                    if (w >= nwork) break;
-                    have = scored_item<C>(a, w, nwork, it);
                 }
+                const bool have = scored_item<C>(a, w, nwork, it);
                 // every tile's roles see every item (a tile without rows in it releases
                 // its ring stages); slot x of tile u is free once the tile's roles are
                 // done with the item before last

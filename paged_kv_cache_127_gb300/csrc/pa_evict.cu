@@ -260,20 +260,19 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     for (int j = keep + rank * kSelThreads + tid; j < a.sum_cols; j += C * kSelThreads) out[j] = 0.f;
 }
 
-// Copy of the listed rows.  A block takes kMoveTiles tiles of rows; in a tile a thread moves
+// Copy of the listed rows.  A block takes `tiles` tiles of rows; in a tile a thread moves
 // 16-byte chunk c of kRowsInFlight rows, K and V, all loads before the stores, and has read
 // the next tile's slots by then.  lb: log2 of the block size, or -1.
 constexpr int kMoveThreads = 256;
 constexpr int kRowsInFlight = 4;
-constexpr int kMoveTiles = 4;
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a, int chunks, int lb) {
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a, int chunks, int lb, int tiles) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int pair = blockIdx.y, s = pair / a.Hkv, h = pair % a.Hkv;
     const int width = min(chunks, kMoveThreads), per = kMoveThreads / width;  // threads of a row, rows side by side
     const int rows = per * kRowsInFlight;                                     // of a tile
-    int r = blockIdx.x * rows * kMoveTiles + (int)threadIdx.x / width;
+    int r = blockIdx.x * rows * tiles + (int)threadIdx.x / width;
     const int count = a.counts[pair];
-    const int end = min(count, (int)(blockIdx.x + 1) * rows * kMoveTiles);
+    const int end = min(count, (int)(blockIdx.x + 1) * rows * tiles);
     if (r >= end || (int)threadIdx.x >= width * per) return;
     const int cap = a.max_blocks * a.B;
     const int32_t *to = a.new_tables + (size_t)s * a.max_blocks;
@@ -385,7 +384,9 @@ cudaError_t launch_evict(const EvictArgs &a, cudaStream_t st) {
     const int chunks = a.row_bytes / 16;
     const int rows = kRowsInFlight * (chunks < kMoveThreads ? kMoveThreads / chunks : 1);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((cap + rows * kMoveTiles - 1) / (rows * kMoveTiles)), (unsigned)pairs);
+    // four tiles a block hide the next slots behind the copy, as long as they leave every SM its blocks
+    const int tiles = (long long)pairs * (cap / rows) >= 4LL * 8 * 152 ? 4 : 1;
+    cfg.gridDim = dim3((unsigned)((cap + rows * tiles - 1) / (rows * tiles)), (unsigned)pairs);
     cfg.blockDim = dim3(kMoveThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -393,7 +394,7 @@ cudaError_t launch_evict(const EvictArgs &a, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, evict_move_kernel, a, chunks, lb);
+    return cudaLaunchKernelEx(&cfg, evict_move_kernel, a, chunks, lb, tiles);
 }
 
 }  // namespace pa

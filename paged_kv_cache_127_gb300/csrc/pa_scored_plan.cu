@@ -106,11 +106,29 @@ __global__ void __launch_bounds__(1024) scored_chunk_plan_kernel(const ScoredArg
     const int Pt = a.umma_rows > 0 ? INT_MAX : a.partition_size;
     const int unit = a.umma_rows > 0 ? PA_CHUNK_UMMA_KEYS : 16;         // keys of a step
     const bool cached = a.S <= kSeqCache;
+    const int blocks = (a.max_query_len + tokens - 1) / tokens;  // of a sequence, at most
+    const unsigned all = (unsigned)a.S * (unsigned)blocks;       // bounded by the entry point
+    const bool masks = a.key_begin || a.key_end;  // else the ranges follow from the positions, and none is empty
+    const bool in_smem = masks && all <= kSpanCache;
+    // the masks of a thread's first kRows rows, read beside the lengths: one trip to memory for both
+    constexpr int kRows = 8;
+    int begin[kRows], end[kRows];
+    auto read_masks = [&](int i0) {
+#pragma unroll
+        for (int e = 0; e < kRows; ++e) {
+            const int i = i0 + 1024 * e + tid;
+            begin[e] = a.key_begin && i < a.T ? a.key_begin[i] : 0;
+            end[e] = a.key_end && i < a.T ? a.key_end[i] : INT_MAX;
+        }
+    };
+    if (in_smem) read_masks(0);
     if (cached) {
         for (int s = tid; s <= a.S; s += blockDim.x) qs_cache[s] = a.query_start[s];
         for (int s = tid; s < a.S; s += blockDim.x) len_cache[s] = a.context_lens[s];
     }
     for (int i = tid; i < kBins; i += blockDim.x) hist[i] = 0;
+    if (in_smem)
+        for (unsigned b = tid; b < all; b += 1024) spans[b] = make_int2(INT_MAX, 0);
     if (tid == 0) {
         a.plan_hdr[1] = 0;
         merges = 0;
@@ -132,8 +150,6 @@ __global__ void __launch_bounds__(1024) scored_chunk_plan_kernel(const ScoredArg
         const int len = lens[s], n = qs[s + 1] - qs[s];
         if (len < 0 || len > cap || n > len || n > a.max_query_len) set_error(a.err, PA_DEVERR_BAD_LEN);
     }
-    const int blocks = (a.max_query_len + tokens - 1) / tokens;  // of a sequence, at most
-    const unsigned all = (unsigned)a.S * (unsigned)blocks;       // bounded by the entry point
     // The row's sequence, or -1 (qs[s0] <= i, or s0 == 0; the row's sequence in [s0, s1)).
     auto seq_of = [&](int i) {
         int s0 = 0, s1 = a.S;
@@ -144,21 +160,12 @@ __global__ void __launch_bounds__(1024) scored_chunk_plan_kernel(const ScoredArg
         const int n = qs[s0 + 1] - qs[s0], len = lens[s0], t = i - qs[s0];
         return t < 0 || t >= n || len < 0 || len > cap || n > len || n > a.max_query_len ? -1 : s0;
     };
-    const bool masks = a.key_begin || a.key_end;  // else the ranges follow from the positions, and none is empty
-    const bool in_smem = masks && all <= kSpanCache;
     if (in_smem) {
-        for (unsigned b = tid; b < all; b += 1024) spans[b] = make_int2(INT_MAX, 0);
-        __syncthreads();
-        for (int i0 = 0; i0 < a.T; i0 += 4096) {
-            int begin[4], end[4];  // four rows a thread in flight
+        for (int i0 = 0; i0 < a.T; i0 += 1024 * kRows) {
+            if (i0 > 0) read_masks(i0);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = i0 + 1024 * e + tid;
-                begin[e] = a.key_begin && i < a.T ? a.key_begin[i] : 0;
-                end[e] = a.key_end && i < a.T ? a.key_end[i] : INT_MAX;
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < kRows; ++e) {
+                if (i0 + 1024 * e >= a.T) break;
                 const int i = i0 + 1024 * e + tid;
                 int lo = INT_MAX, hi = 0, b = -1;
                 const int s = i < a.T ? seq_of(i) : -1;

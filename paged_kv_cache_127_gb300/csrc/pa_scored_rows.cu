@@ -21,6 +21,24 @@ namespace {
 
 constexpr int kWarps = 4;
 
+// A lane's N neighbouring elements of a V row, in one load.
+template <typename T, int N>
+struct Row {
+    float f[N];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int e = 0; e < N; ++e) f[e] = 0.f;
+    }
+    __device__ __forceinline__ void load(const T *p) {
+        struct alignas(sizeof(T) * N) Vec {
+            T e[N];
+        };
+        const Vec v = *reinterpret_cast<const Vec *>(p);
+#pragma unroll
+        for (int e = 0; e < N; ++e) f[e] = static_cast<float>(v.e[e]);
+    }
+};
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kWarps * 32) scored_rows_kernel(const ScoredArgs a) {
     constexpr int kVec = Elem<T>::kVec;
@@ -76,7 +94,7 @@ __global__ void __launch_bounds__(kWarps * 32) scored_rows_kernel(const ScoredAr
             }
             if (in) {
                 float dot = 0.f;
-#pragma unroll 4
+#pragma unroll 8
                 for (int c = 0; c < D / kVec; ++c) {
                     float qf[kVec], kf[kVec];
                     Elem<T>::unpack(__ldg(reinterpret_cast<const uint4 *>(q) + c), qf);
@@ -104,13 +122,22 @@ __global__ void __launch_bounds__(kWarps * 32) scored_rows_kernel(const ScoredAr
 #pragma unroll
             for (int e = 0; e < kPer; ++e) acc[e] *= al;
             const unsigned have = __ballot_sync(0xffffffffu, in);
-            for (int t = 0; t < 32; ++t) {
-                if (!(have >> t & 1)) continue;
-                const float pt = __shfl_sync(0xffffffffu, p, t);
-                const size_t vo = __shfl_sync(0xffffffffu, (unsigned long long)off, t);
-                const T *v = vc + vo + lane * kPer;
+            // eight rows of V in flight; keys without a row (weight 0) load none
+            const int last = 32 - __clz(have);
+            for (int t0v = 0; t0v < last; t0v += 8) {
+                Row<T, kPer> v[8];
 #pragma unroll
-                for (int e = 0; e < kPer; ++e) acc[e] = fmaf(pt, static_cast<float>(v[e]), acc[e]);
+                for (int u = 0; u < 8; ++u) {
+                    const size_t vo = __shfl_sync(0xffffffffu, (unsigned long long)off, t0v + u);
+                    if (have >> (t0v + u) & 1) v[u].load(vc + vo + lane * kPer);
+                    else v[u].zero();
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const float pt = __shfl_sync(0xffffffffu, p, t0v + u);
+#pragma unroll
+                    for (int e = 0; e < kPer; ++e) acc[e] = fmaf(pt, v[u].f[e], acc[e]);
+                }
             }
         }
         const size_t o = ((size_t)i * a.Hq + h) * D + lane * kPer;
