@@ -81,8 +81,8 @@ cudaError_t launch_scored_umma_bf16(const ScoredArgs &a, const CUtensorMap &tmk,
 
 // Merge of the split-K partials of the rows that the plan listed.
 cudaError_t launch_scored_merge(const ScoredArgs &a, bool bf16, cudaStream_t st);
-// The same without a list (f32 caches), and with the sums of attention weights.
-cudaError_t launch_scored_finish(const ScoredArgs &a, bool bf16, cudaStream_t st);
+// The same without a list (f32 caches: listed false), and with the sums of attention weights.
+cudaError_t launch_scored_finish(const ScoredArgs &a, bool listed, bool bf16, cudaStream_t st);
 // CUDA-core kernel, one CTA per (row, KV head, partition): f32 caches.
 cudaError_t launch_scored_rows(const ScoredArgs &a, int dtype, cudaStream_t st);
 

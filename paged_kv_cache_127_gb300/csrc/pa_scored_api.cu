@@ -190,8 +190,9 @@ int32_t pa_decode_scored(const pa_dims *dims, const pa_score *score, const void 
             e = bf16 ? pa::launch_scored_decode_bf16(a, tmk, tmv, st) : pa::launch_scored_decode_f16(a, tmk, tmv, st);
     }
     if (e != cudaSuccess) return to_status(e);
-    const bool listed = dims->kv_dtype != PA_F32 && !a.sums;
-    return to_status(listed ? pa::launch_scored_merge(a, bf16, st) : pa::launch_scored_finish(a, bf16, st));
+    const bool listed = dims->kv_dtype != PA_F32;
+    return to_status(listed && !a.sums ? pa::launch_scored_merge(a, bf16, st)
+                                       : pa::launch_scored_finish(a, listed, bf16, st));
 }
 
 size_t pa_chunk_scored_workspace_bytes(const pa_dims *dims, int32_t num_tokens, int32_t max_query_len) {
@@ -240,7 +241,7 @@ int32_t pa_chunk_scored(const pa_dims *dims, const pa_score *score, const void *
     if (dims->kv_dtype == PA_F32) {
         e = pa::launch_scored_rows(a, PA_F32, st);
         if (e != cudaSuccess) return to_status(e);
-        return to_status(pa::launch_scored_finish(a, false, st));
+        return to_status(pa::launch_scored_finish(a, false, false, st));
     }
     const int G = dims->num_q_heads / dims->num_kv_heads;
     const bool umma = pa::chunk_uses_umma(max_query_len, G);

@@ -65,7 +65,7 @@ struct KeySpan {
 // thread are loaded before the totals are known, and each next four while the
 // last are added, so that a block pays one chain of loads, not one per step.
 template <typename T, int D, int G>
-__global__ void __launch_bounds__(kThreads) scored_finish_kernel(const ScoredArgs a, int splits) {
+__global__ void __launch_bounds__(kThreads) scored_finish_kernel(const ScoredArgs a, int splits, int merges) {
     __shared__ float2 tot[G];  // (M, 1 / L) of each head of the group
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = blockIdx.x % splits, kvh = blockIdx.x / splits % a.Hkv, i = blockIdx.x / splits / a.Hkv;
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kThreads) scored_finish_kernel(const ScoredArg
     const int2 range = row_range(a, i, r.pos, r.len);
     if (range.x >= range.y) return;
     const int p0 = range.x / a.partition_size, p1 = (range.y - 1) / a.partition_size;
-    const bool merge = p0 != p1 && split == 0;  // else written in place, or by another block
+    const bool merge = merges && p0 != p1 && split == 0;  // else written in place, by another block or the merge kernel
     if (!merge && !a.sums) return;
     const size_t head0 = (size_t)i * a.Hq + kvh * G;
     const int row = a.sums ? (a.sum_rows ? a.sum_rows[i] : i) : -1;
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kThreads) scored_finish_kernel(const ScoredArg
 }
 
 template <typename T, int D>
-cudaError_t launch_finish_t(const ScoredArgs &a, cudaStream_t st) {
+cudaError_t launch_finish_t(const ScoredArgs &a, bool merges, cudaStream_t st) {
     if (a.max_parts == 1 && !a.sums) return cudaSuccess;
     const long long pairs = (long long)a.T * a.Hkv;
     // Blocks for the sums: one resident wave (8 per SM), so that a few long sequences fill the GPU,
@@ -156,10 +156,10 @@ cudaError_t launch_finish_t(const ScoredArgs &a, cudaStream_t st) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     switch (a.Hq / a.Hkv) {
-        case 1: return cudaLaunchKernelEx(&cfg, scored_finish_kernel<T, D, 1>, a, (int)splits);
-        case 2: return cudaLaunchKernelEx(&cfg, scored_finish_kernel<T, D, 2>, a, (int)splits);
-        case 4: return cudaLaunchKernelEx(&cfg, scored_finish_kernel<T, D, 4>, a, (int)splits);
-        case 8: return cudaLaunchKernelEx(&cfg, scored_finish_kernel<T, D, 8>, a, (int)splits);
+        case 1: return cudaLaunchKernelEx(&cfg, scored_finish_kernel<T, D, 1>, a, (int)splits, (int)merges);
+        case 2: return cudaLaunchKernelEx(&cfg, scored_finish_kernel<T, D, 2>, a, (int)splits, (int)merges);
+        case 4: return cudaLaunchKernelEx(&cfg, scored_finish_kernel<T, D, 4>, a, (int)splits, (int)merges);
+        case 8: return cudaLaunchKernelEx(&cfg, scored_finish_kernel<T, D, 8>, a, (int)splits, (int)merges);
         default: return cudaErrorNotSupported;
     }
 }
@@ -197,16 +197,53 @@ __device__ __forceinline__ void merge_short(const float *ml, const float *acc, i
         }
 }
 
-// One warp per listed (row, head), lane i owning D / 32 columns; the blocks stride over the list.
+// Partials p0, p0 + step, ... below np of one (row, head), against the maximum M known beforehand.
+template <int D>
+__device__ __forceinline__ void merge_long(const float *ml, const float *acc, int p0, int step, int np, float M,
+                                           float (&o)[D / 32]) {
+    constexpr int kPer = D / 32;
+    constexpr int kU = 8;
+    for (int p = p0; p < np; p += kU * step) {
+        float w[kU], x[kU][kPer];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int q = p + u * step;
+            w[u] = -INFINITY;
+            if (q < np) {
+                w[u] = ml[2 * q];
+#pragma unroll
+                for (int e = 0; e < kPer; e += 2) {
+                    const float2 v = *reinterpret_cast<const float2 *>(acc + (size_t)q * D + e);
+                    x[u][e] = v.x;
+                    x[u][e + 1] = v.y;
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+            if (p + u * step < np) {
+                const float t = ex2(w[u] - M);
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) o[e] = fmaf(t, x[u][e], o[e]);
+            }
+    }
+}
+
+// Listed (row, head) pairs, lane i owning D / 32 columns; the blocks stride over the list.  One
+// warp each, or, while the pairs are fewer than the blocks, a whole block each, whose warps
+// share the partitions: a few long sequences have hundreds, and one warp's chain of loads over them took
+// longer than the attention (4 sequences of 20,000 tokens on average: 109 us a call).
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) scored_merge_kernel(const ScoredArgs a) {
-    constexpr int kPer = D / 32;
-    const int lane = threadIdx.x & 31;
+    constexpr int kPer = D / 32, kWarps = kThreads / 32;
+    __shared__ float part[kWarps][D];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const long long n = (long long)a.plan_hdr[2] * a.Hq;
-    for (long long w = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); w < n;
-         w += (long long)gridDim.x * (kThreads / 32)) {
+    const bool shared = n <= gridDim.x;
+    const long long step = shared ? gridDim.x : (long long)gridDim.x * kWarps;
+    for (long long w = shared ? blockIdx.x : (long long)blockIdx.x * kWarps + warp; w < n; w += step) {
         const int4 e = a.merge_list[w / a.Hq];
         const size_t head = (size_t)e.x * a.Hq + (int)(w % a.Hq);
         const int np = e.z - e.y + 1;
@@ -216,19 +253,27 @@ __global__ void __launch_bounds__(kThreads) scored_merge_kernel(const ScoredArgs
 #pragma unroll
         for (int i = 0; i < kPer; ++i) o[i] = 0.f;
         if (np <= 2) {
-            merge_short<D, 2>(ml, acc, np, o, L);
+            if (!shared || warp == 0) merge_short<D, 2>(ml, acc, np, o, L);
         } else if (np <= 8) {
-            merge_short<D, 8>(ml, acc, np, o, L);
+            if (!shared || warp == 0) merge_short<D, 8>(ml, acc, np, o, L);
         } else {
             const float2 t = merged_ml(ml, 0, np - 1, lane);
             L = t.y;
-#pragma unroll 8
-            for (int p = 0; p < np; ++p) {
-                const float x = ex2(ml[2 * p] - t.x);
+            merge_long<D>(ml, acc, shared ? warp : 0, shared ? kWarps : 1, np, t.x, o);
+            if (shared) {
+                __syncthreads();  // the last pair's parts have been read
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) o[i] = fmaf(x, acc[(size_t)p * D + i], o[i]);
+                for (int i = 0; i < kPer; ++i) part[warp][lane * kPer + i] = o[i];
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    o[i] = 0.f;
+#pragma unroll
+                    for (int v = 0; v < kWarps; ++v) o[i] += part[v][lane * kPer + i];
+                }
             }
         }
+        if (shared && warp != 0) continue;
         const float inv = L != 0.f ? 1.f / L : 0.f;
         const size_t at = head * D + lane * kPer;
 #pragma unroll
@@ -242,9 +287,9 @@ __global__ void __launch_bounds__(kThreads) scored_merge_kernel(const ScoredArgs
 template <typename T, int D>
 cudaError_t launch_merge_t(const ScoredArgs &a, cudaStream_t st) {
     if (a.max_parts == 1) return cudaSuccess;
-    const long long blocks = ((long long)a.T * a.Hq + kThreads / 32 - 1) / (kThreads / 32);
+    const long long pairs = (long long)a.T * a.Hq;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(blocks < 8 * 152 ? blocks : 8 * 152));  // one resident wave at most
+    cfg.gridDim = dim3((unsigned)(pairs < 8 * 152 ? pairs : 8 * 152));  // one resident wave at most
     cfg.blockDim = dim3(kThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -263,9 +308,16 @@ cudaError_t launch_scored_merge(const ScoredArgs &a, bool bf16, cudaStream_t st)
     return cudaErrorNotSupported;
 }
 
-cudaError_t launch_scored_finish(const ScoredArgs &a, bool bf16, cudaStream_t st) {
-    if (a.D == 64) return bf16 ? launch_finish_t<__nv_bfloat16, 64>(a, st) : launch_finish_t<__half, 64>(a, st);
-    if (a.D == 128) return bf16 ? launch_finish_t<__nv_bfloat16, 128>(a, st) : launch_finish_t<__half, 128>(a, st);
+cudaError_t launch_scored_finish(const ScoredArgs &a, bool listed, bool bf16, cudaStream_t st) {
+    // Rows of many partitions are merged by the merge kernel, a block each, before the sums; with up to
+    // 16 partitions the sums' blocks merge them on the way (one launch less).
+    const bool apart = listed && a.max_parts > 16;
+    if (apart) {
+        const cudaError_t e = launch_scored_merge(a, bf16, st);
+        if (e != cudaSuccess) return e;
+    }
+    if (a.D == 64) return bf16 ? launch_finish_t<__nv_bfloat16, 64>(a, !apart, st) : launch_finish_t<__half, 64>(a, !apart, st);
+    if (a.D == 128) return bf16 ? launch_finish_t<__nv_bfloat16, 128>(a, !apart, st) : launch_finish_t<__half, 128>(a, !apart, st);
     return cudaErrorNotSupported;
 }
 
