@@ -468,7 +468,9 @@ typedef struct pa_key_sums {
 
 /*
  * pa_decode_scored -- pa_decode with a pa_score, a choice of the output's type
- * and, optionally, the running sums of attention weights.
+ * and, optionally, the running sums of attention weights.  With a partition_size
+ * of 0 it starts from pa_decode's choice and takes up to four times that (at
+ * most 1024) on the device where the lengths leave enough work items.
  *
  *   score         NULL: plain
  *   key_sums      NULL: none

@@ -5,8 +5,7 @@
 // with z in log2 units and, when sums are asked for, every z_j left in the
 // workspace for the last launch (pa_scored_finish.cu).
 //
-// Work: an item is (sequence, context partition, group of HG KV heads), its keys
-// cut to the range.  The kernel is persistent, two CTAs per SM; a producer warp
+// Work: an item is (sequence, piece of its range, group of HG KV heads).  The kernel is persistent, two CTAs per SM; a producer warp
 // claims items (largest first) and streams their 16-key chunks into a ring of
 // shared-memory stages with TMA (one 3-D box is 16 rows of HG heads, 8 KB at HG =
 // 4), starting at the 16-key chunk that holds the range's first key, so a window or a
@@ -46,7 +45,7 @@ struct ScoredDecodeCfg {
     static constexpr size_t kEmptyOff = kFullOff + 8 * kStages;
     static constexpr size_t kItemFullOff = kEmptyOff + 8 * kStages;
     static constexpr size_t kItemEmptyOff = kItemFullOff + 8 * kSlots;
-    static constexpr size_t kInfoOff = kItemEmptyOff + 8 * kSlots;  // kSlots x (s, part, lo, hi), (g0, chunks, valid, pos)
+    static constexpr size_t kInfoOff = kItemEmptyOff + 8 * kSlots;  // kSlots x (s, piece, lo, hi), (g0, chunks, valid, pos)
     static constexpr size_t kTblOff = kInfoOff + 32 * kSlots;
     static constexpr size_t kSmem = kTblOff + (size_t)kSlots * kMaxPartitionBlocks * 4 + 1024;  // + alignment slack
     static_assert(D == 64 || D == 128, "head_dim");
@@ -121,8 +120,8 @@ __global__ void __launch_bounds__(ScoredDecodeCfg<D, HG>::kThreads, 2)
                 const RowOf r = row_of(a, s, cap);
                 const int2 k = row_range(a, s, r.pos, r.len);
                 if (k.x < k.y) {
-                    const int p0 = k.x / a.partition_size, p1 = (k.y - 1) / a.partition_size;
-                    e = make_int4(s, p0 | (p0 == p1 ? kWholeRange : 0), k.x, min(k.y, (p0 + 1) * a.partition_size));
+                    const int2 p = piece_of(k, a.partition_size, a.partition_size, 0);  // the same for every plan
+                    e = make_int4(s, p.y == k.y ? kWholeRange : 0, p.x, p.y);
                     g0 = (blockIdx.x % ngroups) * HG;
                     have = true;
                 }

@@ -21,6 +21,20 @@ __device__ __forceinline__ int2 row_range(const ScoredArgs &a, int i, int pos, i
     return begin < end ? make_int2(begin, end) : make_int2(0, 0);
 }
 
+// The pieces in which a listed decode splits a sequence's range [x, y): the first ends at
+// the next multiple of the partition size, `size`, the others at multiples of the size that
+// the plan chose, `wide` (a multiple of it).  Their number, and piece i.
+__device__ __forceinline__ int pieces_of(int2 k, int size, int wide) {
+    const int e = (k.x / size + 1) * size;
+    return e >= k.y ? 1 : 1 + (k.y - 1) / wide - e / wide + 1;
+}
+__device__ __forceinline__ int2 piece_of(int2 k, int size, int wide, int i) {
+    const int e = (k.x / size + 1) * size;
+    if (i == 0) return make_int2(k.x, min(k.y, e));
+    const int w = e / wide + i - 1;
+    return make_int2(max(e, w * wide), min(k.y, (w + 1) * wide));
+}
+
 // The sequence, position and length of query row i: a decode's row is its
 // sequence's last token (a length outside [0, cap] is clamped); a chunk's row
 // belongs to the last sequence s with query_start[s] <= i.  s = -1 when the row

@@ -38,7 +38,8 @@ struct ScoredArgs {
     float *ws_ml;                 // [T, Hq, P, 2]  (m in log2 units, l)
     float *ws_acc;                // [T, Hq, P, D]
     float *ws_logits;             // [S, Hq, cap] logits in log2 units; null without sums
-    int *plan_hdr;                // [0] work items, [1] claim counter, [2] rows to merge
+    int *plan_hdr;                // [0] work items, [1] claim counter, [2] rows to merge, [3] the
+                                  // decode plan's partition size
     int4 *plan_list;              // work items
     int4 *merge_list;             // (row, first partition, last partition, -) of the rows to merge
     unsigned int *err;
@@ -55,6 +56,8 @@ struct ScoredArgs {
     int row_warps;                // mma.sync chunk path: 16-row tiles per KV head per item
     int umma_rows;                // tcgen05 chunk path: query rows per CTA, else 0
     int ctas;                     // persistent grid of the tensor-core decode
+    int listed;                   // decode with a plan: pieces as the plan chose them
+    int widen;                    // the plan may choose a multiple of partition_size
     float scale, softcap;         // softcap 0: none
 };
 

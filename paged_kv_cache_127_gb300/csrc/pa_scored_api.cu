@@ -36,7 +36,7 @@ int32_t check_sums(const pa_key_sums *ks, int64_t cap) {
 }
 
 // Scored-attention workspace, each part 256-byte aligned:
-//   header    3 ints: work items, claim counter, CTAs done claiming
+//   header    4 ints: work items, claim counter, rows to merge, partition size chosen
 //   list      int4 [list_entries]
 //   merge     int4 [T]: rows whose range lies in several partitions (only with partials)
 //   acc, ml   float [T, Hq, P, D] and [T, Hq, P, 2]   (acc only if P > 1)
@@ -184,6 +184,8 @@ int32_t pa_decode_scored(const pa_dims *dims, const pa_score *score, const void 
         if (e == cudaSuccess)
             e = pa::cached_cache_map(v_cache, bf16, dims->head_dim, dims->block_size, block_heads, a.head_group, &tmv);
         if (e != cudaSuccess) return PA_ERR_CUDA;
+        a.listed = 1;
+        a.widen = dims->partition_size == 0;
         e = bf16 ? pa::scored_decode_ctas_bf16(a, &a.ctas) : pa::scored_decode_ctas_f16(a, &a.ctas);
         if (e == cudaSuccess) e = pa::launch_scored_decode_plan(a, st);
         if (e == cudaSuccess)

@@ -77,7 +77,11 @@ __global__ void __launch_bounds__(kThreads) scored_finish_kernel(const ScoredArg
     if (r.s < 0) return;
     const int2 range = row_range(a, i, r.pos, r.len);
     if (range.x >= range.y) return;
-    const int p0 = range.x / a.partition_size, p1 = (range.y - 1) / a.partition_size;
+    int p0 = range.x / a.partition_size, p1 = (range.y - 1) / a.partition_size;
+    if (a.listed) {
+        p0 = 0;
+        p1 = pieces_of(range, a.partition_size, a.plan_hdr[3]) - 1;
+    }
     const bool merge = merges && p0 != p1 && split == 0;  // else written in place, by another block or the merge kernel
     if (!merge && !a.sums) return;
     const size_t head0 = (size_t)i * a.Hq + kvh * G;

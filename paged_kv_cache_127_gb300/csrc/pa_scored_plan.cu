@@ -1,12 +1,15 @@
 // pa_scored_plan.cu -- work lists of the scored tensor-core kernels.
 //
-// Decode: one CTA lists every (sequence, partition) that holds keys of the sequence's
-// range, as (sequence, partition, first key, one past the last key), most 16-key
-// chunks first (a counting sort), so that the persistent decode hands out big
-// items before small ones.  Bit 30 of the partition marks an item that holds
-// its sequence's whole range.  The first partition of the first
-// min(S, ctas / groups) sequences is left out: decode CTA b takes it directly
-// (sequence b / groups), before this list is complete.  The plan also
+// Decode: one CTA lists the pieces of every sequence's range (piece_of), as (sequence,
+// piece, first key, one past the last key), most 16-key chunks first (a counting
+// sort), so that the persistent decode hands out big items before small ones.
+// Bit 30 of the piece marks an item that holds its sequence's whole range.  The
+// first piece of the first min(S, ctas / groups) sequences is left out: decode CTA
+// b takes it directly (sequence b / groups), before this list is complete.  Left to
+// choose, the plan widens the other pieces while the batch still has enough of
+// them: the host sees only the batch's shape, the plan its lengths, and longer pieces
+// mean fewer partials (32 sequences of 8192-32768 tokens: 442 us with pieces of 256,
+// 412 with 512, 397 with 1024; of 800 tokens: 26 us with 256, 34 with 512).  The plan also
 // resets the claim counters, writes the zero rows of empty ranges and flags bad
 // lengths.
 #include <climits>
@@ -17,7 +20,8 @@ namespace pa {
 
 namespace {
 
-constexpr int kBins = 1024;  // by chunk count, larger items binned together
+constexpr int kBins = 1024;     // by chunk count, larger items binned together
+constexpr int kMaxPiece = 1024;  // keys of a widened decode piece, at most (measured: 2048 is no faster)
 
 __device__ __forceinline__ void zero_row(const ScoredArgs &a, int i) {
     const int n = a.Hq * a.D;
@@ -31,16 +35,41 @@ __global__ void __launch_bounds__(1024) scored_decode_plan_kernel(const ScoredAr
     __shared__ int warp_sums[32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int tid = threadIdx.x, Pt = a.partition_size, cap = a.max_blocks * a.B;
+    const int tid = threadIdx.x, size = a.partition_size, cap = a.max_blocks * a.B;
     const int groups = a.Hkv / a.head_group;
     const int nstatic = min(a.S, a.ctas / groups);
     for (int i = tid; i < kBins; i += blockDim.x) hist[i] = 0;
-    __shared__ int merges;  // sequences whose range lies in several partitions
+    __shared__ int merges;  // sequences whose range lies in several pieces
+    __shared__ int counts[2];  // pieces of twice and four times the size
     if (tid == 0) {
         a.plan_hdr[1] = 0;
-        merges = 0;
+        merges = counts[0] = counts[1] = 0;
     }
     __syncthreads();
+    int wide = size;
+    if (a.widen) {
+        int n2 = 0, n4 = 0;
+        for (int s = tid; s < a.S; s += blockDim.x) {
+            const RowOf r = row_of(a, s, cap);
+            const int2 k = row_range(a, s, r.pos, r.len);
+            if (k.x >= k.y) continue;
+            n2 += pieces_of(k, size, 2 * size);
+            n4 += pieces_of(k, size, 4 * size);
+        }
+        n2 = __reduce_add_sync(0xffffffffu, n2);
+        n4 = __reduce_add_sync(0xffffffffu, n4);
+        if ((tid & 31) == 0 && n2 > 0) {
+            atomicAdd(&counts[0], n2);
+            atomicAdd(&counts[1], n4);
+        }
+        __syncthreads();
+        // at least 1.5 items a CTA, 3 for pieces of 1024 and more (whose ends leave CTAs idle longer)
+        auto enough = [&](int count, int to) { return 2LL * count * groups >= (to >= 1024 ? 6LL : 3LL) * a.ctas; };
+        if (enough(counts[0], 2 * size) && 2 * size <= kMaxPiece) {
+            wide = 2 * size;
+            if (enough(counts[1], 4 * size) && 4 * size <= kMaxPiece) wide = 4 * size;
+        }
+    }
     for (int s = tid; s < a.S; s += blockDim.x) {
         const int len = a.context_lens[s];
         if (len < 0 || len > cap) set_error(a.err, PA_DEVERR_BAD_LEN);
@@ -50,11 +79,11 @@ __global__ void __launch_bounds__(1024) scored_decode_plan_kernel(const ScoredAr
             zero_row(a, s);
             continue;
         }
-        const int p0 = k.x / Pt, p1 = (k.y - 1) / Pt;
-        if (p0 != p1) a.merge_list[atomicAdd(&merges, 1)] = make_int4(s, p0, p1, 0);
-        for (int p = s < nstatic ? p0 + 1 : p0; p <= p1; ++p) {
-            const int lo = max(k.x, p * Pt), hi = min(k.y, (p + 1) * Pt);
-            atomicAdd(&hist[min((hi - (lo & ~15) + 15) >> 4, kBins - 1)], 1);
+        const int np = pieces_of(k, size, wide);
+        if (np > 1) a.merge_list[atomicAdd(&merges, 1)] = make_int4(s, 0, np - 1, 0);
+        for (int i = s < nstatic ? 1 : 0; i < np; ++i) {
+            const int2 p = piece_of(k, size, wide, i);
+            atomicAdd(&hist[min((p.y - (p.x & ~15) + 15) >> 4, kBins - 1)], 1);
         }
     }
     __syncthreads();
@@ -62,16 +91,17 @@ __global__ void __launch_bounds__(1024) scored_decode_plan_kernel(const ScoredAr
     if (tid == 0) {
         a.plan_hdr[0] = total * groups;
         a.plan_hdr[2] = merges;
+        a.plan_hdr[3] = wide;
     }
     for (int s = tid; s < a.S; s += blockDim.x) {
         const RowOf r = row_of(a, s, cap);
         const int2 k = row_range(a, s, r.pos, r.len);
         if (k.x >= k.y) continue;
-        const int p0 = k.x / Pt, p1 = (k.y - 1) / Pt;
-        for (int p = s < nstatic ? p0 + 1 : p0; p <= p1; ++p) {
-            const int lo = max(k.x, p * Pt), hi = min(k.y, (p + 1) * Pt);
-            const int at = atomicAdd(&start[min((hi - (lo & ~15) + 15) >> 4, kBins - 1)], 1);
-            a.plan_list[at] = make_int4(s, p | (p0 == p1 ? kWholeRange : 0), lo, hi);
+        const int np = pieces_of(k, size, wide);
+        for (int i = s < nstatic ? 1 : 0; i < np; ++i) {
+            const int2 p = piece_of(k, size, wide, i);
+            const int at = atomicAdd(&start[min((p.y - (p.x & ~15) + 15) >> 4, kBins - 1)], 1);
+            a.plan_list[at] = make_int4(s, i | (np == 1 ? kWholeRange : 0), p.x, p.y);
         }
     }
 }
