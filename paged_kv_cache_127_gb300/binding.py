@@ -167,9 +167,14 @@ def _torch():
     return torch
 
 
+_TORCH_DTYPES = {}
+
+
 def _torch_dtype(code: int):
-    t = _torch()
-    return {PA_F32: t.float32, PA_F16: t.float16, PA_BF16: t.bfloat16}[code]
+    if not _TORCH_DTYPES:
+        t = _torch()
+        _TORCH_DTYPES.update({PA_F32: t.float32, PA_F16: t.float16, PA_BF16: t.bfloat16})
+    return _TORCH_DTYPES[code]
 
 
 def _expect(t, name, shape, dtype, device):
@@ -229,8 +234,11 @@ class Prepared:
 def _issue(fn, args, what, device, prepare, keep):
     if prepare:
         return Prepared(fn, args, what, device, keep)
-    with _on(device):
+    if _torch().cuda.current_device() == device.index:
         st = fn(*args)
+    else:
+        with _on(device):
+            st = fn(*args)
     _check(st, what)
     return None
 
