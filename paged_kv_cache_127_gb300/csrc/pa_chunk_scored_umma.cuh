@@ -34,7 +34,7 @@ namespace pa {
 // kGeneral need a positive scale.
 enum ScoredMode {
     kMaskOnly,   // ranges only
-    kCapFixed,   // bf16, cap of at most 59: no running maximum (see below)
+    kCapFixed,   // bf16, cap of at most 55: no running maximum (see below)
     kCapMax,     // cap, running maximum
     kBias,       // distance bias
     kGeneral,    // cap and bias, or a scale that is not positive
@@ -42,7 +42,7 @@ enum ScoredMode {
 inline ScoredMode scored_mode(const ScoredArgs &a, bool bf16) {
     if (!(a.scale > 0.f) || (a.softcap > 0.f && a.slopes)) return kGeneral;
     if (a.slopes) return kBias;
-    if (a.softcap > 0.f) return bf16 && a.softcap * kLog2e <= 86.f ? kCapFixed : kCapMax;
+    if (a.softcap > 0.f) return bf16 && a.softcap * kLog2e <= 80.f ? kCapFixed : kCapMax;
     return kMaskOnly;
 }
 
@@ -438,9 +438,11 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
         const float sl = a.scale * kLog2e;
         // a bias in the units of the logits below (raw, or log2 with a scale that is not positive)
         const float slope_units = kMode == kGeneral && !(sl > 0.f) ? 1.f : 1.f / sl;
-        // kCapFixed: capped logits lie within cap log2(e) <= 86 of 0, so with bf16 weights (the
-        // exponents of fp32) 2^z, its sum over 2^20 keys and its low part stay normal numbers
-        // without a maximum: no maximum, no rescaling.  A bias has no such bound.
+        // kCapFixed: capped logits lie within c = cap log2(e) <= 80 of 0, so with bf16 weights (the
+        // exponents of fp32) a constant, max(0, c - 48), does for the maximum: weights and their
+        // low parts stay normal numbers (2^-121 and above), and sums of 2^22 weights of at most 2^48
+        // leave values up to 2^58 room: no maximum, no rescaling.  A bias has no such bound.
+        const float fixed_max = fmaxf(0.f, a.softcap * kLog2e - 48.f);
         constexpr bool kCap = kMode == kCapFixed || kMode == kCapMax;
         constexpr bool kSlopes = kMode == kBias || kMode == kGeneral;
         const CapFit fit(a.softcap > 0.f ? a.scale / a.softcap : 0.f);
@@ -469,7 +471,7 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
             const int2 range = t < n ? row_range(a, it.qs + t, pos, it.len) : make_int2(0, 0);
             const float slope = kSlopes && a.slopes ? a.slopes[it.kvh * G + R % G] * kLog2e * slope_units : 0.f;
             const int k_first = it.lo / C::kN * C::kN;
-            float m_used = -INFINITY, l = 0.f;
+            float m_used = kMode == kCapFixed ? fixed_max : -INFINITY, l = 0.f;
             for (int j = 0; j < nch; ++j, ++g, ++c) {
                 const int b = c % kSB;
                 const int st = g % C::kStages;

@@ -412,3 +412,95 @@ def test_scored_graph_replay_and_other_stream(gpu):
         assert torch.equal(outs[0], outs[1])
         assert torch.equal(sums[0], sums[1])
     assert pa.pa_device_errors(clear=True) == 0
+
+
+@pytest.mark.parametrize("S,hi,window", [(100, 4000, 0), (100, 12000, 0), (150, 9000, 3000), (1500, 60, 0)])
+def test_decode_scored_wide_pieces_and_many_sequences(gpu, S, hi, window):
+    # enough work for the plan to widen the pieces twofold and fourfold; more sequences than the plan has threads
+    torch, pa = gpu
+    rng = synth.make_rng(7900 + S + hi)
+    Hq = Hkv = 8
+    D, B = 64, 16
+    lens = rng.integers(max(1, hi // 3), hi + 1, S).astype(np.int32)
+    mb = -(-hi // B)
+    N = int((-(-lens // B)).sum())
+    tables = np.full((S, mb), -1, np.int32)
+    perm, at = rng.permutation(N), 0
+    for s, n in enumerate(lens):
+        k = -(-int(n) // B)
+        tables[s, :k] = perm[at:at + k]
+        at += k
+    gen = torch.Generator(device="cuda").manual_seed(S + hi)
+    kc, vc = (torch.randn(N, Hkv, B, D, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    q = torch.randn(S, Hq, D, generator=gen, device="cuda").bfloat16()
+    dims = pa.make_dims(S, Hq, Hkv, D, B, N, mb, 0, "bf16")
+    out, sums = torch.empty(S, Hq, D, device="cuda"), torch.zeros(S, Hkv, mb * B, device="cuda")
+    ws = torch.empty(pa.pa_decode_scored_workspace_bytes(dims, True), dtype=torch.uint8, device="cuda")
+    score = pa.make_score(softcap=6.0, window=window)
+    pa.pa_decode_scored(dims, score, q, kc, vc, i32(torch, tables), i32(torch, lens), 0.125, out, ws, key_sums=sums)
+    plain = torch.empty_like(out)
+    ws2 = torch.empty(pa.pa_decode_scored_workspace_bytes(dims, False), dtype=torch.uint8, device="cuda")
+    pa.pa_decode_scored(dims, score, q, kc, vc, i32(torch, tables), i32(torch, lens), 0.125, plain, ws2)
+    for s in range(S):
+        n = int(lens[s])
+        b = max(0, n - window) if window else 0
+        blocks = torch.from_numpy(tables[s, :-(-n // B)].astype(np.int64)).cuda()
+        K, V = (c[blocks].transpose(0, 1).reshape(Hkv, -1, D)[:, b:n].double() for c in (kc, vc))
+        z = 6.0 * torch.tanh(0.125 * torch.einsum("hjd,hd->hj", K, q[s].double()) / 6.0)
+        p = torch.softmax(z, -1)
+        # logits of |z| <= 6 whose products sum to at most 64 * 0.125 * max|q| max|k|
+        E = weight_error("bf16", 64 * 2.0 ** -23 * 0.125 * 64 * 25 + 6 * 2.0 ** -21 + 6 * 2.0 ** -22, n)
+        ref = torch.einsum("hj,hjd->hd", p, V)
+        for got in (out, plain):   # the sums' kernel joins partials in another order
+            assert (got[s].double() - ref).abs().max() <= 2.5 * E * V.abs().max()
+        assert ((sums[s, :, b:n].double() - p).abs() <= 3 * E * p + 1e-30).all()
+        assert (sums[s, :, :b] == 0).all() and (sums[s, :, n:] == 0).all()
+    assert pa.pa_device_errors(clear=True) == 0
+
+
+@pytest.mark.parametrize("S,nq,hi", [(2100, 3, 40), (9, 1000, 1000), (700, 20, 60)])
+def test_chunk_scored_plans_of_many_rows(gpu, S, nq, hi):
+    # more sequences, blocks or rows than the plan keeps in shared memory or reads at once, with masks
+    torch, pa = gpu
+    rng = synth.make_rng(7950 + S)
+    Hq, Hkv, D, B = 4, 1, 64, 16
+    counts = rng.integers(0 if S > 9 else nq, nq + 1, S)
+    lens = np.array([int(rng.integers(n, max(hi, n) + 1)) for n in counts], np.int32)
+    mb = max(1, -(-int(lens.max()) // B))
+    N = int((-(-lens // B)).sum()) + 1
+    tables = np.full((S, mb), -1, np.int32)
+    perm, at = rng.permutation(N), 0
+    for s, n in enumerate(lens):
+        k = -(-int(n) // B)
+        tables[s, :k] = perm[at:at + k]
+        at += k
+    qs = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    T = int(qs[-1])
+    gen = torch.Generator(device="cuda").manual_seed(S)
+    kc, vc = (torch.randn(N, Hkv, B, D, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    q = torch.randn(T, Hq, D, generator=gen, device="cuda").bfloat16()
+    pos = np.concatenate([np.arange(n - m, n) for n, m in zip(lens, counts)]).astype(np.int64)
+    begin = np.where(rng.random(T) < 0.05, pos + 1, pos - pos % 37)   # documents, and some rows with nothing
+    dims = pa.make_dims(S, Hq, Hkv, D, B, N, mb, 0, "bf16")
+    out = torch.full((T, Hq, D), 7.0, device="cuda")
+    ws = torch.empty(pa.pa_chunk_scored_workspace_bytes(dims, T, nq), dtype=torch.uint8, device="cuda")
+    pa.pa_chunk_scored(dims, pa.make_score(key_begin=i32(torch, begin)), q, kc, vc, i32(torch, tables), i32(torch, lens),
+                       i32(torch, qs), 0.125, out, nq, ws)
+    for s in range(S):
+        n, m = int(lens[s]), int(counts[s])
+        if m == 0:
+            continue
+        blocks = torch.from_numpy(tables[s, :-(-n // B)].astype(np.int64)).cuda()
+        K, V = (c[blocks].transpose(0, 1).reshape(-1, D)[:n].double() for c in (kc, vc))
+        rows = slice(int(qs[s]), int(qs[s + 1]))
+        z = 0.125 * torch.einsum("thd,jd->thj", q[rows].double(), K)
+        j = torch.arange(n, device="cuda")
+        b = torch.from_numpy(begin[rows]).cuda()[:, None]
+        p0 = torch.from_numpy(pos[rows]).cuda()[:, None]
+        seen = (j >= b) & (j <= p0)
+        w = torch.softmax(z.masked_fill(~seen[:, None], -math.inf), -1).nan_to_num(0.0)
+        ref = torch.einsum("thj,jd->thd", w, V)
+        E = weight_error("bf16", 64 * 2.0 ** -23 * 0.125 * 64 * 25 + 2.0 ** -22 * 20, n)
+        assert (out[rows].double() - ref).abs().max() <= 2.5 * E * V.abs().max()
+        assert (out[rows][~seen.any(-1)] == 0).all()
+    assert pa.pa_device_errors(clear=True) == 0
