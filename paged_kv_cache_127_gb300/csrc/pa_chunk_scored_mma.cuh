@@ -325,6 +325,16 @@ __global__ void __launch_bounds__(ChunkCfg<D, HG, RW>::kThreads, ChunkCfg<D, HG,
                     f[i] = sc[c][nt][0][e] + sc[c][nt][1][e];
                     f[8 + i] = sc[c][nt][0][2 + e] + sc[c][nt][1][2 + e];
                 }
+                const bool partial = kb < win0 || kb + 32 > win1;  // some row does not see all of them
+                if (partial && score.cap) {
+                    // which form of the cap a warp takes must not depend on what masked keys hold
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int key = kb + 16 * (i >> 2) + 8 * (i >> 1 & 1) + c2 + (i & 1);
+                        if (key < k0.x || key >= k0.y) f[i] = 0.f;
+                        if (key < k1.x || key >= k1.y) f[8 + i] = 0.f;
+                    }
+                }
                 to_log2(f);
                 float x0[8], x1[8];
 #pragma unroll
@@ -340,7 +350,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, HG, RW>::kThreads, ChunkCfg<D, HG,
                         x1[i] -= s1 * fabsf((float)(pos1 - key));
                     }
                 }
-                if (kb < win0 || kb + 32 > win1) {
+                if (partial) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int key = kb + 16 * (i >> 2) + 8 * (i >> 1 & 1) + c2 + (i & 1);
@@ -471,14 +481,22 @@ __global__ void __launch_bounds__(ChunkCfg<D, HG, RW>::kThreads, ChunkCfg<D, HG,
                     f[i] = sc[nt][0][e] + sc[nt][1][e];
                     f[4 + i] = sc[nt][0][2 + e] + sc[nt][1][2 + e];
                 }
+                bool in0[4], in1[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int key = kb + 8 * (i >> 1) + c2 + (i & 1);
+                    in0[i] = key < kb + n1 && key >= k0.x && key < k0.y;
+                    in1[i] = key < kb + n1 && key >= k1.x && key < k1.y;
+                    if (!in0[i]) f[i] = 0.f;  // as above
+                    if (!in1[i]) f[4 + i] = 0.f;
+                }
                 to_log2(f);
                 float x0[4], x1[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int key = kb + 8 * (i >> 1) + c2 + (i & 1);
-                    const bool in = key < kb + n1;
-                    x0[i] = in && key >= k0.x && key < k0.y ? f[i] - s0 * fabsf((float)(pos0 - key)) : -INFINITY;
-                    x1[i] = in && key >= k1.x && key < k1.y ? f[4 + i] - s1 * fabsf((float)(pos1 - key)) : -INFINITY;
+                    x0[i] = in0[i] ? f[i] - s0 * fabsf((float)(pos0 - key)) : -INFINITY;
+                    x1[i] = in1[i] ? f[4 + i] - s1 * fabsf((float)(pos1 - key)) : -INFINITY;
                 }
                 float mx0 = fmaxf(fmaxf(x0[0], x0[1]), fmaxf(x0[2], x0[3]));
                 float mx1 = fmaxf(fmaxf(x1[0], x1[1]), fmaxf(x1[2], x1[3]));

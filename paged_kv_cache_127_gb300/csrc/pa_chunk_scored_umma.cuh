@@ -490,6 +490,15 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
                 float f[C::kN];
 #pragma unroll
                 for (int cc = 0; cc < C::kN; ++cc) f[cc] = __uint_as_float(sv[cc >> 5][cc & 31]);
+                // every key of the step loaded and seen by all of the warp's rows
+                const bool whole = __all_sync(0xffffffffu, vb <= 0 && ve >= C::kN) && mask == (1 << C::kBoxes) - 1;
+                auto seen = [&](int cc) { return cc >= vb && cc < ve && (mask >> (cc >> 4) & 1); };
+                if (!whole && (kCap || kMode == kGeneral)) {
+                    // which form of the cap a warp takes must not depend on what masked keys hold
+#pragma unroll
+                    for (int cc = 0; cc < C::kN; ++cc)
+                        if (!seen(cc)) f[cc] = 0.f;
+                }
                 // raw units (the positive scale is folded into the exponent's FFMA), or log2 units here
                 float mul = sl;
                 if (kMode == kGeneral && !(sl > 0.f)) {
@@ -517,11 +526,10 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
                         for (int cc = 0; cc < C::kN; ++cc) f[cc] = fmaf(-slope, fabsf(d0 - (float)cc), f[cc]);
                     }
                 }
-                if (!(__all_sync(0xffffffffu, vb <= 0 && ve >= C::kN) && mask == (1 << C::kBoxes) - 1)) {
-                    // a step that some row sees in part, or over boxes not loaded
+                if (!whole) {
 #pragma unroll
                     for (int cc = 0; cc < C::kN; ++cc)
-                        if (!(cc >= vb && cc < ve && (mask >> (cc >> 4) & 1))) f[cc] = -INFINITY;
+                        if (!seen(cc)) f[cc] = -INFINITY;
                 }
                 // row maximum as 8 independent chains (a single 64-long chain of
                 // dependent max operations would sit on the critical path)

@@ -504,3 +504,30 @@ def test_chunk_scored_plans_of_many_rows(gpu, S, nq, hi):
         assert (out[rows].double() - ref).abs().max() <= 2.5 * E * V.abs().max()
         assert (out[rows][~seen.any(-1)] == 0).all()
     assert pa.pa_device_errors(clear=True) == 0
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("nq", [2, 40, 130])
+@pytest.mark.parametrize("opts", [dict(cap=6.0), dict(cap=6.0, slopes=0.25)])
+def test_chunk_scored_bits_do_not_depend_on_masked_keys(gpu, opts, nq, dtype):
+    # slots behind the last token, before every range, and in shared memory from another call
+    torch, pa = gpu
+    rng = synth.make_rng(7980 + nq + len(dtype))
+    lens = [nq, nq + 41, 700]
+    (q, kc, vc, tables, lens), qs = chunk_case(rng, dtype, 8, 2, 64, 16, lens, [nq] * 3)
+    opts = dict(opts, key_begin=[max(0, p - 77) for n in lens for p in range(int(n) - nq, int(n))])
+    if "slopes" in opts:
+        opts["slopes"] = [opts["slopes"]] * 8
+    first = [max(0, int(n) - nq - 77) for n in lens]
+    gots = []
+    for value in (0.0, 200.0, -90.0, 0.0):
+        k1, v1 = kc.copy(), vc.copy()
+        fill = synth.to_storage(np.full(1, value, np.float32), dtype)[0]
+        for s, n in enumerate(lens):
+            for j in list(range(first[s])) + list(range(int(n), -(-int(n) // 16) * 16)):
+                k1[tables[s][j // 16], :, j % 16] = fill
+                v1[tables[s][j // 16], :, j % 16] = fill
+        gots.append(call_chunk(torch, pa, (q, k1, v1, tables, lens), qs, dtype, "f32", 0.05, opts))
+    for got in gots[1:]:
+        assert (got == gots[0]).all()
+    assert pa.pa_device_errors(clear=True) == 0
