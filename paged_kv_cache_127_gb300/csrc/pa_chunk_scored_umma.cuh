@@ -56,8 +56,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // biased, the softmax warpgroups come behind two whole warpgroups of producers and issuers (two
 // warps of which idle), so that the latter's registers can be handed to them: 512 threads
 // are launched at 128 registers, 8 warps keep 72 and 8 take 184 (8 x 72 + 8 x 184 = 16 x 128).
-// Measured on 16 x 512-token chunks: capped 356 -> 348 us, biased 382 -> 373, both 563 -> 534; with
-// ranges only, 280 -> 286, so that kernel keeps the 14 warps.
+// Measured on 16 x 512-token chunks of D 128: capped 356 -> 350 us, both 508 -> 486, ragged
+// biased prompts of D 64 69 -> 65; with ranges only 260 -> 268, so that kernel keeps the 14 warps.
 template <int D, int MT, int kMode>
 struct ScoredUmmaCfg : UmmaCfg<D, MT> {
     static constexpr bool kRegSplit = MT == 2 && kMode != kMaskOnly;
@@ -199,6 +199,7 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
         const uint64_t qpol = policy_evict_first();
         const CUtensorMap *map = is_v ? &tmv : &tmk;
         const uint32_t ring = kvb + (is_v ? (uint32_t)C::kTile : 0u);
+        const int bx = lane % C::kBoxes, sbx = lane / C::kBoxes;
         int g = 0;                  // ring steps issued
         int ku[MT];                 // items published to each tile so far (query-tile sets)
 #pragma unroll
@@ -252,51 +253,39 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
                 if (!ok || sl.end) break;
                 it = sl.it;
             }
+            // One lane per copy: box bx of 16 keys, 64 of their columns; its block id is read a step
+            // ahead.  (One lane reading the four ids and issuing the eight copies in turn held the steps up:
+            // 345 us against 329 on 16 x 512-token capped chunks, 280 against 263 with ranges only.)
             const int32_t *row = a.block_tables + (size_t)it.s * a.max_blocks;
             const int j0 = it.lo / C::kN, lb = __ffs(a.B) - 1;  // B is a power of two
+            auto wanted = [&](int j) {
+                const int tok = j * C::kN + 16 * bx;
+                return lane < C::kBoxes * C::kSub && tok + 15 >= it.lo && tok < it.hi;
+            };
+            int next = wanted(j0) ? row[(j0 * C::kN + 16 * bx) >> lb] : 0;
             for (int j = j0; j < j0 + it.nch; ++j, ++g) {
                 const int st = g % C::kStages;
+                const int pbk = next, tok = j * C::kN + 16 * bx;
+                const bool want = wanted(j), good = want && pbk >= 0 && pbk < a.N;
+                if (j + 1 < j0 + it.nch && wanted(j + 1)) next = row[(tok + C::kN) >> lb];
+                if (want && !good && !is_v) set_error(a.err, PA_DEVERR_BAD_BLOCK);
+                const int mask = (int)(__ballot_sync(0xffffffffu, good) & ((1u << C::kBoxes) - 1u));
                 if (g >= C::kStages &&
                     !mbar_wait_bounded(is_v ? v_empty(st) : k_empty(st), (uint32_t)((g / C::kStages) - 1) & 1u,
                                        kWaitLimit)) {
                     ok = false;
                     break;
                 }
+                const uint32_t bar = is_v ? v_full(st) : k_full(st);
                 if (lane == 0) {
-                    int mask = 0, blk[C::kBoxes];
-#pragma unroll
-                    for (int i = 0; i < C::kBoxes; ++i) {
-                        const int tok = j * C::kN + 16 * i;
-                        blk[i] = -1;
-                        if (tok + 15 >= it.lo && tok < it.hi) {
-                            const int pbk = row[tok >> lb];
-                            if (pbk >= 0 && pbk < a.N) {
-                                blk[i] = pbk;
-                                mask |= 1 << i;
-                            } else if (!is_v) {
-                                set_error(a.err, PA_DEVERR_BAD_BLOCK);
-                            }
-                        }
-                    }
                     if (is_v) vmask[st] = mask;  // read by the softmax after v_full (released with v_empty)
-                    const uint32_t bar = is_v ? v_full(st) : k_full(st);
-                    const uint32_t bytes = (uint32_t)__popc(mask) * C::kSub * 2048u;
-                    if (bytes == 0) {
-                        mbar_arrive(bar);
-                    } else {
-                        mbar_arrive_expect_tx(bar, bytes);
-                        const uint32_t dst = ring + (uint32_t)(st * C::kStageBytes);
-#pragma unroll
-                        for (int i = 0; i < C::kBoxes; ++i) {
-                            if (!(mask >> i & 1)) continue;
-                            const int y = (j * C::kN + 16 * i) & (a.B - 1);
-                            const int z = blk[i] * a.Hkv + it.kvh;
-#pragma unroll
-                            for (int sb = 0; sb < C::kSub; ++sb)
-                                tma_load_3d(dst + (uint32_t)(sb * C::kHalf + i * 2048), map, sb * 64, y, z, bar, pol);
-                        }
-                    }
+                    if (mask == 0) mbar_arrive(bar);
+                    else mbar_arrive_expect_tx(bar, (uint32_t)__popc(mask) * C::kSub * 2048u);
                 }
+                __syncwarp();
+                if (good)
+                    tma_load_3d(ring + (uint32_t)(st * C::kStageBytes + sbx * C::kHalf + bx * 2048), map, sbx * 64,
+                                tok & (a.B - 1), pbk * a.Hkv + it.kvh, bar, pol);
                 __syncwarp();
             }
             if (!ok) break;
@@ -490,15 +479,16 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
                 float f[C::kN];
 #pragma unroll
                 for (int cc = 0; cc < C::kN; ++cc) f[cc] = __uint_as_float(sv[cc >> 5][cc & 31]);
-                // every key of the step loaded and seen by all of the warp's rows
-                const bool whole = __all_sync(0xffffffffu, vb <= 0 && ve >= C::kN) && mask == (1 << C::kBoxes) - 1;
-                auto seen = [&](int cc) { return cc >= vb && cc < ve && (mask >> (cc >> 4) & 1); };
-                if (!whole && (kCap || kMode == kGeneral)) {
-                    // which form of the cap a warp takes must not depend on what masked keys hold
+                // the step's keys that this row sees, a bit each (comparing positions key by key took ragged
+                // prompts with a prefix mask, D 64, from 61 us to 65)
+                uint32_t see[C::kN / 32];
 #pragma unroll
-                    for (int cc = 0; cc < C::kN; ++cc)
-                        if (!seen(cc)) f[cc] = 0.f;
+                for (int w = 0; w < C::kN / 32; ++w) {
+                    auto below = [&](int x) { return x >= 32 ? ~0u : (1u << max(x, 0)) - 1u; };
+                    see[w] = below(ve - 32 * w) & ~below(vb - 32 * w) &
+                             ((mask >> (2 * w) & 1 ? 0xffffu : 0u) | (mask >> (2 * w + 1) & 1 ? 0xffff0000u : 0u));
                 }
+                auto seen = [&](int cc) { return (see[cc >> 5] >> (cc & 31) & 1u) != 0u; };
                 // raw units (the positive scale is folded into the exponent's FFMA), or log2 units here
                 float mul = sl;
                 if (kMode == kGeneral && !(sl > 0.f)) {
@@ -510,7 +500,17 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
                     float am[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int cc = 0; cc < C::kN; cc += 2) am[cc >> 1 & 3] = max3(am[cc >> 1 & 3], fabsf(f[cc]), fabsf(f[cc + 1]));
-                    cap_in_place(f, fit, fmaxf(fmaxf(am[0], am[1]), fmaxf(am[2], am[3])));
+                    float most = fmaxf(fmaxf(am[0], am[1]), fmaxf(am[2], am[3]));
+                    if (__all_sync(0xffffffffu, most <= fit.near)) {
+                        cap_near(f, fit);
+                    } else {
+                        // which form a warp takes must not depend on what masked keys hold (asked only
+                        // here: zeroing their logits in every step that has some took 350 us against 334)
+                        most = 0.f;
+#pragma unroll
+                        for (int cc = 0; cc < C::kN; ++cc) most = fmaxf(most, seen(cc) ? fabsf(f[cc]) : 0.f);
+                        cap_in_place(f, fit, most);
+                    }
                 }
                 // bias: -slope |pos - key| = -slope (pos - k0) + slope cc where no key of the step lies
                 // past pos (any step but the last of a prefix): the first part goes into the exponent's FFMA
@@ -526,6 +526,8 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
                         for (int cc = 0; cc < C::kN; ++cc) f[cc] = fmaf(-slope, fabsf(d0 - (float)cc), f[cc]);
                     }
                 }
+                // every key of the step loaded and seen by all of the warp's rows
+                const bool whole = __all_sync(0xffffffffu, vb <= 0 && ve >= C::kN) && mask == (1 << C::kBoxes) - 1;
                 if (!whole) {
 #pragma unroll
                     for (int cc = 0; cc < C::kN; ++cc)
@@ -607,8 +609,8 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
                             asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vrow + sb * C::kHalf + cc * 16),
                                          "r"(0u)
                                          : "memory");
+                    tc::fence_async_smem();
                 }
-                tc::fence_async_smem();
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) {

@@ -124,20 +124,26 @@ struct CapFit {
         near = in >= 0x1p-14f && in <= 0x1p10f ? 0.5f / in : -1.f;
     }
 };
+// Its first form.
+template <int N>
+__device__ __forceinline__ void cap_near(float (&f)[N], const CapFit &c) {
+    auto both = [](float x) { return tc::f2(x, x); };
+    const uint64_t c1 = both(c.c1), c2 = both(c.c2), c3 = both(c.c3), c4 = both(c.c4);
+#pragma unroll
+    for (int v = 0; v < N / 2; ++v) {
+        const uint64_t x = tc::f2(f[2 * v], f[2 * v + 1]);
+        const uint64_t z = mul2(x, x);
+        const uint64_t q = tc::fma2(tc::fma2(tc::fma2(z, c4, c3), z, c2), z, c1);
+        const float2 r = tc::f2split(tc::fma2(mul2(x, z), q, x));
+        f[2 * v] = r.x;
+        f[2 * v + 1] = r.y;
+    }
+}
 template <int N>
 __device__ __forceinline__ void cap_in_place(float (&f)[N], const CapFit &c, float most) {
     auto both = [](float x) { return tc::f2(x, x); };
     if (__all_sync(0xffffffffu, most <= c.near)) {
-        const uint64_t c1 = both(c.c1), c2 = both(c.c2), c3 = both(c.c3), c4 = both(c.c4);
-#pragma unroll
-        for (int v = 0; v < N / 2; ++v) {
-            const uint64_t x = tc::f2(f[2 * v], f[2 * v + 1]);
-            const uint64_t z = mul2(x, x);
-            const uint64_t q = tc::fma2(tc::fma2(tc::fma2(z, c4, c3), z, c2), z, c1);
-            const float2 r = tc::f2split(tc::fma2(mul2(x, z), q, x));
-            f[2 * v] = r.x;
-            f[2 * v + 1] = r.y;
-        }
+        cap_near(f, c);
     } else if (__all_sync(0xffffffffu, most * c.in <= 0.9f)) {
         const uint64_t in2 = both(c.in);
 #pragma unroll
