@@ -167,14 +167,4 @@ __device__ __forceinline__ void cap_in_place(float (&f)[N], const CapFit &c, flo
     }
 }
 
-// One output value rounded to the output's type.
-template <typename T>
-__device__ __forceinline__ void store_out(T *p, float x);
-template <>
-__device__ __forceinline__ void store_out<float>(float *p, float x) { *p = x; }
-template <>
-__device__ __forceinline__ void store_out<__half>(__half *p, float x) { *p = __float2half_rn(x); }
-template <>
-__device__ __forceinline__ void store_out<__nv_bfloat16>(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
-
 }  // namespace pa

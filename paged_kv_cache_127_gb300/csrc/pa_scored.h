@@ -87,7 +87,7 @@ cudaError_t launch_scored_merge(const ScoredArgs &a, bool bf16, cudaStream_t st)
 // The same without a list (f32 caches: listed false), and with the sums of attention weights.
 cudaError_t launch_scored_finish(const ScoredArgs &a, bool listed, bool bf16, cudaStream_t st);
 // CUDA-core kernel, one CTA per (row, KV head, partition): f32 caches.
-cudaError_t launch_scored_rows(const ScoredArgs &a, int dtype, cudaStream_t st);
+cudaError_t launch_scored_rows(const ScoredArgs &a, cudaStream_t st);
 
 // ------------------------------------------------------------------ rotary positions and KV write
 struct RopeArgs {

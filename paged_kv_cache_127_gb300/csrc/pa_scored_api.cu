@@ -174,7 +174,7 @@ int32_t pa_decode_scored(const pa_dims *dims, const pa_score *score, const void 
     cudaError_t e;
     const bool bf16 = dims->kv_dtype == PA_BF16;
     if (dims->kv_dtype == PA_F32) {
-        e = pa::launch_scored_rows(a, PA_F32, st);
+        e = pa::launch_scored_rows(a, st);
     } else {
         // work list, the persistent tensor-core kernel, then merge and sums
         // (each launch a programmatic dependent of the one before)
@@ -241,7 +241,7 @@ int32_t pa_chunk_scored(const pa_dims *dims, const pa_score *score, const void *
     cudaError_t e;
     const bool bf16 = dims->kv_dtype == PA_BF16;
     if (dims->kv_dtype == PA_F32) {
-        e = pa::launch_scored_rows(a, PA_F32, st);
+        e = pa::launch_scored_rows(a, st);
         if (e != cudaSuccess) return to_status(e);
         return to_status(pa::launch_scored_finish(a, false, false, st));
     }
