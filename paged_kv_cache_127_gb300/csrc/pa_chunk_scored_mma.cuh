@@ -18,6 +18,7 @@
 // partitions store (m, l, acc) and the merge combines those the range touches.
 //
 // Bound: HBM (a chunk's rows share each key).
+// Measured: five drafted tokens of 256 sequences (32 / 8 heads, D 128, bf16, capped) 131 us (floor 116).
 #pragma once
 
 #include <cuda.h>

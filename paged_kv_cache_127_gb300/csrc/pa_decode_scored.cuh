@@ -17,6 +17,9 @@
 // memory, so what they hold does not matter.
 //
 // Bound: HBM (4 D bytes per key and KV head against G x 4 D flops).
+// Measured (D 128): 256 sequences, 32 / 8 heads, bf16, capped 126 us = 6.7 TB/s, 146 with sums; 64
+// sequences, 32 / 32 heads, f16, documents and bias 114 us (floor 113); a window of 4096 over 32 long
+// sequences, 64 / 8 heads, bf16, 89 us, 107 with sums (floor 78, 80).
 #pragma once
 
 #include <cuda.h>

@@ -15,6 +15,8 @@
 // Copy: 16 bytes of a K and a V row per thread and row, several rows in flight.
 //
 // Bound: HBM for a batch (the kept rows, read and written); latency for one sequence.
+// Measured: 64 sequences of 2500 to 4096 tokens cut to 2048 (8 KV heads, D 128, bf16) 184 us, of which the
+// selection 20 and the copy 162 (6.3 TB/s; floor 159); one of 32768 tokens cut to 8192 (D 64) 14 + 10 us.
 #include <cooperative_groups.h>
 
 #include "pa_device.cuh"

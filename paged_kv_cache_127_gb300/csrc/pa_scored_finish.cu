@@ -9,6 +9,9 @@
 //   sums[row, kvh, j] += sum_g 2^(z_gj - M_g) / L_g
 // from the logits z that the partition kernel left (4 bytes per query head and
 // key, against 2 D elements of K and V that a second pass would read again).
+//
+// Bound: latency of short chains of loads.  Measured alone, caches cold: the sums of 256 sequences of 800
+// tokens on average 20 us, of 32 windows of 4096 keys 18 us; the merges of such batches 6 to 9 us.
 #include "pa_mma.cuh"
 #include "pa_score.cuh"
 
