@@ -162,9 +162,15 @@ def make_dims(num_seqs=0, num_q_heads=1, num_kv_heads=1, head_dim=128, block_siz
 
 
 # ------------------------------------------------------------------ GPU calls
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 _TORCH_DTYPES = {}
@@ -193,6 +199,13 @@ def _expect(t, name, shape, dtype, device):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _expect_beside(t, name, shape, dtype, device):
+    # _expect for a call's further tensors: the first was seen to be on a CUDA device
+    if t.shape == shape and t.dtype == dtype and t.device == device and t.is_contiguous():
+        return
+    _expect(t, name, shape, dtype, device)
+
+
 def _on(device):
     """Make `device` current for one library call: the library keeps its
     per-device state (error word, fixed scratch, tensor-map cache) for the
@@ -204,13 +217,14 @@ def _on(device):
 
 
 def _stream_ptr(stream, device):
+    """The handle of a stream (the current one if None) as a plain int (a c_void_p argument)."""
     if stream is None:
         # the current stream's handle without building a Stream object for it
         raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
         if raw is not None and device.index is not None:
-            return ctypes.c_void_p(raw(device.index))
+            return raw(device.index)
         stream = _torch().cuda.current_stream(device)
-    return ctypes.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
 
 
 class Prepared:
@@ -388,9 +402,10 @@ def pa_rope_freqs(rotary_dim: int, theta: float = 10000.0, scaling="plain", fact
 
 def _expect_tokens(t, name, shape, dtype, device):
     """A [tokens, heads, D] tensor whose tokens' rows are contiguous; returns its token stride."""
-    st = t.stride()
-    if st[1:] == (shape[2], 1) and t.shape == shape and t.dtype == dtype and t.device == device and t.is_cuda:
-        return st[0] if shape[0] > 1 else shape[1] * shape[2]
+    if t.shape == shape and t.dtype == dtype and t.device == device and t.is_cuda:
+        first, middle, last = t.stride()
+        if middle == shape[2] and last == 1:
+            return first if shape[0] > 1 else shape[1] * shape[2]
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.device != device:
@@ -419,12 +434,12 @@ def pa_rope_write_kv(dims: pa_dims, rope: Rope, q, k, v, positions, slot_mapping
     ks = _expect_tokens(k, "k", (T, d.num_kv_heads, d.head_dim), kv, dev)
     vs = _expect_tokens(v, "v", (T, d.num_kv_heads, d.head_dim), kv, dev)
     os_ = _expect_tokens(q_out, "q_out", (T, d.num_q_heads, d.head_dim), kv, dev)
-    _expect(positions, "positions", (T,), t.int32, dev)
-    _expect(slot_mapping, "slot_mapping", (T,), t.int64, dev)
-    _expect(rope.freqs, "rope.freqs", (rope.rotary_dim // 2,), t.float64, dev)
+    _expect_beside(positions, "positions", (T,), t.int32, dev)
+    _expect_beside(slot_mapping, "slot_mapping", (T,), t.int64, dev)
+    _expect_beside(rope.freqs, "rope.freqs", (rope.rotary_dim // 2,), t.float64, dev)
     cache_shape = (d.num_blocks, d.num_kv_heads, d.block_size, d.head_dim)
-    _expect(k_cache, "k_cache", cache_shape, kv, dev)
-    _expect(v_cache, "v_cache", cache_shape, kv, dev)
+    _expect_beside(k_cache, "k_cache", cache_shape, kv, dev)
+    _expect_beside(v_cache, "v_cache", cache_shape, kv, dev)
     rp = pa_rope(rope.rotary_dim, int(rope.interleaved), rope.freqs.data_ptr(), rope.mscale)
     args = (ctypes.byref(dims), ctypes.byref(rp), q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
             positions.data_ptr(), slot_mapping.data_ptr(), T, q_out.data_ptr(), os_, k_cache.data_ptr(),
@@ -456,10 +471,10 @@ def _marshal_score(score, num_q_heads, rows, dev):
         return None, ()
     ptr = lambda x: None if x is None else x.data_ptr()  # noqa: E731
     if score.slopes is not None:
-        _expect(score.slopes, "score.slopes", (num_q_heads,), t.float32, dev)
+        _expect_beside(score.slopes, "score.slopes", (num_q_heads,), t.float32, dev)
     for name in ("key_begin", "key_end"):
         if getattr(score, name) is not None:
-            _expect(getattr(score, name), "score." + name, (rows,), t.int32, dev)
+            _expect_beside(getattr(score, name), "score." + name, (rows,), t.int32, dev)
     sc = pa_score(score.softcap, score.window, ptr(score.slopes), ptr(score.key_begin), ptr(score.key_end))
     return ctypes.byref(sc), (sc, score.slopes, score.key_begin, score.key_end)
 
@@ -474,9 +489,9 @@ def _marshal_sums(key_sums, sum_rows, dims, dev):
     if key_sums.dim() != 3:
         raise ValueError(f"key_sums has shape {tuple(key_sums.shape)}, expected (rows, {dims.num_kv_heads}, cols)")
     R, C = int(key_sums.shape[0]), int(key_sums.shape[2])
-    _expect(key_sums, "key_sums", (R, dims.num_kv_heads, C), t.float32, dev)
+    _expect_beside(key_sums, "key_sums", (R, dims.num_kv_heads, C), t.float32, dev)
     if sum_rows is not None:
-        _expect(sum_rows, "sum_rows", (dims.num_seqs,), t.int32, dev)
+        _expect_beside(sum_rows, "sum_rows", (dims.num_seqs,), t.int32, dev)
     ks = pa_key_sums(key_sums.data_ptr(), None if sum_rows is None else sum_rows.data_ptr(), R, C)
     return ctypes.byref(ks), (ks, key_sums, sum_rows)
 
@@ -499,7 +514,7 @@ def _workspace(workspace, need, what, dev):
         raise ValueError(f"{what} needs a workspace of {need} bytes")
     if not workspace.is_cuda or not workspace.is_contiguous() or workspace.device != dev:
         raise ValueError("workspace must be a contiguous CUDA tensor on the same device")
-    return ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size()
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def pa_decode_scored_workspace_bytes(dims: pa_dims, with_sums: bool = False) -> int:
@@ -517,12 +532,12 @@ def pa_decode_scored(dims: pa_dims, score, q, k_cache, v_cache, block_tables, co
     dev = q.device
     _expect(q, "q", (d.num_seqs, d.num_q_heads, d.head_dim), kv, dev)
     cache_shape = (d.num_blocks, d.num_kv_heads, d.block_size, d.head_dim)
-    _expect(k_cache, "k_cache", cache_shape, kv, dev)
-    _expect(v_cache, "v_cache", cache_shape, kv, dev)
-    _expect(block_tables, "block_tables", (d.num_seqs, d.max_blocks_per_seq), t.int32, dev)
-    _expect(context_lens, "context_lens", (d.num_seqs,), t.int32, dev)
+    _expect_beside(k_cache, "k_cache", cache_shape, kv, dev)
+    _expect_beside(v_cache, "v_cache", cache_shape, kv, dev)
+    _expect_beside(block_tables, "block_tables", (d.num_seqs, d.max_blocks_per_seq), t.int32, dev)
+    _expect_beside(context_lens, "context_lens", (d.num_seqs,), t.int32, dev)
     code = _out_code(out, dims)
-    _expect(out, "out", (d.num_seqs, d.num_q_heads, d.head_dim), out.dtype, dev)
+    _expect_beside(out, "out", (d.num_seqs, d.num_q_heads, d.head_dim), out.dtype, dev)
     sc, keep_score = _marshal_score(score, d.num_q_heads, d.num_seqs, dev)
     ks, keep_sums = _marshal_sums(key_sums, sum_rows, dims, dev)
     need = pa_decode_scored_workspace_bytes(dims, key_sums is not None)
@@ -548,13 +563,13 @@ def pa_chunk_scored(dims: pa_dims, score, q, k_cache, v_cache, block_tables, con
     T = int(q.shape[0])
     _expect(q, "q", (T, d.num_q_heads, d.head_dim), kv, dev)
     cache_shape = (d.num_blocks, d.num_kv_heads, d.block_size, d.head_dim)
-    _expect(k_cache, "k_cache", cache_shape, kv, dev)
-    _expect(v_cache, "v_cache", cache_shape, kv, dev)
-    _expect(block_tables, "block_tables", (d.num_seqs, d.max_blocks_per_seq), t.int32, dev)
-    _expect(context_lens, "context_lens", (d.num_seqs,), t.int32, dev)
-    _expect(query_start, "query_start", (d.num_seqs + 1,), t.int32, dev)
+    _expect_beside(k_cache, "k_cache", cache_shape, kv, dev)
+    _expect_beside(v_cache, "v_cache", cache_shape, kv, dev)
+    _expect_beside(block_tables, "block_tables", (d.num_seqs, d.max_blocks_per_seq), t.int32, dev)
+    _expect_beside(context_lens, "context_lens", (d.num_seqs,), t.int32, dev)
+    _expect_beside(query_start, "query_start", (d.num_seqs + 1,), t.int32, dev)
     code = _out_code(out, dims)
-    _expect(out, "out", (T, d.num_q_heads, d.head_dim), out.dtype, dev)
+    _expect_beside(out, "out", (T, d.num_q_heads, d.head_dim), out.dtype, dev)
     sc, keep_score = _marshal_score(score, d.num_q_heads, T, dev)
     need = pa_chunk_scored_workspace_bytes(dims, T, max_query_len)
     ws_ptr, ws_bytes = _workspace(workspace, need, "pa_chunk_scored", dev)
@@ -581,15 +596,15 @@ def pa_evict(dims: pa_dims, k_cache, v_cache, block_tables, context_lens, new_ta
     dev = k_cache.device
     cache_shape = (d.num_blocks, d.num_kv_heads, d.block_size, d.head_dim)
     _expect(k_cache, "k_cache", cache_shape, kv, dev)
-    _expect(v_cache, "v_cache", cache_shape, kv, dev)
+    _expect_beside(v_cache, "v_cache", cache_shape, kv, dev)
     for name, x in (("block_tables", block_tables), ("new_tables", new_tables)):
-        _expect(x, name, (d.num_seqs, d.max_blocks_per_seq), t.int32, dev)
+        _expect_beside(x, name, (d.num_seqs, d.max_blocks_per_seq), t.int32, dev)
     for name, x in (("context_lens", context_lens), ("keep_lens", keep_lens), ("new_lens", new_lens)):
-        _expect(x, name, (d.num_seqs,), t.int32, dev)
+        _expect_beside(x, name, (d.num_seqs,), t.int32, dev)
     if key_sums is None:
         raise ValueError("pa_evict needs key_sums")
     ks, keep_sums = _marshal_sums(key_sums, sum_rows, dims, dev)
-    _expect(sums_out, "sums_out", tuple(key_sums.shape), t.float32, dev)
+    _expect_beside(sums_out, "sums_out", tuple(key_sums.shape), t.float32, dev)
     ws_ptr, ws_bytes = _workspace(workspace, pa_evict_workspace_bytes(dims), "pa_evict", dev)
     args = (ctypes.byref(dims), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
             context_lens.data_ptr(), new_tables.data_ptr(), keep_lens.data_ptr(), int(recent), ks, sums_out.data_ptr(),
