@@ -359,8 +359,8 @@ PA_API int32_t pa_swap_blocks(const pa_dims *dims, void *k_cache, void *v_cache,
  *                 bytes a multiple of 16), so column ranges of one projection
  *                 output need no copy
  *   q_out         [num_tokens, Hq, D], tokens q_out_stride elements apart; may
- *                 be q itself (same pointer and stride), and must not overlap
- *                 q otherwise
+ *                 be q itself (same pointer and stride), and must not share
+ *                 elements with q otherwise, nor with k or v
  *   positions     int32 [num_tokens], device (any value)
  *   slot_mapping  int64 [num_tokens], device, as for pa_write_kv; a token with
  *                 a negative slot is padding: nothing is written for it, in
@@ -532,8 +532,9 @@ PA_API int32_t pa_chunk_scored(const pa_dims *dims, const pa_score *score, const
  *                 not overlap context_lens or keep_lens
  *   workspace     >= pa_evict_workspace_bytes(dims) bytes, 256-byte aligned
  * num_q_heads of dims is not used; num_seqs * num_kv_heads is at most 65535,
- * num_blocks * num_kv_heads * block_size at most 2^31 - 1 (PA_ERR_INVALID above).  Any block_size and any head_dim whose row
- * is a multiple of 16 bytes.  A row whose source or destination block is
+ * max_blocks_per_seq * block_size at most 2^30, num_blocks * num_kv_heads *
+ * block_size at most 2^31 - 1 (PA_ERR_INVALID above).  Any block_size and any
+ * head_dim whose row is a multiple of 16 bytes.  A row whose source or destination block is
  * outside [0, N) is skipped and flagged (PA_DEVERR_BAD_BLOCK).
  */
 PA_API size_t pa_evict_workspace_bytes(const pa_dims *dims);

@@ -16,6 +16,15 @@ bool overlap(const void *p, size_t n, const void *q, size_t m) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
     return n && m && a < b + m && b < a + n;
 }
+// The same for `rows` rows of `row` bytes, `step` and `other` bytes apart: rows of one step
+// that lie in each other's gaps (column ranges of one tensor) are apart.
+bool rows_overlap(const void *p, int64_t step, const void *q, int64_t other, int64_t rows, int64_t row) {
+    if (!overlap(p, (size_t)((rows - 1) * step + row), q, (size_t)((rows - 1) * other + row))) return false;
+    if (step != other) return true;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    const int64_t gap = (int64_t)((a < b ? b - a : a - b) % (uintptr_t)step);
+    return gap < row || step - gap < row;
+}
 int32_t to_status(cudaError_t e) {
     if (e == cudaSuccess) return PA_OK;
     return e == cudaErrorNotSupported ? PA_ERR_UNSUPPORTED : PA_ERR_CUDA;
@@ -302,9 +311,9 @@ int32_t pa_rope_write_kv(const pa_dims *dims, const pa_rope *rope, const void *q
         !aligned(v_cache, 16) || !aligned(slot_mapping, 8) || !aligned(positions, 4) || !aligned(rope->freqs, 8))
         return PA_ERR_INVALID;
     // q_out is q itself, or apart from it (a token's row is read by other CTAs than the one that writes it)
-    const size_t q_span = (size_t)(((int64_t)(num_tokens - 1) * q_stride + q_row) * es);
-    const size_t o_span = (size_t)(((int64_t)(num_tokens - 1) * q_out_stride + q_row) * es);
-    if (!(q == q_out && q_stride == q_out_stride) && overlap(q, q_span, q_out, o_span)) return PA_ERR_INVALID;
+    if (!(q == q_out && q_stride == q_out_stride) &&
+        rows_overlap(q, q_stride * es, q_out, q_out_stride * es, num_tokens, q_row * es))
+        return PA_ERR_INVALID;
     pa::RopeArgs a{};
     a.q = q;
     a.k = k;
@@ -377,7 +386,7 @@ static int32_t check_evict_dims(const pa_dims *d) {
     const int32_t rc = pa::check_cache(d);
     if (rc != PA_OK) return rc;
     if (d->num_seqs < 0 || d->max_blocks_per_seq <= 0) return PA_ERR_INVALID;
-    if ((int64_t)d->max_blocks_per_seq * d->block_size > INT32_MAX) return PA_ERR_INVALID;
+    if ((int64_t)d->max_blocks_per_seq * d->block_size > 1 << 30) return PA_ERR_INVALID;  // loops step past it in 32 bits
     if ((int64_t)d->num_seqs * d->num_kv_heads > 65535) return PA_ERR_INVALID;  // the copy grid's y extent
     // cache rows (N * Hkv * B) are numbered in 32 bits
     if ((int64_t)d->num_blocks * d->num_kv_heads > INT32_MAX / d->block_size) return PA_ERR_INVALID;

@@ -107,3 +107,28 @@ def test_rope_matches_the_separate_write(gpu):
     pa.pa_rope_write_kv(dims, pa.make_rope(D, freqs), q, k, v, torch.zeros(T, dtype=torch.int32, device="cuda"), slots, out,
                         a[2], a[3])
     assert torch.equal(a[0], a[2]) and torch.equal(a[1], a[3]) and torch.equal(out, q)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rope_output_beside_its_input(gpu, interleaved):
+    # q_out as another column range of the tensor that holds q
+    torch, pa = gpu
+    rng = synth.make_rng(8400)
+    T, Hq, Hkv, D, B, N = 50, 4, 2, 64, 16, 6
+    x = synth.normal(rng, (T, Hq, D), 1.0, "bf16")
+    both = torch.zeros(T, 2 * Hq, D, dtype=torch.bfloat16, device="cuda")
+    both[:, Hq:] = to_dev(torch, x, "bf16")
+    k, v = (to_dev(torch, synth.normal(rng, (T, Hkv, D), 1.0, "bf16"), "bf16") for _ in range(2))
+    kc, vc = (torch.zeros(N, Hkv, B, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    pos = rng.integers(0, 3000, T)
+    freqs = pa.pa_rope_freqs(D)[0]
+    pa.pa_rope_write_kv(pa.make_dims(0, Hq, Hkv, D, B, N, 1, 0, "bf16"),
+                        pa.make_rope(D, torch.from_numpy(freqs).cuda(), interleaved), both[:, Hq:], k, v,
+                        torch.from_numpy(pos.astype(np.int32)).cuda(), torch.arange(T, device="cuda"), both[:, :Hq], kc, vc)
+    check(to_host(both[:, :Hq].contiguous(), "bf16"), x, pos, freqs, D, interleaved, 1.0, "bf16")
+    np.testing.assert_array_equal(to_host(both[:, Hq:].contiguous(), "bf16"), x)
+    with pytest.raises(pa.PaError):
+        pa.pa_rope_write_kv(pa.make_dims(0, Hq, Hkv, D, B, N, 1, 0, "bf16"),
+                            pa.make_rope(D, torch.from_numpy(freqs).cuda(), interleaved), both[:, Hq:], k, v,
+                            torch.from_numpy(pos.astype(np.int32)).cuda(), torch.arange(T, device="cuda"),
+                            both[:, Hq - 1:2 * Hq - 1], kc, vc)

@@ -90,6 +90,8 @@ def test_evict_refusals(pa):
         assert evict(pa, d, ks, **bad) == INV, bad
     assert evict(pa, dims(pa, head_dim=12), ks) == pa.PA_ERR_UNSUPPORTED
     assert evict(pa, dims(pa, num_seqs=40000, num_kv_heads=2), ks) == INV
+    assert evict(pa, dims(pa, max_blocks_per_seq=(1 << 26) + 1), pa.pa_key_sums(P, None, 2, (1 << 30) + 16)) == INV
+    assert pa.pa_evict_workspace_bytes(dims(pa, max_blocks_per_seq=(1 << 26) + 1)) == 0
     assert evict(pa, dims(pa, num_seqs=0), ks) == pa.PA_OK
 
 
@@ -106,7 +108,10 @@ def test_rope_refusals(pa):
     d = dims(pa)
     for bad in (dict(R=0), dict(R=3), dict(R=66), dict(R=-2), dict(mscale=float("nan")), dict(inter=2), dict(qs=511),
                 dict(qs=504), dict(ks=127), dict(vs=0), dict(os=100), dict(qs=513), dict(q=P + 2), dict(freqs=None),
-                dict(freqs=P + 4), dict(T=-1), dict(out=P + 512), dict(out=P, os=520), dict(k=None)):
+                dict(freqs=P + 4), dict(T=-1), dict(out=P + 512), dict(out=P, os=520), dict(k=None),
+                # rows of 1024 bytes, 2048 apart: starts nearer than a row, from either side, a row later too
+                dict(qs=1024, os=1024, out=P + 512), dict(qs=1024, os=1024, out=P + 1536),
+                dict(qs=1024, os=1024, out=P + 2048), dict(qs=1024, os=1024, q=P + 512, out=P)):
         assert rope(pa, d, **bad) == INV, bad
     assert rope(pa, dims(pa, num_q_heads=7)) == INV
     assert rope(pa, dims(pa, num_q_heads=0)) == INV
