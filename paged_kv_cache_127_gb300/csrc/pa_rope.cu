@@ -17,8 +17,8 @@
 // dims whose halves are not whole units take the element kernel.
 //
 // Bound: HBM for a prompt (each q, k, v element read and written once), latency for a step.
-// Measured: 8192 tokens of 32 + 32 heads (D 128, f16, 64 elements rotated as neighbours) 69 us back to back,
-// 62 alone (floor 59); the kernel of a step of 256 tokens, 64 + 8 heads, 5.6 us, of one token 2.9 us.
+// Measured: 8192 tokens of 32 + 32 heads (D 128, f16, 64 elements rotated as neighbours) 64 us (floor 59), of
+// 32 + 8 heads (bf16, whole heads in halves) 51; the kernel of a step of 256 tokens, 64 + 8 heads, 5.6 us, of one token 2.9 us.
 #include <cmath>
 
 #include "pa_device.cuh"
@@ -122,7 +122,7 @@ struct Unit {
 // that rotate together, then pairs of the units behind R.  The heads of q, k and v are numbered
 // through; part y of gridDim.y takes every gridDim.y-th group of them, kU a thread in flight.
 // A thread stays with one column, so its offsets within a head are fixed.
-constexpr int kTokens = 4;
+constexpr int kTokens = 2;
 
 template <typename T, bool kInterleaved>
 __global__ void __launch_bounds__(kRopeThreads) rope_units_kernel(const RopeArgs a, int tokens, int upq) {
@@ -241,8 +241,8 @@ cudaError_t launch_rope_t(const RopeArgs &a, cudaStream_t st) {
     const int upq = a.interleaved ? a.D / V : a.R / 2 / V + ((a.D - a.R) / V + 1) / 2;
     if (!whole || upq > kRopeThreads) return launch_rope(rope_elements_kernel<T>, dim3((unsigned)a.T), 0, st, a);
     // Few tokens: their heads over several CTAs, down to one head a thread, so that a step's loads are
-    // all in flight at once.  Many: four tokens a CTA, whose slots, positions and angles then cost
-    // one chain of loads and one barrier.
+    // all in flight at once.  Many: two tokens a CTA, whose slots, positions and angles then cost one
+    // chain of loads and one barrier (8192 tokens: 64 us; one token a CTA 72, three 65, four 70, eight 85).
     const int tokens = a.T >= 16 * 152 && a.R <= 1024 ? kTokens : 1;
     const int groups = (a.T + tokens - 1) / tokens, per = kRopeThreads / upq;
     const int passes = (a.Hq + 2 * a.Hkv + per - 1) / per;
