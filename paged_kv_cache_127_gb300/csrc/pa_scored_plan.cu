@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(1024) scored_decode_plan_kernel(const ScoredAr
 // partition | block << 16, lo, hi), with the keys [lo, hi) that some row of the
 // block sees; most keys first.  Two passes over the blocks, counting and
 // placing, a thread each.  With key_begin or key_end the blocks' spans come
-// first, a thread per row into shared memory (zeroing empty rows on the way); calls of
+// first, a warp per block into shared memory (zeroing empty rows on the way); calls of
 // more than kSpanCache blocks take a warp per block in both passes instead.  On the mma.sync path
 // the rows whose range lies in several partitions are listed for the merge.
 // plan_hdr[0] = -1 when query_start is not non-decreasing within [0, T].
@@ -140,25 +140,11 @@ __global__ void __launch_bounds__(1024) scored_chunk_plan_kernel(const ScoredArg
     const unsigned all = (unsigned)a.S * (unsigned)blocks;       // bounded by the entry point
     const bool masks = a.key_begin || a.key_end;  // else the ranges follow from the positions, and none is empty
     const bool in_smem = masks && all <= kSpanCache;
-    // the masks of a thread's first kRows rows, read beside the lengths: one trip to memory for both
-    constexpr int kRows = 8;
-    int begin[kRows], end[kRows];
-    auto read_masks = [&](int i0) {
-#pragma unroll
-        for (int e = 0; e < kRows; ++e) {
-            const int i = i0 + 1024 * e + tid;
-            begin[e] = a.key_begin && i < a.T ? a.key_begin[i] : 0;
-            end[e] = a.key_end && i < a.T ? a.key_end[i] : INT_MAX;
-        }
-    };
-    if (in_smem) read_masks(0);
     if (cached) {
         for (int s = tid; s <= a.S; s += blockDim.x) qs_cache[s] = a.query_start[s];
         for (int s = tid; s < a.S; s += blockDim.x) len_cache[s] = a.context_lens[s];
     }
     for (int i = tid; i < kBins; i += blockDim.x) hist[i] = 0;
-    if (in_smem)
-        for (unsigned b = tid; b < all; b += 1024) spans[b] = make_int2(INT_MAX, 0);
     if (tid == 0) {
         a.plan_hdr[1] = 0;
         merges = 0;
@@ -190,34 +176,54 @@ __global__ void __launch_bounds__(1024) scored_chunk_plan_kernel(const ScoredArg
         const int n = qs[s0 + 1] - qs[s0], len = lens[s0], t = i - qs[s0];
         return t < 0 || t >= n || len < 0 || len > cap || n > len || n > a.max_query_len ? -1 : s0;
     };
+    // Block b's sequence, first token, one past its last (none: an empty range), and the sequence's rows and length.
+    struct Block {
+        int t0, t1, q0, before, len;
+    };
+    auto block_at = [&](unsigned b) {
+        const int s = (int)(b / (unsigned)blocks), rb = (int)(b - (unsigned)s * (unsigned)blocks);
+        const int q0 = qs[s], n = qs[s + 1] - q0, len = lens[s];
+        Block k{rb * tokens, min(n, (rb + 1) * tokens), q0, len - n, len};
+        if (len < 0 || len > cap || n > len || n > a.max_query_len) k.t1 = 0;
+        return k;
+    };
     if (in_smem) {
-        for (int i0 = 0; i0 < a.T; i0 += 1024 * kRows) {
-            if (i0 > 0) read_masks(i0);
+        // A warp per block, the masks of kAhead blocks in flight (a thread per row, searching its sequence
+        // and updating its block's span: 12.6 us for 16 x 512 rows, this 8.9).
+        constexpr int kAhead = 4;
+        for (unsigned b0 = tid >> 5; b0 < all; b0 += 32 * kAhead) {
+            int lo[kAhead], hi[kAhead];
 #pragma unroll
-            for (int e = 0; e < kRows; ++e) {
-                if (i0 + 1024 * e >= a.T) break;
-                const int i = i0 + 1024 * e + tid;
-                int lo = INT_MAX, hi = 0, b = -1;
-                const int s = i < a.T ? seq_of(i) : -1;
-                if (s >= 0) {
-                    const int t = i - qs[s], pos = lens[s] - (qs[s + 1] - qs[s]) + t;
-                    const int x = max(max(0, begin[e]), a.window > 0 ? pos - a.window + 1 : 0);
-                    const int y = min(lens[s], a.key_end ? end[e] : pos + 1);
-                    b = s * blocks + t / tokens;
-                    if (x < y) lo = x, hi = y;
-                    else zero_row(a, i);
+            for (int u = 0; u < kAhead; ++u) lo[u] = INT_MAX, hi[u] = 0;
+            for (int e = lane; e < tokens; e += 32) {
+                int begin[kAhead], end[kAhead];
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const Block k = block_at(min(b0 + 32u * u, all - 1));
+                    const bool in = b0 + 32u * u < all && k.t0 + e < k.t1;
+                    begin[u] = in && a.key_begin ? a.key_begin[k.q0 + k.t0 + e] : 0;
+                    end[u] = in && a.key_end ? a.key_end[k.q0 + k.t0 + e] : INT_MAX;
                 }
-                // neighbouring rows mostly share their block: one update a warp then
-                int same;
-                __match_all_sync(0xffffffffu, b, &same);
-                if (same) {
-                    lo = __reduce_min_sync(0xffffffffu, lo);
-                    hi = __reduce_max_sync(0xffffffffu, hi);
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const Block k = block_at(min(b0 + 32u * u, all - 1));
+                    const int t = k.t0 + e, pos = k.before + t;
+                    if (b0 + 32u * u >= all || t >= k.t1) continue;
+                    const int x = max(max(0, begin[u]), a.window > 0 ? pos - a.window + 1 : 0);
+                    const int y = min(k.len, a.key_end ? end[u] : pos + 1);
+                    if (x < y) {
+                        lo[u] = min(lo[u], x);
+                        hi[u] = max(hi[u], y);
+                    } else {
+                        zero_row(a, k.q0 + t);
+                    }
                 }
-                if (b >= 0 && lo < hi && (!same || lane == 0)) {
-                    atomicMin(&spans[b].x, lo);
-                    atomicMax(&spans[b].y, hi);
-                }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int x = __reduce_min_sync(0xffffffffu, lo[u]), y = __reduce_max_sync(0xffffffffu, hi[u]);
+                if (lane == 0 && b0 + 32u * u < all) spans[b0 + 32u * u] = make_int2(x, y);
             }
         }
         __syncthreads();
@@ -228,24 +234,23 @@ __global__ void __launch_bounds__(1024) scored_chunk_plan_kernel(const ScoredArg
     for (int pass = 0; pass < 2; ++pass) {
         for (unsigned b = first; b < all; b += stride) {
             const int s = (int)(b / (unsigned)blocks), rb = (int)(b - (unsigned)s * (unsigned)blocks);
-            const int q0 = qs[s], n = qs[s + 1] - q0, len = lens[s];
-            if (len < 0 || len > cap || n > len || n > a.max_query_len || rb * tokens >= n) continue;
-            const int t0 = rb * tokens, t1 = min(n, t0 + tokens);
+            const Block at = block_at(b);
+            if (at.t0 >= at.t1) continue;
             int2 k;
             if (in_smem) {
                 k = spans[b];
             } else if (!masks) {
-                k.x = a.window > 0 ? max(0, len - n + t0 - a.window + 1) : 0;
-                k.y = len - n + t1;
+                k.x = a.window > 0 ? max(0, at.before + at.t0 - a.window + 1) : 0;
+                k.y = at.before + at.t1;
             } else {
                 int lo = INT_MAX, hi = 0;
-                for (int t = t0 + lane; t < t1; t += 32) {
-                    const int2 r = row_range(a, q0 + t, len - n + t, len);
+                for (int t = at.t0 + lane; t < at.t1; t += 32) {
+                    const int2 r = row_range(a, at.q0 + t, at.before + t, at.len);
                     if (r.x < r.y) {
                         lo = min(lo, r.x);
                         hi = max(hi, r.y);
                     } else if (pass == 0) {
-                        zero_row(a, q0 + t);
+                        zero_row(a, at.q0 + t);
                     }
                 }
                 k.x = __reduce_min_sync(0xffffffffu, lo);
@@ -259,8 +264,8 @@ __global__ void __launch_bounds__(1024) scored_chunk_plan_kernel(const ScoredArg
                 if (pass == 0) {
                     atomicAdd(&hist[bin], 1);
                 } else {
-                    const int at = atomicAdd(&start[bin], 1);
-                    a.plan_list[at] = make_int4(s, a.umma_rows > 0 ? rb : p | rb << 16, lo, hi);
+                    const int place = atomicAdd(&start[bin], 1);
+                    a.plan_list[place] = make_int4(s, a.umma_rows > 0 ? rb : p | rb << 16, lo, hi);
                 }
             }
         }
