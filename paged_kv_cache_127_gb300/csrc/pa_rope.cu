@@ -13,8 +13,9 @@
 //
 // Work: a CTA puts the R / 2 (cos, sin) pairs of its tokens into shared memory once and
 // its threads walk the heads in 16-byte units: a pair of units R / 2 apart, one unit of
-// neighbouring pairs, or units behind R, which are copied, as are the values.  Rotary
-// dims whose halves are not whole units take the element kernel.
+// neighbouring pairs, or units behind R, which are copied, as are the values.  Where half
+// the rotary dim is not whole units (in the half layout), a thread takes one unit and its elements'
+// partners one by one (from L1); heads of more than 256 units go element by element.
 //
 // Bound: HBM for a prompt (each q, k, v element read and written once), latency for a step.
 // Measured: 8192 tokens of 32 + 32 heads (D 128, f16, 64 elements rotated as neighbours) 64 us (floor 59), of
@@ -66,7 +67,7 @@ __device__ __forceinline__ int64_t token_slot(const RopeArgs &a, int t, bool fla
     return slot;
 }
 
-// One CTA per token, an element at a time: any even rotary dim.
+// One CTA per token, an element at a time: any even rotary dim and head.
 template <typename T>
 __global__ void __launch_bounds__(kRopeThreads) rope_elements_kernel(const RopeArgs a) {
     __shared__ float2 cs[kMaxPairs];
@@ -143,8 +144,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_units_kernel(const RopeArgs
     __syncthreads();
     const int i = tid % upq, per = kRopeThreads / upq, h0 = tid / upq;
     if (h0 >= per) return;
-    const int turning = kInterleaved ? a.R / V : half / V;  // columns that rotate
+    const int turning = kInterleaved ? (a.R + V - 1) / V : half / V;  // columns that rotate
     const bool turns = i < turning;
+    const int live = kInterleaved ? min(kAngles, half - i * kAngles) : kAngles;  // pairs of the unit that do
     // elements of the column's unit, and from there to its second one
     const int first = kInterleaved || turns ? i * V : a.R + (i - turning) * V;
     const int behind = (a.D - a.R) / V;                     // units behind R, the first half of them paired with the rest
@@ -187,12 +189,22 @@ __global__ void __launch_bounds__(kRopeThreads) rope_units_kernel(const RopeArgs
 #pragma unroll
                         for (int e = 0; e < kAngles; ++e) {
                             float &p = kInterleaved ? f[2 * e] : f[e], &r = kInterleaved ? f[2 * e + 1] : g[e];
+                            if (kInterleaved && e >= live) continue;
                             const float2 c = w[e];
                             const float pn = p * c.x - r * c.y;
                             r = r * c.x + p * c.y;
                             p = pn;
                         }
-                        x[u] = Unit<T>::pack(f);
+                        const uint4 turned = Unit<T>::pack(f);
+                        if constexpr (kInterleaved) {  // the words of pairs behind R stay as they are
+                            constexpr int kWords = 4 / kAngles;  // of a pair
+                            x[u].x = turned.x;
+                            if (1 / kWords < live) x[u].y = turned.y;
+                            if (2 / kWords < live) x[u].z = turned.z;
+                            if (3 / kWords < live) x[u].w = turned.w;
+                        } else {
+                            x[u] = turned;
+                        }
                         if (!kInterleaved) y[u] = Unit<T>::pack(g);
                     }
                     T *to = n < k_head ? qo + (ptrdiff_t)n * a.D : (n < v_head ? kc : vc) + (ptrdiff_t)n * row;
@@ -200,6 +212,61 @@ __global__ void __launch_bounds__(kRopeThreads) rope_units_kernel(const RopeArgs
                     if (two) *reinterpret_cast<uint4 *>(to + delta) = y[u];
                 }
             }
+        }
+    }
+}
+
+// Halves that are not whole units: a thread takes one unit of a head and its elements' partners
+// R / 2 away one by one.  grid: (tokens, parts of their heads); a CTA takes `per` whole heads at
+// a time, kAhead times, and stores them once all of it has read them (q_out may be q).
+template <typename T>
+__global__ void __launch_bounds__(kRopeThreads) rope_split_kernel(const RopeArgs a, int upq) {
+    constexpr int V = Unit<T>::kN, kAhead = 2;
+    __shared__ float2 cs[kMaxPairs];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int t = blockIdx.x, tid = threadIdx.x, half = a.R / 2;
+    const int64_t slot = token_slot(a, t, tid == 0 && blockIdx.y == 0);
+    if (slot < 0) return;
+    const int pos = a.positions[t];
+    for (int p = tid; p < half; p += kRopeThreads) cs[p] = turn_at(turn_fraction(a.freqs[p]), pos, a.mscale);
+    __syncthreads();
+    const int64_t blk = slot / a.B, off = slot % a.B;
+    const int i = tid % upq, per = kRopeThreads / upq, h0 = tid / upq, d0 = i * V;
+    const int k_head = a.Hq, v_head = a.Hq + a.Hkv, heads = a.Hq + 2 * a.Hkv;
+    const T *q = static_cast<const T *>(a.q) + (size_t)t * a.q_stride;
+    const T *k = static_cast<const T *>(a.k) + (size_t)t * a.k_stride, *v = static_cast<const T *>(a.v) + (size_t)t * a.v_stride;
+    for (int g = blockIdx.y * kAhead * per; g < heads; g += (int)gridDim.y * kAhead * per) {
+        union {
+            uint4 raw;
+            T e[V];
+        } x[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int n = g + u * per + h0;
+            if (h0 >= per || n >= heads) continue;
+            const T *head = n < k_head ? q + (size_t)n * a.D : n < v_head ? k + (size_t)(n - k_head) * a.D : v + (size_t)(n - v_head) * a.D;
+            x[u].raw = *reinterpret_cast<const uint4 *>(head + d0);
+            if (n >= v_head || d0 >= a.R) continue;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const int d = d0 + e;
+                if (d >= a.R) break;
+                const bool low = d < half;
+                const float2 c = cs[low ? d : d - half];
+                const float other = static_cast<float>(head[low ? d + half : d - half]), own = static_cast<float>(x[u].e[e]);
+                x[u].e[e] = narrow<T>(low ? own * c.x - other * c.y : own * c.x + other * c.y);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int n = g + u * per + h0;
+            if (h0 >= per || n >= heads) continue;
+            T *to = n < k_head ? static_cast<T *>(a.q_out) + (size_t)t * a.q_out_stride + (size_t)n * a.D
+                               : (n < v_head ? static_cast<T *>(a.k_cache) : static_cast<T *>(a.v_cache)) +
+                                     (((size_t)blk * a.Hkv + (n < v_head ? n - k_head : n - v_head)) * a.B + off) * a.D;
+            *reinterpret_cast<uint4 *>(to + d0) = x[u].raw;
         }
     }
 }
@@ -237,9 +304,16 @@ cudaError_t launch_units(const RopeArgs &a, int tokens, int upq, dim3 grid, size
 template <typename T>
 cudaError_t launch_rope_t(const RopeArgs &a, cudaStream_t st) {
     constexpr int V = Unit<T>::kN;
-    const bool whole = a.interleaved ? a.R % V == 0 : a.R % (2 * V) == 0;
-    const int upq = a.interleaved ? a.D / V : a.R / 2 / V + ((a.D - a.R) / V + 1) / 2;
-    if (!whole || upq > kRopeThreads) return launch_rope(rope_elements_kernel<T>, dim3((unsigned)a.T), 0, st, a);
+    const bool whole = a.interleaved || a.R % (2 * V) == 0;
+    const int upq = a.interleaved || !whole ? a.D / V : a.R / 2 / V + ((a.D - a.R) / V + 1) / 2;
+    if (upq > kRopeThreads) return launch_rope(rope_elements_kernel<T>, dim3((unsigned)a.T), 0, st, a);
+    if (!whole) {
+        // few tokens: their heads over several CTAs
+        const int per = 2 * (kRopeThreads / upq), passes = (a.Hq + 2 * a.Hkv + per - 1) / per;
+        const int parts = 4 * 152 / a.T;
+        return launch_rope(rope_split_kernel<T>, dim3((unsigned)a.T, (unsigned)(parts < 1 ? 1 : parts < passes ? parts : passes)),
+                           0, st, a, upq);
+    }
     // Few tokens: their heads over several CTAs, down to one head a thread, so that a step's loads are
     // all in flight at once.  Many: two tokens a CTA, whose slots, positions and angles then cost one
     // chain of loads and one barrier (8192 tokens: 64 us; one token a CTA 72, three 65, four 70, eight 85).

@@ -60,7 +60,8 @@ def run(torch, pa, dtype, T, Hq, Hkv, D, B, R, interleaved, pos, slots, N, rng, 
 
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
-@pytest.mark.parametrize("D,R", [(128, 128), (128, 64), (64, 64), (64, 20), (128, 2), (96, 90), (80, 48), (8, 8)])
+@pytest.mark.parametrize("D,R", [(128, 128), (128, 64), (64, 64), (64, 20), (128, 2), (96, 90), (80, 48), (8, 8), (128, 74),
+                                 (256, 30), (72, 72), (64, 62), (2560, 1500)])
 def test_rope_layouts_and_sizes(gpu, dtype, D, R, interleaved):
     torch, pa = gpu
     rng = synth.make_rng(8000 + D + R + interleaved)
@@ -132,3 +133,41 @@ def test_rope_output_beside_its_input(gpu, interleaved):
                             pa.make_rope(D, torch.from_numpy(freqs).cuda(), interleaved), both[:, Hq:], k, v,
                             torch.from_numpy(pos.astype(np.int32)).cuda(), torch.arange(T, device="cuda"),
                             both[:, Hq - 1:2 * Hq - 1], kc, vc)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T,Hq,Hkv,D,R", [(3, 40, 8, 128, 20), (700, 12, 4, 64, 38), (40, 5, 1, 80, 6)])
+def test_rope_in_place_where_pairs_lie_across_units(gpu, dtype, T, Hq, Hkv, D, R, interleaved):
+    # heads in several rounds of a block, tokens in several blocks, the output over its input
+    torch, pa = gpu
+    rng = synth.make_rng(8500 + T + R)
+    N = -(-T // 16) + 1
+    slots = np.where(np.arange(T) % 11 == 5, -1, rng.permutation(N * 16)[:T])
+    run(torch, pa, dtype, T, Hq, Hkv, D, 16, R, interleaved, rng.integers(0, 9999, T), slots, N, rng, True, 0.87, True)
+    assert pa.pa_device_errors(clear=True) == 0
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_rope_copies_the_elements_behind_the_rotary_dim_bit_for_bit(gpu, dtype, interleaved):
+    # NaN of any payload, infinities and zeros of both signs there stay as they are
+    torch, pa = gpu
+    D, B, N, T = 64, 16, 2, 9
+    odd = {"f32": np.uint32([0x7f800001, 0xffc12345, 0x7f800000, 0x80000000]), "f16": np.uint16([0x7c01, 0xfe12, 0xfc00, 0x8000]),
+           "bf16": np.uint16([0x7f81, 0xffc5, 0xff80, 0x8000])}[dtype]
+    raw = torch.from_numpy(np.resize(odd.view(np.int32 if dtype == "f32" else np.int16), (T, 3, D)).copy()).cuda()
+    x = raw.view({"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[dtype])
+    for R in (2, 6, 16, 20, 50, 62):
+        y = x.clone()
+        y[:, :, :R] = 1.0
+        kc, vc = (torch.zeros(N, 1, B, D, dtype=x.dtype, device="cuda") for _ in range(2))
+        out = torch.zeros(T, 1, D, dtype=x.dtype, device="cuda")
+        freqs = torch.from_numpy(pa.pa_rope_freqs(R)[0]).cuda()
+        pa.pa_rope_write_kv(pa.make_dims(0, 1, 1, D, B, N, 1, 0, dtype), pa.make_rope(R, freqs, interleaved), y[:, :1], y[:, 1:2],
+                            y[:, 2:], torch.arange(T, dtype=torch.int32, device="cuda"), torch.arange(T, device="cuda"), out, kc, vc)
+        bits = lambda z: z.contiguous().view(raw.dtype)
+        assert torch.equal(bits(out[:, 0, R:]), raw[:, 0, R:])
+        assert torch.equal(bits(kc.view(-1, D)[:T, R:]), raw[:, 1, R:])
+        assert torch.equal(bits(vc.view(-1, D)[:T]), bits(y[:, 2]))
+    assert pa.pa_device_errors(clear=True) == 0
