@@ -71,6 +71,11 @@ struct ScoredUmmaCfg : UmmaCfg<D, MT> {
     static constexpr bool kRegSplit = MT == 2 && kMode != kMaskOnly;
     static constexpr int kSoftWarp0 = kRegSplit ? 8 : UmmaCfg<D, MT>::kSoftWarp0;
     static constexpr int kThreads = 32 * (kSoftWarp0 + 4 * MT);
+    // boxes loaded of the last kMasks steps, in place of the plain kernel's per ring stage
+    static constexpr int kMasks = 8;
+    static constexpr size_t kMasksOff = UmmaCfg<D, MT>::kItemOff + (size_t)MT * 2 * 64;
+    static constexpr size_t kSmem = UmmaCfg<D, MT>::kSmem + 4 * kMasks;
+    static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
 
 // One work item: KV head kvh of the plan's entry (sequence s, tile group), i.e.
@@ -159,7 +164,12 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
     auto qtile = [&](int x, int u) { return qb + (uint32_t)((x * MT + u) * C::kQTile); };
     auto s_col = [&](int u, int b) { return (uint32_t)(128 * u + C::kN * b); };
     auto o_col = [&](int u) { return C::kOCol + (uint32_t)(D * u); };
-    int *vmask = reinterpret_cast<int *>(basep + C::kMaskOff);
+    // Boxes loaded of step g.  The K producer writes it before the step's K lands, so that a tile that has
+    // seen S knows it; the producer is at most 5 steps ahead of a tile's softmax (3 stages, 2 buffers of S).  So the
+    // softmax waits for V only where it zeroes rows of it (waiting in every step: 334 us against 318
+    // on 16 x 512-token capped chunks).
+    int *masks = reinterpret_cast<int *>(basep + C::kMasksOff);
+    static_assert(C::kStages + C::kSB < C::kMasks || C::kN != 64, "steps in flight");
     uint32_t *tslot = reinterpret_cast<uint32_t *>(basep + C::kSlotOff);
 
     if (threadIdx.x == 0) {
@@ -286,7 +296,7 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
                 }
                 const uint32_t bar = is_v ? v_full(st) : k_full(st);
                 if (lane == 0) {
-                    if (is_v) vmask[st] = mask;  // read by the softmax after v_full (released with v_empty)
+                    if (!is_v) masks[g % C::kMasks] = mask;
                     if (mask == 0) mbar_arrive(bar);
                     else mbar_arrive_expect_tx(bar, (uint32_t)__popc(mask) * C::kSub * 2048u);
                 }
@@ -479,9 +489,7 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
 #pragma unroll
                 for (int q = 0; q < C::kN / 32; ++q) tc::tmem_ld32(tl + s_col(u, b) + 32u * q, sv[q]);
                 tc::tmem_wait_ld();
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(v_full(st), (uint32_t)(g / C::kStages) & 1u, kWaitLimit));
-                if (!ok) break;
-                const int mask = vmask[st];
+                const int mask = masks[g % C::kMasks];
                 const int k0 = k_first + j * C::kN;  // first key of this step
                 const int vb = range.x - k0, ve = range.y - k0;  // this row's keys of the step: vb <= cc < ve
                 float f[C::kN];
@@ -608,7 +616,10 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
                 // anything: tile 0's warpgroup zeroes them (row r < kN of this step's
                 // V, whole 128-byte rows) before it publishes its P and v_zeroed, which
                 // the other tile's P V issuer waits for.
-                if (u == 0 && r < C::kN && (k0 + r < it.lo || k0 + r >= it.hi || !(mask >> (r >> 4) & 1))) {
+                if (u == 0 && (k0 < it.lo || k0 + C::kN > it.hi || mask != (1 << C::kBoxes) - 1)) {
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(v_full(st), (uint32_t)(g / C::kStages) & 1u, kWaitLimit));
+                    if (!ok) break;
+                    if (r < C::kN && (k0 + r < it.lo || k0 + r >= it.hi || !(mask >> (r >> 4) & 1))) {
                     const uint32_t vrow = kvb + (uint32_t)(st * C::kStageBytes + C::kTile + r * 128);
 #pragma unroll
                     for (int sb = 0; sb < C::kSub; ++sb)
@@ -617,7 +628,8 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
                             asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vrow + sb * C::kHalf + cc * 16),
                                          "r"(0u)
                                          : "memory");
-                    tc::fence_async_smem();
+                        tc::fence_async_smem();
+                    }
                 }
                 tc::fence_before_sync();
                 __syncwarp();
