@@ -19,12 +19,13 @@
 // TMA with a map like the queries'.
 //
 // Bound: a step's chain from S through the softmax to P V.  Measured, 16 x 512-token chunks over contexts
-// of up to 4096 (32 / 8 heads, D 128, bf16): ranges only 260 us, bias 333, cap 334 (720 TFLOP/s of the 4 D
-// flops a key and head), both 473; f16, cap 373; the tensor cores' own time would be 127 us, 191 with the
-// low parts' products.  Capped, leaving out the softmax's arithmetic takes 256 us, leaving out the products 308,
-// both 192: the handshakes between the roles are most of what is left.  Ragged
-// prompts with a prefix mask and a bias (D 64, f16) 61 us.  Tried and slower: two threads a row (sixteen
-// softmax warps, 344 us), S and P in columns of their own (341), both against 329 at that time.
+// of up to 4096 (32 / 8 heads, D 128, bf16): ranges only 252 us, bias 313, cap 318 (757 TFLOP/s of the 4 D
+// flops a key and head), both 459; f16, cap 354; the tensor cores' own time would be 127 us, 191 with the
+// low parts' products.  At 345 us capped, leaving out the softmax's arithmetic took 267 us, leaving out the
+// products 318, both 254: the handshakes between the roles are most of it.  Ragged prompts with a prefix
+// mask and a bias (D 64, f16) 57 us.  Tried and slower: two threads a row (sixteen softmax warps, 344 us) and S
+// and P in columns of their own (341), both against 329 at that time; P V of the two tiles issued one whole
+// step after the other: 308 here, but 354 -> 364 for f16 and 296 -> 307 at D 64.
 #pragma once
 
 #include <cuda.h>
@@ -73,8 +74,10 @@ struct ScoredUmmaCfg : UmmaCfg<D, MT> {
     static constexpr int kThreads = 32 * (kSoftWarp0 + 4 * MT);
     // boxes loaded of the last kMasks steps, in place of the plain kernel's per ring stage
     static constexpr int kMasks = 8;
-    static constexpr size_t kMasksOff = UmmaCfg<D, MT>::kItemOff + (size_t)MT * 2 * 64;
-    static constexpr size_t kSmem = UmmaCfg<D, MT>::kSmem + 4 * kMasks;
+    static constexpr size_t kMasksOff = (UmmaCfg<D, MT>::kItemOff + (size_t)MT * 2 * 64 + 7) / 8 * 8;
+    static constexpr size_t kZeroedOff = kMasksOff + 4 * kMasks;  // a barrier per entry
+    static constexpr size_t kSmem = UmmaCfg<D, MT>::kSmem + 8 + (4 + 8) * kMasks;
+    static_assert(kZeroedOff % 8 == 0, "barriers");
     static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
 
@@ -138,8 +141,10 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
     auto k_empty = [&](int i) { return bars + 8u * (uint32_t)(C::kStages + i); };
     auto v_full = [&](int i) { return bars + 8u * (uint32_t)(2 * C::kStages + i); };
     auto v_empty = [&](int i) { return bars + 8u * (uint32_t)(3 * C::kStages + i); };
-    // tile 0's softmax has zeroed this step's V rows that must not contribute
-    auto v_zeroed = [&](int i) { return bars + 8u * (uint32_t)(4 * C::kStages + i); };
+    // Tile 0's softmax has zeroed the V rows of step g that must not contribute.  A ring of kMasks, not of
+    // stages: tile 0 publishes step g once P V of g - 2 is done, so once the other tile's P V of g - 5 has
+    // released its V; with 3 barriers it could complete one twice before that tile has seen it once.
+    auto v_zeroed = [&](int g) { return base + (uint32_t)(C::kZeroedOff + 8 * (g % C::kMasks)); };
     auto tbar = [&](int u, int i) { return bars + 8u * (uint32_t)(5 * C::kStages + u * C::kTileBars + i); };
     constexpr int kSB = C::kSB;
     auto s_full = [&](int u, int b) { return tbar(u, b); };
@@ -178,8 +183,8 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
             mbar_init(k_empty(i), MT);  // one arrival per tile's S issuer (a commit, or a plain
             mbar_init(v_full(i), 1);    // arrival when the item has no rows in that tile)
             mbar_init(v_empty(i), MT);  // likewise from each tile's P V issuer
-            mbar_init(v_zeroed(i), 4);
         }
+        for (int i = 0; i < C::kMasks; ++i) mbar_init(v_zeroed(i), 4);
         for (int u = 0; u < MT; ++u) {
             for (int b = 0; b < kSB; ++b) {
                 mbar_init(s_full(u, b), 1);
@@ -410,7 +415,7 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
                 ok = mbar_wait_bounded(v_full(st), (uint32_t)(g / C::kStages) & 1u, kWaitLimit);
                 // tile 0's softmax zeroes the V rows that must not contribute; tile 0's own
                 // P V is issued after that (its P is published after the zeroing)
-                if (ok && u > 0) ok = mbar_wait_bounded(v_zeroed(st), (uint32_t)(g / C::kStages) & 1u, kWaitLimit);
+                if (ok && u > 0) ok = mbar_wait_bounded(v_zeroed(g), (uint32_t)(g / C::kMasks) & 1u, kWaitLimit);
                 if (ok) ok = mbar_wait_bounded(p_full(u, b), (uint32_t)(c / kSB) & 1u, kWaitLimit);
                 if (!ok) break;
                 tc::fence_after_sync();
@@ -635,7 +640,7 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(p_full(u, b));
-                    if (u == 0) mbar_arrive(v_zeroed(st));
+                    if (u == 0) mbar_arrive(v_zeroed(g));
                 }
             }
             const int last = c - 1;  // this tile's last step of the item
