@@ -73,7 +73,7 @@ struct ScoredUmmaCfg : UmmaCfg<D, MT> {
     static constexpr int kSoftWarp0 = kRegSplit ? 8 : UmmaCfg<D, MT>::kSoftWarp0;
     static constexpr int kThreads = 32 * (kSoftWarp0 + 4 * MT);
     // boxes loaded of the last kMasks steps, in place of the plain kernel's per ring stage
-    static constexpr int kMasks = 8;
+    static constexpr int kMasks = 16;
     static constexpr size_t kMasksOff = (UmmaCfg<D, MT>::kItemOff + (size_t)MT * 2 * 64 + 7) / 8 * 8;
     static constexpr size_t kZeroedOff = kMasksOff + 4 * kMasks;  // a barrier per entry
     static constexpr size_t kSmem = UmmaCfg<D, MT>::kSmem + 8 + (4 + 8) * kMasks;
@@ -170,7 +170,8 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
     auto s_col = [&](int u, int b) { return (uint32_t)(128 * u + C::kN * b); };
     auto o_col = [&](int u) { return C::kOCol + (uint32_t)(D * u); };
     // Boxes loaded of step g.  The K producer writes it before the step's K lands, so that a tile that has
-    // seen S knows it; the producer is at most 5 steps ahead of a tile's softmax (3 stages, 2 buffers of S).  So the
+    // seen S knows it.  It writes step g once S of g - 3 is done, so tile 0's P V of g - 5, whose V came when
+    // both tiles' P V had released that of g - 8: every tile has read what lies 8 steps back.  So the
     // softmax waits for V only where it zeroes rows of it (waiting in every step: 334 us against 318
     // on 16 x 512-token capped chunks).
     int *masks = reinterpret_cast<int *>(basep + C::kMasksOff);
