@@ -682,7 +682,8 @@ PA_API int32_t pa_seq_len(const pa_pool *pool, int32_t seq);
 /*
  * Export device-ready tables for n sequences: tables_out int32[n, max_blocks]
  * (row i = table of seqs[i], padded with `pad`) and lens_out int32[n].
- * PA_ERR_INVALID if a table is longer than max_blocks.
+ * PA_ERR_INVALID if a table is longer than max_blocks.  Ends a batch of
+ * evictions (pa_seq_evict).
  */
 PA_API int32_t pa_pool_export(const pa_pool *pool, const int32_t *seqs, int32_t n, int32_t max_blocks,
                        int32_t pad, int32_t *tables_out, int32_t *lens_out);
@@ -721,9 +722,20 @@ PA_API int32_t pa_seq_swap_in(pa_pool *dev, pa_pool *host, int32_t host_seq, int
  * (pa_pool_export) for pa_evict's block_tables and after it for new_tables, and
  * run pa_evict before any kernel writes to a freed block.  A sequence of at
  * most keep_tokens tokens is left as it is.  *evicted (nullable) is 1 if the
- * table changed, else 0.  All-or-nothing: PA_ERR_OOM if fewer blocks are free
- * than the new table needs (evict a few sequences at a time), nothing changed;
- * PA_ERR_INVALID for keep_tokens < 0, PA_ERR_BAD_INDEX for an unknown id.
+ * table changed, else 0.
+ *
+ * The calls between two pa_pool_export calls form a batch, for one pa_evict
+ * call: none of them takes a block that the batch gave up (an old block of
+ * one of its sequences), since pa_evict copies from it.  Other calls may take
+ * such blocks as any free block.  pa_pool_export ends the batch, so what it
+ * evicted has to go through pa_evict before a pa_seq_evict that follows an
+ * export: export the batch's tables together after the last pa_seq_evict, not
+ * one by one between them.
+ *
+ * All-or-nothing: PA_ERR_OOM if fewer blocks are free, apart from those that
+ * the batch gave up, than the new table needs; nothing changed (run pa_evict for
+ * the batch so far, then go on).  PA_ERR_INVALID for keep_tokens < 0,
+ * PA_ERR_BAD_INDEX for an unknown id.
  */
 PA_API int32_t pa_seq_evict(pa_pool *pool, int32_t seq, int32_t keep_tokens, int32_t *evicted);
 

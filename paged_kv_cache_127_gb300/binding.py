@@ -896,7 +896,8 @@ def pa_seq_len(pool, seq: int) -> int:
 
 def pa_seq_evict(pool, seq: int, keep_tokens: int) -> bool:
     """Give a sequence of more than keep_tokens tokens a fresh table of that length;
-    returns whether the table changed."""
+    returns whether the table changed.  The calls between two pa_pool_export calls are one
+    batch, for one pa_evict: none takes a block that another gave up (PA_ERR_OOM instead)."""
     out = ctypes.c_int32(0)
     _check(lib.pa_seq_evict(pool, int(seq), int(keep_tokens), ctypes.byref(out)), "pa_seq_evict")
     return bool(out.value)

@@ -45,6 +45,7 @@ using pa_pool_detail::release_block;
 int32_t take_block(pa_pool *p) {
     int32_t b = p->free_list.front();
     p->free_list.pop_front();
+    if (p->copied_from[b]) --p->free_sources;
     p->ref[b] = 1;
     if (p->fail_budget > 0) --p->fail_budget;
     return b;
@@ -96,6 +97,7 @@ pa_pool *pa_pool_create(int32_t num_blocks, int32_t block_size, const int32_t *f
     p->B = block_size;
     p->ref.assign(num_blocks, 0);
     p->given_up.assign(num_blocks, 0);
+    p->copied_from.assign(num_blocks, 0);
     if (free_order) {
         std::vector<char> seen(num_blocks, 0);
         for (int32_t i = 0; i < num_blocks; ++i) {
@@ -238,6 +240,9 @@ int32_t pa_pool_export(const pa_pool *pool, const int32_t *seqs, int32_t n, int3
         std::fill(row + k, row + max_blocks, pad);
         lens_out[i] = (int32_t)s.len;
     }
+    for (int32_t b : pool->sources) pool->copied_from[b] = 0;
+    pool->sources.clear();
+    pool->free_sources = 0;
     return PA_OK;
 }
 
@@ -326,16 +331,37 @@ int32_t pa_seq_evict(pa_pool *pool, int32_t seq, int32_t keep_tokens, int32_t *e
     pa_seq_rec &s = pool->seqs[seq];
     if (s.len <= keep_tokens) return PA_OK;
     const int64_t nb = blocks_for(keep_tokens, pool->B);
-    if (nb > available(pool)) return PA_ERR_OOM;
-    // the fresh blocks are taken before the old ones are released, so that none is both
+    if (nb > std::min(available(pool), (int64_t)pool->free_list.size() - pool->free_sources)) return PA_ERR_OOM;
+    // the fresh blocks are taken before the old ones are released, and are no source of an earlier
+    // eviction's copy, so that no block of one pa_evict call is both
     std::vector<int32_t> fresh;
     try {
         fresh.reserve((size_t)nb);
+        pool->sources.reserve(pool->sources.size() + s.table.size());
     } catch (const std::bad_alloc &) {
         return PA_ERR_OOM;
     }
-    for (int64_t j = 0; j < nb; ++j) fresh.push_back(take_block(pool));
-    for (int32_t b : s.table) release_block(pool, b);
+    while ((int64_t)fresh.size() < nb && !pool->copied_from[pool->free_list.front()]) fresh.push_back(take_block(pool));
+    if ((int64_t)fresh.size() < nb) {  // the others from between the sources, which stay in their order
+        size_t kept = 0;
+        for (int32_t b : pool->free_list) {
+            if ((int64_t)fresh.size() < nb && !pool->copied_from[b]) {
+                fresh.push_back(b);
+                pool->ref[b] = 1;
+                if (pool->fail_budget > 0) --pool->fail_budget;
+            } else {
+                pool->free_list[kept++] = b;
+            }
+        }
+        pool->free_list.resize(kept);
+    }
+    for (int32_t b : s.table) {
+        if (!pool->copied_from[b]) {
+            pool->copied_from[b] = 1;
+            pool->sources.push_back(b);
+        }
+        release_block(pool, b);
+    }
     s.table.swap(fresh);
     s.len = keep_tokens;
     if (evicted) *evicted = 1;

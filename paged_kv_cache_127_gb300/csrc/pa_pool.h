@@ -28,6 +28,11 @@ struct pa_pool {
     uint32_t batch_epoch = 0;
     std::vector<int32_t> given_up;   // per block: copies made earlier in the batch (zero outside a call)
     std::vector<int32_t> touched;    // blocks whose given_up count is nonzero
+    // Blocks that pa_seq_evict gave up since the last pa_pool_export: a pa_evict call that copies from
+    // them may not have been issued yet, so pa_seq_evict takes none of them, free or not.
+    mutable std::vector<uint8_t> copied_from;  // per block
+    mutable std::vector<int32_t> sources;      // the marked ones
+    mutable int32_t free_sources = 0;          // marked ones in the free list
 };
 
 
@@ -41,7 +46,10 @@ inline int64_t available(const pa_pool *p) {
 
 // Drop one reference; a block reaching zero goes to the back of the free list.
 inline void release_block(pa_pool *p, int32_t b) {
-    if (--p->ref[b] == 0) p->free_list.push_back(b);
+    if (--p->ref[b] == 0) {
+        p->free_list.push_back(b);
+        if (p->copied_from[b]) ++p->free_sources;
+    }
 }
 
 }  // namespace pa_pool_detail

@@ -230,3 +230,85 @@ def test_seq_evict_random_stream_keeps_the_counts(pa):
                     uses[b] += 1
             assert [pa.pa_block_refcount(h, b) for b in range(200)] == uses.tolist()
             assert pa.pa_pool_num_free(h) == int((uses == 0).sum())
+
+
+def test_seq_evict_batch_takes_no_block_that_the_batch_gave_up(pa):
+    """Two evictions for one pa_evict call: the first one's old blocks are still to be copied from."""
+    with pa.Pool(12, 16) as pool:
+        h = pool.handle
+        a, b = pa.pa_seq_create(h), pa.pa_seq_create(h)
+        for s in (a, b):
+            pa.pa_seq_append(h, s, 64)                   # blocks 0..3 and 4..7
+        pa.pa_pool_export(h, [a, b], 4)
+        assert pa.pa_seq_evict(h, a, 40)                 # 8, 9, 10; one block left that no eviction gave up
+        assert pa.pa_seq_table(h, a).tolist() == [8, 9, 10] and pa.pa_pool_num_free(h) == 5
+        with pytest.raises(pa.PaError) as e:
+            pa.pa_seq_evict(h, b, 40)
+        assert e.value.status == pa.PA_ERR_OOM
+        assert pa.pa_seq_table(h, b).tolist() == [4, 5, 6, 7] and pa.pa_seq_len(h, b) == 64
+        assert [pa.pa_block_refcount(h, i) for i in range(12)] == [0] * 4 + [1] * 7 + [0]
+        assert pa.pa_seq_evict(h, b, 16)                 # what fits beside them is done
+        assert pa.pa_seq_table(h, b).tolist() == [11]
+        # the tables for pa_evict are out: the next batch may take the blocks that this one gave up
+        pa.pa_pool_export(h, [a, b], 4)
+        assert pa.pa_seq_evict(h, a, 33) and pa.pa_seq_table(h, a).tolist() == [0, 1, 2]
+
+
+def test_seq_evict_batch_takes_given_up_blocks_neither_freed_nor_reused(pa):
+    """A block given up in the batch stays out of it when a fork, an append or a free puts it through other hands first."""
+    with pa.Pool(10, 16) as pool:
+        h = pool.handle
+        a = pa.pa_seq_create(h)
+        pa.pa_seq_append(h, a, 48)                       # 0, 1, 2
+        f = pa.pa_seq_fork(h, a)
+        b = pa.pa_seq_create(h)
+        pa.pa_seq_append(h, b, 64)                       # 3, 4, 5, 6
+        assert pa.pa_seq_evict(h, a, 16)                 # 7; its old blocks live on in the fork
+        pa.pa_seq_free(h, f)                             # 0, 1, 2 free now
+        assert pa.pa_seq_evict(h, b, 32) and pa.pa_seq_table(h, b).tolist() == [8, 9]
+        c = pa.pa_seq_create(h)
+        pa.pa_seq_append(h, c, 32)                       # another call may take them: 0, 1
+        assert pa.pa_seq_table(h, c).tolist() == [0, 1]
+        pa.pa_seq_free(h, c)                             # free again, still to be copied from
+        for keep in (16, 1):
+            with pytest.raises(pa.PaError) as e:
+                pa.pa_seq_evict(h, b, keep)
+            assert e.value.status == pa.PA_ERR_OOM
+        assert pa.pa_pool_num_free(h) == 7
+
+
+def test_seq_evict_batches_stay_apart_in_a_random_stream(pa):
+    rng = synth.make_rng(78)
+    with pa.Pool(90, 16) as pool:
+        h, live, given, refused = pool.handle, [], set(), 0
+        for _ in range(3000):
+            op = rng.integers(0, 9)
+            try:
+                if op == 0 or not live:
+                    live.append(pa.pa_seq_create(h))
+                elif op <= 2:
+                    pa.pa_seq_append(h, live[rng.integers(len(live))], int(rng.integers(1, 200)))
+                elif op == 3:
+                    live.append(pa.pa_seq_fork(h, live[rng.integers(len(live))]))
+                elif op <= 6:
+                    s = live[rng.integers(len(live))]
+                    keep, old = int(rng.integers(0, 150)), pa.pa_seq_table(h, s).tolist()
+                    need, free = -(-keep // 16), {b for b in range(90) if pa.pa_block_refcount(h, b) == 0}
+                    if pa.pa_seq_len(h, s) > keep:
+                        try:
+                            assert pa.pa_seq_evict(h, s, keep)
+                        except pa.PaError:
+                            assert need > len(free - given) and pa.pa_seq_table(h, s).tolist() == old
+                            refused += need <= len(free)
+                            continue
+                        assert need <= len(free - given)
+                        given |= set(old)
+                        assert not given & set(pa.pa_seq_table(h, s).tolist())
+                elif op == 7:
+                    pa.pa_seq_free(h, live.pop(rng.integers(len(live))))
+                else:
+                    pa.pa_pool_export(h, live, 200)
+                    given = set()
+            except pa.PaError as e:
+                assert e.status == pa.PA_ERR_OOM
+        assert refused  # some for want of blocks that no eviction gave up
