@@ -67,9 +67,11 @@ __device__ __forceinline__ RowOf row_of(const ScoredArgs &a, int i, int cap) {
 // tanh(y) = y P(y^2) / Q(y^2), both of degree 4, on |y| <= 9, past which tanh
 // rounds to 1 in fp32: a least-squares fit of the relative error, reweighted
 // towards its maximum until level (2.1e-8), with fp32 coefficients.  Evaluated in fp32 with
-// the approximate reciprocal it is within 2^-21 of tanh, relative (rms 2^-24).
+// the approximate reciprocal it is within 2^-21 of tanh, relative (rms 2^-24).  NaN stays NaN: fminf and
+// fmaxf would return the bound, and a NaN score would pass for one at the cap.
 __device__ __forceinline__ float rational_tanh(float y) {
-    y = fminf(fmaxf(y, -9.f), 9.f);
+    asm("max.NaN.f32 %0, %0, 0fC1100000;" : "+f"(y));  // -9
+    asm("min.NaN.f32 %0, %0, 0f41100000;" : "+f"(y));  // 9
     const float z = y * y;
     float p = fmaf(z, 1.3354597427905901e-08f, 2.060904989775736e-05f);
     p = fmaf(p, z, 0.0034955868031829596f);
