@@ -12,7 +12,7 @@
 // What differs: an item holds the keys [lo, hi) of its partition that some of its
 // rows see and streams from the chunk of lo; each row masks to its own range; a
 // warp skips chunks that none of its rows sees; cap and bias are applied to the
-// logits; V rows outside [lo, hi) are zeroed in the B fragments.
+// logits; V rows that no row of a warp sees are zeroed in its B fragments.
 //
 // Finish: a row whose range lies in one partition writes out[]; otherwise its
 // partitions store (m, l, acc) and the merge combines those the range touches.
@@ -30,6 +30,22 @@
 #include "pa_score.cuh"
 
 namespace pa {
+
+// Zeroes the V rows of a 16-key chunk whose bit of `any` is not set, in a lane's B fragments (words 0 and 2 hold
+// keys c2, c2 + 1; 1 and 3 keys c2 + 8, c2 + 9): a weight of 0 does not keep out what may be NaN.
+template <int N>
+__device__ __forceinline__ void keep_seen(uint32_t (&bv)[N][4], uint32_t any, int c2) {
+    const uint32_t lo = any >> c2, hi = any >> (c2 + 8);
+    const uint32_t mlo = (lo & 1u ? 0x0000ffffu : 0u) | (lo & 2u ? 0xffff0000u : 0u);
+    const uint32_t mhi = (hi & 1u ? 0x0000ffffu : 0u) | (hi & 2u ? 0xffff0000u : 0u);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        bv[i][0] &= mlo;
+        bv[i][1] &= mhi;
+        bv[i][2] &= mlo;
+        bv[i][3] &= mhi;
+    }
+}
 
 template <typename T, int D, int HG, int RW>
 __global__ void __launch_bounds__(ChunkCfg<D, HG, RW>::kThreads, ChunkCfg<D, HG, RW>::kMinBlocks)
@@ -274,7 +290,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, HG, RW>::kThreads, ChunkCfg<D, HG,
             const int n1 = ctb[(kb >> lb) - blk0] < 0 ? 0 : min(16, hi - kb);
             // two full chunks that some row of this warp sees: one softmax step over 32 keys
             const bool pair = C::kRegSplit && j + 1 < nchunk && n0 == 0 && n1 == 16 && ctb[((kb + 16) >> lb) - blk0] >= 0 &&
-                              hi - kb >= 32 && kb + 16 < wend && kb + 16 > wbegin;
+                              hi - kb >= 32 && kb >= win0 && kb + 32 <= win1;
             if (pair) {
                 const int st2 = (cons + 1) % C::kStages;
                 const uint32_t parity2 = (uint32_t)((cons + 1) / C::kStages) & 1u;
@@ -326,16 +342,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, HG, RW>::kThreads, ChunkCfg<D, HG,
                     f[i] = sc[c][nt][0][e] + sc[c][nt][1][e];
                     f[8 + i] = sc[c][nt][0][2 + e] + sc[c][nt][1][2 + e];
                 }
-                const bool partial = kb < win0 || kb + 32 > win1;  // some row does not see all of them
-                if (partial && score.cap) {
-                    // which form of the cap a warp takes must not depend on what masked keys hold
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int key = kb + 16 * (i >> 2) + 8 * (i >> 1 & 1) + c2 + (i & 1);
-                        if (key < k0.x || key >= k0.y) f[i] = 0.f;
-                        if (key < k1.x || key >= k1.y) f[8 + i] = 0.f;
-                    }
-                }
                 to_log2(f);
                 float x0[8], x1[8];
 #pragma unroll
@@ -349,14 +355,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, HG, RW>::kThreads, ChunkCfg<D, HG,
                         const int key = kb + 16 * (i >> 2) + 8 * (i >> 1 & 1) + c2 + (i & 1);
                         x0[i] -= s0 * fabsf((float)(pos0 - key));
                         x1[i] -= s1 * fabsf((float)(pos1 - key));
-                    }
-                }
-                if (partial) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int key = kb + 16 * (i >> 2) + 8 * (i >> 1 & 1) + c2 + (i & 1);
-                        if (key < k0.x || key >= k0.y) x0[i] = -INFINITY;
-                        if (key < k1.x || key >= k1.y) x1[i] = -INFINITY;
                     }
                 }
                 float mx0 = x0[0], mx1 = x1[0];
@@ -483,6 +481,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, HG, RW>::kThreads, ChunkCfg<D, HG,
                     f[4 + i] = sc[nt][0][2 + e] + sc[nt][1][2 + e];
                 }
                 bool in0[4], in1[4];
+                uint32_t any = 0u;  // the keys that some row of this warp sees
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int key = kb + 8 * (i >> 1) + c2 + (i & 1);
@@ -490,7 +489,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, HG, RW>::kThreads, ChunkCfg<D, HG,
                     in1[i] = key < kb + n1 && key >= k1.x && key < k1.y;
                     if (!in0[i]) f[i] = 0.f;  // as above
                     if (!in1[i]) f[4 + i] = 0.f;
+                    if (in0[i] || in1[i]) any |= 1u << (key - kb);
                 }
+                // (with no partial rows every row that sees any key sees all of these)
+                any = kb < win0 || kb + 16 > win1 ? __reduce_or_sync(0xffffffffu, any) : 0xffffu;
                 to_log2(f);
                 float x0[4], x1[4];
 #pragma unroll
@@ -541,36 +543,22 @@ __global__ void __launch_bounds__(ChunkCfg<D, HG, RW>::kThreads, ChunkCfg<D, HG,
                 const uint32_t l1a = M::pack(p1[0] - f1a.x, p1[1] - f1a.y);
                 const uint32_t l0b = M::pack(p0[2] - f0b.x, p0[3] - f0b.y);
                 const uint32_t l1b = M::pack(p1[2] - f1b.x, p1[3] - f1b.y);
-                // V rows outside the item's span: zero their halves of the B fragments (b0 / b2
-                // hold keys c2, c2+1; b1 / b3 keys 8+c2, 9+c2)
-                uint32_t mlo = 0xffffffffu, mhi = 0xffffffffu;
-                if (n0 > 0 || n1 < 16) {
-                    auto in = [&](int k) { return k >= n0 && k < n1; };
-                    mlo = (in(c2) ? 0x0000ffffu : 0u) | (in(c2 + 1) ? 0xffff0000u : 0u);
-                    mhi = (in(c2 + 8) ? 0x0000ffffu : 0u) | (in(c2 + 9) ? 0xffff0000u : 0u);
-                }
+                if (any != 0xffffu) keep_seen<C::kNT / 2>(bv, any, c2);
                 // ---- O += P_hi V + P_lo V, two 16-column groups at a time so that the
                 // two MMAs into one accumulator are four issues apart
 #pragma unroll
                 for (int ntq = 0; ntq < C::kNT / 4; ++ntq) {
-                    uint32_t b[2][4];
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         const int ntp = 2 * ntq + u;
-                        b[u][0] = bv[ntp][0] & mlo;
-                        b[u][1] = bv[ntp][1] & mhi;
-                        b[u][2] = bv[ntp][2] & mlo;
-                        b[u][3] = bv[ntp][3] & mhi;
+                        M::mma(o[4 * ntq + 2 * u], h0a, h1a, h0b, h1b, bv[ntp][0], bv[ntp][1]);
+                        M::mma(o[4 * ntq + 2 * u + 1], h0a, h1a, h0b, h1b, bv[ntp][2], bv[ntp][3]);
                     }
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        M::mma(o[4 * ntq + 2 * u], h0a, h1a, h0b, h1b, b[u][0], b[u][1]);
-                        M::mma(o[4 * ntq + 2 * u + 1], h0a, h1a, h0b, h1b, b[u][2], b[u][3]);
-                    }
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        M::mma(o[4 * ntq + 2 * u], l0a, l1a, l0b, l1b, b[u][0], b[u][1]);
-                        M::mma(o[4 * ntq + 2 * u + 1], l0a, l1a, l0b, l1b, b[u][2], b[u][3]);
+                        const int ntp = 2 * ntq + u;
+                        M::mma(o[4 * ntq + 2 * u], l0a, l1a, l0b, l1b, bv[ntp][0], bv[ntp][1]);
+                        M::mma(o[4 * ntq + 2 * u + 1], l0a, l1a, l0b, l1b, bv[ntp][2], bv[ntp][3]);
                     }
                 }
             }

@@ -14,7 +14,8 @@
 // rows sees to the last, so a document or a window costs only its own steps; 16-row
 // boxes outside that span are not loaded; each row masks to its own range (steps
 // that every row of a warp sees whole skip the test); cap and bias are
-// applied to the logits in registers; V rows outside the item's span are zeroed;
+// applied to the logits in registers; V rows that no row of the item sees are zeroed (by the softmax outside
+// the item's span, by the P V issuers in holes between the rows' ranges, for the items that the plan marks);
 // the output may be 16-bit, staged in the query tile's own layout and stored by
 // TMA with a map like the queries'.
 //
@@ -55,6 +56,9 @@ inline ScoredMode scored_mode(const ScoredArgs &a, bool bf16) {
     return kMaskOnly;
 }
 
+// Bits 0 .. x - 1 of a word (none for x <= 0, all from 32 on).
+__device__ __forceinline__ uint32_t bits_below(int x) { return x >= 32 ? ~0u : (1u << max(x, 0)) - 1u; }
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -83,7 +87,8 @@ struct ScoredUmmaCfg : UmmaCfg<D, MT> {
 
 // One work item: KV head kvh of the plan's entry (sequence s, tile group), i.e.
 // rows r0 .. r0 + 128 MT - 1 of that head's (query token, query head) rows, and
-// the keys [lo, hi) that some of those rows see, in nch steps from j0 on.
+// the keys [lo, hi) from the first to the last that some of those rows see, in nch steps.
+// s carries kHoles too: whether there may be keys among them that no row sees.
 struct ScoredItem {
     int s, kvh, r0, qs, n, len, tiles, nch, lo, hi;
 };
@@ -101,12 +106,13 @@ __device__ __forceinline__ bool scored_item(const ScoredArgs &a, int w, int nwor
     if (w >= nwork) return false;
     const int4 e = a.plan_list[w / a.Hkv];  // (sequence, tile group, first key, one past the last)
     const int G = a.Hq / a.Hkv;
+    const int s = e.x & ~kHoles;
     it.s = e.x;
     it.kvh = w % a.Hkv;
     it.r0 = e.y * C::kM * C::kMT;
-    it.qs = a.query_start[it.s];
-    it.n = a.query_start[it.s + 1] - it.qs;
-    it.len = a.context_lens[it.s];
+    it.qs = a.query_start[s];
+    it.n = a.query_start[s + 1] - it.qs;
+    it.len = a.context_lens[s];
     it.tiles = min(C::kMT, (it.n * G - it.r0 + C::kM - 1) / C::kM);  // tiles with at least one row
     it.lo = e.z;
     it.hi = e.w;
@@ -175,6 +181,13 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
     // softmax waits for V only where it zeroes rows of it (waiting in every step: 334 us against 318
     // on 16 x 512-token capped chunks).
     int *masks = reinterpret_cast<int *>(basep + C::kMasksOff);
+    auto zero_v_row = [&](uint32_t row) {  // both halves of a row of a step's V
+#pragma unroll
+        for (int sb = 0; sb < C::kSub; ++sb)
+#pragma unroll
+            for (int cc = 0; cc < 8; ++cc)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(row + sb * C::kHalf + cc * 16), "r"(0u) : "memory");
+    };
     static_assert(C::kStages + C::kSB < C::kMasks || C::kN != 64, "steps in flight");
     uint32_t *tslot = reinterpret_cast<uint32_t *>(basep + C::kSlotOff);
 
@@ -280,7 +293,7 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
             // One lane per copy: box bx of 16 keys, 64 of their columns; its block id is read a step
             // ahead.  (One lane reading the four ids and issuing the eight copies in turn held the steps up:
             // 345 us against 329 on 16 x 512-token capped chunks, 280 against 263 with ranges only.)
-            const int32_t *row = a.block_tables + (size_t)it.s * a.max_blocks;
+            const int32_t *row = a.block_tables + (size_t)(it.s & ~kHoles) * a.max_blocks;
             const int j0 = it.lo / C::kN, lb = __ffs(a.B) - 1;  // B is a power of two
             auto wanted = [&](int j) {
                 const int tok = j * C::kN + 16 * bx;
@@ -414,6 +427,27 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
                 const int b = c % kSB;
                 const int st = g % C::kStages;
                 ok = mbar_wait_bounded(v_full(st), (uint32_t)(g / C::kStages) & 1u, kWaitLimit);
+                if (__builtin_expect((it.s & kHoles) != 0 && ok, 0)) {
+                    // V rows between the rows' ranges hold anything, and a weight of 0 does not keep NaN out: the keys
+                    // that no token of the item (of either tile) sees are zeroed, by each tile's issuer for itself (the same
+                    // zeros). Ranges are read again and the item from its slot, the tile's until its softmax is done,
+                    // so that the other items' steps keep none of it in registers.
+                    const ScoredItem &of = slot(u, (ku - 1) & 1).it;
+                    const int k0 = (of.lo / C::kN + j) * C::kN;
+                    uint32_t any[C::kN / 32] = {};
+                    for (int t = of.r0 / G + lane; t < min(of.n, (of.r0 + C::kM * MT) / G); t += 32) {
+                        const int2 k = row_range(a, of.qs + t, of.len - of.n + t, of.len);
+#pragma unroll
+                        for (int w = 0; w < C::kN / 32; ++w)
+                            any[w] |= bits_below(k.y - k0 - 32 * w) & ~bits_below(k.x - k0 - 32 * w);
+                    }
+#pragma unroll
+                    for (int w = 0; w < C::kN / 32; ++w)
+                        if (!(__reduce_or_sync(0xffffffffu, any[w]) >> lane & 1u))
+                            zero_v_row(kvb + (uint32_t)(st * C::kStageBytes + C::kTile + (32 * w + lane) * 128));
+                    tc::fence_async_smem();
+                    __syncwarp();
+                }
                 // tile 0's softmax zeroes the V rows that must not contribute; tile 0's own
                 // P V is issued after that (its P is published after the zeroing)
                 if (ok && u > 0) ok = mbar_wait_bounded(v_zeroed(g), (uint32_t)(g / C::kMasks) & 1u, kWaitLimit);
@@ -506,8 +540,7 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
                 uint32_t see[C::kN / 32];
 #pragma unroll
                 for (int w = 0; w < C::kN / 32; ++w) {
-                    auto below = [&](int x) { return x >= 32 ? ~0u : (1u << max(x, 0)) - 1u; };
-                    see[w] = below(ve - 32 * w) & ~below(vb - 32 * w) &
+                    see[w] = bits_below(ve - 32 * w) & ~bits_below(vb - 32 * w) &
                              ((mask >> (2 * w) & 1 ? 0xffffu : 0u) | (mask >> (2 * w + 1) & 1 ? 0xffff0000u : 0u));
                 }
                 auto seen = [&](int cc) { return (see[cc >> 5] >> (cc & 31) & 1u) != 0u; };
@@ -626,14 +659,7 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
                     ok = __all_sync(0xffffffffu, mbar_wait_bounded(v_full(st), (uint32_t)(g / C::kStages) & 1u, kWaitLimit));
                     if (!ok) break;
                     if (r < C::kN && (k0 + r < it.lo || k0 + r >= it.hi || !(mask >> (r >> 4) & 1))) {
-                    const uint32_t vrow = kvb + (uint32_t)(st * C::kStageBytes + C::kTile + r * 128);
-#pragma unroll
-                    for (int sb = 0; sb < C::kSub; ++sb)
-#pragma unroll
-                        for (int cc = 0; cc < 8; ++cc)
-                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vrow + sb * C::kHalf + cc * 16),
-                                         "r"(0u)
-                                         : "memory");
+                        zero_v_row(kvb + (uint32_t)(st * C::kStageBytes + C::kTile + r * 128));
                         tc::fence_async_smem();
                     }
                 }

@@ -63,6 +63,9 @@ struct ScoredArgs {
 
 // Mark of a work item that holds its sequence's whole range (in the partition's int).
 constexpr int kWholeRange = 1 << 30;
+// Mark of a tcgen05 chunk item whose rows' ranges may leave keys between them that no row sees (in the
+// sequence's int).
+constexpr int kHoles = 1 << 30;
 
 // Tensor-core decode (f16 / bf16): the work list, the persistent kernel, and the
 // CTAs it launches on the current device (SMs x resident CTAs per SM).

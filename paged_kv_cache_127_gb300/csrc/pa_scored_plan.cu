@@ -115,9 +115,37 @@ __global__ void __launch_bounds__(1024) scored_decode_plan_kernel(const ScoredAr
 // first, a warp per block into shared memory (zeroing empty rows on the way); calls of
 // more than kSpanCache blocks take a warp per block in both passes instead.  On the mma.sync path
 // the rows whose range lies in several partitions are listed for the merge.
+// An entry of the tcgen05 path is marked (kHoles) unless one of its rows sees all of [lo, hi), or each row's range
+// meets that of the last one before it that sees anything: then its rows together see every key of [lo, hi).
 // plan_hdr[0] = -1 when query_start is not non-decreasing within [0, T].
 constexpr int kSeqCache = 2048;
 constexpr int kSpanCache = 2048;
+
+// A row block: its first token and one past its last (none: an empty range) of the sequence's chunk, and the
+// sequence's first row, tokens before the chunk and length.
+struct ChunkBlock {
+    int t0, t1, q0, before, len;
+};
+
+// Whether the range of some token of a block does not meet that of the last one before it that sees
+// anything.  Whole warp.  (Out of line: inlined it takes the registers of the masks in flight, 10.1 -> 10.9 us for
+// 16 x 512 rows.)
+__device__ __noinline__ bool ranges_apart(const ScoredArgs &a, ChunkBlock k0, int lane) {
+    int2 last = make_int2(0, 0);
+    bool apart = false;
+    for (int b = k0.t0; b < k0.t1; b += 32) {
+        const int t = b + lane;
+        const int2 k = t < k0.t1 ? row_range(a, k0.q0 + t, k0.before + t, k0.len) : make_int2(0, 0);
+        const unsigned live = __ballot_sync(0xffffffffu, k.x < k.y);
+        const int from = 31 - __clz(live & ((1u << lane) - 1u)), top = 31 - __clz(live);
+        const int x = __shfl_sync(0xffffffffu, k.x, from & 31), y = __shfl_sync(0xffffffffu, k.y, from & 31);
+        const int2 prev = from >= 0 ? make_int2(x, y) : last;
+        apart |= k.x < k.y && prev.x < prev.y && max(k.x, prev.x) > min(k.y, prev.y);
+        const int2 end = make_int2(__shfl_sync(0xffffffffu, k.x, top & 31), __shfl_sync(0xffffffffu, k.y, top & 31));
+        if (live) last = end;
+    }
+    return __any_sync(0xffffffffu, apart);
+}
 
 __global__ void __launch_bounds__(1024) scored_chunk_plan_kernel(const ScoredArgs a) {
     __shared__ int hist[kBins];
@@ -176,14 +204,11 @@ __global__ void __launch_bounds__(1024) scored_chunk_plan_kernel(const ScoredArg
         const int n = qs[s0 + 1] - qs[s0], len = lens[s0], t = i - qs[s0];
         return t < 0 || t >= n || len < 0 || len > cap || n > len || n > a.max_query_len ? -1 : s0;
     };
-    // Block b's sequence, first token, one past its last (none: an empty range), and the sequence's rows and length.
-    struct Block {
-        int t0, t1, q0, before, len;
-    };
+    // Block b of the call.
     auto block_at = [&](unsigned b) {
         const int s = (int)(b / (unsigned)blocks), rb = (int)(b - (unsigned)s * (unsigned)blocks);
         const int q0 = qs[s], n = qs[s + 1] - q0, len = lens[s];
-        Block k{rb * tokens, min(n, (rb + 1) * tokens), q0, len - n, len};
+        ChunkBlock k{rb * tokens, min(n, (rb + 1) * tokens), q0, len - n, len};
         if (len < 0 || len > cap || n > len || n > a.max_query_len) k.t1 = 0;
         return k;
     };
@@ -193,25 +218,28 @@ __global__ void __launch_bounds__(1024) scored_chunk_plan_kernel(const ScoredArg
         constexpr int kAhead = 4;
         for (unsigned b0 = tid >> 5; b0 < all; b0 += 32 * kAhead) {
             int lo[kAhead], hi[kAhead];
+            unsigned covers = 0u;  // bit u: one of the lane's rows sees all of lo[u] .. hi[u]
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) lo[u] = INT_MAX, hi[u] = 0;
             for (int e = lane; e < tokens; e += 32) {
                 int begin[kAhead], end[kAhead];
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) {
-                    const Block k = block_at(min(b0 + 32u * u, all - 1));
+                    const ChunkBlock k = block_at(min(b0 + 32u * u, all - 1));
                     const bool in = b0 + 32u * u < all && k.t0 + e < k.t1;
                     begin[u] = in && a.key_begin ? a.key_begin[k.q0 + k.t0 + e] : 0;
                     end[u] = in && a.key_end ? a.key_end[k.q0 + k.t0 + e] : INT_MAX;
                 }
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) {
-                    const Block k = block_at(min(b0 + 32u * u, all - 1));
+                    const ChunkBlock k = block_at(min(b0 + 32u * u, all - 1));
                     const int t = k.t0 + e, pos = k.before + t;
                     if (b0 + 32u * u >= all || t >= k.t1) continue;
                     const int x = max(max(0, begin[u]), a.window > 0 ? pos - a.window + 1 : 0);
                     const int y = min(k.len, a.key_end ? end[u] : pos + 1);
                     if (x < y) {
+                        if (x <= lo[u] && y >= hi[u]) covers |= 1u << u;
+                        else if (x < lo[u] || y > hi[u]) covers &= ~(1u << u);
                         lo[u] = min(lo[u], x);
                         hi[u] = max(hi[u], y);
                     } else {
@@ -220,10 +248,17 @@ __global__ void __launch_bounds__(1024) scored_chunk_plan_kernel(const ScoredArg
                 }
             }
             __syncwarp();
+            unsigned look = 0u;  // blocks of which no row sees all
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 const int x = __reduce_min_sync(0xffffffffu, lo[u]), y = __reduce_max_sync(0xffffffffu, hi[u]);
                 if (lane == 0 && b0 + 32u * u < all) spans[b0 + 32u * u] = make_int2(x, y);
+                if (a.umma_rows > 0 && x < y && !__any_sync(0xffffffffu, lo[u] == x && hi[u] == y && (covers >> u & 1u)))
+                    look |= 1u << u;
+            }
+            for (; look; look &= look - 1u) {
+                const unsigned b = b0 + 32u * (unsigned)(__ffs(look) - 1);
+                if (ranges_apart(a, block_at(b), lane) && lane == 0) spans[b].y |= kHoles;
             }
         }
         __syncthreads();
@@ -234,27 +269,33 @@ __global__ void __launch_bounds__(1024) scored_chunk_plan_kernel(const ScoredArg
     for (int pass = 0; pass < 2; ++pass) {
         for (unsigned b = first; b < all; b += stride) {
             const int s = (int)(b / (unsigned)blocks), rb = (int)(b - (unsigned)s * (unsigned)blocks);
-            const Block at = block_at(b);
+            const ChunkBlock at = block_at(b);
             if (at.t0 >= at.t1) continue;
             int2 k;
+            int holes = 0;
             if (in_smem) {
                 k = spans[b];
+                holes = k.y & kHoles;
+                k.y &= ~kHoles;
             } else if (!masks) {
                 k.x = a.window > 0 ? max(0, at.before + at.t0 - a.window + 1) : 0;
                 k.y = at.before + at.t1;
             } else {
-                int lo = INT_MAX, hi = 0;
+                int lo = INT_MAX, hi = 0, longest = 0;
                 for (int t = at.t0 + lane; t < at.t1; t += 32) {
                     const int2 r = row_range(a, at.q0 + t, at.before + t, at.len);
                     if (r.x < r.y) {
                         lo = min(lo, r.x);
                         hi = max(hi, r.y);
+                        longest = max(longest, r.y - r.x);
                     } else if (pass == 0) {
                         zero_row(a, at.q0 + t);
                     }
                 }
                 k.x = __reduce_min_sync(0xffffffffu, lo);
                 k.y = __reduce_max_sync(0xffffffffu, hi);
+                if (a.umma_rows > 0 && pass == 1 && __reduce_max_sync(0xffffffffu, longest) < k.y - k.x)
+                    holes = ranges_apart(a, at, lane) ? kHoles : 0;
             }
             if (k.x >= k.y) continue;
             const int p0 = k.x / Pt, p1 = (k.y - 1) / Pt;
@@ -265,7 +306,7 @@ __global__ void __launch_bounds__(1024) scored_chunk_plan_kernel(const ScoredArg
                     atomicAdd(&hist[bin], 1);
                 } else {
                     const int place = atomicAdd(&start[bin], 1);
-                    a.plan_list[place] = make_int4(s, a.umma_rows > 0 ? rb : p | rb << 16, lo, hi);
+                    a.plan_list[place] = make_int4(s | holes, a.umma_rows > 0 ? rb : p | rb << 16, lo, hi);
                 }
             }
         }

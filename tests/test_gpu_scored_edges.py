@@ -79,3 +79,78 @@ def test_chunk_scored_nan_score_under_a_cap(gpu, dtype, scale, cap, nq):
         got = call_chunk(torch, pa, (q1, k1, vc, tables, lens), qs, dtype, dtype, scale, opts)
         assert_nan_where(got, ref, nan, dtype, E, vmax)
     assert pa.pa_device_errors(clear=True) == 0
+
+
+def hide_unseen(case, qs, opts, dtype):
+    """NaN in the keys and values of every position that is in no row's range, holes between ranges too."""
+    q, kc, vc, tables, lens = case
+    B = kc.shape[2]
+    holes = 0
+    for s, n in enumerate(lens):
+        n, rows = int(n), range(int(qs[s]), int(qs[s + 1]))
+        seen = np.zeros(n, bool)
+        for i in rows:
+            seen[max(0, opts["key_begin"][i]):max(0, min(n, opts["key_end"][i]))] = True
+        at = np.nonzero(seen)[0]
+        holes += int((~seen[at.min():at.max()]).sum()) if len(at) else 0
+        for j in np.nonzero(~seen)[0]:
+            for c in (kc, vc):
+                c[tables[s][j // B], :, j % B] = synth.nan_value(dtype)
+    return holes
+
+
+def ranges_with_holes(rng, kind, lens, nq):
+    begin, end = [], []
+    for n, m in zip(lens, nq):
+        cuts = np.sort(rng.integers(0, n + 1, 6))
+        for t in range(m):
+            if kind == "two":            # one of two places, by row
+                b, e = ((0, 10), (n - 17, n))[t * 7 // 3 % 2]
+            elif kind == "last":         # every row but one at the front
+                b, e = (n - 5, n - 2) if t == m - 1 else (3, 21)
+            elif kind == "empty":        # rows that see nothing between rows that do
+                b, e = ((1, 9), (5, 5), (n, 3), (n - 9, n), (7, 7))[t % 5]
+            else:                        # pieces of the context at random, some empty
+                k = int(rng.integers(0, 5))
+                b, e = int(cuts[k]), int(cuts[k]) + int(rng.integers(0, max(1, (cuts[k + 1] - cuts[k]) * 2 // 3) + 1))
+            begin.append(b)
+            end.append(e)
+    return dict(key_begin=begin, key_end=end)
+
+
+@pytest.mark.parametrize("path", ["short", "long", "tiles"])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("kind", ["two", "last", "empty", "random"])
+@pytest.mark.parametrize("D,B,G", [(64, 16, 1), (128, 32, 8), (128, 16, 4)])
+def test_chunk_scored_holes_between_ranges(gpu, D, B, G, kind, dtype, path):
+    torch, pa = gpu
+    rng = synth.make_rng(8100 + D + B + G + len(kind) + len(path))
+    Hkv = {1: 4, 4: 8, 8: 1}[G]
+    nq = {"short": [1, 5, 8, 7], "long": [33, 70, 9, 64], "tiles": [300, 129, 5, 257]}[path]
+    lens = [n + int(x) for n, x in zip(nq, (150, 333, 40, 90))]
+    for more in (dict(), dict(cap=4.0), dict(slopes=np.full(G * Hkv, 0.05))):
+        case, qs = chunk_case(rng, dtype, G * Hkv, Hkv, D, B, lens, nq)
+        opts = dict(ranges_with_holes(rng, kind, lens, nq), **more)
+        clean = (case[0], case[1].copy(), case[2].copy(), case[3], case[4])
+        assert hide_unseen(case, qs, opts, dtype) > 0
+        ref, E, vmax = ref_chunk(clean, qs, dtype, 0.2, opts)
+        got = call_chunk(torch, pa, case, qs, dtype, dtype, 0.2, opts, psize=[0, 4 * B][len(more)])
+        assert_rows_close(got, ref, dtype, dtype, E, vmax)
+    assert pa.pa_device_errors(clear=True) == 0
+
+
+def test_chunk_scored_holes_in_a_plan_of_many_blocks(gpu):
+    # more row blocks than the plan keeps in shared memory: its other way over the masks
+    torch, pa = gpu
+    rng = synth.make_rng(8190)
+    Hq, Hkv, D, B, S = 8, 1, 64, 16, 420
+    nq = [int(x) for x in rng.integers(1, 34, S)]
+    lens = [n + int(x) for n, x in zip(nq, rng.integers(20, 120, S))]
+    case, qs = chunk_case(rng, "bf16", Hq, Hkv, D, B, lens, nq)
+    opts = ranges_with_holes(rng, "random", lens, nq)
+    clean = (case[0], case[1].copy(), case[2].copy(), case[3], case[4])
+    assert hide_unseen(case, qs, opts, "bf16") > 0
+    ref, E, vmax = ref_chunk(clean, qs, "bf16", 0.2, opts)
+    for max_q in (34, 170):           # two blocks of a sequence at most, and six: 840 and 2520 in all
+        assert_rows_close(call_chunk(torch, pa, case, qs, "bf16", "f32", 0.2, opts, max_q=max_q), ref, "bf16", "f32", E, vmax)
+    assert pa.pa_device_errors(clear=True) == 0
