@@ -364,9 +364,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, HG, RW>::kThreads, ChunkCfg<D, HG,
                     mx1 = fmaxf(mx1, x1[i]);
                 }
                 mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
-                mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
+                mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2)) - kWeightLift<T>;
                 mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
-                mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
+                mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2)) - kWeightLift<T>;
                 if (__any_sync(0xffffffffu, mx0 > m0 || mx1 > m1)) {
                     const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
                     const float al0 = mn0 == -INFINITY ? 1.f : ex2(m0 - mn0);
@@ -504,9 +504,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, HG, RW>::kThreads, ChunkCfg<D, HG,
                 float mx0 = fmaxf(fmaxf(x0[0], x0[1]), fmaxf(x0[2], x0[3]));
                 float mx1 = fmaxf(fmaxf(x1[0], x1[1]), fmaxf(x1[2], x1[3]));
                 mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
-                mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
+                mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2)) - kWeightLift<T>;
                 mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
-                mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
+                mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2)) - kWeightLift<T>;
                 if (__any_sync(0xffffffffu, mx0 > m0 || mx1 > m1)) {
                     const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
                     const float al0 = mn0 == -INFINITY ? 1.f : ex2(m0 - mn0);

@@ -12,7 +12,8 @@
 // document costs only the chunks it touches.  Consumer warp w computes KV head
 // g0 + w: S = Q K^T and O += P V with mma.m16n8k16, the G <= 8 query heads as
 // rows 0-7 of A; for P V rows 0-7 carry the weights' high 16-bit part and rows
-// 8-15 the low part, so that weights keep 16 (bf16) or 22 (f16) bits.
+// 8-15 the low part, so that weights keep 16 (bf16) or 22 (f16) bits; the running
+// maximum m is held 15 octaves below the largest logit for f16 (kWeightLift).
 // Keys outside the range get -inf and their V rows are zeroed in shared
 // memory, so what they hold does not matter.
 //
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(ScoredDecodeCfg<D, HG>::kThreads, 2)
             if (n1 > 0) {
                 float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) - kWeightLift<T>;
                 if (__any_sync(0xffffffffu, mx > m_run)) {
                     const float mn = fmaxf(m_run, mx);
                     const float al = mn == -INFINITY ? 1.f : ex2(m_run - mn);

@@ -2,7 +2,10 @@
 // and the cap and bias of a logit.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include <cmath>
+#include <type_traits>
 
 #include "pa_device.cuh"
 #include "pa_scored.h"
@@ -11,6 +14,14 @@
 namespace pa {
 
 constexpr float kLog2e = 1.4426950408889634f;
+
+// How far below a row's largest logit, in log2 units, its softmax takes the maximum that weights are relative
+// to.  Two f16 parts keep a weight to 2^-25 at best, so with weights of at most 1 those below 2^-25 of the largest
+// would be lost from P V but not from the row's sum (a dominant key and 2^17 others at 2^-26: 0.2 % of the mass).
+// Weights of up to 2^15, just inside f16, keep them down to 2^-40 of the largest; the row's sum is in the same units,
+// so nothing is divided out.  bf16 has the exponents of fp32 and needs no lift.
+template <typename T>
+constexpr float kWeightLift = std::is_same<T, __half>::value ? 15.f : 0.f;
 
 // Keys [x, y) that row i, at position pos of a sequence of len tokens, sees;
 // (0, 0) when none is left.

@@ -1,4 +1,6 @@
 """GPU tests of scored attention at the edges of its contract."""
+import math
+
 import numpy as np
 import pytest
 
@@ -153,4 +155,43 @@ def test_chunk_scored_holes_in_a_plan_of_many_blocks(gpu):
     ref, E, vmax = ref_chunk(clean, qs, "bf16", 0.2, opts)
     for max_q in (34, 170):           # two blocks of a sequence at most, and six: 840 and 2520 in all
         assert_rows_close(call_chunk(torch, pa, case, qs, "bf16", "f32", 0.2, opts, max_q=max_q), ref, "bf16", "f32", E, vmax)
+    assert pa.pa_device_errors(clear=True) == 0
+
+
+# Two f16 parts keep a weight to 2^-22 relative, and to 2^-25 absolute in units in which the largest is 2^lift: lift 15,
+# or 7 in the long chunks, whose maximum may lag by 8.  Against weights of 2^-26 of the largest that is 2^(1 - lift).
+def tail_error(z, lift):
+    return 2.0 ** -22 * z + 2.0 ** -22 + 2.0 ** -21 + 2.0 ** (1 - lift) + 64 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("dominant_last", [False, True])
+@pytest.mark.parametrize("opts", [dict(), dict(cap=300.0), dict(slopes=[0.0] * 4)])
+@pytest.mark.parametrize("nq", [0, 3, 70])
+def test_scored_f16_tail_of_small_weights(gpu, nq, opts, dominant_last):
+    """One key of weight near 1 and value 0, thousands at about 2^-26 and value 1: their mass is the result."""
+    torch, pa = gpu
+    Hq, Hkv, D, B, n = 4, 1, 64, 32, 8192
+    n_rows = max(nq, 1)
+    f16 = np.float16
+    q = np.zeros((n_rows, Hq, D), f16)
+    q[..., 0] = 4.5
+    N = n // B
+    kc, vc = np.zeros((N, Hkv, B, D), f16), np.ones((N, Hkv, B, D), f16)
+    at = n - n_rows if dominant_last else 3          # seen by every row
+    kc[at // B, 0, at % B, 0] = 4.0
+    vc[at // B, 0, at % B] = 0.0
+    tables, lens = np.arange(N, dtype=np.int32)[None], np.array([n], np.int32)
+    case = (q, kc, vc, tables, lens)
+    scale, cap = 1.0, opts.get("cap", 0.0)
+    z = 18.0 if not cap else cap * math.tanh(18.0 / cap)
+    keys = np.array([n - n_rows + t + 1 for t in range(n_rows)], np.float64)   # that row t sees
+    small = (keys - 1) * math.exp(-z)
+    ref = small / (1.0 + small)
+    if nq == 0:
+        got = call_decode(torch, pa, case, "f16", "f32", scale, opts, psize=n)
+    else:
+        got = call_chunk(torch, pa, case, np.array([0, nq], np.int32), "f16", "f32", scale, opts, psize=n)
+    E = tail_error(z, 7 if nq * Hq >= 64 else 15) + (cap * 2.0 ** -21 if cap else 0.0)
+    assert (np.abs(got - ref[:, None, None]) <= 2.5 * E * ref[:, None, None]).all(), \
+        f"worst {np.abs(got / ref[:, None, None] - 1).max():.3e} of {2.5 * E:.3e}"
     assert pa.pa_device_errors(clear=True) == 0
