@@ -438,6 +438,17 @@ PA_API int32_t pa_rope_freqs(int32_t rotary_dim, double theta, int32_t scaling, 
  * What slots outside every row's range hold does not matter (NaN included).
  * The rows of one chunk are worked on together: a key or value that some row of
  * a sequence's chunk sees must be finite, or it may reach the chunk's others.
+ * Weights are normalised last, so values have a bound that sums of weighted
+ * ones stay below: magnitudes under 2^100, and under 2^57 for a chunk of a bf16
+ * cache with 0 < softcap <= 55, whose weights are relative to a constant instead
+ * of the row's maximum (up to 2^48) where max_query_len * num_q_heads /
+ * num_kv_heads is 64 or more; larger finite values may give infinities.  A NaN
+ * score makes its row NaN.
+ *
+ * A row's result depends on its own inputs up to rounding only: with a
+ * partition_size of 0 the pieces of a decode follow from the lengths of the whole
+ * batch, and the form in which a cap is evaluated (each within 2^-21) from the
+ * rows worked on beside it.  The same call gives the same bits.
  */
 typedef struct pa_score {
     float softcap;             /* 0: none; else finite and > 0                  */

@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 from gpu_helpers import require_gpu
-from paged_helpers import random_case
+from paged_helpers import random_case, widen
 from paged_kv_cache_127_gb300 import synth
 from scored_helpers import assert_rows_close
 from test_gpu_scored import call_chunk, call_decode, chunk_case, ref_chunk, ref_decode
@@ -194,4 +194,33 @@ def test_scored_f16_tail_of_small_weights(gpu, nq, opts, dominant_last):
     E = tail_error(z, 7 if nq * Hq >= 64 else 15) + (cap * 2.0 ** -21 if cap else 0.0)
     assert (np.abs(got - ref[:, None, None]) <= 2.5 * E * ref[:, None, None]).all(), \
         f"worst {np.abs(got / ref[:, None, None] - 1).max():.3e} of {2.5 * E:.3e}"
+    assert pa.pa_device_errors(clear=True) == 0
+
+
+@pytest.mark.parametrize("cap,sign", [(55.0, 1.0), (55.0, -1.0), (50.0, 1.0), (30.0, 1.0), (60.0, 1.0)])
+@pytest.mark.parametrize("nq", [0, 5, 80])
+def test_scored_values_up_to_the_stated_bound(gpu, nq, cap, sign):
+    """Values of magnitudes up to 2^57 (and in decode, short chunks and with wider caps up to 2^100) with every logit near the
+    cap, where weights relative to a constant are largest, or near minus the cap, where they are smallest."""
+    torch, pa = gpu
+    rng = synth.make_rng(8300 + nq)
+    Hq, Hkv, D, B, n = 8, 2, 128, 16, 3000
+    top = 57 if nq * (Hq // Hkv) >= 64 and cap <= 55.0 else 100
+    N = -(-n // B)
+    rows = max(nq, 1)
+    q = synth.to_storage(np.abs(rng.normal(size=(rows, Hq, D))).astype(np.float32), "bf16")
+    kc = synth.to_storage((sign * np.abs(rng.normal(size=(N, Hkv, B, D)))).astype(np.float32), "bf16")
+    vc = synth.to_storage((rng.uniform(0.5, 1.0, (N, Hkv, B, D)) * rng.choice([-1.0, 1.0], (N, Hkv, B, D))).astype(np.float32)
+                          * np.float32(2.0 ** (top - 1)), "bf16")
+    assert np.abs(widen(vc, "bf16")).max() < 2.0 ** top
+    case = (q, kc, vc, np.arange(N, dtype=np.int32)[None], np.array([n], np.int32))
+    opts = dict(cap=cap)
+    if nq == 0:
+        ref, _, E, vmax = ref_decode(case, "bf16", 2.0, opts)
+        got = call_decode(torch, pa, case, "bf16", "f32", 2.0, opts)
+    else:
+        qs = np.array([0, nq], np.int32)
+        ref, E, vmax = ref_chunk(case, qs, "bf16", 2.0, opts)
+        got = call_chunk(torch, pa, case, qs, "bf16", "f32", 2.0, opts)
+    assert_rows_close(got, ref, "bf16", "f32", E, vmax)
     assert pa.pa_device_errors(clear=True) == 0
