@@ -148,8 +148,8 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
     auto v_full = [&](int i) { return bars + 8u * (uint32_t)(2 * C::kStages + i); };
     auto v_empty = [&](int i) { return bars + 8u * (uint32_t)(3 * C::kStages + i); };
     // Tile 0's softmax has zeroed the V rows of step g that must not contribute.  A ring of kMasks, not of
-    // stages: tile 0 publishes step g once P V of g - 2 is done, so once the other tile's P V of g - 5 has
-    // released its V; with 3 barriers it could complete one twice before that tile has seen it once.
+    // stages: tile 0 publishes step g once P V of g - kSB is done, so once the other tile's P V of g - kSB - kStages
+    // has released its V; with kStages barriers it could complete one twice before that tile has seen it once.
     auto v_zeroed = [&](int g) { return base + (uint32_t)(C::kZeroedOff + 8 * (g % C::kMasks)); };
     auto tbar = [&](int u, int i) { return bars + 8u * (uint32_t)(5 * C::kStages + u * C::kTileBars + i); };
     constexpr int kSB = C::kSB;
@@ -176,10 +176,10 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
     auto s_col = [&](int u, int b) { return (uint32_t)(128 * u + C::kN * b); };
     auto o_col = [&](int u) { return C::kOCol + (uint32_t)(D * u); };
     // Boxes loaded of step g.  The K producer writes it before the step's K lands, so that a tile that has
-    // seen S knows it.  It writes step g once S of g - 3 is done, so tile 0's P V of g - 5, whose V came when
-    // both tiles' P V had released that of g - 8: every tile has read what lies 8 steps back.  So the
-    // softmax waits for V only where it zeroes rows of it (waiting in every step: 334 us against 318
-    // on 16 x 512-token capped chunks).
+    // seen S knows it.  It writes step g once S of g - kStages is done, so tile 0's P V of kSB steps before, whose V
+    // came when both tiles' P V had released that of kStages before: every tile has read what lies
+    // 2 kStages + kSB steps back (8; 16 with steps of 32 keys).  So the softmax waits for V only where it zeroes
+    // rows of it (waiting in every step: 334 us against 318 on 16 x 512-token capped chunks).
     int *masks = reinterpret_cast<int *>(basep + C::kMasksOff);
     auto zero_v_row = [&](uint32_t row) {  // both halves of a row of a step's V
 #pragma unroll
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
             for (int cc = 0; cc < 8; ++cc)
                 asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(row + sb * C::kHalf + cc * 16), "r"(0u) : "memory");
     };
-    static_assert(C::kStages + C::kSB < C::kMasks || C::kN != 64, "steps in flight");
+    static_assert(2 * C::kStages + C::kSB <= C::kMasks, "a mask must outlive its readers");
     uint32_t *tslot = reinterpret_cast<uint32_t *>(basep + C::kSlotOff);
 
     if (threadIdx.x == 0) {
