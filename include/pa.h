@@ -743,6 +743,10 @@ PA_API int32_t pa_seq_swap_in(pa_pool *dev, pa_pool *host, int32_t host_seq, int
  * export: export the batch's tables together after the last pa_seq_evict, not
  * one by one between them.
  *
+ * A slot of an evicted sequence holds another token for each KV head, and its
+ * tokens are no contiguous prefix: pa_prefix_insert refuses its blocks, and their
+ * copies by an append or a swap.
+ *
  * All-or-nothing: PA_ERR_OOM if fewer blocks are free, apart from those that
  * the batch gave up, than the new table needs; nothing changed (run pa_evict for
  * the batch so far, then go on).  PA_ERR_INVALID for keep_tokens < 0,
@@ -767,7 +771,8 @@ PA_API int32_t pa_seq_evict(pa_pool *pool, int32_t seq, int32_t keep_tokens, int
  *    sequence under its tokens; prefixes already cached keep their blocks; the
  *    return value counts newly cached blocks.  A block is cached under one
  *    prefix at most: if a block to be newly cached is cached already, or occurs
- *    twice among them, it returns -PA_ERR_INVALID and changes nothing; a block
+ *    twice among them, it returns -PA_ERR_INVALID and changes nothing; so it
+ *    does when one of the first blocks holds what pa_seq_evict kept; a block
  *    id out of range or not allocated gives -PA_ERR_BAD_INDEX;
  *  - pa_prefix_evict drops, one block at a time, a cached prefix with no cached
  *    extension whose block no sequence uses (pool refcount 1), least recently

@@ -47,6 +47,7 @@ int32_t take_block(pa_pool *p) {
     p->free_list.pop_front();
     if (p->copied_from[b]) --p->free_sources;
     p->ref[b] = 1;
+    p->rearranged[b] = 0;
     if (p->fail_budget > 0) --p->fail_budget;
     return b;
 }
@@ -70,6 +71,7 @@ void do_append(pa_pool *p, pa_seq_rec &s, int64_t n, int64_t *slots, int64_t *pa
         int32_t old = s.table.back();
         int32_t fresh = take_block(p);
         --p->ref[old];  // another sequence still holds it: stays >= 1
+        p->rearranged[fresh] = p->rearranged[old];
         s.table.back() = fresh;
         pair[0] = old;
         pair[1] = fresh;
@@ -98,6 +100,7 @@ pa_pool *pa_pool_create(int32_t num_blocks, int32_t block_size, const int32_t *f
     p->ref.assign(num_blocks, 0);
     p->given_up.assign(num_blocks, 0);
     p->copied_from.assign(num_blocks, 0);
+    p->rearranged.assign(num_blocks, 0);
     if (free_order) {
         std::vector<char> seen(num_blocks, 0);
         for (int32_t i = 0; i < num_blocks; ++i) {
@@ -290,6 +293,7 @@ int32_t pa_seq_swap_out(pa_pool *dev, pa_pool *host, int32_t seq, int32_t *host_
     pa_seq_rec &hs = host->seqs[h];
     for (int64_t j = 0; j < nb; ++j) {
         const int32_t hb = take_block(host);
+        host->rearranged[hb] = dev->rearranged[s.table[j]];
         hs.table.push_back(hb);
         pairs_out[2 * j] = s.table[j];
         pairs_out[2 * j + 1] = hb;
@@ -313,6 +317,7 @@ int32_t pa_seq_swap_in(pa_pool *dev, pa_pool *host, int32_t host_seq, int32_t *d
     pa_seq_rec &ds = dev->seqs[d];
     for (int64_t j = 0; j < nb; ++j) {
         const int32_t db = take_block(dev);
+        dev->rearranged[db] = host->rearranged[hs.table[j]];
         ds.table.push_back(db);
         pairs_out[2 * j] = hs.table[j];
         pairs_out[2 * j + 1] = db;
@@ -355,6 +360,7 @@ int32_t pa_seq_evict(pa_pool *pool, int32_t seq, int32_t keep_tokens, int32_t *e
         }
         pool->free_list.resize(kept);
     }
+    for (int32_t b : fresh) pool->rearranged[b] = 1;
     for (int32_t b : s.table) {
         if (!pool->copied_from[b]) {
             pool->copied_from[b] = 1;

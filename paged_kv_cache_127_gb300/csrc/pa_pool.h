@@ -33,6 +33,9 @@ struct pa_pool {
     mutable std::vector<uint8_t> copied_from;  // per block
     mutable std::vector<int32_t> sources;      // the marked ones
     mutable int32_t free_sources = 0;          // marked ones in the free list
+    // Blocks that hold what an eviction kept, or a copy of it: their slots hold other tokens for each KV
+    // head, so the prefix cache refuses them.
+    std::vector<uint8_t> rearranged;           // per block
 };
 
 

@@ -23,7 +23,8 @@
 //    first, until n blocks are free or none qualifies.
 //  - a physical block is cached under at most one prefix: insert rejects, and
 //    changes nothing, when a block it would newly cache is cached already or
-//    appears twice among the new ones.
+//    appears twice among the new ones; so it does when one of the sequence's blocks
+//    holds what an eviction kept (pa_seq_evict).
 // Edges are runs of whole blocks (path compression), split at block
 // boundaries when a sequence diverges inside an edge; stamps are per block.
 // The tails of childless nodes are kept in one ordered set keyed by
@@ -197,6 +198,8 @@ int32_t pa_prefix_insert(pa_prefix_cache *cache, const int32_t *tokens, int32_t 
     const int64_t m = n_blocks < n_tokens / B ? n_blocks : n_tokens / B;
     for (int64_t j = 0; j < m; ++j)
         if (blocks[j] < 0 || blocks[j] >= pool->num_blocks || pool->ref[blocks[j]] < 1) return -PA_ERR_BAD_INDEX;
+    for (int64_t j = 0; j < m; ++j)
+        if (pool->rearranged[blocks[j]]) return -PA_ERR_INVALID;
     // prefixes are cached closed under shortening, so the new entries are exactly blocks [j0, m)
     const int64_t j0 = cached_prefix_blocks(&cache->root, tokens, m, B);
     int64_t marked = j0;

@@ -312,3 +312,52 @@ def test_seq_evict_batches_stay_apart_in_a_random_stream(pa):
             except pa.PaError as e:
                 assert e.status == pa.PA_ERR_OOM
         assert refused  # some for want of blocks that no eviction gave up
+
+
+def test_prefix_cache_refuses_blocks_of_an_evicted_sequence(pa):
+    """After an eviction a block's slots hold other tokens for each KV head: they are no prefix of anything."""
+    with pa.Pool(40, 4) as pool, pa.Pool(20, 4) as host:
+        h = pool.handle
+        cache = pa.pa_prefix_cache_create(h)
+        tokens = np.arange(100, 140, dtype=np.int32)
+        insert = lambda s, n: pa.pa_prefix_insert(cache, tokens[:n], pa.pa_seq_table(h, s))
+
+        def refused(s, n):
+            before = [pa.pa_block_refcount(h, b) for b in range(40)], pa.pa_prefix_cached_blocks(cache)
+            with pytest.raises(pa.PaError) as e:
+                insert(s, n)
+            assert e.value.status == pa.PA_ERR_INVALID
+            assert before == ([pa.pa_block_refcount(h, b) for b in range(40)], pa.pa_prefix_cached_blocks(cache))
+
+        a = pa.pa_seq_create(h)
+        pa.pa_seq_append(h, a, 24)
+        assert insert(a, 24) == 6                        # before the eviction, as ever
+        assert pa.pa_seq_evict(h, a, 10)
+        refused(a, 8)
+        pa.pa_seq_append(h, a, 6)                        # new tokens behind the kept ones: the prefix before them is not theirs
+        refused(a, 16)
+        f = pa.pa_seq_fork(h, a)
+        refused(f, 16)
+        pa.pa_seq_append(h, f, 2)
+        b = pa.pa_seq_create(h)
+        pa.pa_seq_append(h, b, 9)
+        assert pa.pa_seq_evict(h, b, 3)
+        c = pa.pa_seq_fork(h, b)
+        _, pairs = pa.pa_seq_append(h, c, 1)             # the shared partial block is copied, what it holds with it
+        assert len(pairs) == 1
+        refused(c, 4)
+        out, _ = pa.pa_seq_swap_out(h, host.handle, c)
+        back, _ = pa.pa_seq_swap_in(h, host.handle, out)
+        refused(back, 4)
+        # nothing kept, or the blocks in other hands: as new ones
+        assert pa.pa_seq_evict(h, b, 0)
+        pa.pa_seq_append(h, b, 8)
+        tokens = tokens + 1000
+        assert insert(b, 8) == 2
+        for s in (a, f, back):
+            pa.pa_seq_free(h, s)
+        d = pa.pa_seq_create(h)
+        pa.pa_seq_append(h, d, 4 * pa.pa_pool_num_free(h))
+        tokens = np.arange(5000, 5200, dtype=np.int32)
+        assert insert(d, 200) == len(pa.pa_seq_table(h, d))
+        pa.pa_prefix_cache_destroy(cache)
