@@ -543,7 +543,7 @@ PA_API int32_t pa_chunk_scored(const pa_dims *dims, const pa_score *score, const
  *                 not overlap context_lens or keep_lens
  *   workspace     >= pa_evict_workspace_bytes(dims) bytes, 256-byte aligned
  * num_q_heads of dims is not used; num_seqs * num_kv_heads is at most 65535,
- * max_blocks_per_seq * block_size at most 2^30, num_blocks * num_kv_heads *
+ * max_blocks_per_seq * block_size and key_sums->cols at most 2^30, num_blocks * num_kv_heads *
  * block_size at most 2^31 - 1 (PA_ERR_INVALID above).  Any block_size and any
  * head_dim whose row is a multiple of 16 bytes.  A row whose source or destination block is
  * outside [0, N) is skipped and flagged (PA_DEVERR_BAD_BLOCK).

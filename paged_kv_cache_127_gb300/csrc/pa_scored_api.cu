@@ -409,6 +409,7 @@ int32_t pa_evict(const pa_dims *dims, void *k_cache, void *v_cache, const int32_
     if (recent < 0 || !key_sums) return PA_ERR_INVALID;
     rc = check_sums(key_sums, (int64_t)dims->max_blocks_per_seq * dims->block_size);
     if (rc != PA_OK) return rc;
+    if (key_sums->cols > 1 << 30) return PA_ERR_INVALID;  // rows are walked in 32-bit steps
     if (dims->num_seqs == 0) return PA_OK;
     if (!k_cache || !v_cache || !block_tables || !context_lens || !new_tables || !keep_lens || !sums_out || !new_lens)
         return PA_ERR_INVALID;

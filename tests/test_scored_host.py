@@ -361,3 +361,11 @@ def test_prefix_cache_refuses_blocks_of_an_evicted_sequence(pa):
         tokens = np.arange(5000, 5200, dtype=np.int32)
         assert insert(d, 200) == len(pa.pa_seq_table(h, d))
         pa.pa_prefix_cache_destroy(cache)
+
+
+def test_evict_refuses_rows_of_sums_that_its_loops_would_step_past(pa):
+    # the kernel walks a row of sums in 32-bit steps of up to 8192
+    far = P + (1 << 45)
+    for cols in ((1 << 30) + 4, (1 << 31) - 4):
+        assert evict(pa, dims(pa), pa.pa_key_sums(P, None, 2, cols), out=far) == pa.PA_ERR_INVALID
+    assert evict(pa, dims(pa, num_seqs=0), pa.pa_key_sums(P, None, 2, 1 << 30), out=far) == pa.PA_OK
