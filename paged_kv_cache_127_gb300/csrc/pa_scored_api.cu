@@ -16,14 +16,14 @@ bool overlap(const void *p, size_t n, const void *q, size_t m) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
     return n && m && a < b + m && b < a + n;
 }
-// The same for `rows` rows of `row` bytes, `step` and `other` bytes apart: rows of one step
-// that lie in each other's gaps (column ranges of one tensor) are apart.
-bool rows_overlap(const void *p, int64_t step, const void *q, int64_t other, int64_t rows, int64_t row) {
-    if (!overlap(p, (size_t)((rows - 1) * step + row), q, (size_t)((rows - 1) * other + row))) return false;
+// The same for `rows` rows of `row` bytes, `step` bytes apart, and as many of `wide` bytes, `other` apart:
+// rows of one step that lie in each other's gaps (column ranges of one tensor) are apart.
+bool rows_overlap(const void *p, int64_t step, int64_t row, const void *q, int64_t other, int64_t wide, int64_t rows) {
+    if (!overlap(p, (size_t)((rows - 1) * step + row), q, (size_t)((rows - 1) * other + wide))) return false;
     if (step != other) return true;
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-    const int64_t gap = (int64_t)((a < b ? b - a : a - b) % (uintptr_t)step);
-    return gap < row || step - gap < row;
+    const int64_t off = (int64_t)(reinterpret_cast<uintptr_t>(q) - reinterpret_cast<uintptr_t>(p)) % step;
+    const int64_t gap = off < 0 ? off + step : off;  // from a row of p to the next row of q
+    return gap < row || step - gap < wide;
 }
 int32_t to_status(cudaError_t e) {
     if (e == cudaSuccess) return PA_OK;
@@ -312,7 +312,10 @@ int32_t pa_rope_write_kv(const pa_dims *dims, const pa_rope *rope, const void *q
         return PA_ERR_INVALID;
     // q_out is q itself, or apart from it (a token's row is read by other CTAs than the one that writes it)
     if (!(q == q_out && q_stride == q_out_stride) &&
-        rows_overlap(q, q_stride * es, q_out, q_out_stride * es, num_tokens, q_row * es))
+        rows_overlap(q_out, q_out_stride * es, q_row * es, q, q_stride * es, q_row * es, num_tokens))
+        return PA_ERR_INVALID;
+    if (rows_overlap(q_out, q_out_stride * es, q_row * es, k, k_stride * es, kv_row * es, num_tokens) ||
+        rows_overlap(q_out, q_out_stride * es, q_row * es, v, v_stride * es, kv_row * es, num_tokens))
         return PA_ERR_INVALID;
     pa::RopeArgs a{};
     a.q = q;

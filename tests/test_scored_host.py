@@ -369,3 +369,14 @@ def test_evict_refuses_rows_of_sums_that_its_loops_would_step_past(pa):
     for cols in ((1 << 30) + 4, (1 << 31) - 4):
         assert evict(pa, dims(pa), pa.pa_key_sums(P, None, 2, cols), out=far) == pa.PA_ERR_INVALID
     assert evict(pa, dims(pa, num_seqs=0), pa.pa_key_sums(P, None, 2, 1 << 30), out=far) == pa.PA_OK
+
+
+def test_rope_refuses_queries_written_over_keys_or_values(pa):
+    INV, d = pa.PA_ERR_INVALID, dims(pa)
+    far = P + (1 << 30)
+    # q rows of 1024 bytes, k and v rows of 256
+    for bad in (dict(k=far), dict(v=far), dict(k=far + 512), dict(k=far - 128), dict(v=far - 128, vs=512),
+                # column ranges of one tensor, 2048 bytes a token: starting in the queries, ending in them, a token later
+                dict(os=1024, k=far + 1008, ks=1024), dict(os=1024, v=far - 240, vs=1024),
+                dict(os=1024, k=far + 2048 + 16, ks=1024), dict(os=1024, v=far - 2048 - 240, vs=1024)):
+        assert rope(pa, d, out=far, **bad) == INV, bad
