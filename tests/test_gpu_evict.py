@@ -134,3 +134,43 @@ def test_evict_bad_inputs_are_flagged(gpu):
     for i, j in enumerate(kept[:16]):
         assert torch.equal(kc[10, 0, i], k0[4 + j // 16, 0, j % 16])
     assert torch.equal(kc[11:], k0[11:])
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_many_pairs_take_small_blocks(gpu, in_place):
+    # 320 (sequence, KV head) pairs, a CTA of 256 threads each; more kept than a tile of 1024 places
+    torch, pa = gpu
+    rng = synth.make_rng(9500)
+    S, Hkv, B, cap = 40, 8, 16, 2048
+    lens = [int(x) for x in rng.integers(1100, cap + 1, S)]
+    lens[3], lens[7], lens[11] = 0, cap, 5
+    keeps = [int(x) for x in rng.integers(1, 1900, S)]
+    keeps[0], keeps[7] = 1025, cap - 1
+    sums = rng.lognormal(0.0, 2.0, (S, Hkv, cap + 4)).astype(np.float32)
+    sums[5] = rng.integers(0, 4, (Hkv, cap + 4))
+    assert run(torch, pa, "bf16", Hkv, 8, B, lens, keeps, 77, sums, in_place=in_place, spare_cols=4) == 0
+
+
+def test_evict_copies_several_tiles_a_block(gpu):
+    # 512 pairs over tables of 1296 places: copy blocks of four tiles of 128 rows, counts that end inside each of them
+    torch, pa = gpu
+    rng = synth.make_rng(9510)
+    S, Hkv, B, cap = 64, 8, 16, 1296
+    lens = [int(x) for x in rng.integers(1000, cap + 1, S)]
+    keeps = [int(x) for x in rng.integers(1, 900, S)]
+    keeps[:6] = [128, 127, 129, 512, 513, 640]
+    sums = rng.lognormal(0.0, 2.0, (S, Hkv, cap)).astype(np.float32)
+    assert run(torch, pa, "bf16", Hkv, 64, B, lens, keeps, 30, sums) == 0
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("n,keep", [(393400, 100001), (393500, 700), (61000, 50000)])
+def test_evict_past_shared_memory_and_past_a_tile(gpu, n, keep, in_place):
+    # tables of more than 393,152 places, whose keys a cluster's shared memory does not hold; more kept than a
+    # tile of 32,768 places, with the sums moved in place
+    torch, pa = gpu
+    rng = synth.make_rng(9520 + keep)
+    cap = -(-n // 32) * 32
+    sums = rng.lognormal(0.0, 2.0, (1, 1, cap)).astype(np.float32)
+    sums[0, 0, ::7] = 0.25
+    assert run(torch, pa, "f16", 1, 64, 32, [n], [keep], 333, sums, in_place=in_place) == 0

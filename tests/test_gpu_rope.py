@@ -171,3 +171,18 @@ def test_rope_copies_the_elements_behind_the_rotary_dim_bit_for_bit(gpu, dtype, 
         assert torch.equal(bits(kc.view(-1, D)[:T, R:]), raw[:, 1, R:])
         assert torch.equal(bits(vc.view(-1, D)[:T]), bits(y[:, 2]))
     assert pa.pa_device_errors(clear=True) == 0
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("T,Hq,Hkv,D,R", [(2433, 4, 2, 64, 64), (2432, 8, 1, 128, 32), (2501, 2, 2, 40, 16)])
+def test_rope_two_tokens_a_block(gpu, T, Hq, Hkv, D, R, interleaved):
+    # many tokens: two a block, the last block's second one missing, padding and bad slots in either place
+    torch, pa = gpu
+    rng = synth.make_rng(10500 + T + R)
+    N, B = T // 16 + 4, 16
+    pos = rng.integers(-5, 200000, T)
+    slots = rng.permutation(N * B)[:T]
+    slots[rng.integers(0, T, 60)] = -1
+    slots[[0, 1, 7, 100, T - 1]] = [-1, N * B, N * B + 5, -7, slots[T - 1]]
+    run(torch, pa, "bf16", T, Hq, Hkv, D, B, R, interleaved, pos, slots, N, rng, mscale=1.25)
+    assert pa.pa_device_errors(clear=True) == pa.PA_DEVERR_BAD_SLOT
