@@ -741,7 +741,7 @@ PA_API int32_t pa_seq_swap_in(pa_pool *dev, pa_pool *host, int32_t host_seq, int
  * such blocks as any free block.  pa_pool_export ends the batch, so what it
  * evicted has to go through pa_evict before a pa_seq_evict that follows an
  * export: export the batch's tables together after the last pa_seq_evict, not
- * one by one between them.
+ * one by one between them (pa_seq_table does not end it).
  *
  * A slot of an evicted sequence holds another token for each KV head, and its
  * tokens are no contiguous prefix: pa_prefix_insert refuses its blocks, and their

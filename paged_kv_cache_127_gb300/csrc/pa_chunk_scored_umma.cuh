@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
                 const int b = c % kSB;
                 const int st = g % C::kStages;
                 ok = mbar_wait_bounded(v_full(st), (uint32_t)(g / C::kStages) & 1u, kWaitLimit);
-                if (__builtin_expect((it.s & kHoles) != 0 && ok, 0)) {
+                if (__builtin_expect((it.s & kHoles) != 0, 0) && __all_sync(0xffffffffu, ok)) {
                     // V rows between the rows' ranges hold anything, and a weight of 0 does not keep NaN out: the keys
                     // that no token of the item (of either tile) sees are zeroed, by each tile's issuer for itself (the same
                     // zeros). Ranges are read again and the item from its slot, the tile's until its softmax is done,
