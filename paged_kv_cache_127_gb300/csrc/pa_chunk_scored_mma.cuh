@@ -18,7 +18,8 @@
 // partitions store (m, l, acc) and the merge combines those the range touches.
 //
 // Bound: HBM (a chunk's rows share each key).
-// Measured: five drafted tokens of 256 sequences (32 / 8 heads, D 128, bf16, capped) 131 us (floor 116).
+// Measured: five drafted tokens of 256 sequences (32 / 8 heads, D 128, bf16, capped) 133 us (floor 116), 128 of them
+// this kernel's.
 #pragma once
 
 #include <cuda.h>
@@ -288,9 +289,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, HG, RW>::kThreads, ChunkCfg<D, HG,
             const int kb = k16 + 16 * j;
             const int n0 = max(lo - kb, 0);  // keys n0 .. n1 - 1 of the chunk are in the item's span
             const int n1 = ctb[(kb >> lb) - blk0] < 0 ? 0 : min(16, hi - kb);
-            // two full chunks that some row of this warp sees: one softmax step over 32 keys
+            // two full chunks that every row of this warp sees whole (those that see anything; the others' results are
+            // dropped): one softmax step over 32 keys
             const bool pair = C::kRegSplit && j + 1 < nchunk && n0 == 0 && n1 == 16 && ctb[((kb + 16) >> lb) - blk0] >= 0 &&
-                              hi - kb >= 32 && kb >= win0 && kb + 32 <= win1;
+                              hi - kb >= 32 && kb >= win0 && kb + 32 <= min(win1, wend);
             if (pair) {
                 const int st2 = (cons + 1) % C::kStages;
                 const uint32_t parity2 = (uint32_t)((cons + 1) / C::kStages) & 1u;

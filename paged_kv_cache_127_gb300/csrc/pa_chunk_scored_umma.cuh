@@ -19,14 +19,15 @@
 // the output may be 16-bit, staged in the query tile's own layout and stored by
 // TMA with a map like the queries'.
 //
-// Bound: a step's chain from S through the softmax to P V.  Measured, 16 x 512-token chunks over contexts
-// of up to 4096 (32 / 8 heads, D 128, bf16): ranges only 252 us, bias 313, cap 318 (757 TFLOP/s of the 4 D
-// flops a key and head), both 459; f16, cap 354; the tensor cores' own time would be 127 us, 191 with the
-// low parts' products.  At 345 us capped, leaving out the softmax's arithmetic took 267 us, leaving out the
-// products 318, both 254: the handshakes between the roles are most of it.  Ragged prompts with a prefix
-// mask and a bias (D 64, f16) 57 us.  Tried and slower: two threads a row (sixteen softmax warps, 344 us) and S
-// and P in columns of their own (341), both against 329 at that time; P V of the two tiles issued one whole
-// step after the other: 308 here, but 354 -> 364 for f16 and 296 -> 307 at D 64.
+// Bound: a step's chain from S through the softmax to P V.  Measured (the kernel alone), 16 x 512-token chunks over
+// contexts of up to 4096 (32 / 8 heads, D 128, bf16): ranges only 255 us, bias 314, cap 319 (753 TFLOP/s of the 4 D
+// flops a key and head), both 465; f16, cap 358; D 64, cap 297; the tensor cores' own time would be 127 us, 191 with
+// the low parts' products.  Of the 319 capped, 148 are left without the softmax's arithmetic (cap, masks, exponentials,
+// split) and without the products, 210 without the arithmetic, 278 without the products: about half is the
+// roles' waiting for each other, and most of the rest the arithmetic, which the products only partly hide.
+// Ragged prompts with a prefix mask and a bias (D 64, f16) 58 us.  Tried and slower, against the time of
+// then: two threads a row (sixteen softmax warps, 329 -> 344 us), S and P in columns of their own (329 -> 341);
+// P V of the two tiles issued one whole step after the other: 318 -> 308, but f16 354 -> 364 and D 64 296 -> 307.
 #pragma once
 
 #include <cuda.h>
@@ -179,7 +180,7 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
     // seen S knows it.  It writes step g once S of g - kStages is done, so tile 0's P V of kSB steps before, whose V
     // came when both tiles' P V had released that of kStages before: every tile has read what lies
     // 2 kStages + kSB steps back (8; 16 with steps of 32 keys).  So the softmax waits for V only where it zeroes
-    // rows of it (waiting in every step: 334 us against 318 on 16 x 512-token capped chunks).
+    // rows of it (waiting in every step: 325 us against 319 on 16 x 512-token capped chunks).
     int *masks = reinterpret_cast<int *>(basep + C::kMasksOff);
     auto zero_v_row = [&](uint32_t row) {  // both halves of a row of a step's V
 #pragma unroll

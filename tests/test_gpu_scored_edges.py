@@ -224,3 +224,35 @@ def test_scored_values_up_to_the_stated_bound(gpu, nq, cap, sign):
         got = call_chunk(torch, pa, case, qs, "bf16", "f32", 2.0, opts)
     assert_rows_close(got, ref, "bf16", "f32", E, vmax)
     assert pa.pa_device_errors(clear=True) == 0
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_short_chunks_of_warps_with_few_rows_or_none(gpu, dtype):
+    """Eight heads' warps over two row tiles of which the second has no token, or only ones that see nothing, beside rows that see
+    every key: what the others do not see may be NaN, and their results are their own."""
+    torch, pa = gpu
+    rng = synth.make_rng(8400)
+    Hq, Hkv, D, B = 16, 4, 128, 16
+    nq = [8, 3, 4, 5, 8, 1]
+    lens = [500, 330, 290, 1000, 260, 70]
+    case, qs = chunk_case(rng, dtype, Hq, Hkv, D, B, lens, nq)
+    begin, end = [], []
+    for s, (n, m) in enumerate(zip(lens, nq)):
+        for t in range(m):
+            empty = (s == 0 and t >= 4) or (s == 4 and t < 5) or (s == 3 and t == 2)
+            begin.append(n if empty else 96 if s == 4 else 0)
+            end.append(0 if empty else n - m + t + 1)
+    opts = dict(key_begin=begin, key_end=end, cap=5.0)
+    clean = (case[0], case[1].copy(), case[2].copy(), case[3], case[4])
+    hide_unseen(case, qs, opts, dtype)
+    q = case[0].copy()
+    for s, n in enumerate(lens):            # a row that sees nothing may hold anything
+        for t in range(nq[s]):
+            if begin[int(qs[s]) + t] >= end[int(qs[s]) + t]:
+                q[int(qs[s]) + t] = synth.nan_value(dtype)
+    ref, E, vmax = ref_chunk(clean, qs, dtype, 0.2, opts)
+    for max_q in (8, 15):
+        got = call_chunk(torch, pa, (q,) + case[1:], qs, dtype, "f32", 0.2, opts, max_q=max_q)
+        assert_rows_close(got, ref, dtype, "f32", E, vmax)
+        assert (got[np.array(begin) >= np.array(end)] == 0).all()
+    assert pa.pa_device_errors(clear=True) == 0
