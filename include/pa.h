@@ -367,10 +367,11 @@ PA_API int32_t pa_swap_blocks(const pa_dims *dims, void *k_cache, void *v_cache,
  *                 q_out either; one with a slot >= N * B is skipped the same
  *                 way and flagged (PA_DEVERR_BAD_SLOT)
  * Distinct tokens must have distinct slots, and the caches must not overlap the
- * other tensors.  rotary_dim is at most 2048.  Any head_dim whose row is a
- * multiple of 16 bytes; num_q_heads a multiple of num_kv_heads; only the heads,
- * head_dim, block_size, num_blocks and kv_dtype of dims are used.  Returns
- * PA_OK, PA_ERR_INVALID, PA_ERR_UNSUPPORTED (head_dim, rotary_dim) or PA_ERR_CUDA.
+ * other tensors.  rotary_dim is at most 2048, block_size * head_dim at most
+ * 2^31 - 1.  Any head_dim whose row is a multiple of 16 bytes; num_q_heads a
+ * multiple of num_kv_heads; only the heads, head_dim, block_size, num_blocks and
+ * kv_dtype of dims are used.  Returns PA_OK, PA_ERR_INVALID, PA_ERR_UNSUPPORTED
+ * (head_dim, rotary_dim) or PA_ERR_CUDA.
  */
 typedef struct pa_rope {
     int32_t rotary_dim;

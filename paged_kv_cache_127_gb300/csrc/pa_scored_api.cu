@@ -302,6 +302,7 @@ int32_t pa_rope_write_kv(const pa_dims *dims, const pa_rope *rope, const void *q
     const int64_t es = elem_bytes(dims->kv_dtype);
     const int64_t q_row = (int64_t)dims->num_q_heads * dims->head_dim, kv_row = (int64_t)dims->num_kv_heads * dims->head_dim;
     if (q_row > INT32_MAX / 4) return PA_ERR_INVALID;
+    if ((int64_t)dims->block_size * dims->head_dim > INT32_MAX) return PA_ERR_INVALID;  // a head's rows of a block, in 32 bits
     if (num_tokens == 0) return PA_OK;
     if (!rope->freqs || !q || !k || !v || !positions || !slot_mapping || !q_out || !k_cache || !v_cache)
         return PA_ERR_INVALID;

@@ -380,3 +380,10 @@ def test_rope_refuses_queries_written_over_keys_or_values(pa):
                 dict(os=1024, k=far + 1008, ks=1024), dict(os=1024, v=far - 240, vs=1024),
                 dict(os=1024, k=far + 2048 + 16, ks=1024), dict(os=1024, v=far - 2048 - 240, vs=1024)):
         assert rope(pa, d, out=far, **bad) == INV, bad
+
+
+def test_rope_refuses_blocks_of_more_elements_than_32_bits_hold(pa):
+    # the kernel steps from head to head of a block by block_size * head_dim elements, in 32 bits
+    for B, D in ((1 << 25, 64), (1 << 24, 128), (1 << 30, 64)):
+        assert rope(pa, dims(pa, block_size=B, head_dim=D, num_kv_heads=1, num_q_heads=1, num_blocks=1)) == pa.PA_ERR_INVALID
+    assert rope(pa, dims(pa, block_size=(1 << 25) - 1), T=0) == pa.PA_OK
