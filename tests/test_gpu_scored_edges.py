@@ -20,7 +20,7 @@ def gpu():
 
 # Logits of std `scale * 8`, up to five times that: with these (scale, cap) a warp takes each form of the cap.
 # Caps of more than 55 have a running maximum for bf16 too.
-CAPS = [(0.1, 30.0), (0.1, 6.0), (0.1, 1.0), (1.0, 60.0), (1.0, 20.0), (-0.1, 5.0)]
+CAPS = [(0.1, 0.0), (0.1, 30.0), (0.1, 6.0), (0.1, 1.0), (1.0, 60.0), (1.0, 20.0), (-0.1, 5.0)]
 
 
 def assert_nan_where(got, ref, nan, dtype, E, vmax):
