@@ -30,7 +30,8 @@
  *    one (block, kv head) row set is B * D contiguous elements.
  *  - Supported shapes: head_dim D in {64, 128}; block_size B in {16, 32};
  *    group G = Hq / Hkv in {1, 2, 4, 8}; kv_dtype f32, f16 or bf16.  Other
- *    valid shapes return PA_ERR_UNSUPPORTED.
+ *    valid shapes return PA_ERR_UNSUPPORTED.  A cache may also be held in 8
+ *    bits (pa_cache8), with calls of its own.
  *  - Host allocator calls (pa_pool_*, pa_seq_*) touch no GPU and are not
  *    thread-safe: one pool is used from one thread at a time.
  */
@@ -91,6 +92,8 @@ typedef struct pa_dims {
 #define PA_DEVERR_BAD_PAIR 8u    /* pa_copy_blocks id outside [0, N): pair skipped    */
 #define PA_DEVERR_TIMEOUT 16u    /* a bounded in-kernel wait gave up; outputs of the  */
                                  /* affected work item were not written              */
+#define PA_DEVERR_BAD_AXIS 64u   /* an axis of a rotated pair outside [0, num_axes):  */
+                                 /* the pair is not turned                           */
 #define PA_DEVERR_BAD_ROW 32u    /* a row of key sums outside [0, num_rows): the      */
                                  /* sequence's sums are not updated, and pa_evict     */
                                  /* leaves the sequence as it is                      */
@@ -383,6 +386,138 @@ PA_API int32_t pa_rope_write_kv(const pa_dims *dims, const pa_rope *rope, const 
                                 const void *k, int64_t k_stride, const void *v, int64_t v_stride,
                                 const int32_t *positions, const int64_t *slot_mapping, int32_t num_tokens,
                                 void *q_out, int64_t q_out_stride, void *k_cache, void *v_cache, void *stream);
+
+/*
+ * pa_rope_axes_write_kv -- pa_rope_write_kv for positions with several axes (the
+ * time, row and column of a picture's or a film's patches): pair i turns by
+ *
+ *     t = positions[pair_axis[i], token] * freqs[i]
+ *
+ * so how the pairs are dealt out to the axes, section by section or woven into each
+ * other, is the caller's.  Text has the same position on every axis, and then this is
+ * pa_rope_write_kv.
+ *
+ *   axes          pair_axis: int32 [rotary_dim / 2], device, each 0 .. num_axes - 1
+ *                 (a pair of another axis is not turned, and flagged:
+ *                 PA_DEVERR_BAD_AXIS); num_axes 1 .. 16.  NULL: one axis
+ *   positions     int32 [num_axes, num_tokens], device (any value)
+ *   other arguments, shapes and errors as for pa_rope_write_kv
+ */
+typedef struct pa_axes {
+    int32_t num_axes;
+    const int32_t *pair_axis;
+} pa_axes;
+PA_API int32_t pa_rope_axes_write_kv(const pa_dims *dims, const pa_rope *rope, const pa_axes *axes, const void *q,
+                                     int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                     const int32_t *positions, const int64_t *slot_mapping, int32_t num_tokens,
+                                     void *q_out, int64_t q_out_stride, void *k_cache, void *v_cache, void *stream);
+
+/*
+ * A cache held in 8 bits: each value is an e4m3 code (4 exponent bits, 3 of the
+ * fraction, no infinity, NaN 0x7f and 0xff; torch.float8_e4m3fn) times the scale of its
+ * block and KV head,
+ *
+ *     K[block, h, slot, :] = k_scales[block, h] * k[block, h, slot, :]
+ *
+ * and the same for V.  Half the memory and half the reads of a 16-bit cache.  The calls
+ * below work on it as their counterparts do on the others; kv_dtype of their dims is
+ * the type of the queries, keys and values that go in and of the outputs, PA_F16 or
+ * PA_BF16 (PA_ERR_UNSUPPORTED for PA_F32), D is 64 or 128 and B 16 or 32.
+ *   k, v                 codes [N, Hkv, B, D], device, 16-byte aligned
+ *   k_scales, v_scales   float32 [N, Hkv], device.  The writes store powers of two.  The
+ *                        attention calls take any positive finite scale (those of V within
+ *                        2^60 of each other in one sequence); a block whose V scale is not
+ *                        positive counts as not there
+ */
+typedef struct pa_cache8 {
+    void *k, *v;
+    float *k_scales, *v_scales;
+} pa_cache8;
+
+/*
+ * pa_rope_write_kv8 -- pa_rope_axes_write_kv into an 8-bit cache.  The new scale of a
+ * (block, KV head) is the smallest power of two 2^e, e >= -40, with
+ *     max |v| <= 448 * 2^e                         for V,
+ *     max |k| * max(1, |mscale|) <= 316 * 2^e      for K, before its rotation (which may
+ *                                                  grow a value by sqrt(2), to 448 * 2^e)
+ * over the call's finite values for that block, and at least the block's old scale
+ * unless a token of the call goes to the block's first slot: that starts the block anew,
+ * whatever it held.  Where an old scale grows, the codes in the slots before the call's
+ * first one are brought to the new scale (rounded again, so only codes that become
+ * subnormal change what they stand for).  Slots behind are left as they are.  So:
+ * fill a block's slots in order, from its first one on; an append that goes back, as after
+ * rejected drafts, is fine, and voids what lies behind it.
+ *
+ *   axes          as for pa_rope_axes_write_kv; NULL: positions int32 [num_tokens]
+ *   slot_mapping  as for pa_write_kv; moreover the tokens of one block stand next to each
+ *                 other in the list (with nothing between them, padding neither), as the
+ *                 tokens of a sequence do: two stretches of one block in one call
+ *                 leave that block's scale and codes unspecified
+ * A value is rounded once, to the nearest code (ties to even); what is not finite, or is
+ * not after its rotation, becomes NaN.  The queries go to q_out in kv_dtype.  Other
+ * arguments and errors as for pa_rope_write_kv.
+ *
+ * pa_write_kv8 -- the write without a rotation: K's scale as V's.  k and v are
+ * [num_tokens, Hkv, D], tokens *_stride elements apart.
+ *
+ * pa_copy_blocks8 -- pa_copy_blocks for an 8-bit cache: the codes and the scales of whole
+ * blocks.
+ */
+PA_API int32_t pa_rope_write_kv8(const pa_dims *dims, const pa_rope *rope, const pa_axes *axes, const void *q,
+                                 int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                 const int32_t *positions, const int64_t *slot_mapping, int32_t num_tokens, void *q_out,
+                                 int64_t q_out_stride, const pa_cache8 *cache, void *stream);
+PA_API int32_t pa_write_kv8(const pa_dims *dims, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                            const int64_t *slot_mapping, int32_t num_tokens, const pa_cache8 *cache, void *stream);
+PA_API int32_t pa_copy_blocks8(const pa_dims *dims, const pa_cache8 *cache, const int64_t *src_dst_pairs,
+                               int32_t num_pairs, void *stream);
+
+/*
+ * Which keys a query row at position pos sees, for pa_decode8 and pa_chunk8:
+ * the keys j <= pos with
+ *     j > pos - window   or   j < sinks
+ * -- a sliding window and a few first tokens that stay visible.  A window of 0 is none
+ * (all keys j <= pos; sinks is not used), and so is a NULL pa_window.  Only the blocks
+ * that some row of a sequence sees are read.
+ */
+typedef struct pa_window {
+    int32_t window;   /* 0: none; else > 0 */
+    int32_t sinks;    /* >= 0              */
+} pa_window;
+
+/*
+ * pa_decode8, pa_chunk8 -- pa_decode and pa_chunk_attention over an 8-bit cache, with
+ * a choice of the output's type and, optionally, a window:
+ *
+ *     out[i, h, :] = sum_j p_j V_j,  p = softmax_j(scale * q[i, h, :] . K_j)
+ *
+ * with K_j, V_j the values that the codes stand for.  Scores, weights' sums and outputs are held
+ * in fp32; the codes go into the products as they are (exact in 16 bits), and the weights are
+ * rounded to 11 bits (22 in a decode) before the second one.
+ *
+ *   window        NULL: all keys
+ *   out           [S | T, Hq, D] float32, or kv_dtype when out_dtype == kv_dtype
+ *                 (out_dtype is PA_F32 or kv_dtype); must not overlap q or the cache
+ *   workspace     >= pa_*8_workspace_bytes bytes, 256-byte aligned, uninitialised;
+ *                 concurrent calls, and graphs that may run at the same time, need
+ *                 separate workspaces
+ *   partition_size of dims is not used
+ * What slots that no row sees hold does not matter (NaN included).  The rows of one chunk are
+ * worked on together: a key or value that some row of a sequence's chunk sees must be
+ * finite, or it may reach the chunk's others.  A row of which no key is there gets zeros.  The same
+ * call gives the same bits; how a sequence's keys are split depends on the whole batch,
+ * and a row's last bits with it.  Other arguments, shapes and errors as for pa_decode and
+ * pa_chunk_attention (G in {1, 2, 4, 8}).
+ */
+PA_API size_t pa_decode8_workspace_bytes(const pa_dims *dims);
+PA_API int32_t pa_decode8(const pa_dims *dims, const pa_window *window, const void *q, const pa_cache8 *cache,
+                          const int32_t *block_tables, const int32_t *context_lens, float scale, void *out,
+                          int32_t out_dtype, void *workspace, size_t workspace_bytes, void *stream);
+PA_API size_t pa_chunk8_workspace_bytes(const pa_dims *dims, int32_t num_tokens, int32_t max_query_len);
+PA_API int32_t pa_chunk8(const pa_dims *dims, const pa_window *window, const void *q, const pa_cache8 *cache,
+                         const int32_t *block_tables, const int32_t *context_lens, const int32_t *query_start,
+                         int32_t num_tokens, int32_t max_query_len, float scale, void *out, int32_t out_dtype,
+                         void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * pa_rope_freqs -- the rotary frequencies of a model on the host:

@@ -26,7 +26,7 @@ STATUS_NAMES = {0: "PA_OK", 1: "PA_ERR_INVALID", 2: "PA_ERR_UNSUPPORTED", 3: "PA
 PA_SWAP_OUT, PA_SWAP_IN = 0, 1
 PA_DEVERR_BAD_BLOCK, PA_DEVERR_BAD_LEN, PA_DEVERR_BAD_SLOT, PA_DEVERR_BAD_PAIR, PA_DEVERR_TIMEOUT = (
     1, 2, 4, 8, 16)
-PA_DEVERR_BAD_ROW = 32
+PA_DEVERR_BAD_ROW, PA_DEVERR_BAD_AXIS = 32, 64
 PA_ROPE_PLAIN, PA_ROPE_LINEAR, PA_ROPE_BASE, PA_ROPE_RAMP, PA_ROPE_BANDS = range(5)
 ROPE_SCALINGS = {"plain": PA_ROPE_PLAIN, "linear": PA_ROPE_LINEAR, "base": PA_ROPE_BASE, "ramp": PA_ROPE_RAMP,
                  "bands": PA_ROPE_BANDS}
@@ -57,6 +57,19 @@ class pa_pool_stats(ctypes.Structure):
 class pa_rope(ctypes.Structure):
     _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("freqs", ctypes.c_void_p),
                 ("mscale", ctypes.c_float)]
+
+
+class pa_axes(ctypes.Structure):
+    _fields_ = [("num_axes", ctypes.c_int32), ("pair_axis", ctypes.c_void_p)]
+
+
+class pa_cache8(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p)]
+
+
+class pa_window(ctypes.Structure):
+    _fields_ = [("window", ctypes.c_int32), ("sinks", ctypes.c_int32)]
 
 
 class pa_score(ctypes.Structure):
@@ -116,6 +129,15 @@ _SIGNATURES = {
     "pa_seq_create_from_prefix": (_i32, [_vp, _vp, _i32]),
     "pa_rope_write_kv": (_i32, [_vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _vp, _i64, _vp, _vp,
                                 _vp]),
+    "pa_rope_axes_write_kv": (_i32, [_vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _vp, _i64, _vp, _vp,
+                                     _vp]),
+    "pa_rope_write_kv8": (_i32, [_vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _vp, _i64, _vp, _vp]),
+    "pa_write_kv8": (_i32, [_vp, _vp, _i64, _vp, _i64, _vp, _i32, _vp, _vp]),
+    "pa_copy_blocks8": (_i32, [_vp, _vp, _vp, _i32, _vp]),
+    "pa_decode8_workspace_bytes": (_sz, [_vp]),
+    "pa_decode8": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_float, _vp, _i32, _vp, _sz, _vp]),
+    "pa_chunk8_workspace_bytes": (_sz, [_vp, _i32, _i32]),
+    "pa_chunk8": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, ctypes.c_float, _vp, _i32, _vp, _sz, _vp]),
     "pa_rope_freqs": (_i32, [_i32, ctypes.c_double, _i32, ctypes.c_double, ctypes.c_double, ctypes.c_double,
                              ctypes.c_double, _vp, _vp]),
     "pa_decode_scored_workspace_bytes": (_sz, [_vp, _i32]),
@@ -446,6 +468,181 @@ def pa_rope_write_kv(dims: pa_dims, rope: Rope, q, k, v, positions, slot_mapping
             v_cache.data_ptr(), _stream_ptr(stream, dev))
     return _issue(lib.pa_rope_write_kv, args, "pa_rope_write_kv", dev, prepare,
                   (dims, rp, rope.freqs, q, k, v, positions, slot_mapping, q_out, k_cache, v_cache))
+
+
+class Axes:
+    """How the rotated pairs are dealt out to the axes of a position: see make_axes."""
+
+    __slots__ = ("num_axes", "pair_axis")
+
+    def __init__(self, num_axes, pair_axis):
+        self.num_axes, self.pair_axis = int(num_axes), pair_axis
+
+
+def make_axes(num_axes: int, pair_axis) -> Axes:
+    """Positions with num_axes axes (time, row, column): pair_axis is an int32 CUDA
+    tensor [rotary_dim // 2] with the axis of each rotated pair."""
+    return Axes(num_axes, pair_axis)
+
+
+def _rotary_args(dims, rope, axes, q, k, v, positions, slot_mapping, q_out):
+    """The arguments that the rotary writes share, checked: (rope, axes, q .. q_out's stride), and what to keep alive."""
+    t = _torch()
+    d, kv = dims, _torch_dtype(dims.kv_dtype)
+    dev = q.device
+    T = int(slot_mapping.shape[0])
+    qs = _expect_tokens(q, "q", (T, d.num_q_heads, d.head_dim), kv, dev)
+    ks = _expect_tokens(k, "k", (T, d.num_kv_heads, d.head_dim), kv, dev)
+    vs = _expect_tokens(v, "v", (T, d.num_kv_heads, d.head_dim), kv, dev)
+    os_ = _expect_tokens(q_out, "q_out", (T, d.num_q_heads, d.head_dim), kv, dev)
+    _expect_beside(positions, "positions", (T,) if axes is None else (axes.num_axes, T), t.int32, dev)
+    _expect_beside(slot_mapping, "slot_mapping", (T,), t.int64, dev)
+    _expect_beside(rope.freqs, "rope.freqs", (rope.rotary_dim // 2,), t.float64, dev)
+    rp, ax = pa_rope(rope.rotary_dim, int(rope.interleaved), rope.freqs.data_ptr(), rope.mscale), None
+    if axes is not None:
+        _expect_beside(axes.pair_axis, "axes.pair_axis", (rope.rotary_dim // 2,), t.int32, dev)
+        ax = pa_axes(axes.num_axes, axes.pair_axis.data_ptr())
+    args = (ctypes.byref(rp), None if ax is None else ctypes.byref(ax), q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+            positions.data_ptr(), slot_mapping.data_ptr(), T, q_out.data_ptr(), os_)
+    return args, (rp, ax, rope.freqs, None if axes is None else axes.pair_axis, q, k, v, positions, slot_mapping, q_out)
+
+
+def pa_rope_axes_write_kv(dims: pa_dims, rope: Rope, axes, q, k, v, positions, slot_mapping, q_out, k_cache, v_cache,
+                          stream=None, prepare: bool = False):
+    """pa_rope_write_kv for positions [num_axes, T] with several axes, each pair turned by
+    its own (make_axes); with axes None, positions [T] and pa_rope_write_kv itself.
+    With prepare=True nothing runs: the checked call is returned as a Prepared."""
+    d, dev = dims, q.device
+    args, keep = _rotary_args(dims, rope, axes, q, k, v, positions, slot_mapping, q_out)
+    cache_shape = (d.num_blocks, d.num_kv_heads, d.block_size, d.head_dim)
+    _expect_beside(k_cache, "k_cache", cache_shape, _torch_dtype(d.kv_dtype), dev)
+    _expect_beside(v_cache, "v_cache", cache_shape, _torch_dtype(d.kv_dtype), dev)
+    args = (ctypes.byref(dims), *args, k_cache.data_ptr(), v_cache.data_ptr(), _stream_ptr(stream, dev))
+    return _issue(lib.pa_rope_axes_write_kv, args, "pa_rope_axes_write_kv", dev, prepare, (dims, keep, k_cache, v_cache))
+
+
+class Cache8:
+    """A cache of 8-bit codes and their scales: see make_cache8."""
+
+    __slots__ = ("k", "v", "k_scales", "v_scales")
+
+    def __init__(self, k, v, k_scales, v_scales):
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+
+
+def make_cache8(k, v, k_scales, v_scales) -> Cache8:
+    """A cache held in 8 bits: k and v are float8_e4m3fn CUDA tensors [N, Hkv, B, D],
+    k_scales and v_scales float32 [N, Hkv]; a value is its code times its block's and head's scale."""
+    return Cache8(k, v, k_scales, v_scales)
+
+
+def _marshal_cache8(cache, d, dev):
+    t = _torch()
+    shape, heads = (d.num_blocks, d.num_kv_heads, d.block_size, d.head_dim), (d.num_blocks, d.num_kv_heads)
+    _expect(cache.k, "cache.k", shape, t.float8_e4m3fn, dev)
+    _expect_beside(cache.v, "cache.v", shape, t.float8_e4m3fn, dev)
+    _expect_beside(cache.k_scales, "cache.k_scales", heads, t.float32, dev)
+    _expect_beside(cache.v_scales, "cache.v_scales", heads, t.float32, dev)
+    return pa_cache8(cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scales.data_ptr(), cache.v_scales.data_ptr())
+
+
+def _keep8(cache):
+    return (cache.k, cache.v, cache.k_scales, cache.v_scales)
+
+
+def pa_rope_write_kv8(dims: pa_dims, rope: Rope, axes, q, k, v, positions, slot_mapping, q_out, cache: Cache8,
+                      stream=None, prepare: bool = False):
+    """pa_rope_axes_write_kv into an 8-bit cache (axes None: positions [T]); the tokens
+    of one block stand next to each other in the list.
+    With prepare=True nothing runs: the checked call is returned as a Prepared."""
+    dev = q.device
+    args, keep = _rotary_args(dims, rope, axes, q, k, v, positions, slot_mapping, q_out)
+    c8 = _marshal_cache8(cache, dims, dev)
+    args = (ctypes.byref(dims), *args, ctypes.byref(c8), _stream_ptr(stream, dev))
+    return _issue(lib.pa_rope_write_kv8, args, "pa_rope_write_kv8", dev, prepare, (dims, keep, c8, _keep8(cache)))
+
+
+def pa_write_kv8(dims: pa_dims, k, v, slot_mapping, cache: Cache8, stream=None, prepare: bool = False):
+    """pa_write_kv into an 8-bit cache; k and v are [T, Hkv, D] with any token stride.
+    With prepare=True nothing runs: the checked call is returned as a Prepared."""
+    t = _torch()
+    d, kv = dims, _torch_dtype(dims.kv_dtype)
+    dev = k.device
+    T = int(slot_mapping.shape[0])
+    ks = _expect_tokens(k, "k", (T, d.num_kv_heads, d.head_dim), kv, dev)
+    vs = _expect_tokens(v, "v", (T, d.num_kv_heads, d.head_dim), kv, dev)
+    _expect_beside(slot_mapping, "slot_mapping", (T,), t.int64, dev)
+    c8 = _marshal_cache8(cache, d, dev)
+    args = (ctypes.byref(dims), k.data_ptr(), ks, v.data_ptr(), vs, slot_mapping.data_ptr(), T, ctypes.byref(c8),
+            _stream_ptr(stream, dev))
+    return _issue(lib.pa_write_kv8, args, "pa_write_kv8", dev, prepare, (dims, k, v, slot_mapping, c8, _keep8(cache)))
+
+
+def pa_copy_blocks8(dims: pa_dims, cache: Cache8, src_dst_pairs, stream=None, prepare: bool = False):
+    """pa_copy_blocks for an 8-bit cache: codes and scales.
+    With prepare=True nothing runs: the checked call is returned as a Prepared."""
+    t = _torch()
+    dev = src_dst_pairs.device
+    P = int(src_dst_pairs.shape[0])
+    c8 = _marshal_cache8(cache, dims, dev)
+    _expect_beside(src_dst_pairs, "src_dst_pairs", (P, 2), t.int64, dev)
+    args = (ctypes.byref(dims), ctypes.byref(c8), src_dst_pairs.data_ptr(), P, _stream_ptr(stream, dev))
+    return _issue(lib.pa_copy_blocks8, args, "pa_copy_blocks8", dev, prepare, (dims, c8, _keep8(cache), src_dst_pairs))
+
+
+def pa_decode8_workspace_bytes(dims: pa_dims) -> int:
+    return int(lib.pa_decode8_workspace_bytes(ctypes.byref(dims)))
+
+
+def pa_decode8(dims: pa_dims, q, cache: Cache8, block_tables, context_lens, scale: float, out, workspace=None,
+               window: int = 0, sinks: int = 0, stream=None, prepare: bool = False):
+    """pa_decode over an 8-bit cache, with an out of float32 or the queries' dtype; under a
+    window each row sees its last `window` keys and the first `sinks` ones.
+    With prepare=True nothing runs: the checked call is returned as a Prepared."""
+    t = _torch()
+    d, kv = dims, _torch_dtype(dims.kv_dtype)
+    dev = q.device
+    _expect(q, "q", (d.num_seqs, d.num_q_heads, d.head_dim), kv, dev)
+    c8 = _marshal_cache8(cache, d, dev)
+    _expect_beside(block_tables, "block_tables", (d.num_seqs, d.max_blocks_per_seq), t.int32, dev)
+    _expect_beside(context_lens, "context_lens", (d.num_seqs,), t.int32, dev)
+    code = _out_code(out, dims)
+    _expect_beside(out, "out", (d.num_seqs, d.num_q_heads, d.head_dim), out.dtype, dev)
+    win = pa_window(int(window), int(sinks))
+    ws_ptr, ws_bytes = _workspace(workspace, pa_decode8_workspace_bytes(dims), "pa_decode8", dev)
+    args = (ctypes.byref(dims), ctypes.byref(win), q.data_ptr(), ctypes.byref(c8), block_tables.data_ptr(),
+            context_lens.data_ptr(), float(scale), out.data_ptr(), code, ws_ptr, ws_bytes, _stream_ptr(stream, dev))
+    return _issue(lib.pa_decode8, args, "pa_decode8", dev, prepare,
+                  (dims, win, q, c8, _keep8(cache), block_tables, context_lens, out, workspace))
+
+
+def pa_chunk8_workspace_bytes(dims: pa_dims, num_tokens: int, max_query_len: int) -> int:
+    return int(lib.pa_chunk8_workspace_bytes(ctypes.byref(dims), int(num_tokens), int(max_query_len)))
+
+
+def pa_chunk8(dims: pa_dims, q, cache: Cache8, block_tables, context_lens, query_start, scale: float, out,
+              max_query_len: int, workspace=None, window: int = 0, sinks: int = 0, stream=None, prepare: bool = False):
+    """pa_chunk_attention over an 8-bit cache, with an out of float32 or the queries' dtype and
+    the window of pa_decode8.
+    With prepare=True nothing runs: the checked call is returned as a Prepared."""
+    t = _torch()
+    d, kv = dims, _torch_dtype(dims.kv_dtype)
+    dev = q.device
+    T = int(q.shape[0])
+    _expect(q, "q", (T, d.num_q_heads, d.head_dim), kv, dev)
+    c8 = _marshal_cache8(cache, d, dev)
+    _expect_beside(block_tables, "block_tables", (d.num_seqs, d.max_blocks_per_seq), t.int32, dev)
+    _expect_beside(context_lens, "context_lens", (d.num_seqs,), t.int32, dev)
+    _expect_beside(query_start, "query_start", (d.num_seqs + 1,), t.int32, dev)
+    code = _out_code(out, dims)
+    _expect_beside(out, "out", (T, d.num_q_heads, d.head_dim), out.dtype, dev)
+    win = pa_window(int(window), int(sinks))
+    ws_ptr, ws_bytes = _workspace(workspace, pa_chunk8_workspace_bytes(dims, T, max_query_len), "pa_chunk8", dev)
+    args = (ctypes.byref(dims), ctypes.byref(win), q.data_ptr(), ctypes.byref(c8), block_tables.data_ptr(),
+            context_lens.data_ptr(), query_start.data_ptr(), T, int(max_query_len), float(scale), out.data_ptr(), code,
+            ws_ptr, ws_bytes, _stream_ptr(stream, dev))
+    return _issue(lib.pa_chunk8, args, "pa_chunk8", dev, prepare,
+                  (dims, win, q, c8, _keep8(cache), block_tables, context_lens, query_start, out, workspace))
 
 
 class Score:

@@ -1,0 +1,71 @@
+// pa_kv8.h -- host-side interface of the 8-bit cache's kernels: what their entry
+// points (pa_kv8_api.cu) hand to the translation units.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/pa.h"
+#include "pa_internal.h"
+
+namespace pa {
+
+// Scales are powers of two from 2^kScaleFloor on.  kLoudestPlain times its scale is the largest value of a
+// block's codes; a pair that a rotation turns grows by sqrt(2) at most, and 316 sqrt(2) < 448.
+constexpr int kScaleFloor = -40;
+constexpr float kLoudestPlain = 448.f, kLoudestTurned = 316.f;
+
+// ------------------------------------------------------------------ the write
+struct Write8Args {
+    const void *q, *k, *v;          // q null: keys and values only
+    const int32_t *positions;       // [num_axes, T]
+    const int32_t *pair_axis;       // [R / 2], or null: one axis
+    const int64_t *slots;
+    const double *freqs;
+    void *q_out;
+    uint8_t *k_cache, *v_cache;
+    float *k_scales, *v_scales;
+    unsigned int *err;
+    long long q_stride, k_stride, v_stride, q_out_stride;  // elements between tokens
+    int T, Hq, Hkv, D, R, B, N, num_axes, interleaved;
+    float mscale;
+};
+cudaError_t launch_write8(const Write8Args &a, bool bf16, cudaStream_t st);
+cudaError_t launch_copy_blocks8(uint8_t *k, uint8_t *v, float *ks, float *vs, const int64_t *pairs, int P, int N,
+                                int64_t block_bytes, int Hkv, unsigned int *err, cudaStream_t st);
+
+// ------------------------------------------------------------------ attention
+// A decode is the case of one row per sequence: query_start is null, T = S.
+struct Attend8Args {
+    const void *q;                  // [T, Hq, D]
+    const float *k_scales, *v_scales;  // [N, Hkv]
+    const int32_t *block_tables;
+    const int32_t *context_lens;
+    const int32_t *query_start;     // [S + 1], or null
+    void *out;                      // [T, Hq, D], f32 or the queries' type
+    int *hdr;                       // [0] whether query_start is in order (mma.sync); work items, claims (tcgen05)
+    int4 *list;                     // per (sequence, KV head, row block): its first part and their number (int2); tcgen05: work items
+    float *parts;                   // mma.sync: two parts of a (row block, KV head) per warp, O and (m, l)
+    const uint8_t *k_cache, *v_cache;
+    unsigned int *err;
+    int S, T, Hq, Hkv, D, B, N, max_blocks, max_query_len;
+    int window, sinks;              // window 0: none
+    int out16;
+    int units;                      // mma.sync path: warps that take a share of the keys
+    float scale;
+};
+// mma.sync path, and the join of its parts: row blocks of 16 * row_tiles rows of a KV head (0: 8 rows, a decode).
+constexpr int kUnits8 = 152 * 8;   // warps that share a call's keys, at most: eight per SM
+inline int attend8_row_tiles(int max_query_len, int G) {
+    return (long long)max_query_len * G <= 16 ? 1 : 2;
+}
+cudaError_t launch_attend8_mma_f16(const Attend8Args &a, int row_tiles, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
+cudaError_t launch_attend8_mma_bf16(const Attend8Args &a, int row_tiles, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
+// A cache of codes [N, Hkv, B, D]: boxes of one (block, KV head), rows of D bytes with the swizzle of that width.
+cudaError_t make_codes_tensor_map(CUtensorMap *map, const void *codes, int D, int B, long long block_heads);
+// tcgen05 path.
+cudaError_t launch_attend8_umma(const Attend8Args &a, bool bf16, cudaStream_t st);
+
+}  // namespace pa

@@ -1,0 +1,299 @@
+// pa_kv8_api.cu -- C-ABI entry points of the 8-bit cache: argument validation,
+// workspace sizing and dispatch.  See include/pa.h for the contract of each call.
+#include <cstdint>
+
+#include "../../include/pa.h"
+#include "pa_kv8.h"
+#include "pa_scored.h"
+
+namespace {
+
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+int32_t to_status(cudaError_t e) {
+    if (e == cudaSuccess) return PA_OK;
+    return e == cudaErrorNotSupported ? PA_ERR_UNSUPPORTED : PA_ERR_CUDA;
+}
+
+// What all calls ask of the cache's shape.
+int32_t check_shape8(const pa_dims *d) {
+    const int32_t rc = pa::check_cache(d);
+    if (rc != PA_OK) return rc;
+    if (d->kv_dtype == PA_F32 || !(d->head_dim == 64 || d->head_dim == 128) || !(d->block_size == 16 || d->block_size == 32))
+        return PA_ERR_UNSUPPORTED;
+    // cache rows (N * Hkv * B) are addressed with 32-bit coordinates
+    if ((int64_t)d->num_blocks * d->num_kv_heads > INT32_MAX / d->block_size) return PA_ERR_INVALID;
+    return PA_OK;
+}
+int32_t check_cache8(const pa_cache8 *c) {
+    if (!c || !c->k || !c->v || !c->k_scales || !c->v_scales) return PA_ERR_INVALID;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scales, 4) || !aligned(c->v_scales, 4)) return PA_ERR_INVALID;
+    return PA_OK;
+}
+
+int32_t check_attend8(const pa_dims *d) {
+    const int32_t rc = check_shape8(d);
+    if (rc != PA_OK) return rc;
+    if (d->num_seqs < 0 || d->num_q_heads <= 0 || d->max_blocks_per_seq <= 0) return PA_ERR_INVALID;
+    if (d->num_q_heads % d->num_kv_heads != 0) return PA_ERR_INVALID;
+    const int32_t G = d->num_q_heads / d->num_kv_heads;
+    if (!(G == 1 || G == 2 || G == 4 || G == 8)) return PA_ERR_UNSUPPORTED;
+    // positions, and the step behind the last one, in 32 bits
+    if ((int64_t)d->max_blocks_per_seq * d->block_size > INT32_MAX - 4096) return PA_ERR_INVALID;
+    if ((int64_t)d->num_seqs * d->num_q_heads > INT32_MAX) return PA_ERR_INVALID;
+    return PA_OK;
+}
+int32_t check_chunk8(const pa_dims *d, int32_t T, int32_t max_q) {
+    const int32_t rc = check_attend8(d);
+    if (rc != PA_OK) return rc;
+    if (T < 0 || max_q < 1 || max_q > (1 << 20) || d->num_seqs > 65535) return PA_ERR_INVALID;
+    if ((int64_t)T * d->num_q_heads > INT32_MAX) return PA_ERR_INVALID;
+    // the grid of the join: (sequence, KV head, row block of 16 rows or more)
+    const int64_t blocks = ((int64_t)max_q * (d->num_q_heads / d->num_kv_heads) + 15) / 16;
+    return (int64_t)d->num_seqs * d->num_kv_heads > INT32_MAX / blocks ? PA_ERR_INVALID : PA_OK;
+}
+int32_t check_window(const pa_window *w) { return w && (w->window < 0 || w->sinks < 0) ? PA_ERR_INVALID : PA_OK; }
+
+// Workspace, each part 256-byte aligned: a header, the notes of each (sequence, KV head, row block), and two parts
+// for each warp that shares the keys (mma.sync path).
+struct Layout8 {
+    int row_tiles, units;
+    size_t list, parts, total;
+};
+Layout8 layout8(const pa_dims *d, int row_tiles, int32_t max_q) {
+    Layout8 L{};
+    const int64_t G = d->num_q_heads / d->num_kv_heads;
+    L.row_tiles = row_tiles;
+    const int64_t rows = row_tiles ? 16 * row_tiles : 8, blocks = (max_q * G + rows - 1) / rows;
+    // no more warps than give each of them four steps of 32 keys
+    const int64_t steps = ((int64_t)d->max_blocks_per_seq * d->block_size + 31) / 32;
+    const int64_t most = (int64_t)d->num_seqs * d->num_kv_heads * blocks;  // at most 2^31
+    const int64_t units = most > pa::kUnits8 * (int64_t)4 / steps ? pa::kUnits8 : (most * steps + 3) / 4;
+    L.units = (int)(units < pa::kUnits8 ? (units > 0 ? units : 1) : pa::kUnits8);
+    L.list = 256;
+    L.parts = L.list + up256((size_t)most * sizeof(int2));
+    L.total = L.parts + up256((size_t)2 * L.units * rows * (d->head_dim + 2) * sizeof(float));
+    return L;
+}
+Layout8 decode_layout8(const pa_dims *d) { return layout8(d, 0, 1); }
+Layout8 chunk_layout8(const pa_dims *d, int32_t max_q) {
+    return layout8(d, pa::attend8_row_tiles(max_q, d->num_q_heads / d->num_kv_heads), max_q);
+}
+
+// The tensor maps of the caches, re-encoded only when a cache or its shape changes (per host thread).
+cudaError_t codes_map(const void *ptr, int D, int B, long long block_heads, CUtensorMap *out) {
+    struct Entry {
+        const void *ptr = nullptr;
+        long long block_heads = 0;
+        int D = 0, B = 0;
+        CUtensorMap map;
+    };
+    thread_local Entry cache[4];
+    thread_local int next = 0;
+    for (auto &e : cache)
+        if (e.ptr == ptr && e.block_heads == block_heads && e.D == D && e.B == B) {
+            *out = e.map;
+            return cudaSuccess;
+        }
+    Entry &e = cache[next];
+    next = (next + 1) % 4;
+    e.ptr = nullptr;
+    const cudaError_t rc = pa::make_codes_tensor_map(&e.map, ptr, D, B, block_heads);
+    if (rc != cudaSuccess) return rc;
+    e.ptr = ptr;
+    e.block_heads = block_heads;
+    e.D = D;
+    e.B = B;
+    *out = e.map;
+    return cudaSuccess;
+}
+
+void fill8(pa::Attend8Args &a, const pa_dims *d, const pa_window *w, const void *q, const pa_cache8 *c,
+           const int32_t *tables, const int32_t *lens, float scale, void *out, int32_t out_dtype, const Layout8 &L, void *workspace) {
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    a.q = q;
+    a.k_cache = static_cast<const uint8_t *>(c->k);
+    a.v_cache = static_cast<const uint8_t *>(c->v);
+    a.k_scales = c->k_scales;
+    a.v_scales = c->v_scales;
+    a.block_tables = tables;
+    a.context_lens = lens;
+    a.out = out;
+    a.out16 = out_dtype != PA_F32;
+    a.scale = scale;
+    a.hdr = reinterpret_cast<int *>(ws);
+    a.list = reinterpret_cast<int4 *>(ws + L.list);
+    a.parts = reinterpret_cast<float *>(ws + L.parts);
+    a.units = L.units;
+    a.S = d->num_seqs;
+    a.Hq = d->num_q_heads;
+    a.Hkv = d->num_kv_heads;
+    a.D = d->head_dim;
+    a.B = d->block_size;
+    a.N = d->num_blocks;
+    a.max_blocks = d->max_blocks_per_seq;
+    a.window = w ? w->window : 0;
+    a.sinks = w && w->window ? w->sinks : 0;
+}
+
+int32_t run_mma(pa::Attend8Args &a, const pa_dims *d, const Layout8 &L, void *stream) {
+    a.err = pa::device_error_word();
+    if (!a.err) return PA_ERR_CUDA;
+    CUtensorMap tmk, tmv;
+    const long long block_heads = (long long)a.N * a.Hkv;
+    cudaError_t e = codes_map(a.k_cache, a.D, a.B, block_heads, &tmk);
+    if (e == cudaSuccess) e = codes_map(a.v_cache, a.D, a.B, block_heads, &tmv);
+    if (e != cudaSuccess) return PA_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return to_status(d->kv_dtype == PA_BF16 ? pa::launch_attend8_mma_bf16(a, L.row_tiles, tmk, tmv, st)
+                                            : pa::launch_attend8_mma_f16(a, L.row_tiles, tmk, tmv, st));
+}
+
+void fill_write8(pa::Write8Args &a, const pa_dims *d, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                 const int64_t *slots, int32_t T, const pa_cache8 *c) {
+    a.k = k;
+    a.v = v;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.slots = slots;
+    a.k_cache = static_cast<uint8_t *>(c->k);
+    a.v_cache = static_cast<uint8_t *>(c->v);
+    a.k_scales = c->k_scales;
+    a.v_scales = c->v_scales;
+    a.T = T;
+    a.Hkv = d->num_kv_heads;
+    a.D = d->head_dim;
+    a.B = d->block_size;
+    a.N = d->num_blocks;
+    a.num_axes = 1;
+    a.mscale = 1.f;
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t pa_rope_write_kv8(const pa_dims *dims, const pa_rope *rope, const pa_axes *axes, const void *q, int64_t q_stride,
+                          const void *k, int64_t k_stride, const void *v, int64_t v_stride, const int32_t *positions,
+                          const int64_t *slot_mapping, int32_t num_tokens, void *q_out, int64_t q_out_stride,
+                          const pa_cache8 *cache, void *stream) {
+    int32_t rc = check_shape8(dims);
+    if (rc == PA_OK) rc = pa::check_rope(dims, rope, axes);
+    if (rc != PA_OK) return rc;
+    if (num_tokens < 0) return PA_ERR_INVALID;
+    if (num_tokens == 0) return PA_OK;
+    rc = check_cache8(cache);
+    if (rc == PA_OK)
+        rc = pa::check_rope_tokens(dims, rope, q, q_stride, k, k_stride, v, v_stride, positions, slot_mapping, num_tokens,
+                                   q_out, q_out_stride);
+    if (rc != PA_OK) return rc;
+    pa::Write8Args a{};
+    fill_write8(a, dims, k, k_stride, v, v_stride, slot_mapping, num_tokens, cache);
+    a.q = q;
+    a.q_out = q_out;
+    a.q_stride = q_stride;
+    a.q_out_stride = q_out_stride;
+    a.Hq = dims->num_q_heads;
+    a.positions = positions;
+    a.pair_axis = axes ? axes->pair_axis : nullptr;
+    a.num_axes = axes ? axes->num_axes : 1;
+    a.freqs = rope->freqs;
+    a.R = rope->rotary_dim;
+    a.interleaved = rope->interleaved;
+    a.mscale = rope->mscale;
+    a.err = pa::device_error_word();
+    if (!a.err) return PA_ERR_CUDA;
+    return to_status(pa::launch_write8(a, dims->kv_dtype == PA_BF16, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t pa_write_kv8(const pa_dims *dims, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                     const int64_t *slot_mapping, int32_t num_tokens, const pa_cache8 *cache, void *stream) {
+    int32_t rc = check_shape8(dims);
+    if (rc != PA_OK) return rc;
+    if (num_tokens < 0) return PA_ERR_INVALID;
+    if (num_tokens == 0) return PA_OK;
+    rc = check_cache8(cache);
+    if (rc != PA_OK) return rc;
+    const int64_t row = (int64_t)dims->num_kv_heads * dims->head_dim;
+    if (!k || !v || !slot_mapping || k_stride < row || v_stride < row || k_stride % 8 || v_stride % 8) return PA_ERR_INVALID;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slot_mapping, 8)) return PA_ERR_INVALID;
+    pa::Write8Args a{};
+    fill_write8(a, dims, k, k_stride, v, v_stride, slot_mapping, num_tokens, cache);
+    a.err = pa::device_error_word();
+    if (!a.err) return PA_ERR_CUDA;
+    return to_status(pa::launch_write8(a, dims->kv_dtype == PA_BF16, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t pa_copy_blocks8(const pa_dims *dims, const pa_cache8 *cache, const int64_t *src_dst_pairs, int32_t num_pairs,
+                        void *stream) {
+    int32_t rc = check_shape8(dims);
+    if (rc != PA_OK) return rc;
+    if (num_pairs < 0) return PA_ERR_INVALID;
+    if (num_pairs == 0) return PA_OK;
+    rc = check_cache8(cache);
+    if (rc != PA_OK) return rc;
+    if (!src_dst_pairs || !aligned(src_dst_pairs, 8)) return PA_ERR_INVALID;
+    unsigned int *err = pa::device_error_word();
+    if (!err) return PA_ERR_CUDA;
+    const int64_t block_bytes = (int64_t)dims->num_kv_heads * dims->block_size * dims->head_dim;
+    return to_status(pa::launch_copy_blocks8(static_cast<uint8_t *>(cache->k), static_cast<uint8_t *>(cache->v), cache->k_scales,
+                                             cache->v_scales, src_dst_pairs, num_pairs, dims->num_blocks, block_bytes,
+                                             dims->num_kv_heads, err, static_cast<cudaStream_t>(stream)));
+}
+
+size_t pa_decode8_workspace_bytes(const pa_dims *dims) {
+    if (check_attend8(dims) != PA_OK || dims->num_seqs == 0) return 0;
+    return decode_layout8(dims).total;
+}
+
+int32_t pa_decode8(const pa_dims *dims, const pa_window *window, const void *q, const pa_cache8 *cache,
+                   const int32_t *block_tables, const int32_t *context_lens, float scale, void *out, int32_t out_dtype,
+                   void *workspace, size_t workspace_bytes, void *stream) {
+    int32_t rc = check_attend8(dims);
+    if (rc == PA_OK) rc = check_window(window);
+    if (rc != PA_OK) return rc;
+    if (out_dtype != PA_F32 && out_dtype != dims->kv_dtype) return PA_ERR_INVALID;
+    if (dims->num_seqs == 0) return PA_OK;
+    rc = check_cache8(cache);
+    if (rc != PA_OK) return rc;
+    if (!q || !block_tables || !context_lens || !out) return PA_ERR_INVALID;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(block_tables, 4) || !aligned(context_lens, 4)) return PA_ERR_INVALID;
+    const Layout8 L = decode_layout8(dims);
+    if (!workspace || workspace_bytes < L.total || !aligned(workspace, 256)) return PA_ERR_INVALID;
+    pa::Attend8Args a{};
+    fill8(a, dims, window, q, cache, block_tables, context_lens, scale, out, out_dtype, L, workspace);
+    a.T = dims->num_seqs;
+    a.max_query_len = 1;
+    return run_mma(a, dims, L, stream);
+}
+
+size_t pa_chunk8_workspace_bytes(const pa_dims *dims, int32_t num_tokens, int32_t max_query_len) {
+    if (check_chunk8(dims, num_tokens, max_query_len) != PA_OK) return 0;
+    return chunk_layout8(dims, max_query_len).total;
+}
+
+int32_t pa_chunk8(const pa_dims *dims, const pa_window *window, const void *q, const pa_cache8 *cache,
+                  const int32_t *block_tables, const int32_t *context_lens, const int32_t *query_start, int32_t num_tokens,
+                  int32_t max_query_len, float scale, void *out, int32_t out_dtype, void *workspace, size_t workspace_bytes,
+                  void *stream) {
+    int32_t rc = check_chunk8(dims, num_tokens, max_query_len);
+    if (rc == PA_OK) rc = check_window(window);
+    if (rc != PA_OK) return rc;
+    if (out_dtype != PA_F32 && out_dtype != dims->kv_dtype) return PA_ERR_INVALID;
+    if (dims->num_seqs == 0 || num_tokens == 0) return PA_OK;
+    rc = check_cache8(cache);
+    if (rc != PA_OK) return rc;
+    if (!q || !block_tables || !context_lens || !query_start || !out) return PA_ERR_INVALID;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(query_start, 4))
+        return PA_ERR_INVALID;
+    const Layout8 L = chunk_layout8(dims, max_query_len);
+    if (!workspace || workspace_bytes < L.total || !aligned(workspace, 256)) return PA_ERR_INVALID;
+    pa::Attend8Args a{};
+    fill8(a, dims, window, q, cache, block_tables, context_lens, scale, out, out_dtype, L, workspace);
+    a.query_start = query_start;
+    a.T = num_tokens;
+    a.max_query_len = max_query_len;
+    return run_mma(a, dims, L, stream);
+}
+
+}  // extern "C"

@@ -2,7 +2,8 @@
 // and values into their cache slots, in one pass.
 //
 // Pair (a, b) of a head at angle t = pos * freq becomes mscale * (a cos t -
-// b sin t, b cos t + a sin t).
+// b sin t, b cos t + a sin t).  With several axes each pair has a position of its own
+// (pair_position); everything behind the angles is the same.
 //
 // Angles.  A frequency becomes a fraction of a turn in 64-bit fixed point, freq / 2 pi mod 1 times
 // 2^64 (three fp64 operations per pair and CTA, exact to the frequency's own 53 bits); then
@@ -24,6 +25,7 @@
 
 #include "pa_device.cuh"
 #include "pa_mma.cuh"
+#include "pa_rope.cuh"
 #include "pa_scored.h"
 
 namespace pa {
@@ -41,20 +43,6 @@ template <>
 __device__ __forceinline__ __half narrow<__half>(float x) { return __float2half_rn(x); }
 template <>
 __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
-
-// freq / 2 pi mod 1 in units of 2^-64 turns.
-__device__ __forceinline__ unsigned long long turn_fraction(double freq) {
-    const double t = freq * 0.15915494309189535;  // 1 / (2 pi)
-    return (unsigned long long)((t - floor(t)) * 0x1p64);  // the conversion saturates at 2^64 - 1
-}
-
-// (cos, sin) of pos steps of that fraction, times mscale.
-__device__ __forceinline__ float2 turn_at(unsigned long long fraction, int pos, float mscale) {
-    const int t = (int)((fraction * (unsigned long long)(long long)pos) >> 32);  // turns mod 1, signed, in 2^-32
-    float s, c;
-    sincospif((float)t * 0x1p-31f, &s, &c);
-    return make_float2(c * mscale, s * mscale);
-}
 
 // The slot of a token, or -1 for padding; slots past the cache are flagged by one CTA.
 __device__ __forceinline__ int64_t token_slot(const RopeArgs &a, int t, bool flag) {
@@ -76,8 +64,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_elements_kernel(const RopeA
     const int t = blockIdx.x;
     const int64_t slot = token_slot(a, t, threadIdx.x == 0);
     if (slot < 0) return;
-    const int half = a.R / 2, pos = a.positions[t];
-    for (int i = threadIdx.x; i < half; i += blockDim.x) cs[i] = turn_at(turn_fraction(a.freqs[i]), pos, a.mscale);
+    const int half = a.R / 2;
+    for (int i = threadIdx.x; i < half; i += blockDim.x)
+        cs[i] = turn_at(turn_fraction(a.freqs[i]), pair_position(a, t, i), a.mscale);
     __syncthreads();
     const int64_t blk = slot / a.B, off = slot % a.B;
     const int units = a.D - half;  // per head: R / 2 pairs, then D - R single elements
@@ -139,7 +128,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_units_kernel(const RopeArgs
     if (tid < nt) slots[tid] = token_slot(a, t0 + tid, blockIdx.y == 0);
     for (int e = tid; e < nt * half; e += kRopeThreads) {
         const int t = e / half, p = e - t * half;
-        cs[e] = turn_at(turn_fraction(a.freqs[p]), a.positions[t0 + t], a.mscale);
+        cs[e] = turn_at(turn_fraction(a.freqs[p]), pair_position(a, t0 + t, p), a.mscale);
     }
     __syncthreads();
     const int i = tid % upq, per = kRopeThreads / upq, h0 = tid / upq;
@@ -230,8 +219,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_split_kernel(const RopeArgs
     const int t = blockIdx.x, tid = threadIdx.x, half = a.R / 2;
     const int64_t slot = token_slot(a, t, tid == 0 && blockIdx.y == 0);
     if (slot < 0) return;
-    const int pos = a.positions[t];
-    for (int p = tid; p < half; p += kRopeThreads) cs[p] = turn_at(turn_fraction(a.freqs[p]), pos, a.mscale);
+    for (int p = tid; p < half; p += kRopeThreads)
+        cs[p] = turn_at(turn_fraction(a.freqs[p]), pair_position(a, t, p), a.mscale);
     __syncthreads();
     const int64_t blk = slot / a.B, off = slot % a.B;
     const int i = tid % upq, per = kRopeThreads / upq, h0 = tid / upq, d0 = i * V;

@@ -95,16 +95,22 @@ cudaError_t launch_scored_rows(const ScoredArgs &a, cudaStream_t st);
 // ------------------------------------------------------------------ rotary positions and KV write
 struct RopeArgs {
     const void *q, *k, *v;
-    const int32_t *positions;
+    const int32_t *positions;   // [num_axes, T]
+    const int32_t *pair_axis;   // [R / 2], or null: one axis
     const int64_t *slots;
     const double *freqs;
     void *q_out, *k_cache, *v_cache;
     unsigned int *err;
     long long q_stride, k_stride, v_stride, q_out_stride;  // elements between tokens
-    int T, Hq, Hkv, D, R, B, N, interleaved;
+    int T, Hq, Hkv, D, R, B, N, num_axes, interleaved;
     float mscale;
 };
 cudaError_t launch_rope_write_kv(const RopeArgs &a, int dtype, cudaStream_t st);
+// The checks of a rotary write, of its shapes and of its tokens' tensors (num_tokens > 0), apart from the caches.
+int32_t check_rope(const pa_dims *dims, const pa_rope *rope, const pa_axes *axes);
+int32_t check_rope_tokens(const pa_dims *dims, const pa_rope *rope, const void *q, int64_t q_stride, const void *k,
+                          int64_t k_stride, const void *v, int64_t v_stride, const int32_t *positions,
+                          const int64_t *slot_mapping, int32_t num_tokens, void *q_out, int64_t q_out_stride);
 
 // ------------------------------------------------------------------ eviction
 struct EvictArgs {

@@ -127,6 +127,45 @@ void fill_args(pa::ScoredArgs &a, const pa_dims *d, const pa_score *sc, const Sc
 
 }  // namespace
 
+namespace pa {
+
+int32_t check_rope(const pa_dims *dims, const pa_rope *rope, const pa_axes *axes) {
+    const int32_t rc = check_cache(dims);
+    if (rc != PA_OK) return rc;
+    if (!rope) return PA_ERR_INVALID;
+    if (dims->num_q_heads <= 0 || dims->num_q_heads % dims->num_kv_heads != 0) return PA_ERR_INVALID;
+    if (rope->rotary_dim < 2 || rope->rotary_dim > dims->head_dim || rope->rotary_dim % 2 != 0 ||
+        (rope->interleaved != 0 && rope->interleaved != 1) || !std::isfinite(rope->mscale))
+        return PA_ERR_INVALID;
+    if (axes && (axes->num_axes < 1 || axes->num_axes > 16 || !axes->pair_axis || !aligned(axes->pair_axis, 4))) return PA_ERR_INVALID;
+    if ((int64_t)dims->num_q_heads * dims->head_dim > INT32_MAX / 4) return PA_ERR_INVALID;
+    if ((int64_t)dims->block_size * dims->head_dim > INT32_MAX) return PA_ERR_INVALID;  // a head's rows of a block, in 32 bits
+    return PA_OK;
+}
+
+int32_t check_rope_tokens(const pa_dims *dims, const pa_rope *rope, const void *q, int64_t q_stride, const void *k,
+                          int64_t k_stride, const void *v, int64_t v_stride, const int32_t *positions,
+                          const int64_t *slot_mapping, int32_t num_tokens, void *q_out, int64_t q_out_stride) {
+    const int64_t es = elem_bytes(dims->kv_dtype);
+    const int64_t q_row = (int64_t)dims->num_q_heads * dims->head_dim, kv_row = (int64_t)dims->num_kv_heads * dims->head_dim;
+    if (!rope->freqs || !q || !k || !v || !positions || !slot_mapping || !q_out) return PA_ERR_INVALID;
+    if (q_stride < q_row || q_out_stride < q_row || k_stride < kv_row || v_stride < kv_row) return PA_ERR_INVALID;
+    if (q_stride * es % 16 || q_out_stride * es % 16 || k_stride * es % 16 || v_stride * es % 16) return PA_ERR_INVALID;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(slot_mapping, 8) ||
+        !aligned(positions, 4) || !aligned(rope->freqs, 8))
+        return PA_ERR_INVALID;
+    // q_out is q itself, or apart from it (a token's row is read by other CTAs than the one that writes it)
+    if (!(q == q_out && q_stride == q_out_stride) &&
+        rows_overlap(q_out, q_out_stride * es, q_row * es, q, q_stride * es, q_row * es, num_tokens))
+        return PA_ERR_INVALID;
+    if (rows_overlap(q_out, q_out_stride * es, q_row * es, k, k_stride * es, kv_row * es, num_tokens) ||
+        rows_overlap(q_out, q_out_stride * es, q_row * es, v, v_stride * es, kv_row * es, num_tokens))
+        return PA_ERR_INVALID;
+    return PA_OK;
+}
+
+}  // namespace pa
+
 extern "C" {
 
 size_t pa_decode_scored_workspace_bytes(const pa_dims *dims, int32_t with_sums) {
@@ -288,41 +327,25 @@ int32_t pa_chunk_scored(const pa_dims *dims, const pa_score *score, const void *
     return to_status(pa::launch_scored_merge(a, bf16, st));
 }
 
-int32_t pa_rope_write_kv(const pa_dims *dims, const pa_rope *rope, const void *q, int64_t q_stride, const void *k,
-                         int64_t k_stride, const void *v, int64_t v_stride, const int32_t *positions,
-                         const int64_t *slot_mapping, int32_t num_tokens, void *q_out, int64_t q_out_stride,
-                         void *k_cache, void *v_cache, void *stream) {
-    const int32_t rc = pa::check_cache(dims);
+int32_t pa_rope_axes_write_kv(const pa_dims *dims, const pa_rope *rope, const pa_axes *axes, const void *q, int64_t q_stride,
+                              const void *k, int64_t k_stride, const void *v, int64_t v_stride, const int32_t *positions,
+                              const int64_t *slot_mapping, int32_t num_tokens, void *q_out, int64_t q_out_stride,
+                              void *k_cache, void *v_cache, void *stream) {
+    int32_t rc = pa::check_rope(dims, rope, axes);
     if (rc != PA_OK) return rc;
-    if (!rope || num_tokens < 0) return PA_ERR_INVALID;
-    if (dims->num_q_heads <= 0 || dims->num_q_heads % dims->num_kv_heads != 0) return PA_ERR_INVALID;
-    if (rope->rotary_dim < 2 || rope->rotary_dim > dims->head_dim || rope->rotary_dim % 2 != 0 ||
-        (rope->interleaved != 0 && rope->interleaved != 1) || !std::isfinite(rope->mscale))
-        return PA_ERR_INVALID;
-    const int64_t es = elem_bytes(dims->kv_dtype);
-    const int64_t q_row = (int64_t)dims->num_q_heads * dims->head_dim, kv_row = (int64_t)dims->num_kv_heads * dims->head_dim;
-    if (q_row > INT32_MAX / 4) return PA_ERR_INVALID;
-    if ((int64_t)dims->block_size * dims->head_dim > INT32_MAX) return PA_ERR_INVALID;  // a head's rows of a block, in 32 bits
+    if (num_tokens < 0) return PA_ERR_INVALID;
     if (num_tokens == 0) return PA_OK;
-    if (!rope->freqs || !q || !k || !v || !positions || !slot_mapping || !q_out || !k_cache || !v_cache)
-        return PA_ERR_INVALID;
-    if (q_stride < q_row || q_out_stride < q_row || k_stride < kv_row || v_stride < kv_row) return PA_ERR_INVALID;
-    if (q_stride * es % 16 || q_out_stride * es % 16 || k_stride * es % 16 || v_stride * es % 16) return PA_ERR_INVALID;
-    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(k_cache, 16) ||
-        !aligned(v_cache, 16) || !aligned(slot_mapping, 8) || !aligned(positions, 4) || !aligned(rope->freqs, 8))
-        return PA_ERR_INVALID;
-    // q_out is q itself, or apart from it (a token's row is read by other CTAs than the one that writes it)
-    if (!(q == q_out && q_stride == q_out_stride) &&
-        rows_overlap(q_out, q_out_stride * es, q_row * es, q, q_stride * es, q_row * es, num_tokens))
-        return PA_ERR_INVALID;
-    if (rows_overlap(q_out, q_out_stride * es, q_row * es, k, k_stride * es, kv_row * es, num_tokens) ||
-        rows_overlap(q_out, q_out_stride * es, q_row * es, v, v_stride * es, kv_row * es, num_tokens))
-        return PA_ERR_INVALID;
+    if (!k_cache || !v_cache || !aligned(k_cache, 16) || !aligned(v_cache, 16)) return PA_ERR_INVALID;
+    rc = pa::check_rope_tokens(dims, rope, q, q_stride, k, k_stride, v, v_stride, positions, slot_mapping, num_tokens, q_out,
+                               q_out_stride);
+    if (rc != PA_OK) return rc;
     pa::RopeArgs a{};
     a.q = q;
     a.k = k;
     a.v = v;
     a.positions = positions;
+    a.pair_axis = axes ? axes->pair_axis : nullptr;
+    a.num_axes = axes ? axes->num_axes : 1;
     a.slots = slot_mapping;
     a.freqs = rope->freqs;
     a.q_out = q_out;
@@ -344,6 +367,14 @@ int32_t pa_rope_write_kv(const pa_dims *dims, const pa_rope *rope, const void *q
     a.err = pa::device_error_word();
     if (!a.err) return PA_ERR_CUDA;
     return to_status(pa::launch_rope_write_kv(a, dims->kv_dtype, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t pa_rope_write_kv(const pa_dims *dims, const pa_rope *rope, const void *q, int64_t q_stride, const void *k,
+                         int64_t k_stride, const void *v, int64_t v_stride, const int32_t *positions,
+                         const int64_t *slot_mapping, int32_t num_tokens, void *q_out, int64_t q_out_stride,
+                         void *k_cache, void *v_cache, void *stream) {
+    return pa_rope_axes_write_kv(dims, rope, nullptr, q, q_stride, k, k_stride, v, v_stride, positions, slot_mapping,
+                                 num_tokens, q_out, q_out_stride, k_cache, v_cache, stream);
 }
 
 int32_t pa_rope_freqs(int32_t rotary_dim, double theta, int32_t scaling, double factor, double original_len,
