@@ -426,8 +426,7 @@ PA_API int32_t pa_rope_axes_write_kv(const pa_dims *dims, const pa_rope *rope, c
  *   k, v                 codes [N, Hkv, B, D], device, 16-byte aligned
  *   k_scales, v_scales   float32 [N, Hkv], device.  The writes store powers of two.  The
  *                        attention calls take any positive finite scale (those of V within
- *                        2^60 of each other in one sequence); a block whose V scale is not
- *                        positive counts as not there
+ *                        2^60 of each other in one sequence)
  */
 typedef struct pa_cache8 {
     void *k, *v;

@@ -23,6 +23,9 @@ namespace pa {
 
 constexpr float kLog2e8 = 1.4426950408889634f;
 constexpr int kStep8 = 32;          // keys of a step of the mma.sync path
+constexpr int kStepU8 = 64;         // and of the tcgen05 path
+// The largest weights are 2^7 (2^15 with the maximum's lag of 2^8): f16 then keeps 2^-32 of them.
+constexpr float kLift8 = 7.f;
 
 // Two e4m3 codes (low byte first) as two f16.
 __device__ __forceinline__ uint32_t f16_of_codes(uint32_t lo16) {
@@ -55,7 +58,7 @@ __device__ __forceinline__ Seq8 seq_of(const Attend8Args &a, int s, bool flag) {
     if (a.query_start) {
         r.q0 = a.query_start[s];
         r.n = a.query_start[s + 1] - r.q0;
-        if (r.n > r.len || r.n > a.max_query_len) {
+        if (a.context_lens[s] != r.len || r.n > r.len || r.n > a.max_query_len) {
             if (flag) set_error(a.err, PA_DEVERR_BAD_LEN);
             r.n = 0;
         }
@@ -81,6 +84,20 @@ __device__ __forceinline__ Steps8 steps_of(const Attend8Args &a, int first_pos, 
     r.ns = min(b, (min(a.sinks, begin) + keys - 1) / keys);
     r.gap = b - r.ns;
     r.count = max(0, e - r.gap);
+    return r;
+}
+
+// tcgen05 path: the keys [lo, hi) (and sinks) that rows r0 .. r0 + 128 a.tiles - 1 of a sequence see, and their steps.
+struct Span8 {
+    int lo, hi;
+    Steps8 st;
+};
+__device__ __forceinline__ Span8 span_of(const Attend8Args &a, const Seq8 &q, int r0) {
+    const int G = a.Hq / a.Hkv, first = q.len - q.n + r0 / G;
+    Span8 r;
+    r.hi = q.len - q.n + min(q.n - 1, (r0 + 128 * a.tiles - 1) / G) + 1;
+    r.lo = a.window > 0 ? max(0, first - a.window + 1) : 0;
+    r.st = steps_of(a, first, r.hi, kStepU8);
     return r;
 }
 

@@ -26,7 +26,6 @@
 namespace pa {
 
 constexpr int kWarps8 = 4;   // warps of a CTA
-constexpr float kLift8 = 7.f;   // the largest weights are 2^7 (2^15 with the maximum's lag of 2^8): f16 keeps 2^-32 of them
 
 // RT: 16-row tiles of a chunk's row block; 0: a decode (8 rows).
 template <int D, int RT>

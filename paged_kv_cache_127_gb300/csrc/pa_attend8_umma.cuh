@@ -1,0 +1,689 @@
+// pa_attend8_umma.cuh -- long chunks over the 8-bit cache (the formulas are in
+// pa_attend8.cuh) on the 5th-generation tensor cores: tcgen05.mma with operands in
+// shared memory and the accumulators in tensor memory (TMEM).
+//
+// Work: an item is (MT 128-row tiles, KV head, sequence), row r = token r / G, head r % G; its CTA walks the keys
+// that some of its rows see in steps of 64, with no split and no merge.  Persistent CTAs, one per SM, claim items from
+// a longest-first list.  Warps:
+//   0, 1       issue tile 0's and tile 1's  S_u = Q_u K^T  (M 128, N 64, K = D)
+//   2, 3       issue their  O_u += P_u V    (M 128, N = D, K = 64), P from TMEM
+//   4 .. 7     converters: read the codes of a step (16 bytes a lane, a step ahead), turn them into 16-bit floats (K
+//              into the queries' type, V into f16; both exact) and store them as the swizzled operands; they also
+//              claim the items, send for the query tiles (TMA) and publish each step's scales
+//   8 ..       one softmax warpgroup per tile, one thread per row
+// Converting once per step serves both tiles, and the codes' 16-bit form never leaves the SM.  The alternative, e4m3
+// operands with Q and P split in two terms each, would need as many products, and the split of P in the softmax
+// costs it more instructions than the whole conversion takes here.
+//
+// The softmax applies scales per 16-key box: the box's largest score times ks (with log2 vs added) enters the row's
+// maximum, the exponent's multiply-add carries ks and log2 vs, and the box's sum of weights 1 / vs.  The running
+// maximum moves only when a row's new one is 2^8 larger, as in the kernel for 16-bit caches.
+//
+// Synchronisation is by mbarriers, every wait bounded: on a timeout the kernel sets PA_DEVERR_TIMEOUT, waits
+// (bounded) for the MMAs and copies it issued, frees its TMEM and returns.
+#pragma once
+
+#include <cuda.h>
+
+#include <cmath>
+#include <type_traits>
+
+#include "pa_attend8.cuh"
+#include "pa_tcgen05.cuh"
+
+namespace pa {
+
+template <int D, int MT>
+struct Umma8Cfg {
+    static constexpr int kM = 128;                         // rows per tile (TMEM lanes)
+    static constexpr int kN = 64;                          // keys per step
+    static constexpr int kSB = 2;                          // S/P buffers per tile
+    static constexpr int kBoxes = kN / 16;                 // 16-key boxes of a step
+    static constexpr int kSub = D / 64;                    // 128-byte halves of an operand row
+    static constexpr int kKS = D / 16;                     // k-steps of S = Q K^T
+    static constexpr int kStages = 3;
+    static constexpr int kThreads = 32 * (8 + 4 * MT);
+    static constexpr int kHalf = kN * 128;                 // one half of K (or V) of a step
+    static constexpr int kTile = kSub * kHalf;             // K (or V) of a step
+    static constexpr int kStageBytes = 2 * kTile;
+    static constexpr int kQHalf = kM * 128;
+    static constexpr int kQTile = kSub * kQHalf;
+    // scales and loaded boxes of the last kNotes steps: a step's are written once S of kStages steps before is done,
+    // so once tile 0's P V of kSB steps before that is, whose V came when both tiles' P V had released that of kStages
+    // before: every tile has read what lies 2 kStages + kSB steps back
+    static constexpr int kNotes = 16;
+    static constexpr int kNoteBytes = 4 * 4 * kBoxes;      // ck, lv, ivs per box, the mask
+    static constexpr size_t kKVOff = (size_t)2 * MT * kQTile;
+    static constexpr size_t kNoteOff = kKVOff + (size_t)kStages * kStageBytes;
+    static constexpr size_t kItemOff = kNoteOff + (size_t)kNotes * kNoteBytes;   // per tile and set: 16 ints
+    static constexpr size_t kBarOff = kItemOff + (size_t)MT * 2 * 64;
+    // k_full, k_empty, v_full, v_empty [kStages] | per tile: s_full, p_full, o_done [kSB], q_full [2], q_free [2],
+    // item_ready [2], drain_s, drain_p
+    static constexpr int kTileBars = 3 * kSB + 8;
+    static constexpr int kNumBars = 4 * kStages + MT * kTileBars;
+    static constexpr size_t kSlotOff = kBarOff + 8 * kNumBars;
+    static constexpr size_t kSmem = kSlotOff + 16 + 1024;  // + alignment slack
+    static constexpr uint32_t kTmemCols = 256 * MT;
+    static constexpr uint32_t kOCol = 128 * MT;            // S[u][b] at 128 u + kN b; O[u] at kOCol + D u; P over its S
+    static_assert(2 * kStages + kSB <= kNotes, "a note must outlive its readers");
+    static_assert(kOCol + MT * D <= kTmemCols, "TMEM budget");
+    static_assert(kSmem <= 227 * 1024, "shared memory budget");
+};
+
+// One work item, as the converters publish it to a tile's roles; end: no more items.
+struct Item8 {
+    int s, kvh, r0, qs, n, len, tiles, count, ns, gap, lo, hi, end;
+};
+static_assert(sizeof(Item8) <= 64, "an item's share of shared memory");
+
+template <typename C>
+__device__ __forceinline__ bool umma_item8(const Attend8Args &a, int w, int nwork, Item8 &it) {
+    it.end = w >= nwork;
+    if (it.end) return false;
+    const int4 e = a.list[w / a.Hkv];   // (sequence, tile group, -, -)
+    const int G = a.Hq / a.Hkv, MT = a.tiles;
+    const Seq8 q = seq_of(a, e.x, false);
+    it.s = e.x;
+    it.kvh = w % a.Hkv;
+    it.r0 = e.y * C::kM * MT;
+    it.qs = q.q0;
+    it.n = q.n;
+    it.len = q.len;
+    it.tiles = min(MT, (q.n * G - it.r0 + C::kM - 1) / C::kM);
+    const Span8 span = span_of(a, q, it.r0);
+    it.hi = span.hi;
+    it.lo = span.lo;
+    const Steps8 st = span.st;
+    it.ns = st.ns;
+    it.gap = st.gap;
+    it.count = st.count;
+    return true;
+}
+
+// Bits 0 .. x - 1 of a word (none for x <= 0, all from 32 on).
+__device__ __forceinline__ uint32_t low_bits(int x) { return x >= 32 ? ~0u : (1u << max(x, 0)) - 1u; }
+
+// 16 codes as 16-bit floats, for K in the queries' type.
+template <typename T>
+__device__ __forceinline__ void widen16(const uint4 &w, uint4 &x, uint4 &y) {
+    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+    uint32_t out[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t h = f16_of_codes(i & 1 ? in[i >> 1] >> 16 : in[i >> 1] & 0xffffu);
+        if constexpr (std::is_same<T, __half>::value) {
+            out[i] = h;
+        } else {
+            const float2 f = Mma16<__half>::unpack(h);
+            out[i] = Mma16<T>::pack(f.x, f.y);
+        }
+    }
+    x = make_uint4(out[0], out[1], out[2], out[3]);
+    y = make_uint4(out[4], out[5], out[6], out[7]);
+}
+
+__device__ __forceinline__ void sts128(uint32_t at, const uint4 &x) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+}
+__device__ __forceinline__ uint4 ldg_codes(const uint8_t *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ float4 lds_f4(uint32_t at) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
+    return v;
+}
+__device__ __forceinline__ float max3f(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ bool group_all(int id, bool pred) {   // barrier over a warpgroup
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 q, %1, 0;\n\t"
+        "bar.red.and.pred p, %2, 128, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)pred), "r"(id)
+        : "memory");
+    return r != 0;
+}
+
+// The ring's stage and phase follow the count g of steps so far, the S/P buffers and their phases the count c of the
+// tile's own steps, the item slots and query-tile sets the count of items.
+template <typename T, int D, int MT>
+__global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
+    attend8_umma_kernel(const Attend8Args a, const __grid_constant__ CUtensorMap tmq) {
+    using C = Umma8Cfg<D, MT>;
+    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    constexpr int kSB = C::kSB;
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    unsigned char *basep = smem_raw + (base - raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = a.Hq / a.Hkv;
+
+    const uint32_t kvb = base + (uint32_t)C::kKVOff, bars = base + (uint32_t)C::kBarOff;
+    auto k_full = [&](int i) { return bars + 8u * (uint32_t)i; };
+    auto k_empty = [&](int i) { return bars + 8u * (uint32_t)(C::kStages + i); };
+    auto v_full = [&](int i) { return bars + 8u * (uint32_t)(2 * C::kStages + i); };
+    auto v_empty = [&](int i) { return bars + 8u * (uint32_t)(3 * C::kStages + i); };
+    auto tbar = [&](int u, int i) { return bars + 8u * (uint32_t)(4 * C::kStages + u * C::kTileBars + i); };
+    auto s_full = [&](int u, int b) { return tbar(u, b); };
+    auto p_full = [&](int u, int b) { return tbar(u, kSB + b); };
+    auto o_done = [&](int u, int b) { return tbar(u, 2 * kSB + b); };  // P V done: O is up to date, S/P[u][b] is free
+    auto q_full = [&](int u, int x) { return tbar(u, 3 * kSB + x); };
+    auto q_free = [&](int u, int x) { return tbar(u, 3 * kSB + 2 + x); };
+    auto item_ready = [&](int u, int x) { return tbar(u, 3 * kSB + 4 + x); };
+    auto drain_s = [&](int u) { return tbar(u, 3 * kSB + 6); };
+    auto drain_p = [&](int u) { return tbar(u, 3 * kSB + 7); };
+    Item8 *slots = reinterpret_cast<Item8 *>(basep + C::kItemOff);
+    auto slot = [&](int u, int x) -> Item8 & { return *reinterpret_cast<Item8 *>(reinterpret_cast<unsigned char *>(slots) + 64 * (2 * u + x)); };
+    auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kWaitLimit)); };
+    auto take = [&](int u, int k, Item8 &out) {   // tile u's k-th item; false on a timeout
+        const bool got = wait(item_ready(u, k & 1), (uint32_t)(k >> 1) & 1u);
+        if (got) out = slot(u, k & 1);
+        return got;
+    };
+    auto qtile = [&](int x, int u) { return base + (uint32_t)((x * MT + u) * C::kQTile); };
+    auto s_col = [&](int u, int b) { return (uint32_t)(128 * u + C::kN * b); };
+    auto o_col = [&](int u) { return C::kOCol + (uint32_t)(D * u); };
+    auto note = [&](int g) { return base + (uint32_t)(C::kNoteOff + (size_t)(g % C::kNotes) * C::kNoteBytes); };
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(basep + C::kSlotOff);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(k_full(i), 4);    // the converters
+            mbar_init(k_empty(i), MT);  // one arrival per tile's S issuer (a commit, or a plain one without rows)
+            mbar_init(v_full(i), 4);
+            mbar_init(v_empty(i), MT);  // likewise from each tile's P V issuer
+        }
+        for (int u = 0; u < MT; ++u) {
+            for (int b = 0; b < kSB; ++b) {
+                mbar_init(s_full(u, b), 1);
+                mbar_init(p_full(u, b), 4);
+                mbar_init(o_done(u, b), 1);
+            }
+            for (int x = 0; x < 2; ++x) {
+                mbar_init(q_full(u, x), 1);
+                mbar_init(q_free(u, x), 4 + 2);  // the softmax warps, and both issuers once they have read the slot
+                mbar_init(item_ready(u, x), 1);
+            }
+            mbar_init(drain_s(u), 1);
+            mbar_init(drain_p(u), 1);
+        }
+        fence_mbar_init();
+        prefetch_tmap(&tmq);
+    }
+    if (warp == 0) tc::tmem_alloc(smem_addr(tslot), C::kTmemCols);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tbase = *tslot;
+    griddep_wait();  // the plan's list, longest first
+    const int nwork = max(0, a.hdr[0]) * a.Hkv;
+
+    if (warp >= 4 && warp < 8) {
+        // ------------------------------------------------------------ converters
+        constexpr int kLanes = D / 16;                 // threads of a key's row, 16 codes each
+        constexpr int kPass = 128 / kLanes;            // rows of a pass
+        constexpr int kP = C::kN / kPass;              // passes: 4 (D 128) or 2
+        const int ct = threadIdx.x - 128;              // 0 .. 127
+        const int row = ct / kLanes, ch = ct % kLanes;
+        const int lb = __ffs(a.B) - 1;
+        const uint64_t qpol = policy_evict_first();
+        // a row's two 16-byte chunks of its swizzled operand; the second half's lanes store theirs in the other
+        // order, which keeps a store free of bank conflicts
+        const bool flip = (ch & 4) != 0;
+        int g = 0, k = 0;
+        bool ok = true;
+        for (;;) {
+            Item8 it;
+            if (warp == 4) {
+                int w = blockIdx.x;  // a CTA's first item needs no claim
+                if (k > 0) {
+                    if (lane == 0) w = (int)gridDim.x + atomicAdd(&a.hdr[1], 1);
+                    w = __shfl_sync(0xffffffffu, w, 0);
+                }
+                const bool have = umma_item8<C>(a, w, nwork, it);
+                const int x = k & 1;
+#pragma unroll 1
+                for (int u = 0; ok && u < MT; ++u) {
+                    if (k >= 2) ok = wait(q_free(u, x), (uint32_t)((k >> 1) - 1) & 1u);
+                    if (ok && lane == 0) {
+                        slot(u, x) = it;
+                        mbar_arrive(item_ready(u, x));
+                        if (have && u >= it.tiles) {
+                            mbar_arrive(q_full(u, x));  // no query tile: keep the set's phases in step
+                        } else if (have) {
+                            mbar_arrive_expect_tx(q_full(u, x), (uint32_t)C::kQTile);
+#pragma unroll
+                            for (int sb = 0; sb < C::kSub; ++sb)
+                                tma_load_3d(qtile(x, u) + (uint32_t)(sb * C::kQHalf), &tmq, sb * 64, it.kvh * G,
+                                            it.qs + (it.r0 + C::kM * u) / G, q_full(u, x), qpol);
+                        }
+                    }
+                    __syncwarp();
+                }
+                ++k;
+                if (!ok || !have) break;
+            } else {
+                ok = take(0, k++, it);  // tile 0 has rows in every item
+                if (!ok || it.end) break;
+            }
+            const int32_t *table = a.block_tables + (size_t)it.s * a.max_blocks;
+            auto key_of = [&](int j) { return (j < it.ns ? j : j + it.gap) * C::kN; };
+            auto wanted = [&](int key) { return key < it.hi && (key >= it.lo || key < a.sinks); };
+            // the block ids of step j's rows (-2: not wanted), and of box `lane`
+            int id[kP], box_id = -2;
+            auto look = [&](int j) {
+                const int kb = key_of(j);
+#pragma unroll
+                for (int i = 0; i < kP; ++i) {
+                    const int key = kb + row + kPass * i;
+                    id[i] = wanted(key) ? table[key >> lb] : -2;
+                }
+                if (warp == 4) {
+                    const int b0 = kb + 16 * lane;
+                    const bool any = lane < C::kBoxes && b0 < it.hi && (b0 + 15 >= it.lo || b0 < a.sinks);
+                    box_id = any ? table[b0 >> lb] : -2;
+                }
+            };
+            auto offset_of = [&](int i, int j) {   // of this thread's codes, or -1
+                if (id[i] < 0 || id[i] >= a.N) return (long long)-1;
+                const int key = key_of(j) + row + kPass * i;
+                return (((long long)id[i] * a.Hkv + it.kvh) * a.B + (key & (a.B - 1))) * D + 16 * ch;
+            };
+            uint4 kw[kP], vw[kP];
+            float ks = 1.f, vs = 1.f;
+            bool good = false;
+            auto load = [&](const uint8_t *cache, uint4 (&w)[kP], int j) {
+#pragma unroll
+                for (int i = 0; i < kP; ++i) {
+                    const long long at = offset_of(i, j);
+                    w[i] = at >= 0 ? ldg_codes(cache + at) : make_uint4(0, 0, 0, 0);
+                }
+            };
+            auto load_scales = [&]() {
+                good = box_id >= 0 && box_id < a.N;
+                ks = vs = 1.f;
+                if (good) {
+                    ks = a.k_scales[(size_t)box_id * a.Hkv + it.kvh];
+                    vs = a.v_scales[(size_t)box_id * a.Hkv + it.kvh];
+                } else if (box_id != -2) {
+                    set_error(a.err, PA_DEVERR_BAD_BLOCK);
+                }
+            };
+            auto store = [&](uint32_t tile, int i, const uint4 &x, const uint4 &y) {
+                const int r = row + kPass * i;
+                const uint32_t at = tile + (uint32_t)((ch >> 2) * C::kHalf + r * 128);
+                const uint32_t c0 = (uint32_t)((2 * (ch & 3)) ^ (r & 7)) << 4, c1 = (uint32_t)((2 * (ch & 3) + 1) ^ (r & 7)) << 4;
+                sts128(at + (flip ? c1 : c0), flip ? y : x);
+                sts128(at + (flip ? c0 : c1), flip ? x : y);
+            };
+            look(0);
+            load(a.k_cache, kw, 0);
+            load(a.v_cache, vw, 0);
+            if (warp == 4) load_scales();
+            if (it.count > 1) look(1);
+            for (int j = 0; j < it.count; ++j, ++g) {
+                const int st = g % C::kStages;
+                const uint32_t par = (uint32_t)((g / C::kStages) - 1) & 1u;
+                const uint32_t ktile = kvb + (uint32_t)(st * C::kStageBytes), vtile = ktile + C::kTile;
+                if (g >= C::kStages) ok = wait(k_empty(st), par);
+                if (!ok) break;
+                if (warp == 4) {
+                    const uint32_t mask = __ballot_sync(0xffffffffu, good) & ((1u << C::kBoxes) - 1u);
+                    if (lane < C::kBoxes) {
+                        const uint32_t at = note(g) + 4 * lane;
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(ks * a.scale * kLog2e8) : "memory");
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 4 * C::kBoxes), "f"(lg2(vs)) : "memory");
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 8 * C::kBoxes), "f"(1.f / vs) : "memory");
+                        if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 12 * C::kBoxes), "r"(mask) : "memory");
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kP; ++i) {
+                    uint4 x, y;
+                    widen16<T>(kw[i], x, y);
+                    store(ktile, i, x, y);
+                }
+                tc::fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(k_full(st));
+                if (j + 1 < it.count) load(a.k_cache, kw, j + 1);
+                if (g >= C::kStages) ok = wait(v_empty(st), par);
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < kP; ++i) {
+                    uint4 x, y;
+                    widen16<__half>(vw[i], x, y);
+                    store(vtile, i, x, y);
+                }
+                tc::fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(v_full(st));
+                if (j + 1 < it.count) {
+                    load(a.v_cache, vw, j + 1);
+                    if (warp == 4) load_scales();
+                    if (j + 2 < it.count) look(j + 2);
+                }
+            }
+            if (!ok) break;
+        }
+        if (!ok && lane == 0) set_error(a.err, PA_DEVERR_TIMEOUT);
+        // query tiles still in flight must land before the CTA's shared memory is released
+        if (warp == 4 && !ok)
+            for (int u = 0; u < MT; ++u)
+                for (int n = max(0, k - 2); n < k; ++n) mbar_wait_bounded(q_full(u, n & 1), (uint32_t)(n >> 1) & 1u, 1u << 16);
+    } else if (warp < 2) {
+        // ------------------------------------------------------------ S = Q K^T issuer of tile u
+        const int u = warp;
+        if (u < MT) {
+            constexpr uint32_t idesc_s = tc::f16_idesc(kBf16, false, C::kM, C::kN);
+            const uint64_t kdesc0 = tc::sw128_desc(kvb, 16u, 1024u);
+            int g = 0, c = 0, k = 0;
+            bool ok = true;
+            for (;;) {
+                Item8 it;
+                ok = take(u, k, it);
+                if (!ok || it.end) break;
+                const int x = k & 1;
+                const uint32_t qpar = (uint32_t)(k >> 1) & 1u;
+                ++k;
+                if (lane == 0) mbar_arrive(q_free(u, x));  // done with the slot
+                if (u >= it.tiles) {
+                    for (int j = 0; ok && j < it.count; ++j, ++g) {
+                        const int st = g % C::kStages;
+                        ok = wait(k_full(st), (uint32_t)(g / C::kStages) & 1u);
+                        if (ok && lane == 0) mbar_arrive(k_empty(st));
+                        __syncwarp();
+                    }
+                    if (!ok) break;
+                    continue;
+                }
+                ok = wait(q_full(u, x), qpar);
+                const uint64_t qdesc = tc::sw128_desc(qtile(x, u), 16u, 1024u);
+                for (int j = 0; ok && j < it.count; ++j, ++g, ++c) {
+                    const int st = g % C::kStages, b = c % kSB;
+                    ok = wait(k_full(st), (uint32_t)(g / C::kStages) & 1u);
+                    if (ok && c >= kSB) ok = wait(o_done(u, b), (uint32_t)((c / kSB) - 1) & 1u);  // P V has read P[u][b]
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    if (lane == 0) {
+                        const uint64_t kdesc = tc::desc_add(kdesc0, (uint32_t)(st * C::kStageBytes));
+                        const uint32_t sd = tbase + s_col(u, b);
+#pragma unroll
+                        for (int i = 0; i < C::kKS; ++i)
+                            tc::mma_f16_ss(sd, tc::desc_add(qdesc, (uint32_t)((i >> 2) * C::kQHalf + 32 * (i & 3))),
+                                           tc::desc_add(kdesc, (uint32_t)((i >> 2) * C::kHalf + 32 * (i & 3))), idesc_s, i > 0 ? 1u : 0u);
+                        tc::mma_commit(s_full(u, b));
+                        tc::mma_commit(k_empty(st));
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+            }
+            if (!ok && lane == 0) set_error(a.err, PA_DEVERR_TIMEOUT);
+            // every MMA issued by this thread has completed before TMEM is freed
+            if (lane == 0) tc::mma_commit(drain_s(u));
+            __syncwarp();
+            mbar_wait_bounded(drain_s(u), 0u, kWaitLimit);
+        }
+    } else if (warp < 4) {
+        // ------------------------------------------------------------ O += P V issuer of tile u
+        const int u = warp - 2;
+        if (u < MT) {
+            constexpr uint32_t idesc_o = tc::f16_idesc(false, true, C::kM, D);
+            const uint64_t vdesc0 = tc::sw128_desc(kvb + (uint32_t)C::kTile, (uint32_t)C::kHalf, 1024u);
+            const uint32_t od = tbase + o_col(u);
+            int g = 0, c = 0, k = 0;
+            bool ok = true;
+            for (;;) {
+                Item8 it;
+                ok = take(u, k, it);
+                if (!ok || it.end) break;
+                if (lane == 0) mbar_arrive(q_free(u, k & 1));
+                ++k;
+                if (u >= it.tiles) {
+                    for (int j = 0; ok && j < it.count; ++j, ++g) {
+                        const int st = g % C::kStages;
+                        ok = wait(v_full(st), (uint32_t)(g / C::kStages) & 1u);
+                        if (ok && lane == 0) mbar_arrive(v_empty(st));
+                        __syncwarp();
+                    }
+                    if (!ok) break;
+                    continue;
+                }
+                for (int j = 0; ok && j < it.count; ++j, ++g, ++c) {
+                    const int b = c % kSB, st = g % C::kStages;
+                    ok = wait(v_full(st), (uint32_t)(g / C::kStages) & 1u);
+                    if (ok) ok = wait(p_full(u, b), (uint32_t)(c / kSB) & 1u);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    if (lane == 0) {
+                        const uint64_t vdesc = tc::desc_add(vdesc0, (uint32_t)(st * C::kStageBytes));
+                        const uint32_t pa0 = tbase + s_col(u, b);
+#pragma unroll
+                        for (int i = 0; i < C::kN / 16; ++i)
+                            tc::mma_f16_ts(od, pa0 + (uint32_t)(8 * i), tc::desc_add(vdesc, 2048u * i), idesc_o, (j > 0 || i > 0) ? 1u : 0u);
+                        tc::mma_commit(o_done(u, b));
+                        tc::mma_commit(v_empty(st));
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+            }
+            if (!ok && lane == 0) set_error(a.err, PA_DEVERR_TIMEOUT);
+            if (lane == 0) tc::mma_commit(drain_p(u));
+            __syncwarp();
+            mbar_wait_bounded(drain_p(u), 0u, kWaitLimit);
+        }
+    } else {
+        // ------------------------------------------------------------ softmax (one row per thread)
+        const int u = (warp - 8) / 4;
+        const int wq = warp & 3;                 // TMEM lanes 32 wq ..
+        const uint32_t tl = tbase + ((uint32_t)(wq * 32) << 16);
+        int g = 0, c = 0, k = 0;
+        bool ok = true;
+        for (;;) {
+            Item8 it;
+            ok = take(u, k, it);
+            if (!ok || it.end) break;
+            const int x = k & 1;
+            ++k;
+            if (u >= it.tiles) {
+                g += it.count;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_free(u, x));
+                continue;
+            }
+            const int R = it.r0 + C::kM * u + 32 * wq + lane, t = R / G;
+            const int pos = t < it.n ? it.len - it.n + t : it.len - 1;
+            float m = -INFINITY, l = 0.f;
+            for (int j = 0; j < it.count; ++j, ++g, ++c) {
+                const int b = c % kSB;
+                ok = wait(s_full(u, b), (uint32_t)(c / kSB) & 1u);
+                if (!ok) break;
+                tc::fence_after_sync();
+                uint32_t sv[2][32];
+                tc::tmem_ld32(tl + s_col(u, b), sv[0]);
+                tc::tmem_ld32(tl + s_col(u, b) + 32u, sv[1]);
+                const uint32_t nt = note(g);
+                const float4 ck4 = lds_f4(nt), lv4 = lds_f4(nt + 16), iv4 = lds_f4(nt + 32);
+                uint32_t boxes;
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(boxes) : "r"(nt + 48));
+                float ck[4] = {ck4.x, ck4.y, ck4.z, ck4.w}, lv[4] = {lv4.x, lv4.y, lv4.z, lv4.w};
+                const float iv[4] = {iv4.x, iv4.y, iv4.z, iv4.w};
+                const int kb = (j < it.ns ? j : j + it.gap) * C::kN;
+                const int lim = pos - kb;                                     // last visible key of the step
+                const int from = a.window > 0 ? lim - a.window + 1 : 0;       // first one of the window
+                tc::tmem_wait_ld();
+                float f[C::kN];
+#pragma unroll
+                for (int i = 0; i < C::kN; ++i) f[i] = __uint_as_float(sv[i >> 5][i & 31]);
+                const bool plain = fminf(fminf(ck[0], ck[1]), fminf(ck[2], ck[3])) >= 0x1p-120f;
+                if (!(__all_sync(0xffffffffu, lim >= C::kN - 1 && (from <= 0 || kb + C::kN <= a.sinks)) && boxes == 15u && plain)) {
+                    // a step on the diagonal, on a window's border, over a block not loaded; a scale that is not positive
+                    const int sk = a.window > 0 ? a.sinks - kb : 0;
+                    uint32_t see[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        see[h] = low_bits(lim + 1 - 32 * h) & (~low_bits(from - 32 * h) | low_bits(sk - 32 * h));
+                        see[h] &= (boxes >> (2 * h) & 1 ? 0xffffu : 0u) | (boxes >> (2 * h + 1) & 1 ? 0xffff0000u : 0u);
+                    }
+#pragma unroll
+                    for (int i = 0; i < C::kN; ++i) {
+                        if (!plain) f[i] = fmaf(f[i], ck[i >> 4], lv[i >> 4]);
+                        if (!(see[i >> 5] >> (i & 31) & 1u)) f[i] = -INFINITY;
+                    }
+                    if (!plain) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) ck[i] = 1.f, lv[i] = 0.f;
+                    }
+                }
+                // the row's maximum: of each box's scores, then scaled
+                float mc = -INFINITY;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float y = max3f(f[16 * q], f[16 * q + 1], f[16 * q + 2]), z = max3f(f[16 * q + 3], f[16 * q + 4], f[16 * q + 5]);
+#pragma unroll
+                    for (int i = 6; i < 14; i += 4) {
+                        y = max3f(y, f[16 * q + i], f[16 * q + i + 1]);
+                        z = max3f(z, f[16 * q + i + 2], f[16 * q + i + 3]);
+                    }
+                    y = max3f(y, f[16 * q + 14], f[16 * q + 15]);
+                    mc = fmaxf(mc, fmaf(fmaxf(y, z), ck[q], lv[q]));
+                }
+                const bool need = mc > m + (8.f + kLift8);
+                const float to = mc - kLift8;
+                const float alpha = (need && j > 0) ? ex2(m - to) : 1.f;
+                if (need) m = to;
+                const float mu = m == -INFINITY ? 0.f : m;
+                uint32_t pw[C::kN / 2];
+                l *= alpha;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float nm = lv[q] - mu;
+                    const uint64_t ck2 = tc::f2(ck[q], ck[q]), nm2 = tc::f2(nm, nm);
+                    uint64_t s0 = 0ull, s1 = 0ull;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int v = 8 * q + i;
+                        const float2 y = tc::f2split(tc::fma2(tc::f2(f[2 * v], f[2 * v + 1]), ck2, nm2));
+                        const float p0 = ex2(y.x), p1 = ex2(y.y);
+                        if (i & 1) s1 = tc::add2(s1, tc::f2(p0, p1));
+                        else s0 = tc::add2(s0, tc::f2(p0, p1));
+                        pw[v] = Mma16<__half>::pack(p0, p1);
+                    }
+                    const float2 s = tc::f2split(tc::add2(s0, s1));
+                    l = fmaf(s.x + s.y, iv[q], l);
+                }
+                // O may be rescaled only once the P V of the step before has landed in it
+                if (j > 0 && __any_sync(0xffffffffu, need)) {
+                    ok = wait(o_done(u, (c - 1) % kSB), (uint32_t)((c - 1) / kSB) & 1u);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+#pragma unroll 1
+                    for (int q = 0; q < D / 16; ++q) {
+                        uint32_t ov[16];
+                        tc::tmem_ld16(tl + o_col(u) + 16u * q, ov);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+                        tc::tmem_st16(tl + o_col(u) + 16u * q, ov);
+                    }
+                    tc::tmem_wait_st();
+                }
+                tc::tmem_st32(tl + s_col(u, b), pw);   // P over the S just read
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full(u, b));
+            }
+            const int last = c - 1;
+            if (ok) ok = wait(o_done(u, last % kSB), (uint32_t)(last / kSB) & 1u);
+            // one decision for the warpgroup
+            ok = group_all(1 + u, ok);
+            if (!ok) break;
+            tc::fence_after_sync();
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const size_t at = ((size_t)(it.qs + t) * a.Hq + it.kvh * G + (R - t * G)) * D;
+#pragma unroll
+            for (int cb = 0; cb < D / 32; ++cb) {
+                uint32_t ov[32];
+                tc::tmem_ld32(tl + o_col(u) + (uint32_t)(32 * cb), ov);
+                tc::tmem_wait_ld();
+                if (t >= it.n) continue;
+                if (a.out16) {
+                    uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at + 32 * cb);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = Mma16<T>::pack(__uint_as_float(ov[8 * i + 2 * e]) * inv, __uint_as_float(ov[8 * i + 2 * e + 1]) * inv);
+                        to[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                } else {
+                    float4 *to = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at + 32 * cb);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        to[i] = make_float4(__uint_as_float(ov[4 * i]) * inv, __uint_as_float(ov[4 * i + 1]) * inv,
+                                            __uint_as_float(ov[4 * i + 2]) * inv, __uint_as_float(ov[4 * i + 3]) * inv);
+                }
+            }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_free(u, x));
+        }
+        if (!ok && lane == 0) set_error(a.err, PA_DEVERR_TIMEOUT);
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 0) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tbase, C::kTmemCols);
+    }
+}
+
+template <typename T, int D, int MT>
+cudaError_t launch_umma8_t(const Attend8Args &a, const CUtensorMap &tmq, cudaStream_t st) {
+    using C = Umma8Cfg<D, MT>;
+    static std::atomic<int> sms_of[kMaxLaunchDevices];
+    int sms = 0;
+    cudaError_t e = per_device_value(sms_of, &sms, [](int dev, int *v) {
+        cudaError_t r = cudaFuncSetAttribute(attend8_umma_kernel<T, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+        if (r != cudaSuccess) return r;
+        return cudaDeviceGetAttribute(v, cudaDevAttrMultiProcessorCount, dev);
+    });
+    if (e != cudaSuccess) return e;
+    const long long rows = (long long)a.max_query_len * (a.Hq / a.Hkv);
+    const long long work = (rows + C::kM * MT - 1) / (C::kM * MT) * a.S * a.Hkv;
+    if (work > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const long long ctas = work < sms ? work : sms;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(ctas > 0 ? ctas : 1));
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attend8_umma_kernel<T, D, MT>, a, tmq);
+}
+
+template <typename T>
+cudaError_t dispatch_umma8(const Attend8Args &a, const CUtensorMap &tmq, cudaStream_t st) {
+    if (a.D == 64) return a.tiles == 2 ? launch_umma8_t<T, 64, 2>(a, tmq, st) : launch_umma8_t<T, 64, 1>(a, tmq, st);
+    return a.tiles == 2 ? launch_umma8_t<T, 128, 2>(a, tmq, st) : launch_umma8_t<T, 128, 1>(a, tmq, st);
+}
+
+}  // namespace pa

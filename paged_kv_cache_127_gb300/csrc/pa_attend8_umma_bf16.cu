@@ -1,0 +1,10 @@
+// pa_attend8_umma_bf16.cu -- long chunks over the 8-bit cache, bf16 queries.
+#include "pa_attend8_umma.cuh"
+
+namespace pa {
+
+cudaError_t launch_attend8_umma_bf16(const Attend8Args &a, const CUtensorMap &tmq, cudaStream_t st) {
+    return dispatch_umma8<__nv_bfloat16>(a, tmq, st);
+}
+
+}  // namespace pa

@@ -54,6 +54,7 @@ struct Attend8Args {
     int window, sinks;              // window 0: none
     int out16;
     int units;                      // mma.sync path: warps that take a share of the keys
+    int tiles;                      // tcgen05 path: 128-row tiles of an item (1 or 2)
     float scale;
 };
 // mma.sync path, and the join of its parts: row blocks of 16 * row_tiles rows of a KV head (0: 8 rows, a decode).
@@ -65,7 +66,9 @@ cudaError_t launch_attend8_mma_f16(const Attend8Args &a, int row_tiles, const CU
 cudaError_t launch_attend8_mma_bf16(const Attend8Args &a, int row_tiles, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
 // A cache of codes [N, Hkv, B, D]: boxes of one (block, KV head), rows of D bytes with the swizzle of that width.
 cudaError_t make_codes_tensor_map(CUtensorMap *map, const void *codes, int D, int B, long long block_heads);
-// tcgen05 path.
-cudaError_t launch_attend8_umma(const Attend8Args &a, bool bf16, cudaStream_t st);
+// tcgen05 path, from 64 rows of a KV head on: the work list, and the kernel (tmq: the queries' map).
+cudaError_t launch_attend8_plan(const Attend8Args &a, cudaStream_t st);
+cudaError_t launch_attend8_umma_f16(const Attend8Args &a, const CUtensorMap &tmq, cudaStream_t st);
+cudaError_t launch_attend8_umma_bf16(const Attend8Args &a, const CUtensorMap &tmq, cudaStream_t st);
 
 }  // namespace pa

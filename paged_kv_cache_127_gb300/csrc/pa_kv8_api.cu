@@ -57,7 +57,7 @@ int32_t check_window(const pa_window *w) { return w && (w->window < 0 || w->sink
 // Workspace, each part 256-byte aligned: a header, the notes of each (sequence, KV head, row block), and two parts
 // for each warp that shares the keys (mma.sync path).
 struct Layout8 {
-    int row_tiles, units;
+    int row_tiles, units, tiles;  // tiles 0: the mma.sync path
     size_t list, parts, total;
 };
 Layout8 layout8(const pa_dims *d, int row_tiles, int32_t max_q) {
@@ -77,7 +77,14 @@ Layout8 layout8(const pa_dims *d, int row_tiles, int32_t max_q) {
 }
 Layout8 decode_layout8(const pa_dims *d) { return layout8(d, 0, 1); }
 Layout8 chunk_layout8(const pa_dims *d, int32_t max_q) {
-    return layout8(d, pa::attend8_row_tiles(max_q, d->num_q_heads / d->num_kv_heads), max_q);
+    const int G = d->num_q_heads / d->num_kv_heads;
+    if (!pa::chunk_uses_umma(max_q, G)) return layout8(d, pa::attend8_row_tiles(max_q, G), max_q);
+    Layout8 L{};   // a header and the work list
+    L.tiles = pa::chunk_umma_rows(max_q, G) / 128;
+    L.list = 256;
+    const int64_t groups = ((int64_t)max_q * G + 128 * L.tiles - 1) / (128 * L.tiles);
+    L.total = L.list + up256((size_t)(groups * d->num_seqs) * sizeof(int4));
+    return L;
 }
 
 // The tensor maps of the caches, re-encoded only when a cache or its shape changes (per host thread).
@@ -125,6 +132,7 @@ void fill8(pa::Attend8Args &a, const pa_dims *d, const pa_window *w, const void 
     a.list = reinterpret_cast<int4 *>(ws + L.list);
     a.parts = reinterpret_cast<float *>(ws + L.parts);
     a.units = L.units;
+    a.tiles = L.tiles;
     a.S = d->num_seqs;
     a.Hq = d->num_q_heads;
     a.Hkv = d->num_kv_heads;
@@ -147,6 +155,19 @@ int32_t run_mma(pa::Attend8Args &a, const pa_dims *d, const Layout8 &L, void *st
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return to_status(d->kv_dtype == PA_BF16 ? pa::launch_attend8_mma_bf16(a, L.row_tiles, tmk, tmv, st)
                                             : pa::launch_attend8_mma_f16(a, L.row_tiles, tmk, tmv, st));
+}
+
+int32_t run_umma(pa::Attend8Args &a, const pa_dims *d, void *stream) {
+    a.err = pa::device_error_word();
+    if (!a.err) return PA_ERR_CUDA;
+    const bool bf16 = d->kv_dtype == PA_BF16;
+    CUtensorMap tmq;
+    cudaError_t e = pa::cached_query_map(a.q, bf16, a.D, a.Hq, a.T, a.Hq / a.Hkv, &tmq);
+    if (e != cudaSuccess) return PA_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    e = pa::launch_attend8_plan(a, st);
+    if (e == cudaSuccess) e = bf16 ? pa::launch_attend8_umma_bf16(a, tmq, st) : pa::launch_attend8_umma_f16(a, tmq, st);
+    return to_status(e);
 }
 
 void fill_write8(pa::Write8Args &a, const pa_dims *d, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
@@ -293,7 +314,7 @@ int32_t pa_chunk8(const pa_dims *dims, const pa_window *window, const void *q, c
     a.query_start = query_start;
     a.T = num_tokens;
     a.max_query_len = max_query_len;
-    return run_mma(a, dims, L, stream);
+    return L.tiles ? run_umma(a, dims, stream) : run_mma(a, dims, L, stream);
 }
 
 }  // extern "C"
