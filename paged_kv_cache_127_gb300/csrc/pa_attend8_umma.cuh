@@ -5,12 +5,14 @@
 // Work: an item is (MT 128-row tiles, KV head, sequence), row r = token r / G, head r % G; its CTA walks the keys
 // that some of its rows see in steps of 64, with no split and no merge.  Persistent CTAs, one per SM, claim items from
 // a longest-first list.  Warps:
-//   0, 1       issue tile 0's and tile 1's  S_u = Q_u K^T  (M 128, N 64, K = D)
+//   0, 1       send for tile 0's and tile 1's queries (TMA) and issue  S_u = Q_u K^T  (M 128, N 64, K = D)
 //   2, 3       issue their  O_u += P_u V    (M 128, N = D, K = 64), P from TMEM
-//   4 .. 7     converters: read the codes of a step (16 bytes a lane, a step ahead), turn them into 16-bit floats (K
-//              into the queries' type, V into f16; both exact) and store them as the swizzled operands; they also
-//              claim the items, send for the query tiles (TMA) and publish each step's scales
-//   8 ..       one softmax warpgroup per tile, one thread per row
+//   4 .. 11    converters, a warpgroup for K and one for V, each warp with one 16-key box of every step: it sends for its
+//              box's codes four steps ahead (one bulk copy), turns them into 16-bit floats (K into the queries' type, V
+//              into f16; both exact) and stores them as the swizzled operands; K's also publish the box's scales, and warp 4
+//              claims the items.  (Loads into registers instead, however far ahead, are waited for by the next arrive,
+//              which releases: 341 us against ## on 16 x 512-token chunks.)
+//   12 ..      one softmax warpgroup per tile, one thread per row
 // Converting once per step serves both tiles, and the codes' 16-bit form never leaves the SM.  The alternative, e4m3
 // operands with Q and P split in two terms each, would need as many products, and the split of P in the softmax
 // costs it more instructions than the whole conversion takes here.
@@ -42,30 +44,36 @@ struct Umma8Cfg {
     static constexpr int kSub = D / 64;                    // 128-byte halves of an operand row
     static constexpr int kKS = D / 16;                     // k-steps of S = Q K^T
     static constexpr int kStages = 3;
-    static constexpr int kThreads = 32 * (8 + 4 * MT);
+    static constexpr int kThreads = 32 * (12 + 4 * MT);
+    // two tiles: 640 threads are launched at 96 registers; the issuers keep 40, the converters 72, the softmax gets 144
+    // (4 x 40 + 8 x 72 + 8 x 144 < 20 x 96)
+    static constexpr bool kRegSplit = MT == 2;
     static constexpr int kHalf = kN * 128;                 // one half of K (or V) of a step
     static constexpr int kTile = kSub * kHalf;             // K (or V) of a step
     static constexpr int kStageBytes = 2 * kTile;
     static constexpr int kQHalf = kM * 128;
     static constexpr int kQTile = kSub * kQHalf;
-    // scales and loaded boxes of the last kNotes steps: a step's are written once S of kStages steps before is done,
-    // so once tile 0's P V of kSB steps before that is, whose V came when both tiles' P V had released that of kStages
-    // before: every tile has read what lies 2 kStages + kSB steps back
+    // scales of the last kNotes steps.  Those of step g + kRaw are written while step g is converted, so once S of
+    // g - kStages is done, so once tile 0's P V of kSB steps before that is, whose V came when both tiles' P V had
+    // released that of kStages before: every tile has read what lies 2 kStages + kSB steps back from g
     static constexpr int kNotes = 16;
-    static constexpr int kNoteBytes = 4 * 4 * kBoxes;      // ck, lv, ivs per box, the mask
-    static constexpr size_t kKVOff = (size_t)2 * MT * kQTile;
-    static constexpr size_t kNoteOff = kKVOff + (size_t)kStages * kStageBytes;
-    static constexpr size_t kItemOff = kNoteOff + (size_t)kNotes * kNoteBytes;   // per tile and set: 16 ints
+    static constexpr int kNoteBytes = 4 * 4 * kBoxes;      // per box: ck, lv, 1 / vs, whether it is there
+    static constexpr int kRaw = 4;                         // steps of codes in flight
+    static constexpr int kBoxBytes = 16 * D;               // a box's codes
+    static constexpr size_t kKVOff = (size_t)MT * kQTile;
+    static constexpr size_t kRawOff = kKVOff + (size_t)kStages * kStageBytes;    // per converter warp kRaw boxes
+    static constexpr size_t kNoteOff = kRawOff + (size_t)8 * kRaw * kBoxBytes;
+    static constexpr size_t kItemOff = kNoteOff + (size_t)kNotes * kNoteBytes;   // per tile two items of 16 ints
     static constexpr size_t kBarOff = kItemOff + (size_t)MT * 2 * 64;
-    // k_full, k_empty, v_full, v_empty [kStages] | per tile: s_full, p_full, o_done [kSB], q_full [2], q_free [2],
-    // item_ready [2], drain_s, drain_p
+    // k_full, k_empty, v_full, v_empty [kStages] | raw_full [8 warps][kRaw] | per tile: s_full, p_full, o_done [kSB],
+    // item_free [2], item_ready [2], q_full, q_done, drain_s, drain_p
     static constexpr int kTileBars = 3 * kSB + 8;
-    static constexpr int kNumBars = 4 * kStages + MT * kTileBars;
+    static constexpr int kNumBars = 4 * kStages + 8 * kRaw + MT * kTileBars;
     static constexpr size_t kSlotOff = kBarOff + 8 * kNumBars;
     static constexpr size_t kSmem = kSlotOff + 16 + 1024;  // + alignment slack
     static constexpr uint32_t kTmemCols = 256 * MT;
     static constexpr uint32_t kOCol = 128 * MT;            // S[u][b] at 128 u + kN b; O[u] at kOCol + D u; P over its S
-    static_assert(2 * kStages + kSB <= kNotes, "a note must outlive its readers");
+    static_assert(2 * kStages + kSB + kRaw <= kNotes, "a note must outlive its readers");
     static_assert(kOCol + MT * D <= kTmemCols, "TMEM budget");
     static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
@@ -125,11 +133,6 @@ __device__ __forceinline__ void widen16(const uint4 &w, uint4 &x, uint4 &y) {
 __device__ __forceinline__ void sts128(uint32_t at, const uint4 &x) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
 }
-__device__ __forceinline__ uint4 ldg_codes(const uint8_t *p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
-}
 __device__ __forceinline__ float4 lds_f4(uint32_t at) {
     float4 v;
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
@@ -173,13 +176,15 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
     auto k_empty = [&](int i) { return bars + 8u * (uint32_t)(C::kStages + i); };
     auto v_full = [&](int i) { return bars + 8u * (uint32_t)(2 * C::kStages + i); };
     auto v_empty = [&](int i) { return bars + 8u * (uint32_t)(3 * C::kStages + i); };
-    auto tbar = [&](int u, int i) { return bars + 8u * (uint32_t)(4 * C::kStages + u * C::kTileBars + i); };
+    auto raw_full = [&](int w, int i) { return bars + 8u * (uint32_t)(4 * C::kStages + w * C::kRaw + i); };
+    auto tbar = [&](int u, int i) { return bars + 8u * (uint32_t)(4 * C::kStages + 8 * C::kRaw + u * C::kTileBars + i); };
     auto s_full = [&](int u, int b) { return tbar(u, b); };
     auto p_full = [&](int u, int b) { return tbar(u, kSB + b); };
     auto o_done = [&](int u, int b) { return tbar(u, 2 * kSB + b); };  // P V done: O is up to date, S/P[u][b] is free
-    auto q_full = [&](int u, int x) { return tbar(u, 3 * kSB + x); };
-    auto q_free = [&](int u, int x) { return tbar(u, 3 * kSB + 2 + x); };
-    auto item_ready = [&](int u, int x) { return tbar(u, 3 * kSB + 4 + x); };
+    auto item_free = [&](int u, int x) { return tbar(u, 3 * kSB + x); };
+    auto item_ready = [&](int u, int x) { return tbar(u, 3 * kSB + 2 + x); };
+    auto q_full = [&](int u) { return tbar(u, 3 * kSB + 4); };
+    auto q_done = [&](int u) { return tbar(u, 3 * kSB + 5); };   // the S MMAs of an item are complete
     auto drain_s = [&](int u) { return tbar(u, 3 * kSB + 6); };
     auto drain_p = [&](int u) { return tbar(u, 3 * kSB + 7); };
     Item8 *slots = reinterpret_cast<Item8 *>(basep + C::kItemOff);
@@ -190,7 +195,7 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
         if (got) out = slot(u, k & 1);
         return got;
     };
-    auto qtile = [&](int x, int u) { return base + (uint32_t)((x * MT + u) * C::kQTile); };
+    auto qtile = [&](int u) { return base + (uint32_t)(u * C::kQTile); };
     auto s_col = [&](int u, int b) { return (uint32_t)(128 * u + C::kN * b); };
     auto o_col = [&](int u) { return C::kOCol + (uint32_t)(D * u); };
     auto note = [&](int g) { return base + (uint32_t)(C::kNoteOff + (size_t)(g % C::kNotes) * C::kNoteBytes); };
@@ -203,6 +208,8 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
             mbar_init(v_full(i), 4);
             mbar_init(v_empty(i), MT);  // likewise from each tile's P V issuer
         }
+        for (int w = 0; w < 8; ++w)
+            for (int i = 0; i < C::kRaw; ++i) mbar_init(raw_full(w, i), 1);
         for (int u = 0; u < MT; ++u) {
             for (int b = 0; b < kSB; ++b) {
                 mbar_init(s_full(u, b), 1);
@@ -210,10 +217,11 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
                 mbar_init(o_done(u, b), 1);
             }
             for (int x = 0; x < 2; ++x) {
-                mbar_init(q_full(u, x), 1);
-                mbar_init(q_free(u, x), 4 + 2);  // the softmax warps, and both issuers once they have read the slot
+                mbar_init(item_free(u, x), 4 + 2);  // the softmax warps, and both issuers once they have read it
                 mbar_init(item_ready(u, x), 1);
             }
+            mbar_init(q_full(u), 1);
+            mbar_init(q_done(u), 1);
             mbar_init(drain_s(u), 1);
             mbar_init(drain_p(u), 1);
         }
@@ -228,23 +236,30 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
     griddep_wait();  // the plan's list, longest first
     const int nwork = max(0, a.hdr[0]) * a.Hkv;
 
-    if (warp >= 4 && warp < 8) {
-        // ------------------------------------------------------------ converters
-        constexpr int kLanes = D / 16;                 // threads of a key's row, 16 codes each
-        constexpr int kPass = 128 / kLanes;            // rows of a pass
-        constexpr int kP = C::kN / kPass;              // passes: 4 (D 128) or 2
-        const int ct = threadIdx.x - 128;              // 0 .. 127
-        const int row = ct / kLanes, ch = ct % kLanes;
+    // The converters of K or of V: warp w of the group has box w of every step.
+    auto convert = [&](auto of_v) {
+        constexpr bool kV = decltype(of_v)::value;
+        constexpr int kLanes = D / 16;                 // lanes of a key's row, 16 codes each
+        constexpr int kPass = 32 / kLanes;             // rows of a pass
+        constexpr int kP = 16 / kPass;                 // passes: 4 (D 128) or 2
+        const int box = warp & 3, row = lane / kLanes, ch = lane % kLanes;
         const int lb = __ffs(a.B) - 1;
-        const uint64_t qpol = policy_evict_first();
+        const bool first = !kV && box == 0;            // claims the items
         // a row's two 16-byte chunks of its swizzled operand; the second half's lanes store theirs in the other
         // order, which keeps a store free of bank conflicts
         const bool flip = (ch & 4) != 0;
+        const uint8_t *cache = kV ? a.v_cache : a.k_cache;
+        auto full = [&](int i) { return kV ? v_full(i) : k_full(i); };
+        auto empty = [&](int i) { return kV ? v_empty(i) : k_empty(i); };
+        auto got = [&](int i) { return raw_full(warp - 4, i); };
+        const uint32_t ring = kvb + (kV ? (uint32_t)C::kTile : 0u) + (uint32_t)((ch >> 2) * C::kHalf + (16 * box + row) * 128);
+        const uint32_t raw0 = base + (uint32_t)(C::kRawOff + (size_t)(warp - 4) * C::kRaw * C::kBoxBytes);
         int g = 0, k = 0;
+        uint32_t there = 0;                            // bit i: raw slot i holds a box
         bool ok = true;
         for (;;) {
             Item8 it;
-            if (warp == 4) {
+            if (first) {
                 int w = blockIdx.x;  // a CTA's first item needs no claim
                 if (k > 0) {
                     if (lane == 0) w = (int)gridDim.x + atomicAdd(&a.hdr[1], 1);
@@ -254,19 +269,10 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
                 const int x = k & 1;
 #pragma unroll 1
                 for (int u = 0; ok && u < MT; ++u) {
-                    if (k >= 2) ok = wait(q_free(u, x), (uint32_t)((k >> 1) - 1) & 1u);
+                    if (k >= 2) ok = wait(item_free(u, x), (uint32_t)((k >> 1) - 1) & 1u);
                     if (ok && lane == 0) {
                         slot(u, x) = it;
                         mbar_arrive(item_ready(u, x));
-                        if (have && u >= it.tiles) {
-                            mbar_arrive(q_full(u, x));  // no query tile: keep the set's phases in step
-                        } else if (have) {
-                            mbar_arrive_expect_tx(q_full(u, x), (uint32_t)C::kQTile);
-#pragma unroll
-                            for (int sb = 0; sb < C::kSub; ++sb)
-                                tma_load_3d(qtile(x, u) + (uint32_t)(sb * C::kQHalf), &tmq, sb * 64, it.kvh * G,
-                                            it.qs + (it.r0 + C::kM * u) / G, q_full(u, x), qpol);
-                        }
                     }
                     __syncwarp();
                 }
@@ -277,126 +283,108 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
                 if (!ok || it.end) break;
             }
             const int32_t *table = a.block_tables + (size_t)it.s * a.max_blocks;
-            auto key_of = [&](int j) { return (j < it.ns ? j : j + it.gap) * C::kN; };
-            auto wanted = [&](int key) { return key < it.hi && (key >= it.lo || key < a.sinks); };
-            // the block ids of step j's rows (-2: not wanted), and of box `lane`
-            int id[kP], box_id = -2;
-            auto look = [&](int j) {
-                const int kb = key_of(j);
-#pragma unroll
-                for (int i = 0; i < kP; ++i) {
-                    const int key = kb + row + kPass * i;
-                    id[i] = wanted(key) ? table[key >> lb] : -2;
-                }
-                if (warp == 4) {
-                    const int b0 = kb + 16 * lane;
-                    const bool any = lane < C::kBoxes && b0 < it.hi && (b0 + 15 >= it.lo || b0 < a.sinks);
-                    box_id = any ? table[b0 >> lb] : -2;
-                }
-            };
-            auto offset_of = [&](int i, int j) {   // of this thread's codes, or -1
-                if (id[i] < 0 || id[i] >= a.N) return (long long)-1;
-                const int key = key_of(j) + row + kPass * i;
-                return (((long long)id[i] * a.Hkv + it.kvh) * a.B + (key & (a.B - 1))) * D + 16 * ch;
-            };
-            uint4 kw[kP], vw[kP];
+            auto box_key = [&](int j) { return (j < it.ns ? j : j + it.gap) * C::kN + 16 * box; };
+            int id = -2;                               // lane l: the block of step 32 n + l (-2: no row sees it)
             float ks = 1.f, vs = 1.f;
-            bool good = false;
-            auto load = [&](const uint8_t *cache, uint4 (&w)[kP], int j) {
-#pragma unroll
-                for (int i = 0; i < kP; ++i) {
-                    const long long at = offset_of(i, j);
-                    w[i] = at >= 0 ? ldg_codes(cache + at) : make_uint4(0, 0, 0, 0);
-                }
-            };
-            auto load_scales = [&]() {
-                good = box_id >= 0 && box_id < a.N;
-                ks = vs = 1.f;
-                if (good) {
-                    ks = a.k_scales[(size_t)box_id * a.Hkv + it.kvh];
-                    vs = a.v_scales[(size_t)box_id * a.Hkv + it.kvh];
-                } else if (box_id != -2) {
-                    set_error(a.err, PA_DEVERR_BAD_BLOCK);
-                }
-            };
-            auto store = [&](uint32_t tile, int i, const uint4 &x, const uint4 &y) {
-                const int r = row + kPass * i;
-                const uint32_t at = tile + (uint32_t)((ch >> 2) * C::kHalf + r * 128);
-                const uint32_t c0 = (uint32_t)((2 * (ch & 3)) ^ (r & 7)) << 4, c1 = (uint32_t)((2 * (ch & 3) + 1) ^ (r & 7)) << 4;
-                sts128(at + (flip ? c1 : c0), flip ? y : x);
-                sts128(at + (flip ? c0 : c1), flip ? x : y);
-            };
-            look(0);
-            load(a.k_cache, kw, 0);
-            load(a.v_cache, vw, 0);
-            if (warp == 4) load_scales();
-            if (it.count > 1) look(1);
-            for (int j = 0; j < it.count; ++j, ++g) {
-                const int st = g % C::kStages;
-                const uint32_t par = (uint32_t)((g / C::kStages) - 1) & 1u;
-                const uint32_t ktile = kvb + (uint32_t)(st * C::kStageBytes), vtile = ktile + C::kTile;
-                if (g >= C::kStages) ok = wait(k_empty(st), par);
-                if (!ok) break;
-                if (warp == 4) {
-                    const uint32_t mask = __ballot_sync(0xffffffffu, good) & ((1u << C::kBoxes) - 1u);
-                    if (lane < C::kBoxes) {
-                        const uint32_t at = note(g) + 4 * lane;
-                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(ks * a.scale * kLog2e8) : "memory");
-                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 4 * C::kBoxes), "f"(lg2(vs)) : "memory");
-                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 8 * C::kBoxes), "f"(1.f / vs) : "memory");
-                        if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 12 * C::kBoxes), "r"(mask) : "memory");
+            // step j's box on its way, and its note (K)
+            auto send = [&](int j, int n) {            // n: the step's number in the ring
+                if ((j & 31) == 0) {
+                    const int b0 = box_key(j + lane);
+                    id = -2;
+                    if (j + lane < it.count && b0 < it.hi && (b0 + 15 >= it.lo || b0 < a.sinks)) id = table[b0 >> lb];
+                    if (!kV) {
+                        ks = vs = 1.f;
+                        if ((unsigned)id < (unsigned)a.N) {
+                            ks = a.k_scales[(size_t)id * a.Hkv + it.kvh];
+                            vs = a.v_scales[(size_t)id * a.Hkv + it.kvh];
+                        } else if (id != -2) {
+                            set_error(a.err, PA_DEVERR_BAD_BLOCK);
+                        }
                     }
                 }
-#pragma unroll
-                for (int i = 0; i < kP; ++i) {
-                    uint4 x, y;
-                    widen16<T>(kw[i], x, y);
-                    store(ktile, i, x, y);
+                const int pb = __shfl_sync(0xffffffffu, id, j & 31), i = n % C::kRaw;
+                const bool good = (unsigned)pb < (unsigned)a.N;
+                if (!kV) {
+                    const float k1 = __shfl_sync(0xffffffffu, ks, j & 31), v1 = __shfl_sync(0xffffffffu, vs, j & 31);
+                    if (lane == 0) {
+                        const uint32_t at = note(n) + 4 * box;
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(k1 * a.scale * kLog2e8) : "memory");
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 16), "f"(lg2(v1)) : "memory");
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 32), "f"(1.f / v1) : "memory");
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 48), "r"(good ? ~0u : 0u) : "memory");
+                    }
                 }
-                tc::fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(k_full(st));
-                if (j + 1 < it.count) load(a.k_cache, kw, j + 1);
-                if (g >= C::kStages) ok = wait(v_empty(st), par);
+                if (good) there |= 1u << i;
+                else there &= ~(1u << i);
+                if (good && lane == 0) {
+                    const size_t at = (((size_t)pb * a.Hkv + it.kvh) * a.B + (box_key(j) & (a.B - 1))) * D;
+                    mbar_arrive_expect_tx(got(i), C::kBoxBytes);
+                    bulk_g2s(raw0 + (uint32_t)(i * C::kBoxBytes), cache + at, C::kBoxBytes, got(i));
+                } else if (lane == 0) {
+                    mbar_arrive(got(i));
+                }
+            };
+#pragma unroll 1
+            for (int j = 0; j < min(C::kRaw, it.count); ++j) send(j, g + j);
+#pragma unroll 1
+            for (int j = 0; j < it.count; ++j, ++g) {
+                const int st = g % C::kStages, i = g % C::kRaw;
+                ok = wait(got(i), (uint32_t)(g / C::kRaw) & 1u);
+                if (ok && g >= C::kStages) ok = wait(empty(st), (uint32_t)((g / C::kStages) - 1) & 1u);
                 if (!ok) break;
+                const int kb = box_key(j);
+                const bool good = there >> i & 1u;
 #pragma unroll
-                for (int i = 0; i < kP; ++i) {
-                    uint4 x, y;
-                    widen16<__half>(vw[i], x, y);
-                    store(vtile, i, x, y);
+                for (int n = 0; n < kP; ++n) {
+                    const int r = row + kPass * n;
+                    uint4 w = lds128(raw0 + (uint32_t)(i * C::kBoxBytes + n * 512 + lane * 16)), x, y;
+                    if constexpr (kV) {
+                        // a key that no row of the item sees may hold anything
+                        if (!(good && kb + r < it.hi && (kb + r >= it.lo || kb + r < a.sinks))) w = make_uint4(0, 0, 0, 0);
+                        widen16<__half>(w, x, y);
+                    } else {
+                        widen16<T>(w, x, y);
+                    }
+                    const uint32_t at = ring + (uint32_t)(st * C::kStageBytes + kPass * n * 128), sw = (uint32_t)(r & 7);
+                    const uint32_t c0 = ((uint32_t)(2 * (ch & 3)) ^ sw) << 4, c1 = ((uint32_t)(2 * (ch & 3) + 1) ^ sw) << 4;
+                    sts128(at + (flip ? c1 : c0), flip ? y : x);
+                    sts128(at + (flip ? c0 : c1), flip ? x : y);
                 }
                 tc::fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(v_full(st));
-                if (j + 1 < it.count) {
-                    load(a.v_cache, vw, j + 1);
-                    if (warp == 4) load_scales();
-                    if (j + 2 < it.count) look(j + 2);
-                }
+                __syncwarp();  // every lane has read the raw box and stored its part
+                if (lane == 0) mbar_arrive(full(st));
+                if (j + C::kRaw < it.count) send(j + C::kRaw, g + C::kRaw);
             }
-            if (!ok) break;
+            if (!ok) {  // copies still in flight must land before the CTA's shared memory is released
+                for (int n = g; n < g + C::kRaw; ++n) mbar_wait_bounded(got(n % C::kRaw), (uint32_t)(n / C::kRaw) & 1u, 1u << 16);
+                break;
+            }
         }
         if (!ok && lane == 0) set_error(a.err, PA_DEVERR_TIMEOUT);
-        // query tiles still in flight must land before the CTA's shared memory is released
-        if (warp == 4 && !ok)
-            for (int u = 0; u < MT; ++u)
-                for (int n = max(0, k - 2); n < k; ++n) mbar_wait_bounded(q_full(u, n & 1), (uint32_t)(n >> 1) & 1u, 1u << 16);
+    };
+
+    if (warp >= 4 && warp < 12) {
+        // ------------------------------------------------------------ converters: K (warps 4-7), V (8-11)
+        if constexpr (C::kRegSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n" ::: "memory");
+        if (warp < 8) convert(std::integral_constant<bool, false>());
+        else convert(std::integral_constant<bool, true>());
     } else if (warp < 2) {
         // ------------------------------------------------------------ S = Q K^T issuer of tile u
         const int u = warp;
+        if constexpr (C::kRegSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n" ::: "memory");
         if (u < MT) {
             constexpr uint32_t idesc_s = tc::f16_idesc(kBf16, false, C::kM, C::kN);
             const uint64_t kdesc0 = tc::sw128_desc(kvb, 16u, 1024u);
-            int g = 0, c = 0, k = 0;
+            const uint64_t qpol = policy_evict_first();
+            const uint64_t qdesc = tc::sw128_desc(qtile(u), 16u, 1024u);
+            int g = 0, c = 0, k = 0, nq = 0;  // nq: items with rows in this tile
             bool ok = true;
             for (;;) {
                 Item8 it;
                 ok = take(u, k, it);
                 if (!ok || it.end) break;
-                const int x = k & 1;
-                const uint32_t qpar = (uint32_t)(k >> 1) & 1u;
+                if (lane == 0) mbar_arrive(item_free(u, k & 1));  // done with the slot
                 ++k;
-                if (lane == 0) mbar_arrive(q_free(u, x));  // done with the slot
                 if (u >= it.tiles) {
                     for (int j = 0; ok && j < it.count; ++j, ++g) {
                         const int st = g % C::kStages;
@@ -407,8 +395,19 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
                     if (!ok) break;
                     continue;
                 }
-                ok = wait(q_full(u, x), qpar);
-                const uint64_t qdesc = tc::sw128_desc(qtile(x, u), 16u, 1024u);
+                // the query tile, once the MMAs of the last one are complete: rows r0 + 128 u .., G heads of a token at
+                // a time; rows of tokens past the chunk are never used
+                if (nq > 0) ok = wait(q_done(u), (uint32_t)(nq - 1) & 1u);
+                if (ok && lane == 0) {
+                    mbar_arrive_expect_tx(q_full(u), (uint32_t)C::kQTile);
+#pragma unroll
+                    for (int sb = 0; sb < C::kSub; ++sb)
+                        tma_load_3d(qtile(u) + (uint32_t)(sb * C::kQHalf), &tmq, sb * 64, it.kvh * G, it.qs + (it.r0 + C::kM * u) / G,
+                                    q_full(u), qpol);
+                }
+                __syncwarp();
+                if (ok) ok = wait(q_full(u), (uint32_t)nq & 1u);
+                ++nq;
                 for (int j = 0; ok && j < it.count; ++j, ++g, ++c) {
                     const int st = g % C::kStages, b = c % kSB;
                     ok = wait(k_full(st), (uint32_t)(g / C::kStages) & 1u);
@@ -424,6 +423,7 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
                                            tc::desc_add(kdesc, (uint32_t)((i >> 2) * C::kHalf + 32 * (i & 3))), idesc_s, i > 0 ? 1u : 0u);
                         tc::mma_commit(s_full(u, b));
                         tc::mma_commit(k_empty(st));
+                        if (j + 1 == it.count) tc::mma_commit(q_done(u));
                     }
                     __syncwarp();
                 }
@@ -438,6 +438,7 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
     } else if (warp < 4) {
         // ------------------------------------------------------------ O += P V issuer of tile u
         const int u = warp - 2;
+        if constexpr (C::kRegSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n" ::: "memory");
         if (u < MT) {
             constexpr uint32_t idesc_o = tc::f16_idesc(false, true, C::kM, D);
             const uint64_t vdesc0 = tc::sw128_desc(kvb + (uint32_t)C::kTile, (uint32_t)C::kHalf, 1024u);
@@ -448,7 +449,7 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
                 Item8 it;
                 ok = take(u, k, it);
                 if (!ok || it.end) break;
-                if (lane == 0) mbar_arrive(q_free(u, k & 1));
+                if (lane == 0) mbar_arrive(item_free(u, k & 1));
                 ++k;
                 if (u >= it.tiles) {
                     for (int j = 0; ok && j < it.count; ++j, ++g) {
@@ -486,7 +487,8 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
         }
     } else {
         // ------------------------------------------------------------ softmax (one row per thread)
-        const int u = (warp - 8) / 4;
+        if constexpr (C::kRegSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 144;\n" ::: "memory");
+        const int u = (warp - 12) / 4;
         const int wq = warp & 3;                 // TMEM lanes 32 wq ..
         const uint32_t tl = tbase + ((uint32_t)(wq * 32) << 16);
         int g = 0, c = 0, k = 0;
@@ -500,7 +502,7 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
             if (u >= it.tiles) {
                 g += it.count;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(q_free(u, x));
+                if (lane == 0) mbar_arrive(item_free(u, x));
                 continue;
             }
             const int R = it.r0 + C::kM * u + 32 * wq + lane, t = R / G;
@@ -516,8 +518,7 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
                 tc::tmem_ld32(tl + s_col(u, b) + 32u, sv[1]);
                 const uint32_t nt = note(g);
                 const float4 ck4 = lds_f4(nt), lv4 = lds_f4(nt + 16), iv4 = lds_f4(nt + 32);
-                uint32_t boxes;
-                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(boxes) : "r"(nt + 48));
+                const uint4 bx = lds128(nt + 48);
                 float ck[4] = {ck4.x, ck4.y, ck4.z, ck4.w}, lv[4] = {lv4.x, lv4.y, lv4.z, lv4.w};
                 const float iv[4] = {iv4.x, iv4.y, iv4.z, iv4.w};
                 const int kb = (j < it.ns ? j : j + it.gap) * C::kN;
@@ -528,14 +529,14 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < C::kN; ++i) f[i] = __uint_as_float(sv[i >> 5][i & 31]);
                 const bool plain = fminf(fminf(ck[0], ck[1]), fminf(ck[2], ck[3])) >= 0x1p-120f;
-                if (!(__all_sync(0xffffffffu, lim >= C::kN - 1 && (from <= 0 || kb + C::kN <= a.sinks)) && boxes == 15u && plain)) {
+                if (!(__all_sync(0xffffffffu, lim >= C::kN - 1 && (from <= 0 || kb + C::kN <= a.sinks)) && (bx.x & bx.y & bx.z & bx.w) && plain)) {
                     // a step on the diagonal, on a window's border, over a block not loaded; a scale that is not positive
                     const int sk = a.window > 0 ? a.sinks - kb : 0;
                     uint32_t see[2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         see[h] = low_bits(lim + 1 - 32 * h) & (~low_bits(from - 32 * h) | low_bits(sk - 32 * h));
-                        see[h] &= (boxes >> (2 * h) & 1 ? 0xffffu : 0u) | (boxes >> (2 * h + 1) & 1 ? 0xffff0000u : 0u);
+                        see[h] &= ((h ? bx.z : bx.x) & 0xffffu) | ((h ? bx.w : bx.y) & 0xffff0000u);
                     }
 #pragma unroll
                     for (int i = 0; i < C::kN; ++i) {
@@ -640,7 +641,7 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
             }
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(q_free(u, x));
+            if (lane == 0) mbar_arrive(item_free(u, x));
         }
         if (!ok && lane == 0) set_error(a.err, PA_DEVERR_TIMEOUT);
     }
