@@ -45,8 +45,8 @@ struct Umma8Cfg {
     static constexpr int kKS = D / 16;                     // k-steps of S = Q K^T
     static constexpr int kStages = 3;
     static constexpr int kThreads = 32 * (12 + 4 * MT);
-    // two tiles: 640 threads are launched at 96 registers; the issuers keep 40, the converters 72, the softmax gets 144
-    // (4 x 40 + 8 x 72 + 8 x 144 < 20 x 96)
+    // two tiles: 640 threads are launched at 96 registers; the issuers keep 40, the converters 80, the softmax gets 136
+    // (4 x 40 + 8 x 80 + 8 x 136 < 20 x 96)
     static constexpr bool kRegSplit = MT == 2;
     static constexpr int kHalf = kN * 128;                 // one half of K (or V) of a step
     static constexpr int kTile = kSub * kHalf;             // K (or V) of a step
@@ -57,7 +57,7 @@ struct Umma8Cfg {
     // g - kStages is done, so once tile 0's P V of kSB steps before that is, whose V came when both tiles' P V had
     // released that of kStages before: every tile has read what lies 2 kStages + kSB steps back from g
     static constexpr int kNotes = 16;
-    static constexpr int kNoteBytes = 4 * 4 * kBoxes;      // per box: ck, lv, 1 / vs, whether it is there
+    static constexpr int kNoteBytes = 4 * 4 * kBoxes;      // per box: ck, lv, 1 / vs, 1 or 0 (not there)
     static constexpr int kRaw = 4;                         // steps of codes in flight
     static constexpr int kBoxBytes = 16 * D;               // a box's codes
     static constexpr size_t kKVOff = (size_t)MT * kQTile;
@@ -70,7 +70,8 @@ struct Umma8Cfg {
     static constexpr int kTileBars = 3 * kSB + 8;
     static constexpr int kNumBars = 4 * kStages + 8 * kRaw + MT * kTileBars;
     static constexpr size_t kSlotOff = kBarOff + 8 * kNumBars;
-    static constexpr size_t kSmem = kSlotOff + 16 + 1024;  // + alignment slack
+    static constexpr size_t kSeenOff = kSlotOff + 16;      // per V box and raw slot: its keys that some row sees
+    static constexpr size_t kSmem = kSeenOff + 16 * kRaw + 1024;  // + alignment slack
     static constexpr uint32_t kTmemCols = 256 * MT;
     static constexpr uint32_t kOCol = 128 * MT;            // S[u][b] at 128 u + kN b; O[u] at kOCol + D u; P over its S
     static_assert(2 * kStages + kSB + kRaw <= kNotes, "a note must outlive its readers");
@@ -252,20 +253,24 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
         auto full = [&](int i) { return kV ? v_full(i) : k_full(i); };
         auto empty = [&](int i) { return kV ? v_empty(i) : k_empty(i); };
         auto got = [&](int i) { return raw_full(warp - 4, i); };
+        auto seen_at = [&](int i) { return base + (uint32_t)(C::kSeenOff + 4 * (box * C::kRaw + i)); };
         const uint32_t ring = kvb + (kV ? (uint32_t)C::kTile : 0u) + (uint32_t)((ch >> 2) * C::kHalf + (16 * box + row) * 128);
         const uint32_t raw0 = base + (uint32_t)(C::kRawOff + (size_t)(warp - 4) * C::kRaw * C::kBoxBytes);
-        int g = 0, k = 0;
-        uint32_t there = 0;                            // bit i: raw slot i holds a box
-        bool ok = true;
-        for (;;) {
-            Item8 it;
+        // Two walks over the items' steps: `sent` sends for the codes, kRaw steps ahead of `g`, which converts them.
+        int sent = 0, g = 0, k = 0;
+        int j = 0, count = 0, next_w = blockIdx.x;     // the sending walk: step of its item; a CTA's first item needs no claim
+        int before = 0;                                // steps up to the end of the item before the walk's
+        Item8 it;
+        bool more = true, ok = true;
+        // per lane, for the item's steps 32 n + lane: where the box's codes are (null: no row sees them, or the block
+        // is none), the note of the box (K), and which of its keys some row sees (V)
+        const uint8_t *src = nullptr;
+        float4 box_note = make_float4(1.f, 0.f, 1.f, 0.f);
+        int seen = 0;                                  // bits: keys of the box
+        // the next item; false when there is none (or on a timeout)
+        auto next_item = [&]() {
             if (first) {
-                int w = blockIdx.x;  // a CTA's first item needs no claim
-                if (k > 0) {
-                    if (lane == 0) w = (int)gridDim.x + atomicAdd(&a.hdr[1], 1);
-                    w = __shfl_sync(0xffffffffu, w, 0);
-                }
-                const bool have = umma_item8<C>(a, w, nwork, it);
+                const bool have = umma_item8<C>(a, next_w, nwork, it);
                 const int x = k & 1;
 #pragma unroll 1
                 for (int u = 0; ok && u < MT; ++u) {
@@ -276,96 +281,111 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
                     }
                     __syncwarp();
                 }
-                ++k;
-                if (!ok || !have) break;
+                if (have) {
+                    int w = 0;
+                    if (lane == 0) w = (int)gridDim.x + atomicAdd(&a.hdr[1], 1);
+                    next_w = __shfl_sync(0xffffffffu, w, 0);
+                }
             } else {
-                ok = take(0, k++, it);  // tile 0 has rows in every item
-                if (!ok || it.end) break;
+                ok = take(0, k, it);  // tile 0 has rows in every item
             }
-            const int32_t *table = a.block_tables + (size_t)it.s * a.max_blocks;
-            auto box_key = [&](int j) { return (j < it.ns ? j : j + it.gap) * C::kN + 16 * box; };
-            int id = -2;                               // lane l: the block of step 32 n + l (-2: no row sees it)
-            float ks = 1.f, vs = 1.f;
-            // step j's box on its way, and its note (K)
-            auto send = [&](int j, int n) {            // n: the step's number in the ring
-                if ((j & 31) == 0) {
-                    const int b0 = box_key(j + lane);
-                    id = -2;
-                    if (j + lane < it.count && b0 < it.hi && (b0 + 15 >= it.lo || b0 < a.sinks)) id = table[b0 >> lb];
-                    if (!kV) {
-                        ks = vs = 1.f;
-                        if ((unsigned)id < (unsigned)a.N) {
-                            ks = a.k_scales[(size_t)id * a.Hkv + it.kvh];
-                            vs = a.v_scales[(size_t)id * a.Hkv + it.kvh];
-                        } else if (id != -2) {
-                            set_error(a.err, PA_DEVERR_BAD_BLOCK);
-                        }
+            ++k;
+            j = 0;
+            count = it.count;
+            return ok && !it.end;
+        };
+        auto send = [&]() {
+            if ((j & 31) == 0) {
+                const int v = j + lane, b0 = (v < it.ns ? v : v + it.gap) * C::kN + 16 * box;
+                int id = -2;
+                if (v < it.count && b0 < it.hi && (b0 + 15 >= it.lo || b0 < a.sinks)) id = a.block_tables[(size_t)it.s * a.max_blocks + (b0 >> lb)];
+                const bool good = (unsigned)id < (unsigned)a.N;
+                const size_t bh = (size_t)id * a.Hkv + it.kvh;
+                src = good ? cache + (bh * a.B + (b0 & (a.B - 1))) * D : nullptr;
+                if constexpr (kV) {
+                    seen = good ? (int)(low_bits(it.hi - b0) & (~low_bits(it.lo - b0) | low_bits(a.sinks - b0)) & 0xffffu) : 0;
+                } else {
+                    float ks = 1.f, vs = 1.f;
+                    if (good) {
+                        ks = a.k_scales[bh];
+                        vs = a.v_scales[bh];
+                    } else if (id != -2) {
+                        set_error(a.err, PA_DEVERR_BAD_BLOCK);
                     }
+                    box_note = make_float4(ks * a.scale * kLog2e8, lg2(vs), 1.f / vs, good ? 1.f : 0.f);
                 }
-                const int pb = __shfl_sync(0xffffffffu, id, j & 31), i = n % C::kRaw;
-                const bool good = (unsigned)pb < (unsigned)a.N;
-                if (!kV) {
-                    const float k1 = __shfl_sync(0xffffffffu, ks, j & 31), v1 = __shfl_sync(0xffffffffu, vs, j & 31);
-                    if (lane == 0) {
-                        const uint32_t at = note(n) + 4 * box;
-                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(k1 * a.scale * kLog2e8) : "memory");
-                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 16), "f"(lg2(v1)) : "memory");
-                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 32), "f"(1.f / v1) : "memory");
-                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 48), "r"(good ? ~0u : 0u) : "memory");
-                    }
-                }
-                if (good) there |= 1u << i;
-                else there &= ~(1u << i);
-                if (good && lane == 0) {
-                    const size_t at = (((size_t)pb * a.Hkv + it.kvh) * a.B + (box_key(j) & (a.B - 1))) * D;
+            }
+            const int i = sent % C::kRaw;
+            if (lane == (j & 31)) {
+                if constexpr (kV) asm volatile("st.shared.u32 [%0], %1;" ::"r"(seen_at(i)), "r"(seen) : "memory");
+                else
+                    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(note(sent) + 16 * box), "f"(box_note.x), "f"(box_note.y),
+                                 "f"(box_note.z), "f"(box_note.w)
+                                 : "memory");
+                if (src) {
                     mbar_arrive_expect_tx(got(i), C::kBoxBytes);
-                    bulk_g2s(raw0 + (uint32_t)(i * C::kBoxBytes), cache + at, C::kBoxBytes, got(i));
-                } else if (lane == 0) {
+                    bulk_g2s(raw0 + (uint32_t)(i * C::kBoxBytes), src, C::kBoxBytes, got(i));
+                } else {
                     mbar_arrive(got(i));
                 }
-            };
+            }
+            ++sent;
+            ++j;
+        };
+        // Sends up to kRaw steps past the `done` ones.  An item's slots are those of the item before last, which ends
+        // only with its last step converted: until then the walk stops in front of it.
+        auto fill = [&](int done) {
 #pragma unroll 1
-            for (int j = 0; j < min(C::kRaw, it.count); ++j) send(j, g + j);
-#pragma unroll 1
-            for (int j = 0; j < it.count; ++j, ++g) {
-                const int st = g % C::kStages, i = g % C::kRaw;
-                ok = wait(got(i), (uint32_t)(g / C::kRaw) & 1u);
-                if (ok && g >= C::kStages) ok = wait(empty(st), (uint32_t)((g / C::kStages) - 1) & 1u);
-                if (!ok) break;
-                const int kb = box_key(j);
-                const bool good = there >> i & 1u;
-#pragma unroll
-                for (int n = 0; n < kP; ++n) {
-                    const int r = row + kPass * n;
-                    uint4 w = lds128(raw0 + (uint32_t)(i * C::kBoxBytes + n * 512 + lane * 16)), x, y;
-                    if constexpr (kV) {
-                        // a key that no row of the item sees may hold anything
-                        if (!(good && kb + r < it.hi && (kb + r >= it.lo || kb + r < a.sinks))) w = make_uint4(0, 0, 0, 0);
-                        widen16<__half>(w, x, y);
-                    } else {
-                        widen16<T>(w, x, y);
-                    }
-                    const uint32_t at = ring + (uint32_t)(st * C::kStageBytes + kPass * n * 128), sw = (uint32_t)(r & 7);
-                    const uint32_t c0 = ((uint32_t)(2 * (ch & 3)) ^ sw) << 4, c1 = ((uint32_t)(2 * (ch & 3) + 1) ^ sw) << 4;
-                    sts128(at + (flip ? c1 : c0), flip ? y : x);
-                    sts128(at + (flip ? c0 : c1), flip ? x : y);
+            while (more && sent < done + C::kRaw) {
+                if (j == count) {
+                    if (done < before) return;
+                    before = sent;
+                    more = next_item();
+                    if (!more) return;
                 }
-                tc::fence_async_smem();
-                __syncwarp();  // every lane has read the raw box and stored its part
-                if (lane == 0) mbar_arrive(full(st));
-                if (j + C::kRaw < it.count) send(j + C::kRaw, g + C::kRaw);
+                send();
             }
-            if (!ok) {  // copies still in flight must land before the CTA's shared memory is released
-                for (int n = g; n < g + C::kRaw; ++n) mbar_wait_bounded(got(n % C::kRaw), (uint32_t)(n / C::kRaw) & 1u, 1u << 16);
-                break;
+        };
+        fill(0);
+#pragma unroll 1
+        for (; ok && g < sent; ++g) {
+            const int st = g % C::kStages, i = g % C::kRaw;
+            ok = wait(got(i), (uint32_t)(g / C::kRaw) & 1u);
+            if (ok && g >= C::kStages) ok = wait(empty(st), (uint32_t)((g / C::kStages) - 1) & 1u);
+            if (!ok) break;
+            uint32_t keys = 0;
+            if constexpr (kV) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(keys) : "r"(seen_at(i)));
+            uint4 w[kP];
+#pragma unroll
+            for (int n = 0; n < kP; ++n) w[n] = lds128(raw0 + (uint32_t)(i * C::kBoxBytes + n * 512 + lane * 16));
+#pragma unroll
+            for (int n = 0; n < kP; ++n) {
+                const int r = row + kPass * n;
+                uint4 x, y;
+                if constexpr (kV) {
+                    if (!(keys >> r & 1u)) w[n] = make_uint4(0, 0, 0, 0);  // a key that no row of the item sees may hold anything
+                    widen16<__half>(w[n], x, y);
+                } else {
+                    widen16<T>(w[n], x, y);
+                }
+                const uint32_t at = ring + (uint32_t)(st * C::kStageBytes + kPass * n * 128), sw = (uint32_t)(r & 7);
+                const uint32_t c0 = ((uint32_t)(2 * (ch & 3)) ^ sw) << 4, c1 = ((uint32_t)(2 * (ch & 3) + 1) ^ sw) << 4;
+                sts128(at + (flip ? c1 : c0), flip ? y : x);
+                sts128(at + (flip ? c0 : c1), flip ? x : y);
             }
+            tc::fence_async_smem();
+            __syncwarp();  // every lane has read the raw box and stored its part
+            if (lane == 0) mbar_arrive(full(st));
+            fill(g + 1);
         }
+        // copies still in flight must land before the CTA's shared memory is released
+        for (int n = g; n < sent; ++n) mbar_wait_bounded(got(n % C::kRaw), (uint32_t)(n / C::kRaw) & 1u, kWaitLimit);
         if (!ok && lane == 0) set_error(a.err, PA_DEVERR_TIMEOUT);
     };
 
     if (warp >= 4 && warp < 12) {
         // ------------------------------------------------------------ converters: K (warps 4-7), V (8-11)
-        if constexpr (C::kRegSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n" ::: "memory");
+        if constexpr (C::kRegSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n" ::: "memory");
         if (warp < 8) convert(std::integral_constant<bool, false>());
         else convert(std::integral_constant<bool, true>());
     } else if (warp < 2) {
@@ -487,7 +507,7 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
         }
     } else {
         // ------------------------------------------------------------ softmax (one row per thread)
-        if constexpr (C::kRegSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 144;\n" ::: "memory");
+        if constexpr (C::kRegSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 136;\n" ::: "memory");
         const int u = (warp - 12) / 4;
         const int wq = warp & 3;                 // TMEM lanes 32 wq ..
         const uint32_t tl = tbase + ((uint32_t)(wq * 32) << 16);
@@ -517,10 +537,10 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
                 tc::tmem_ld32(tl + s_col(u, b), sv[0]);
                 tc::tmem_ld32(tl + s_col(u, b) + 32u, sv[1]);
                 const uint32_t nt = note(g);
-                const float4 ck4 = lds_f4(nt), lv4 = lds_f4(nt + 16), iv4 = lds_f4(nt + 32);
-                const uint4 bx = lds128(nt + 48);
-                float ck[4] = {ck4.x, ck4.y, ck4.z, ck4.w}, lv[4] = {lv4.x, lv4.y, lv4.z, lv4.w};
-                const float iv[4] = {iv4.x, iv4.y, iv4.z, iv4.w};
+                const float4 n4[4] = {lds_f4(nt), lds_f4(nt + 16), lds_f4(nt + 32), lds_f4(nt + 48)};
+                float ck[4] = {n4[0].x, n4[1].x, n4[2].x, n4[3].x}, lv[4] = {n4[0].y, n4[1].y, n4[2].y, n4[3].y};
+                const float iv[4] = {n4[0].z, n4[1].z, n4[2].z, n4[3].z};
+                const bool whole = fminf(fminf(n4[0].w, n4[1].w), fminf(n4[2].w, n4[3].w)) > 0.f;
                 const int kb = (j < it.ns ? j : j + it.gap) * C::kN;
                 const int lim = pos - kb;                                     // last visible key of the step
                 const int from = a.window > 0 ? lim - a.window + 1 : 0;       // first one of the window
@@ -529,14 +549,14 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < C::kN; ++i) f[i] = __uint_as_float(sv[i >> 5][i & 31]);
                 const bool plain = fminf(fminf(ck[0], ck[1]), fminf(ck[2], ck[3])) >= 0x1p-120f;
-                if (!(__all_sync(0xffffffffu, lim >= C::kN - 1 && (from <= 0 || kb + C::kN <= a.sinks)) && (bx.x & bx.y & bx.z & bx.w) && plain)) {
+                if (!(__all_sync(0xffffffffu, lim >= C::kN - 1 && (from <= 0 || kb + C::kN <= a.sinks)) && whole && plain)) {
                     // a step on the diagonal, on a window's border, over a block not loaded; a scale that is not positive
                     const int sk = a.window > 0 ? a.sinks - kb : 0;
                     uint32_t see[2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         see[h] = low_bits(lim + 1 - 32 * h) & (~low_bits(from - 32 * h) | low_bits(sk - 32 * h));
-                        see[h] &= ((h ? bx.z : bx.x) & 0xffffu) | ((h ? bx.w : bx.y) & 0xffff0000u);
+                        see[h] &= (n4[2 * h].w > 0.f ? 0xffffu : 0u) | (n4[2 * h + 1].w > 0.f ? 0xffff0000u : 0u);
                     }
 #pragma unroll
                     for (int i = 0; i < C::kN; ++i) {
