@@ -7,11 +7,10 @@
 // a longest-first list.  Warps:
 //   0, 1       send for tile 0's and tile 1's queries (TMA) and issue  S_u = Q_u K^T  (M 128, N 64, K = D)
 //   2, 3       issue their  O_u += P_u V    (M 128, N = D, K = 64), P from TMEM
-//   4 .. 11    converters, a warpgroup for K and one for V, each warp with one 16-key box of every step: it sends for its
-//              box's codes four steps ahead (one bulk copy), turns them into 16-bit floats (K into the queries' type, V
-//              into f16; both exact) and stores them as the swizzled operands; K's also publish the box's scales, and warp 4
-//              claims the items.  (Loads into registers instead, however far ahead, are waited for by the next arrive,
-//              which releases: 341 us against ## on 16 x 512-token chunks.)
+//   4 .. 11    converters, a warpgroup for K and one for V, each warp with one 16-key box of every step: it loads its
+//              box's codes a step ahead, turns them into 16-bit floats (K into the queries' type, V into f16; both
+//              exact) and stores them as the swizzled operands; K's also publish the box's scales, and warp 4 claims
+//              the items.
 //   12 ..      one softmax warpgroup per tile, one thread per row
 // Converting once per step serves both tiles, and the codes' 16-bit form never leaves the SM.  The alternative, e4m3
 // operands with Q and P split in two terms each, would need as many products, and the split of P in the softmax
@@ -45,36 +44,34 @@ struct Umma8Cfg {
     static constexpr int kKS = D / 16;                     // k-steps of S = Q K^T
     static constexpr int kStages = 3;
     static constexpr int kThreads = 32 * (12 + 4 * MT);
-    // two tiles: 640 threads are launched at 96 registers; the issuers keep 40, the converters 80, the softmax gets 136
-    // (4 x 40 + 8 x 80 + 8 x 136 < 20 x 96)
+    // two tiles: 640 threads are launched at 96 registers; the issuers keep 40, the converters 88, the softmax gets 128
+    // (4 x 40 + 8 x 88 + 8 x 128 < 20 x 96)
     static constexpr bool kRegSplit = MT == 2;
     static constexpr int kHalf = kN * 128;                 // one half of K (or V) of a step
     static constexpr int kTile = kSub * kHalf;             // K (or V) of a step
     static constexpr int kStageBytes = 2 * kTile;
     static constexpr int kQHalf = kM * 128;
     static constexpr int kQTile = kSub * kQHalf;
-    // scales of the last kNotes steps.  Those of step g + kRaw are written while step g is converted, so once S of
+    // scales of the last kNotes steps.  Those of step g + 1 are written once step g is converted, so once S of
     // g - kStages is done, so once tile 0's P V of kSB steps before that is, whose V came when both tiles' P V had
     // released that of kStages before: every tile has read what lies 2 kStages + kSB steps back from g
     static constexpr int kNotes = 16;
     static constexpr int kNoteBytes = 4 * 4 * kBoxes;      // per box: ck, lv, 1 / vs, 1 or 0 (not there)
-    static constexpr int kRaw = 4;                         // steps of codes in flight
-    static constexpr int kBoxBytes = 16 * D;               // a box's codes
     static constexpr size_t kKVOff = (size_t)MT * kQTile;
-    static constexpr size_t kRawOff = kKVOff + (size_t)kStages * kStageBytes;    // per converter warp kRaw boxes
-    static constexpr size_t kNoteOff = kRawOff + (size_t)8 * kRaw * kBoxBytes;
+    static constexpr int kOutBytes = 32 * 256;             // of a softmax warp: its rows on their way out, 256 bytes at a time
+    static constexpr size_t kOutOff = kKVOff + (size_t)kStages * kStageBytes;
+    static constexpr size_t kNoteOff = kOutOff + (size_t)4 * MT * kOutBytes;
     static constexpr size_t kItemOff = kNoteOff + (size_t)kNotes * kNoteBytes;   // per tile two items of 16 ints
     static constexpr size_t kBarOff = kItemOff + (size_t)MT * 2 * 64;
-    // k_full, k_empty, v_full, v_empty [kStages] | raw_full [8 warps][kRaw] | per tile: s_full, p_full, o_done [kSB],
+    // k_full, k_empty, v_full, v_empty [kStages] | per tile: s_full, p_full, o_done [kSB],
     // item_free [2], item_ready [2], q_full, q_done, drain_s, drain_p
     static constexpr int kTileBars = 3 * kSB + 8;
-    static constexpr int kNumBars = 4 * kStages + 8 * kRaw + MT * kTileBars;
+    static constexpr int kNumBars = 4 * kStages + MT * kTileBars;
     static constexpr size_t kSlotOff = kBarOff + 8 * kNumBars;
-    static constexpr size_t kSeenOff = kSlotOff + 16;      // per V box and raw slot: its keys that some row sees
-    static constexpr size_t kSmem = kSeenOff + 16 * kRaw + 1024;  // + alignment slack
+    static constexpr size_t kSmem = kSlotOff + 16 + 1024;  // + alignment slack
     static constexpr uint32_t kTmemCols = 256 * MT;
     static constexpr uint32_t kOCol = 128 * MT;            // S[u][b] at 128 u + kN b; O[u] at kOCol + D u; P over its S
-    static_assert(2 * kStages + kSB + kRaw <= kNotes, "a note must outlive its readers");
+    static_assert(2 * kStages + kSB + 1 <= kNotes, "a note must outlive its readers");
     static_assert(kOCol + MT * D <= kTmemCols, "TMEM budget");
     static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
@@ -134,6 +131,16 @@ __device__ __forceinline__ void widen16(const uint4 &w, uint4 &x, uint4 &y) {
 __device__ __forceinline__ void sts128(uint32_t at, const uint4 &x) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
 }
+// 16 codes, or zeros where there are none: the load is predicated, so that nothing waits for it before its use.
+__device__ __forceinline__ void ldg_codes(uint4 &v, const uint8_t *p, bool want) {
+    v = make_uint4(0, 0, 0, 0);
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %5, 0;\n\t"
+        "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+        : "l"(p), "r"((uint32_t)want));
+}
 __device__ __forceinline__ float4 lds_f4(uint32_t at) {
     float4 v;
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
@@ -177,8 +184,7 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
     auto k_empty = [&](int i) { return bars + 8u * (uint32_t)(C::kStages + i); };
     auto v_full = [&](int i) { return bars + 8u * (uint32_t)(2 * C::kStages + i); };
     auto v_empty = [&](int i) { return bars + 8u * (uint32_t)(3 * C::kStages + i); };
-    auto raw_full = [&](int w, int i) { return bars + 8u * (uint32_t)(4 * C::kStages + w * C::kRaw + i); };
-    auto tbar = [&](int u, int i) { return bars + 8u * (uint32_t)(4 * C::kStages + 8 * C::kRaw + u * C::kTileBars + i); };
+    auto tbar = [&](int u, int i) { return bars + 8u * (uint32_t)(4 * C::kStages + u * C::kTileBars + i); };
     auto s_full = [&](int u, int b) { return tbar(u, b); };
     auto p_full = [&](int u, int b) { return tbar(u, kSB + b); };
     auto o_done = [&](int u, int b) { return tbar(u, 2 * kSB + b); };  // P V done: O is up to date, S/P[u][b] is free
@@ -209,8 +215,6 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
             mbar_init(v_full(i), 4);
             mbar_init(v_empty(i), MT);  // likewise from each tile's P V issuer
         }
-        for (int w = 0; w < 8; ++w)
-            for (int i = 0; i < C::kRaw; ++i) mbar_init(raw_full(w, i), 1);
         for (int u = 0; u < MT; ++u) {
             for (int b = 0; b < kSB; ++b) {
                 mbar_init(s_full(u, b), 1);
@@ -252,16 +256,11 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
         const uint8_t *cache = kV ? a.v_cache : a.k_cache;
         auto full = [&](int i) { return kV ? v_full(i) : k_full(i); };
         auto empty = [&](int i) { return kV ? v_empty(i) : k_empty(i); };
-        auto got = [&](int i) { return raw_full(warp - 4, i); };
-        auto seen_at = [&](int i) { return base + (uint32_t)(C::kSeenOff + 4 * (box * C::kRaw + i)); };
         const uint32_t ring = kvb + (kV ? (uint32_t)C::kTile : 0u) + (uint32_t)((ch >> 2) * C::kHalf + (16 * box + row) * 128);
-        const uint32_t raw0 = base + (uint32_t)(C::kRawOff + (size_t)(warp - 4) * C::kRaw * C::kBoxBytes);
-        // Two walks over the items' steps: `sent` sends for the codes, kRaw steps ahead of `g`, which converts them.
-        int sent = 0, g = 0, k = 0;
-        int j = 0, count = 0, next_w = blockIdx.x;     // the sending walk: step of its item; a CTA's first item needs no claim
-        int before = 0;                                // steps up to the end of the item before the walk's
+        int g = 0, k = 0, j = 0, count = 0;            // ring steps, items, the step to fetch next and its item's
+        int next_w = blockIdx.x;                       // a CTA's first item needs no claim
         Item8 it;
-        bool more = true, ok = true;
+        bool ok = true;
         // per lane, for the item's steps 32 n + lane: where the box's codes are (null: no row sees them, or the block
         // is none), the note of the box (K), and which of its keys some row sees (V)
         const uint8_t *src = nullptr;
@@ -294,7 +293,12 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
             count = it.count;
             return ok && !it.end;
         };
-        auto send = [&]() {
+        // The next step's codes on their way into `w`, and its note (K); false past the last item.  What an arrive
+        // releases includes this warp's loads, so these are sent for behind one step's arrive and used before the next one's.
+        uint4 w[kP];
+        uint32_t keys = 0;                             // V: the box's keys that some row sees
+        auto fetch = [&]() {
+            if (j == count && !next_item()) return false;
             if ((j & 31) == 0) {
                 const int v = j + lane, b0 = (v < it.ns ? v : v + it.gap) * C::kN + 16 * box;
                 int id = -2;
@@ -315,77 +319,45 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
                     box_note = make_float4(ks * a.scale * kLog2e8, lg2(vs), 1.f / vs, good ? 1.f : 0.f);
                 }
             }
-            const int i = sent % C::kRaw;
-            if (lane == (j & 31)) {
-                if constexpr (kV) asm volatile("st.shared.u32 [%0], %1;" ::"r"(seen_at(i)), "r"(seen) : "memory");
-                else
-                    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(note(sent) + 16 * box), "f"(box_note.x), "f"(box_note.y),
-                                 "f"(box_note.z), "f"(box_note.w)
-                                 : "memory");
-                if (src) {
-                    mbar_arrive_expect_tx(got(i), C::kBoxBytes);
-                    bulk_g2s(raw0 + (uint32_t)(i * C::kBoxBytes), src, C::kBoxBytes, got(i));
-                } else {
-                    mbar_arrive(got(i));
-                }
-            }
-            ++sent;
-            ++j;
-        };
-        // Sends up to kRaw steps past the `done` ones.  An item's slots are those of the item before last, which ends
-        // only with its last step converted: until then the walk stops in front of it.
-        auto fill = [&](int done) {
-#pragma unroll 1
-            while (more && sent < done + C::kRaw) {
-                if (j == count) {
-                    if (done < before) return;
-                    before = sent;
-                    more = next_item();
-                    if (!more) return;
-                }
-                send();
-            }
-        };
-        fill(0);
-#pragma unroll 1
-        for (; ok && g < sent; ++g) {
-            const int st = g % C::kStages, i = g % C::kRaw;
-            ok = wait(got(i), (uint32_t)(g / C::kRaw) & 1u);
-            if (ok && g >= C::kStages) ok = wait(empty(st), (uint32_t)((g / C::kStages) - 1) & 1u);
-            if (!ok) break;
-            uint32_t keys = 0;
-            if constexpr (kV) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(keys) : "r"(seen_at(i)));
-            uint4 w[kP];
+            const uint8_t *from = reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), j & 31));
+            if constexpr (kV) keys = __shfl_sync(0xffffffffu, seen, j & 31);
+            else if (lane == (j & 31))
+                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(note(g) + 16 * box), "f"(box_note.x), "f"(box_note.y),
+                             "f"(box_note.z), "f"(box_note.w)
+                             : "memory");
+            // a key that no row of the item sees may hold anything: its V counts as zeros
 #pragma unroll
-            for (int n = 0; n < kP; ++n) w[n] = lds128(raw0 + (uint32_t)(i * C::kBoxBytes + n * 512 + lane * 16));
+            for (int n = 0; n < kP; ++n) ldg_codes(w[n], from + n * 512 + lane * 16, kV ? (keys >> (row + kPass * n) & 1u) : from != nullptr);
+            ++j;
+            return true;
+        };
+#pragma unroll 1
+        for (bool more = fetch(); more; more = fetch()) {
+            const int st = g % C::kStages;
+            if (g >= C::kStages) ok = wait(empty(st), (uint32_t)((g / C::kStages) - 1) & 1u);
+            if (!ok) break;
 #pragma unroll
             for (int n = 0; n < kP; ++n) {
                 const int r = row + kPass * n;
                 uint4 x, y;
-                if constexpr (kV) {
-                    if (!(keys >> r & 1u)) w[n] = make_uint4(0, 0, 0, 0);  // a key that no row of the item sees may hold anything
-                    widen16<__half>(w[n], x, y);
-                } else {
-                    widen16<T>(w[n], x, y);
-                }
+                if constexpr (kV) widen16<__half>(w[n], x, y);
+                else widen16<T>(w[n], x, y);
                 const uint32_t at = ring + (uint32_t)(st * C::kStageBytes + kPass * n * 128), sw = (uint32_t)(r & 7);
                 const uint32_t c0 = ((uint32_t)(2 * (ch & 3)) ^ sw) << 4, c1 = ((uint32_t)(2 * (ch & 3) + 1) ^ sw) << 4;
                 sts128(at + (flip ? c1 : c0), flip ? y : x);
                 sts128(at + (flip ? c0 : c1), flip ? x : y);
             }
             tc::fence_async_smem();
-            __syncwarp();  // every lane has read the raw box and stored its part
+            __syncwarp();
             if (lane == 0) mbar_arrive(full(st));
-            fill(g + 1);
+            ++g;
         }
-        // copies still in flight must land before the CTA's shared memory is released
-        for (int n = g; n < sent; ++n) mbar_wait_bounded(got(n % C::kRaw), (uint32_t)(n / C::kRaw) & 1u, kWaitLimit);
         if (!ok && lane == 0) set_error(a.err, PA_DEVERR_TIMEOUT);
     };
 
     if (warp >= 4 && warp < 12) {
         // ------------------------------------------------------------ converters: K (warps 4-7), V (8-11)
-        if constexpr (C::kRegSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n" ::: "memory");
+        if constexpr (C::kRegSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n" ::: "memory");
         if (warp < 8) convert(std::integral_constant<bool, false>());
         else convert(std::integral_constant<bool, true>());
     } else if (warp < 2) {
@@ -507,7 +479,7 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
         }
     } else {
         // ------------------------------------------------------------ softmax (one row per thread)
-        if constexpr (C::kRegSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 136;\n" ::: "memory");
+        if constexpr (C::kRegSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;\n" ::: "memory");
         const int u = (warp - 12) / 4;
         const int wq = warp & 3;                 // TMEM lanes 32 wq ..
         const uint32_t tl = tbase + ((uint32_t)(wq * 32) << 16);
@@ -634,29 +606,49 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
             if (!ok) break;
             tc::fence_after_sync();
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            const size_t at = ((size_t)(it.qs + t) * a.Hq + it.kvh * G + (R - t * G)) * D;
+            // through shared memory, so that a store writes whole rows: 32 columns a turn into it, in 16-byte pieces swizzled by
+            // row, then up to 256 bytes of each row out of it
+            const uint32_t stage = base + (uint32_t)(C::kOutOff + (size_t)(warp - 12) * C::kOutBytes);
+            const int lg = __ffs(G) - 1, R0 = it.r0 + C::kM * u + 32 * wq;   // this warp's first row; G is a power of two
+            auto put = [&](int piece, const uint4 &v) { sts128(stage + (uint32_t)(lane * 256) + ((uint32_t)(piece ^ (lane & 7)) << 4), v); };
+            auto flush = [&](int bytes, int at) {   // `bytes` of each row, to byte `at` of its head's output
+                __syncwarp();
+                const int per = bytes >> 4, each = 32 / per;        // lanes of a row, rows of a store
+                const size_t row_bytes = (size_t)D * (a.out16 ? 2 : 4);
+#pragma unroll 4
+                for (int r = lane / per; r < 32; r += each) {
+                    const int piece = lane % per, Rr = R0 + r, tr = Rr >> lg;
+                    const uint4 v = lds128(stage + (uint32_t)(r * 256) + ((uint32_t)(piece ^ (r & 7)) << 4));
+                    if (tr < it.n)
+                        *reinterpret_cast<uint4 *>(static_cast<unsigned char *>(a.out) +
+                                                   ((size_t)(it.qs + tr) * a.Hq + it.kvh * G + (Rr & (G - 1))) * row_bytes + at + 16 * piece) = v;
+                }
+                __syncwarp();
+            };
 #pragma unroll
             for (int cb = 0; cb < D / 32; ++cb) {
                 uint32_t ov[32];
                 tc::tmem_ld32(tl + o_col(u) + (uint32_t)(32 * cb), ov);
                 tc::tmem_wait_ld();
-                if (t >= it.n) continue;
                 if (a.out16) {
-                    uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at + 32 * cb);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t w[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             w[e] = Mma16<T>::pack(__uint_as_float(ov[8 * i + 2 * e]) * inv, __uint_as_float(ov[8 * i + 2 * e + 1]) * inv);
-                        to[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                        put(4 * cb + i, make_uint4(w[0], w[1], w[2], w[3]));
                     }
+                    if (cb == D / 32 - 1) flush(2 * D, 0);
                 } else {
-                    float4 *to = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at + 32 * cb);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        to[i] = make_float4(__uint_as_float(ov[4 * i]) * inv, __uint_as_float(ov[4 * i + 1]) * inv,
-                                            __uint_as_float(ov[4 * i + 2]) * inv, __uint_as_float(ov[4 * i + 3]) * inv);
+                    for (int i = 0; i < 8; ++i) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(__uint_as_float(ov[4 * i + e]) * inv);
+                        put(8 * (cb & 1) + i, make_uint4(w[0], w[1], w[2], w[3]));
+                    }
+                    if (cb & 1) flush(256, 256 * (cb >> 1));
                 }
             }
             tc::fence_before_sync();
