@@ -3,9 +3,9 @@
 
 namespace pa {
 
-cudaError_t launch_attend8_mma_f16(const Attend8Args &a, int row_tiles, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st) {
-    const cudaError_t e = dispatch_attend8<__half>(a, row_tiles, tmk, tmv, st);
-    return e != cudaSuccess ? e : dispatch_merge8<__half>(a, row_tiles, st);
+cudaError_t launch_attend8_mma_f16(const Attend8Args &a, int team, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st) {
+    const cudaError_t e = dispatch_attend8<__half>(a, team, tmk, tmv, st);
+    return e != cudaSuccess ? e : dispatch_merge8<__half>(a, team, st);
 }
 
 }  // namespace pa

@@ -47,23 +47,25 @@ struct Attend8Args {
     void *out;                      // [T, Hq, D], f32 or the queries' type
     int *hdr;                       // [0] whether query_start is in order (mma.sync); work items, claims (tcgen05)
     int4 *list;                     // per (sequence, KV head, row block): its first part and their number (int2); tcgen05: work items
-    float *parts;                   // mma.sync: two parts of a (row block, KV head) per warp, O and (m, l)
+    float *parts;                   // mma.sync: two parts of a (row block, KV head) per team, O and (m, l)
     const uint8_t *k_cache, *v_cache;
     unsigned int *err;
     int S, T, Hq, Hkv, D, B, N, max_blocks, max_query_len;
     int window, sinks;              // window 0: none
     int out16;
-    int units;                      // mma.sync path: warps that take a share of the keys
+    int units;                      // mma.sync path: teams of warps that take a share of the keys
     int tiles;                      // tcgen05 path: 128-row tiles of an item (1 or 2)
     float scale;
 };
-// mma.sync path, and the join of its parts: row blocks of 16 * row_tiles rows of a KV head (0: 8 rows, a decode).
+// mma.sync path, and the join of its parts: teams of `team` warps, row blocks of 16 * team rows of a KV head (0: a
+// decode, one warp and 8 rows).
 constexpr int kUnits8 = 152 * 8;   // warps that share a call's keys, at most: eight per SM
-inline int attend8_row_tiles(int max_query_len, int G) {
-    return (long long)max_query_len * G <= 16 ? 1 : 2;
+inline int attend8_team(int max_query_len, int G) {
+    const long long rows = (long long)max_query_len * G;
+    return rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
 }
-cudaError_t launch_attend8_mma_f16(const Attend8Args &a, int row_tiles, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
-cudaError_t launch_attend8_mma_bf16(const Attend8Args &a, int row_tiles, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
+cudaError_t launch_attend8_mma_f16(const Attend8Args &a, int team, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
+cudaError_t launch_attend8_mma_bf16(const Attend8Args &a, int team, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
 // A cache of codes [N, Hkv, B, D]: boxes of one (block, KV head), rows of D bytes with the swizzle of that width.
 cudaError_t make_codes_tensor_map(CUtensorMap *map, const void *codes, int D, int B, long long block_heads);
 // tcgen05 path, from 64 rows of a KV head on: the work list, and the kernel (tmq: the queries' map).

@@ -55,21 +55,22 @@ int32_t check_chunk8(const pa_dims *d, int32_t T, int32_t max_q) {
 int32_t check_window(const pa_window *w) { return w && (w->window < 0 || w->sinks < 0) ? PA_ERR_INVALID : PA_OK; }
 
 // Workspace, each part 256-byte aligned: a header, the notes of each (sequence, KV head, row block), and two parts
-// for each warp that shares the keys (mma.sync path).
+// for each team that shares the keys (mma.sync path).
 struct Layout8 {
-    int row_tiles, units, tiles;  // tiles 0: the mma.sync path
+    int team, units, tiles;  // tiles 0: the mma.sync path
     size_t list, parts, total;
 };
-Layout8 layout8(const pa_dims *d, int row_tiles, int32_t max_q) {
+Layout8 layout8(const pa_dims *d, int team, int32_t max_q) {
     Layout8 L{};
     const int64_t G = d->num_q_heads / d->num_kv_heads;
-    L.row_tiles = row_tiles;
-    const int64_t rows = row_tiles ? 16 * row_tiles : 8, blocks = (max_q * G + rows - 1) / rows;
-    // no more warps than give each of them four steps of 32 keys
+    L.team = team;
+    const int64_t rows = team ? 16 * team : 8, blocks = (max_q * G + rows - 1) / rows;
+    // no more teams than give each of them four steps of 32 keys
     const int64_t steps = ((int64_t)d->max_blocks_per_seq * d->block_size + 31) / 32;
     const int64_t most = (int64_t)d->num_seqs * d->num_kv_heads * blocks;  // at most 2^31
-    const int64_t units = most > pa::kUnits8 * (int64_t)4 / steps ? pa::kUnits8 : (most * steps + 3) / 4;
-    L.units = (int)(units < pa::kUnits8 ? (units > 0 ? units : 1) : pa::kUnits8);
+    const int64_t cap = pa::kUnits8 / (team ? team : 1);
+    const int64_t units = most > cap * 4 / steps ? cap : (most * steps + 3) / 4;
+    L.units = (int)(units < cap ? (units > 0 ? units : 1) : cap);
     L.list = 256;
     L.parts = L.list + up256((size_t)most * sizeof(int2));
     L.total = L.parts + up256((size_t)2 * L.units * rows * (d->head_dim + 2) * sizeof(float));
@@ -78,7 +79,7 @@ Layout8 layout8(const pa_dims *d, int row_tiles, int32_t max_q) {
 Layout8 decode_layout8(const pa_dims *d) { return layout8(d, 0, 1); }
 Layout8 chunk_layout8(const pa_dims *d, int32_t max_q) {
     const int G = d->num_q_heads / d->num_kv_heads;
-    if (!pa::chunk_uses_umma(max_q, G)) return layout8(d, pa::attend8_row_tiles(max_q, G), max_q);
+    if (!pa::chunk_uses_umma(max_q, G)) return layout8(d, pa::attend8_team(max_q, G), max_q);
     Layout8 L{};   // a header and the work list
     L.tiles = pa::chunk_umma_rows(max_q, G) / 128;
     L.list = 256;
@@ -153,8 +154,8 @@ int32_t run_mma(pa::Attend8Args &a, const pa_dims *d, const Layout8 &L, void *st
     if (e == cudaSuccess) e = codes_map(a.v_cache, a.D, a.B, block_heads, &tmv);
     if (e != cudaSuccess) return PA_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return to_status(d->kv_dtype == PA_BF16 ? pa::launch_attend8_mma_bf16(a, L.row_tiles, tmk, tmv, st)
-                                            : pa::launch_attend8_mma_f16(a, L.row_tiles, tmk, tmv, st));
+    return to_status(d->kv_dtype == PA_BF16 ? pa::launch_attend8_mma_bf16(a, L.team, tmk, tmv, st)
+                                            : pa::launch_attend8_mma_f16(a, L.team, tmk, tmv, st));
 }
 
 int32_t run_umma(pa::Attend8Args &a, const pa_dims *d, void *stream) {
