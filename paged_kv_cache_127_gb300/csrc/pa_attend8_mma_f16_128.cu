@@ -1,0 +1,10 @@
+// pa_attend8_mma_f16_128.cu -- decode and short chunks over the 8-bit cache, f16 queries, head_dim 128.
+#include "pa_attend8_mma.cuh"
+
+namespace pa {
+
+cudaError_t launch_attend8_mma_f16_128(const Attend8Args &a, int tw, int hg, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st) {
+    return dispatch_attend8<__half, 128>(a, tw, hg, tmk, tmv, st);
+}
+
+}  // namespace pa

@@ -46,28 +46,34 @@ struct Attend8Args {
     const int32_t *query_start;     // [S + 1], or null
     void *out;                      // [T, Hq, D], f32 or the queries' type
     int *hdr;                       // [0] whether query_start is in order (mma.sync); work items, claims (tcgen05)
-    int4 *list;                     // per (sequence, KV head, row block): its first part and their number (int2); tcgen05: work items
-    float *parts;                   // mma.sync: two parts of a (row block, KV head) per team, O and (m, l)
+    int4 *list;                     // per (sequence, head group, row block): its first part and their number (int2); tcgen05: work items
+    float *parts;                   // mma.sync: two parts of a (row block, head group) per CTA, O and (m, l)
     const uint8_t *k_cache, *v_cache;
     unsigned int *err;
     int S, T, Hq, Hkv, D, B, N, max_blocks, max_query_len;
     int window, sinks;              // window 0: none
     int out16;
-    int units;                      // mma.sync path: teams of warps that take a share of the keys
+    int units;                      // mma.sync path: CTAs, which share the keys
     int tiles;                      // tcgen05 path: 128-row tiles of an item (1 or 2)
     float scale;
 };
-// mma.sync path, and the join of its parts: teams of `team` warps, row blocks of 16 * team rows of a KV head (0: a
-// decode, one warp and 8 rows).
-constexpr int kUnits8 = 152 * 8;   // warps that share a call's keys, at most: eight per SM
-inline int attend8_team(int max_query_len, int G) {
+// mma.sync path, and the join of its parts: row blocks of `tw` 16-row tiles of a KV head (0: a decode, 8 rows), `hg`
+// KV heads a CTA.  A CTA has hg * max(tw, 1) consumer warps of up to 200 registers a thread and a producer: ten warps an SM.
+constexpr int kSms8 = 152;
+constexpr int attend8_ctas(int tw, int hg) { return 10 / (hg * (tw ? tw : 1) + 1); }   // per SM
+inline int attend8_tiles(int max_query_len, int G) {
     const long long rows = (long long)max_query_len * G;
     return rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
 }
-cudaError_t launch_attend8_mma_f16(const Attend8Args &a, int team, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
-cudaError_t launch_attend8_mma_bf16(const Attend8Args &a, int team, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
-// A cache of codes [N, Hkv, B, D]: boxes of one (block, KV head), rows of D bytes with the swizzle of that width.
-cudaError_t make_codes_tensor_map(CUtensorMap *map, const void *codes, int D, int B, long long block_heads);
+inline int attend8_heads(int Hkv, int tw) {
+    return Hkv % 4 == 0 && tw < 4 ? 4 : Hkv % 2 == 0 ? 2 : 1;
+}
+cudaError_t launch_attend8_mma_f16_64(const Attend8Args &a, int tw, int hg, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
+cudaError_t launch_attend8_mma_f16_128(const Attend8Args &a, int tw, int hg, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
+cudaError_t launch_attend8_mma_bf16_64(const Attend8Args &a, int tw, int hg, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
+cudaError_t launch_attend8_mma_bf16_128(const Attend8Args &a, int tw, int hg, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
+// A cache of codes [N, Hkv, B, D]: boxes of `heads` heads of one block, rows of D bytes with the swizzle of that width.
+cudaError_t make_codes_tensor_map(CUtensorMap *map, const void *codes, int D, int B, long long block_heads, int heads);
 // tcgen05 path, from 64 rows of a KV head on: the work list, and the kernel (tmq: the queries' map).
 cudaError_t launch_attend8_plan(const Attend8Args &a, cudaStream_t st);
 cudaError_t launch_attend8_umma_f16(const Attend8Args &a, const CUtensorMap &tmq, cudaStream_t st);

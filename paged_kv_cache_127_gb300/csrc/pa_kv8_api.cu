@@ -55,31 +55,32 @@ int32_t check_chunk8(const pa_dims *d, int32_t T, int32_t max_q) {
 int32_t check_window(const pa_window *w) { return w && (w->window < 0 || w->sinks < 0) ? PA_ERR_INVALID : PA_OK; }
 
 // Workspace, each part 256-byte aligned: a header, the notes of each (sequence, KV head, row block), and two parts
-// for each team that shares the keys (mma.sync path).
+// for each CTA that shares the keys (mma.sync path).
 struct Layout8 {
-    int team, units, tiles;  // tiles 0: the mma.sync path
+    int tw, hg, units, tiles;  // tiles 0: the mma.sync path
     size_t list, parts, total;
 };
-Layout8 layout8(const pa_dims *d, int team, int32_t max_q) {
+Layout8 layout8(const pa_dims *d, int tw, int32_t max_q) {
     Layout8 L{};
     const int64_t G = d->num_q_heads / d->num_kv_heads;
-    L.team = team;
-    const int64_t rows = team ? 16 * team : 8, blocks = (max_q * G + rows - 1) / rows;
-    // no more teams than give each of them four steps of 32 keys
+    L.tw = tw;
+    L.hg = pa::attend8_heads(d->num_kv_heads, tw);
+    const int64_t rows = tw ? 16 * tw : 8, blocks = (max_q * G + rows - 1) / rows;
+    // no more CTAs than give each of them four steps of 32 keys
     const int64_t steps = ((int64_t)d->max_blocks_per_seq * d->block_size + 31) / 32;
-    const int64_t most = (int64_t)d->num_seqs * d->num_kv_heads * blocks;  // at most 2^31
-    const int64_t cap = pa::kUnits8 / (team ? team : 1);
+    const int64_t most = (int64_t)d->num_seqs * (d->num_kv_heads / L.hg) * blocks;  // at most 2^31
+    const int64_t cap = pa::kSms8 * pa::attend8_ctas(tw, L.hg);
     const int64_t units = most > cap * 4 / steps ? cap : (most * steps + 3) / 4;
     L.units = (int)(units < cap ? (units > 0 ? units : 1) : cap);
     L.list = 256;
     L.parts = L.list + up256((size_t)most * sizeof(int2));
-    L.total = L.parts + up256((size_t)2 * L.units * rows * (d->head_dim + 2) * sizeof(float));
+    L.total = L.parts + up256((size_t)2 * L.units * L.hg * rows * (d->head_dim + 2) * sizeof(float));
     return L;
 }
 Layout8 decode_layout8(const pa_dims *d) { return layout8(d, 0, 1); }
 Layout8 chunk_layout8(const pa_dims *d, int32_t max_q) {
     const int G = d->num_q_heads / d->num_kv_heads;
-    if (!pa::chunk_uses_umma(max_q, G)) return layout8(d, pa::attend8_team(max_q, G), max_q);
+    if (!pa::chunk_uses_umma(max_q, G)) return layout8(d, pa::attend8_tiles(max_q, G), max_q);
     Layout8 L{};   // a header and the work list
     L.tiles = pa::chunk_umma_rows(max_q, G) / 128;
     L.list = 256;
@@ -89,29 +90,30 @@ Layout8 chunk_layout8(const pa_dims *d, int32_t max_q) {
 }
 
 // The tensor maps of the caches, re-encoded only when a cache or its shape changes (per host thread).
-cudaError_t codes_map(const void *ptr, int D, int B, long long block_heads, CUtensorMap *out) {
+cudaError_t codes_map(const void *ptr, int D, int B, long long block_heads, int heads, CUtensorMap *out) {
     struct Entry {
         const void *ptr = nullptr;
         long long block_heads = 0;
-        int D = 0, B = 0;
+        int D = 0, B = 0, heads = 0;
         CUtensorMap map;
     };
     thread_local Entry cache[4];
     thread_local int next = 0;
     for (auto &e : cache)
-        if (e.ptr == ptr && e.block_heads == block_heads && e.D == D && e.B == B) {
+        if (e.ptr == ptr && e.block_heads == block_heads && e.D == D && e.B == B && e.heads == heads) {
             *out = e.map;
             return cudaSuccess;
         }
     Entry &e = cache[next];
     next = (next + 1) % 4;
     e.ptr = nullptr;
-    const cudaError_t rc = pa::make_codes_tensor_map(&e.map, ptr, D, B, block_heads);
+    const cudaError_t rc = pa::make_codes_tensor_map(&e.map, ptr, D, B, block_heads, heads);
     if (rc != cudaSuccess) return rc;
     e.ptr = ptr;
     e.block_heads = block_heads;
     e.D = D;
     e.B = B;
+    e.heads = heads;
     *out = e.map;
     return cudaSuccess;
 }
@@ -150,12 +152,15 @@ int32_t run_mma(pa::Attend8Args &a, const pa_dims *d, const Layout8 &L, void *st
     if (!a.err) return PA_ERR_CUDA;
     CUtensorMap tmk, tmv;
     const long long block_heads = (long long)a.N * a.Hkv;
-    cudaError_t e = codes_map(a.k_cache, a.D, a.B, block_heads, &tmk);
-    if (e == cudaSuccess) e = codes_map(a.v_cache, a.D, a.B, block_heads, &tmv);
+    cudaError_t e = codes_map(a.k_cache, a.D, a.B, block_heads, L.hg, &tmk);
+    if (e == cudaSuccess) e = codes_map(a.v_cache, a.D, a.B, block_heads, L.hg, &tmv);
     if (e != cudaSuccess) return PA_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return to_status(d->kv_dtype == PA_BF16 ? pa::launch_attend8_mma_bf16(a, L.team, tmk, tmv, st)
-                                            : pa::launch_attend8_mma_f16(a, L.team, tmk, tmv, st));
+    if (d->kv_dtype == PA_BF16)
+        e = a.D == 64 ? pa::launch_attend8_mma_bf16_64(a, L.tw, L.hg, tmk, tmv, st) : pa::launch_attend8_mma_bf16_128(a, L.tw, L.hg, tmk, tmv, st);
+    else
+        e = a.D == 64 ? pa::launch_attend8_mma_f16_64(a, L.tw, L.hg, tmk, tmv, st) : pa::launch_attend8_mma_f16_128(a, L.tw, L.hg, tmk, tmv, st);
+    return to_status(e);
 }
 
 int32_t run_umma(pa::Attend8Args &a, const pa_dims *d, void *stream) {

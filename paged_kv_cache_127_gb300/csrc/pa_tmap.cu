@@ -101,12 +101,12 @@ cudaError_t make_output_tensor_map(CUtensorMap *map, float *out, int D, int Hq, 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t make_codes_tensor_map(CUtensorMap *map, const void *codes, int D, int B, long long block_heads) {
+cudaError_t make_codes_tensor_map(CUtensorMap *map, const void *codes, int D, int B, long long block_heads, int heads) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
     if (!enc) return cudaErrorNotSupported;
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)B, (cuuint64_t)block_heads};
     const cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)B * D};
-    const cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)B, 1u};
+    const cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)B, (cuuint32_t)heads};
     const cuuint32_t estr[3] = {1u, 1u, 1u};
     CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(codes), dims, strides, box, estr,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
