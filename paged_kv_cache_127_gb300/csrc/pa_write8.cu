@@ -10,10 +10,11 @@
 // function of the 16-bit inputs alone.
 //
 // Work.  The tokens of one block stand next to each other in the list (a run).  A CTA takes the runs that start
-// among its tile of tokens, so a block's scale has one writer: it reads the keys and values of its rows once for their
-// maxima, settles the scales, turns its queries meanwhile, then reads keys and values again (from L1), and turns, divides and stores
-// them.  grid.y splits the heads.  Rows of a block that were there before are rescaled by the same CTA where the
-// scale grew.  Angles as in pa_rope.cuh, once per (token, pair) in shared memory.
+// among its tile of 16 tokens, for one KV head (two at D 64) with its query heads, so a block's scale has one writer.
+// Sixteen rows of keys and values stay in registers from the maxima, through the scales, to the codes; further rows
+// (runs may begin anywhere in a tile) are read again.  The queries of the same rows are turned while the scales
+// settle, and all first loads are under way before the angles are computed (as in pa_rope.cuh, once per (row, pair) in
+// shared memory).  Rows that a block held before are rescaled by the same CTA where the scale grew.
 //
 // Bound: HBM for a prompt (each q element read and written, each k, v element read as 16 bits and written
 // as 8), latency for a step.
@@ -26,10 +27,9 @@ namespace pa {
 
 namespace {
 
-constexpr int kThreads8 = 256;
-constexpr int kTile = 16;          // tokens of a CTA's tile, at most
+constexpr int kThreads8 = 128;
+constexpr int kTile = 16;          // tokens of a CTA's tile, and rows of a pass
 constexpr int kRows = kTile + 32;  // rows of the runs that start in it, at most (block_size <= 32)
-constexpr int kHeads8 = 8;         // KV heads of a CTA, at most
 
 enum Pairing { kHalves, kNeighbours, kSplit };  // kSplit: halves that are not whole units of 8
 
@@ -91,20 +91,26 @@ __device__ __forceinline__ float scale_of(float x, float most) {
 }
 
 template <typename T, int D, int kPairing>
-__global__ void __launch_bounds__(kThreads8) write8_kernel(const Write8Args a, int tile) {
-    constexpr int L = D / 16;        // lanes of a row: two units of 8 elements each
-    constexpr int RW = 32 / L;       // rows of a warp
-    extern __shared__ float2 cs[];   // [rows][R / 2]
+__global__ void __launch_bounds__(kThreads8) write8_kernel(const Write8Args a) {
+    constexpr int L = D / 16;                 // lanes of a row: two units of 8 elements each
+    constexpr int kHeads = 128 / (kTile * L);  // KV heads of a CTA: 1 (D 128) or 2
+    constexpr int kQ = 4;                     // query heads in flight
+    // [rows][kRow]: a row's (cos, sin), those that one thread needs kCols apart, rows off each other by some banks
+    constexpr int kA = kPairing == kHalves ? 8 : kPairing == kNeighbours ? 4 : 1;   // pairs of a unit
+    constexpr int kCols = D / 2 / kA, kRow = D / 2 + 8;
+    extern __shared__ float2 cs[];
+    __shared__ unsigned long long fractions[D / 2];   // of a turn, per pair: fp64 work, once a CTA
     __shared__ int64_t slots[kRows + 2];
-    __shared__ uint32_t top[2][kHeads8][kRows];   // loudest value of each row (bits)
-    __shared__ float inv[2][kHeads8][kRows];      // per run: 1 / scale
-    __shared__ float ratio[2][kHeads8][kRows];    // per run: old scale / new where the block's earlier rows change, else 1
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    __shared__ uint32_t top[2][kHeads][kRows];   // loudest value of each row (bits)
+    __shared__ float inv[2][kHeads][kRows];      // per run: 1 / scale
+    __shared__ float ratio[2][kHeads][kRows];    // per run: old scale / new where the block's earlier rows change, else 1
+    const int tid = threadIdx.x, lane = tid & 31;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // ---- the runs that start in the tile: slots[j] is token t0 + j - 1
-    const int t0 = blockIdx.x * tile, span = tile + a.B;
+    const int t0 = blockIdx.x * kTile, span = kTile + a.B, half = a.R / 2;
+    if (tid < half) fractions[tid] = turn_fraction(a.freqs[tid]);
     if (tid <= span) {
         const int t = t0 + tid - 1;
         int64_t slot = t >= 0 && t < a.T ? a.slots[t] : -1;
@@ -122,43 +128,122 @@ __global__ void __launch_bounds__(kThreads8) write8_kernel(const Write8Args a, i
     };
     const uint64_t mask = (uint64_t)__ballot_sync(0xffffffffu, starts(lane)) |
                           (uint64_t)__ballot_sync(0xffffffffu, starts(lane + 32)) << 32;
-    const uint64_t mine = mask & ((1ull << tile) - 1ull);
+    const uint64_t mine = mask & ((1ull << kTile) - 1ull);
     if (mine == 0) return;
     const int first = __ffsll((long long)mine) - 1;
-    const uint64_t behind = mask >> tile;
-    const int rows = min(a.T - t0, behind ? tile + __ffsll((long long)behind) - 1 : span - 1) - first;
+    const uint64_t behind = mask >> kTile;
+    const int rows = min(a.T - t0, behind ? kTile + __ffsll((long long)behind) - 1 : span - 1) - first;
     if (rows <= 0) return;
+    auto begins = [&](int r) { return (mask >> (first + r) & 1ull) != 0; };
     auto run_of = [&](int r) { return __popcll((mask >> first) & ((2ull << r) - 1ull)) - 1; };
     auto slot_of = [&](int r) { return slots[1 + first + r]; };
     const int tok0 = t0 + first;
 
-    const int half = kPairing == kNeighbours && a.R == 0 ? 0 : a.R / 2;
-    for (int e = tid; e < rows * half; e += kThreads8) {
-        const int r = e / half, p = e - r * half;
-        cs[e] = turn_at(turn_fraction(a.freqs[p]), pair_position(a, tok0 + r, p), a.mscale);
-    }
-
-    // ---- this part's heads; a lane's two units of a head
-    const int parts = gridDim.y, nq = a.q ? a.Hq / parts : 0, nkv = a.Hkv / parts;
-    const int q0 = blockIdx.y * nq, kv0 = blockIdx.y * nkv;
-    const int lrow = lane / L, c = lane % L;
+    // ---- a thread's row of a pass, its KV head and its two units of a head
+    const int prow = tid / L % kTile, own = tid / (kTile * L), c = tid % L;
+    const bool live_head = blockIdx.y * kHeads + own < a.Hkv;
+    const int h = min((int)blockIdx.y * kHeads + own, a.Hkv - 1);   // KV head
     const int turning = half / 8;
-    const bool turns = kPairing != kHalves || c < turning;  // kHalves: whether the lane's units are a pair that turns
+    const bool turns = kPairing != kHalves || c < turning;  // kHalves: whether the units are a pair that turns
     const int u0 = kPairing == kHalves ? (turns ? 8 * c : a.R + 8 * (c - turning)) : 8 * c;
     const int du = kPairing == kHalves ? (turns ? half : (D - a.R) / 2) : D / 2;
-    const int quads = (rows + RW - 1) / RW;
+    auto load = [&](const T *head, uint4 &x, uint4 &y) {
+        x = *reinterpret_cast<const uint4 *>(head + u0);
+        y = *reinterpret_cast<const uint4 *>(head + u0 + du);
+    };
+    auto k_row = [&](int r) { return static_cast<const T *>(a.k) + (size_t)(tok0 + r) * a.k_stride + (size_t)h * D; };
+    auto v_row = [&](int r) { return static_cast<const T *>(a.v) + (size_t)(tok0 + r) * a.v_stride + (size_t)h * D; };
+    const int G = a.q ? a.Hq / a.Hkv : 0;
+    auto q_row = [&](int r, int n) { return static_cast<const T *>(a.q) + (size_t)(tok0 + r) * a.q_stride + ((size_t)h * G + n) * D; };
 
-    // f: the lane's 16 values of a head, turned.  (x, y) are its units, `head` where they come from.
-    auto turn = [&](const uint4 &x, const uint4 &y, const T *head, const float2 *w, float (&f)[16]) {
+    // ---- the first pass's loads
+    // (threads past the rows or heads load what others do, so that nothing branches around a load)
+    uint4 kx, ky, vx, vy, qx[kQ], qy[kQ];
+    float old_scale = 0.f;   // of K in lane 0 of a run's first row, of V in lane 1
+    {
+        const int r = min(prow, rows - 1);
+        load(k_row(r), kx, ky);
+        load(v_row(r), vx, vy);
+#pragma unroll
+        for (int n = 0; n < kQ; ++n)
+            if (n < G) load(q_row(r, n), qx[n], qy[n]);
+        const int64_t slot = slot_of(r);
+        if (c < 2 && slot >= 0) old_scale = (c ? a.v_scales : a.k_scales)[(size_t)(slot >> lb) * a.Hkv + h];
+    }
+    for (int e = tid; e < rows * half; e += kThreads8) {
+        const int r = e / half, p = e - r * half;
+        cs[r * kRow + p % kA * kCols + p / kA] = turn_at(fractions[p], pair_position(a, tok0 + r, p), a.mscale);
+    }
+
+    // ---- the loudest value of each row and head
+    auto loudest_of_row = [&](const uint4 &x, const uint4 &y) {
+        uint32_t m = loudest<T>(x, y);
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        return m;
+    };
+    for (int r = prow; r < (rows + kTile - 1) / kTile * kTile; r += kTile) {
+        uint4 x = kx, y = ky, z = vx, w = vy;
+        const bool here = r < rows && live_head;
+        if (r >= kTile && here) {
+            load(k_row(r), x, y);
+            load(v_row(r), z, w);
+        }
+        const uint32_t mk = loudest_of_row(x, y), mv = loudest_of_row(z, w);
+        if (c == 0 && here) {
+            top[0][own][r] = mk;
+            top[1][own][r] = mv;
+        }
+    }
+    __syncthreads();
+
+    // ---- the scales of each run: lane 0 of its first row for K, lane 1 for V
+    for (int r = prow; r < rows; r += kTile) {
+        const int64_t slot = slot_of(r);
+        if (c >= 2 || !live_head || slot < 0 || !begins(r)) continue;
+        uint32_t m = top[c][own][r];
+        int off = (int)(slot & (a.B - 1));
+        for (int n = r + 1; n < rows && !begins(n); ++n) {
+            m = max(m, top[c][own][n]);
+            off = min(off, (int)(slot_of(n) & (a.B - 1)));
+        }
+        const float x = Bits16<T>::value(m);
+        float *at = (c ? a.v_scales : a.k_scales) + (size_t)(slot >> lb) * a.Hkv + h;
+        float s = c || half == 0 ? scale_of(x, kLoudestPlain) : scale_of(x * fmaxf(1.f, fabsf(a.mscale)), kLoudestTurned);
+        float grew = 1.f;
+        if (off > 0) {
+            const float old = r < kTile ? old_scale : *at;
+            if (old < s) grew = old / s;
+            else s = fmaxf(old, s);  // an old scale that is no number counts as none
+        }
+        *at = s;
+        const int run = run_of(r);
+        inv[c][own][run] = 1.f / s;
+        ratio[c][own][run] = grew;
+    }
+
+    // f: the 16 values of a head that this thread has, turned by w, its pairs' (cos, sin).  (x, y) are its units, `head`
+    // where they come from.
+    constexpr int kW = kPairing == kSplit ? 1 : 8;
+    auto angles = [&](int r, float2 (&w)[kW]) {
+        if (half == 0) return;  // nothing turns, and no angles were computed
+        if constexpr (kPairing == kHalves) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = cs[r * kRow + e * kCols + (turns ? c : 0)];
+        } else if constexpr (kPairing == kNeighbours) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = cs[r * kRow + (e & 3) * kCols + (e < 4 ? c : c + L)];
+        }
+    };
+    auto turn = [&](const uint4 &x, const uint4 &y, const T *head, int r, const float2 (&w)[kW], float (&f)[16]) {
         Elem<T>::unpack(x, f);
         Elem<T>::unpack(y, f + 8);
         if constexpr (kPairing == kHalves) {
             if (turns) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float2 t = w[8 * c + e];
-                    const float p = f[e] * t.x - f[8 + e] * t.y;
-                    f[8 + e] = f[8 + e] * t.x + f[e] * t.y;
+                    const float p = f[e] * w[e].x - f[8 + e] * w[e].y;
+                    f[8 + e] = f[8 + e] * w[e].x + f[e] * w[e].y;
                     f[e] = p;
                 }
             }
@@ -167,9 +252,8 @@ __global__ void __launch_bounds__(kThreads8) write8_kernel(const Write8Args a, i
             for (int e = 0; e < 8; ++e) {
                 const int p = (e < 4 ? u0 : u0 + du) / 2 + (e & 3);
                 if (p < half) {
-                    const float2 t = w[p];
-                    const float v = f[2 * e] * t.x - f[2 * e + 1] * t.y;
-                    f[2 * e + 1] = f[2 * e + 1] * t.x + f[2 * e] * t.y;
+                    const float v = f[2 * e] * w[e].x - f[2 * e + 1] * w[e].y;
+                    f[2 * e + 1] = f[2 * e + 1] * w[e].x + f[2 * e] * w[e].y;
                     f[2 * e] = v;
                 }
             }
@@ -179,114 +263,59 @@ __global__ void __launch_bounds__(kThreads8) write8_kernel(const Write8Args a, i
                 const int d = (e < 8 ? u0 : u0 + du) + (e & 7);
                 if (d < a.R) {
                     const bool low = d < half;
-                    const float2 t = w[low ? d : d - half];
+                    const float2 t = cs[r * kRow + (low ? d : d - half)];
                     const float other = static_cast<float>(head[low ? d + half : d - half]);
                     f[e] = low ? f[e] * t.x - other * t.y : f[e] * t.x + other * t.y;
                 }
             }
         }
     };
-    auto load = [&](const T *head, uint4 &x, uint4 &y) {
-        x = *reinterpret_cast<const uint4 *>(head + u0);
-        y = *reinterpret_cast<const uint4 *>(head + u0 + du);
-    };
-    auto k_head = [&](int r, int h) { return static_cast<const T *>(a.k) + (size_t)(tok0 + r) * a.k_stride + (size_t)(kv0 + h) * D; };
-    auto v_head = [&](int r, int h) { return static_cast<const T *>(a.v) + (size_t)(tok0 + r) * a.v_stride + (size_t)(kv0 + h) * D; };
-
-    // ---- the loudest value of each row and head
-    for (int task = warp; task < quads * nkv; task += kThreads8 / 32) {
-        const int r = task % quads * RW + lrow, h = task / quads;
-        uint32_t mk = 0, mv = 0;
-        if (r < rows) {
-            uint4 x, y, z, w;
-            load(k_head(r, h), x, y);
-            load(v_head(r, h), z, w);
-            mk = loudest<T>(x, y);
-            mv = loudest<T>(z, w);
-        }
-#pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) {
-            mk = max(mk, __shfl_xor_sync(0xffffffffu, mk, o));
-            mv = max(mv, __shfl_xor_sync(0xffffffffu, mv, o));
-        }
-        if (c == 0 && r < rows) {
-            top[0][h][r] = mk;
-            top[1][h][r] = mv;
-        }
-    }
-    __syncthreads();
-
-    // ---- the scales of each run
-    for (int i = tid; i < rows * nkv * 2; i += kThreads8) {
-        const int r = i % rows, h = i / rows % nkv, which = i / (rows * nkv);
-        if (!(mask >> (first + r) & 1)) continue;  // not a run's first row
-        const int64_t slot = slot_of(r);
-        if (slot < 0) continue;
-        uint32_t m = top[which][h][r];
-        int off = (int)(slot & (a.B - 1));
-        for (int n = r + 1; n < rows && !(mask >> (first + n) & 1); ++n) {
-            m = max(m, top[which][h][n]);
-            off = min(off, (int)(slot_of(n) & (a.B - 1)));
-        }
-        const float x = Bits16<T>::value(m);
-        float *at = (which ? a.v_scales : a.k_scales) + (size_t)(slot >> lb) * a.Hkv + kv0 + h;
-        float s = which || half == 0 ? scale_of(x, kLoudestPlain) : scale_of(x * fmaxf(1.f, fabsf(a.mscale)), kLoudestTurned);
-        float grew = 1.f;
-        if (off > 0) {
-            const float old = *at;
-            if (old < s) grew = old / s;
-            else s = fmaxf(old, s);  // an old scale that is no number counts as none
-        }
-        *at = s;
-        const int run = run_of(r);
-        inv[which][h][run] = 1.f / s;
-        ratio[which][h][run] = grew;
-    }
 
     // ---- queries, while the scales settle
-    constexpr int kQ = 4;
-    const int qchunks = (nq + kQ - 1) / kQ;
-    for (int task = warp; task < quads * qchunks; task += kThreads8 / 32) {
-        const int r = task % quads * RW + lrow, h0 = task / quads * kQ;
-        const bool on = r < rows && slot_of(r < rows ? r : 0) >= 0;
-        uint4 x[kQ], y[kQ];
-        const T *from = static_cast<const T *>(a.q) + (size_t)(tok0 + r) * a.q_stride + (size_t)(q0 + h0) * D;
-        T *to = static_cast<T *>(a.q_out) + (size_t)(tok0 + r) * a.q_out_stride + (size_t)(q0 + h0) * D;
-        if (on) {
+    for (int r = prow; r < (rows + kTile - 1) / kTile * kTile; r += kTile) {
+        const bool here = r < rows && live_head && slot_of(r < rows ? r : 0) >= 0;
+        float2 w[kW];
+        if (here) angles(r, w);
+        for (int n0 = 0; n0 < G; n0 += kQ) {
+            if (here) {
+                if (r >= kTile || n0 > 0) {
 #pragma unroll
-            for (int u = 0; u < kQ; ++u)
-                if (h0 + u < nq) load(from + u * D, x[u], y[u]);
-#pragma unroll
-            for (int u = 0; u < kQ; ++u) {
-                if (h0 + u >= nq) break;
-                float f[16];
-                turn(x[u], y[u], from + u * D, cs + r * half, f);
-                x[u] = make_uint4(Mma16<T>::pack(f[0], f[1]), Mma16<T>::pack(f[2], f[3]), Mma16<T>::pack(f[4], f[5]), Mma16<T>::pack(f[6], f[7]));
-                y[u] = make_uint4(Mma16<T>::pack(f[8], f[9]), Mma16<T>::pack(f[10], f[11]), Mma16<T>::pack(f[12], f[13]), Mma16<T>::pack(f[14], f[15]));
-            }
-        }
-        __syncwarp();  // q_out may be q: the warp has read its rows
-        if (on) {
-#pragma unroll
-            for (int u = 0; u < kQ; ++u)
-                if (h0 + u < nq) {
-                    *reinterpret_cast<uint4 *>(to + u * D + u0) = x[u];
-                    *reinterpret_cast<uint4 *>(to + u * D + u0 + du) = y[u];
+                    for (int n = 0; n < kQ; ++n)
+                        if (n0 + n < G) load(q_row(r, n0 + n), qx[n], qy[n]);
                 }
+#pragma unroll
+                for (int n = 0; n < kQ; ++n) {
+                    if (n0 + n >= G) break;
+                    float f[16];
+                    turn(qx[n], qy[n], q_row(r, n0 + n), r, w, f);
+                    qx[n] = make_uint4(Mma16<T>::pack(f[0], f[1]), Mma16<T>::pack(f[2], f[3]), Mma16<T>::pack(f[4], f[5]), Mma16<T>::pack(f[6], f[7]));
+                    qy[n] = make_uint4(Mma16<T>::pack(f[8], f[9]), Mma16<T>::pack(f[10], f[11]), Mma16<T>::pack(f[12], f[13]), Mma16<T>::pack(f[14], f[15]));
+                }
+            }
+            __syncwarp();  // q_out may be q: the lanes of a row have read it
+            if (here) {
+                T *to = static_cast<T *>(a.q_out) + (size_t)(tok0 + r) * a.q_out_stride + ((size_t)h * G + n0) * D + u0;
+#pragma unroll
+                for (int n = 0; n < kQ; ++n)
+                    if (n0 + n < G) {
+                        *reinterpret_cast<uint4 *>(to + n * D) = qx[n];
+                        *reinterpret_cast<uint4 *>(to + n * D + du) = qy[n];
+                    }
+            }
         }
     }
     __syncthreads();
 
     // ---- keys and values
-    for (int task = warp; task < quads * nkv; task += kThreads8 / 32) {
-        const int r = task % quads * RW + lrow, h = task / quads;
-        if (r >= rows || slot_of(r) < 0) continue;
+    for (int r = prow; r < rows && live_head; r += kTile) {
         const int64_t slot = slot_of(r);
+        if (slot < 0) continue;
+        if (r >= kTile) {
+            load(k_row(r), kx, ky);
+            load(v_row(r), vx, vy);
+        }
         const int run = run_of(r);
-        const size_t at = (((size_t)(slot >> lb) * a.Hkv + kv0 + h) * a.B + (size_t)(slot & (a.B - 1))) * D;
-        uint4 x, y, z, w;
-        load(k_head(r, h), x, y);
-        load(v_head(r, h), z, w);
+        const size_t at = (((size_t)(slot >> lb) * a.Hkv + h) * a.B + (size_t)(slot & (a.B - 1))) * D;
         float f[16];
         auto store = [&](uint8_t *row, float s) {
             uint32_t p[8];
@@ -295,23 +324,25 @@ __global__ void __launch_bounds__(kThreads8) write8_kernel(const Write8Args a, i
             *reinterpret_cast<uint2 *>(row + u0) = make_uint2(p[0] | p[1] << 16, p[2] | p[3] << 16);
             *reinterpret_cast<uint2 *>(row + u0 + du) = make_uint2(p[4] | p[5] << 16, p[6] | p[7] << 16);
         };
-        turn(x, y, k_head(r, h), cs + r * half, f);
-        store(a.k_cache + at, inv[0][h][run]);
-        Elem<T>::unpack(z, f);
-        Elem<T>::unpack(w, f + 8);
-        store(a.v_cache + at, inv[1][h][run]);
+        float2 w[kW];
+        angles(r, w);
+        turn(kx, ky, k_row(r), r, w, f);
+        store(a.k_cache + at, inv[0][own][run]);
+        Elem<T>::unpack(vx, f);
+        Elem<T>::unpack(vy, f + 8);
+        store(a.v_cache + at, inv[1][own][run]);
     }
 
     // ---- the rows that a block held before, where its scale grew
-    for (int task = warp; task < rows * nkv * 2; task += kThreads8 / 32) {
-        const int r = task % rows, h = task / rows % nkv, which = task / (rows * nkv);
-        if (!(mask >> (first + r) & 1) || slot_of(r) < 0) continue;
-        const float s = ratio[which][h][run_of(r)];
-        if (s == 1.f) continue;
+    for (int task = tid >> 5; task < rows * 2 * kHeads; task += kThreads8 / 32) {
+        const int r = task % rows, which = task / rows & 1, o = task / (2 * rows);
         const int64_t slot = slot_of(r);
+        if (!begins(r) || slot < 0 || blockIdx.y * kHeads + o >= a.Hkv) continue;
+        const float s = ratio[which][o][run_of(r)];
+        if (s == 1.f) continue;
         int off = (int)(slot & (a.B - 1));
-        for (int n = r + 1; n < rows && !(mask >> (first + n) & 1); ++n) off = min(off, (int)(slot_of(n) & (a.B - 1)));
-        uint8_t *block = (which ? a.v_cache : a.k_cache) + ((size_t)(slot >> lb) * a.Hkv + kv0 + h) * a.B * D;
+        for (int n = r + 1; n < rows && !begins(n); ++n) off = min(off, (int)(slot_of(n) & (a.B - 1)));
+        uint8_t *block = (which ? a.v_cache : a.k_cache) + ((size_t)(slot >> lb) * a.Hkv + blockIdx.y * kHeads + o) * a.B * D;
         for (int i = lane * 4; i < off * D; i += 128) {
             const uint32_t w = *reinterpret_cast<const uint32_t *>(block + i);
             const float2 lo = values2(w & 0xffffu), hi = values2(w >> 16);
@@ -337,17 +368,13 @@ cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, int threads, si
 
 template <typename T, int D>
 cudaError_t launch_write8_t(const Write8Args &a, cudaStream_t st) {
-    // Few tokens: small tiles and the heads over several CTAs, so that a step's loads are all in flight at
-    // once.  Many: tiles of 16, whose angles then serve all of their heads.
-    const int tile = a.T >= 4 * 152 * 4 ? kTile : 4;
-    const int tiles = (a.T + tile - 1) / tile;
-    int parts = 1;
-    while (parts < a.Hkv && (a.Hkv % parts != 0 || a.Hkv / parts > kHeads8 || (long long)tiles * parts < 4 * 152)) ++parts;
-    const dim3 grid((unsigned)tiles, (unsigned)parts);
-    const size_t smem = (size_t)(tile + a.B) * (a.R / 2) * sizeof(float2);  // at most 24 KB
-    if (a.R == 0 || a.interleaved) return launch_dependent(write8_kernel<T, D, kNeighbours>, grid, kThreads8, smem, st, a, tile);
-    if (a.R % 16 == 0) return launch_dependent(write8_kernel<T, D, kHalves>, grid, kThreads8, smem, st, a, tile);
-    return launch_dependent(write8_kernel<T, D, kSplit>, grid, kThreads8, smem, st, a, tile);
+    constexpr int kHeads = 128 / (kTile * (D / 16));
+    const dim3 grid((unsigned)((a.T + kTile - 1) / kTile), (unsigned)((a.Hkv + kHeads - 1) / kHeads));
+    if (grid.y > 65535) return cudaErrorNotSupported;
+    const size_t smem = a.R ? (size_t)(kTile + a.B) * (D / 2 + 8) * sizeof(float2) : 0;  // at most 27 KB
+    if (a.R == 0 || a.interleaved) return launch_dependent(write8_kernel<T, D, kNeighbours>, grid, kThreads8, smem, st, a);
+    if (a.R % 16 == 0) return launch_dependent(write8_kernel<T, D, kHalves>, grid, kThreads8, smem, st, a);
+    return launch_dependent(write8_kernel<T, D, kSplit>, grid, kThreads8, smem, st, a);
 }
 
 // grid (pairs, K and V): a block's codes in 16-byte units, and its scales.
