@@ -9,12 +9,14 @@
 // louder (a code only loses bits where it becomes subnormal).  The bound before the rotation makes the scale a
 // function of the 16-bit inputs alone.
 //
-// Work.  The tokens of one block stand next to each other in the list (a run).  A CTA takes the runs that start
-// among its tile of 16 tokens, for one KV head (two at D 64) with its query heads, so a block's scale has one writer.
-// Sixteen rows of keys and values stay in registers from the maxima, through the scales, to the codes; further rows
-// (runs may begin anywhere in a tile) are read again.  The queries of the same rows are turned while the scales
-// settle, and all first loads are under way before the angles are computed (as in pa_rope.cuh, once per (row, pair) in
-// shared memory).  Rows that a block held before are rescaled by the same CTA where the scale grew.
+// Work.  Two kinds of CTAs in one launch.  One kind takes keys and values: the tokens of one block stand next to each
+// other in the list (a run), and a CTA takes the runs that start among its tile of 16 tokens, for some of the KV heads,
+// one after the other (at D 64 two at a time), so a block's scale has one writer.  Sixteen rows of a head's keys
+// and values stay in registers from the maxima, through the scales, to the codes, while the next head's are on their way;
+// further rows (runs may begin anywhere in a tile) are read again.  Rows that a block held before are rescaled by the
+// same CTA where the scale grew.  The other kind turns the queries of two tokens each, as the write into a 16-bit cache
+// does.  First loads are under way before the angles are computed (as in pa_rope.cuh, once per (row, pair), in shared memory).
+// (Queries in the same CTAs as their KV head: 63 us instead of 39 for 8192 tokens of 32 + 8 heads, as each head then pays for the angles.)
 //
 // Bound: HBM for a prompt (each q element read and written, each k, v element read as 16 bits and written
 // as 8), latency for a step.
@@ -90,26 +92,156 @@ __device__ __forceinline__ float scale_of(float x, float most) {
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
+// What a thread has of a head: two units of 8 elements, u0 and u0 + du, that turn with each other or each with itself.
 template <typename T, int D, int kPairing>
-__global__ void __launch_bounds__(kThreads8) write8_kernel(const Write8Args a) {
-    constexpr int L = D / 16;                 // lanes of a row: two units of 8 elements each
-    constexpr int kHeads = 128 / (kTile * L);  // KV heads of a CTA: 1 (D 128) or 2
-    constexpr int kQ = 4;                     // query heads in flight
-    // [rows][kRow]: a row's (cos, sin), those that one thread needs kCols apart, rows off each other by some banks
-    constexpr int kA = kPairing == kHalves ? 8 : kPairing == kNeighbours ? 4 : 1;   // pairs of a unit
-    constexpr int kCols = D / 2 / kA, kRow = D / 2 + 8;
+struct Part8 {
+    static constexpr int L = D / 16;                                                     // lanes of a row
+    static constexpr int kA = kPairing == kHalves ? 8 : kPairing == kNeighbours ? 4 : 1;  // pairs of a unit
+    // (cos, sin) of a row: those that one thread needs kCols apart, rows off each other by some banks
+    static constexpr int kCols = D / 2 / kA, kRow = D / 2 + 8;
+    static constexpr int kW = kPairing == kSplit ? 1 : 8;
+    int R, half, c, u0, du;
+    bool turns;   // kHalves: whether the units are a pair that turns
+    __device__ __forceinline__ Part8(int R_, int lane) : R(R_), half(R_ / 2), c(lane) {
+        const int turning = half / 8;
+        turns = kPairing != kHalves || c < turning;
+        u0 = kPairing == kHalves ? (turns ? 8 * c : R + 8 * (c - turning)) : 8 * c;
+        du = kPairing == kHalves ? (turns ? half : (D - R) / 2) : D / 2;
+    }
+    static __device__ __forceinline__ int place(int r, int p) { return r * kRow + p % kA * kCols + p / kA; }
+    __device__ __forceinline__ void load(const T *head, uint4 &x, uint4 &y) const {
+        x = *reinterpret_cast<const uint4 *>(head + u0);
+        y = *reinterpret_cast<const uint4 *>(head + u0 + du);
+    }
+    // its pairs' (cos, sin) of row r
+    __device__ __forceinline__ void angles(const float2 *cs, int r, float2 (&w)[kW]) const {
+        if (half == 0) return;  // nothing turns, and no angles were computed
+        if constexpr (kPairing == kHalves) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = cs[r * kRow + e * kCols + (turns ? c : 0)];
+        } else if constexpr (kPairing == kNeighbours) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = cs[r * kRow + (e & 3) * kCols + (e < 4 ? c : c + L)];
+        }
+    }
+    // The 16 values, turned by w (kSplit: by row r of cs).  (x, y) are its units, `head` where they come from.
+    __device__ __forceinline__ void turn(const uint4 &x, const uint4 &y, const T *head, const float2 *cs, int r,
+                                         const float2 (&w)[kW], float (&f)[16]) const {
+        Elem<T>::unpack(x, f);
+        Elem<T>::unpack(y, f + 8);
+        if constexpr (kPairing == kHalves) {
+            if (turns) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float p = f[e] * w[e].x - f[8 + e] * w[e].y;
+                    f[8 + e] = f[8 + e] * w[e].x + f[e] * w[e].y;
+                    f[e] = p;
+                }
+            }
+        } else if constexpr (kPairing == kNeighbours) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int p = (e < 4 ? u0 : u0 + du) / 2 + (e & 3);
+                if (p < half) {
+                    const float v = f[2 * e] * w[e].x - f[2 * e + 1] * w[e].y;
+                    f[2 * e + 1] = f[2 * e + 1] * w[e].x + f[2 * e] * w[e].y;
+                    f[2 * e] = v;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int d = (e < 8 ? u0 : u0 + du) + (e & 7);
+                if (d < R) {
+                    const bool low = d < half;
+                    const float2 t = cs[r * kRow + (low ? d : d - half)];
+                    const float other = static_cast<float>(head[low ? d + half : d - half]);
+                    f[e] = low ? f[e] * t.x - other * t.y : f[e] * t.x + other * t.y;
+                }
+            }
+        }
+    }
+};
+
+// The queries of tokens t0, t0 + 1, every parts-th round of their heads.
+template <typename T, int D, int kPairing>
+__device__ __forceinline__ void turn_queries(const Write8Args &a, int t0, int part, int parts, float2 *cs) {
+    using P = Part8<T, D, kPairing>;
+    constexpr int kU = 4, kStep = kThreads8 / P::L;   // heads of a thread in flight; heads of a round
+    const P my(a.R, threadIdx.x % P::L);
+    const int nt = min(2, a.T - t0), all = nt * a.Hq, step = kStep * parts;
+    auto head = [&](int m) { return static_cast<const T *>(a.q) + (size_t)(t0 + (m >= a.Hq)) * a.q_stride + (size_t)(m >= a.Hq ? m - a.Hq : m) * D; };
+    uint4 x[kU], y[kU];
+    auto load = [&](int m0) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u) my.load(head(min(m0 + u * step, all - 1)), x[u], y[u]);  // past the end: what others load
+    };
+    const int m0 = part * kStep + threadIdx.x / P::L;
+    load(m0);
+    bool on[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int64_t slot = t < nt ? a.slots[t0 + t] : -1;
+        on[t] = slot >= 0 && slot < (int64_t)a.N * a.B;   // (the CTAs of keys and values report the others)
+    }
+    for (int e = threadIdx.x; e < nt * my.half; e += kThreads8) {
+        const int r = e / my.half, p = e - r * my.half;
+        cs[P::place(r, p)] = turn_at(turn_fraction(a.freqs[p]), pair_position(a, t0 + r, p), a.mscale);
+    }
+    __syncthreads();
+    for (int m1 = m0; m1 - (int)threadIdx.x / P::L < all; m1 += kU * step) {   // the same rounds for the whole CTA
+        if (m1 != m0) load(m1);
+        float2 w[P::kW];
+        int row = -1;
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int m = min(m1 + u * step, all - 1), r = m >= a.Hq;
+            if (r != row) my.angles(cs, row = r, w);
+            float f[16];
+            my.turn(x[u], y[u], head(m), cs, r, w, f);
+            x[u] = make_uint4(Mma16<T>::pack(f[0], f[1]), Mma16<T>::pack(f[2], f[3]), Mma16<T>::pack(f[4], f[5]), Mma16<T>::pack(f[6], f[7]));
+            y[u] = make_uint4(Mma16<T>::pack(f[8], f[9]), Mma16<T>::pack(f[10], f[11]), Mma16<T>::pack(f[12], f[13]), Mma16<T>::pack(f[14], f[15]));
+        }
+        __syncwarp();  // q_out may be q: the lanes of a head have read it
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int m = m1 + u * step;
+            if (m >= all || !(m >= a.Hq ? on[1] : on[0])) continue;
+            T *to = static_cast<T *>(a.q_out) + (size_t)(t0 + (m >= a.Hq)) * a.q_out_stride + (size_t)(m >= a.Hq ? m - a.Hq : m) * D + my.u0;
+            *reinterpret_cast<uint4 *>(to) = x[u];
+            *reinterpret_cast<uint4 *>(to + my.du) = y[u];
+        }
+    }
+}
+
+// grid: tiles * kv_parts CTAs of keys and values, which take longest, then those of the queries, q_parts for two tokens.
+template <typename T, int D, int kPairing>
+__global__ void __launch_bounds__(kThreads8, kPairing == kSplit ? 3 : 7) write8_kernel(const Write8Args a, int kv_parts, int q_parts) {
+    using P = Part8<T, D, kPairing>;
+    constexpr int L = P::L;
+    constexpr int kHeads = kThreads8 / (kTile * L);  // KV heads at a time: 1 (D 128) or 2
     extern __shared__ float2 cs[];
     __shared__ unsigned long long fractions[D / 2];   // of a turn, per pair: fp64 work, once a CTA
     __shared__ int64_t slots[kRows + 2];
-    __shared__ uint32_t top[2][kHeads][kRows];   // loudest value of each row (bits)
-    __shared__ float inv[2][kHeads][kRows];      // per run: 1 / scale
-    __shared__ float ratio[2][kHeads][kRows];    // per run: old scale / new where the block's earlier rows change, else 1
+    __shared__ uint32_t top[2][kRows][2 * kHeads];  // per run: its loudest value of K and of V (bits), for heads in turn
+    __shared__ float inv[kRows][2 * kHeads];        // per run: 1 / scale
+    __shared__ float ratio[kRows][2 * kHeads];      // per run: old scale / new where the block's earlier rows change, else 1
+    __shared__ int run_row[kRows], run_off[kRows];  // per run: its first row, and the first slot of its block that it takes
+    __shared__ int grown[2];                        // whether some ratio is not 1, for heads in turn
     const int tid = threadIdx.x, lane = tid & 31;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int kv_ctas = (a.T + kTile - 1) / kTile * kv_parts;
+    if ((int)blockIdx.x >= kv_ctas) {
+        const int i = blockIdx.x - kv_ctas;
+        turn_queries<T, D, kPairing>(a, i / q_parts * 2, i % q_parts, q_parts, cs);
+        return;
+    }
 
     // ---- the runs that start in the tile: slots[j] is token t0 + j - 1
-    const int t0 = blockIdx.x * kTile, span = kTile + a.B, half = a.R / 2;
+    const P my(a.R, tid % L);
+    const int half = my.half;
+    const int t0 = (int)(blockIdx.x / kv_parts) * kTile, span = kTile + a.B;
     if (tid < half) fractions[tid] = turn_fraction(a.freqs[tid]);
     if (tid <= span) {
         const int t = t0 + tid - 1;
@@ -139,215 +271,153 @@ __global__ void __launch_bounds__(kThreads8) write8_kernel(const Write8Args a) {
     auto slot_of = [&](int r) { return slots[1 + first + r]; };
     const int tok0 = t0 + first;
 
-    // ---- a thread's row of a pass, its KV head and its two units of a head
-    const int prow = tid / L % kTile, own = tid / (kTile * L), c = tid % L;
-    const bool live_head = blockIdx.y * kHeads + own < a.Hkv;
-    const int h = min((int)blockIdx.y * kHeads + own, a.Hkv - 1);   // KV head
-    const int turning = half / 8;
-    const bool turns = kPairing != kHalves || c < turning;  // kHalves: whether the units are a pair that turns
-    const int u0 = kPairing == kHalves ? (turns ? 8 * c : a.R + 8 * (c - turning)) : 8 * c;
-    const int du = kPairing == kHalves ? (turns ? half : (D - a.R) / 2) : D / 2;
-    auto load = [&](const T *head, uint4 &x, uint4 &y) {
-        x = *reinterpret_cast<const uint4 *>(head + u0);
-        y = *reinterpret_cast<const uint4 *>(head + u0 + du);
-    };
-    auto k_row = [&](int r) { return static_cast<const T *>(a.k) + (size_t)(tok0 + r) * a.k_stride + (size_t)h * D; };
-    auto v_row = [&](int r) { return static_cast<const T *>(a.v) + (size_t)(tok0 + r) * a.v_stride + (size_t)h * D; };
-    const int G = a.q ? a.Hq / a.Hkv : 0;
-    auto q_row = [&](int r, int n) { return static_cast<const T *>(a.q) + (size_t)(tok0 + r) * a.q_stride + ((size_t)h * G + n) * D; };
-
-    // ---- the first pass's loads
-    // (threads past the rows or heads load what others do, so that nothing branches around a load)
-    uint4 kx, ky, vx, vy, qx[kQ], qy[kQ];
-    float old_scale = 0.f;   // of K in lane 0 of a run's first row, of V in lane 1
-    {
-        const int r = min(prow, rows - 1);
-        load(k_row(r), kx, ky);
-        load(v_row(r), vx, vy);
-#pragma unroll
-        for (int n = 0; n < kQ; ++n)
-            if (n < G) load(q_row(r, n), qx[n], qy[n]);
-        const int64_t slot = slot_of(r);
-        if (c < 2 && slot >= 0) old_scale = (c ? a.v_scales : a.k_scales)[(size_t)(slot >> lb) * a.Hkv + h];
+    // ---- what the runs are, once for all heads
+    const int runs = __popcll((mask >> first) & ((1ull << rows) - 1ull));
+    if (tid < rows && begins(tid)) {
+        const int run = run_of(tid);
+        int off = 0;
+        if (slot_of(tid) >= 0) {
+            off = (int)(slot_of(tid) & (a.B - 1));
+            for (int n = tid + 1; n < rows && !begins(n); ++n) off = min(off, (int)(slot_of(n) & (a.B - 1)));
+        }
+        run_row[run] = tid;
+        run_off[run] = off;
     }
+    for (int i = tid; i < runs * 2 * kHeads; i += kThreads8) top[0][i / (2 * kHeads)][i % (2 * kHeads)] = 0u;
+    if (tid < 2) grown[tid] = 0;
+
+    // ---- a thread's row of a pass, and its KV head h (of the part's, kHeads at a time)
+    const int prow = tid / L % kTile, own = tid / (kTile * L), c = my.c, prun = prow < rows ? run_of(prow) : 0;
+    const int per = (a.Hkv + kv_parts - 1) / kv_parts, h0 = (int)(blockIdx.x % kv_parts) * per, h_end = min(a.Hkv, h0 + per);
+    auto k_row = [&](int r, int h) { return static_cast<const T *>(a.k) + (size_t)(tok0 + r) * a.k_stride + (size_t)h * D; };
+    auto v_row = [&](int r, int h) { return static_cast<const T *>(a.v) + (size_t)(tok0 + r) * a.v_stride + (size_t)h * D; };
+    // the first pass's rows of a head (threads past the rows or heads load what others do, so that nothing branches around a load)
+    uint4 kx, ky, vx, vy, kx1, ky1, vx1, vy1;
+    auto fetch = [&](int h, uint4 &k0, uint4 &k1, uint4 &v0, uint4 &v1) {
+        const int r = min(prow, rows - 1);
+        h = min(h, a.Hkv - 1);
+        my.load(k_row(r, h), k0, k1);
+        my.load(v_row(r, h), v0, v1);
+    };
+    if (h0 >= h_end) return;
+    fetch(h0 + own, kx, ky, vx, vy);
     for (int e = tid; e < rows * half; e += kThreads8) {
         const int r = e / half, p = e - r * half;
-        cs[r * kRow + p % kA * kCols + p / kA] = turn_at(fractions[p], pair_position(a, tok0 + r, p), a.mscale);
+        cs[P::place(r, p)] = turn_at(fractions[p], pair_position(a, tok0 + r, p), a.mscale);
     }
-
-    // ---- the loudest value of each row and head
+    __syncthreads();
     auto loudest_of_row = [&](const uint4 &x, const uint4 &y) {
         uint32_t m = loudest<T>(x, y);
 #pragma unroll
         for (int o = L / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
         return m;
     };
-    for (int r = prow; r < (rows + kTile - 1) / kTile * kTile; r += kTile) {
-        uint4 x = kx, y = ky, z = vx, w = vy;
-        const bool here = r < rows && live_head;
-        if (r >= kTile && here) {
-            load(k_row(r), x, y);
-            load(v_row(r), z, w);
-        }
-        const uint32_t mk = loudest_of_row(x, y), mv = loudest_of_row(z, w);
-        if (c == 0 && here) {
-            top[0][own][r] = mk;
-            top[1][own][r] = mv;
-        }
-    }
-    __syncthreads();
 
-    // ---- the scales of each run: lane 0 of its first row for K, lane 1 for V
-    for (int r = prow; r < rows; r += kTile) {
-        const int64_t slot = slot_of(r);
-        if (c >= 2 || !live_head || slot < 0 || !begins(r)) continue;
-        uint32_t m = top[c][own][r];
-        int off = (int)(slot & (a.B - 1));
-        for (int n = r + 1; n < rows && !begins(n); ++n) {
-            m = max(m, top[c][own][n]);
-            off = min(off, (int)(slot_of(n) & (a.B - 1)));
-        }
-        const float x = Bits16<T>::value(m);
-        float *at = (c ? a.v_scales : a.k_scales) + (size_t)(slot >> lb) * a.Hkv + h;
-        float s = c || half == 0 ? scale_of(x, kLoudestPlain) : scale_of(x * fmaxf(1.f, fabsf(a.mscale)), kLoudestTurned);
-        float grew = 1.f;
-        if (off > 0) {
-            const float old = r < kTile ? old_scale : *at;
-            if (old < s) grew = old / s;
-            else s = fmaxf(old, s);  // an old scale that is no number counts as none
-        }
-        *at = s;
-        const int run = run_of(r);
-        inv[c][own][run] = 1.f / s;
-        ratio[c][own][run] = grew;
-    }
-
-    // f: the 16 values of a head that this thread has, turned by w, its pairs' (cos, sin).  (x, y) are its units, `head`
-    // where they come from.
-    constexpr int kW = kPairing == kSplit ? 1 : 8;
-    auto angles = [&](int r, float2 (&w)[kW]) {
-        if (half == 0) return;  // nothing turns, and no angles were computed
-        if constexpr (kPairing == kHalves) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = cs[r * kRow + e * kCols + (turns ? c : 0)];
-        } else if constexpr (kPairing == kNeighbours) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = cs[r * kRow + (e & 3) * kCols + (e < 4 ? c : c + L)];
-        }
+    // thread i: run i / (2 kHeads), of head own_i, K or V
+    const int run_i = tid / (2 * kHeads), which_i = tid & 1, own_i = (tid >> 1) % kHeads;
+    auto scale_at = [&](int run, int which, int h) {
+        return (which ? a.v_scales : a.k_scales) + (size_t)(slot_of(run_row[run]) >> lb) * a.Hkv + h;
     };
-    auto turn = [&](const uint4 &x, const uint4 &y, const T *head, int r, const float2 (&w)[kW], float (&f)[16]) {
-        Elem<T>::unpack(x, f);
-        Elem<T>::unpack(y, f + 8);
-        if constexpr (kPairing == kHalves) {
-            if (turns) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float p = f[e] * w[e].x - f[8 + e] * w[e].y;
-                    f[8 + e] = f[8 + e] * w[e].x + f[e] * w[e].y;
-                    f[e] = p;
-                }
-            }
-        } else if constexpr (kPairing == kNeighbours) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int p = (e < 4 ? u0 : u0 + du) / 2 + (e & 3);
-                if (p < half) {
-                    const float v = f[2 * e] * w[e].x - f[2 * e + 1] * w[e].y;
-                    f[2 * e + 1] = f[2 * e + 1] * w[e].x + f[2 * e] * w[e].y;
-                    f[2 * e] = v;
-                }
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int d = (e < 8 ? u0 : u0 + du) + (e & 7);
-                if (d < a.R) {
-                    const bool low = d < half;
-                    const float2 t = cs[r * kRow + (low ? d : d - half)];
-                    const float other = static_cast<float>(head[low ? d + half : d - half]);
-                    f[e] = low ? f[e] * t.x - other * t.y : f[e] * t.x + other * t.y;
-                }
-            }
-        }
+    auto old_of = [&](int hb) {   // the old scale of this thread's run and head, where it counts
+        if (run_i >= runs || hb + own_i >= h_end || slot_of(run_row[run_i]) < 0 || run_off[run_i] == 0) return 0.f;
+        return *scale_at(run_i, which_i, hb + own_i);
     };
+    float old = old_of(h0);
+    int turn_of = 0;
+    for (int hb = h0; hb < h_end; hb += kHeads, turn_of ^= 1) {
+        const int h = hb + own;
+        const bool live = h < h_end;
+        // ---- the loudest value of each run
+        for (int r = prow; r < (rows + kTile - 1) / kTile * kTile; r += kTile) {
+            uint4 x = kx, y = ky, z = vx, w = vy;
+            const bool here = r < rows && live;
+            if (r >= kTile && here) {
+                my.load(k_row(r, h), x, y);
+                my.load(v_row(r, h), z, w);
+            }
+            const uint32_t mk = loudest_of_row(x, y), mv = loudest_of_row(z, w);
+            if (c < 2 && here) atomicMax(&top[turn_of][r < kTile ? prun : run_of(r)][2 * own + c], c ? mv : mk);
+        }
+        if (hb + kHeads < h_end) fetch(h + kHeads, kx1, ky1, vx1, vy1);
+        __syncthreads();
 
-    // ---- queries, while the scales settle
-    for (int r = prow; r < (rows + kTile - 1) / kTile * kTile; r += kTile) {
-        const bool here = r < rows && live_head && slot_of(r < rows ? r : 0) >= 0;
-        float2 w[kW];
-        if (here) angles(r, w);
-        for (int n0 = 0; n0 < G; n0 += kQ) {
-            if (here) {
-                if (r >= kTile || n0 > 0) {
+        // ---- the scales of each run, and the next head's maxima set back
+        for (int i = tid; i < runs * 2 * kHeads; i += kThreads8) {
+            const int run = i / (2 * kHeads), which = i & 1, o = (i >> 1) % kHeads;
+            const uint32_t m = top[turn_of][run][i % (2 * kHeads)];
+            top[turn_of ^ 1][run][i % (2 * kHeads)] = 0u;
+            if (hb + o >= h_end || slot_of(run_row[run]) < 0) continue;
+            const float x = Bits16<T>::value(m);
+            float s = which || half == 0 ? scale_of(x, kLoudestPlain) : scale_of(x * fmaxf(1.f, fabsf(a.mscale)), kLoudestTurned);
+            float grew = 1.f;
+            float *at = scale_at(run, which, hb + o);
+            if (run_off[run] > 0) {
+                const float was = i == tid ? old : *at;
+                if (was < s) grew = was / s;
+                else s = fmaxf(was, s);  // an old scale that is no number counts as none
+            }
+            *at = s;
+            inv[run][i % (2 * kHeads)] = 1.f / s;
+            ratio[run][i % (2 * kHeads)] = grew;
+            if (grew != 1.f) grown[turn_of] = 1;
+        }
+        if (tid == 0) grown[turn_of ^ 1] = 0;
+        if (hb + kHeads < h_end) old = old_of(hb + kHeads);
+        __syncthreads();
+
+        // ---- keys and values
+        for (int r = prow; r < rows && live; r += kTile) {
+            const int64_t slot = slot_of(r);
+            if (slot < 0) continue;
+            if (r >= kTile) {
+                my.load(k_row(r, h), kx, ky);
+                my.load(v_row(r, h), vx, vy);
+            }
+            const int run = r < kTile ? prun : run_of(r);
+            const size_t at = (((size_t)(slot >> lb) * a.Hkv + h) * a.B + (size_t)(slot & (a.B - 1))) * D;
+            float f[16];
+            auto store = [&](uint8_t *row, float s) {
+                uint32_t p[8];
 #pragma unroll
-                    for (int n = 0; n < kQ; ++n)
-                        if (n0 + n < G) load(q_row(r, n0 + n), qx[n], qy[n]);
-                }
+                for (int e = 0; e < 8; ++e) p[e] = codes2(f[2 * e] * s, f[2 * e + 1] * s);
+                *reinterpret_cast<uint2 *>(row + my.u0) = make_uint2(p[0] | p[1] << 16, p[2] | p[3] << 16);
+                *reinterpret_cast<uint2 *>(row + my.u0 + my.du) = make_uint2(p[4] | p[5] << 16, p[6] | p[7] << 16);
+            };
+            float2 w[P::kW];
+            my.angles(cs, r, w);
+            my.turn(kx, ky, k_row(r, h), cs, r, w, f);
+            store(a.k_cache + at, inv[run][2 * own]);
+            Elem<T>::unpack(vx, f);
+            Elem<T>::unpack(vy, f + 8);
+            store(a.v_cache + at, inv[run][2 * own + 1]);
+        }
+
+        // ---- the rows that a block held before, where its scale grew
+        for (int task = tid >> 5; grown[turn_of] && task < runs * 2 * kHeads; task += kThreads8 / 32) {
+            const int run = task / (2 * kHeads), which = task & 1, o = (task >> 1) % kHeads;
+            const int64_t slot = slot_of(run_row[run]);
+            if (slot < 0 || hb + o >= h_end) continue;
+            const float s = ratio[run][task % (2 * kHeads)];
+            if (s == 1.f) continue;
+            const int off = run_off[run];
+            uint8_t *block = (which ? a.v_cache : a.k_cache) + ((size_t)(slot >> lb) * a.Hkv + hb + o) * a.B * D;
+            // a lane's 16 codes of every 512, four loads in flight (a block has at most 4096)
+            for (int i0 = lane * 16; i0 < off * D; i0 += 2048) {
+                uint4 w[4];
 #pragma unroll
-                for (int n = 0; n < kQ; ++n) {
-                    if (n0 + n >= G) break;
-                    float f[16];
-                    turn(qx[n], qy[n], q_row(r, n0 + n), r, w, f);
-                    qx[n] = make_uint4(Mma16<T>::pack(f[0], f[1]), Mma16<T>::pack(f[2], f[3]), Mma16<T>::pack(f[4], f[5]), Mma16<T>::pack(f[6], f[7]));
-                    qy[n] = make_uint4(Mma16<T>::pack(f[8], f[9]), Mma16<T>::pack(f[10], f[11]), Mma16<T>::pack(f[12], f[13]), Mma16<T>::pack(f[14], f[15]));
+                for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4 *>(block + min(i0 + 512 * i, off * D - 16));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    auto again = [&](uint32_t x) {
+                        const float2 lo = values2(x & 0xffffu), hi = values2(x >> 16);
+                        return codes2(lo.x * s, lo.y * s) | codes2(hi.x * s, hi.y * s) << 16;
+                    };
+                    if (i0 + 512 * i < off * D)
+                        *reinterpret_cast<uint4 *>(block + i0 + 512 * i) = make_uint4(again(w[i].x), again(w[i].y), again(w[i].z), again(w[i].w));
                 }
             }
-            __syncwarp();  // q_out may be q: the lanes of a row have read it
-            if (here) {
-                T *to = static_cast<T *>(a.q_out) + (size_t)(tok0 + r) * a.q_out_stride + ((size_t)h * G + n0) * D + u0;
-#pragma unroll
-                for (int n = 0; n < kQ; ++n)
-                    if (n0 + n < G) {
-                        *reinterpret_cast<uint4 *>(to + n * D) = qx[n];
-                        *reinterpret_cast<uint4 *>(to + n * D + du) = qy[n];
-                    }
-            }
         }
-    }
-    __syncthreads();
-
-    // ---- keys and values
-    for (int r = prow; r < rows && live_head; r += kTile) {
-        const int64_t slot = slot_of(r);
-        if (slot < 0) continue;
-        if (r >= kTile) {
-            load(k_row(r), kx, ky);
-            load(v_row(r), vx, vy);
-        }
-        const int run = run_of(r);
-        const size_t at = (((size_t)(slot >> lb) * a.Hkv + h) * a.B + (size_t)(slot & (a.B - 1))) * D;
-        float f[16];
-        auto store = [&](uint8_t *row, float s) {
-            uint32_t p[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) p[e] = codes2(f[2 * e] * s, f[2 * e + 1] * s);
-            *reinterpret_cast<uint2 *>(row + u0) = make_uint2(p[0] | p[1] << 16, p[2] | p[3] << 16);
-            *reinterpret_cast<uint2 *>(row + u0 + du) = make_uint2(p[4] | p[5] << 16, p[6] | p[7] << 16);
-        };
-        float2 w[kW];
-        angles(r, w);
-        turn(kx, ky, k_row(r), r, w, f);
-        store(a.k_cache + at, inv[0][own][run]);
-        Elem<T>::unpack(vx, f);
-        Elem<T>::unpack(vy, f + 8);
-        store(a.v_cache + at, inv[1][own][run]);
-    }
-
-    // ---- the rows that a block held before, where its scale grew
-    for (int task = tid >> 5; task < rows * 2 * kHeads; task += kThreads8 / 32) {
-        const int r = task % rows, which = task / rows & 1, o = task / (2 * rows);
-        const int64_t slot = slot_of(r);
-        if (!begins(r) || slot < 0 || blockIdx.y * kHeads + o >= a.Hkv) continue;
-        const float s = ratio[which][o][run_of(r)];
-        if (s == 1.f) continue;
-        int off = (int)(slot & (a.B - 1));
-        for (int n = r + 1; n < rows && !begins(n); ++n) off = min(off, (int)(slot_of(n) & (a.B - 1)));
-        uint8_t *block = (which ? a.v_cache : a.k_cache) + ((size_t)(slot >> lb) * a.Hkv + blockIdx.y * kHeads + o) * a.B * D;
-        for (int i = lane * 4; i < off * D; i += 128) {
-            const uint32_t w = *reinterpret_cast<const uint32_t *>(block + i);
-            const float2 lo = values2(w & 0xffffu), hi = values2(w >> 16);
-            *reinterpret_cast<uint32_t *>(block + i) = codes2(lo.x * s, lo.y * s) | codes2(hi.x * s, hi.y * s) << 16;
-        }
+        kx = kx1, ky = ky1, vx = vx1, vy = vy1;
     }
 }
 
@@ -368,13 +438,22 @@ cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, int threads, si
 
 template <typename T, int D>
 cudaError_t launch_write8_t(const Write8Args &a, cudaStream_t st) {
-    constexpr int kHeads = 128 / (kTile * (D / 16));
-    const dim3 grid((unsigned)((a.T + kTile - 1) / kTile), (unsigned)((a.Hkv + kHeads - 1) / kHeads));
-    if (grid.y > 65535) return cudaErrorNotSupported;
+    // CTAs enough for the card where the work allows: KV heads each in CTAs of their own for a step, two CTAs a
+    // tile and more heads each for a prompt (the angles of a tile then serve them all); the same for the queries' heads
+    constexpr int kHeads = kThreads8 / (kTile * (D / 16)), kRound = kThreads8 / (D / 16);
+    const int tiles = (a.T + kTile - 1) / kTile, steps = (a.Hkv + kHeads - 1) / kHeads;
+    int kv_parts = (4 * 152 + tiles - 1) / tiles;
+    kv_parts = kv_parts < steps ? kv_parts : steps;
+    const int pairs = a.q ? (a.T + 1) / 2 : 0, rounds = a.q ? (2 * a.Hq + kRound - 1) / kRound : 1;
+    int q_parts = pairs ? (4 * 152 + pairs - 1) / pairs : 1;
+    q_parts = q_parts < rounds ? q_parts : rounds;
+    const long long ctas = (long long)tiles * kv_parts + (long long)pairs * q_parts;
+    if (ctas > 0x7fffffffLL) return cudaErrorNotSupported;
+    const dim3 grid((unsigned)ctas);
     const size_t smem = a.R ? (size_t)(kTile + a.B) * (D / 2 + 8) * sizeof(float2) : 0;  // at most 27 KB
-    if (a.R == 0 || a.interleaved) return launch_dependent(write8_kernel<T, D, kNeighbours>, grid, kThreads8, smem, st, a);
-    if (a.R % 16 == 0) return launch_dependent(write8_kernel<T, D, kHalves>, grid, kThreads8, smem, st, a);
-    return launch_dependent(write8_kernel<T, D, kSplit>, grid, kThreads8, smem, st, a);
+    if (a.R == 0 || a.interleaved) return launch_dependent(write8_kernel<T, D, kNeighbours>, grid, kThreads8, smem, st, a, kv_parts, q_parts);
+    if (a.R % 16 == 0) return launch_dependent(write8_kernel<T, D, kHalves>, grid, kThreads8, smem, st, a, kv_parts, q_parts);
+    return launch_dependent(write8_kernel<T, D, kSplit>, grid, kThreads8, smem, st, a, kv_parts, q_parts);
 }
 
 // grid (pairs, K and V): a block's codes in 16-byte units, and its scales.
