@@ -492,7 +492,7 @@ typedef struct pa_window {
  *
  * with K_j, V_j the values that the codes stand for.  Scores, weights' sums and outputs are held
  * in fp32; the codes go into the products as they are (exact in 16 bits), and the weights are
- * rounded to 11 bits (22 in a decode) before the second one.
+ * rounded to 11 bits before the second one.
  *
  *   window        NULL: all keys
  *   out           [S | T, Hq, D] float32, or kv_dtype when out_dtype == kv_dtype

@@ -6,16 +6,22 @@
 // ends within a (sequence, row block, group) leaves a partial (m, l, O) in the workspace; the one that takes its first
 // step notes how many there are, and a second launch joins them.
 //
-// A CTA is a producer warp and one consumer warp per KV head of the group and 16 rows of the row block (TW of them; a
-// decode: one, with 8 rows).  The producer fills a ring of steps by TMA, one box per block (all HG heads) for K and for
-// V; every 32 steps, lane l looks up step l's blocks and scales.  (Warps that fill rings of their own spend 700 of 2700
-// cycles a step on it: 88.6 us on 256 sequences.)  A consumer computes S = Q K^T and O += P V with mma.m16n8k16, 32 keys
-// at a time.  In a decode the G <= 8 heads are rows 0-7 of A, and rows 8-15 carry the low parts of P, so that weights
-// keep 22 bits; in a chunk all 16 rows are query rows.
+// A CTA is a producer warp and MB consumer warps per KV head of the group, each with 8 NQ of the row block's rows.  The
+// producer fills a ring of steps by TMA, one box per block (all HG heads) for K and for V; every 32 steps, lane l looks
+// up step l's blocks and scales.  (Warps that fill rings of their own spend 700 of 2700 cycles a step on it.)
+//
+// A consumer works on the transposed products, 32 keys at a time: S^T = K Q^T with mma.m16n8k32 on the e4m3 codes as they
+// are, and O^T += V^T P^T with mma.m16n8k16 on f16.  So the keys, of which there are enough, take the products' 16 rows,
+// and the query rows come in eights.  The queries are split into e4m3 terms of four bits each: of bf16 two (its
+// 8 bits), of f16 three, scaled by a power of two per row that brings the row's largest to 2^7; the first term and the
+// others have accumulators of their own, the others 16 times as large, so that elements of less than 2^-14 of the row's
+// largest still count (to 2^-21 of it).  These products run at four times f16's rate, accumulate as exactly, and K needs no
+// conversion.  P^T comes out of S^T with keys as rows, and movmatrix turns it into the other product's operand.  (Both
+// products in f16 with the query rows as the 16: verify 162 us.)
 //
 // Codes come out of shared memory in 16-byte pieces with the products' dimensions and keys permuted to fit: lane
-// (g, c) of a warp takes bytes 16 c .. of key row perm(g) for S (its 16 bytes are 4 k-steps), and for P V bytes
-// 16 g .. of the key rows perm(2c), perm(2c + 1), whose bytes it pairs up (prmt) and converts.  perm makes both
+// (g, c) of a warp takes bytes 16 c .. of the key rows perm(g) and 8 + perm(g) for S (four k-steps' words), and for P V
+// bytes 16 g .. of the key rows perm(2c), perm(2c + 1), whose bytes it pairs up (prmt) and converts.  perm makes both
 // free of bank conflicts under the TMA swizzle (128 bytes at D 128, 64 at D 64).
 #pragma once
 
@@ -26,13 +32,13 @@
 
 namespace pa {
 
-// TW: row tiles of 16 of a row block; 0: a decode (8 rows).  HG: KV heads of a CTA.
-template <int D, int TW, int HG>
+// NQ: tiles of 8 query rows of a warp; MB: warps of a head's row block; HG: KV heads of a CTA.
+template <int D, int NQ, int MB, int HG>
 struct Attend8Cfg {
-    static constexpr int kRows = TW ? 16 * TW : 8;           // of a row block
-    static constexpr int kConsumers = HG * (TW ? TW : 1);
+    static constexpr int kRows = 8 * NQ * MB;                // of a row block
+    static constexpr int kConsumers = HG * MB;
     static constexpr int kThreads = 32 * (kConsumers + 1);
-    static constexpr int kCtas = attend8_ctas(TW, HG);       // per SM
+    static constexpr int kCtas = attend8_ctas(MB, HG);       // per SM
     static constexpr int kTileBytes = kStep8 * D * HG;       // K (or V) of a step
     static constexpr int kStagesRaw = 192 * 1024 / kCtas / (2 * kTileBytes);
     static constexpr int kStages = kStagesRaw > 8 ? 8 : kStagesRaw;
@@ -43,6 +49,27 @@ struct Attend8Cfg {
     static_assert(kStages >= 3, "ring");
     static_assert((kSmem + 2048) * kCtas <= 228 * 1024, "shared memory budget");
 };
+
+__device__ __forceinline__ void mma_codes(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The transpose of an 8 x 8 matrix of 16-bit elements, two of a row per lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+// Two fp32 values as e4m3 codes (x0 in the low byte); what is infinite becomes NaN.
+__device__ __forceinline__ uint32_t codes_of(float x0, float x1) {
+    uint16_t r;
+    x0 += x0 - x0;
+    x1 += x1 - x1;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(x1), "f"(x0));
+    return r;
+}
 
 // The physical key row (of 8) of index n of a product.
 template <int D>
@@ -70,12 +97,13 @@ struct Place8 {
     Steps8 st;
 };
 
-template <typename T, int D, int TW, int HG>
-__global__ void __launch_bounds__(Attend8Cfg<D, TW, HG>::kThreads, Attend8Cfg<D, TW, HG>::kCtas)
+template <typename T, int D, int NQ, int MB, int HG>
+__global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cfg<D, NQ, MB, HG>::kCtas)
     attend8_mma_kernel(const Attend8Args a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
-    using C = Attend8Cfg<D, TW, HG>;
+    using C = Attend8Cfg<D, NQ, MB, HG>;
     using H = Mma16<__half>;
-    constexpr int kNT = D / 8, kKS = D / 16, kRows = C::kRows, kHi = TW ? 2 : 1;  // kHi: halves of A's rows that are query rows
+    constexpr int kKS = D / 32, kMT = D / 16, kRows = C::kRows;             // k-steps of S, 16-row tiles of O^T
+    constexpr int kTerms = std::is_same<T, __half>::value ? 3 : 2;
     constexpr int kWarps = C::kConsumers + 1;
     extern __shared__ unsigned char smem_raw[];
     __shared__ long long sums[kWarps];
@@ -249,7 +277,7 @@ __global__ void __launch_bounds__(Attend8Cfg<D, TW, HG>::kThreads, Attend8Cfg<D,
     }
 
     // ------------------------------------------------------------ consumers
-    const int head = warp % HG, member = warp / HG;        // of the group, of the row block's tiles
+    const int head = warp % HG, member = warp / HG;        // of the group, of the row block's warps
     const uint32_t head_at = (uint32_t)(head * a.B * D);   // of a box
     const uint32_t half_at = (uint32_t)(a.B == 16 ? 16 * D * HG : 16 * D);   // from key 0 to key 16 of a head
     bool timed_out = false;
@@ -261,21 +289,21 @@ __global__ void __launch_bounds__(Attend8Cfg<D, TW, HG>::kThreads, Attend8Cfg<D,
         const int n = min(left, p.st.count - p.v);           // steps of this head
         const bool whole = n == p.st.count;
         const int kvh = p.h * HG + head;
-        const int r0 = p.rb * kRows + 16 * member;           // first row of the warp: row r is token r / G, head r % G
+        const int r0 = p.rb * kRows + 8 * NQ * member;       // first row of the warp: row r is token r / G, head r % G
         const bool any = r0 < p.q.n * G;
-        // queries as A fragments
-        uint32_t qa[kKS][2 * kHi];
-        float qs[kHi];                                       // scale log2(e) over the row's factor
-        int pos[kHi];
+        // queries as B fragments (lane (g, c): row g of a tile); what belongs to the rows 2 c, 2 c + 1 that a lane has of S^T
+        uint32_t qb[kTerms][kKS][NQ][2];
+        float qs[NQ][2];                                     // scale log2(e) over the row's factor
+        int pos[NQ][2];
 #pragma unroll
-        for (int hi = 0; hi < kHi; ++hi) {
-            const int r = r0 + 8 * hi + g;
+        for (int t8 = 0; t8 < NQ; ++t8) {
+            const int r = r0 + 8 * t8 + g;
             const bool on = r < p.q.n * G;
             const int t = on ? r >> lg : 0;
-            pos[hi] = on ? p.q.len - p.q.n + t : p.q.len - 1;
             const uint16_t *row = static_cast<const uint16_t *>(a.q) +
                                   ((size_t)(p.q.q0 + t) * a.Hq + kvh * G + (on ? r & (G - 1) : 0)) * D;
-            uint32_t w[kKS][2];
+            uint32_t w[D / 64][8];
+            float top = 0.f;
 #pragma unroll
             for (int ch = 0; ch < D / 64; ++ch) {
                 uint4 x = make_uint4(0, 0, 0, 0), y = x;
@@ -283,51 +311,55 @@ __global__ void __launch_bounds__(Attend8Cfg<D, TW, HG>::kThreads, Attend8Cfg<D,
                     x = *reinterpret_cast<const uint4 *>(row + 16 * (c + 4 * ch));
                     y = *reinterpret_cast<const uint4 *>(row + 16 * (c + 4 * ch) + 8);
                 }
-                w[4 * ch][0] = x.x, w[4 * ch][1] = x.y, w[4 * ch + 1][0] = x.z, w[4 * ch + 1][1] = x.w;
-                w[4 * ch + 2][0] = y.x, w[4 * ch + 2][1] = y.y, w[4 * ch + 3][0] = y.z, w[4 * ch + 3][1] = y.w;
+                w[ch][0] = x.x, w[ch][1] = x.y, w[ch][2] = x.z, w[ch][3] = x.w;
+                w[ch][4] = y.x, w[ch][5] = y.y, w[ch][6] = y.z, w[ch][7] = y.w;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 v = Mma16<T>::unpack(w[ch][i]);
+                    top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+                }
             }
-            float back = 1.f;
-            if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-                float top = 0.f;
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int e = min(100, max(-100, 7 - ((int)(__float_as_uint(top) >> 23) - 127)));
+            const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+            const float back = a.scale * kLog2e8 * __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
-                for (int ks = 0; ks < kKS; ++ks)
+            for (int ch = 0; ch < D / 64; ++ch)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float2 v = Mma16<T>::unpack(w[ks][i]);
-                        top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+                for (int i = 0; i < 4; ++i) {   // four elements: a word of each term
+                    const float2 u = Mma16<T>::unpack(w[ch][2 * i]), v = Mma16<T>::unpack(w[ch][2 * i + 1]);
+                    float x[4] = {u.x * up, u.y * up, v.x * up, v.y * up};
+#pragma unroll
+                    for (int term = 0; term < kTerms; ++term) {
+                        const uint32_t lo = codes_of(x[0], x[1]), hi = codes_of(x[2], x[3]);
+                        qb[term][2 * ch + (i >> 1)][t8][i & 1] = lo | hi << 16;
+                        const float2 a0 = H::unpack(f16_of_codes(lo)), a1 = H::unpack(f16_of_codes(hi));
+                        const float by = term == 0 ? 16.f : 1.f;   // the later terms are in sixteenths
+                        x[0] = (x[0] - a0.x) * by, x[1] = (x[1] - a0.y) * by, x[2] = (x[2] - a1.x) * by, x[3] = (x[3] - a1.y) * by;
                     }
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const int e = min(100, max(-100, 10 - ((int)(__float_as_uint(top) >> 23) - 127)));
-                const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-                back = __uint_as_float((uint32_t)(127 - e) << 23);
+                }
 #pragma unroll
-                for (int ks = 0; ks < kKS; ++ks)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float2 v = Mma16<T>::unpack(w[ks][i]);
-                        w[ks][i] = H::pack(v.x * up, v.y * up);
-                    }
-            }
-            qs[hi] = a.scale * kLog2e8 * back;
-#pragma unroll
-            for (int ks = 0; ks < kKS; ++ks) {
-                qa[ks][hi] = w[ks][0];
-                qa[ks][kHi + hi] = w[ks][1];
+            for (int o = 0; o < 2; ++o) {
+                qs[t8][o] = __shfl_sync(0xffffffffu, back, 4 * (2 * c + o));
+                const int ro = r0 + 8 * t8 + 2 * c + o;
+                pos[t8][o] = ro < p.q.n * G ? p.q.len - p.q.n + (ro >> lg) : p.q.len - 1;
             }
         }
         // keys that every row of the warp sees: up to its first row's position, and above its last row's window
-        const int t_first = min(p.q.n - 1, r0 >> lg), t_last = min(p.q.n - 1, (r0 + (TW ? 15 : 7)) >> lg);
+        const int t_first = min(p.q.n - 1, r0 >> lg), t_last = min(p.q.n - 1, (r0 + 8 * NQ - 1) >> lg);
         const int pos_first = p.q.len - p.q.n + t_first, pos_last = p.q.len - p.q.n + t_last;
         const int seen_from = a.window > 0 ? pos_first - a.window + 1 : 0;   // below: only sinks are seen by some row
         const int whole_from = a.window > 0 ? pos_last - a.window + 1 : 0;
 
-        float o[kNT][4];
+        float o[kMT][NQ][4];    // O^T: columns (D / 8) g + 2 j + (0, 1), of the rows 2 c, 2 c + 1
+        float m[NQ][2], l[NQ][2];   // m: the weights' reference (log2); l: this lane's keys only
 #pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) o[nt][0] = o[nt][1] = o[nt][2] = o[nt][3] = 0.f;
-        float m[kHi], l[kHi];   // m: the weights' reference (log2); l: this lane's keys only
+        for (int t8 = 0; t8 < NQ; ++t8) {
 #pragma unroll
-        for (int hi = 0; hi < kHi; ++hi) m[hi] = -INFINITY, l[hi] = 0.f;
+            for (int j = 0; j < kMT; ++j) o[j][t8][0] = o[j][t8][1] = o[j][t8][2] = o[j][t8][3] = 0.f;
+            m[t8][0] = m[t8][1] = -INFINITY, l[t8][0] = l[t8][1] = 0.f;
+        }
 
         for (int i = 0; i < n; ++i) {
             const int st = taken % C::kStages;
@@ -340,140 +372,143 @@ __global__ void __launch_bounds__(Attend8Cfg<D, TW, HG>::kThreads, Attend8Cfg<D,
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     float pad;
-                    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(ks[b]), "=f"(lv[b]), "=f"(iv[b]), "=f"(pad) : "r"(notes + (uint32_t)(C::kNotes * st + 32 * head + 16 * b)));
+                    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(ks[b]), "=f"(lv[b]), "=f"(iv[b]), "=f"(pad)
+                                 : "r"(notes + (uint32_t)(C::kNotes * st + 32 * head + 16 * b)));
                 }
                 const bool clear = kb + kStep8 - 1 <= pos_first && (kb >= whole_from || kb + kStep8 <= a.sinks) && iv[0] > 0.f && iv[1] > 0.f;
-                // ---- S = Q K^T: 32 keys, four n-tiles of 8
-                float s[4][4];
+                // With one tile of rows both halves of the step go through each stage together; with more, registers are short
+                // and the halves go one after the other.
+                constexpr int kKK = NQ == 1 ? 2 : 1;
 #pragma unroll
-                for (int nt = 0; nt < 4; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+                for (int k0 = 0; k0 < 2; k0 += kKK) {
+                    // ---- S^T = K Q^T, 16 keys at a time: rows g (key perm(g)) and g + 8, columns 2 c, 2 c + 1 of each tile
+                    float s[kKK][NQ][4];
 #pragma unroll
-                for (int ch = 0; ch < D / 64; ++ch) {
-                    uint4 w[4];
+                    for (int i2 = 0; i2 < kKK; ++i2) {
+                        const int kk = k0 + i2;
+                        float rest[NQ][4];
 #pragma unroll
-                    for (int nt = 0; nt < 4; ++nt) w[nt] = lds128(kst + (nt & 2 ? half_at : 0u) + piece8<D>(8 * (nt & 1) + perm8<D>(g), c + 4 * ch));
+                        for (int t8 = 0; t8 < NQ; ++t8)
 #pragma unroll
-                    for (int i4 = 0; i4 < 4; ++i4) {
-                        const uint32_t *q = qa[4 * ch + i4];
+                            for (int e = 0; e < 4; ++e) s[i2][t8][e] = rest[t8][e] = 0.f;
+                        const uint32_t at = kst + (kk ? half_at : 0u);
 #pragma unroll
-                        for (int nt = 0; nt < 4; ++nt) {
-                            const uint32_t x = i4 == 0 ? w[nt].x : i4 == 1 ? w[nt].y : i4 == 2 ? w[nt].z : w[nt].w;
-                            H::mma(s[nt], q[0], TW ? q[kHi - 1] : 0u, q[kHi], TW ? q[2 * kHi - 1] : 0u, f16_of_codes(x & 0xffffu), f16_of_codes(x >> 16));
+                        for (int ch = 0; ch < D / 64; ++ch) {
+                            const uint4 lo = lds128(at + piece8<D>(perm8<D>(g), c + 4 * ch)), hi = lds128(at + piece8<D>(8 + perm8<D>(g), c + 4 * ch));
+#pragma unroll
+                            for (int t8 = 0; t8 < NQ; ++t8)
+#pragma unroll
+                                for (int term = 0; term < kTerms; ++term) {
+                                    float(&d)[4] = term ? rest[t8] : s[i2][t8];
+                                    mma_codes(d, lo.x, hi.x, lo.y, hi.y, qb[term][2 * ch][t8][0], qb[term][2 * ch][t8][1]);
+                                    mma_codes(d, lo.z, hi.z, lo.w, hi.w, qb[term][2 * ch + 1][t8][0], qb[term][2 * ch + 1][t8][1]);
+                                }
                         }
-                    }
-                }
-                // this lane's bytes of its four keys' rows of V, of the first or second 16 keys
-                auto load_v = [&](uint32_t (&vw)[4][D / 32], int kk) {
+                        // a_j = z_j + log2 vs
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int row = 8 * (e >> 1) + perm8<D>(2 * c + (e & 1));
-                        const uint32_t tile = vst + (kk ? half_at : 0u);
-                        if constexpr (D == 128) {
-                            const uint4 x = lds128(tile + piece8<D>(row, g));
-                            vw[e][0] = x.x, vw[e][1] = x.y, vw[e][2] = x.z, vw[e][3] = x.w;
-                        } else {
-                            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                                         : "=r"(vw[e][0]), "=r"(vw[e][1])
-                                         : "r"(tile + piece8<D>(row, g >> 1) + 8 * (g & 1)));
-                        }
-                        if (!clear) {  // a key that no row sees may hold anything
-                            const int j = kb + 16 * kk + row;
-                            if (!(iv[kk] > 0.f && j <= pos_last && (j >= seen_from || j < a.sinks))) {
+                        for (int t8 = 0; t8 < NQ; ++t8) {
+                            const float mul[2] = {qs[t8][0] * ks[kk], qs[t8][1] * ks[kk]};
 #pragma unroll
-                                for (int x = 0; x < D / 32; ++x) vw[e][x] = 0u;
+                            for (int e = 0; e < 4; ++e) {
+                                float x = fmaf(rest[t8][e], 0.0625f, s[i2][t8][e]);
+                                x = fmaf(x, mul[e & 1], lv[kk]);
+                                if (!clear) {
+                                    const int j = kb + 16 * kk + 8 * (e >> 1) + perm8<D>(g);
+                                    if (!(iv[kk] > 0.f && j <= pos[t8][e & 1] && (a.window == 0 || j > pos[t8][e & 1] - a.window || j < a.sinks)))
+                                        x = -INFINITY;
+                                }
+                                s[i2][t8][e] = x;
                             }
                         }
                     }
-                };
-                uint32_t va[4][D / 32], vb[4][D / 32];
-                load_v(va, 0);
-                // ---- a_j = z_j + log2 vs, the running reference, weights
-                float mx[kHi];
-                bool need = false;
-#pragma unroll
-                for (int hi = 0; hi < kHi; ++hi) {
-                    float mul[2] = {qs[hi] * ks[0], qs[hi] * ks[1]};
-#pragma unroll
-                    for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) s[nt][2 * hi + e] = fmaf(s[nt][2 * hi + e], mul[nt >> 1], lv[nt >> 1]);
-                }
-                if (!clear) {
-#pragma unroll
-                    for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int j = kb + 8 * nt + perm8<D>(2 * c + e);
-#pragma unroll
-                            for (int hi = 0; hi < kHi; ++hi)
-                                if (!(iv[nt >> 1] > 0.f && j <= pos[hi] && (a.window == 0 || j > pos[hi] - a.window || j < a.sinks)))
-                                    s[nt][2 * hi + e] = -INFINITY;
-                        }
-                }
-#pragma unroll
-                for (int hi = 0; hi < kHi; ++hi) {
-                    mx[hi] = fmaxf(fmaxf(fmaxf(s[0][2 * hi], s[0][2 * hi + 1]), fmaxf(s[1][2 * hi], s[1][2 * hi + 1])),
-                                   fmaxf(fmaxf(s[2][2 * hi], s[2][2 * hi + 1]), fmaxf(s[3][2 * hi], s[3][2 * hi + 1])));
-                    need = need || mx[hi] > m[hi] + (8.f + kLift8);
-                }
-                if (__any_sync(0xffffffffu, need)) {
-#pragma unroll
-                    for (int hi = 0; hi < kHi; ++hi) {
-                        float x = mx[hi];
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                        x = fmaxf(m[hi], x - kLift8);
-                        const float alpha = x == -INFINITY ? 1.f : ex2(m[hi] - x);
-                        m[hi] = x;
-                        l[hi] *= alpha;
-#pragma unroll
-                        for (int nt = 0; nt < kNT; ++nt) {
-                            o[nt][2 * hi] *= alpha;
-                            o[nt][2 * hi + 1] *= alpha;
-                            if (TW == 0) {
-                                o[nt][2] *= alpha;
-                                o[nt][3] *= alpha;
-                            }
-                        }
-                    }
-                }
-                uint32_t pa[2][4];   // P as A fragments of 16 keys each
-#pragma unroll
-                for (int hi = 0; hi < kHi; ++hi) {
-                    const float mr = m[hi] == -INFINITY ? 0.f : m[hi];
-#pragma unroll
-                    for (int kk = 0; kk < 2; ++kk) {
-                        float w[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) w[e] = ex2(s[2 * kk + (e >> 1)][2 * hi + (e & 1)] - mr);
-                        // a block that is not there has weights of 0 (and an iv of -1)
-                        l[hi] = fmaf((w[0] + w[1]) + (w[2] + w[3]), iv[kk], l[hi]);
-                        pa[kk][hi] = H::pack(w[0], w[1]);
-                        pa[kk][2 + hi] = H::pack(w[2], w[3]);
-                        if (TW == 0) {
-                            const float2 x = H::unpack(pa[kk][0]), y = H::unpack(pa[kk][2]);
-                            pa[kk][1] = H::pack(w[0] - x.x, w[1] - x.y);
-                            pa[kk][3] = H::pack(w[2] - y.x, w[3] - y.y);
-                        }
-                    }
-                }
-                // ---- O += P V
-                load_v(vb, 1);
-                auto product = [&](const uint32_t (&vw)[4][D / 32], const uint32_t (&w)[4]) {
-#pragma unroll
-                    for (int x = 0; x < D / 32; ++x) {
-                        const uint32_t p0 = __byte_perm(vw[0][x], vw[1][x], 0x5140), p1 = __byte_perm(vw[0][x], vw[1][x], 0x7362);
-                        const uint32_t y0 = __byte_perm(vw[2][x], vw[3][x], 0x5140), y1 = __byte_perm(vw[2][x], vw[3][x], 0x7362);
+                    // this lane's bytes of its four keys' rows of V
+                    uint32_t vw[kKK][4][D / 32];
+                    auto load_v = [&](int i2) {
+                        const int kk = k0 + i2;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const uint32_t lo = e < 2 ? p0 : p1, hi = e < 2 ? y0 : y1;
-                            H::mma(o[4 * x + e], w[0], w[1], w[2], w[3], f16_of_codes(e & 1 ? lo >> 16 : lo & 0xffffu),
-                                   f16_of_codes(e & 1 ? hi >> 16 : hi & 0xffffu));
+                            const int row = 8 * (e >> 1) + perm8<D>(2 * c + (e & 1));
+                            const uint32_t tile = vst + (kk ? half_at : 0u);
+                            if constexpr (D == 128) {
+                                const uint4 x = lds128(tile + piece8<D>(row, g));
+                                vw[i2][e][0] = x.x, vw[i2][e][1] = x.y, vw[i2][e][2] = x.z, vw[i2][e][3] = x.w;
+                            } else {
+                                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                                             : "=r"(vw[i2][e][0]), "=r"(vw[i2][e][1])
+                                             : "r"(tile + piece8<D>(row, g >> 1) + 8 * (g & 1)));
+                            }
+                            if (!clear) {  // a key that no row sees may hold anything
+                                const int j = kb + 16 * kk + row;
+                                if (!(iv[kk] > 0.f && j <= pos_last && (j >= seen_from || j < a.sinks))) {
+#pragma unroll
+                                    for (int x = 0; x < D / 32; ++x) vw[i2][e][x] = 0u;
+                                }
+                            }
+                        }
+                    };
+                    load_v(0);
+                    // ---- the running reference
+                    bool need = false;
+                    float mx[NQ][2];
+#pragma unroll
+                    for (int t8 = 0; t8 < NQ; ++t8)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            mx[t8][e] = fmaxf(s[0][t8][e], s[0][t8][2 + e]);
+                            if constexpr (kKK == 2) mx[t8][e] = fmaxf(mx[t8][e], fmaxf(s[1][t8][e], s[1][t8][2 + e]));
+                            need = need || mx[t8][e] > m[t8][e] + (8.f + kLift8);
+                        }
+                    if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+                        for (int t8 = 0; t8 < NQ; ++t8)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float x = mx[t8][e];
+                                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                                x = fmaxf(m[t8][e], x - kLift8);
+                                const float alpha = x == -INFINITY ? 1.f : ex2(m[t8][e] - x);
+                                m[t8][e] = x;
+                                l[t8][e] *= alpha;
+#pragma unroll
+                                for (int j = 0; j < kMT; ++j) {
+                                    o[j][t8][e] *= alpha;
+                                    o[j][t8][2 + e] *= alpha;
+                                }
+                            }
+                    }
+                    // ---- weights, as B fragments: keys as k
+                    uint32_t pb[kKK][NQ][2];
+#pragma unroll
+                    for (int t8 = 0; t8 < NQ; ++t8) {
+                        const float m0 = m[t8][0] == -INFINITY ? 0.f : m[t8][0], m1 = m[t8][1] == -INFINITY ? 0.f : m[t8][1];
+#pragma unroll
+                        for (int i2 = 0; i2 < kKK; ++i2) {
+                            const float w0 = ex2(s[i2][t8][0] - m0), w1 = ex2(s[i2][t8][1] - m1), w2 = ex2(s[i2][t8][2] - m0), w3 = ex2(s[i2][t8][3] - m1);
+                            // a block that is not there has weights of 0 (and an iv of -1)
+                            l[t8][0] = fmaf(w0 + w2, iv[k0 + i2], l[t8][0]);
+                            l[t8][1] = fmaf(w1 + w3, iv[k0 + i2], l[t8][1]);
+                            pb[i2][t8][0] = transpose8(H::pack(w0, w1));
+                            pb[i2][t8][1] = transpose8(H::pack(w2, w3));
                         }
                     }
-                };
-                product(va, pa[0]);
-                product(vb, pa[1]);
+                    // ---- O^T += V^T P^T
+                    if constexpr (kKK == 2) load_v(1);
+#pragma unroll
+                    for (int i2 = 0; i2 < kKK; ++i2)
+#pragma unroll
+                        for (int j = 0; j < kMT; ++j) {
+                            const int x = j >> 1;
+                            const uint32_t lo = __byte_perm(vw[i2][0][x], vw[i2][1][x], j & 1 ? 0x7362 : 0x5140);
+                            const uint32_t hi = __byte_perm(vw[i2][2][x], vw[i2][3][x], j & 1 ? 0x7362 : 0x5140);
+                            const uint32_t a0 = f16_of_codes(lo & 0xffffu), a1 = f16_of_codes(lo >> 16);
+                            const uint32_t a2 = f16_of_codes(hi & 0xffffu), a3 = f16_of_codes(hi >> 16);
+#pragma unroll
+                            for (int t8 = 0; t8 < NQ; ++t8) H::mma(o[j][t8], a0, a1, a2, a3, pb[i2][t8][0], pb[i2][t8][1]);
+                        }
+                }
             }
             __syncwarp();  // every lane has read the stage
             if (lane == 0) mbar_arrive(empty(st));
@@ -495,45 +530,39 @@ __global__ void __launch_bounds__(Attend8Cfg<D, TW, HG>::kThreads, Attend8Cfg<D,
             *note = make_int2(slot, whole ? 0 : 1 + (int)((p.st.count - n + each - 1) / each));
         }
 #pragma unroll
-        for (int hi = 0; hi < kHi; ++hi) {
-            float sum = l[hi];
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            const int row = 16 * member + 8 * hi + g, r = p.rb * kRows + row;
-            if (r >= p.q.n * G) continue;
-            const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
-            // this lane's columns: kNT from 2 kNT c on, and the kNT behind them
-            float v[2][kNT];
-#pragma unroll
-            for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) v[e][nt] = (TW ? o[nt][2 * hi + e] : o[nt][e] + o[nt][2 + e]) * inv;
-            if (!whole) {
-                float4 *to = reinterpret_cast<float4 *>(part + (size_t)row * D + 2 * kNT * c);
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-#pragma unroll
-                    for (int x = 0; x < kNT / 4; ++x)
-                        to[e * kNT / 4 + x] = make_float4(v[e][4 * x], v[e][4 * x + 1], v[e][4 * x + 2], v[e][4 * x + 3]);
-                if (c == 0) *reinterpret_cast<float2 *>(part + (size_t)kRows * D + 2 * row) = make_float2(m[hi], sum);
-                continue;
-            }
-            const size_t at = ((size_t)(p.q.q0 + (r >> lg)) * a.Hq + kvh * G + (r & (G - 1))) * D + 2 * kNT * c;
+        for (int t8 = 0; t8 < NQ; ++t8)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
+                float sum = l[t8][e];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+                const int row = 8 * NQ * member + 8 * t8 + 2 * c + e, r = p.rb * kRows + row;
+                if (r >= p.q.n * G) continue;
+                const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+                float v[D / 8];
+#pragma unroll
+                for (int j = 0; j < kMT; ++j) v[2 * j] = o[j][t8][e] * inv, v[2 * j + 1] = o[j][t8][2 + e] * inv;
+                if (!whole) {
+                    float4 *to = reinterpret_cast<float4 *>(part + (size_t)row * D + D / 8 * g);
+#pragma unroll
+                    for (int x = 0; x < D / 32; ++x) to[x] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+                    if (g == 0) *reinterpret_cast<float2 *>(part + (size_t)kRows * D + 2 * row) = make_float2(m[t8][e], sum);
+                    continue;
+                }
+                const size_t at = ((size_t)(p.q.q0 + (r >> lg)) * a.Hq + kvh * G + (r & (G - 1))) * D + D / 8 * g;
                 if (a.out16) {
-                    uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at + e * kNT);
+                    uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at);
 #pragma unroll
-                    for (int x = 0; x < kNT / 8; ++x)
-                        to[x] = make_uint4(Mma16<T>::pack(v[e][8 * x], v[e][8 * x + 1]), Mma16<T>::pack(v[e][8 * x + 2], v[e][8 * x + 3]),
-                                           Mma16<T>::pack(v[e][8 * x + 4], v[e][8 * x + 5]), Mma16<T>::pack(v[e][8 * x + 6], v[e][8 * x + 7]));
+                    for (int x = 0; x < D / 64; ++x)
+                        to[x] = make_uint4(Mma16<T>::pack(v[8 * x], v[8 * x + 1]), Mma16<T>::pack(v[8 * x + 2], v[8 * x + 3]),
+                                           Mma16<T>::pack(v[8 * x + 4], v[8 * x + 5]), Mma16<T>::pack(v[8 * x + 6], v[8 * x + 7]));
                 } else {
-                    float4 *to = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at + e * kNT);
+                    float4 *to = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at);
 #pragma unroll
-                    for (int x = 0; x < kNT / 4; ++x) to[x] = make_float4(v[e][4 * x], v[e][4 * x + 1], v[e][4 * x + 2], v[e][4 * x + 3]);
+                    for (int x = 0; x < D / 32; ++x) to[x] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
                 }
             }
-        }
         first_piece = false;
         if (left > 0) next_head(p);
     }
@@ -542,13 +571,13 @@ __global__ void __launch_bounds__(Attend8Cfg<D, TW, HG>::kThreads, Attend8Cfg<D,
 // One CTA per (sequence, row block, KV head) joins its parts,
 //   out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i,   M = max m_i,
 // and writes the zeros of a sequence without keys.  A warp takes a row, a lane D / 32 of its columns.
-template <typename T, int D, int TW, int HG>
-__global__ void __launch_bounds__(128) attend8_merge_kernel(const Attend8Args a) {
-    using C = Attend8Cfg<D, TW, HG>;
-    constexpr int kRows = C::kRows, kPer = D / 32;
-    griddep_wait();
+// (nrb row blocks of kRows rows)
+template <typename T, int D, int HG>
+__global__ void __launch_bounds__(128) attend8_merge_kernel(const Attend8Args a, int kRows, int nrb) {
+    constexpr int kPer = D / 32;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int G = a.Hq / a.Hkv, nrb = (a.max_query_len * G + kRows - 1) / kRows;
+    griddep_wait();
+    const int G = a.Hq / a.Hkv;
     const int s = blockIdx.x / (a.Hkv * nrb), h = blockIdx.x / nrb % a.Hkv, rb = blockIdx.x % nrb;
     if (!a.hdr[0]) return;
     const Seq8 q = seq_of(a, s, false);
@@ -592,14 +621,14 @@ __global__ void __launch_bounds__(128) attend8_merge_kernel(const Attend8Args a)
     }
 }
 
-template <typename T, int D, int TW, int HG>
+template <typename T, int D, int NQ, int MB, int HG>
 cudaError_t launch_attend8_t(const Attend8Args &a, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st) {
-    using C = Attend8Cfg<D, TW, HG>;
+    using C = Attend8Cfg<D, NQ, MB, HG>;
     static std::atomic<int> configured[kMaxLaunchDevices];
     int one = 0;
     cudaError_t e = per_device_value(configured, &one, [](int, int *v) {
         *v = 1;
-        return cudaFuncSetAttribute(attend8_mma_kernel<T, D, TW, HG>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+        return cudaFuncSetAttribute(attend8_mma_kernel<T, D, NQ, MB, HG>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
     });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -612,7 +641,7 @@ cudaError_t launch_attend8_t(const Attend8Args &a, const CUtensorMap &tmk, const
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, attend8_mma_kernel<T, D, TW, HG>, a, tmk, tmv);
+    e = cudaLaunchKernelEx(&cfg, attend8_mma_kernel<T, D, NQ, MB, HG>, a, tmk, tmv);
     if (e != cudaSuccess) return e;
     // the join: a CTA per (sequence, KV head, row block)
     const long long blocks = ((long long)a.max_query_len * (a.Hq / a.Hkv) + C::kRows - 1) / C::kRows;
@@ -620,23 +649,25 @@ cudaError_t launch_attend8_t(const Attend8Args &a, const CUtensorMap &tmk, const
     cfg.gridDim = dim3((unsigned)(blocks * a.S * a.Hkv));
     cfg.blockDim = dim3(128);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, attend8_merge_kernel<T, D, TW, HG>, a);
+    return cudaLaunchKernelEx(&cfg, attend8_merge_kernel<T, D, HG>, a, (int)C::kRows, (int)blocks);
 }
 
-template <typename T, int D, int TW>
+template <typename T, int D, int NQ, int MB>
 cudaError_t dispatch_heads(const Attend8Args &a, int hg, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st) {
-    if constexpr (TW < 4)
-        if (hg == 4) return launch_attend8_t<T, D, TW, 4>(a, tmk, tmv, st);
-    return hg == 2 ? launch_attend8_t<T, D, TW, 2>(a, tmk, tmv, st) : launch_attend8_t<T, D, TW, 1>(a, tmk, tmv, st);
+    if constexpr (MB < 4)
+        if (hg == 4) return launch_attend8_t<T, D, NQ, MB, 4>(a, tmk, tmv, st);
+    return hg == 2 ? launch_attend8_t<T, D, NQ, MB, 2>(a, tmk, tmv, st) : launch_attend8_t<T, D, NQ, MB, 1>(a, tmk, tmv, st);
 }
 template <typename T, int D>
-cudaError_t dispatch_attend8(const Attend8Args &a, int tw, int hg, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st) {
-    switch (tw) {
-        case 0: return dispatch_heads<T, D, 0>(a, hg, tmk, tmv, st);
-        case 1: return dispatch_heads<T, D, 1>(a, hg, tmk, tmv, st);
-        case 2: return dispatch_heads<T, D, 2>(a, hg, tmk, tmv, st);
-        default: return dispatch_heads<T, D, 4>(a, hg, tmk, tmv, st);
+cudaError_t dispatch_attend8(const Attend8Args &a, Rows8 r, int hg, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st) {
+    if (r.nq == 1) {
+        switch (r.mb) {
+            case 1: return dispatch_heads<T, D, 1, 1>(a, hg, tmk, tmv, st);
+            case 2: return dispatch_heads<T, D, 1, 2>(a, hg, tmk, tmv, st);
+            default: return dispatch_heads<T, D, 1, 3>(a, hg, tmk, tmv, st);
+        }
     }
+    return r.mb == 2 ? dispatch_heads<T, D, 2, 2>(a, hg, tmk, tmv, st) : dispatch_heads<T, D, 2, 4>(a, hg, tmk, tmv, st);
 }
 
 }  // namespace pa

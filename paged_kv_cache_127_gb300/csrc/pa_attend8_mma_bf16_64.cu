@@ -3,8 +3,8 @@
 
 namespace pa {
 
-cudaError_t launch_attend8_mma_bf16_64(const Attend8Args &a, int tw, int hg, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st) {
-    return dispatch_attend8<__nv_bfloat16, 64>(a, tw, hg, tmk, tmv, st);
+cudaError_t launch_attend8_mma_bf16_64(const Attend8Args &a, Rows8 rows, int hg, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st) {
+    return dispatch_attend8<__nv_bfloat16, 64>(a, rows, hg, tmk, tmv, st);
 }
 
 }  // namespace pa

@@ -57,21 +57,24 @@ struct Attend8Args {
     int tiles;                      // tcgen05 path: 128-row tiles of an item (1 or 2)
     float scale;
 };
-// mma.sync path, and the join of its parts: row blocks of `tw` 16-row tiles of a KV head (0: a decode, 8 rows), `hg`
-// KV heads a CTA.  A CTA has hg * max(tw, 1) consumer warps of up to 200 registers a thread and a producer: ten warps an SM.
+// mma.sync path, and the join of its parts: `mb` warps with 8 * nq rows each for a row block of a KV head, `hg` KV heads
+// a CTA, which has a producer warp besides; up to ten warps an SM, or one CTA.
 constexpr int kSms8 = 152;
-constexpr int attend8_ctas(int tw, int hg) { return 10 / (hg * (tw ? tw : 1) + 1); }   // per SM
-inline int attend8_tiles(int max_query_len, int G) {
+constexpr int attend8_ctas(int mb, int hg) { return hg * mb < 10 ? 10 / (hg * mb + 1) : 1; }   // per SM
+struct Rows8 {
+    int nq, mb;
+};
+inline Rows8 attend8_rows(int max_query_len, int G) {
     const long long rows = (long long)max_query_len * G;
-    return rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+    return rows <= 8 ? Rows8{1, 1} : rows <= 16 ? Rows8{1, 2} : rows <= 24 ? Rows8{1, 3} : rows <= 32 ? Rows8{2, 2} : Rows8{2, 4};
 }
-inline int attend8_heads(int Hkv, int tw) {
-    return Hkv % 4 == 0 && tw < 4 ? 4 : Hkv % 2 == 0 ? 2 : 1;
+inline int attend8_heads(int Hkv, int mb) {
+    return Hkv % 4 == 0 && mb < 4 ? 4 : Hkv % 2 == 0 ? 2 : 1;
 }
-cudaError_t launch_attend8_mma_f16_64(const Attend8Args &a, int tw, int hg, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
-cudaError_t launch_attend8_mma_f16_128(const Attend8Args &a, int tw, int hg, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
-cudaError_t launch_attend8_mma_bf16_64(const Attend8Args &a, int tw, int hg, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
-cudaError_t launch_attend8_mma_bf16_128(const Attend8Args &a, int tw, int hg, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
+cudaError_t launch_attend8_mma_f16_64(const Attend8Args &a, Rows8 rows, int hg, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
+cudaError_t launch_attend8_mma_f16_128(const Attend8Args &a, Rows8 rows, int hg, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
+cudaError_t launch_attend8_mma_bf16_64(const Attend8Args &a, Rows8 rows, int hg, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
+cudaError_t launch_attend8_mma_bf16_128(const Attend8Args &a, Rows8 rows, int hg, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
 // A cache of codes [N, Hkv, B, D]: boxes of `heads` heads of one block, rows of D bytes with the swizzle of that width.
 cudaError_t make_codes_tensor_map(CUtensorMap *map, const void *codes, int D, int B, long long block_heads, int heads);
 // tcgen05 path, from 64 rows of a KV head on: the work list, and the kernel (tmq: the queries' map).

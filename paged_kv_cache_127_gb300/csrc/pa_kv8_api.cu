@@ -48,8 +48,8 @@ int32_t check_chunk8(const pa_dims *d, int32_t T, int32_t max_q) {
     if (rc != PA_OK) return rc;
     if (T < 0 || max_q < 1 || max_q > (1 << 20) || d->num_seqs > 65535) return PA_ERR_INVALID;
     if ((int64_t)T * d->num_q_heads > INT32_MAX) return PA_ERR_INVALID;
-    // the grid of the join: (sequence, KV head, row block of 16 rows or more)
-    const int64_t blocks = ((int64_t)max_q * (d->num_q_heads / d->num_kv_heads) + 15) / 16;
+    // the grid of the join: (sequence, KV head, row block of 8 rows or more)
+    const int64_t blocks = ((int64_t)max_q * (d->num_q_heads / d->num_kv_heads) + 7) / 8;
     return (int64_t)d->num_seqs * d->num_kv_heads > INT32_MAX / blocks ? PA_ERR_INVALID : PA_OK;
 }
 int32_t check_window(const pa_window *w) { return w && (w->window < 0 || w->sinks < 0) ? PA_ERR_INVALID : PA_OK; }
@@ -57,19 +57,20 @@ int32_t check_window(const pa_window *w) { return w && (w->window < 0 || w->sink
 // Workspace, each part 256-byte aligned: a header, the notes of each (sequence, KV head, row block), and two parts
 // for each CTA that shares the keys (mma.sync path).
 struct Layout8 {
-    int tw, hg, units, tiles;  // tiles 0: the mma.sync path
+    pa::Rows8 rows;
+    int hg, units, tiles;  // tiles 0: the mma.sync path
     size_t list, parts, total;
 };
-Layout8 layout8(const pa_dims *d, int tw, int32_t max_q) {
+Layout8 layout8(const pa_dims *d, int32_t max_q) {
     Layout8 L{};
-    const int64_t G = d->num_q_heads / d->num_kv_heads;
-    L.tw = tw;
-    L.hg = pa::attend8_heads(d->num_kv_heads, tw);
-    const int64_t rows = tw ? 16 * tw : 8, blocks = (max_q * G + rows - 1) / rows;
+    const int G = d->num_q_heads / d->num_kv_heads;
+    L.rows = pa::attend8_rows(max_q, G);
+    L.hg = pa::attend8_heads(d->num_kv_heads, L.rows.mb);
+    const int64_t rows = 8 * L.rows.nq * L.rows.mb, blocks = ((int64_t)max_q * G + rows - 1) / rows;
     // no more CTAs than give each of them four steps of 32 keys
     const int64_t steps = ((int64_t)d->max_blocks_per_seq * d->block_size + 31) / 32;
     const int64_t most = (int64_t)d->num_seqs * (d->num_kv_heads / L.hg) * blocks;  // at most 2^31
-    const int64_t cap = pa::kSms8 * pa::attend8_ctas(tw, L.hg);
+    const int64_t cap = pa::kSms8 * pa::attend8_ctas(L.rows.mb, L.hg);
     const int64_t units = most > cap * 4 / steps ? cap : (most * steps + 3) / 4;
     L.units = (int)(units < cap ? (units > 0 ? units : 1) : cap);
     L.list = 256;
@@ -77,10 +78,10 @@ Layout8 layout8(const pa_dims *d, int tw, int32_t max_q) {
     L.total = L.parts + up256((size_t)2 * L.units * L.hg * rows * (d->head_dim + 2) * sizeof(float));
     return L;
 }
-Layout8 decode_layout8(const pa_dims *d) { return layout8(d, 0, 1); }
+Layout8 decode_layout8(const pa_dims *d) { return layout8(d, 1); }
 Layout8 chunk_layout8(const pa_dims *d, int32_t max_q) {
     const int G = d->num_q_heads / d->num_kv_heads;
-    if (!pa::chunk_uses_umma(max_q, G)) return layout8(d, pa::attend8_tiles(max_q, G), max_q);
+    if (!pa::chunk_uses_umma(max_q, G)) return layout8(d, max_q);
     Layout8 L{};   // a header and the work list
     L.tiles = pa::chunk_umma_rows(max_q, G) / 128;
     L.list = 256;
@@ -157,9 +158,9 @@ int32_t run_mma(pa::Attend8Args &a, const pa_dims *d, const Layout8 &L, void *st
     if (e != cudaSuccess) return PA_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (d->kv_dtype == PA_BF16)
-        e = a.D == 64 ? pa::launch_attend8_mma_bf16_64(a, L.tw, L.hg, tmk, tmv, st) : pa::launch_attend8_mma_bf16_128(a, L.tw, L.hg, tmk, tmv, st);
+        e = a.D == 64 ? pa::launch_attend8_mma_bf16_64(a, L.rows, L.hg, tmk, tmv, st) : pa::launch_attend8_mma_bf16_128(a, L.rows, L.hg, tmk, tmv, st);
     else
-        e = a.D == 64 ? pa::launch_attend8_mma_f16_64(a, L.tw, L.hg, tmk, tmv, st) : pa::launch_attend8_mma_f16_128(a, L.tw, L.hg, tmk, tmv, st);
+        e = a.D == 64 ? pa::launch_attend8_mma_f16_64(a, L.rows, L.hg, tmk, tmv, st) : pa::launch_attend8_mma_f16_128(a, L.rows, L.hg, tmk, tmv, st);
     return to_status(e);
 }
 
