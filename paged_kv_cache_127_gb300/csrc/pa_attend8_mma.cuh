@@ -10,14 +10,11 @@
 // producer fills a ring of steps by TMA, one box per block (all HG heads) for K and for V; every 32 steps, lane l looks
 // up step l's blocks and scales.  (Warps that fill rings of their own spend 700 of 2700 cycles a step on it.)
 //
-// A consumer works on the transposed products, 32 keys at a time: S^T = K Q^T with mma.m16n8k32 on the e4m3 codes as they
-// are, and O^T += V^T P^T with mma.m16n8k16 on f16.  So the keys, of which there are enough, take the products' 16 rows,
-// and the query rows come in eights.  The queries are split into e4m3 terms of four bits each: of bf16 two (its
-// 8 bits), of f16 three, scaled by a power of two per row that brings the row's largest to 2^7; the first term and the
-// others have accumulators of their own, the others 16 times as large, so that elements of less than 2^-14 of the row's
-// largest still count (to 2^-21 of it).  These products run at four times f16's rate, accumulate as exactly, and K needs no
-// conversion.  P^T comes out of S^T with keys as rows, and movmatrix turns it into the other product's operand.  (Both
-// products in f16 with the query rows as the 16: verify 162 us.)
+// A consumer works on the transposed products, 32 keys at a time, S^T = K Q^T and O^T += V^T P^T, both with mma.m16n8k16
+// on f16: the keys, of which there are enough, take the products' 16 rows, and the query rows come in eights.  P^T comes
+// out of S^T with keys as rows, and movmatrix turns it into the other product's operand.  (With query rows as the 16: 84 us
+// on 256 sequences.  With e4m3 mma on the codes as they are, and queries in e4m3 terms: as fast there, where
+// HBM bounds, but nearly twice the cycles of the conversions and f16 products.)
 //
 // Codes come out of shared memory in 16-byte pieces with the products' dimensions and keys permuted to fit: lane
 // (g, c) of a warp takes bytes 16 c .. of the key rows perm(g) and 8 + perm(g) for S (four k-steps' words), and for P V
@@ -42,35 +39,22 @@ struct Attend8Cfg {
     static constexpr int kTileBytes = kStep8 * D * HG;       // K (or V) of a step
     static constexpr int kStagesRaw = 192 * 1024 / kCtas / (2 * kTileBytes);
     static constexpr int kStages = kStagesRaw > 8 ? 8 : kStagesRaw;
-    static constexpr int kNotes = HG * 32;                   // per stage (ks, log2 vs, 1 / vs, -) of two blocks and each head
+    // (ks, log2 vs, 1 / vs, -) of two blocks and each head, of 64 steps: a batch of 32 is written at once, and consumers are
+    // at most kStages steps behind it
+    static constexpr int kNotes = HG * 32;
     static constexpr size_t kNoteOff = (size_t)kStages * 2 * kTileBytes;
-    static constexpr size_t kBarOff = kNoteOff + (size_t)kStages * kNotes;   // full and empty [kStages]
+    static constexpr size_t kBarOff = kNoteOff + (size_t)64 * kNotes;   // full and empty [kStages]
     static constexpr size_t kSmem = kBarOff + (size_t)kStages * 16 + 1024;   // + alignment slack
     static_assert(kStages >= 3, "ring");
     static_assert((kSmem + 2048) * kCtas <= 228 * 1024, "shared memory budget");
 };
 
-__device__ __forceinline__ void mma_codes(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 // The transpose of an 8 x 8 matrix of 16-bit elements, two of a row per lane.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-// Two fp32 values as e4m3 codes (x0 in the low byte); what is infinite becomes NaN.
-__device__ __forceinline__ uint32_t codes_of(float x0, float x1) {
-    uint16_t r;
-    x0 += x0 - x0;
-    x1 += x1 - x1;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(x1), "f"(x0));
-    return r;
-}
-
 // The physical key row (of 8) of index n of a product.
 template <int D>
 __device__ __forceinline__ int perm8(int n) {
@@ -102,8 +86,7 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
     attend8_mma_kernel(const Attend8Args a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
     using C = Attend8Cfg<D, NQ, MB, HG>;
     using H = Mma16<__half>;
-    constexpr int kKS = D / 32, kMT = D / 16, kRows = C::kRows;             // k-steps of S, 16-row tiles of O^T
-    constexpr int kTerms = std::is_same<T, __half>::value ? 3 : 2;
+    constexpr int kKS = D / 16, kMT = D / 16, kRows = C::kRows;             // k-steps of S, 16-row tiles of O^T
     constexpr int kWarps = C::kConsumers + 1;
     extern __shared__ unsigned char smem_raw[];
     __shared__ long long sums[kWarps];
@@ -210,9 +193,7 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
     if (warp == C::kConsumers) {
         // ------------------------------------------------------------ producer
         const uint64_t pol = policy_evict_first();
-        // per lane, of the batch's step `lane`: its blocks (-1: none) and the notes of their heads
-        int z[2] = {-1, -1}, issued = 0;
-        float ks[2][HG], vs[2][HG];
+        int z[2] = {-1, -1}, issued = 0;   // per lane: the blocks of the batch's step `lane` (first head's index, or -1)
         bool ok = true;
         while (ok && left > 0) {
             const int n = min(left, p.st.count - p.v);
@@ -222,46 +203,45 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
                     Place8 x = p;
                     x.v += lane;
                     const int key = first_key(x);
+                    const bool mine = i + lane < n;
+                    const uint32_t at = notes + (uint32_t)(C::kNotes * ((issued + lane) & 63));
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
                         const int k = key + b * a.B;
                         z[b] = -1;
-                        if (b < nb && i + lane < n && k < p.q.len) {
+                        if (b < nb && mine && k < p.q.len) {
                             const int pb = a.block_tables[(size_t)p.s * a.max_blocks + (k >> lb)];
                             if (pb >= 0 && pb < a.N) z[b] = pb * a.Hkv + p.h * HG;
                             else set_error(a.err, PA_DEVERR_BAD_BLOCK);
                         }
+                        if (!mine) continue;
 #pragma unroll
                         for (int h = 0; h < HG; ++h) {
-                            ks[b][h] = z[b] >= 0 ? a.k_scales[z[b] + h] : 0.f;
-                            vs[b][h] = z[b] >= 0 ? a.v_scales[z[b] + h] : -1.f;
-                        }
-                    }
-                }
-                const int st = issued % C::kStages;
-                if (issued >= C::kStages) ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty(st), (uint32_t)((issued / C::kStages) - 1) & 1u, kWaitLimit));
-                if (ok && lane == turn) {
-                    const uint32_t at = notes + (uint32_t)(C::kNotes * st), dst = ring + (uint32_t)(st * 2 * C::kTileBytes);
-#pragma unroll
-                    for (int h = 0; h < HG; ++h)
-#pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            const int from = b < nb ? b : 0;
-                            const float k1 = from ? ks[1][h] : ks[0][h], v1 = from ? vs[1][h] : vs[0][h];
-                            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %3};" ::"r"(at + 32 * h + 16 * b), "f"(k1),
-                                         "f"(v1 > 0.f ? lg2(v1) : 0.f), "f"(1.f / v1)
+                            // a block that is not there has no scale; the second half of a block of 32 has the first's
+                            const int from = nb == 1 ? z[0] : z[b];
+                            const float ks = from >= 0 ? a.k_scales[from + h] : 0.f, vs = from >= 0 ? a.v_scales[from + h] : -1.f;
+                            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %3};" ::"r"(at + 32 * h + 16 * b), "f"(ks),
+                                         "f"(vs > 0.f ? lg2(vs) : 0.f), "f"(1.f / vs)
                                          : "memory");
                         }
-                    const int there = (z[0] >= 0) + (z[1] >= 0);
+                    }
+                    __syncwarp();
+                }
+                const int st = issued % C::kStages;
+                const int z0 = __shfl_sync(0xffffffffu, z[0], turn), z1 = __shfl_sync(0xffffffffu, z[1], turn);
+                if (issued >= C::kStages) ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty(st), (uint32_t)((issued / C::kStages) - 1) & 1u, kWaitLimit));
+                if (ok && lane == 0) {
+                    const uint32_t dst = ring + (uint32_t)(st * 2 * C::kTileBytes);
+                    const int there = (z0 >= 0) + (z1 >= 0);
                     if (there) mbar_arrive_expect_tx(full(st), (uint32_t)(there * 2 * a.B * D * HG));
                     else mbar_arrive(full(st));
-                    if (z[0] >= 0) {
-                        tma_load_3d(dst, &tmk, 0, 0, z[0], full(st), pol);
-                        tma_load_3d(dst + C::kTileBytes, &tmv, 0, 0, z[0], full(st), pol);
+                    if (z0 >= 0) {
+                        tma_load_3d(dst, &tmk, 0, 0, z0, full(st), pol);
+                        tma_load_3d(dst + C::kTileBytes, &tmv, 0, 0, z0, full(st), pol);
                     }
-                    if (z[1] >= 0) {
-                        tma_load_3d(dst + (uint32_t)(a.B * D * HG), &tmk, 0, 0, z[1], full(st), pol);
-                        tma_load_3d(dst + (uint32_t)(C::kTileBytes + a.B * D * HG), &tmv, 0, 0, z[1], full(st), pol);
+                    if (z1 >= 0) {
+                        tma_load_3d(dst + (uint32_t)(a.B * D * HG), &tmk, 0, 0, z1, full(st), pol);
+                        tma_load_3d(dst + (uint32_t)(C::kTileBytes + a.B * D * HG), &tmv, 0, 0, z1, full(st), pol);
                     }
                 }
                 __syncwarp();
@@ -292,7 +272,7 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
         const int r0 = p.rb * kRows + 8 * NQ * member;       // first row of the warp: row r is token r / G, head r % G
         const bool any = r0 < p.q.n * G;
         // queries as B fragments (lane (g, c): row g of a tile); what belongs to the rows 2 c, 2 c + 1 that a lane has of S^T
-        uint32_t qb[kTerms][kKS][NQ][2];
+        uint32_t qb[kKS][NQ][2];
         float qs[NQ][2];                                     // scale log2(e) over the row's factor
         int pos[NQ][2];
 #pragma unroll
@@ -302,7 +282,6 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
             const int t = on ? r >> lg : 0;
             const uint16_t *row = static_cast<const uint16_t *>(a.q) +
                                   ((size_t)(p.q.q0 + t) * a.Hq + kvh * G + (on ? r & (G - 1) : 0)) * D;
-            uint32_t w[D / 64][8];
             float top = 0.f;
 #pragma unroll
             for (int ch = 0; ch < D / 64; ++ch) {
@@ -311,34 +290,31 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
                     x = *reinterpret_cast<const uint4 *>(row + 16 * (c + 4 * ch));
                     y = *reinterpret_cast<const uint4 *>(row + 16 * (c + 4 * ch) + 8);
                 }
-                w[ch][0] = x.x, w[ch][1] = x.y, w[ch][2] = x.z, w[ch][3] = x.w;
-                w[ch][4] = y.x, w[ch][5] = y.y, w[ch][6] = y.z, w[ch][7] = y.w;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 v = Mma16<T>::unpack(w[ch][i]);
-                    top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
-                }
+                qb[4 * ch][t8][0] = x.x, qb[4 * ch][t8][1] = x.y, qb[4 * ch + 1][t8][0] = x.z, qb[4 * ch + 1][t8][1] = x.w;
+                qb[4 * ch + 2][t8][0] = y.x, qb[4 * ch + 2][t8][1] = y.y, qb[4 * ch + 3][t8][0] = y.z, qb[4 * ch + 3][t8][1] = y.w;
             }
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const int e = min(100, max(-100, 7 - ((int)(__float_as_uint(top) >> 23) - 127)));
-            const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-            const float back = a.scale * kLog2e8 * __uint_as_float((uint32_t)(127 - e) << 23);
+            float back = a.scale * kLog2e8;
+            if constexpr (std::is_same<T, __nv_bfloat16>::value) {   // as f16, the row's largest at 2^10
 #pragma unroll
-            for (int ch = 0; ch < D / 64; ++ch)
+                for (int ks = 0; ks < kKS; ++ks)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {   // four elements: a word of each term
-                    const float2 u = Mma16<T>::unpack(w[ch][2 * i]), v = Mma16<T>::unpack(w[ch][2 * i + 1]);
-                    float x[4] = {u.x * up, u.y * up, v.x * up, v.y * up};
-#pragma unroll
-                    for (int term = 0; term < kTerms; ++term) {
-                        const uint32_t lo = codes_of(x[0], x[1]), hi = codes_of(x[2], x[3]);
-                        qb[term][2 * ch + (i >> 1)][t8][i & 1] = lo | hi << 16;
-                        const float2 a0 = H::unpack(f16_of_codes(lo)), a1 = H::unpack(f16_of_codes(hi));
-                        const float by = term == 0 ? 16.f : 1.f;   // the later terms are in sixteenths
-                        x[0] = (x[0] - a0.x) * by, x[1] = (x[1] - a0.y) * by, x[2] = (x[2] - a1.x) * by, x[3] = (x[3] - a1.y) * by;
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 v = Mma16<T>::unpack(qb[ks][t8][i]);
+                        top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
                     }
-                }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const int e = min(100, max(-100, 10 - ((int)(__float_as_uint(top) >> 23) - 127)));
+                const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+                back *= __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+                for (int ks = 0; ks < kKS; ++ks)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 v = Mma16<T>::unpack(qb[ks][t8][i]);
+                        qb[ks][t8][i] = H::pack(v.x * up, v.y * up);
+                    }
+            }
 #pragma unroll
             for (int o = 0; o < 2; ++o) {
                 qs[t8][o] = __shfl_sync(0xffffffffu, back, 4 * (2 * c + o));
@@ -374,48 +350,58 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
                     float pad;
                     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                                  : "=f"(ks[b]), "=f"(lv[b]), "=f"(iv[b]), "=f"(pad)
-                                 : "r"(notes + (uint32_t)(C::kNotes * st + 32 * head + 16 * b)));
+                                 : "r"(notes + (uint32_t)(C::kNotes * (taken & 63) + 32 * head + 16 * b)));
                 }
                 const bool clear = kb + kStep8 - 1 <= pos_first && (kb >= whole_from || kb + kStep8 <= a.sinks) && iv[0] > 0.f && iv[1] > 0.f;
-                // With one tile of rows both halves of the step go through each stage together; with more, registers are short
-                // and the halves go one after the other.
-                constexpr int kKK = NQ == 1 ? 2 : 1;
-#pragma unroll
+                // Both halves of the step go through each stage together; where registers are short (more rows a warp, or
+                // twelve warps) one after the other.
+                constexpr int kKK = NQ == 1 && C::kConsumers <= 8 ? 2 : 1;
+#pragma unroll 1
                 for (int k0 = 0; k0 < 2; k0 += kKK) {
+                    // the notes of half i2 of this turn
+                    auto of_half = [&](const float (&x)[2], int i2) { return kKK == 2 ? x[i2] : k0 ? x[1] : x[0]; };
                     // ---- S^T = K Q^T, 16 keys at a time: rows g (key perm(g)) and g + 8, columns 2 c, 2 c + 1 of each tile
                     float s[kKK][NQ][4];
 #pragma unroll
-                    for (int i2 = 0; i2 < kKK; ++i2) {
-                        const int kk = k0 + i2;
-                        float rest[NQ][4];
+                    for (int i2 = 0; i2 < kKK; ++i2)
 #pragma unroll
                         for (int t8 = 0; t8 < NQ; ++t8)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) s[i2][t8][e] = rest[t8][e] = 0.f;
-                        const uint32_t at = kst + (kk ? half_at : 0u);
+                            for (int e = 0; e < 4; ++e) s[i2][t8][e] = 0.f;
 #pragma unroll
-                        for (int ch = 0; ch < D / 64; ++ch) {
-                            const uint4 lo = lds128(at + piece8<D>(perm8<D>(g), c + 4 * ch)), hi = lds128(at + piece8<D>(8 + perm8<D>(g), c + 4 * ch));
+                    for (int ch = 0; ch < D / 64; ++ch) {
+                        uint4 lo[kKK], hi[kKK];
 #pragma unroll
-                            for (int t8 = 0; t8 < NQ; ++t8)
-#pragma unroll
-                                for (int term = 0; term < kTerms; ++term) {
-                                    float(&d)[4] = term ? rest[t8] : s[i2][t8];
-                                    mma_codes(d, lo.x, hi.x, lo.y, hi.y, qb[term][2 * ch][t8][0], qb[term][2 * ch][t8][1]);
-                                    mma_codes(d, lo.z, hi.z, lo.w, hi.w, qb[term][2 * ch + 1][t8][0], qb[term][2 * ch + 1][t8][1]);
-                                }
+                        for (int i2 = 0; i2 < kKK; ++i2) {
+                            const uint32_t at = kst + (k0 + i2 ? half_at : 0u);
+                            lo[i2] = lds128(at + piece8<D>(perm8<D>(g), c + 4 * ch));
+                            hi[i2] = lds128(at + piece8<D>(8 + perm8<D>(g), c + 4 * ch));
                         }
+#pragma unroll
+                        for (int w = 0; w < 4; ++w)
+#pragma unroll
+                            for (int i2 = 0; i2 < kKK; ++i2) {
+                                const uint32_t x = w == 0 ? lo[i2].x : w == 1 ? lo[i2].y : w == 2 ? lo[i2].z : lo[i2].w;
+                                const uint32_t y = w == 0 ? hi[i2].x : w == 1 ? hi[i2].y : w == 2 ? hi[i2].z : hi[i2].w;
+                                const uint32_t a0 = f16_of_codes(x & 0xffffu), a1 = f16_of_codes(y & 0xffffu);
+                                const uint32_t a2 = f16_of_codes(x >> 16), a3 = f16_of_codes(y >> 16);
+#pragma unroll
+                                for (int t8 = 0; t8 < NQ; ++t8) H::mma(s[i2][t8], a0, a1, a2, a3, qb[4 * ch + w][t8][0], qb[4 * ch + w][t8][1]);
+                            }
+                    }
+#pragma unroll
+                    for (int i2 = 0; i2 < kKK; ++i2) {
+                        const int kk = k0 + i2;
                         // a_j = z_j + log2 vs
 #pragma unroll
                         for (int t8 = 0; t8 < NQ; ++t8) {
-                            const float mul[2] = {qs[t8][0] * ks[kk], qs[t8][1] * ks[kk]};
+                            const float mul[2] = {qs[t8][0] * of_half(ks, i2), qs[t8][1] * of_half(ks, i2)};
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                float x = fmaf(rest[t8][e], 0.0625f, s[i2][t8][e]);
-                                x = fmaf(x, mul[e & 1], lv[kk]);
+                                float x = fmaf(s[i2][t8][e], mul[e & 1], of_half(lv, i2));
                                 if (!clear) {
                                     const int j = kb + 16 * kk + 8 * (e >> 1) + perm8<D>(g);
-                                    if (!(iv[kk] > 0.f && j <= pos[t8][e & 1] && (a.window == 0 || j > pos[t8][e & 1] - a.window || j < a.sinks)))
+                                    if (!(of_half(iv, i2) > 0.f && j <= pos[t8][e & 1] && (a.window == 0 || j > pos[t8][e & 1] - a.window || j < a.sinks)))
                                         x = -INFINITY;
                                 }
                                 s[i2][t8][e] = x;
@@ -440,7 +426,7 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
                             }
                             if (!clear) {  // a key that no row sees may hold anything
                                 const int j = kb + 16 * kk + row;
-                                if (!(iv[kk] > 0.f && j <= pos_last && (j >= seen_from || j < a.sinks))) {
+                                if (!(of_half(iv, i2) > 0.f && j <= pos_last && (j >= seen_from || j < a.sinks))) {
 #pragma unroll
                                     for (int x = 0; x < D / 32; ++x) vw[i2][e][x] = 0u;
                                 }
@@ -488,8 +474,8 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
                         for (int i2 = 0; i2 < kKK; ++i2) {
                             const float w0 = ex2(s[i2][t8][0] - m0), w1 = ex2(s[i2][t8][1] - m1), w2 = ex2(s[i2][t8][2] - m0), w3 = ex2(s[i2][t8][3] - m1);
                             // a block that is not there has weights of 0 (and an iv of -1)
-                            l[t8][0] = fmaf(w0 + w2, iv[k0 + i2], l[t8][0]);
-                            l[t8][1] = fmaf(w1 + w3, iv[k0 + i2], l[t8][1]);
+                            l[t8][0] = fmaf(w0 + w2, of_half(iv, i2), l[t8][0]);
+                            l[t8][1] = fmaf(w1 + w3, of_half(iv, i2), l[t8][1]);
                             pb[i2][t8][0] = transpose8(H::pack(w0, w1));
                             pb[i2][t8][1] = transpose8(H::pack(w2, w3));
                         }
