@@ -34,18 +34,25 @@ template <int D, int NQ, int MB, int HG>
 struct Attend8Cfg {
     static constexpr int kRows = 8 * NQ * MB;                // of a row block
     static constexpr int kConsumers = HG * MB;
-    static constexpr int kThreads = 32 * (kConsumers + 1);
-    static constexpr int kCtas = attend8_ctas(MB, HG);       // per SM
+    static constexpr int kCtas = attend8_ctas(NQ, MB, HG);   // per SM
+    // More than 8 rows a warp: the queries' fragments lie in shared memory.  24 rows: O^T alone takes 96 registers, and whole
+    // warpgroups of consumers take over registers of a producer warpgroup (of which one warp works): two CTAs of 4 + 4
+    // warps are launched at 128 registers, producers keep 24 and consumers get 232 (verify 147 us; 40 and 216: 159).
+    static constexpr bool kWide = NQ > 1;
+    static constexpr bool kSplit = NQ == 3 && kConsumers == 4;
+    static constexpr int kThreads = 32 * (kConsumers + (kSplit ? 4 : 1));
+    static constexpr int kQBytes = kWide ? kConsumers * NQ * D * 16 : 0;
     static constexpr int kTileBytes = kStep8 * D * HG;       // K (or V) of a step
-    static constexpr int kStagesRaw = 192 * 1024 / kCtas / (2 * kTileBytes);
+    static constexpr int kStagesRaw = (192 * 1024 / kCtas - kQBytes) / (2 * kTileBytes);
     static constexpr int kStages = kStagesRaw > 8 ? 8 : kStagesRaw;
     // (ks, log2 vs, 1 / vs, -) of two blocks and each head, of 64 steps: a batch of 32 is written at once, and consumers are
     // at most kStages steps behind it
     static constexpr int kNotes = HG * 32;
     static constexpr size_t kNoteOff = (size_t)kStages * 2 * kTileBytes;
-    static constexpr size_t kBarOff = kNoteOff + (size_t)64 * kNotes;   // full and empty [kStages]
+    static constexpr size_t kQOff = kNoteOff + (size_t)64 * kNotes;
+    static constexpr size_t kBarOff = kQOff + kQBytes;       // full and empty [kStages]
     static constexpr size_t kSmem = kBarOff + (size_t)kStages * 16 + 1024;   // + alignment slack
-    static_assert(kStages >= 3, "ring");
+    static_assert(kStages >= 2, "ring");
     static_assert((kSmem + 2048) * kCtas <= 228 * 1024, "shared memory budget");
 };
 
@@ -87,7 +94,7 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
     using C = Attend8Cfg<D, NQ, MB, HG>;
     using H = Mma16<__half>;
     constexpr int kKS = D / 16, kMT = D / 16, kRows = C::kRows;             // k-steps of S, 16-row tiles of O^T
-    constexpr int kWarps = C::kConsumers + 1;
+    constexpr int kWarps = C::kThreads / 32;
     extern __shared__ unsigned char smem_raw[];
     __shared__ long long sums[kWarps];
     __shared__ int4 begin_at;  // (sequence, -, rest low, rest high) of the first step
@@ -190,8 +197,10 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
     };
     auto first_key = [&](const Place8 &x) { return (x.v < x.st.ns ? x.v : x.v + x.st.gap) * kStep8; };
 
-    if (warp == C::kConsumers) {
+    if (warp >= C::kConsumers) {
         // ------------------------------------------------------------ producer
+        if constexpr (C::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 24;\n" ::: "memory");
+        if (warp > C::kConsumers) return;
         const uint64_t pol = policy_evict_first();
         int z[2] = {-1, -1}, issued = 0;   // per lane: the blocks of the batch's step `lane` (first head's index, or -1)
         bool ok = true;
@@ -215,7 +224,7 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
                             else set_error(a.err, PA_DEVERR_BAD_BLOCK);
                         }
                         if (!mine) continue;
-#pragma unroll
+#pragma unroll 1
                         for (int h = 0; h < HG; ++h) {
                             // a block that is not there has no scale; the second half of a block of 32 has the first's
                             const int from = nb == 1 ? z[0] : z[b];
@@ -257,6 +266,7 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
     }
 
     // ------------------------------------------------------------ consumers
+    if constexpr (C::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;\n" ::: "memory");
     const int head = warp % HG, member = warp / HG;        // of the group, of the row block's warps
     const uint32_t head_at = (uint32_t)(head * a.B * D);   // of a box
     const uint32_t half_at = (uint32_t)(a.B == 16 ? 16 * D * HG : 16 * D);   // from key 0 to key 16 of a head
@@ -272,11 +282,13 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
         const int r0 = p.rb * kRows + 8 * NQ * member;       // first row of the warp: row r is token r / G, head r % G
         const bool any = r0 < p.q.n * G;
         // queries as B fragments (lane (g, c): row g of a tile); what belongs to the rows 2 c, 2 c + 1 that a lane has of S^T
-        uint32_t qb[kKS][NQ][2];
+        uint32_t qb[kKS][C::kWide ? 1 : NQ][2];
+        const uint32_t q_at = ring + (uint32_t)C::kQOff + (uint32_t)(warp * NQ * D * 16 + lane * 16);   // [k-step pair][tile][lane]: two k-steps
         float qs[NQ][2];                                     // scale log2(e) over the row's factor
         int pos[NQ][2];
 #pragma unroll
         for (int t8 = 0; t8 < NQ; ++t8) {
+            const int tq = C::kWide ? 0 : t8;
             const int r = r0 + 8 * t8 + g;
             const bool on = r < p.q.n * G;
             const int t = on ? r >> lg : 0;
@@ -290,8 +302,8 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
                     x = *reinterpret_cast<const uint4 *>(row + 16 * (c + 4 * ch));
                     y = *reinterpret_cast<const uint4 *>(row + 16 * (c + 4 * ch) + 8);
                 }
-                qb[4 * ch][t8][0] = x.x, qb[4 * ch][t8][1] = x.y, qb[4 * ch + 1][t8][0] = x.z, qb[4 * ch + 1][t8][1] = x.w;
-                qb[4 * ch + 2][t8][0] = y.x, qb[4 * ch + 2][t8][1] = y.y, qb[4 * ch + 3][t8][0] = y.z, qb[4 * ch + 3][t8][1] = y.w;
+                qb[4 * ch][tq][0] = x.x, qb[4 * ch][tq][1] = x.y, qb[4 * ch + 1][tq][0] = x.z, qb[4 * ch + 1][tq][1] = x.w;
+                qb[4 * ch + 2][tq][0] = y.x, qb[4 * ch + 2][tq][1] = y.y, qb[4 * ch + 3][tq][0] = y.z, qb[4 * ch + 3][tq][1] = y.w;
             }
             float back = a.scale * kLog2e8;
             if constexpr (std::is_same<T, __nv_bfloat16>::value) {   // as f16, the row's largest at 2^10
@@ -299,7 +311,7 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
                 for (int ks = 0; ks < kKS; ++ks)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float2 v = Mma16<T>::unpack(qb[ks][t8][i]);
+                        const float2 v = Mma16<T>::unpack(qb[ks][tq][i]);
                         top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
                     }
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -311,9 +323,16 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
                 for (int ks = 0; ks < kKS; ++ks)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float2 v = Mma16<T>::unpack(qb[ks][t8][i]);
-                        qb[ks][t8][i] = H::pack(v.x * up, v.y * up);
+                        const float2 v = Mma16<T>::unpack(qb[ks][tq][i]);
+                        qb[ks][tq][i] = H::pack(v.x * up, v.y * up);
                     }
+            }
+            if constexpr (C::kWide) {
+#pragma unroll
+                for (int ks = 0; ks < kKS; ks += 2)
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(q_at + (uint32_t)((ks / 2 * NQ + t8) * 512)), "r"(qb[ks][0][0]),
+                                 "r"(qb[ks][0][1]), "r"(qb[ks + 1][0][0]), "r"(qb[ks + 1][0][1])
+                                 : "memory");
             }
 #pragma unroll
             for (int o = 0; o < 2; ++o) {
@@ -378,16 +397,27 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
                             hi[i2] = lds128(at + piece8<D>(8 + perm8<D>(g), c + 4 * ch));
                         }
 #pragma unroll
-                        for (int w = 0; w < 4; ++w)
+                        for (int w2 = 0; w2 < 4; w2 += 2) {
+                            uint4 q4[C::kWide ? NQ : 1];
+                            if constexpr (C::kWide) {
 #pragma unroll
-                            for (int i2 = 0; i2 < kKK; ++i2) {
-                                const uint32_t x = w == 0 ? lo[i2].x : w == 1 ? lo[i2].y : w == 2 ? lo[i2].z : lo[i2].w;
-                                const uint32_t y = w == 0 ? hi[i2].x : w == 1 ? hi[i2].y : w == 2 ? hi[i2].z : hi[i2].w;
-                                const uint32_t a0 = f16_of_codes(x & 0xffffu), a1 = f16_of_codes(y & 0xffffu);
-                                const uint32_t a2 = f16_of_codes(x >> 16), a3 = f16_of_codes(y >> 16);
-#pragma unroll
-                                for (int t8 = 0; t8 < NQ; ++t8) H::mma(s[i2][t8], a0, a1, a2, a3, qb[4 * ch + w][t8][0], qb[4 * ch + w][t8][1]);
+                                for (int t8 = 0; t8 < NQ; ++t8) q4[t8] = lds128(q_at + (uint32_t)(((2 * ch + w2 / 2) * NQ + t8) * 512));
                             }
+#pragma unroll
+                            for (int w = w2; w < w2 + 2; ++w)
+#pragma unroll
+                                for (int i2 = 0; i2 < kKK; ++i2) {
+                                    const uint32_t x = w == 0 ? lo[i2].x : w == 1 ? lo[i2].y : w == 2 ? lo[i2].z : lo[i2].w;
+                                    const uint32_t y = w == 0 ? hi[i2].x : w == 1 ? hi[i2].y : w == 2 ? hi[i2].z : hi[i2].w;
+                                    const uint32_t a0 = f16_of_codes(x & 0xffffu), a1 = f16_of_codes(y & 0xffffu);
+                                    const uint32_t a2 = f16_of_codes(x >> 16), a3 = f16_of_codes(y >> 16);
+#pragma unroll
+                                    for (int t8 = 0; t8 < NQ; ++t8) {
+                                        if constexpr (C::kWide) H::mma(s[i2][t8], a0, a1, a2, a3, w & 1 ? q4[t8].z : q4[t8].x, w & 1 ? q4[t8].w : q4[t8].y);
+                                        else H::mma(s[i2][t8], a0, a1, a2, a3, qb[4 * ch + w][t8][0], qb[4 * ch + w][t8][1]);
+                                    }
+                                }
+                        }
                     }
 #pragma unroll
                     for (int i2 = 0; i2 < kKK; ++i2) {
@@ -433,7 +463,7 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
                             }
                         }
                     };
-                    load_v(0);
+                    if constexpr (NQ < 3) load_v(0);   // (24 rows a warp: registers for it come free later)
                     // ---- the running reference
                     bool need = false;
                     float mx[NQ][2];
@@ -481,6 +511,7 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
                         }
                     }
                     // ---- O^T += V^T P^T
+                    if constexpr (NQ >= 3) load_v(0);
                     if constexpr (kKK == 2) load_v(1);
 #pragma unroll
                     for (int i2 = 0; i2 < kKK; ++i2)
@@ -640,19 +671,14 @@ cudaError_t launch_attend8_t(const Attend8Args &a, const CUtensorMap &tmk, const
 
 template <typename T, int D, int NQ, int MB>
 cudaError_t dispatch_heads(const Attend8Args &a, int hg, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st) {
-    if constexpr (MB < 4)
+    if constexpr (NQ * MB < 6)
         if (hg == 4) return launch_attend8_t<T, D, NQ, MB, 4>(a, tmk, tmv, st);
     return hg == 2 ? launch_attend8_t<T, D, NQ, MB, 2>(a, tmk, tmv, st) : launch_attend8_t<T, D, NQ, MB, 1>(a, tmk, tmv, st);
 }
 template <typename T, int D>
 cudaError_t dispatch_attend8(const Attend8Args &a, Rows8 r, int hg, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st) {
-    if (r.nq == 1) {
-        switch (r.mb) {
-            case 1: return dispatch_heads<T, D, 1, 1>(a, hg, tmk, tmv, st);
-            case 2: return dispatch_heads<T, D, 1, 2>(a, hg, tmk, tmv, st);
-            default: return dispatch_heads<T, D, 1, 3>(a, hg, tmk, tmv, st);
-        }
-    }
+    if (r.nq == 1) return r.mb == 1 ? dispatch_heads<T, D, 1, 1>(a, hg, tmk, tmv, st) : dispatch_heads<T, D, 1, 2>(a, hg, tmk, tmv, st);
+    if (r.nq == 3) return r.mb == 1 ? dispatch_heads<T, D, 3, 1>(a, hg, tmk, tmv, st) : dispatch_heads<T, D, 3, 2>(a, hg, tmk, tmv, st);
     return r.mb == 2 ? dispatch_heads<T, D, 2, 2>(a, hg, tmk, tmv, st) : dispatch_heads<T, D, 2, 4>(a, hg, tmk, tmv, st);
 }
 

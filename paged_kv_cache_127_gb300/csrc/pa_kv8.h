@@ -58,18 +58,20 @@ struct Attend8Args {
     float scale;
 };
 // mma.sync path, and the join of its parts: `mb` warps with 8 * nq rows each for a row block of a KV head, `hg` KV heads
-// a CTA, which has a producer warp besides; up to ten warps an SM, or one CTA.
+// a CTA, which has a producer warp besides; up to eight consumers and ten warps an SM.
 constexpr int kSms8 = 152;
-constexpr int attend8_ctas(int mb, int hg) { return hg * mb < 10 ? 10 / (hg * mb + 1) : 1; }   // per SM
+constexpr int attend8_ctas(int nq, int mb, int hg) {   // per SM
+    return nq < 3 ? 10 / (hg * mb + 1) : hg * mb == 4 ? 2 : 8 / (hg * mb + 1);
+}
 struct Rows8 {
     int nq, mb;
 };
 inline Rows8 attend8_rows(int max_query_len, int G) {
     const long long rows = (long long)max_query_len * G;
-    return rows <= 8 ? Rows8{1, 1} : rows <= 16 ? Rows8{1, 2} : rows <= 24 ? Rows8{1, 3} : rows <= 32 ? Rows8{2, 2} : Rows8{2, 4};
+    return rows <= 8 ? Rows8{1, 1} : rows <= 16 ? Rows8{1, 2} : rows <= 24 ? Rows8{3, 1} : rows <= 32 ? Rows8{2, 2} : rows <= 48 ? Rows8{3, 2} : Rows8{2, 4};
 }
-inline int attend8_heads(int Hkv, int mb) {
-    return Hkv % 4 == 0 && mb < 4 ? 4 : Hkv % 2 == 0 ? 2 : 1;
+inline int attend8_heads(int Hkv, Rows8 r) {
+    return Hkv % 4 == 0 && r.nq * r.mb < 6 ? 4 : Hkv % 2 == 0 ? 2 : 1;
 }
 cudaError_t launch_attend8_mma_f16_64(const Attend8Args &a, Rows8 rows, int hg, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
 cudaError_t launch_attend8_mma_f16_128(const Attend8Args &a, Rows8 rows, int hg, const CUtensorMap &tmk, const CUtensorMap &tmv, cudaStream_t st);
