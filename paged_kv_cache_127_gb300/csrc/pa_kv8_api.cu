@@ -67,11 +67,12 @@ Layout8 layout8(const pa_dims *d, int32_t max_q) {
     L.rows = pa::attend8_rows(max_q, G);
     L.hg = pa::attend8_heads(d->num_kv_heads, L.rows);
     const int64_t rows = 8 * L.rows.nq * L.rows.mb, blocks = ((int64_t)max_q * G + rows - 1) / rows;
-    // no more CTAs than give each of them four steps of 32 keys
+    // no more CTAs than give each of them four steps of 32 keys, or one where 64 CTAs suffice for that
     const int64_t steps = ((int64_t)d->max_blocks_per_seq * d->block_size + 31) / 32;
     const int64_t most = (int64_t)d->num_seqs * (d->num_kv_heads / L.hg) * blocks;  // at most 2^31
     const int64_t cap = pa::kSms8 * pa::attend8_ctas(L.rows.nq, L.rows.mb, L.hg);
-    const int64_t units = most > cap * 4 / steps ? cap : (most * steps + 3) / 4;
+    const int64_t all = most > cap * 4 / steps ? cap * 4 : most * steps, fours = (all + 3) / 4;
+    const int64_t units = fours > 64 ? fours : (all < 64 ? all : 64);
     L.units = (int)(units < cap ? (units > 0 ? units : 1) : cap);
     L.list = 256;
     L.parts = L.list + up256((size_t)most * sizeof(int2));
