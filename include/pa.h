@@ -425,8 +425,8 @@ PA_API int32_t pa_rope_axes_write_kv(const pa_dims *dims, const pa_rope *rope, c
  * PA_BF16 (PA_ERR_UNSUPPORTED for PA_F32), D is 64 or 128 and B 16 or 32.
  *   k, v                 codes [N, Hkv, B, D], device, 16-byte aligned
  *   k_scales, v_scales   float32 [N, Hkv], device.  The writes store powers of two.  The
- *                        attention calls take any positive finite scale (those of V within
- *                        2^60 of each other in one sequence)
+ *                        attention calls take any scales from 2^-80 to 2^120 (those of V
+ *                        within 2^60 of each other in one sequence)
  */
 typedef struct pa_cache8 {
     void *k, *v;
@@ -450,8 +450,8 @@ typedef struct pa_cache8 {
  *   axes          as for pa_rope_axes_write_kv; NULL: positions int32 [num_tokens]
  *   slot_mapping  as for pa_write_kv; moreover the tokens of one block stand next to each
  *                 other in the list (with nothing between them, padding neither), as the
- *                 tokens of a sequence do: two stretches of one block in one call
- *                 leave that block's scale and codes unspecified
+ *                 tokens of a sequence do: two stretches of one block in one call, or
+ *                 one slot twice, leave that block's scale and codes unspecified
  * A value is rounded once, to the nearest code (ties to even); what is not finite, or is
  * not after its rotation, becomes NaN.  The queries go to q_out in kv_dtype.  Other
  * arguments and errors as for pa_rope_write_kv.
@@ -492,7 +492,8 @@ typedef struct pa_window {
  *
  * with K_j, V_j the values that the codes stand for.  Scores, weights' sums and outputs are held
  * in fp32; the codes go into the products as they are (exact in 16 bits), and the weights are
- * rounded to 11 bits before the second one.
+ * rounded to 11 bits before the second one.  Short chunks and decodes over bf16 take a row's queries as f16 by a power of
+ * two, exactly down to 2^-24 of the row's largest.  |q| < 2^110.
  *
  *   window        NULL: all keys
  *   out           [S | T, Hq, D] float32, or kv_dtype when out_dtype == kv_dtype

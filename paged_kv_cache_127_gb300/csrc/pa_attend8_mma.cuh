@@ -608,6 +608,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps8) attend8_merge_kernel(const 
     if (q.len > 0) {
         note = reinterpret_cast<const int2 *>(a.list)[((size_t)s * (a.Hkv / HG) + h / HG) * nrb + rb];
         if (note.y == 0) return;
+        // (the note of a group whose first step timed out was not written: the parts that are read exist all the same)
+        if (note.y < 0 || note.x < 0 || note.x >= 2 * a.units || note.y > a.units - note.x / 2) return;
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     // the parts: the first in slot note.x, the others in the following CTAs' first slots

@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
                 const bool whole = fminf(fminf(n4[0].w, n4[1].w), fminf(n4[2].w, n4[3].w)) > 0.f;
                 const int kb = (j < it.ns ? j : j + it.gap) * C::kN;
                 const int lim = pos - kb;                                     // last visible key of the step
-                const int from = a.window > 0 ? lim - a.window + 1 : 0;       // first one of the window
+                const int from = a.window > 0 ? max(lim, -1) - a.window + 1 : 0;   // first one of the window
                 tc::tmem_wait_ld();
                 float f[C::kN];
 #pragma unroll

@@ -31,6 +31,8 @@ int32_t check_cache8(const pa_cache8 *c) {
     return PA_OK;
 }
 
+constexpr int32_t kMaxTokens8 = INT32_MAX - 64;   // a write's tokens, and the tile behind the last one, in 32 bits
+
 int32_t check_attend8(const pa_dims *d) {
     const int32_t rc = check_shape8(d);
     if (rc != PA_OK) return rc;
@@ -209,7 +211,7 @@ int32_t pa_rope_write_kv8(const pa_dims *dims, const pa_rope *rope, const pa_axe
     int32_t rc = check_shape8(dims);
     if (rc == PA_OK) rc = pa::check_rope(dims, rope, axes);
     if (rc != PA_OK) return rc;
-    if (num_tokens < 0) return PA_ERR_INVALID;
+    if (num_tokens < 0 || num_tokens > kMaxTokens8) return PA_ERR_INVALID;
     if (num_tokens == 0) return PA_OK;
     rc = check_cache8(cache);
     if (rc == PA_OK)
@@ -239,7 +241,7 @@ int32_t pa_write_kv8(const pa_dims *dims, const void *k, int64_t k_stride, const
                      const int64_t *slot_mapping, int32_t num_tokens, const pa_cache8 *cache, void *stream) {
     int32_t rc = check_shape8(dims);
     if (rc != PA_OK) return rc;
-    if (num_tokens < 0) return PA_ERR_INVALID;
+    if (num_tokens < 0 || num_tokens > kMaxTokens8) return PA_ERR_INVALID;
     if (num_tokens == 0) return PA_OK;
     rc = check_cache8(cache);
     if (rc != PA_OK) return rc;

@@ -147,3 +147,9 @@ def test_workspaces(pa):
     # no more than the warps of the card can fill, whatever the tables hold
     most = pa.pa_decode8_workspace_bytes(dims(pa, num_seqs=4000, max_blocks_per_seq=10000, head_dim=128))
     assert most < 12 << 20
+
+
+def test_writes_of_too_many_tokens_are_refused(pa):
+    assert plain_write8(pa, dims(pa), T=2 ** 31 - 1) == pa.PA_ERR_INVALID
+    assert plain_write8(pa, dims(pa), T=2 ** 31 - 20) == pa.PA_ERR_INVALID
+    assert write8(pa, dims(pa), T=2 ** 31 - 1) == pa.PA_ERR_INVALID
