@@ -3,14 +3,16 @@
 // shared memory and the accumulators in tensor memory (TMEM).
 //
 // Work: an item is (MT 128-row tiles, KV head, sequence), row r = token r / G, head r % G; its CTA walks the keys
-// that some of its rows see in steps of 64, with no split and no merge.  Persistent CTAs, one per SM, claim items from
-// a longest-first list.  Warps:
+// that some of its rows see in steps of 64.  Persistent CTAs, one per SM, claim items from a longest-first list; or, where
+// items are few and long, all items' steps stand in one line of which each CTA takes an equal stretch, pieces of items leave
+// their (m, l, O) in the workspace, and a second launch joins them.  (The line for all calls: 356 us instead of 221 for
+// 16 x 512 tokens, as each CTA then works on keys of its own instead of all on the same few sequences'.)  Warps:
 //   0, 1       send for tile 0's and tile 1's queries (TMA) and issue  S_u = Q_u K^T  (M 128, N 64, K = D)
 //   2, 3       issue their  O_u += P_u V    (M 128, N = D, K = 64), P from TMEM
 //   4 .. 11    converters, a warpgroup for K and one for V, each warp with one 16-key box of every step: it loads its
 //              box's codes a step ahead, turns them into 16-bit floats (K into the queries' type, V into f16; both
-//              exact) and stores them as the swizzled operands; K's also publish the box's scales, and warp 4 claims
-//              the items.
+//              exact) and stores them as the swizzled operands; K's also publish the box's scales, and warp 4
+//              publishes the items.
 //   12 ..      one softmax warpgroup per tile, one thread per row
 // Converting once per step serves both tiles, and the codes' 16-bit form never leaves the SM.  The alternative, e4m3
 // operands with Q and P split in two terms each, would need as many products, and the split of P in the softmax
@@ -76,22 +78,21 @@ struct Umma8Cfg {
     static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
 
-// One work item, as the converters publish it to a tile's roles; end: no more items.
+// One work item, or a piece of one, as the converters publish it to a tile's roles; end: no more items.
 struct Item8 {
-    int s, kvh, r0, qs, n, len, tiles, count, ns, gap, lo, hi, end;
+    int s, kvh, r0, qs, n, len, tiles, v0, count, ns, gap, lo, hi, part, end;   // its steps v0 .. v0 + count - 1; part -1: the whole item
 };
 static_assert(sizeof(Item8) <= 64, "an item's share of shared memory");
 
 template <typename C>
-__device__ __forceinline__ bool umma_item8(const Attend8Args &a, int w, int nwork, Item8 &it) {
-    it.end = w >= nwork;
-    if (it.end) return false;
-    const int4 e = a.list[w / a.Hkv];   // (sequence, tile group, -, -)
+__device__ __forceinline__ bool umma_item8(const Attend8Args &a, int s, int group, int kvh, Item8 &it) {
     const int G = a.Hq / a.Hkv, MT = a.tiles;
-    const Seq8 q = seq_of(a, e.x, false);
-    it.s = e.x;
-    it.kvh = w % a.Hkv;
-    it.r0 = e.y * C::kM * MT;
+    const Seq8 q = seq_of(a, s, false);
+    it.s = s;
+    it.kvh = kvh;
+    it.r0 = group * C::kM * MT;
+    it.v0 = 0;
+    it.part = -1;
     it.qs = q.q0;
     it.n = q.n;
     it.len = q.len;
@@ -103,7 +104,7 @@ __device__ __forceinline__ bool umma_item8(const Attend8Args &a, int w, int nwor
     it.ns = st.ns;
     it.gap = st.gap;
     it.count = st.count;
-    return true;
+    return q.n * G > it.r0;
 }
 
 // Bits 0 .. x - 1 of a word (none for x <= 0, all from 32 on).
@@ -166,7 +167,7 @@ __device__ __forceinline__ bool group_all(int id, bool pred) {   // barrier over
 
 // The ring's stage and phase follow the count g of steps so far, the S/P buffers and their phases the count c of the
 // tile's own steps, the item slots and query-tile sets the count of items.
-template <typename T, int D, int MT>
+template <typename T, int D, int MT, bool kLine>
 __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
     attend8_umma_kernel(const Attend8Args a, const __grid_constant__ CUtensorMap tmq) {
     using C = Umma8Cfg<D, MT>;
@@ -239,7 +240,7 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
     tc::fence_after_sync();
     const uint32_t tbase = *tslot;
     griddep_wait();  // the plan's list, longest first
-    const int nwork = max(0, a.hdr[0]) * a.Hkv;
+    const int nwork = kLine ? 0 : max(0, a.hdr[0]) * a.Hkv;
 
     // The converters of K or of V: warp w of the group has box w of every step.
     auto convert = [&](auto of_v) {
@@ -259,6 +260,8 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
         const uint32_t ring = kvb + (kV ? (uint32_t)C::kTile : 0u) + (uint32_t)((ch >> 2) * C::kHalf + (16 * box + row) * 128);
         int g = 0, k = 0, j = 0, count = 0;            // ring steps, items, the step to fetch next and its item's
         int next_w = blockIdx.x;                       // a CTA's first item needs no claim
+        int4 at_line = make_int4(0, 0, 0, 0);          // (entry, KV head, step, steps left)
+        if constexpr (kLine) at_line = a.starts[blockIdx.x];
         Item8 it;
         bool ok = true;
         // per lane, for the item's steps 32 n + lane: where the box's codes are (null: no row sees them, or the block
@@ -269,7 +272,26 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
         // the next item; false when there is none (or on a timeout)
         auto next_item = [&]() {
             if (first) {
-                const bool have = umma_item8<C>(a, next_w, nwork, it);
+                const bool have = kLine ? at_line.w > 0 : next_w < nwork;
+                it.end = !have;
+                if (!kLine && have) {
+                    const int4 e = a.list[next_w / a.Hkv];   // (sequence, tile group, -, -)
+                    umma_item8<C>(a, e.x, e.y, next_w % a.Hkv, it);
+                } else if (have) {
+                    for (;; ++at_line.x) {
+                        const bool there = umma_item8<C>(a, at_line.x / a.groups, at_line.x % a.groups, at_line.y, it);
+                        if (there || at_line.x >= a.S * a.groups - 1) break;
+                    }
+                    const int all = it.count, n = min(at_line.w, all - at_line.z);
+                    it.v0 = at_line.z;
+                    it.count = n;
+                    it.part = n == all ? -1 : 2 * (int)blockIdx.x + (k > 0);
+                    if (n < all && at_line.z == 0 && lane == 0)
+                        a.notes[blockIdx.x] = make_int4(at_line.x, at_line.y, it.part, 1 + (all - n + a.hdr[1] - 1) / a.hdr[1]);
+                    at_line.w -= n;
+                    at_line.z = 0;
+                    if (++at_line.y == a.Hkv) at_line.y = 0, ++at_line.x;
+                }
                 const int x = k & 1;
 #pragma unroll 1
                 for (int u = 0; ok && u < MT; ++u) {
@@ -280,7 +302,7 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
                     }
                     __syncwarp();
                 }
-                if (have) {
+                if (!kLine && have) {
                     int w = 0;
                     if (lane == 0) w = (int)gridDim.x + atomicAdd(&a.hdr[1], 1);
                     next_w = __shfl_sync(0xffffffffu, w, 0);
@@ -300,9 +322,9 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
         auto fetch = [&]() {
             if (j == count && !next_item()) return false;
             if ((j & 31) == 0) {
-                const int v = j + lane, b0 = (v < it.ns ? v : v + it.gap) * C::kN + 16 * box;
+                const int v = (kLine ? it.v0 : 0) + j + lane, b0 = (v < it.ns ? v : v + it.gap) * C::kN + 16 * box;
                 int id = -2;
-                if (v < it.count && b0 < it.hi && (b0 + 15 >= it.lo || b0 < a.sinks)) id = a.block_tables[(size_t)it.s * a.max_blocks + (b0 >> lb)];
+                if (j + lane < it.count && b0 < it.hi && (b0 + 15 >= it.lo || b0 < a.sinks)) id = a.block_tables[(size_t)it.s * a.max_blocks + (b0 >> lb)];
                 const bool good = (unsigned)id < (unsigned)a.N;
                 const size_t bh = (size_t)id * a.Hkv + it.kvh;
                 src = good ? cache + (bh * a.B + (b0 & (a.B - 1))) * D : nullptr;
@@ -513,7 +535,7 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
                 float ck[4] = {n4[0].x, n4[1].x, n4[2].x, n4[3].x}, lv[4] = {n4[0].y, n4[1].y, n4[2].y, n4[3].y};
                 const float iv[4] = {n4[0].z, n4[1].z, n4[2].z, n4[3].z};
                 const bool whole = fminf(fminf(n4[0].w, n4[1].w), fminf(n4[2].w, n4[3].w)) > 0.f;
-                const int kb = (j < it.ns ? j : j + it.gap) * C::kN;
+                const int v = (kLine ? it.v0 : 0) + j, kb = (v < it.ns ? v : v + it.gap) * C::kN;
                 const int lim = pos - kb;                                     // last visible key of the step
                 const int from = a.window > 0 ? max(lim, -1) - a.window + 1 : 0;   // first one of the window
                 tc::tmem_wait_ld();
@@ -605,7 +627,10 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
             ok = group_all(1 + u, ok);
             if (!ok) break;
             tc::fence_after_sync();
-            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const bool in_part = kLine && it.part >= 0;
+            const float inv = in_part ? 1.f : l == 0.f ? 0.f : 1.f / l;
+            float *part = a.parts + (size_t)(in_part ? it.part : 0) * (C::kM * MT) * (D + 2);
+            if (in_part) *reinterpret_cast<float2 *>(part + (size_t)(C::kM * MT) * D + 2 * (C::kM * u + 32 * wq + lane)) = make_float2(m, l);
             // through shared memory, so that a store writes whole rows: 32 columns a turn into it, in 16-byte pieces swizzled by
             // row, then up to 256 bytes of each row out of it
             const uint32_t stage = base + (uint32_t)(C::kOutOff + (size_t)(warp - 12) * C::kOutBytes);
@@ -619,9 +644,9 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
                 for (int r = lane / per; r < 32; r += each) {
                     const int piece = lane % per, Rr = R0 + r, tr = Rr >> lg;
                     const uint4 v = lds128(stage + (uint32_t)(r * 256) + ((uint32_t)(piece ^ (r & 7)) << 4));
-                    if (tr < it.n)
-                        *reinterpret_cast<uint4 *>(static_cast<unsigned char *>(a.out) +
-                                                   ((size_t)(it.qs + tr) * a.Hq + it.kvh * G + (Rr & (G - 1))) * row_bytes + at + 16 * piece) = v;
+                    unsigned char *row = in_part ? reinterpret_cast<unsigned char *>(part + (size_t)(Rr - it.r0) * D)
+                                                 : static_cast<unsigned char *>(a.out) + ((size_t)(it.qs + tr) * a.Hq + it.kvh * G + (Rr & (G - 1))) * row_bytes;
+                    if (tr < it.n) *reinterpret_cast<uint4 *>(row + at + 16 * piece) = v;
                 }
                 __syncwarp();
             };
@@ -630,7 +655,7 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
                 uint32_t ov[32];
                 tc::tmem_ld32(tl + o_col(u) + (uint32_t)(32 * cb), ov);
                 tc::tmem_wait_ld();
-                if (a.out16) {
+                if (a.out16 && !in_part) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t w[4];
@@ -665,13 +690,78 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
     }
 }
 
+// CTA (x, y): where CTA x of the line began an item that others went on with, rows 32 y .. of that item's parts joined,
+//   out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i,   M = max m_i,
+// a warp for four rows at a time, a lane D / 32 columns of each.
+template <typename T, int D, int MT>
+__global__ void __launch_bounds__(256) attend8_join_kernel(const Attend8Args a) {
+    constexpr int kRows = 128 * MT, kPer = D / 32, kR = 4;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    griddep_wait();
+    const int4 note = a.notes[blockIdx.x];   // (entry, KV head, the first part's slot, parts)
+    // (parts past the last CTA's: none, as when the CTA gave up on a wait before it noted anything)
+    if (note.w <= 0 || note.w > a.units - (int)blockIdx.x) return;
+    const int G = a.Hq / a.Hkv, lg = __ffs(G) - 1, lane = threadIdx.x & 31;
+    const Seq8 q = seq_of(a, note.x / a.groups, false);
+    const int row0 = 32 * blockIdx.y + kR * (threadIdx.x >> 5), R0 = note.x % a.groups * kRows + row0;
+    if (R0 >= q.n * G) return;
+    auto part = [&](int i) { return a.parts + (size_t)(i == 0 ? note.z : 2 * ((int)blockIdx.x + i)) * kRows * (D + 2); };
+    auto ml = [&](int i, int r) { return *reinterpret_cast<const float2 *>(part(i) + (size_t)kRows * D + 2 * (row0 + r)); };
+    float M[kR], l[kR], o[kR][kPer];
+#pragma unroll
+    for (int r = 0; r < kR; ++r) M[r] = -INFINITY;
+    for (int i = lane; i < note.w; i += 32)
+#pragma unroll
+        for (int r = 0; r < kR; ++r) M[r] = fmaxf(M[r], ml(i, r).x);
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) M[r] = fmaxf(M[r], __shfl_xor_sync(0xffffffffu, M[r], x));
+        if (M[r] == -INFINITY) M[r] = 0.f;
+        l[r] = 0.f;
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) o[r][x] = 0.f;
+    }
+#pragma unroll 4
+    for (int i = 0; i < note.w; ++i) {
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            const float2 y = ml(i, r);
+            const float w = ex2(y.x - M[r]), *at = part(i) + (size_t)(row0 + r) * D + kPer * lane;
+            l[r] = fmaf(w, y.y, l[r]);
+#pragma unroll
+            for (int x = 0; x < kPer; x += 2) {
+                const float2 v = *reinterpret_cast<const float2 *>(at + x);
+                o[r][x] = fmaf(w, v.x, o[r][x]);
+                o[r][x + 1] = fmaf(w, v.y, o[r][x + 1]);
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+        const int R = R0 + r, t = R >> lg;
+        if (t >= q.n) break;
+        const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+        const size_t at = ((size_t)(q.q0 + t) * a.Hq + note.y * G + (R & (G - 1))) * D + kPer * lane;
+        if (a.out16) {
+#pragma unroll
+            for (int x = 0; x < kPer; x += 2) *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + at + x) = Mma16<T>::pack(o[r][x] * inv, o[r][x + 1] * inv);
+        } else {
+#pragma unroll
+            for (int x = 0; x < kPer; ++x) static_cast<float *>(a.out)[at + x] = o[r][x] * inv;
+        }
+    }
+}
+
 template <typename T, int D, int MT>
 cudaError_t launch_umma8_t(const Attend8Args &a, const CUtensorMap &tmq, cudaStream_t st) {
     using C = Umma8Cfg<D, MT>;
     static std::atomic<int> sms_of[kMaxLaunchDevices];
     int sms = 0;
     cudaError_t e = per_device_value(sms_of, &sms, [](int dev, int *v) {
-        cudaError_t r = cudaFuncSetAttribute(attend8_umma_kernel<T, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+        cudaError_t r = cudaFuncSetAttribute(attend8_umma_kernel<T, D, MT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+        if (r == cudaSuccess)
+            r = cudaFuncSetAttribute(attend8_umma_kernel<T, D, MT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
         if (r != cudaSuccess) return r;
         return cudaDeviceGetAttribute(v, cudaDevAttrMultiProcessorCount, dev);
     });
@@ -679,7 +769,7 @@ cudaError_t launch_umma8_t(const Attend8Args &a, const CUtensorMap &tmq, cudaStr
     const long long rows = (long long)a.max_query_len * (a.Hq / a.Hkv);
     const long long work = (rows + C::kM * MT - 1) / (C::kM * MT) * a.S * a.Hkv;
     if (work > 0x7fffffffLL) return cudaErrorInvalidValue;
-    const long long ctas = work < sms ? work : sms;
+    const long long ctas = a.units ? a.units : work < sms ? work : sms;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(ctas > 0 ? ctas : 1));
     cfg.blockDim = dim3(C::kThreads);
@@ -690,7 +780,13 @@ cudaError_t launch_umma8_t(const Attend8Args &a, const CUtensorMap &tmq, cudaStr
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attend8_umma_kernel<T, D, MT>, a, tmq);
+    if (!a.units) return cudaLaunchKernelEx(&cfg, attend8_umma_kernel<T, D, MT, false>, a, tmq);
+    e = cudaLaunchKernelEx(&cfg, attend8_umma_kernel<T, D, MT, true>, a, tmq);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3((unsigned)a.units, 4u * MT);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, attend8_join_kernel<T, D, MT>, a);
 }
 
 template <typename T>

@@ -45,21 +45,24 @@ struct Attend8Args {
     const int32_t *context_lens;
     const int32_t *query_start;     // [S + 1], or null
     void *out;                      // [T, Hq, D], f32 or the queries' type
-    int *hdr;                       // [0] whether query_start is in order (mma.sync); work items, claims (tcgen05)
+    int *hdr;                       // [0] whether query_start is in order (mma.sync); work items, claims (tcgen05), or steps of a CTA in [1]
     int4 *list;                     // per (sequence, head group, row block): its first part and their number (int2); tcgen05: work items
     float *parts;                   // mma.sync: two parts of a (row block, head group) per CTA, O and (m, l)
+    int4 *notes, *starts;           // tcgen05 line, per CTA: the item it began and others go on with; where it starts
     const uint8_t *k_cache, *v_cache;
     unsigned int *err;
+    int groups;                     // tcgen05: row groups of a sequence, at most
     int S, T, Hq, Hkv, D, B, N, max_blocks, max_query_len;
     int window, sinks;              // window 0: none
     int out16;
-    int units;                      // mma.sync path: CTAs, which share the keys
+    int units;                      // CTAs, which share the keys (tcgen05: 0: whole items, claimed)
     int tiles;                      // tcgen05 path: 128-row tiles of an item (1 or 2)
     float scale;
 };
 // mma.sync path, and the join of its parts: `mb` warps with 8 * nq rows each for a row block of a KV head, `hg` KV heads
 // a CTA, which has a producer warp besides; up to eight consumers and ten warps an SM.
 constexpr int kSms8 = 152;
+constexpr int kLeastSteps8 = 4;   // tcgen05 line: steps of a CTA at least, where a call has that many
 constexpr int attend8_ctas(int nq, int mb, int hg) {   // per SM
     return nq < 3 ? 10 / (hg * mb + 1) : hg * mb == 4 ? 2 : 8 / (hg * mb + 1);
 }

@@ -60,7 +60,7 @@ int32_t check_window(const pa_window *w) { return w && (w->window < 0 || w->sink
 // for each CTA that shares the keys (mma.sync path).
 struct Layout8 {
     pa::Rows8 rows;
-    int hg, units, tiles;  // tiles 0: the mma.sync path
+    int hg, units, tiles, groups;  // tiles 0: the mma.sync path
     size_t list, parts, total;
 };
 Layout8 layout8(const pa_dims *d, int32_t max_q) {
@@ -82,13 +82,29 @@ Layout8 layout8(const pa_dims *d, int32_t max_q) {
     return L;
 }
 Layout8 decode_layout8(const pa_dims *d) { return layout8(d, 1); }
-Layout8 chunk_layout8(const pa_dims *d, int32_t max_q) {
+Layout8 chunk_layout8(const pa_dims *d, int32_t max_q, const pa_window *w) {
     const int G = d->num_q_heads / d->num_kv_heads;
     if (!pa::chunk_uses_umma(max_q, G)) return layout8(d, max_q);
     Layout8 L{};   // a header and the work list
     L.tiles = pa::chunk_umma_rows(max_q, G) / 128;
     L.list = 256;
     const int64_t groups = ((int64_t)max_q * G + 128 * L.tiles - 1) / (128 * L.tiles);
+    L.groups = (int)groups;
+    const int64_t items = groups * d->num_seqs * d->num_kv_heads;
+    // Fewer items than SMs, with many steps each: all steps in a line that the CTAs share equally (list: notes and starts).
+    // That costs some 24 steps' time more (plan, parts, join), and saves a whole item's steps but for the SMs' share.
+    // (8 KV heads of 128, by items and with the line: 512 tokens over 30000 keys 475 and 234 us, over 2000 keys 48 and 44;
+    // 64 tokens over 2000 keys 40 and 34; a window of 1024 of 64 dimensions 26 and 32, 4 chunks of 512 82 and 87)
+    const int64_t keys = (int64_t)d->max_blocks_per_seq * d->block_size;
+    const int64_t reach = w && w->window ? (int64_t)w->window + w->sinks + max_q : keys;
+    const int64_t steps = ((reach < keys ? reach : keys) + 63) / 64;
+    if (items < pa::kSms8 && steps * (pa::kSms8 - items) > 24 * pa::kSms8) {
+        const int64_t units = (items * steps + pa::kLeastSteps8 - 1) / pa::kLeastSteps8;
+        L.units = units < pa::kSms8 ? (int)units : pa::kSms8;
+        L.parts = L.list + up256((size_t)2 * L.units * sizeof(int4));
+        L.total = L.parts + up256((size_t)2 * L.units * 128 * L.tiles * (d->head_dim + 2) * sizeof(float));
+        return L;
+    }
     L.total = L.list + up256((size_t)(groups * d->num_seqs) * sizeof(int4));
     return L;
 }
@@ -138,8 +154,11 @@ void fill8(pa::Attend8Args &a, const pa_dims *d, const pa_window *w, const void 
     a.hdr = reinterpret_cast<int *>(ws);
     a.list = reinterpret_cast<int4 *>(ws + L.list);
     a.parts = reinterpret_cast<float *>(ws + L.parts);
+    a.notes = a.list;
+    a.starts = a.list + L.units;
     a.units = L.units;
     a.tiles = L.tiles;
+    a.groups = L.groups;
     a.S = d->num_seqs;
     a.Hq = d->num_q_heads;
     a.Hkv = d->num_kv_heads;
@@ -300,7 +319,8 @@ int32_t pa_decode8(const pa_dims *dims, const pa_window *window, const void *q, 
 
 size_t pa_chunk8_workspace_bytes(const pa_dims *dims, int32_t num_tokens, int32_t max_query_len) {
     if (check_chunk8(dims, num_tokens, max_query_len) != PA_OK) return 0;
-    return chunk_layout8(dims, max_query_len).total;
+    // (a window may save the line; what is left then needs less)
+    return chunk_layout8(dims, max_query_len, nullptr).total;
 }
 
 int32_t pa_chunk8(const pa_dims *dims, const pa_window *window, const void *q, const pa_cache8 *cache,
@@ -317,7 +337,7 @@ int32_t pa_chunk8(const pa_dims *dims, const pa_window *window, const void *q, c
     if (!q || !block_tables || !context_lens || !query_start || !out) return PA_ERR_INVALID;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(query_start, 4))
         return PA_ERR_INVALID;
-    const Layout8 L = chunk_layout8(dims, max_query_len);
+    const Layout8 L = chunk_layout8(dims, max_query_len, window);
     if (!workspace || workspace_bytes < L.total || !aligned(workspace, 256)) return PA_ERR_INVALID;
     pa::Attend8Args a{};
     fill8(a, dims, window, q, cache, block_tables, context_lens, scale, out, out_dtype, L, workspace);

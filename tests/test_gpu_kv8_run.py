@@ -406,3 +406,45 @@ def test_pools_past_32_bits_of_codes(gpu):
         for src, dst in ((N - 1, N // 2), (ids[1], N - 400)):
             assert torch.equal(c.view(torch.uint8)[dst], c.view(torch.uint8)[src]) and torch.equal(s[dst], s[src])
     assert pa.pa_device_errors(clear=True) == 0
+
+
+@pytest.mark.parametrize("dtype,D,B,Hq,Hkv", [("bf16", 128, 16, 32, 8), ("f16", 64, 32, 4, 4), ("bf16", 64, 16, 8, 1), ("f16", 128, 32, 2, 1)])
+@pytest.mark.parametrize("lens,counts", [([5000], [160]), ([4100, 77, 2500], [70, 0, 200]), ([300, 64, 900], [150, 64, 129]),
+                                         ([9000, 150], [64, 64]), ([12, 40], [12, 0])])
+def test_chunks_whose_keys_are_shared_out(gpu, dtype, D, B, Hq, Hkv, lens, counts):
+    """Few rows over many keys (or a table that could hold many): pieces of items, whole ones and their joins."""
+    torch, pa = gpu
+    gen = generator(torch, sum(lens) + D)
+    tables, N = tables_for(torch, gen, lens, B, columns=400)
+    T, most = sum(counts), max(max(counts), 64)
+    q = (2 * torch.randn(T + 2, Hq, D, generator=gen, device="cuda")).to(dtype_of(torch, dtype))
+    cache = make_cache(torch, gen, N, Hkv, B, D, odd_scales=True)
+    dims = pa.make_dims(len(lens), Hq, Hkv, D, B, N, tables.shape[1], 0, dtype)
+    c8 = pa.make_cache8(*cache)
+    for window, sinks in ((0, 0), (3000, 100), (2000, 2500)):
+        ref, bound = attend_ref(torch, q[:T], cache, tables, lens, counts, 0.09, window, sinks)
+        for out_dtype in ("f32", dtype):
+            outs = []
+            for fill in (255, 0):
+                out = torch.full((T + 2, Hq, D), math.nan, dtype=dtype_of(torch, out_dtype), device="cuda")
+                ws = torch.full((pa.pa_chunk8_workspace_bytes(dims, T + 2, most),), fill, dtype=torch.uint8, device="cuda")
+                pa.pa_chunk8(dims, q, c8, tables, ints(torch, lens), ints(torch, starts_of(counts)), 0.09, out, most, ws,
+                             window=window, sinks=sinks)
+                torch.cuda.synchronize()
+                assert_within(out[:T], ref, bound, out_dtype)
+                assert bool(out[T:].isnan().all()), "rows behind the last sequence"
+                outs.append(out[:T])
+            assert torch.equal(outs[0], outs[1]), "the same call gives the same bits"
+    assert pa.pa_device_errors(clear=True) == 0
+    # blocks that are not there, and an order that is none
+    gone = [(0, 0)] + ([(0, 3), (0, 100)] if lens[0] > 101 * B else [])
+    for s, c in gone:
+        tables[s, c] = N + c
+    ref, bound = attend_ref(torch, q[:T], cache, tables, lens, counts, 0.09, bad=gone)
+    pa.pa_chunk8(dims, q, c8, tables, ints(torch, lens), ints(torch, starts_of(counts)), 0.09, out, most, ws)
+    assert pa.pa_device_errors(clear=True) == pa.PA_DEVERR_BAD_BLOCK
+    assert_within(out[:T], ref, bound, dtype)
+    out.fill_(math.nan)
+    pa.pa_chunk8(dims, q, c8, tables, ints(torch, lens), ints(torch, [1] + [0] * len(lens)), 0.09, out, most, ws)
+    assert pa.pa_device_errors(clear=True) == pa.PA_DEVERR_BAD_LEN
+    assert bool(out.isnan().all())
