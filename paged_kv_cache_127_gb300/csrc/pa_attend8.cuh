@@ -10,7 +10,7 @@
 // the weights that go into the second product are P_j = 2^(a_j - m) = p_j vs up to a factor, and the
 // normaliser is sum_j P_j / vs.  So a scale costs one multiply-add per block and row, the products run on the bare
 // codes, and P stays within a bound of its own whatever the blocks' scales are.  Both products take 16-bit floats: an
-// e4m3 code is exactly an f16 value (and a bf16 one), and P is rounded to f16 (2^-12).  On the tcgen05 path K goes in in the queries' type; on the
+// e4m3 code is exactly an f16 value (and a bf16 one), and P is rounded to f16 (2^-11).  On the tcgen05 path K goes in in the queries' type; on the
 // mma.sync path bf16 queries go in as f16, by a power of two per row that brings the row's largest to 2^10, which is
 // exact for every element that is within 2^-24 of it.
 #pragma once
