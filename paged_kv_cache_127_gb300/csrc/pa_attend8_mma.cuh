@@ -4,7 +4,8 @@
 // Work.  All steps of 32 keys of all (sequence, row block, group of HG KV heads) stand in one line, and each CTA takes an
 // equal stretch of it: no work list, no claims, and every CTA reads the same number of bytes.  A CTA that begins or
 // ends within a (sequence, row block, group) leaves a partial (m, l, O) in the workspace; the one that takes its first
-// step notes how many there are, and a second launch joins them.
+// step notes how many there are, and a second launch joins them.  Where no group has more than a few steps (short tables or
+// windows), a CTA takes whole groups instead, and there is nothing to join.
 //
 // A CTA is a producer warp and MB consumer warps per KV head of the group, each with 8 NQ of the row block's rows.  The
 // producer fills a ring of steps by TMA, one box per block (all HG heads) for K and for V; every 32 steps, lane l looks
@@ -79,6 +80,7 @@ __device__ __forceinline__ uint32_t piece8(int r, int ch) {
 // Steps of a CTA's stretch: an equal share, but at least four (128 keys) where that leaves 64 CTAs, so that a long sequence
 // has not too many parts to join; fewer where there are few steps at all and only latency counts.
 __device__ __forceinline__ long long share_of(const Attend8Args &a, long long total) {
+    if (a.whole) return (total + a.units - 1) / a.units;   // groups, not steps
     return max(min(4ll, (total + 63) / 64), (total + a.units - 1) / a.units);
 }
 
@@ -127,6 +129,8 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
         p.st = steps_of(a, p.q.len - p.q.n, p.q.n > 0 ? p.q.len : 0, kStep8);
     };
     auto blocks_of = [&](const Seq8 &q) { return (q.n * G + kRows - 1) / kRows; };
+    // (where a.whole, a group counts as one, and one without keys too: its rows are zeros)
+    auto steps_in = [&](const Place8 &p) { return (long long)blocks_of(p.q) * groups * (a.whole ? 1 : p.st.count); };
     long long total = 0, each;
     {
         const int per = (a.S + C::kThreads - 1) / C::kThreads;
@@ -137,7 +141,7 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
         for (int s = s0; s < s1; ++s) {
             place_seq(p, s, blockIdx.x == 0);
             ok = ok && order_ok(a, s);
-            own += (long long)blocks_of(p.q) * groups * p.st.count;
+            own += steps_in(p);
         }
         long long incl = own;
 #pragma unroll
@@ -164,7 +168,7 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
             u -= before;
             for (int s = s0; s < s1; ++s) {
                 place_seq(p, s, false);
-                const long long mine = (long long)blocks_of(p.q) * groups * p.st.count;
+                const long long mine = steps_in(p);
                 if (u < mine) {
                     begin_at = make_int4(s, 0, (int)(u & 0xffffffffll), (int)(u >> 32));
                     break;
@@ -176,14 +180,15 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
     }
     const int unit = blockIdx.x;
     if (each * unit >= total) return;
-    int left = (int)min(each, total - each * unit);   // steps still to take
+    int left = (int)min(each, total - each * unit);   // steps (groups) still to take
 
     Place8 p;
     place_seq(p, begin_at.x, false);
     {
         const long long u = (long long)(uint32_t)begin_at.z | (long long)begin_at.w << 32;
-        const long long head = u / p.st.count;
-        p.v = (int)(u % p.st.count);
+        const int of_head = a.whole ? 1 : p.st.count;
+        const long long head = u / of_head;
+        p.v = (int)(u % of_head);
         p.h = (int)(head % groups);
         p.rb = (int)(head / groups);
     }
@@ -194,7 +199,7 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
         if (++p.rb < blocks_of(p.q)) return;
         p.rb = 0;
         do place_seq(p, p.s + 1, false);
-        while ((p.q.n == 0 || p.st.count == 0) && p.s + 1 < a.S);
+        while (steps_in(p) == 0 && p.s + 1 < a.S);
     };
     auto first_key = [&](const Place8 &x) { return (x.v < x.st.ns ? x.v : x.v + x.st.gap) * kStep8; };
 
@@ -206,7 +211,7 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
         int z[2] = {-1, -1}, issued = 0;   // per lane: the blocks of the batch's step `lane` (first head's index, or -1)
         bool ok = true;
         while (ok && left > 0) {
-            const int n = min(left, p.st.count - p.v);
+            const int n = a.whole ? p.st.count : min(left, p.st.count - p.v);
             for (int i = 0; ok && i < n; ++i, ++issued, ++p.v) {
                 const int turn = i & 31;
                 if (turn == 0) {
@@ -256,7 +261,7 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
                 }
                 __syncwarp();
             }
-            left -= n;
+            left -= a.whole ? 1 : n;
             if (ok && left > 0) next_head(p);
         }
         if (!ok && lane == 0) set_error(a.err, PA_DEVERR_TIMEOUT);
@@ -277,7 +282,7 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
     int taken = 0;
     bool first_piece = true;
     while (left > 0) {
-        const int n = min(left, p.st.count - p.v);           // steps of this head
+        const int n = a.whole ? p.st.count : min(left, p.st.count - p.v);   // steps of this head
         const bool whole = n == p.st.count;
         const int kvh = p.h * HG + head;
         const int r0 = p.rb * kRows + 8 * NQ * member;       // first row of the warp: row r is token r / G, head r % G
@@ -533,7 +538,7 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
             ++taken;
             ++p.v;
         }
-        left -= n;
+        left -= a.whole ? 1 : n;
         if (timed_out) {
             if (lane == 0) set_error(a.err, PA_DEVERR_TIMEOUT);
             break;
@@ -702,7 +707,7 @@ cudaError_t launch_attend8_t(const Attend8Args &a, const CUtensorMap &tmk, const
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, attend8_mma_kernel<T, D, NQ, MB, HG>, a, tmk, tmv);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || a.whole) return e;
     // the join: a CTA per (sequence, KV head, row block)
     const long long blocks = ((long long)a.max_query_len * (a.Hq / a.Hkv) + C::kRows - 1) / C::kRows;
     if (blocks * a.S * a.Hkv > 0x7fffffffLL) return cudaErrorInvalidValue;

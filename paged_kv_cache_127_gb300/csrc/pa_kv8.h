@@ -55,6 +55,7 @@ struct Attend8Args {
     int S, T, Hq, Hkv, D, B, N, max_blocks, max_query_len;
     int window, sinks;              // window 0: none
     int out16;
+    int whole;                      // mma.sync path: CTAs take whole (sequence, row block, head group)s
     int units;                      // CTAs, which share the keys (tcgen05: 0: whole items, claimed)
     int tiles;                      // tcgen05 path: 128-row tiles of an item (1 or 2)
     float scale;

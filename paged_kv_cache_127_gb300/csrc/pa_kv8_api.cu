@@ -56,14 +56,22 @@ int32_t check_chunk8(const pa_dims *d, int32_t T, int32_t max_q) {
 }
 int32_t check_window(const pa_window *w) { return w && (w->window < 0 || w->sinks < 0) ? PA_ERR_INVALID : PA_OK; }
 
+constexpr int64_t kWholeKeys8 = 256;
+
 // Workspace, each part 256-byte aligned: a header, the notes of each (sequence, KV head, row block), and two parts
 // for each CTA that shares the keys (mma.sync path).
 struct Layout8 {
     pa::Rows8 rows;
-    int hg, units, tiles, groups;  // tiles 0: the mma.sync path
+    int hg, units, whole, tiles, groups;  // tiles 0: the mma.sync path
     size_t list, parts, total;
 };
-Layout8 layout8(const pa_dims *d, int32_t max_q) {
+// Keys that the rows of a sequence see, at most.
+int64_t reach8(const pa_dims *d, int32_t max_q, const pa_window *w) {
+    const int64_t keys = (int64_t)d->max_blocks_per_seq * d->block_size;
+    const int64_t seen = w && w->window ? (int64_t)w->window + w->sinks + max_q : keys;
+    return seen < keys ? seen : keys;
+}
+Layout8 layout8(const pa_dims *d, int32_t max_q, const pa_window *w) {
     Layout8 L{};
     const int G = d->num_q_heads / d->num_kv_heads;
     L.rows = pa::attend8_rows(max_q, G);
@@ -78,13 +86,22 @@ Layout8 layout8(const pa_dims *d, int32_t max_q) {
     L.units = (int)(units < cap ? (units > 0 ? units : 1) : cap);
     L.list = 256;
     L.parts = L.list + up256((size_t)most * sizeof(int2));
+    // Up to kWholeKeys8 keys a sequence: whole (sequence, row block, head group)s for each CTA, and no launch that joins parts.
+    // (3 sequences of up to 47 keys 8.4 us with equal stretches, 6.3 so; 32 of up to 250 16.2 and 11.7; 256 behind a window
+    // of 128 29.8 and 24.6; but 8 behind a window of 512 15.8 and 21.0)
+    L.whole = reach8(d, max_q, w) <= kWholeKeys8;
+    if (L.whole) {
+        L.units = (int)(most < cap ? most : cap);
+        L.total = L.parts;
+        return L;
+    }
     L.total = L.parts + up256((size_t)2 * L.units * L.hg * rows * (d->head_dim + 2) * sizeof(float));
     return L;
 }
-Layout8 decode_layout8(const pa_dims *d) { return layout8(d, 1); }
+Layout8 decode_layout8(const pa_dims *d, const pa_window *w) { return layout8(d, 1, w); }
 Layout8 chunk_layout8(const pa_dims *d, int32_t max_q, const pa_window *w) {
     const int G = d->num_q_heads / d->num_kv_heads;
-    if (!pa::chunk_uses_umma(max_q, G)) return layout8(d, max_q);
+    if (!pa::chunk_uses_umma(max_q, G)) return layout8(d, max_q, w);
     Layout8 L{};   // a header and the work list
     L.tiles = pa::chunk_umma_rows(max_q, G) / 128;
     L.list = 256;
@@ -95,9 +112,7 @@ Layout8 chunk_layout8(const pa_dims *d, int32_t max_q, const pa_window *w) {
     // That costs some 24 steps' time more (plan, parts, join), and saves a whole item's steps but for the SMs' share.
     // (8 KV heads of 128, by items and with the line: 512 tokens over 30000 keys 475 and 234 us, over 2000 keys 48 and 44;
     // 64 tokens over 2000 keys 40 and 34; a window of 1024 of 64 dimensions 26 and 32, 4 chunks of 512 82 and 87)
-    const int64_t keys = (int64_t)d->max_blocks_per_seq * d->block_size;
-    const int64_t reach = w && w->window ? (int64_t)w->window + w->sinks + max_q : keys;
-    const int64_t steps = ((reach < keys ? reach : keys) + 63) / 64;
+    const int64_t steps = (reach8(d, max_q, w) + 63) / 64;
     if (items < pa::kSms8 && steps * (pa::kSms8 - items) > 24 * pa::kSms8) {
         const int64_t units = (items * steps + pa::kLeastSteps8 - 1) / pa::kLeastSteps8;
         L.units = units < pa::kSms8 ? (int)units : pa::kSms8;
@@ -157,6 +172,7 @@ void fill8(pa::Attend8Args &a, const pa_dims *d, const pa_window *w, const void 
     a.notes = a.list;
     a.starts = a.list + L.units;
     a.units = L.units;
+    a.whole = L.whole;
     a.tiles = L.tiles;
     a.groups = L.groups;
     a.S = d->num_seqs;
@@ -293,7 +309,7 @@ int32_t pa_copy_blocks8(const pa_dims *dims, const pa_cache8 *cache, const int64
 
 size_t pa_decode8_workspace_bytes(const pa_dims *dims) {
     if (check_attend8(dims) != PA_OK || dims->num_seqs == 0) return 0;
-    return decode_layout8(dims).total;
+    return decode_layout8(dims, nullptr).total;   // (a window may save the joins; what is left then needs less)
 }
 
 int32_t pa_decode8(const pa_dims *dims, const pa_window *window, const void *q, const pa_cache8 *cache,
@@ -308,7 +324,7 @@ int32_t pa_decode8(const pa_dims *dims, const pa_window *window, const void *q, 
     if (rc != PA_OK) return rc;
     if (!q || !block_tables || !context_lens || !out) return PA_ERR_INVALID;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(block_tables, 4) || !aligned(context_lens, 4)) return PA_ERR_INVALID;
-    const Layout8 L = decode_layout8(dims);
+    const Layout8 L = decode_layout8(dims, window);
     if (!workspace || workspace_bytes < L.total || !aligned(workspace, 256)) return PA_ERR_INVALID;
     pa::Attend8Args a{};
     fill8(a, dims, window, q, cache, block_tables, context_lens, scale, out, out_dtype, L, workspace);
