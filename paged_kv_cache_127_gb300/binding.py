@@ -228,14 +228,25 @@ def _expect_beside(t, name, shape, dtype, device):
     _expect(t, name, shape, dtype, device)
 
 
+def _current_device() -> int:
+    # torch.cuda.current_device() without its check that CUDA is set up (the tensors of a call have seen to that)
+    global _CURRENT_DEVICE
+    if _CURRENT_DEVICE is None:
+        t = _torch()
+        _CURRENT_DEVICE = getattr(t._C, "_cuda_getDevice", None) or t.cuda.current_device
+    return _CURRENT_DEVICE()
+
+
+_CURRENT_DEVICE = None
+
+
 def _on(device):
     """Make `device` current for one library call: the library keeps its
     per-device state (error word, fixed scratch, tensor-map cache) for the
     current device, and every pointer and the stream of a call must belong to it."""
-    t = _torch()
-    if t.cuda.current_device() == device.index:
+    if _current_device() == device.index:
         return contextlib.nullcontext()
-    return t.cuda.device(device)
+    return _torch().cuda.device(device)
 
 
 def _stream_ptr(stream, device):
@@ -270,7 +281,7 @@ class Prepared:
 def _issue(fn, args, what, device, prepare, keep):
     if prepare:
         return Prepared(fn, args, what, device, keep)
-    if _torch().cuda.current_device() == device.index:
+    if _current_device() == device.index:
         st = fn(*args)
     else:
         with _on(device):
@@ -491,16 +502,22 @@ def _rotary_args(dims, rope, axes, q, k, v, positions, slot_mapping, q_out):
     d, kv = dims, _torch_dtype(dims.kv_dtype)
     dev = q.device
     T = int(slot_mapping.shape[0])
-    qs = _expect_tokens(q, "q", (T, d.num_q_heads, d.head_dim), kv, dev)
-    ks = _expect_tokens(k, "k", (T, d.num_kv_heads, d.head_dim), kv, dev)
-    vs = _expect_tokens(v, "v", (T, d.num_kv_heads, d.head_dim), kv, dev)
-    os_ = _expect_tokens(q_out, "q_out", (T, d.num_q_heads, d.head_dim), kv, dev)
-    _expect_beside(positions, "positions", (T,) if axes is None else (axes.num_axes, T), t.int32, dev)
-    _expect_beside(slot_mapping, "slot_mapping", (T,), t.int64, dev)
-    _expect_beside(rope.freqs, "rope.freqs", (rope.rotary_dim // 2,), t.float64, dev)
+    Hq, Hkv, D = d.num_q_heads, d.num_kv_heads, d.head_dim
+    qs = _expect_tokens(q, "q", (T, Hq, D), kv, dev)
+    ks = _expect_tokens(k, "k", (T, Hkv, D), kv, dev)
+    vs = _expect_tokens(v, "v", (T, Hkv, D), kv, dev)
+    os_ = _expect_tokens(q_out, "q_out", (T, Hq, D), kv, dev)
+    freqs, where, pairs = rope.freqs, (T,) if axes is None else (axes.num_axes, T), (rope.rotary_dim // 2,)
+    # one expression on the way that every good call takes
+    if not (positions.shape == where and positions.dtype == t.int32 and positions.device == dev and positions.is_contiguous() and
+            slot_mapping.dtype == t.int64 and slot_mapping.dim() == 1 and slot_mapping.device == dev and slot_mapping.is_contiguous() and
+            freqs.shape == pairs and freqs.dtype == t.float64 and freqs.device == dev and freqs.is_contiguous()):
+        _expect(positions, "positions", where, t.int32, dev)
+        _expect(slot_mapping, "slot_mapping", (T,), t.int64, dev)
+        _expect(freqs, "rope.freqs", pairs, t.float64, dev)
     rp, ax = pa_rope(rope.rotary_dim, int(rope.interleaved), rope.freqs.data_ptr(), rope.mscale), None
     if axes is not None:
-        _expect_beside(axes.pair_axis, "axes.pair_axis", (rope.rotary_dim // 2,), t.int32, dev)
+        _expect_beside(axes.pair_axis, "axes.pair_axis", pairs, t.int32, dev)
         ax = pa_axes(axes.num_axes, axes.pair_axis.data_ptr())
     args = (ctypes.byref(rp), None if ax is None else ctypes.byref(ax), q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
             positions.data_ptr(), slot_mapping.data_ptr(), T, q_out.data_ptr(), os_)
@@ -538,12 +555,19 @@ def make_cache8(k, v, k_scales, v_scales) -> Cache8:
 
 def _marshal_cache8(cache, d, dev):
     t = _torch()
-    shape, heads = (d.num_blocks, d.num_kv_heads, d.block_size, d.head_dim), (d.num_blocks, d.num_kv_heads)
-    _expect(cache.k, "cache.k", shape, t.float8_e4m3fn, dev)
-    _expect_beside(cache.v, "cache.v", shape, t.float8_e4m3fn, dev)
-    _expect_beside(cache.k_scales, "cache.k_scales", heads, t.float32, dev)
-    _expect_beside(cache.v_scales, "cache.v_scales", heads, t.float32, dev)
-    return pa_cache8(cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scales.data_ptr(), cache.v_scales.data_ptr())
+    k, v, ks, vs = cache.k, cache.v, cache.k_scales, cache.v_scales
+    heads = (d.num_blocks, d.num_kv_heads)
+    shape = (*heads, d.block_size, d.head_dim)
+    code, f32 = t.float8_e4m3fn, t.float32
+    # one expression on the way that every good call takes
+    if not (k.shape == shape and k.dtype == code and k.device == dev and k.is_cuda and k.is_contiguous() and
+            v.shape == shape and v.dtype == code and v.device == dev and v.is_contiguous() and
+            ks.shape == heads and ks.dtype == f32 and ks.device == dev and ks.is_contiguous() and
+            vs.shape == heads and vs.dtype == f32 and vs.device == dev and vs.is_contiguous()):
+        for x, name, size, dtype in ((k, "cache.k", shape, code), (v, "cache.v", shape, code),
+                                     (ks, "cache.k_scales", heads, f32), (vs, "cache.v_scales", heads, f32)):
+            _expect(x, name, size, dtype, dev)
+    return pa_cache8(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr())
 
 
 def _keep8(cache):
@@ -590,6 +614,28 @@ def pa_copy_blocks8(dims: pa_dims, cache: Cache8, src_dst_pairs, stream=None, pr
     return _issue(lib.pa_copy_blocks8, args, "pa_copy_blocks8", dev, prepare, (dims, c8, _keep8(cache), src_dst_pairs))
 
 
+def _expect_attend8(d, rows, kv, dev, q, block_tables, context_lens, out):
+    """The checks that decode and chunk attention over an 8-bit cache share."""
+    t = _torch()
+    i32, heads = t.int32, (rows, d.num_q_heads, d.head_dim)
+    tables, lens = (d.num_seqs, d.max_blocks_per_seq), (d.num_seqs,)
+    # one expression on the way that every good call takes
+    if not (q.shape == heads and q.dtype == kv and q.is_cuda and q.is_contiguous() and
+            block_tables.shape == tables and block_tables.dtype == i32 and block_tables.device == dev and block_tables.is_contiguous() and
+            context_lens.shape == lens and context_lens.dtype == i32 and context_lens.device == dev and context_lens.is_contiguous() and
+            out.shape == heads and out.device == dev and out.is_contiguous()):
+        for x, name, size, dtype in ((q, "q", heads, kv), (block_tables, "block_tables", tables, i32),
+                                     (context_lens, "context_lens", lens, i32), (out, "out", heads, out.dtype)):
+            _expect(x, name, size, dtype, dev)
+
+
+def _workspace8(workspace, need, what, dev):
+    """(pointer, bytes) of a caller's workspace; need() says how large it has to be (the library checks that it is)."""
+    if workspace is not None and workspace.is_cuda and workspace.device == dev and workspace.is_contiguous():
+        return workspace.data_ptr(), workspace.nbytes
+    return _workspace(workspace, need(), what, dev)
+
+
 def pa_decode8_workspace_bytes(dims: pa_dims) -> int:
     return int(lib.pa_decode8_workspace_bytes(ctypes.byref(dims)))
 
@@ -599,17 +645,13 @@ def pa_decode8(dims: pa_dims, q, cache: Cache8, block_tables, context_lens, scal
     """pa_decode over an 8-bit cache, with an out of float32 or the queries' dtype; under a
     window each row sees its last `window` keys and the first `sinks` ones.
     With prepare=True nothing runs: the checked call is returned as a Prepared."""
-    t = _torch()
     d, kv = dims, _torch_dtype(dims.kv_dtype)
     dev = q.device
-    _expect(q, "q", (d.num_seqs, d.num_q_heads, d.head_dim), kv, dev)
-    c8 = _marshal_cache8(cache, d, dev)
-    _expect_beside(block_tables, "block_tables", (d.num_seqs, d.max_blocks_per_seq), t.int32, dev)
-    _expect_beside(context_lens, "context_lens", (d.num_seqs,), t.int32, dev)
     code = _out_code(out, dims)
-    _expect_beside(out, "out", (d.num_seqs, d.num_q_heads, d.head_dim), out.dtype, dev)
+    _expect_attend8(d, d.num_seqs, kv, dev, q, block_tables, context_lens, out)
+    c8 = _marshal_cache8(cache, d, dev)
     win = pa_window(int(window), int(sinks))
-    ws_ptr, ws_bytes = _workspace(workspace, pa_decode8_workspace_bytes(dims), "pa_decode8", dev)
+    ws_ptr, ws_bytes = _workspace8(workspace, lambda: pa_decode8_workspace_bytes(dims), "pa_decode8", dev)
     args = (ctypes.byref(dims), ctypes.byref(win), q.data_ptr(), ctypes.byref(c8), block_tables.data_ptr(),
             context_lens.data_ptr(), float(scale), out.data_ptr(), code, ws_ptr, ws_bytes, _stream_ptr(stream, dev))
     return _issue(lib.pa_decode8, args, "pa_decode8", dev, prepare,
@@ -629,15 +671,12 @@ def pa_chunk8(dims: pa_dims, q, cache: Cache8, block_tables, context_lens, query
     d, kv = dims, _torch_dtype(dims.kv_dtype)
     dev = q.device
     T = int(q.shape[0])
-    _expect(q, "q", (T, d.num_q_heads, d.head_dim), kv, dev)
-    c8 = _marshal_cache8(cache, d, dev)
-    _expect_beside(block_tables, "block_tables", (d.num_seqs, d.max_blocks_per_seq), t.int32, dev)
-    _expect_beside(context_lens, "context_lens", (d.num_seqs,), t.int32, dev)
-    _expect_beside(query_start, "query_start", (d.num_seqs + 1,), t.int32, dev)
     code = _out_code(out, dims)
-    _expect_beside(out, "out", (T, d.num_q_heads, d.head_dim), out.dtype, dev)
+    _expect_attend8(d, T, kv, dev, q, block_tables, context_lens, out)
+    _expect_beside(query_start, "query_start", (d.num_seqs + 1,), t.int32, dev)
+    c8 = _marshal_cache8(cache, d, dev)
     win = pa_window(int(window), int(sinks))
-    ws_ptr, ws_bytes = _workspace(workspace, pa_chunk8_workspace_bytes(dims, T, max_query_len), "pa_chunk8", dev)
+    ws_ptr, ws_bytes = _workspace8(workspace, lambda: pa_chunk8_workspace_bytes(dims, T, max_query_len), "pa_chunk8", dev)
     args = (ctypes.byref(dims), ctypes.byref(win), q.data_ptr(), ctypes.byref(c8), block_tables.data_ptr(),
             context_lens.data_ptr(), query_start.data_ptr(), T, int(max_query_len), float(scale), out.data_ptr(), code,
             ws_ptr, ws_bytes, _stream_ptr(stream, dev))

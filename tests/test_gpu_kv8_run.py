@@ -448,3 +448,61 @@ def test_chunks_whose_keys_are_shared_out(gpu, dtype, D, B, Hq, Hkv, lens, count
     pa.pa_chunk8(dims, q, c8, tables, ints(torch, lens), ints(torch, [1] + [0] * len(lens)), 0.09, out, most, ws)
     assert pa.pa_device_errors(clear=True) == pa.PA_DEVERR_BAD_LEN
     assert bool(out.isnan().all())
+
+
+@pytest.mark.parametrize("nq", [1, 3, 80])
+def test_binding_refuses_what_the_calls_cannot_take(gpu, nq):
+    torch, pa = gpu
+    c = Bench(torch, pa, 7, nq)
+    good = {"q": c.q, "tables": c.tables, "dl": c.dl, "qs": c.qs, "c8": c.c8, "ws": c.ws, "out": c.out}
+    k, v, ks, vs = c.cache
+    two = lambda x: torch.cat([x, x], -1)[..., : x.shape[-1]]      # the right shape, other strides
+    bad = [("q", c.q[:-1]), ("q", c.q.float()), ("q", c.q.cpu()), ("q", two(c.q)), ("tables", c.tables[:, :-1]),
+           ("tables", c.tables.long()), ("tables", c.tables.cpu()), ("tables", two(c.tables)), ("dl", c.dl[:-1]), ("dl", c.dl.long()),
+           ("dl", c.dl.cpu()), ("out", c.out[:-1]), ("out", c.out.double()), ("out", two(c.out)), ("out", c.out.cpu()),
+           ("ws", None), ("ws", c.ws.cpu()), ("ws", c.ws[::2]), ("c8", pa.make_cache8(k[:-1], v, ks, vs)),
+           ("c8", pa.make_cache8(k.view(torch.uint8), v, ks, vs)), ("c8", pa.make_cache8(k, v.cpu(), ks, vs)),
+           ("c8", pa.make_cache8(k, v, ks.double(), vs)), ("c8", pa.make_cache8(k, v, ks, vs[:, :1])), ("c8", pa.make_cache8(k, v, ks, two(vs)))]
+    if nq > 1:
+        bad += [("qs", c.qs[:-1]), ("qs", c.qs.long()), ("qs", c.qs.cpu())]
+    for name, x in bad:
+        for key, value in good.items():
+            setattr(c, key, value)
+        setattr(c, name, x)
+        if name == "ws" and x is None:
+            with pytest.raises(ValueError):
+                if nq == 1:
+                    pa.pa_decode8(c.dims, c.q, c.c8, c.tables, c.dl, c.scale, c.out)
+                else:
+                    pa.pa_chunk8(c.dims, c.q, c.c8, c.tables, c.dl, c.qs, c.scale, c.out, nq)
+        else:
+            with pytest.raises(ValueError):
+                c.call()
+    for key, value in good.items():
+        setattr(c, key, value)
+    for ws in (c.ws[:256], c.ws[16:]):
+        with pytest.raises(pa.PaError):
+            c.call(ws=ws)
+    c.call()
+    c.check(c.out)
+    x = torch.zeros(5, 2, 64, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(5, 8, 64, dtype=torch.bfloat16, device="cuda")
+    slots, pos = torch.arange(5, device="cuda"), torch.zeros(5, dtype=torch.int32, device="cuda")
+    freqs = torch.zeros(32, dtype=torch.float64, device="cuda")
+    rope, axes = pa.make_rope(64, freqs), pa.make_axes(2, torch.zeros(32, dtype=torch.int32, device="cuda"))
+    for args in ((rope, None, q, x, x, pos[:-1], slots, q), (rope, None, q, x, x, pos.long(), slots, q), (rope, None, q, x, x, pos, slots.int(), q),
+                 (rope, None, q, x, x, pos, slots[:, None], q), (rope, None, q, x, x, pos.cpu(), slots, q), (rope, axes, q, x, x, pos, slots, q),
+                 (rope, None, q, x, q, pos, slots, q), (rope, None, q, x[:4], x, pos, slots, q), (rope, None, x, x, x, pos, slots, q),
+                 (rope, None, q, x, x, pos, slots, q.float()), (pa.make_rope(64, freqs[:-1]), None, q, x, x, pos, slots, q),
+                 (rope, pa.make_axes(1, axes.pair_axis[:-1]), q, x, x, pos[None], slots, q)):
+        with pytest.raises(ValueError):
+            pa.pa_rope_write_kv8(c.dims, *args, c.c8)
+        with pytest.raises(ValueError):
+            pa.pa_rope_axes_write_kv(c.dims, *args, torch.zeros(k.shape, dtype=torch.bfloat16, device="cuda"),
+                                     torch.zeros(k.shape, dtype=torch.bfloat16, device="cuda"))
+    for args in ((x, x, slots.int()), (x[:4], x, slots), (x, q, slots), (x, x.float(), slots)):
+        with pytest.raises(ValueError):
+            pa.pa_write_kv8(c.dims, *args, c.c8)
+    for pairs in (slots, torch.zeros(2, 2, dtype=torch.int32, device="cuda"), torch.zeros(2, 3, dtype=torch.int64, device="cuda")):
+        with pytest.raises(ValueError):
+            pa.pa_copy_blocks8(c.dims, c.c8, pairs)
