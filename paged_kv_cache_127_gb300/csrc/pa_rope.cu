@@ -20,7 +20,8 @@
 //
 // Bound: HBM for a prompt (each q, k, v element read and written once), latency for a step.
 // Measured: 8192 tokens of 32 + 32 heads (D 128, f16, 64 elements rotated as neighbours) 64 us (floor 59), of
-// 32 + 8 heads (bf16, whole heads in halves) 51; the kernel of a step of 256 tokens, 64 + 8 heads, 5.6 us, of one token 2.9 us.
+// 32 + 8 heads (bf16, whole heads in halves) 37 (floor 30), with three axes 38; the kernel of a step of 256 tokens, 64 + 8
+// heads, 4.8 us, of one token 2.8 us.
 #include <cmath>
 
 #include "pa_device.cuh"
@@ -115,17 +116,24 @@ struct Unit {
 constexpr int kTokens = 2;
 
 template <typename T, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads) rope_units_kernel(const RopeArgs a, int tokens, int upq) {
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_units_kernel(const RopeArgs a, int tokens, int upq) {
     constexpr int V = Unit<T>::kN;
     constexpr int kAngles = kInterleaved ? V / 2 : V;  // (cos, sin) pairs of a column
     constexpr int kU = kInterleaved ? 6 : 4;
-    extern __shared__ float2 cs[];  // [tokens][kAngles][columns that rotate]: lanes next to each other read neighbours
+    extern __shared__ float2 cs[];  // [tokens][R / 2]
     __shared__ int64_t slots[kTokens];
     const int half = a.R / 2, tid = threadIdx.x;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int t0 = blockIdx.x * tokens, nt = min(tokens, a.T - t0);
+    if (tid < nt) slots[tid] = token_slot(a, t0 + tid, blockIdx.y == 0);
+    for (int e = tid; e < nt * half; e += kRopeThreads) {
+        const int t = e / half, p = e - t * half;
+        cs[e] = turn_at(turn_fraction(a.freqs[p]), pair_position(a, t0 + t, p), a.mscale);
+    }
+    __syncthreads();
     const int i = tid % upq, per = kRopeThreads / upq, h0 = tid / upq;
+    if (h0 >= per) return;
     const int turning = kInterleaved ? (a.R + V - 1) / V : half / V;  // columns that rotate
     const bool turns = i < turning;
     const int live = kInterleaved ? min(kAngles, half - i * kAngles) : kAngles;  // pairs of the unit that do
@@ -136,30 +144,110 @@ __global__ void __launch_bounds__(kRopeThreads) rope_units_kernel(const RopeArgs
     const bool two = !kInterleaved && (turns || first + delta < a.D);
     const int k_head = a.Hq, v_head = a.Hq + a.Hkv, heads = a.Hq + 2 * a.Hkv;
     const int step = per * (int)gridDim.y, row = a.B * a.D;
-    // The tokens' heads stand in one line, m = t * heads + head; a thread takes every step-th of them, kU a round.  The first
-    // round's loads need no slot and no angle, so they are under way before those are there.
-    const int all = nt * heads;
+    for (int t = 0; t < nt; ++t) {
+        const int64_t slot = slots[t];
+        if (slot < 0) continue;
+        const int64_t blk = slot / a.B;
+        const size_t place = ((size_t)blk * a.Hkv * a.B + (size_t)(slot - blk * a.B)) * a.D + first;  // head 0's row
+        // each kind's head 0 stands at its own number, so that head h is `h * D` (or rows of the cache) on
+        const T *q = static_cast<const T *>(a.q) + (size_t)(t0 + t) * a.q_stride + first;
+        const T *k = static_cast<const T *>(a.k) + (size_t)(t0 + t) * a.k_stride + first - (ptrdiff_t)k_head * a.D;
+        const T *v = static_cast<const T *>(a.v) + (size_t)(t0 + t) * a.v_stride + first - (ptrdiff_t)v_head * a.D;
+        T *qo = static_cast<T *>(a.q_out) + (size_t)(t0 + t) * a.q_out_stride + first;
+        T *kc = static_cast<T *>(a.k_cache) + place - (ptrdiff_t)k_head * row;
+        T *vc = static_cast<T *>(a.v_cache) + place - (ptrdiff_t)v_head * row;
+        const float2 *w = cs + t * half + i * kAngles;
+        for (int h = blockIdx.y * per + h0; h < heads; h += kU * step) {
+            uint4 x[kU], y[kU];
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                const int n = h + u * step;
+                if (n < heads) {
+                    const T *from = (n < k_head ? q : n < v_head ? k : v) + (ptrdiff_t)n * a.D;
+                    x[u] = *reinterpret_cast<const uint4 *>(from);
+                    if (two) y[u] = *reinterpret_cast<const uint4 *>(from + delta);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                const int n = h + u * step;
+                if (n < heads) {
+                    if (turns && n < v_head) {
+                        float f[V], g[V];
+                        Elem<T>::unpack(x[u], f);
+                        if (!kInterleaved) Elem<T>::unpack(y[u], g);
+#pragma unroll
+                        for (int e = 0; e < kAngles; ++e) {
+                            float &p = kInterleaved ? f[2 * e] : f[e], &r = kInterleaved ? f[2 * e + 1] : g[e];
+                            if (kInterleaved && e >= live) continue;
+                            const float2 c = w[e];
+                            const float pn = p * c.x - r * c.y;
+                            r = r * c.x + p * c.y;
+                            p = pn;
+                        }
+                        const uint4 turned = Unit<T>::pack(f);
+                        if constexpr (kInterleaved) {  // the words of pairs behind R stay as they are
+                            constexpr int kWords = 4 / kAngles;  // of a pair
+                            x[u].x = turned.x;
+                            if (1 / kWords < live) x[u].y = turned.y;
+                            if (2 / kWords < live) x[u].z = turned.z;
+                            if (3 / kWords < live) x[u].w = turned.w;
+                        } else {
+                            x[u] = turned;
+                        }
+                        if (!kInterleaved) y[u] = Unit<T>::pack(g);
+                    }
+                    T *to = n < k_head ? qo + (ptrdiff_t)n * a.D : (n < v_head ? kc : vc) + (ptrdiff_t)n * row;
+                    *reinterpret_cast<uint4 *>(to) = x[u];
+                    if (two) *reinterpret_cast<uint4 *>(to + delta) = y[u];
+                }
+            }
+        }
+    }
+}
+
+// Whole heads of 16-bit elements in halves: every column is two units that turn together (upq of them a head).  The tokens' heads stand in one line,
+// m = t * heads + head; a thread takes every step-th of them, kU a round.  The first round's loads need no slot and no
+// angle, so they are under way before those are there; (cos, sin) lie so that lanes next to each other read neighbours.
+// (8192 tokens of 32 + 8 heads, bf16: 36.6 us, 50.3 in rope_units_kernel; of 32 + 32 heads of 64, f16, 32.5 and 41.5.
+// Elsewhere this form loses: 32 + 32 heads, 64 of 128 elements turned, 69.6 and 63.2, as neighbouring pairs 85.5 and 63.6;
+// 4096 tokens of 32 + 32 whole fp32 heads 70.0 and 65.4.)
+template <typename T>
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_whole_kernel(const RopeArgs a, int tokens, int upq) {
+    constexpr int V = Unit<T>::kN, kU = 4;
+    extern __shared__ float2 cs[];  // [tokens][V][upq]
+    __shared__ int64_t places[kTokens];  // of each token's row of KV head 0, or -1 for padding
+    const int half = a.R / 2, tid = threadIdx.x;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int t0 = blockIdx.x * tokens, nt = min(tokens, a.T - t0);
+    const int i = tid % upq, per = kRopeThreads / upq, h0 = tid / upq, first = i * V;
+    const int k_head = a.Hq, v_head = a.Hq + a.Hkv, heads = a.Hq + 2 * a.Hkv;
+    const int step = per * (int)gridDim.y, row = a.B * a.D, all = nt * heads;
     uint4 x[kU], y[kU];
     auto load = [&](int m0) {
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
             const int m = m0 + u * step;
             if (m < all) {
-                const int t = tokens > 1 && m >= heads ? 1 : 0, n = m - t * heads;
+                const int t = m >= heads ? 1 : 0, n = m - t * heads;
                 const T *from = n < k_head   ? static_cast<const T *>(a.q) + (size_t)(t0 + t) * a.q_stride + (ptrdiff_t)n * a.D
                                 : n < v_head ? static_cast<const T *>(a.k) + (size_t)(t0 + t) * a.k_stride + (ptrdiff_t)(n - k_head) * a.D
                                              : static_cast<const T *>(a.v) + (size_t)(t0 + t) * a.v_stride + (ptrdiff_t)(n - v_head) * a.D;
                 x[u] = *reinterpret_cast<const uint4 *>(from + first);
-                if (two) y[u] = *reinterpret_cast<const uint4 *>(from + first + delta);
+                y[u] = *reinterpret_cast<const uint4 *>(from + first + half);
             }
         }
     };
     const int m0 = blockIdx.y * per + h0;
     if (h0 < per) load(m0);
-    if (tid < nt) slots[tid] = token_slot(a, t0 + tid, blockIdx.y == 0);
+    if (tid < nt) {
+        const int64_t slot = token_slot(a, t0 + tid, blockIdx.y == 0), blk = slot / a.B;
+        places[tid] = slot < 0 ? -1 : (blk * a.Hkv * a.B + (slot - blk * a.B)) * a.D;
+    }
     for (int e = tid; e < nt * half; e += kRopeThreads) {
         const int t = e / half, p = e - t * half;
-        cs[(t * kAngles + p % kAngles) * turning + p / kAngles] = turn_at(turn_fraction(a.freqs[p]), pair_position(a, t0 + t, p), a.mscale);
+        cs[(t * V + p % V) * upq + p / V] = turn_at(turn_fraction(a.freqs[p]), pair_position(a, t0 + t, p), a.mscale);
     }
     __syncthreads();
     if (h0 >= per) return;
@@ -169,45 +257,28 @@ __global__ void __launch_bounds__(kRopeThreads) rope_units_kernel(const RopeArgs
         for (int u = 0; u < kU; ++u) {
             const int m = m1 + u * step;
             if (m >= all) break;
-            const int t = tokens > 1 && m >= heads ? 1 : 0, n = m - t * heads;
-            const int64_t slot = slots[t];
-            if (slot < 0) continue;
-            if (turns && n < v_head) {
-                const float2 *w = cs + t * kAngles * turning + i;
+            const int t = m >= heads ? 1 : 0, n = m - t * heads;
+            const int64_t place = places[t];
+            if (place < 0) continue;
+            if (n < v_head) {
+                const float2 *w = cs + t * V * upq + i;
                 float f[V], g[V];
                 Elem<T>::unpack(x[u], f);
-                if (!kInterleaved) Elem<T>::unpack(y[u], g);
+                Elem<T>::unpack(y[u], g);
 #pragma unroll
-                for (int e = 0; e < kAngles; ++e) {
-                    float &p = kInterleaved ? f[2 * e] : f[e], &r = kInterleaved ? f[2 * e + 1] : g[e];
-                    if (kInterleaved && e >= live) continue;
-                    const float2 c = w[e * turning];
-                    const float pn = p * c.x - r * c.y;
-                    r = r * c.x + p * c.y;
-                    p = pn;
+                for (int e = 0; e < V; ++e) {
+                    const float2 c = w[e * upq];
+                    const float p = f[e] * c.x - g[e] * c.y;
+                    g[e] = g[e] * c.x + f[e] * c.y;
+                    f[e] = p;
                 }
-                const uint4 turned = Unit<T>::pack(f);
-                if constexpr (kInterleaved) {  // the words of pairs behind R stay as they are
-                    constexpr int kWords = 4 / kAngles;  // of a pair
-                    x[u].x = turned.x;
-                    if (1 / kWords < live) x[u].y = turned.y;
-                    if (2 / kWords < live) x[u].z = turned.z;
-                    if (3 / kWords < live) x[u].w = turned.w;
-                } else {
-                    x[u] = turned;
-                }
-                if (!kInterleaved) y[u] = Unit<T>::pack(g);
+                x[u] = Unit<T>::pack(f);
+                y[u] = Unit<T>::pack(g);
             }
-            T *to;
-            if (n < k_head) {
-                to = static_cast<T *>(a.q_out) + (size_t)(t0 + t) * a.q_out_stride + (ptrdiff_t)n * a.D;
-            } else {
-                const int64_t blk = slot / a.B;
-                to = static_cast<T *>(n < v_head ? a.k_cache : a.v_cache) +
-                     ((size_t)blk * a.Hkv * a.B + (size_t)(slot - blk * a.B)) * a.D + (ptrdiff_t)(n < v_head ? n - k_head : n - v_head) * row;
-            }
+            T *to = n < k_head ? static_cast<T *>(a.q_out) + (size_t)(t0 + t) * a.q_out_stride + (ptrdiff_t)n * a.D
+                               : static_cast<T *>(n < v_head ? a.k_cache : a.v_cache) + place + (ptrdiff_t)(n < v_head ? n - k_head : n - v_head) * row;
             *reinterpret_cast<uint4 *>(to + first) = x[u];
-            if (two) *reinterpret_cast<uint4 *>(to + first + delta) = y[u];
+            *reinterpret_cast<uint4 *>(to + first + half) = y[u];
         }
     }
 }
@@ -285,17 +356,16 @@ cudaError_t launch_rope(void (*kernel)(Args...), dim3 grid, size_t smem, cudaStr
 
 // The unit kernels want the whole L1 for their loads in flight, also right after a kernel
 // that asked for a large part of it as shared memory.
-template <typename T, bool kInterleaved>
+template <typename T, void (*kKernel)(RopeArgs, int, int)>
 cudaError_t launch_units(const RopeArgs &a, int tokens, int upq, dim3 grid, size_t smem, cudaStream_t st) {
     static std::atomic<int> configured[kMaxLaunchDevices];
     int one = 0;
     const cudaError_t e = per_device_value(configured, &one, [](int, int *v) {
         *v = 1;
-        return cudaFuncSetAttribute(rope_units_kernel<T, kInterleaved>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                    cudaSharedmemCarveoutMaxL1);
+        return cudaFuncSetAttribute(kKernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxL1);
     });
     if (e != cudaSuccess) return e;
-    return launch_rope(rope_units_kernel<T, kInterleaved>, grid, smem, st, a, tokens, upq);
+    return launch_rope(kKernel, grid, smem, st, a, tokens, upq);
 }
 
 template <typename T>
@@ -320,9 +390,11 @@ cudaError_t launch_rope_t(const RopeArgs &a, cudaStream_t st) {
     int parts = (4 * 152 + groups - 1) / groups;
     parts = parts < passes ? parts : passes;
     const dim3 grid((unsigned)groups, (unsigned)(parts > 0 ? parts : 1));
-    const size_t smem = (size_t)tokens * ((a.R + V - 1) / V * V / 2) * sizeof(float2);  // whole units of pairs
-    return a.interleaved ? launch_units<T, true>(a, tokens, upq, grid, smem, st)
-                         : launch_units<T, false>(a, tokens, upq, grid, smem, st);
+    const size_t smem = (size_t)tokens * (a.R / 2) * sizeof(float2);
+    if (a.interleaved) return launch_units<T, rope_units_kernel<T, true>>(a, tokens, upq, grid, smem, st);
+    if constexpr (sizeof(T) == 2)
+        if (a.R == a.D) return launch_units<T, rope_whole_kernel<T>>(a, tokens, upq, grid, smem, st);
+    return launch_units<T, rope_units_kernel<T, false>>(a, tokens, upq, grid, smem, st);
 }
 
 }  // namespace
