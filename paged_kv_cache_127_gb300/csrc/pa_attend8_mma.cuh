@@ -220,24 +220,44 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
                     const int key = first_key(x);
                     const bool mine = i + lane < n;
                     const uint32_t at = notes + (uint32_t)(C::kNotes * ((issued + lane) & 63));
+                    int id[2];
+                    bool want[2];
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
                         const int k = key + b * a.B;
-                        z[b] = -1;
-                        if (b < nb && mine && k < p.q.len) {
-                            const int pb = a.block_tables[(size_t)p.s * a.max_blocks + (k >> lb)];
-                            if (pb >= 0 && pb < a.N) z[b] = pb * a.Hkv + p.h * HG;
-                            else set_error(a.err, PA_DEVERR_BAD_BLOCK);
-                        }
-                        if (!mine) continue;
-#pragma unroll 1
-                        for (int h = 0; h < HG; ++h) {
-                            // a block that is not there has no scale; the second half of a block of 32 has the first's
-                            const int from = nb == 1 ? z[0] : z[b];
-                            const float ks = from >= 0 ? a.k_scales[from + h] : 0.f, vs = from >= 0 ? a.v_scales[from + h] : -1.f;
-                            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %3};" ::"r"(at + 32 * h + 16 * b), "f"(ks),
-                                         "f"(vs > 0.f ? lg2(vs) : 0.f), "f"(1.f / vs)
-                                         : "memory");
+                        want[b] = b < nb && mine && k < p.q.len;
+                        id[b] = want[b] ? a.block_tables[(size_t)p.s * a.max_blocks + (k >> lb)] : 0;
+                    }
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const bool there = want[b] && id[b] >= 0 && id[b] < a.N;
+                        if (want[b] && !there) set_error(a.err, PA_DEVERR_BAD_BLOCK);
+                        z[b] = there ? id[b] * a.Hkv + p.h * HG : -1;
+                    }
+                    // a block that is not there has no scale; the second half of a block of 32 has the first's
+                    const int from[2] = {z[0], nb == 1 ? z[0] : z[1]};
+                    // as many scales on their way together as there are registers for (one head at a time: windows 56.9 us, so 55.7)
+                    constexpr int kB = C::kSplit ? 1 : 2;
+                    if (mine) {
+#pragma unroll
+                        for (int b0 = 0; b0 < 2; b0 += kB) {
+                            float ks[kB][HG], vs[kB][HG];
+#pragma unroll
+                            for (int b = 0; b < kB; ++b)
+#pragma unroll
+                                for (int h = 0; h < HG; ++h) {
+                                    ks[b][h] = a.k_scales[max(from[b0 + b], 0) + h];
+                                    vs[b][h] = a.v_scales[max(from[b0 + b], 0) + h];
+                                }
+#pragma unroll
+                            for (int b = 0; b < kB; ++b)
+#pragma unroll
+                                for (int h = 0; h < HG; ++h) {
+                                    const float k1 = from[b0 + b] >= 0 ? ks[b][h] : 0.f, v1 = from[b0 + b] >= 0 ? vs[b][h] : -1.f;
+                                    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %3};" ::"r"(at + 32 * h + 16 * (b0 + b)), "f"(k1),
+                                                 "f"(v1 > 0.f ? lg2(v1) : 0.f), "f"(1.f / v1)
+                                                 : "memory");
+                                }
                         }
                     }
                     __syncwarp();
