@@ -323,9 +323,9 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
             if (j == count && !next_item()) return false;
             if ((j & 31) == 0) {
                 const int v = (kLine ? it.v0 : 0) + j + lane, b0 = (v < it.ns ? v : v + it.gap) * C::kN + 16 * box;
-                int id = -2;
-                if (j + lane < it.count && b0 < it.hi && (b0 + 15 >= it.lo || b0 < a.sinks)) id = a.block_tables[(size_t)it.s * a.max_blocks + (b0 >> lb)];
-                const bool good = (unsigned)id < (unsigned)a.N;
+                const bool want = j + lane < it.count && b0 < it.hi && (b0 + 15 >= it.lo || b0 < a.sinks);
+                const int id = want ? a.block_tables[(size_t)it.s * a.max_blocks + (b0 >> lb)] : 0;
+                const bool good = want && (unsigned)id < (unsigned)a.N;
                 const size_t bh = (size_t)id * a.Hkv + it.kvh;
                 src = good ? cache + (bh * a.B + (b0 & (a.B - 1))) * D : nullptr;
                 if constexpr (kV) {
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
                     if (good) {
                         ks = a.k_scales[bh];
                         vs = a.v_scales[bh];
-                    } else if (id != -2) {
+                    } else if (want) {
                         set_error(a.err, PA_DEVERR_BAD_BLOCK);
                     }
                     box_note = make_float4(ks * a.scale * kLog2e8, lg2(vs), 1.f / vs, good ? 1.f : 0.f);

@@ -506,3 +506,22 @@ def test_binding_refuses_what_the_calls_cannot_take(gpu, nq):
     for pairs in (slots, torch.zeros(2, 2, dtype=torch.int32, device="cuda"), torch.zeros(2, 3, dtype=torch.int64, device="cuda")):
         with pytest.raises(ValueError):
             pa.pa_copy_blocks8(c.dims, c.c8, pairs)
+
+
+@pytest.mark.parametrize("nq", [1, 6, 90])
+@pytest.mark.parametrize("B", [16, 32])
+def test_every_id_that_is_no_block_is_flagged(gpu, nq, B):
+    torch, pa = gpu
+    c = Bench(torch, pa, 31 + nq, nq, B=B, S=2)
+    for bad in (-1, -2, -3, len(c.cache[0]), 2 ** 31 - 1, -2 ** 31):
+        for place in (0, (c.lens[1] - 1) // B):
+            was = int(c.tables[1, place])
+            c.tables[1, place] = bad
+            c.call()
+            assert pa.pa_device_errors(clear=True) == pa.PA_DEVERR_BAD_BLOCK, (bad, place)
+            ref, bound = attend_ref(torch, c.q, c.cache, c.tables, c.lens, c.counts, c.scale, bad=[(1, place)])
+            assert_within(c.out, ref, bound, "f32")
+            c.tables[1, place] = was
+    c.call()
+    assert pa.pa_device_errors(clear=True) == 0
+    c.check(c.out)
