@@ -63,7 +63,8 @@ struct Attend8Args {
 // mma.sync path, and the join of its parts: `mb` warps with 8 * nq rows each for a row block of a KV head, `hg` KV heads
 // a CTA, which has a producer warp besides; up to eight consumers and ten warps an SM.
 constexpr int kSms8 = 152;
-constexpr int kLeastSteps8 = 4;   // tcgen05 line: steps of a CTA at least, where a call has that many
+// tcgen05 line: steps of a CTA at least, where a call has that many (64 tokens over 2000 keys 42 us with 2, 34 with 4, 32 with 8)
+constexpr int kLeastSteps8 = 8;
 constexpr int attend8_ctas(int nq, int mb, int hg) {   // per SM
     return nq < 3 ? 10 / (hg * mb + 1) : hg * mb == 4 ? 2 : 8 / (hg * mb + 1);
 }

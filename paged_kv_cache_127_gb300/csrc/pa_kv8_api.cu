@@ -111,7 +111,7 @@ Layout8 chunk_layout8(const pa_dims *d, int32_t max_q, const pa_window *w) {
     // Fewer items than SMs, with many steps each: all steps in a line that the CTAs share equally (list: notes and starts).
     // That costs some 24 steps' time more (plan, parts, join), and saves a whole item's steps but for the SMs' share.
     // (8 KV heads of 128, by items and with the line: 512 tokens over 30000 keys 475 and 234 us, over 2000 keys 48 and 44;
-    // 64 tokens over 2000 keys 40 and 34; a window of 1024 of 64 dimensions 26 and 32, 4 chunks of 512 82 and 87)
+    // 64 tokens over 2000 keys 40 and 32; a window of 1024 of 64 dimensions 26 and 32, 4 chunks of 512 82 and 87)
     const int64_t steps = (reach8(d, max_q, w) + 63) / 64;
     if (items < pa::kSms8 && steps * (pa::kSms8 - items) > 24 * pa::kSms8) {
         const int64_t units = (items * steps + pa::kLeastSteps8 - 1) / pa::kLeastSteps8;
