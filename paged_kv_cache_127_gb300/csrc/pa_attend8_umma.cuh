@@ -382,11 +382,12 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
         if constexpr (C::kRegSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n" ::: "memory");
         if (warp < 8) convert(std::integral_constant<bool, false>());
         else convert(std::integral_constant<bool, true>());
-    } else if (warp < 2) {
-        // ------------------------------------------------------------ S = Q K^T issuer of tile u
-        const int u = warp;
+    } else if (warp < 4) {
+        // one instruction for all four warps of the warpgroup, as setmaxnreg asks
         if constexpr (C::kRegSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n" ::: "memory");
-        if (u < MT) {
+        const int u = warp & 1;
+        if (u < MT && warp < 2) {
+            // -------------------------------------------------------- S = Q K^T issuer of tile u
             constexpr uint32_t idesc_s = tc::f16_idesc(kBf16, false, C::kM, C::kN);
             const uint64_t kdesc0 = tc::sw128_desc(kvb, 16u, 1024u);
             const uint64_t qpol = policy_evict_first();
@@ -448,12 +449,8 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
             if (lane == 0) tc::mma_commit(drain_s(u));
             __syncwarp();
             mbar_wait_bounded(drain_s(u), 0u, kWaitLimit);
-        }
-    } else if (warp < 4) {
-        // ------------------------------------------------------------ O += P V issuer of tile u
-        const int u = warp - 2;
-        if constexpr (C::kRegSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n" ::: "memory");
-        if (u < MT) {
+        } else if (u < MT) {
+            // -------------------------------------------------------- O += P V issuer of tile u
             constexpr uint32_t idesc_o = tc::f16_idesc(false, true, C::kM, D);
             const uint64_t vdesc0 = tc::sw128_desc(kvb + (uint32_t)C::kTile, (uint32_t)C::kHalf, 1024u);
             const uint32_t od = tbase + o_col(u);
