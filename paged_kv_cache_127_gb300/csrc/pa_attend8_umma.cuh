@@ -201,6 +201,7 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
     auto take = [&](int u, int k, Item8 &out) {   // tile u's k-th item; false on a timeout
         const bool got = wait(item_ready(u, k & 1), (uint32_t)(k >> 1) & 1u);
         if (got) out = slot(u, k & 1);
+        __syncwarp();  // every lane has read it before one of them frees the slot
         return got;
     };
     auto qtile = [&](int u) { return base + (uint32_t)(u * C::kQTile); };

@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(ScoredUmmaCfg<D, MT, kMode>::kThreads, 1)
     auto take = [&](int u, int k, ScoredSlot &out) {
         const bool got = __all_sync(0xffffffffu, mbar_wait_bounded(item_ready(u, k & 1), (uint32_t)(k >> 1) & 1u, kWaitLimit));
         if (got) out = slot(u, k & 1);
+        __syncwarp();  // every lane has read it before one of them frees the slot
         return got;
     };
     auto qtile = [&](int x, int u) { return qb + (uint32_t)((x * MT + u) * C::kQTile); };

@@ -237,6 +237,7 @@ __global__ void __launch_bounds__(UmmaCfg<D, MT>::kThreads, 1)
     auto take = [&](int u, int k, UmmaSlot &out) {
         const bool got = __all_sync(0xffffffffu, mbar_wait_bounded(item_ready(u, k & 1), (uint32_t)(k >> 1) & 1u, kWaitLimit));
         if (got) out = slot(u, k & 1);
+        __syncwarp();  // every lane has read it before one of them frees the slot
         return got;
     };
     auto qtile = [&](int x, int u) { return qb + (uint32_t)((x * MT + u) * C::kQTile); };

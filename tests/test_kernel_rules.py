@@ -69,3 +69,12 @@ def test_every_warp_of_a_warpgroup_runs_the_same_setmaxnreg():
                                               ("else if (warp < 6)", True), ("if (warp >= C::kConsumers)", False), ("if (u < MT)", False)])
 def test_the_rule_tells_conditions_apart(condition, splits):
     assert splits_a_warpgroup(condition) == splits
+
+
+@pytest.mark.parametrize("name", ["pa_chunk_umma.cuh", "pa_chunk_scored_umma.cuh", "pa_attend8_umma.cuh"])
+def test_a_published_item_is_read_by_the_whole_warp_before_it_is_freed(name):
+    """Every lane copies an item's slot, and one lane's arrive frees it: a barrier of the warp between the two."""
+    code = code_of(os.path.join(CSRC, name))
+    body = re.search(r"auto take = \[&\].*?\};", code, flags=re.S).group(0)
+    copy, barrier = body.find("out = slot("), body.find("__syncwarp()")
+    assert 0 <= copy < barrier < body.find("return got")
