@@ -508,7 +508,12 @@ __global__ void __launch_bounds__(Umma8Cfg<D, MT>::kThreads, 1)
         for (;;) {
             Item8 it;
             ok = take(u, k, it);
-            if (!ok || it.end) break;
+            if (!ok || it.end) {
+                // A warp whose wait ran out joins the others' next decision all the same: each warp goes through one
+                // barrier for every item with rows here, and through one on its way out.
+                group_all(1 + u, false);
+                break;
+            }
             const int x = k & 1;
             ++k;
             if (u >= it.tiles) {

@@ -528,7 +528,12 @@ __global__ void __launch_bounds__(UmmaCfg<D, MT>::kThreads, 1)
         for (;;) {
             UmmaSlot item;
             ok = take(u, ku, item);
-            if (!ok || item.end) break;
+            if (!ok || item.end) {
+                // A warp whose wait ran out joins the others' next decision all the same: each warp goes through one
+                // barrier for every item with rows here, and through one on its way out.
+                warpgroup_all(1 + u, false);
+                break;
+            }
             const UmmaItem it = item.it;
             const int x = ku & 1;
             ++ku;

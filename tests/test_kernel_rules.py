@@ -78,3 +78,14 @@ def test_a_published_item_is_read_by_the_whole_warp_before_it_is_freed(name):
     body = re.search(r"auto take = \[&\].*?\};", code, flags=re.S).group(0)
     copy, barrier = body.find("out = slot("), body.find("__syncwarp()")
     assert 0 <= copy < barrier < body.find("return got")
+
+
+@pytest.mark.parametrize("name", ["pa_chunk_umma.cuh", "pa_chunk_scored_umma.cuh", "pa_attend8_umma.cuh"])
+def test_softmax_warps_leave_together(name):
+    """The warpgroup's barriers have no limit, so a warp that leaves the loop over items (at their end, or because its wait
+    ran out) goes through one of them first: otherwise the other three might wait there for good."""
+    code = re.sub(r"\s+", " ", code_of(os.path.join(CSRC, name)))
+    loop = code[code.rfind("take(u,"):]           # the softmax role is the last one that takes items
+    assert re.match(r"take\(u, ku?, \w+\); if \(!ok \|\| \w+\.end\) \{ (warp)?group_all\(1 \+ u, false\); break; \}", loop)
+    # behind the steps: one decision for all four warps
+    assert re.search(r"ok = (warp)?group_all\(1 \+ u, ok\); if \(!ok\) break;", loop)
