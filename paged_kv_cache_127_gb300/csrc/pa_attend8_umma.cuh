@@ -133,12 +133,13 @@ __device__ __forceinline__ void sts128(uint32_t at, const uint4 &x) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
 }
 // 16 codes, or zeros where there are none: the load is predicated, so that nothing waits for it before its use.
+// (Not by the read-only path: this grid may start while the launch before it, a write into the cache, is still running.)
 __device__ __forceinline__ void ldg_codes(uint4 &v, const uint8_t *p, bool want) {
     v = make_uint4(0, 0, 0, 0);
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.u32 p, %5, 0;\n\t"
-        "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+        "@p ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
         : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
         : "l"(p), "r"((uint32_t)want));
 }

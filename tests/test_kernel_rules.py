@@ -89,3 +89,10 @@ def test_softmax_warps_leave_together(name):
     assert re.match(r"take\(u, ku?, \w+\); if \(!ok \|\| \w+\.end\) \{ (warp)?group_all\(1 \+ u, false\); break; \}", loop)
     # behind the steps: one decision for all four warps
     assert re.search(r"ok = (warp)?group_all\(1 \+ u, ok\); if \(!ok\) break;", loop)
+
+
+def test_no_cache_is_read_by_the_read_only_path():
+    """ld.global.nc is for memory that nothing writes while a kernel lives; a kernel launched ahead of its predecessor's
+    end lives while that one writes the cache."""
+    for path in SOURCES:
+        assert "ld.global.nc" not in code_of(path), os.path.basename(path)
