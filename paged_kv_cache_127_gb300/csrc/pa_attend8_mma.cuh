@@ -219,13 +219,15 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
                     x.v += lane;
                     const int key = first_key(x);
                     const bool mine = i + lane < n;
+                    const int seen_from = a.window > 0 ? p.q.len - p.q.n - a.window + 1 : 0;   // by the sequence's first row
                     const uint32_t at = notes + (uint32_t)(C::kNotes * ((issued + lane) & 63));
                     int id[2];
                     bool want[2];
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
                         const int k = key + b * a.B;
-                        want[b] = b < nb && mine && k < p.q.len;
+                        // only blocks that some row sees: behind a window, half a step of two blocks may be none of them
+                        want[b] = b < nb && mine && k < p.q.len && (k + a.B > seen_from || k < a.sinks);
                         id[b] = want[b] ? a.block_tables[(size_t)p.s * a.max_blocks + (k >> lb)] : 0;
                     }
 #pragma unroll

@@ -1,0 +1,76 @@
+"""GPU tests of the 8-bit cache's attention at the edges of its contract: blocks that no row sees, queries and scales far
+from one, the bits of a decode's weights, many small items."""
+import math
+
+import pytest
+
+from gpu_helpers import require_gpu
+from kv8_helpers import assert_within, attend_ref, dtype_of, make_cache, tables_for
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def gpu():
+    return require_gpu()
+
+
+def generator(torch, seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def attend(torch, pa, q, cache, tables, lens, counts, scale, dtype, window=0, sinks=0, most=None, out_dtype="f32"):
+    """A decode where every sequence has one row and `most` is none, else a chunk call."""
+    T, Hq, D = q.shape
+    N, Hkv, B, _ = cache[0].shape
+    dims = pa.make_dims(len(lens), Hq, Hkv, D, B, N, tables.shape[1], 0, dtype)
+    out = torch.full((T, Hq, D), math.nan, dtype=dtype_of(torch, out_dtype), device="cuda")
+    dl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    c8 = pa.make_cache8(*cache)
+    if most is None and all(c == 1 for c in counts):
+        ws = torch.full((pa.pa_decode8_workspace_bytes(dims),), 255, dtype=torch.uint8, device="cuda")
+        pa.pa_decode8(dims, q, c8, tables, dl, scale, out, ws, window=window, sinks=sinks)
+    else:
+        qs = torch.tensor([sum(counts[:i]) for i in range(len(counts) + 1)], dtype=torch.int32, device="cuda")
+        most = most or max(counts)
+        ws = torch.full((pa.pa_chunk8_workspace_bytes(dims, T, most),), 255, dtype=torch.uint8, device="cuda")
+        pa.pa_chunk8(dims, q, c8, tables, dl, qs, scale, out, most, ws, window=window, sinks=sinks)
+    torch.cuda.synchronize()
+    return out
+
+
+def unseen_blocks(n, m, B, window, sinks):
+    """Columns of a sequence of n keys of which its last m tokens see no key."""
+    begin = n - m - window + 1
+    return [b for b in range(-(-n // B)) if (b + 1) * B <= begin and b * B >= sinks]
+
+
+@pytest.mark.parametrize("dtype,D,B,Hq,Hkv", [("bf16", 128, 16, 32, 8), ("f16", 64, 32, 4, 4), ("bf16", 64, 16, 12, 6)])
+@pytest.mark.parametrize("nq", [1, 3, 6, 20, 80])
+@pytest.mark.parametrize("window,sinks", [(40, 4), (33, 0), (1, 0), (17, 20), (100, 33), (300, 1)])
+def test_blocks_that_no_row_sees_need_not_be_there(gpu, dtype, D, B, Hq, Hkv, nq, window, sinks):
+    """A server that frees what a window has left behind: such blocks' table entries may be anything, and so may the scales
+    of the block that an entry names."""
+    torch, pa = gpu
+    gen = generator(torch, 7 * window + nq)
+    lens = [nq + x for x in (0, 47, 48, 63, 64, 79, 95, 101, 500, 900)]
+    counts = [nq] * len(lens)
+    tables, N = tables_for(torch, gen, lens, B)
+    cache = make_cache(torch, gen, N, Hkv, B, D)
+    q = torch.randn(sum(counts), Hq, D, generator=gen, device="cuda").to(dtype_of(torch, dtype))
+    ref, bound = attend_ref(torch, q, cache, tables, lens, counts, 0.09, window, sinks)
+    gone = [(s, b) for s, n in enumerate(lens) for b in unseen_blocks(n, nq, B, window, sinks)]
+    assert gone
+    # the scales of the blocks: what an earlier user left
+    for i, (s, b) in enumerate(gone):
+        for scales in cache[2:]:
+            scales[tables[s, b].long()] = (math.nan, 0.0, math.inf, -1.0)[i % 4]
+    got = attend(torch, pa, q, cache, tables, lens, counts, 0.09, dtype, window, sinks)
+    assert pa.pa_device_errors(clear=True) == 0
+    assert_within(got, ref, bound, "f32")
+    # the table entries: no block at all
+    for i, (s, b) in enumerate(gone):
+        tables[s, b] = (-1, N, -(2 ** 31), 2 ** 31 - 1)[i % 4]
+    got = attend(torch, pa, q, cache, tables, lens, counts, 0.09, dtype, window, sinks)
+    assert pa.pa_device_errors(clear=True) == 0
+    assert_within(got, ref, bound, "f32")
