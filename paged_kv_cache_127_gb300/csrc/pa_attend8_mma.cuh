@@ -46,7 +46,7 @@ struct Attend8Cfg {
     static constexpr int kTileBytes = kStep8 * D * HG;       // K (or V) of a step
     static constexpr int kStagesRaw = (192 * 1024 / kCtas - kQBytes) / (2 * kTileBytes);
     static constexpr int kStages = kStagesRaw > 8 ? 8 : kStagesRaw;
-    // (ks, log2 vs, 1 / vs, -) of two blocks and each head, of 64 steps: a batch of 32 is written at once, and consumers are
+    // (ks scale log2(e), log2 vs, 1 / vs, -) of two blocks and each head, of 64 steps: a batch of 32 is written at once, and consumers are
     // at most kStages steps behind it
     static constexpr int kNotes = HG * 32;
     static constexpr size_t kNoteOff = (size_t)kStages * 2 * kTileBytes;
@@ -98,6 +98,7 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
     using H = Mma16<__half>;
     constexpr int kKS = D / 16, kMT = D / 16, kRows = C::kRows;             // k-steps of S, 16-row tiles of O^T
     constexpr int kWarps = C::kThreads / 32;
+    constexpr bool kLifted = std::is_same<T, __nv_bfloat16>::value;   // queries go in as f16, by a power of two per row
     extern __shared__ unsigned char smem_raw[];
     __shared__ long long sums[kWarps];
     __shared__ int4 begin_at;  // (sequence, -, rest low, rest high) of the first step
@@ -255,7 +256,7 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
                             for (int b = 0; b < kB; ++b)
 #pragma unroll
                                 for (int h = 0; h < HG; ++h) {
-                                    const float k1 = from[b0 + b] >= 0 ? ks[b][h] : 0.f, v1 = from[b0 + b] >= 0 ? vs[b][h] : -1.f;
+                                    const float k1 = from[b0 + b] >= 0 ? ks[b][h] * (a.scale * kLog2e8) : 0.f, v1 = from[b0 + b] >= 0 ? vs[b][h] : -1.f;
                                     asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %3};" ::"r"(at + 32 * h + 16 * (b0 + b)), "f"(k1),
                                                  "f"(v1 > 0.f ? lg2(v1) : 0.f), "f"(1.f / v1)
                                                  : "memory");
@@ -312,7 +313,7 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
         // queries as B fragments (lane (g, c): row g of a tile); what belongs to the rows 2 c, 2 c + 1 that a lane has of S^T
         uint32_t qb[kKS][C::kWide ? 1 : NQ][2];
         const uint32_t q_at = ring + (uint32_t)C::kQOff + (uint32_t)(warp * NQ * D * 16 + lane * 16);   // [k-step pair][tile][lane]: two k-steps
-        float qs[NQ][2];                                     // scale log2(e) over the row's factor
+        float qs[NQ][2];                                     // one over the row's factor (bf16)
         int pos[NQ][2];
 #pragma unroll
         for (int t8 = 0; t8 < NQ; ++t8) {
@@ -333,8 +334,8 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
                 qb[4 * ch][tq][0] = x.x, qb[4 * ch][tq][1] = x.y, qb[4 * ch + 1][tq][0] = x.z, qb[4 * ch + 1][tq][1] = x.w;
                 qb[4 * ch + 2][tq][0] = y.x, qb[4 * ch + 2][tq][1] = y.y, qb[4 * ch + 3][tq][0] = y.z, qb[4 * ch + 3][tq][1] = y.w;
             }
-            float back = a.scale * kLog2e8;
-            if constexpr (std::is_same<T, __nv_bfloat16>::value) {   // as f16, the row's largest at 2^10
+            float back = 1.f;
+            if constexpr (kLifted) {   // as f16, the row's largest at 2^10
 #pragma unroll
                 for (int ks = 0; ks < kKS; ++ks)
 #pragma unroll
@@ -344,9 +345,9 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
                     }
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const int e = min(100, max(-100, 10 - ((int)(__float_as_uint(top) >> 23) - 127)));
+                const int e = min(126, 10 - ((int)(__float_as_uint(top) >> 23) - 127));   // -118 .. 126; what 2^126 lifts is exact in f16
                 const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-                back *= __uint_as_float((uint32_t)(127 - e) << 23);
+                back = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
                 for (int ks = 0; ks < kKS; ++ks)
 #pragma unroll
@@ -453,7 +454,9 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
                         // a_j = z_j + log2 vs
 #pragma unroll
                         for (int t8 = 0; t8 < NQ; ++t8) {
-                            const float mul[2] = {qs[t8][0] * of_half(ks, i2), qs[t8][1] * of_half(ks, i2)};
+                            // (a row's factor, of up to 2^126, meets the scales only here: either may be far from 1 alone)
+                            const float ck = of_half(ks, i2);
+                            const float mul[2] = {kLifted ? qs[t8][0] * ck : ck, kLifted ? qs[t8][1] * ck : ck};
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 float x = fmaf(s[i2][t8][e], mul[e & 1], of_half(lv, i2));

@@ -74,3 +74,26 @@ def test_blocks_that_no_row_sees_need_not_be_there(gpu, dtype, D, B, Hq, Hkv, nq
     got = attend(torch, pa, q, cache, tables, lens, counts, 0.09, dtype, window, sinks)
     assert pa.pa_device_errors(clear=True) == 0
     assert_within(got, ref, bound, "f32")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("nq", [1, 5, 9, 70])
+@pytest.mark.parametrize("q_exp,k_exp", [((-126, -110), (112, 118)), ((-100, -90), (90, 96)), ((90, 98), (-80, -76))])
+def test_queries_and_scales_far_from_one(gpu, D, nq, q_exp, k_exp):
+    """Tiny queries over loud keys and loud ones over quiet keys, with logits of order one: rows in bf16 down to its
+    subnormal numbers."""
+    torch, pa = gpu
+    gen = generator(torch, 11 * nq + D)
+    B, Hq, Hkv = 16, 8, 2
+    lens = [nq + 200, nq + 31]
+    tables, N = tables_for(torch, gen, lens, B)
+    k, v, _, vs = make_cache(torch, gen, N, Hkv, B, D)
+    ks = torch.exp2(torch.randint(k_exp[0], k_exp[1] + 1, (N, Hkv), generator=gen, device="cuda").float())
+    q = torch.randn(2 * nq, Hq, D, generator=gen, device="cuda").double()
+    q = (q * torch.exp2(torch.randint(q_exp[0], q_exp[1] + 1, (2 * nq, Hq, 1), generator=gen, device="cuda").double())).to(torch.bfloat16)
+    q[0, 3] = 0.0
+    scale = 2.0 ** -(sum(k_exp) / 2 + sum(q_exp) / 2 + 9)
+    ref, bound = attend_ref(torch, q, (k, v, ks, vs), tables, lens, [nq, nq], scale)
+    got = attend(torch, pa, q, (k, v, ks, vs), tables, lens, [nq, nq], scale, "bf16")
+    assert_within(got, ref, bound, "f32")
+    assert pa.pa_device_errors(clear=True) == 0
