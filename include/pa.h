@@ -491,9 +491,10 @@ typedef struct pa_window {
  *     out[i, h, :] = sum_j p_j V_j,  p = softmax_j(scale * q[i, h, :] . K_j)
  *
  * with K_j, V_j the values that the codes stand for.  Scores, weights' sums and outputs are held
- * in fp32; the codes go into the products as they are (exact in 16 bits), and the weights are
- * rounded to 11 bits before the second one.  Short chunks and decodes over bf16 take a row's queries as f16 by a power of
- * two, exactly down to 2^-24 of the row's largest.  |q| < 2^110.
+ * in fp32; the codes go into the products as they are (exact in 16 bits).  Into the second one weights go
+ * with 22 bits in decodes and where max_query_len * G <= 16, else rounded once to 11 bits
+ * (pa_chunk_attention splits its weights in two 16-bit terms).  Short chunks and decodes over bf16 take a row's
+ * queries as f16 by a power of two, exactly down to 2^-24 of the row's largest.  |q| < 2^110.
  *
  *   window        NULL: all keys
  *   out           [S | T, Hq, D] float32, or kv_dtype when out_dtype == kv_dtype

@@ -98,6 +98,7 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
     using H = Mma16<__half>;
     constexpr int kKS = D / 16, kMT = D / 16, kRows = C::kRows;             // k-steps of S, 16-row tiles of O^T
     constexpr int kWarps = C::kThreads / 32;
+    constexpr bool kTwoTerms = NQ == 1;   // of the weights in the second product (pa_attend8.cuh has both sides)
     constexpr bool kLifted = std::is_same<T, __nv_bfloat16>::value;   // queries go in as f16, by a power of two per row
     extern __shared__ unsigned char smem_raw[];
     __shared__ long long sums[kWarps];
@@ -527,7 +528,7 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
                             }
                     }
                     // ---- weights, as B fragments: keys as k
-                    uint32_t pb[kKK][NQ][2];
+                    uint32_t pb[kKK][NQ][2], pl[kKK][kTwoTerms ? NQ : 1][2];
 #pragma unroll
                     for (int t8 = 0; t8 < NQ; ++t8) {
                         const float m0 = m[t8][0] == -INFINITY ? 0.f : m[t8][0], m1 = m[t8][1] == -INFINITY ? 0.f : m[t8][1];
@@ -537,8 +538,14 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
                             // a block that is not there has weights of 0 (and an iv of -1)
                             l[t8][0] = fmaf(w0 + w2, of_half(iv, i2), l[t8][0]);
                             l[t8][1] = fmaf(w1 + w3, of_half(iv, i2), l[t8][1]);
-                            pb[i2][t8][0] = transpose8(H::pack(w0, w1));
-                            pb[i2][t8][1] = transpose8(H::pack(w2, w3));
+                            const uint32_t h0 = H::pack(w0, w1), h1 = H::pack(w2, w3);
+                            pb[i2][t8][0] = transpose8(h0);
+                            pb[i2][t8][1] = transpose8(h1);
+                            if constexpr (kTwoTerms) {   // what the rounding left
+                                const float2 f0 = H::unpack(h0), f1 = H::unpack(h1);
+                                pl[i2][t8][0] = transpose8(H::pack(w0 - f0.x, w1 - f0.y));
+                                pl[i2][t8][1] = transpose8(H::pack(w2 - f1.x, w3 - f1.y));
+                            }
                         }
                     }
                     // ---- O^T += V^T P^T
@@ -554,7 +561,10 @@ __global__ void __launch_bounds__(Attend8Cfg<D, NQ, MB, HG>::kThreads, Attend8Cf
                             const uint32_t a0 = f16_of_codes(lo & 0xffffu), a1 = f16_of_codes(lo >> 16);
                             const uint32_t a2 = f16_of_codes(hi & 0xffffu), a3 = f16_of_codes(hi >> 16);
 #pragma unroll
-                            for (int t8 = 0; t8 < NQ; ++t8) H::mma(o[j][t8], a0, a1, a2, a3, pb[i2][t8][0], pb[i2][t8][1]);
+                            for (int t8 = 0; t8 < NQ; ++t8) {
+                                H::mma(o[j][t8], a0, a1, a2, a3, pb[i2][t8][0], pb[i2][t8][1]);
+                                if constexpr (kTwoTerms) H::mma(o[j][t8], a0, a1, a2, a3, pl[i2][t8][0], pl[i2][t8][1]);
+                            }
                         }
                 }
             }

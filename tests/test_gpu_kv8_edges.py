@@ -97,3 +97,23 @@ def test_queries_and_scales_far_from_one(gpu, D, nq, q_exp, k_exp):
     got = attend(torch, pa, q, (k, v, ks, vs), tables, lens, [nq, nq], scale, "bf16")
     assert_within(got, ref, bound, "f32")
     assert pa.pa_device_errors(clear=True) == 0
+
+
+@pytest.mark.parametrize("dtype,D,B,Hq,Hkv,nq", [("bf16", 128, 16, 32, 8, 1), ("f16", 64, 32, 4, 4, 1), ("bf16", 64, 16, 12, 6, 8), ("f16", 128, 32, 8, 1, 2),
+                                                 ("bf16", 128, 32, 4, 2, 3), ("f16", 64, 16, 8, 8, 16)])
+def test_up_to_16_rows_weights_keep_22_bits(gpu, dtype, D, B, Hq, Hkv, nq):
+    """Decodes, and chunks with at most 16 rows of a KV head: weights in two f16 terms.  attend_ref's bound has one term of
+    2^-11 for them, once above and once below the fraction; two terms leave 2^-22.  With small logits and few keys
+    one rounding to f16 would stand out (logits' own errors are 2^-23 D reach + 2^-20)."""
+    torch, pa = gpu
+    gen = generator(torch, D + nq)
+    lens = [nq + x for x in (1, 2, 3, 5, 7, 11, 17, 40, 100)]
+    counts = [nq] * len(lens)
+    tables, N = tables_for(torch, gen, lens, B)
+    k, v, ks, vs = make_cache(torch, gen, N, Hkv, B, D)
+    q = torch.randn(sum(counts), Hq, D, generator=gen, device="cuda").to(dtype_of(torch, dtype))
+    scale = 0.004
+    ref, bound = attend_ref(torch, q, (k, v, ks, vs), tables, lens, counts, scale)
+    weighted, _ = attend_ref(torch, q, (k, v.float().abs().to(v.dtype), ks, vs), tables, lens, counts, scale)   # sum p |V|
+    got = attend(torch, pa, q, (k, v, ks, vs), tables, lens, counts, scale, dtype)
+    assert_within(got, ref, bound - 2 * (2.0 ** -11 - 2.0 ** -22) * weighted, "f32")
