@@ -614,6 +614,14 @@ def pa_copy_blocks8(dims: pa_dims, cache: Cache8, src_dst_pairs, stream=None, pr
     return _issue(lib.pa_copy_blocks8, args, "pa_copy_blocks8", dev, prepare, (dims, c8, _keep8(cache), src_dst_pairs))
 
 
+def _i32(value, name):
+    """A whole number as the library takes it (ctypes would cut off what is beyond 32 bits)."""
+    value = int(value)
+    if not -2 ** 31 <= value < 2 ** 31:
+        raise ValueError(f"{name} is {value}, beyond 32 bits")
+    return value
+
+
 def _expect_attend8(d, rows, kv, dev, q, block_tables, context_lens, out):
     """The checks that decode and chunk attention over an 8-bit cache share."""
     t = _torch()
@@ -650,7 +658,7 @@ def pa_decode8(dims: pa_dims, q, cache: Cache8, block_tables, context_lens, scal
     code = _out_code(out, dims)
     _expect_attend8(d, d.num_seqs, kv, dev, q, block_tables, context_lens, out)
     c8 = _marshal_cache8(cache, d, dev)
-    win = pa_window(int(window), int(sinks))
+    win = pa_window(_i32(window, "window"), _i32(sinks, "sinks"))
     ws_ptr, ws_bytes = _workspace8(workspace, lambda: pa_decode8_workspace_bytes(dims), "pa_decode8", dev)
     args = (ctypes.byref(dims), ctypes.byref(win), q.data_ptr(), ctypes.byref(c8), block_tables.data_ptr(),
             context_lens.data_ptr(), float(scale), out.data_ptr(), code, ws_ptr, ws_bytes, _stream_ptr(stream, dev))
@@ -675,7 +683,7 @@ def pa_chunk8(dims: pa_dims, q, cache: Cache8, block_tables, context_lens, query
     _expect_attend8(d, T, kv, dev, q, block_tables, context_lens, out)
     _expect_beside(query_start, "query_start", (d.num_seqs + 1,), t.int32, dev)
     c8 = _marshal_cache8(cache, d, dev)
-    win = pa_window(int(window), int(sinks))
+    win = pa_window(_i32(window, "window"), _i32(sinks, "sinks"))
     ws_ptr, ws_bytes = _workspace8(workspace, lambda: pa_chunk8_workspace_bytes(dims, T, max_query_len), "pa_chunk8", dev)
     args = (ctypes.byref(dims), ctypes.byref(win), q.data_ptr(), ctypes.byref(c8), block_tables.data_ptr(),
             context_lens.data_ptr(), query_start.data_ptr(), T, int(max_query_len), float(scale), out.data_ptr(), code,
@@ -711,7 +719,7 @@ def _marshal_score(score, num_q_heads, rows, dev):
     for name in ("key_begin", "key_end"):
         if getattr(score, name) is not None:
             _expect_beside(getattr(score, name), "score." + name, (rows,), t.int32, dev)
-    sc = pa_score(score.softcap, score.window, ptr(score.slopes), ptr(score.key_begin), ptr(score.key_end))
+    sc = pa_score(score.softcap, _i32(score.window, "score.window"), ptr(score.slopes), ptr(score.key_begin), ptr(score.key_end))
     return ctypes.byref(sc), (sc, score.slopes, score.key_begin, score.key_end)
 
 

@@ -117,3 +117,17 @@ def test_up_to_16_rows_weights_keep_22_bits(gpu, dtype, D, B, Hq, Hkv, nq):
     weighted, _ = attend_ref(torch, q, (k, v.float().abs().to(v.dtype), ks, vs), tables, lens, counts, scale)   # sum p |V|
     got = attend(torch, pa, q, (k, v, ks, vs), tables, lens, counts, scale, dtype)
     assert_within(got, ref, bound - 2 * (2.0 ** -11 - 2.0 ** -22) * weighted, "f32")
+
+
+@pytest.mark.parametrize("nq", [1, 4])
+def test_windows_and_sinks_beyond_32_bits_are_refused(gpu, nq):
+    torch, pa = gpu
+    gen = generator(torch, nq)
+    tables, N = tables_for(torch, gen, [60], 16)
+    cache = make_cache(torch, gen, N, 2, 16, 64)
+    q = torch.randn(nq, 4, 64, generator=gen, device="cuda").to(torch.float16)
+    for window, sinks in ((2 ** 32, 0), (2 ** 32 + 5, 1), (8, 2 ** 32), (8, 2 ** 31), (2 ** 31, 0)):
+        with pytest.raises(ValueError):
+            attend(torch, pa, q, cache, tables, [60], [nq], 0.1, "f16", window, sinks)
+    ref, bound = attend_ref(torch, q, cache, tables, [60], [nq], 0.1, 8, 2 ** 31 - 1)
+    assert_within(attend(torch, pa, q, cache, tables, [60], [nq], 0.1, "f16", 8, 2 ** 31 - 1), ref, bound, "f32")
