@@ -268,8 +268,9 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_whole_kernel(const RopeA
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     const float2 c = w[e * upq];
-                    const float p = f[e] * c.x - g[e] * c.y;
-                    g[e] = g[e] * c.x + f[e] * c.y;
+                    // rounded as rope_units_kernel's, so that a layout's bits do not depend on which kernel takes it
+                    const float p = fmaf(f[e], c.x, -__fmul_rn(g[e], c.y));
+                    g[e] = fmaf(f[e], c.y, __fmul_rn(g[e], c.x));
                     f[e] = p;
                 }
                 x[u] = Unit<T>::pack(f);
