@@ -81,9 +81,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_elements_kernel(const RopeA
         if (i < half) {
             const int ia = a.interleaved ? 2 * i : i, ib = a.interleaved ? 2 * i + 1 : i + half;
             const float x = static_cast<float>(src[ia]), y = static_cast<float>(src[ib]);
-            const float2 w = cs[i];
-            dst[ia] = narrow<T>(x * w.x - y * w.y);
-            dst[ib] = narrow<T>(y * w.x + x * w.y);
+            const float2 w = turned(x, y, cs[i]);
+            dst[ia] = narrow<T>(w.x);
+            dst[ib] = narrow<T>(w.y);
         } else {
             dst[half + i] = src[half + i];
         }
@@ -180,20 +180,18 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_units_kernel(const RopeA
                         for (int e = 0; e < kAngles; ++e) {
                             float &p = kInterleaved ? f[2 * e] : f[e], &r = kInterleaved ? f[2 * e + 1] : g[e];
                             if (kInterleaved && e >= live) continue;
-                            const float2 c = w[e];
-                            const float pn = p * c.x - r * c.y;
-                            r = r * c.x + p * c.y;
-                            p = pn;
+                            const float2 t = turned(p, r, w[e]);
+                            p = t.x, r = t.y;
                         }
-                        const uint4 turned = Unit<T>::pack(f);
+                        const uint4 packed = Unit<T>::pack(f);
                         if constexpr (kInterleaved) {  // the words of pairs behind R stay as they are
                             constexpr int kWords = 4 / kAngles;  // of a pair
-                            x[u].x = turned.x;
-                            if (1 / kWords < live) x[u].y = turned.y;
-                            if (2 / kWords < live) x[u].z = turned.z;
-                            if (3 / kWords < live) x[u].w = turned.w;
+                            x[u].x = packed.x;
+                            if (1 / kWords < live) x[u].y = packed.y;
+                            if (2 / kWords < live) x[u].z = packed.z;
+                            if (3 / kWords < live) x[u].w = packed.w;
                         } else {
-                            x[u] = turned;
+                            x[u] = packed;
                         }
                         if (!kInterleaved) y[u] = Unit<T>::pack(g);
                     }
@@ -268,10 +266,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_whole_kernel(const RopeA
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     const float2 c = w[e * upq];
-                    // rounded as rope_units_kernel's, so that a layout's bits do not depend on which kernel takes it
-                    const float p = fmaf(f[e], c.x, -__fmul_rn(g[e], c.y));
-                    g[e] = fmaf(f[e], c.y, __fmul_rn(g[e], c.x));
-                    f[e] = p;
+                    const float2 r = turned(f[e], g[e], c);
+                    f[e] = r.x, g[e] = r.y;
                 }
                 x[u] = Unit<T>::pack(f);
                 y[u] = Unit<T>::pack(g);
@@ -326,7 +322,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_split_kernel(const RopeArgs
                     const bool low = d < half;
                     const float2 c = cs[low ? d : d - half];
                     const float other = static_cast<float>(head[low ? d + half : d - half]), own = static_cast<float>(x.e[e]);
-                    x.e[e] = narrow<T>(low ? own * c.x - other * c.y : own * c.x + other * c.y);
+                    x.e[e] = narrow<T>(low ? turned(own, other, c).x : turned(other, own, c).y);
                 }
             }
         }

@@ -133,9 +133,8 @@ struct Part8 {
             if (turns) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float p = f[e] * w[e].x - f[8 + e] * w[e].y;
-                    f[8 + e] = f[8 + e] * w[e].x + f[e] * w[e].y;
-                    f[e] = p;
+                    const float2 t = turned(f[e], f[8 + e], w[e]);
+                    f[e] = t.x, f[8 + e] = t.y;
                 }
             }
         } else if constexpr (kPairing == kNeighbours) {
@@ -143,9 +142,8 @@ struct Part8 {
             for (int e = 0; e < 8; ++e) {
                 const int p = (e < 4 ? u0 : u0 + du) / 2 + (e & 3);
                 if (p < half) {
-                    const float v = f[2 * e] * w[e].x - f[2 * e + 1] * w[e].y;
-                    f[2 * e + 1] = f[2 * e + 1] * w[e].x + f[2 * e] * w[e].y;
-                    f[2 * e] = v;
+                    const float2 t = turned(f[2 * e], f[2 * e + 1], w[e]);
+                    f[2 * e] = t.x, f[2 * e + 1] = t.y;
                 }
             }
         } else {
@@ -156,7 +154,7 @@ struct Part8 {
                     const bool low = d < half;
                     const float2 t = cs[r * kRow + (low ? d : d - half)];
                     const float other = static_cast<float>(head[low ? d + half : d - half]);
-                    f[e] = low ? f[e] * t.x - other * t.y : f[e] * t.x + other * t.y;
+                    f[e] = low ? turned(f[e], other, t).x : turned(other, f[e], t).y;
                 }
             }
         }
