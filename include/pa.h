@@ -93,7 +93,7 @@ typedef struct pa_dims {
 #define PA_DEVERR_TIMEOUT 16u    /* a bounded in-kernel wait gave up; outputs of the  */
                                  /* affected work item were not written              */
 #define PA_DEVERR_BAD_AXIS 64u   /* an axis of a rotated pair outside [0, num_axes):  */
-                                 /* the pair is not turned                           */
+                                 /* the pair turns as at position 0                  */
 #define PA_DEVERR_BAD_ROW 32u    /* a row of key sums outside [0, num_rows): the      */
                                  /* sequence's sums are not updated, and pa_evict     */
                                  /* leaves the sequence as it is                      */
@@ -398,8 +398,9 @@ PA_API int32_t pa_rope_write_kv(const pa_dims *dims, const pa_rope *rope, const 
  * pa_rope_write_kv.
  *
  *   axes          pair_axis: int32 [rotary_dim / 2], device, each 0 .. num_axes - 1
- *                 (a pair of another axis is not turned, and flagged:
- *                 PA_DEVERR_BAD_AXIS); num_axes 1 .. 16.  NULL: one axis
+ *                 (a pair of another axis turns as at position 0, so mscale alone
+ *                 acts on it, and is flagged: PA_DEVERR_BAD_AXIS); num_axes 1 .. 16.
+ *                 NULL: one axis
  *   positions     int32 [num_axes, num_tokens], device (any value)
  *   other arguments, shapes and errors as for pa_rope_write_kv
  */
@@ -420,8 +421,8 @@ PA_API int32_t pa_rope_axes_write_kv(const pa_dims *dims, const pa_rope *rope, c
  *     K[block, h, slot, :] = k_scales[block, h] * k[block, h, slot, :]
  *
  * and the same for V.  Half the memory and half the reads of a 16-bit cache.  The calls
- * below work on it as their counterparts do on the others; kv_dtype of their dims is
- * the type of the queries, keys and values that go in and of the outputs, PA_F16 or
+ * below work on it as their counterparts do on the others (large chunks with fewer bits
+ * of the weights: pa_chunk8); kv_dtype of their dims is the type of the queries, keys and values that go in and of the outputs, PA_F16 or
  * PA_BF16 (PA_ERR_UNSUPPORTED for PA_F32), D is 64 or 128 and B 16 or 32.
  *   k, v                 codes [N, Hkv, B, D], device, 16-byte aligned
  *   k_scales, v_scales   float32 [N, Hkv], device.  The writes store powers of two.  The
@@ -477,7 +478,8 @@ PA_API int32_t pa_copy_blocks8(const pa_dims *dims, const pa_cache8 *cache, cons
  *     j > pos - window   or   j < sinks
  * -- a sliding window and a few first tokens that stay visible.  A window of 0 is none
  * (all keys j <= pos; sinks is not used), and so is a NULL pa_window.  Only the blocks
- * that some row of a sequence sees are read.
+ * that some row of a sequence sees are read: other entries of its table, and the codes and
+ * scales of other blocks, may be anything.
  */
 typedef struct pa_window {
     int32_t window;   /* 0: none; else > 0 */

@@ -11,12 +11,12 @@
 // normaliser is sum_j P_j / vs.  So a scale costs one multiply-add per block and row, the products run on the bare
 // codes, and P stays within a bound of its own whatever the blocks' scales are.  Both products take 16-bit floats: an
 // e4m3 code is exactly an f16 value (and a bf16 one).  P goes in as two f16 terms (22 bits) where a KV head has at most 16
-// rows, as decodes have: HBM bounds those, and the second term costs them 1 % at most (32 long sequences 207 -> 209 us, a
+// rows, as decodes have: HBM bounds those, and the second term costs them little (32 long sequences 207 -> 209 us, a
 // batch of 256 79 -> 79, 3 short ones 5.8 -> 6.0).  For more rows P is rounded to f16 once (2^-11 of a weight, where a
 // code is off by up to 2^-4 of its value): a second term takes five drafted tokens of 256 sequences from 145 to
-// 161 us, 16 x 512-token chunks from 221 to 277 and windowed ones of D 64 from 44 to 54.  On the tcgen05 path K goes in in the queries' type; on the
-// mma.sync path bf16 queries go in as f16, by a power of two per row that brings the row's largest to 2^10, which is
-// exact for every element that is within 2^-24 of it.
+// 161 us, 16 x 512-token chunks from 221 to 277 and windowed ones of D 64 from 44 to 54.
+// On the tcgen05 path K goes in in the queries' type; on the mma.sync path bf16 queries go in as f16, by a power of two
+// per row that brings the row's largest to 2^10, which is exact for every element that is within 2^-24 of it.
 #pragma once
 
 #include "pa_device.cuh"

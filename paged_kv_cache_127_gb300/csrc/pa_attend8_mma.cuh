@@ -38,7 +38,8 @@ struct Attend8Cfg {
     static constexpr int kCtas = attend8_ctas(NQ, MB, HG);   // per SM
     // More than 8 rows a warp: the queries' fragments lie in shared memory.  24 rows: O^T alone takes 96 registers, and whole
     // warpgroups of consumers take over registers of a producer warpgroup (of which one warp works): two CTAs of 4 + 4
-    // warps are launched at 128 registers, producers keep 24 and consumers get 232 (verify 147 us; 40 and 216: 159).
+    // warps are launched at 128 registers, producers keep 24 and consumers get 232 (verify 147 us; 40 and 216: 159).  At D 128
+    // these kernels still spill some 300 bytes a thread (stores; 450 of loads).
     static constexpr bool kWide = NQ > 1;
     static constexpr bool kSplit = NQ == 3 && kConsumers == 4;
     static constexpr int kThreads = 32 * (kConsumers + (kSplit ? 4 : 1));

@@ -23,7 +23,8 @@
 // maximum moves only when a row's new one is 2^8 larger, as in the kernel for 16-bit caches.
 //
 // Synchronisation is by mbarriers, every wait bounded: on a timeout the kernel sets PA_DEVERR_TIMEOUT, waits
-// (bounded) for the MMAs and copies it issued, frees its TMEM and returns.
+// (bounded) for the MMAs and copies it issued, frees its TMEM and returns.  (A softmax warpgroup's own barriers have
+// no limit: each of its warps goes through as many of them, whatever it gave up on.)
 #pragma once
 
 #include <cuda.h>

@@ -124,7 +124,8 @@ Layout8 chunk_layout8(const pa_dims *d, int32_t max_q, const pa_window *w) {
     return L;
 }
 
-// The tensor maps of the caches, re-encoded only when a cache or its shape changes (per host thread).
+// The tensor maps of the caches: the last four (caches, shapes) of a host thread.  A model with a cache for each layer
+// encodes both maps in every call, which takes 0.1 us (32 caches in turn 3.8 us a prepared decode, one cache 3.7).
 cudaError_t codes_map(const void *ptr, int D, int B, long long block_heads, int heads, CUtensorMap *out) {
     struct Entry {
         const void *ptr = nullptr;
