@@ -1,5 +1,5 @@
 """GPU tests of the 8-bit cache's attention at the edges of its contract: blocks that no row sees, queries and scales far
-from one, the bits of a decode's weights, many small items."""
+from one, the bits of a decode's weights, many small items, steps behind each other without a wait."""
 import math
 
 import pytest
@@ -131,3 +131,79 @@ def test_windows_and_sinks_beyond_32_bits_are_refused(gpu, nq):
             attend(torch, pa, q, cache, tables, [60], [nq], 0.1, "f16", window, sinks)
     ref, bound = attend_ref(torch, q, cache, tables, [60], [nq], 0.1, 8, 2 ** 31 - 1)
     assert_within(attend(torch, pa, q, cache, tables, [60], [nq], 0.1, "f16", 8, 2 ** 31 - 1), ref, bound, "f32")
+
+
+@pytest.mark.parametrize("dtype,D,B,nq,window", [("bf16", 64, 16, 33, 20), ("f16", 128, 32, 17, 0), ("bf16", 128, 16, 48, 16)])
+def test_many_items_of_few_steps(gpu, dtype, D, B, nq, window):
+    """Several hundred items of one to four steps, most with a last tile of few rows: slots of items change hands all the time."""
+    torch, pa = gpu
+    gen = generator(torch, nq)
+    S, Hq, Hkv = 300, 8, 1
+    counts = [1 + int(x) for x in torch.randint(0, nq, (S,), generator=gen, device="cuda")]
+    lens = [c + int(x) for c, x in zip(counts, torch.randint(0, 90, (S,), generator=gen, device="cuda"))]
+    tables, N = tables_for(torch, gen, lens, B)
+    cache = make_cache(torch, gen, N, Hkv, B, D)
+    q = torch.randn(sum(counts), Hq, D, generator=gen, device="cuda").to(dtype_of(torch, dtype))
+    ref, bound = attend_ref(torch, q, cache, tables, lens, counts, 0.09, window, 3)
+    first = None
+    for _ in range(5):
+        got = attend(torch, pa, q, cache, tables, lens, counts, 0.09, dtype, window, 3, most=nq)
+        assert_within(got, ref, bound, "f32")
+        first = got if first is None else first
+        assert torch.equal(got, first)
+    assert pa.pa_device_errors(clear=True) == 0
+
+
+@pytest.mark.parametrize("nq", [1, 5, 20])
+def test_steps_in_flight_are_the_steps_one_at_a_time(gpu, nq):
+    """Writes and attention behind each other without a wait between them, scales growing at every step (neighbouring blocks'
+    scales share cache lines): each launch sees what the one before it wrote."""
+    torch, pa = gpu
+    dtype, D, B, Hq, Hkv, S, steps = "bf16", 128, 16, 32, 8, 24, 60
+    gen = generator(torch, nq)
+    most = 20 + nq * steps
+    tables, N = tables_for(torch, gen, [most] * S, B)
+    start = make_cache(torch, gen, N, Hkv, B, D)
+    start[2].fill_(2.0 ** -20)
+    start[3].fill_(2.0 ** -20)
+    freqs = torch.from_numpy(pa.pa_rope_freqs(D, 10000.0)[0].copy()).cuda()
+    rope = pa.make_rope(D, freqs)
+    dims = pa.make_dims(S, Hq, Hkv, D, B, N, tables.shape[1], 0, dtype)
+    T = S * nq
+    loud = torch.exp2(torch.arange(steps, device="cuda") / 4.0 - 6)[:, None, None, None]
+    xs = (loud * torch.randn(steps, T, Hq + 2 * Hkv, D, generator=gen, device="cuda")).to(torch.bfloat16)
+    at = [torch.arange(20 + i * nq, 20 + (i + 1) * nq, device="cuda") for i in range(steps)]
+    slots = [(tables.long()[:, a // B] * B + a % B).reshape(-1).contiguous() for a in at]
+    pos = [a.int().repeat(S).contiguous() for a in at]
+    lens = [torch.full((S,), 20 + (i + 1) * nq, dtype=torch.int32, device="cuda") for i in range(steps)]
+    starts = torch.arange(S + 1, dtype=torch.int32, device="cuda") * nq
+    ws = torch.empty(pa.pa_decode8_workspace_bytes(dims) if nq == 1 else pa.pa_chunk8_workspace_bytes(dims, T, nq), dtype=torch.uint8, device="cuda")
+
+    def run(wait):
+        cache = tuple(c.clone() for c in start)
+        c8 = pa.make_cache8(*cache)
+        outs = [torch.empty(T, Hq, D, dtype=torch.bfloat16, device="cuda") for _ in range(steps)]
+        q = torch.empty(T, Hq, D, dtype=torch.bfloat16, device="cuda")
+        torch.cuda.synchronize()
+        for i in range(steps):
+            x = xs[i]
+            pa.pa_rope_write_kv8(dims, rope, None, x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], pos[i], slots[i], q, c8)
+            if wait:
+                torch.cuda.synchronize()
+            if nq == 1:
+                pa.pa_decode8(dims, q, c8, tables, lens[i], 0.01, outs[i], ws)
+            else:
+                pa.pa_chunk8(dims, q, c8, tables, lens[i], starts, 0.01, outs[i], nq, ws)
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return outs, cache
+
+    want, kept = run(True)
+    for _ in range(3):
+        got, cache = run(False)
+        for i, (x, y) in enumerate(zip(got, want)):
+            assert torch.equal(x, y), f"step {i}"
+        for x, y in zip(cache, kept):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    assert pa.pa_device_errors(clear=True) == 0
