@@ -422,8 +422,9 @@ PA_API int32_t pa_rope_axes_write_kv(const pa_dims *dims, const pa_rope *rope, c
  *
  * and the same for V.  Half the memory and half the reads of a 16-bit cache.  The calls
  * below work on it as their counterparts do on the others (large chunks with fewer bits
- * of the weights: pa_chunk8); kv_dtype of their dims is the type of the queries, keys and values that go in and of the outputs, PA_F16 or
- * PA_BF16 (PA_ERR_UNSUPPORTED for PA_F32), D is 64 or 128 and B 16 or 32.
+ * of the weights: pa_chunk8); kv_dtype of their dims is the type of the queries, keys
+ * and values that go in and of the outputs, PA_F16 or PA_BF16 (PA_ERR_UNSUPPORTED for
+ * PA_F32), D is 64 or 128 and B 16 or 32.
  *   k, v                 codes [N, Hkv, B, D], device, 16-byte aligned
  *   k_scales, v_scales   float32 [N, Hkv], device.  The writes store powers of two.  The
  *                        attention calls take any scales from 2^-80 to 2^120 (those of V
@@ -493,10 +494,11 @@ typedef struct pa_window {
  *     out[i, h, :] = sum_j p_j V_j,  p = softmax_j(scale * q[i, h, :] . K_j)
  *
  * with K_j, V_j the values that the codes stand for.  Scores, weights' sums and outputs are held
- * in fp32; the codes go into the products as they are (exact in 16 bits).  Into the second one weights go
- * with 22 bits in decodes and where max_query_len * G <= 16, else rounded once to 11 bits
- * (pa_chunk_attention splits its weights in two 16-bit terms).  Short chunks and decodes over bf16 take a row's
- * queries as f16 by a power of two, exactly down to 2^-24 of the row's largest.  |q| < 2^110.
+ * in fp32; the codes go into the products as they are (exact in 16 bits).  Into the
+ * second one weights go with 22 bits in decodes and where max_query_len * G <= 16, else
+ * rounded once to 11 bits (pa_chunk_attention splits its weights in two 16-bit terms).
+ * Short chunks and decodes over bf16 take a row's queries as f16 by a power of two,
+ * exactly down to 2^-24 of the row's largest.  |q| < 2^110.
  *
  *   window        NULL: all keys
  *   out           [S | T, Hq, D] float32, or kv_dtype when out_dtype == kv_dtype
